@@ -13,7 +13,10 @@ Low-level (same names as the C entry points): ``gdn_chunk_fwd``,
 High-level: ``chunk_gated_delta_rule_fwd/_bwd`` (allocate outputs; optionally
 the forward keeps the per-chunk states and WY tiles for the backward),
 ``chunk_gated_delta_rule`` (autograd), ``recurrent_gated_delta_rule`` (decode);
-``cp`` splits sequences across ranks.
+``cp`` splits sequences across ranks.  Operators next to the delta rule (``block``, include/gdn_block.h):
+``paged_attention``, ``rotary_table``, ``rotary``, ``rotary_embedding`` (autograd), ``rotary_append``,
+``extend_pages``, ``fork_pages``, ``free_pages``, ``compact_pages``, ``copy_slots``, ``rms_norm``,
+``rms_norm_bwd``, ``residual_rms_norm`` (autograd).
 """
 from __future__ import annotations
 
@@ -24,6 +27,8 @@ from typing import Optional
 import torch
 
 from . import _lib
+from . import block
+from .block import *  # noqa: F401,F403
 from ._lib import (GDN_BF16, GDN_FP32, GDN_L2NORM_QK, GDN_SP_OFF, GDN_WINDOW_OFF, GdnShape)
 
 __all__ = ["GdnShape", "make_shape", "gdn_chunk_fwd", "gdn_chunk_fwd_static", "gdn_chunk_bwd", "gdn_fwd_workspace_size",
@@ -31,7 +36,7 @@ __all__ = ["GdnShape", "make_shape", "gdn_chunk_fwd", "gdn_chunk_fwd_static", "g
            "gdn_chunk_bwd_saved", "gdn_plan_query", "gdn_plan_estimate", "gdn_get_device_status", "gdn_device_status_code",
            "gdn_profile_enable", "gdn_profile_only", "gdn_profile_report",
            "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd", "chunk_gated_delta_rule",
-           "GDN_L2NORM_QK", "GDN_SP_OFF", "GDN_WINDOW_OFF"]
+           "GDN_L2NORM_QK", "GDN_SP_OFF", "GDN_WINDOW_OFF"] + block.__all__
 
 
 def _ptr(t) -> Optional[int]:

@@ -1,4 +1,4 @@
-"""ctypes view of the C ABI declared in include/gdn.h (argument marshalling only)."""
+"""ctypes view of the C ABI declared in include/gdn.h and include/gdn_block.h (argument marshalling only)."""
 from __future__ import annotations
 
 import ctypes
@@ -23,6 +23,13 @@ EXPORTS = ("gdn_fwd_workspace_size", "gdn_bwd_workspace_size", "gdn_chunk_fwd", 
            "gdn_status_string", "gdn_last_error_string")
 
 
+# every symbol include/gdn_block.h declares
+BLOCK_EXPORTS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_rotary_table", "gdn_rotary",
+                 "gdn_rotary_append", "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork",
+                 "gdn_pages_free", "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size",
+                 "gdn_rmsnorm_bwd")
+
+
 class GdnShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("Dk", ctypes.c_int), ("Dv", ctypes.c_int),
@@ -30,6 +37,37 @@ class GdnShape(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("flags", ctypes.c_uint),
                 ("seg_chunks", ctypes.c_int), ("seg_first", ctypes.c_int),
                 ("reserved", ctypes.c_int * 2)]
+
+
+_I, _L, _F = ctypes.c_int, ctypes.c_int64, ctypes.c_float
+
+
+class GdnPagedShape(ctypes.Structure):
+    _fields_ = [(n, _I) for n in ("num_seqs", "total_q", "num_heads", "num_kv_heads", "head_dim", "page_size", "num_pages",
+                                  "max_pages", "dtype", "max_q", "window")] + [("scale", _F)] + \
+               [(n, _L) for n in ("table_stride", "q_tok", "q_head", "k_page", "k_tok", "k_head", "v_page", "v_tok", "v_head",
+                                  "o_tok", "o_head", "kn_tok", "kn_head", "vn_tok", "vn_head")] + \
+               [(n, _I) for n in ("rot", "interleaved", "table_rows", "reserved")]
+
+
+class GdnRotaryShape(ctypes.Structure):
+    _fields_ = [(n, _I) for n in ("tokens", "q_heads", "k_heads", "head_dim", "rot", "interleaved", "inverse", "table_rows",
+                                  "dtype", "reserved")] + \
+               [(n, _L) for n in ("q_tok", "q_head", "k_tok", "k_head", "qo_tok", "qo_head", "ko_tok", "ko_head")]
+
+
+class GdnPagesShape(ctypes.Structure):
+    _fields_ = [("num_seqs", _I), ("max_pages", _I), ("num_pages", _I), ("page_size", _I), ("table_stride", _L),
+                ("reserved", _I * 2)]
+
+
+class GdnSlotPool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("stride", _L), ("bytes", _L), ("slots", _L)]
+
+
+class GdnNormShape(ctypes.Structure):
+    _fields_ = [("rows", _L), ("dim", _I), ("dtype", _I), ("fp8", _I), ("group", _I), ("eps", _F), ("weight_offset", _F),
+                ("x_row", _L), ("r_row", _L), ("h_row", _L), ("y_row", _L), ("reserved", _I * 2)]
 
 
 _lock = threading.Lock()
@@ -92,6 +130,25 @@ def load():
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_last_error_string.argtypes = []
         lib.gdn_last_error_string.restype = ctypes.c_char_p
+        Z, D = ctypes.c_size_t, ctypes.c_double
+        for name, args in {
+                "gdn_paged_attn_fwd": [P] * 10 + [Z, P],
+                "gdn_rotary_table": [P, _I, _I, D, P, P],
+                "gdn_rotary": [P] * 8,
+                "gdn_rotary_append": [P] * 12,
+                "gdn_slots_copy": [P, _I, P, P, _I, P],
+                "gdn_pages_extend": [P] * 6 + [_I, P, P, Z, P],
+                "gdn_pages_fork": [P] * 6 + [_I, P, _I, P, _I, P, P, Z, P],
+                "gdn_pages_free": [P] * 5 + [_I, P],
+                "gdn_pages_compact": [P] * 6 + [_I, P, P, Z, P],
+                "gdn_rmsnorm_fwd": [P] * 9,
+                "gdn_rmsnorm_bwd": [P] * 9 + [Z, P]}.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = ctypes.c_int
+        for name, args in {"gdn_paged_attn_workspace_size": [P], "gdn_pages_workspace_size": [P, _I],
+                           "gdn_rmsnorm_bwd_workspace_size": [P]}.items():
+            getattr(lib, name).argtypes = args
+            getattr(lib, name).restype = Z
         _lib = lib
         return lib
 

@@ -1,7 +1,7 @@
 """Build step of the CUDA library: nvcc for sm_103a, in-tree (``_build/libgdn.so``).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library with the C ABI of ``include/gdn.h``.
+library with the C ABI of ``include/gdn.h`` and ``include/gdn_block.h``.
 """
 from __future__ import annotations
 
@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
 SOURCES = ["api.cu", "plan.cu", "fwd.cu", "fwd_prep_tc.cu", "fwd_tc.cu", "bwd.cu", "bwd_chain_tc.cu", "bwd_local_tc.cu",
-           "recurrent.cu"]
+           "recurrent.cu", "block_api.cu", "attn_rows.cu", "rope.cu", "pages.cu", "rmsnorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -29,7 +29,8 @@ def _nvcc() -> str:
 
 
 def _deps_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "gdn.h"), __file__]
+    inc = os.path.join(ROOT, "include")
+    files = [os.path.join(d, f) for d in (CSRC, inc) for f in os.listdir(d)] + [__file__]
     return max(os.path.getmtime(f) for f in files)
 
 

@@ -12,13 +12,17 @@
 #include <vector>
 
 #include "../../include/gdn.h"
+#include "host.h"
 #include "kernels.h"
 
 using namespace gdn;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+// helpers shared with the other translation unit of C entry points, declared in host.h
+namespace gdn {
 
 int fail(int code, const char *fmt, ...) {
   char buf[512];
@@ -44,6 +48,10 @@ int num_sms() {
   }
   return cache[dev];
 }
+
+}  // namespace gdn
+
+namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -380,7 +388,6 @@ Plan plan_of(const Layout &L, char *ws) {
   return pl;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int check_ptrs(std::initializer_list<std::pair<const void *, const char *>> req,
                std::initializer_list<std::pair<const void *, const char *>> opt) {
@@ -414,25 +421,41 @@ struct Profiler {
 };
 Profiler g_prof;
 
-struct ProfScope {
-  int idx = -1;
-  cudaStream_t st;
-  const char *name;
-  ProfScope(const char *n, cudaStream_t s) : st(s), name(n) {
-    std::lock_guard<std::mutex> lk(g_prof.mu);
-    if (!g_prof.on || g_prof.used + 2 > (int)g_prof.pool.size()) return;
-    if (!g_prof.only.empty() && g_prof.only != n) return;
-    idx = g_prof.used;
-    g_prof.used += 2;
-    cudaEventRecord(g_prof.pool[idx], st);
-  }
-  ~ProfScope() {
-    if (idx < 0) return;
-    std::lock_guard<std::mutex> lk(g_prof.mu);
-    cudaEventRecord(g_prof.pool[idx + 1], st);
-    g_prof.recs.push_back({name, idx, idx + 1});
-  }
-};
+}  // namespace
+
+namespace gdn {
+
+ProfScope::ProfScope(const char *n, cudaStream_t s) : st(s), name(n) {
+  std::lock_guard<std::mutex> lk(g_prof.mu);
+  if (!g_prof.on || g_prof.used + 2 > (int)g_prof.pool.size()) return;
+  if (!g_prof.only.empty() && g_prof.only != n) return;
+  idx = g_prof.used;
+  g_prof.used += 2;
+  cudaEventRecord(g_prof.pool[idx], st);
+}
+ProfScope::~ProfScope() {
+  if (idx < 0) return;
+  std::lock_guard<std::mutex> lk(g_prof.mu);
+  cudaEventRecord(g_prof.pool[idx + 1], st);
+  g_prof.recs.push_back({name, idx, idx + 1});
+}
+
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+}  // namespace gdn
+
+namespace {
 
 void prof_drain_locked() {
   for (auto &r : g_prof.recs) {
@@ -454,13 +477,6 @@ void prof_drain_locked() {
   g_prof.used = 0;
 }
 
-#define PROF(name) ProfScope _prof_scope(name, st)
-
-#define CK(expr)                                                                                  \
-  do {                                                                                            \
-    int _e = (expr);                                                                              \
-    if (_e != 0) return fail(GDN_ERR_CUDA, "%s failed: %s", #expr, cudaGetErrorString((cudaError_t)_e)); \
-  } while (0)
 
 // The chunk forward kernel for this problem: tcgen05 for bf16 with d = 128 (its recurrent half, on the
 // context that the chunk-local half stored), the mma.sync/CUDA-core kernel otherwise (d = 64, fp32
@@ -527,23 +543,6 @@ int prologue_saved(const gdn_shape *s, const Layout &L, char *ws, const float *g
 }
 
 // ------------------------------------------------------------------ TMA tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static std::once_flag once;
-  static EncodeTiledFn fn = nullptr;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // [tokens, H, 128] bf16 tensor, box = 64 features x 1 head x 64 tokens, 128-byte swizzle
 int qkv_map(CUtensorMap *m, const void *ptr, long tokens, int H) {
   EncodeTiledFn fn = encode_fn();

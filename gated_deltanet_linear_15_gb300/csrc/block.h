@@ -1,0 +1,75 @@
+// Host-visible launchers of the operators declared in include/gdn_block.h (internal to the library).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/gdn_block.h"
+
+namespace gdn {
+
+// ---- rotary positions
+// One head group of a launch: heads of one tensor, turned (or only copied, when `turn` is 0) from src to dst; dst NULL
+// for the keys and values of an append, which go to the cache.
+struct RopeGroup {
+  const void *src;
+  void *dst;
+  long long s_tok, s_head, d_tok, d_head, d_page;  // elements; with d_page != 0: d_tok is the slot stride in a page
+  int heads, turn;
+};
+struct RopeArgs {
+  RopeGroup grp[3];
+  int ngrp, tokens, heads, D, rot, interleaved, inverse, rows;
+  const float *table;
+  const int *positions;                 // NULL: positions from cu_q and kv_lens
+  const int *cu_q, *kv_lens, *pages;    // append
+  long long table_stride;
+  int N, per_seq, log2P, num_pages, max_pages;
+};
+cudaError_t launch_rope(const RopeArgs &a, bool bf16_type, bool vec, cudaStream_t st);
+cudaError_t launch_rope_table(const double *freq, int pairs, int rows, double amplitude, float *table, cudaStream_t st);
+
+// ---- pages
+constexpr int MAX_POOLS = 64;  // pools of one launch
+struct PoolList {
+  gdn_slot_pool p[MAX_POOLS];
+  long long chunk0[MAX_POOLS + 1];  // chunks of the pools before, per pair
+  int n;
+};
+struct PagesArgs {
+  int S, W, NP, P;
+  long long ts;
+  int *table, *lens, *ref;
+};
+// pairs src[i] -> dst[i] for i < (count_dev ? *count_dev : count); negative numbers are left out
+cudaError_t launch_slots_copy(const PoolList &pl, const int *src, const int *dst, int count, const int *count_dev,
+                              cudaStream_t st);
+cudaError_t launch_pages_extend(const PagesArgs &a, const int *seqs, const int *add, int m, int *ok, int *ws,
+                                cudaStream_t st);
+cudaError_t launch_pages_fork_plan(const PagesArgs &a, const int *parents, const int *children, int m, int *new_page,
+                                   int *src, int *psrc, int *pdst, cudaStream_t st);
+cudaError_t launch_pages_fork_rows(const PagesArgs &a, const int *psrc, const int *pdst, const int *new_page, int m,
+                                   cudaStream_t st);
+cudaError_t launch_pages_free(const PagesArgs &a, const int *seqs, int m, cudaStream_t st);
+cudaError_t launch_pages_compact_plan(const PagesArgs &a, const int *ref_in, int *map, int *src, int *dst, int *moves,
+                                      cudaStream_t st);
+cudaError_t launch_pages_remap(const PagesArgs &a, const int *table_in, const int *map, cudaStream_t st);
+
+// ---- norm
+struct NormArgs {
+  const void *x, *res;      // backward: dy, dh
+  const void *h;            // backward
+  const float *weight;
+  void *h_out, *y;          // backward: dx in y
+  float *scale, *rstd;
+  const float *rstd_in;
+  float *dw, *part;
+  long long T, x_row, r_row, h_row, y_row;
+  int D, group, fp8;
+  float eps, off;
+};
+int norm_bwd_ctas(const NormArgs &a, bool bf16_type, bool vec, int sms);
+cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16_type, bool vec, int sms, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16_type, bool vec, int sms, cudaStream_t st);
+
+}  // namespace gdn

@@ -1,0 +1,381 @@
+// Upkeep of a paged cache: growing, branching, ending and compacting sequences, and copying pages or per-sequence
+// states (the caches of a hybrid stack: pages for its softmax layers, one recurrent state per sequence and delta-rule
+// layer; onedev.kr summary of the FlashQLA talk, background paragraph).
+//
+// The bookkeeping is whole numbers: free pages are handed out lowest first, in the order of the request list, by
+// prefix sums, so every run gives the same tables.  One CTA plans (its scans run over the requests and, until enough
+// are found, over the pages' counts, 4096 of them a step); what is long, the rows of the tables and the copies, goes to
+// the whole GPU in a second launch.  Copies are bound by bytes (each slot read and written once): a slot is cut into
+// 16 KB chunks, the chunks of all pairs and pools stand in one line, and a warp-coalesced thread moves four 16-byte
+// pieces at a time, loaded before the first is stored.
+#include "block.h"
+#include "common.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int NP_T = 1024;      // threads of a planning CTA
+constexpr int CHUNK = 16384;    // bytes of a copy chunk
+constexpr int COPY_T = 256;
+
+// inclusive sum over the CTA; sh holds 32 ints.  Every thread takes part.
+__device__ __forceinline__ int scan_1024(int x, int *sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    sh[lane] = y;
+  }
+  __syncthreads();
+  return x + (warp ? sh[warp - 1] : 0);
+}
+
+// counts ref[i], i = base + 4 tid + e, of a step of 4096 pages (1 past the end)
+__device__ __forceinline__ void load_refs(const int *ref, int NP, int base, int (&r)[4]) {
+  const int i = base + 4 * threadIdx.x;
+  if (i + 3 < NP && (reinterpret_cast<uintptr_t>(ref) & 15) == 0) {
+    const int4 v = *reinterpret_cast<const int4 *>(ref + i);
+    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = i + e < NP ? ref[i + e] : 1;
+  }
+}
+
+// Calls give(rank, page) for the free pages of rank 0 .. want - 1 (ascending numbers), and returns how many free pages
+// were seen (at least `want` when there are so many).
+template <class F> __device__ __forceinline__ int hand_out(const int *ref, int NP, int want, int *sh, F give) {
+  int seen = 0;
+  for (int base = 0; base < NP && seen < want; base += 4 * NP_T) {
+    int r[4];
+    load_refs(ref, NP, base, r);
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n += r[e] <= 0;
+    const int inc = scan_1024(n, sh);
+    int rank = seen + inc - n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (r[e] <= 0) {
+        if (rank < want) give(rank, base + 4 * (int)threadIdx.x + e);
+        ++rank;
+      }
+    const int all = sh[31];
+    __syncthreads();
+    seen += all;
+  }
+  return seen;
+}
+
+// free pages in all, up to `want`
+__device__ __forceinline__ int count_free(const int *ref, int NP, int want, int *sh) {
+  return hand_out(ref, NP, want, sh, [](int, int) {});
+}
+
+__device__ __forceinline__ int pages_of(int len, int P) { return (int)(((long long)len + P - 1) / P); }
+
+}  // namespace
+
+// ws: prefix[m + 1] of the pages that the granted requests take
+__global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const int *seqs, const int *add, int m, int *ok, int *pre) {
+  __shared__ int sh[32];
+  __shared__ int granted;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  // what each request needs, and the prefix of the needs in list order
+  long long total = 0;
+  for (int b = 0; b < m; b += NP_T) {
+    const int i = b + tid;
+    int need = 0;
+    bool good = false;
+    if (i < m) {
+      const int s = seqs[i], d = add[i];
+      if ((unsigned)s < (unsigned)a.S && d >= 0) {
+        const int len = a.lens[s], have = pages_of(max(len, 0), a.P);
+        const long long end = (long long)len + d;
+        good = len >= 0 && end <= (long long)a.W * a.P;
+        if (good && len % a.P != 0 && d > 0) {  // it will write into its last page: that page has to be its own
+          const int pg = a.table[s * a.ts + have - 1];
+          good = (unsigned)pg < (unsigned)a.NP && a.ref[pg] == 1;
+        }
+        if (good) need = min(pages_of((int)end, a.P) - have, a.NP + 1);
+      }
+    }
+    const int inc = scan_1024(need, sh);
+    // past INT_MAX / 2 nothing can be granted any more, so the prefix stops growing there
+    const long long upto = min(total + inc, 1ll << 30);
+    if (i < m) {
+      pre[i + 1] = (int)upto;
+      ok[i] = good;
+    }
+    const int all = sh[31];
+    __syncthreads();
+    total = min(total + all, 1ll << 30);
+  }
+  if (tid == 0) {
+    pre[0] = 0;
+    granted = 0;
+  }
+  __syncthreads();
+  const int avail = count_free(a.ref, a.NP, (int)total, sh);
+  // the requests whose pages, and all before theirs, are there
+  for (int i = tid; i < m; i += NP_T) {
+    const int need = pre[i + 1] - pre[i];
+    if (need > 0 && pre[i + 1] > avail) ok[i] = 0;
+    else atomicMax(&granted, pre[i + 1] <= avail ? pre[i + 1] : 0);
+  }
+  __syncthreads();
+  const int want = granted;
+  hand_out(a.ref, a.NP, want, sh, [&](int rank, int page) {
+    int lo = 0, hi = m;  // the request with pre[lo] <= rank < pre[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= rank) lo = mid;
+      else hi = mid;
+    }
+    const int s = seqs[lo];
+    a.table[s * a.ts + pages_of(a.lens[s], a.P) + rank - pre[lo]] = page;
+    a.ref[page] = 1;
+  });
+  __syncthreads();
+  for (int i = tid; i < m; i += NP_T)
+    if (ok[i]) a.lens[seqs[i]] += add[i];
+}
+
+// Which forks happen, the new page of each, the copy pairs.  src[i]: the parent's last page, psrc / pdst: parent and
+// child, all -1 for what is not to be done; the new page is the copy's target (negative: none).
+__global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, const int *parents, const int *children, int m,
+                                                               int *new_page, int *src, int *psrc, int *pdst) {
+  __shared__ int sh[32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  int total = 0;
+  for (int b = 0; b < m; b += NP_T) {  // new_page holds the rank of the page until it is known
+    const int i = b + tid;
+    int need = 0, p = -1, c = -1, from = -1;
+    bool good = false;
+    if (i < m) {
+      p = parents[i];
+      c = children[i];
+      good = (unsigned)p < (unsigned)a.S && (unsigned)c < (unsigned)a.S && p != c && a.lens[c] == 0;
+      if (good) {
+        const int len = a.lens[p];
+        good = len >= 0 && len <= (long long)a.W * a.P;
+        if (good && len % a.P != 0) {
+          from = a.table[p * a.ts + len / a.P];
+          good = (unsigned)from < (unsigned)a.NP;
+          need = good;
+        }
+      }
+    }
+    const int inc = scan_1024(need, sh);
+    if (i < m) {
+      new_page[i] = !good ? -2 : (need ? total + inc - 1 : -1);
+      src[i] = need ? from : -1;
+      psrc[i] = good ? p : -1;
+      pdst[i] = good ? c : -1;
+    }
+    const int all = sh[31];
+    __syncthreads();
+    total += all;
+  }
+  __syncthreads();
+  int *list = pdst + m;  // the request of every rank, then the page of every rank
+  for (int i = tid; i < m; i += NP_T)
+    if (new_page[i] >= 0) list[new_page[i]] = i;
+  __syncthreads();
+  const int seen = hand_out(a.ref, a.NP, total, sh, [&](int rank, int page) { list[m + rank] = page; });
+  __syncthreads();
+  for (int r = tid; r < total; r += NP_T) {
+    const int i = list[r];
+    if (r < seen) {
+      new_page[i] = list[m + r];
+      a.ref[list[m + r]] = 1;
+    } else {  // no page left: the fork is left out
+      new_page[i] = -2;
+      src[i] = psrc[i] = pdst[i] = -1;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < m; i += NP_T)
+    if (pdst[i] >= 0) a.lens[pdst[i]] = a.lens[psrc[i]];
+}
+
+// the children's table rows, and a reference more for every page that they share
+__global__ void __launch_bounds__(256) pages_fork_rows_kernel(PagesArgs a, const int *psrc, const int *pdst, const int *new_page) {
+  pdl_trigger();
+  pdl_wait();
+  const int i = blockIdx.x, p = psrc[i], c = pdst[i];
+  if (p < 0) return;
+  const int len = a.lens[p], full = len / a.P;
+  for (int j = blockIdx.y * 256 + threadIdx.x; j < a.W; j += 256 * gridDim.y) {
+    int pg = -1;
+    if (j < full) {
+      pg = a.table[p * a.ts + j];
+      if ((unsigned)pg < (unsigned)a.NP) atomicAdd(a.ref + pg, 1);
+    } else if (j == full && len % a.P != 0) {
+      pg = new_page[i];
+    }
+    a.table[c * a.ts + j] = pg;
+  }
+}
+
+__global__ void __launch_bounds__(256) pages_free_kernel(PagesArgs a, const int *seqs) {
+  pdl_trigger();
+  pdl_wait();
+  const int s = seqs[blockIdx.x];
+  if ((unsigned)s >= (unsigned)a.S) return;
+  for (int j = blockIdx.y * 256 + threadIdx.x; j < a.W; j += 256 * gridDim.y) {
+    // taken by exchange, so that a sequence named twice gives its pages back once
+    const int pg = atomicExch(a.table + s * a.ts + j, -1);
+    if ((unsigned)pg < (unsigned)a.NP) atomicAdd(a.ref + pg, -1);
+  }
+  if (blockIdx.y == 0 && threadIdx.x == 0) a.lens[s] = 0;
+}
+
+// map[page]: the page's number after compaction.  src / dst: the moves, ascending; *moves their number.
+__global__ void __launch_bounds__(NP_T) pages_compact_plan_kernel(PagesArgs a, const int *ref_in, int *map, int *src, int *dst, int *moves) {
+  __shared__ int sh[32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  int live = 0;
+  for (int base = 0; base < a.NP; base += 4 * NP_T) {
+    int r[4];
+    load_refs(ref_in, a.NP, base, r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) live += base + 4 * tid + e < a.NP && r[e] > 0;
+  }
+  scan_1024(live, sh);
+  live = sh[31];
+  __syncthreads();
+  int holes = 0, highs = 0;
+  for (int base = 0; base < a.NP; base += 4 * NP_T) {
+    int r[4];
+    load_refs(ref_in, a.NP, base, r);
+    int nh = 0, ng = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = base + 4 * tid + e;
+      nh += i < live && r[e] <= 0;
+      ng += i < a.NP && i >= live && r[e] > 0;
+    }
+    const int ih = scan_1024(nh, sh);
+    const int ah = sh[31];
+    __syncthreads();
+    const int ig = scan_1024(ng, sh);
+    const int ag = sh[31];
+    __syncthreads();
+    int kh = holes + ih - nh, kg = highs + ig - ng;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = base + 4 * tid + e;
+      if (i >= a.NP) continue;
+      if (i < live && r[e] <= 0) dst[kh++] = i;
+      else if (i >= live && r[e] > 0) src[kg++] = i;
+      map[i] = i;
+      a.ref[i] = r[e];
+    }
+    holes += ah;
+    highs += ag;
+  }
+  __syncthreads();
+  for (int k = tid; k < highs; k += NP_T) {  // as many holes below `live` as pages in use above
+    const int s = src[k], d = dst[k];
+    map[s] = d;
+    a.ref[d] = a.ref[s];
+    a.ref[s] = 0;
+  }
+  if (tid == 0) *moves = highs;
+}
+
+__global__ void __launch_bounds__(256) pages_remap_kernel(PagesArgs a, const int *table_in, const int *map) {
+  pdl_trigger();
+  pdl_wait();
+  const long long n = (long long)a.S * a.W;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+    const long long at = (i / a.W) * a.ts + i % a.W;
+    const int pg = table_in[at];
+    a.table[at] = (unsigned)pg < (unsigned)a.NP ? map[pg] : pg;
+  }
+}
+
+__global__ void __launch_bounds__(COPY_T) slots_copy_kernel(const __grid_constant__ PoolList pl, const int *src, const int *dst,
+                                                           int count, const int *count_dev) {
+  pdl_trigger();
+  pdl_wait();
+  if (count_dev) count = min(count, *count_dev);
+  const long long per = pl.chunk0[pl.n], total = per * count;  // chunks of a pair in all pools
+  for (long long x = blockIdx.x; x < total; x += gridDim.x) {
+    const int i = (int)(x / per);
+    const long long in = x - i * per;
+    int p = 0;
+    while (in >= pl.chunk0[p + 1]) ++p;
+    const gdn_slot_pool &g = pl.p[p];
+    const int s = src[i], d = dst[i];
+    if (s < 0 || d < 0 || s >= g.slots || d >= g.slots) continue;
+    const long long b0 = (in - pl.chunk0[p]) * CHUNK;
+    const int n16 = (int)(min((long long)CHUNK, g.bytes - b0) >> 4);
+    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const char *>(g.base) + s * g.stride + b0);
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<char *>(g.base) + d * g.stride + b0);
+    uint4 v[CHUNK / 16 / COPY_T];
+#pragma unroll
+    for (int k = 0; k < CHUNK / 16 / COPY_T; ++k)
+      if ((int)threadIdx.x + k * COPY_T < n16) v[k] = __ldcs(from + threadIdx.x + k * COPY_T);
+#pragma unroll
+    for (int k = 0; k < CHUNK / 16 / COPY_T; ++k)
+      if ((int)threadIdx.x + k * COPY_T < n16) __stcs(to + threadIdx.x + k * COPY_T, v[k]);
+  }
+}
+
+cudaError_t launch_slots_copy(const PoolList &pl, const int *src, const int *dst, int count, const int *count_dev, cudaStream_t st) {
+  PoolList l = pl;
+  l.chunk0[0] = 0;
+  for (int i = 0; i < l.n; ++i) l.chunk0[i + 1] = l.chunk0[i] + (l.p[i].bytes + CHUNK - 1) / CHUNK;
+  const long long total = l.chunk0[l.n] * count;
+  if (total <= 0) return cudaSuccess;
+  const long long cap = 152 * 8;  // eight CTAs of 256 threads fill an SM
+  return launch_pdl(slots_copy_kernel, dim3((unsigned)(total < cap ? total : cap)), dim3(COPY_T), 0, st, l, src, dst, count, count_dev);
+}
+
+namespace {
+dim3 rows_grid(int m, int W) { return dim3((unsigned)m, (unsigned)((W + 1023) / 1024 < 64 ? (W + 1023) / 1024 : 64)); }
+}  // namespace
+
+cudaError_t launch_pages_extend(const PagesArgs &a, const int *seqs, const int *add, int m, int *ok, int *ws, cudaStream_t st) {
+  return launch_pdl(pages_extend_kernel, dim3(1), dim3(NP_T), 0, st, a, seqs, add, m, ok, ws);
+}
+cudaError_t launch_pages_fork_plan(const PagesArgs &a, const int *parents, const int *children, int m, int *new_page, int *src,
+                                   int *psrc, int *pdst, cudaStream_t st) {
+  return launch_pdl(pages_fork_plan_kernel, dim3(1), dim3(NP_T), 0, st, a, parents, children, m, new_page, src, psrc, pdst);
+}
+cudaError_t launch_pages_fork_rows(const PagesArgs &a, const int *psrc, const int *pdst, const int *new_page, int m, cudaStream_t st) {
+  return launch_pdl(pages_fork_rows_kernel, rows_grid(m, a.W), dim3(256), 0, st, a, psrc, pdst, new_page);
+}
+cudaError_t launch_pages_free(const PagesArgs &a, const int *seqs, int m, cudaStream_t st) {
+  return launch_pdl(pages_free_kernel, rows_grid(m, a.W), dim3(256), 0, st, a, seqs);
+}
+cudaError_t launch_pages_compact_plan(const PagesArgs &a, const int *ref_in, int *map, int *src, int *dst, int *moves, cudaStream_t st) {
+  return launch_pdl(pages_compact_plan_kernel, dim3(1), dim3(NP_T), 0, st, a, ref_in, map, src, dst, moves);
+}
+cudaError_t launch_pages_remap(const PagesArgs &a, const int *table_in, const int *map, cudaStream_t st) {
+  const long long n = ((long long)a.S * a.W + 255) / 256;
+  return launch_pdl(pages_remap_kernel, dim3((unsigned)(n < 152 * 8 ? n : 152 * 8)), dim3(256), 0, st, a, table_in, map);
+}
+
+}  // namespace gdn

@@ -1,0 +1,445 @@
+// Root-mean-square norm of the residual stream, forward and backward:
+//   h = x + residual,  rstd = (mean(h^2) + eps)^(-1/2),  y = h rstd w,
+//   fp8: per row or per 128 features  scale = amax |y| / 448,  y8 = e4m3(y / scale);
+//   dx = rstd w dy - h rstd^3 <w dy, h> / D + dh,  dw = sum over rows of dy h rstd.
+// (The norm in front of the projections of every layer of the stacks that onedev.kr's summary of the FlashQLA talk
+// describes, background paragraph.)
+//
+// Bound by bytes: a row is read once into registers (16-byte pieces, neighbours in neighbouring threads), reduced, and
+// written once; the fp8 scales come from the same registers.  TPR threads hold a row: 32 (no barrier at all) for short
+// rows, 128 for rows up to a few thousand features, 512 for longer ones or when there are fewer rows than SMs and
+// latency counts.  CTAs stay and walk over rows, with the weight in registers.  The backward keeps its share of dw in
+// registers too; each CTA leaves one partial row, and a second kernel adds these in order.  Sums are fp32; rows of
+// which dim, stride or alignment does not allow 16-byte pieces go one feature at a time.
+#include <cuda_fp8.h>
+
+#include "block.h"
+#include "common.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr float E4M3_MAX = 448.f, AMAX_FLOOR = 1e-30f;
+
+template <typename I> struct Vec { static constexpr int N = 16 / sizeof(I); };
+template <typename I> __device__ __forceinline__ void widen(const uint4 &u, float *x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(I) == 2) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+template <typename I> __device__ __forceinline__ uint4 narrow(const float *x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(I) == 2) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    } else {
+      w[i] = __float_as_uint(x[i]);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+__device__ __forceinline__ uint8_t fp8x1(float a) { return __nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3); }
+
+// reduction over the TPR threads of a row; sh: this row group's 2 x (TPR / 32) floats, halves used in turn so that
+// one barrier per reduction is enough.  Every thread of the CTA takes part.
+template <int TPR, bool MAX> __device__ __forceinline__ float row_reduce(float x, float *sh, int &turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, x, o);
+    x = MAX ? fmaxf(x, y) : x + y;
+  }
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    float *b = sh + turn * W;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) b[(threadIdx.x % TPR) >> 5] = x;
+    __syncthreads();
+    x = b[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) x = MAX ? fmaxf(x, b[i]) : x + b[i];
+  }
+  return x;
+}
+
+}  // namespace
+
+template <typename I, int NTH, int TPR, int NV>
+__global__ void __launch_bounds__(NTH) norm_fwd_kernel(NormArgs a) {
+  constexpr int V = Vec<I>::N, RPC = NTH / TPR;
+  __shared__ float sh[RPC][2 * (TPR / 32)];
+  pdl_trigger();
+  pdl_wait();
+  const int tr = threadIdx.x % TPR, grp = threadIdx.x / TPR, pieces = a.D / V;
+  int turn = 0;
+  float w[NV][V];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = tr + k * TPR;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 t = c < pieces ? *reinterpret_cast<const float4 *>(a.weight + c * V + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      w[k][i] = t.x + a.off;
+      w[k][i + 1] = t.y + a.off;
+      w[k][i + 2] = t.z + a.off;
+      w[k][i + 3] = t.w + a.off;
+    }
+  }
+  const float invD = 1.f / a.D;
+  for (long long r0 = (long long)blockIdx.x * RPC; r0 < a.T; r0 += (long long)gridDim.x * RPC) {
+    const long long r = r0 + grp;
+    const bool live = r < a.T;
+    float h[NV][V];
+    float ss = 0.f;
+    uint4 xr[NV], rr[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = tr + k * TPR;
+      xr[k] = rr[k] = make_uint4(0, 0, 0, 0);
+      if (live && c < pieces) {
+        xr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.x) + r * a.x_row + c * V);
+        if (a.res) rr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.res) + r * a.r_row + c * V);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = tr + k * TPR;
+      float t[V];
+      widen<I>(xr[k], h[k]);
+      widen<I>(rr[k], t);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (a.res) h[k][i] += t[i];
+        ss += h[k][i] * h[k][i];
+      }
+      if (a.h_out && live && c < pieces)
+        *reinterpret_cast<uint4 *>(static_cast<I *>(a.h_out) + r * a.h_row + c * V) = narrow<I>(h[k]);
+    }
+    const float rstd = rsqrtf(row_reduce<TPR, false>(ss, sh[grp], turn) * invD + a.eps);
+    if (a.rstd && live && tr == 0) a.rstd[r] = rstd;
+    if (!a.fp8) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int c = tr + k * TPR;
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[k][i] = h[k][i] * rstd * w[k][i];
+        if (live && c < pieces) *reinterpret_cast<uint4 *>(static_cast<I *>(a.y) + r * a.y_row + c * V) = narrow<I>(h[k]);
+      }
+      continue;
+    }
+    float amax = 0.f, gm[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      gm[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        h[k][i] = h[k][i] * rstd * w[k][i];
+        gm[k] = fmaxf(gm[k], fabsf(h[k][i]));
+      }
+      amax = fmaxf(amax, gm[k]);
+    }
+    if (a.group == 0) {
+      amax = row_reduce<TPR, true>(amax, sh[grp], turn);
+      if (live && tr == 0) a.scale[r] = fmaxf(amax, AMAX_FLOOR) / E4M3_MAX;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = tr + k * TPR;
+      float m = amax;
+      if (a.group) {  // 128 features: 16 (bf16) or 32 (fp32) neighbouring threads
+        m = gm[k];
+#pragma unroll
+        for (int o = 64 / V; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (live && c < pieces && c % (128 / V) == 0) a.scale[r * (a.D / 128) + c / (128 / V)] = fmaxf(m, AMAX_FLOOR) / E4M3_MAX;
+      }
+      const float inv = E4M3_MAX / fmaxf(m, AMAX_FLOOR);
+      if (live && c < pieces) {
+        uint8_t *y = static_cast<uint8_t *>(a.y) + r * a.y_row + c * V;
+        const uint32_t lo = fp8x4(h[k][0] * inv, h[k][1] * inv, h[k][2] * inv, h[k][3] * inv);
+        if constexpr (V == 8) {
+          *reinterpret_cast<uint2 *>(y) = make_uint2(lo, fp8x4(h[k][4] * inv, h[k][5] * inv, h[k][6] * inv, h[k][7] * inv));
+        } else {
+          *reinterpret_cast<uint32_t *>(y) = lo;
+        }
+      }
+    }
+  }
+}
+
+// one feature at a time, a CTA per row
+template <typename I> __global__ void __launch_bounds__(256) norm_fwd_any_kernel(NormArgs a) {
+  __shared__ float sh[2 * 8];
+  pdl_trigger();
+  pdl_wait();
+  int turn = 0;
+  for (long long r = blockIdx.x; r < a.T; r += gridDim.x) {
+    const I *x = static_cast<const I *>(a.x) + r * a.x_row;
+    const I *q = a.res ? static_cast<const I *>(a.res) + r * a.r_row : nullptr;
+    float ss = 0.f;
+    for (int i = threadIdx.x; i < a.D; i += 256) {
+      const float h = tof(x[i]) + (q ? tof(q[i]) : 0.f);
+      ss += h * h;
+    }
+    const float rstd = rsqrtf(row_reduce<256, false>(ss, sh, turn) / a.D + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+    auto y_at = [&](int i) { return (tof(x[i]) + (q ? tof(q[i]) : 0.f)) * rstd * (a.weight[i] + a.off); };
+    const int gsz = a.group ? a.group : a.D;
+    float inv = 0.f;
+    for (int g0 = 0; a.fp8 && g0 < a.D; g0 += gsz) {
+      float m = 0.f;
+      for (int i = g0 + threadIdx.x; i < g0 + gsz; i += 256) m = fmaxf(m, fabsf(y_at(i)));
+      m = fmaxf(row_reduce<256, true>(m, sh, turn), AMAX_FLOOR);
+      if (threadIdx.x == 0) a.scale[r * (a.D / gsz) + g0 / gsz] = m / E4M3_MAX;
+      inv = E4M3_MAX / m;
+      if (a.group)
+        for (int i = g0 + threadIdx.x; i < g0 + gsz; i += 256) static_cast<uint8_t *>(a.y)[r * a.y_row + i] = fp8x1(y_at(i) * inv);
+    }
+    // outputs that may take an input's place are written once nothing of the feature is read any more
+    for (int i = threadIdx.x; i < a.D; i += 256) {
+      const float h = tof(x[i]) + (q ? tof(q[i]) : 0.f), y = h * rstd * (a.weight[i] + a.off);
+      if (a.h_out) static_cast<I *>(a.h_out)[r * a.h_row + i] = fromf<I>(h);
+      if (!a.fp8) static_cast<I *>(a.y)[r * a.y_row + i] = fromf<I>(y);
+      else if (!a.group) static_cast<uint8_t *>(a.y)[r * a.y_row + i] = fp8x1(y * inv);
+    }
+  }
+}
+
+template <typename I, int NTH, int TPR, int NV>
+__global__ void __launch_bounds__(NTH) norm_bwd_kernel(NormArgs a) {
+  constexpr int V = Vec<I>::N, RPC = NTH / TPR;
+  __shared__ float sh[RPC][2 * (TPR / 32)];
+  extern __shared__ float dsh[];  // [D], when several row groups share a CTA
+  pdl_trigger();
+  pdl_wait();
+  const int tr = threadIdx.x % TPR, grp = threadIdx.x / TPR, pieces = a.D / V;
+  int turn = 0;
+  float w[NV][V], dw[NV][V];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int c = tr + k * TPR;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[k][i] = c < pieces ? a.weight[c * V + i] + a.off : 0.f;
+      dw[k][i] = 0.f;
+    }
+  }
+  const float invD = 1.f / a.D;
+  for (long long r0 = (long long)blockIdx.x * RPC; r0 < a.T; r0 += (long long)gridDim.x * RPC) {
+    const long long r = r0 + grp;
+    const bool live = r < a.T;
+    uint4 hr[NV], gr[NV], er[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = tr + k * TPR;
+      hr[k] = gr[k] = er[k] = make_uint4(0, 0, 0, 0);
+      if (live && c < pieces) {
+        hr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.h) + r * a.x_row + c * V);
+        gr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.x) + r * a.y_row + c * V);
+        if (a.res) er[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.res) + r * a.r_row + c * V);
+      }
+    }
+    const float rstd = live ? a.rstd_in[r] : 0.f;
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float h[V], g[V];
+      widen<I>(hr[k], h);
+      widen<I>(gr[k], g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        dot += g[i] * w[k][i] * h[i];
+        dw[k][i] += g[i] * (h[i] * rstd);
+      }
+    }
+    const float s = row_reduce<TPR, false>(dot, sh[grp], turn) * invD * rstd * rstd * rstd;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = tr + k * TPR;
+      float h[V], g[V], e[V];
+      widen<I>(hr[k], h);
+      widen<I>(gr[k], g);
+      widen<I>(er[k], e);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = rstd * w[k][i] * g[i] - s * h[i];
+        e[i] = a.res ? d + e[i] : d;
+      }
+      if (live && c < pieces) *reinterpret_cast<uint4 *>(static_cast<I *>(a.y) + r * a.h_row + c * V) = narrow<I>(e);
+    }
+  }
+  // this CTA's share of dw: the row groups one after another, then to its row of the partials
+  if constexpr (RPC > 1) {
+    for (int x = 0; x < RPC; ++x) {
+      if (grp == x) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int c = tr + k * TPR;
+          if (c < pieces) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              if (x == 0) dsh[c * V + i] = dw[k][i];
+              else dsh[c * V + i] += dw[k][i];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < a.D; i += NTH) a.part[(long long)blockIdx.x * a.D + i] = dsh[i];
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = tr + k * TPR;
+      if (c < pieces) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+          *reinterpret_cast<float4 *>(a.part + (long long)blockIdx.x * a.D + c * V + i) =
+              make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
+      }
+    }
+  }
+}
+
+template <typename I> __global__ void __launch_bounds__(256) norm_bwd_any_kernel(NormArgs a) {
+  __shared__ float sh[2 * 8];
+  pdl_trigger();
+  pdl_wait();
+  int turn = 0;
+  float *part = a.part + (long long)blockIdx.x * a.D;  // thread t owns columns t, t + 256, ...
+  for (int i = threadIdx.x; i < a.D; i += 256) part[i] = 0.f;
+  for (long long r = blockIdx.x; r < a.T; r += gridDim.x) {
+    const I *g = static_cast<const I *>(a.x) + r * a.y_row, *h = static_cast<const I *>(a.h) + r * a.x_row;
+    const I *e = a.res ? static_cast<const I *>(a.res) + r * a.r_row : nullptr;
+    const float rstd = a.rstd_in[r];
+    float dot = 0.f;
+    for (int i = threadIdx.x; i < a.D; i += 256) dot += tof(g[i]) * (a.weight[i] + a.off) * tof(h[i]);
+    const float s = row_reduce<256, false>(dot, sh, turn) / a.D * rstd * rstd * rstd;
+    for (int i = threadIdx.x; i < a.D; i += 256) {
+      const float gi = tof(g[i]), hi = tof(h[i]);
+      part[i] += gi * (hi * rstd);
+      const float d = rstd * (a.weight[i] + a.off) * gi - s * hi;
+      static_cast<I *>(a.y)[r * a.h_row + i] = fromf<I>(e ? d + tof(e[i]) : d);
+    }
+  }
+}
+
+// dw = the partial rows, added in order: eight threads per column take every eighth row, then join
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float *part, int rows, int D, float *dw) {
+  __shared__ float sh[8][33];
+  pdl_trigger();
+  pdl_wait();
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+  float s = 0.f;
+  if (c < D) {
+#pragma unroll 8
+    for (int r = y; r < rows; r += 8) s += part[(long long)r * D + c];
+  }
+  sh[y][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (y == 0 && c < D) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
+    dw[c] = s;
+  }
+}
+
+namespace {
+
+template <typename I, int NTH, int TPR, int NV> cudaError_t fwd(const NormArgs &a, int sms, cudaStream_t st) {
+  static const int per_sm = [] {  // resident CTAs of this kernel, the same on every GB300
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_fwd_kernel<I, NTH, TPR, NV>, NTH, 0) == cudaSuccess && n > 0 ? n : 1;
+  }();
+  const long long want = (a.T + NTH / TPR - 1) / (NTH / TPR), cap = (long long)sms * per_sm;
+  return launch_pdl(norm_fwd_kernel<I, NTH, TPR, NV>, dim3((unsigned)(want < cap ? want : cap)), dim3(NTH), 0, st, a);
+}
+// how many threads hold a row, and how many pieces each: the first shape that holds it (0: none)
+int row_shape(const NormArgs &a, int V, int sms) {
+  const int pieces = a.D / V;
+  if (pieces <= 32 * 4) return a.T < sms && pieces > 32 ? (pieces <= 128 ? 2 : 3) : (pieces <= 32 ? 0 : 1);
+  if (pieces <= 128 * 4) return a.T < sms && pieces > 128 ? 4 : 3;
+  return pieces <= 512 ? 4 : (pieces <= 512 * 4 ? 5 : -1);
+}
+template <typename I> cudaError_t fwd_shape(const NormArgs &a, int sms, cudaStream_t st) {
+  switch (row_shape(a, Vec<I>::N, sms)) {
+    case 0: return fwd<I, 128, 32, 1>(a, sms, st);
+    case 1: return fwd<I, 128, 32, 4>(a, sms, st);
+    case 2: return fwd<I, 128, 128, 1>(a, sms, st);
+    case 3: return fwd<I, 128, 128, 4>(a, sms, st);
+    case 4: return fwd<I, 512, 512, 1>(a, sms, st);
+    case 5: return fwd<I, 512, 512, 4>(a, sms, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+constexpr int BWD_PER_SM = 2;
+template <typename I, int NTH, int TPR, int NV> cudaError_t bwd(const NormArgs &a, int ctas, cudaStream_t st) {
+  const size_t smem = NTH > TPR ? (size_t)a.D * 4 : 0;
+  return launch_pdl(norm_bwd_kernel<I, NTH, TPR, NV>, dim3(ctas), dim3(NTH), smem, st, a);
+}
+template <typename I> int bwd_rows_per_cta(const NormArgs &a, int sms) {
+  switch (row_shape(a, Vec<I>::N, sms)) {
+    case 0: case 1: return 8;
+    case 2: case 3: return 2;
+  }
+  return 1;
+}
+template <typename I> cudaError_t bwd_shape(const NormArgs &a, int sms, int ctas, cudaStream_t st) {
+  switch (row_shape(a, Vec<I>::N, sms)) {
+    case 0: return bwd<I, 256, 32, 1>(a, ctas, st);
+    case 1: return bwd<I, 256, 32, 4>(a, ctas, st);
+    case 2: return bwd<I, 256, 128, 1>(a, ctas, st);
+    case 3: return bwd<I, 256, 128, 4>(a, ctas, st);
+    case 4: return bwd<I, 512, 512, 1>(a, ctas, st);
+    case 5: return bwd<I, 512, 512, 4>(a, ctas, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+bool in_registers(const NormArgs &a, bool bf, bool vec, int sms) { return vec && row_shape(a, bf ? 8 : 4, sms) >= 0; }
+
+}  // namespace
+
+int norm_bwd_ctas(const NormArgs &a, bool bf, bool vec, int sms) {
+  const long long cap = (long long)sms * BWD_PER_SM;
+  long long rows = 1;
+  if (in_registers(a, bf, vec, sms)) rows = bf ? bwd_rows_per_cta<bf16>(a, sms) : bwd_rows_per_cta<float>(a, sms);
+  const long long want = (a.T + rows - 1) / rows;
+  return (int)(want < cap ? (want > 0 ? want : 1) : cap);
+}
+
+cudaError_t launch_norm_fwd(const NormArgs &a, bool bf, bool vec, int sms, cudaStream_t st) {
+  if (in_registers(a, bf, vec, sms)) return bf ? fwd_shape<bf16>(a, sms, st) : fwd_shape<float>(a, sms, st);
+  const unsigned grid = (unsigned)(a.T < 8ll * sms ? a.T : 8ll * sms);
+  return bf ? launch_pdl(norm_fwd_any_kernel<bf16>, dim3(grid), dim3(256), 0, st, a)
+            : launch_pdl(norm_fwd_any_kernel<float>, dim3(grid), dim3(256), 0, st, a);
+}
+
+cudaError_t launch_norm_bwd(const NormArgs &a, bool bf, bool vec, int sms, cudaStream_t st) {
+  const int ctas = norm_bwd_ctas(a, bf, vec, sms);
+  cudaError_t e;
+  if (in_registers(a, bf, vec, sms)) {
+    e = bf ? bwd_shape<bf16>(a, sms, ctas, st) : bwd_shape<float>(a, sms, ctas, st);
+  } else {
+    e = bf ? launch_pdl(norm_bwd_any_kernel<bf16>, dim3(ctas), dim3(256), 0, st, a)
+           : launch_pdl(norm_bwd_any_kernel<float>, dim3(ctas), dim3(256), 0, st, a);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_dw_kernel, dim3((a.D + 31) / 32), dim3(256), 0, st, (const float *)a.part, ctas, a.D, a.dw);
+}
+
+}  // namespace gdn

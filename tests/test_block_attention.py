@@ -1,0 +1,323 @@
+"""Attention over a paged cache against the definition in 64 bits, and its refusals.
+
+Bounds.  bf16: the products are exact and the sums fp32; the weights are rounded to bf16 before the second product
+(at most 2^-8 of each, so 2^-8 sum p |v|) and the output once (2^-8 |o|); 5 % on top for fp32 sums and the power of two.
+fp32: each product loses at most 2^-20 of its magnitude (three TF32 parts), the logits sum D of them:
+|ds| <= 2^-20 scale sum |q k|, which is below 8e-6 for the N(0, 1) inputs here; a weight is off by at most twice that,
+and the second product adds 2^-20: 3e-5 sum p |v| holds with room for fp32 sums.  lse: |ds| plus fp32 rounding."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from gated_deltanet_linear_15_gb300 import _lib
+from tests import block_ref as ref
+
+gpu = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    return _lib.load()
+
+
+def make(seqs, dtype, D, Hkv, G, page, seed=0, head_major=False, spare=3, dev=DEV, fill=float("nan")):
+    """seqs: (new, cached) tokens of each.  Every slot that holds no token is `fill` (NaN)."""
+    gen = torch.Generator().manual_seed(seed)
+    qs, ks = [s[0] for s in seqs], [s[1] for s in seqs]
+    need = [-(-k // page) for k in ks]
+    width = max(max(need), 1) + 1
+    perm = torch.randperm(sum(need) + spare, generator=gen)
+    shape = (sum(need) + spare, Hkv, page, D) if head_major else (sum(need) + spare, page, Hkv, D)
+    kc, vc = torch.full(shape, fill), torch.full(shape, fill)
+    if head_major:
+        kc, vc = kc.transpose(1, 2), vc.transpose(1, 2)
+    table = torch.full((len(seqs), width), -1, dtype=torch.int32)
+    at = 0
+    for n, k in enumerate(ks):
+        for j in range(need[n]):
+            pg = int(perm[at])
+            at += 1
+            table[n, j] = pg
+            m = min(page, k - j * page)
+            kc[pg, :m], vc[pg, :m] = torch.randn(m, Hkv, D, generator=gen), torch.randn(m, Hkv, D, generator=gen)
+    q = torch.randn(sum(qs), Hkv * G, D, generator=gen)
+    kc, vc = kc.to(dev, dtype), vc.to(dev, dtype)  # .to keeps the head-major strides
+    return dict(q=q.to(dev, dtype), k_cache=kc, v_cache=vc, page_table=table.to(dev),
+                kv_lens=torch.tensor(ks, dtype=torch.int32, device=dev)), qs
+
+
+def close(o, lse, x, qs, scale, window=0):
+    ro, rl, mag = ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["kv_lens"], qs, scale, window)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    if x["q"].dtype == torch.bfloat16:
+        tol = 1.05 * 2 ** -8 * (ro.abs() + mag) + 1e-30
+    else:
+        tol = 3e-5 * mag + 1e-30
+    assert torch.isfinite(o).all()
+    bad = (o - ro).abs() > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, worst {((o - ro).abs() / tol).max():.2f} of the bound"
+    empty = rl == -math.inf
+    assert torch.equal(lse == -math.inf, empty)
+    assert (o[empty] == 0).all()
+    if (~empty).any():
+        assert ((lse - rl)[~empty].abs() <= 1e-5 + 1e-6 * rl[~empty].abs()).all()
+
+
+BF, F32 = torch.bfloat16, torch.float32
+CASES = [
+    # (new, cached) tokens, dtype, D, Hkv, G, page, window
+    ([(1, 1)], BF, 128, 1, 1, 16, 0),
+    ([(1, 17)], BF, 64, 2, 3, 16, 0),
+    ([(1, 100), (1, 1), (1, 64), (1, 333)], BF, 128, 2, 4, 16, 0),
+    ([(1, 1000), (1, 129)], BF, 64, 1, 16, 64, 0),
+    ([(4, 300), (4, 4), (4, 67)], BF, 128, 2, 4, 32, 0),
+    ([(5, 257), (0, 40), (1, 40), (3, 3)], BF, 128, 1, 6, 128, 0),
+    ([(70, 200), (1, 90), (33, 33)], BF, 128, 2, 2, 16, 0),
+    ([(300, 300)], BF, 64, 1, 4, 64, 0),
+    ([(130, 1000)], BF, 128, 1, 1, 256, 0),
+    ([(1, 500), (40, 333)], BF, 128, 2, 4, 16, 37),
+    ([(1, 500), (200, 400)], BF, 64, 1, 8, 32, 16),
+    ([(1, 3000)], BF, 128, 1, 2, 64, 1),
+    ([(9, 4), (2, 0), (1, 7)], BF, 128, 2, 4, 16, 0),        # fewer cached tokens than new ones: the first see nothing
+    ([(140, 12)], BF, 128, 1, 2, 16, 0),
+    ([(1, 0), (1, 0)], BF, 64, 1, 1, 16, 0),
+    ([(1, 1)], F32, 64, 1, 1, 16, 0),
+    ([(1, 300), (1, 77)], F32, 128, 2, 4, 32, 0),
+    ([(40, 100), (1, 50), (0, 9), (17, 17)], F32, 64, 2, 3, 16, 0),
+    ([(90, 333)], F32, 128, 1, 2, 64, 50),
+    ([(3, 1)], F32, 64, 2, 2, 16, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("seqs,dtype,D,Hkv,G,page,window", CASES)
+@pytest.mark.parametrize("hint", [True, False])
+def test_matches_definition(seqs, dtype, D, Hkv, G, page, window, hint):
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make(seqs, dtype, D, Hkv, G, page, seed=len(seqs) + D + G)
+    o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs) if hint else 1, window=window, return_lse=True)
+    close(o, lse, x, qs, D ** -0.5, window)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,D,G,q", [(BF, 128, 4, 1), (BF, 64, 2, 40), (F32, 64, 2, 3), (BF, 128, 4, 150)])
+def test_strided_inputs_and_scale(dtype, D, G, q):
+    """q as a slice of a wider projection, head-major caches, a table that is a slice, an output view, another scale, and
+    equal new lengths without cu_q."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(q, q + 31), (q, q + 160)], dtype, D, 2, G, 32, seed=3, head_major=True)
+    T, Hq = x["q"].shape[:2]
+    assert x["k_cache"].stride(1) == D
+    wide = torch.full((T, Hq + 4, D), float("nan"), dtype=dtype, device=DEV)
+    wide[:, 2:2 + Hq] = x["q"]
+    x["q"] = wide[:, 2:2 + Hq]
+    tab = torch.full((2, x["page_table"].shape[1] + 5), 1 << 30, dtype=torch.int32, device=DEV)
+    tab[:, 1:-4] = x["page_table"]
+    x["page_table"] = tab[:, 1:-4]
+    out = torch.full((T, 2 * Hq, D), 7.0, dtype=dtype, device=DEV)
+    o, lse = g.paged_attention(**x, max_q=q, scale=0.31, return_lse=True, out=out[:, Hq:])
+    assert (out[:, :Hq] == 7).all()
+    close(o, lse, x, qs, 0.31)
+
+
+@gpu
+def test_long_context_is_split_and_joined():
+    """A single sequence that many CTAs share, decoded and drafted, and a ragged batch; two calls agree bit for bit."""
+    import gated_deltanet_linear_15_gb300 as g
+    for seqs, G in (([(1, 20001)], 4), ([(4, 9999)], 8), ([(1, 5000), (1, 31), (2, 7777), (1, 0)], 2), ([(150, 4000)], 2)):
+        x, qs = make(seqs, BF, 128, 1, G, 64, seed=5)
+        a = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), return_lse=True)
+        b = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), return_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        close(*a, x, qs, 128 ** -0.5)
+
+
+@gpu
+def test_peaked_and_growing_logits():
+    """Logits that grow along the context (the maximum rises at every step) and by far more than fp32's exponent range
+    would bear without it."""
+    import gated_deltanet_linear_15_gb300 as g
+    for q in (1, 140):
+        x, qs = make([(q, 900)], BF, 128, 1, 2, 64, seed=7)
+        P = x["k_cache"].shape[1]
+        for j in range(-(-900 // P)):
+            pg = int(x["page_table"][0, j])
+            ramp = torch.linspace(j, j + 1, P, device=DEV)[:, None, None]
+            x["k_cache"][pg] = (x["q"][-1, 0] * ramp * 0.7).to(BF)
+        o, lse = g.paged_attention(**x, max_q=q, return_lse=True)
+        ro, rl, mag = ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["kv_lens"], qs, 128 ** -0.5)
+        # the logits reach several hundred: fp32 sums are off by up to 128 * 2^-24 of their magnitude
+        slack = 128 * 2 ** -24 * 128 ** -0.5 * float((x["q"].float().abs().max() ** 2) * 0.7 * 15 * 128)
+        assert ((o.cpu().double() - ro).abs() <= (2.1 * 2 ** -8 + 2 * slack) * mag).all()
+        assert ((lse.cpu().double() - rl).abs() <= slack + 1e-6 * rl.abs()).all()
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes and more than 2^31 elements, its last pages in use."""
+    import gated_deltanet_linear_15_gb300 as g
+    pages, P, H, D = 66000, 64, 4, 128
+    kc = torch.empty(pages, P, H, D, dtype=BF, device=DEV)
+    vc = torch.empty(pages, P, H, D, dtype=BF, device=DEV)
+    assert kc.numel() > 1 << 31
+    for q in (1, 70):
+        x, qs = make([(q, 300)], BF, D, H, 2, P, seed=9, spare=0)
+        far = pages - 1 - torch.arange(5, device=DEV) * 3
+        near = x["page_table"][0, :5].long()
+        kc[far], vc[far] = x["k_cache"][near], x["v_cache"][near]
+        table = far.to(torch.int32)[None].contiguous()
+        o, lse = g.paged_attention(x["q"], kc, vc, table, x["kv_lens"], max_q=q, return_lse=True)
+        close(o, lse, x, qs, D ** -0.5)
+
+
+@gpu
+def test_bad_device_data_stays_in_bounds():
+    """Page numbers outside the pool count as pages of zeros, lengths are cut to the table, cu_q to the tokens."""
+    import gated_deltanet_linear_15_gb300 as g
+    for q in (2, 140):
+        x, qs = make([(q, 200)], BF, 128, 1, 2, 64, seed=11)
+        bad = dict(x, page_table=x["page_table"].clone())
+        bad["page_table"][0, 1] = 1 << 30
+        zero = dict(x, k_cache=x["k_cache"].clone(), v_cache=x["v_cache"].clone())
+        zero["k_cache"][int(x["page_table"][0, 1])] = 0
+        zero["v_cache"][int(x["page_table"][0, 1])] = 0
+        a, b = g.paged_attention(**bad, max_q=q), g.paged_attention(**zero, max_q=q)
+        assert torch.equal(a, b)
+        long = dict(x, kv_lens=torch.full_like(x["kv_lens"], 2 ** 31 - 1))
+        g.paged_attention(**long, max_q=q)
+        g.paged_attention(**dict(x, kv_lens=torch.full_like(x["kv_lens"], -5)), max_q=q)
+        g.paged_attention(**x, cu_q=torch.tensor([-7, 10 ** 6], dtype=torch.int32, device=DEV), max_q=q)
+        torch.cuda.synchronize()
+
+
+@gpu
+def test_non_finite_values_reach_only_their_readers():
+    """A NaN in one cached value of an early token reaches every query; infinities and NaN behind a window, in later
+    tokens' tiles or in free slots reach none."""
+    import gated_deltanet_linear_15_gb300 as g
+    for q in (1, 150):
+        x, qs = make([(q, 1200)], BF, 128, 1, 2, 64, seed=13)
+        lo = 1200 - q - 200 + 1
+        for t in range(0, lo - 1, 7):
+            pg = int(x["page_table"][0, t // 64])
+            x["k_cache"][pg, t % 64] = float("inf")
+            x["v_cache"][pg, t % 64] = float("nan")
+        o, lse = g.paged_attention(**x, max_q=q, window=200, return_lse=True)
+        close(o, lse, dict(x, k_cache=x["k_cache"].nan_to_num(0, 0, 0), v_cache=x["v_cache"].nan_to_num(0, 0, 0)), qs, 128 ** -0.5, 200)
+        y, qs = make([(q, 300)], BF, 128, 1, 2, 64, seed=14)
+        y["v_cache"][int(y["page_table"][0, 0]), 3, 0, 5] = float("nan")
+        o = g.paged_attention(**y, max_q=q)
+        assert torch.isnan(o[:, :, 5]).all() and torch.isfinite(o[:, :, :5]).all()
+
+
+@gpu
+def test_runs_on_the_current_stream():
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(1, 3000)], BF, 128, 2, 4, 64, seed=15)
+    want = g.paged_attention(**x, max_q=1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = {k: v.clone() for k, v in x.items()}
+        got = g.paged_attention(**y, max_q=1)
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+@gpu
+def test_captured_in_a_graph():
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(1, 700), (1, 20)], BF, 128, 2, 4, 64, seed=16)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(x["q"])
+    g.paged_attention(**x, max_q=1, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.paged_attention(**x, max_q=1, out=out, workspace=ws)
+    x["kv_lens"][0] -= 100  # the graph reads the lengths of the replay
+    x["q"].mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, g.paged_attention(**x, max_q=1))
+
+
+@gpu
+@pytest.mark.parametrize("change", [
+    dict(q=lambda t: t.half()), dict(q=lambda t: t[:, :3]), dict(q=lambda t: t.cpu()), dict(kv_lens=lambda t: t.long()),
+    dict(page_table=lambda t: t[:, ::2]), dict(page_table=lambda t: t.long()), dict(k_cache=lambda t: t[..., :64]),
+    dict(v_cache=lambda t: t.float()), dict(q=lambda t: t[..., :100]), dict(kv_lens=lambda t: t[:1]),
+])
+def test_binding_refuses(change):
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(1, 20), (1, 30)], BF, 128, 2, 2, 16)
+    for k, f in change.items():
+        x[k] = f(x[k])
+    with pytest.raises((ValueError, RuntimeError)):
+        g.paged_attention(**x, max_q=1)
+
+
+# ------------------------------------------------------------------ refusals of the C entry point (no GPU needed)
+def _shape(**kw):
+    s = _lib.GdnPagedShape()
+    s.num_seqs, s.total_q, s.num_heads, s.num_kv_heads, s.head_dim = 2, 4, 8, 2, 128
+    s.page_size, s.num_pages, s.max_pages, s.dtype, s.max_q, s.scale, s.table_stride = 16, 100, 10, _lib.GDN_BF16, 2, 0.1, 10
+    s.q_tok, s.q_head, s.o_tok, s.o_head = 1024, 128, 1024, 128
+    s.k_page = s.v_page = 16 * 256
+    s.k_tok = s.v_tok = 256
+    s.k_head = s.v_head = 128
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def _call(lib, s, ws=1 << 40, **p):
+    a = dict(q=0x10000, k=0x10000, v=0x10000, table=0x10000, cu=0x10000, kv=0x10000, o=0x10000, lse=None, w=0x10000)
+    a.update(p)
+    return lib.gdn_paged_attn_fwd(ctypes.byref(s), a["q"], a["k"], a["v"], a["table"], a["cu"], a["kv"], a["o"], a["lse"],
+                                  a["w"], ws, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(head_dim=96), 2), (dict(head_dim=256), 2), (dict(num_heads=7), 1), (dict(num_kv_heads=0), 1), (dict(dtype=5), 1),
+    (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=8192), 2), (dict(num_pages=0), 1), (dict(total_q=-1), 1),
+    (dict(window=-1), 1), (dict(max_q=-1), 1), (dict(scale=math.inf), 1), (dict(reserved=1), 1), (dict(q_tok=1020), 1),
+    (dict(k_head=-128), 1), (dict(v_tok=4), 1), (dict(table_stride=9), 1), (dict(total_q=1 << 30), 2),
+])
+def test_c_entry_refuses_shapes(lib, kw, code):
+    s = _shape(**kw)
+    assert _call(lib, s) == code
+    assert lib.gdn_last_error_string() != b""
+    assert lib.gdn_paged_attn_workspace_size(ctypes.byref(s)) == 0
+
+
+def test_c_entry_refuses_pointers(lib):
+    s = _shape()
+    need = lib.gdn_paged_attn_workspace_size(ctypes.byref(s))
+    assert need > 0
+    for name in ("q", "k", "v", "table", "kv", "o"):
+        assert _call(lib, s, **{name: None}) == 1, name
+    for name in ("q", "k", "v", "o", "w"):
+        assert _call(lib, s, **{name: 0x10008}) == 1, name
+    assert _call(lib, s, ws=need - 1) == 3 and b"workspace" in lib.gdn_last_error_string()
+    assert _call(lib, s, w=None) == 3
+    assert _call(lib, _shape(total_q=5), cu=None) == 1   # not the same number for each of two sequences
+    assert lib.gdn_paged_attn_fwd(None, *[0x10000] * 9, 1 << 40, None) == 1
+    assert _call(lib, _shape(total_q=0)) == 0            # nothing to do: no launch
+
+
+def test_header_and_binding_agree(lib):
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(_lib.__file__), "..", "include", "gdn_block.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    declared = sorted(set(re.findall(r"\b(gdn_[a-z_]+)\s*\(", src)))
+    assert declared == sorted(_lib.BLOCK_EXPORTS)
+    for name in declared:
+        assert hasattr(lib, name)

@@ -1,0 +1,249 @@
+"""Upkeep of a paged cache against the rules in plain Python: tables, counts and lengths have to be equal, copies exact."""
+import ctypes
+import random
+
+import pytest
+import torch
+
+from gated_deltanet_linear_15_gb300 import _lib
+from tests.block_ref import Pages
+
+gpu = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    return _lib.load()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+class Device:
+    """The tensors of a cache beside their Python model; two pools and a state tensor whose slots are told apart by value."""
+
+    def __init__(self, seqs, width, pages, page, strided=False):
+        self.m = Pages(seqs, width, pages, page)
+        wide = torch.full((seqs, width + (3 if strided else 0)), -1, dtype=torch.int32, device=DEV)
+        self.table = wide[:, :width]
+        self.lens, self.ref = ints([0] * seqs), ints([0] * pages)
+        gen = torch.Generator(device=DEV).manual_seed(pages)
+        self.pools = [torch.randn(pages, page, 2, 24, generator=gen, device=DEV).bfloat16(),
+                      torch.randn(pages, 3 if not strided else 5, 8, generator=gen, device=DEV)[:, :3]]
+        self.states = torch.randn(seqs, 2, 6, 10, generator=gen, device=DEV)
+
+    def same(self):
+        assert self.table.tolist() == self.m.table
+        assert self.lens.tolist() == self.m.lens
+        assert self.ref.tolist() == self.m.ref
+
+    def extend(self, g, seqs, add):
+        ok = g.extend_pages(self.table, self.lens, self.ref, ints(seqs), ints(add), self.m.page)
+        assert ok.tolist() == self.m.extend(seqs, add)
+        self.same()
+
+    def fork(self, g, parents, children):
+        pools, states = [p.clone() for p in self.pools], self.states.clone()
+        new = g.fork_pages(self.table, self.lens, self.ref, ints(parents), ints(children), self.pools, self.m.page, [self.states])
+        want, copies, moved = self.m.fork(parents, children)
+        assert new.tolist() == want
+        for a, b in copies:
+            for p in pools:
+                p[b] = p[a]
+        for a, b in moved:
+            states[b] = states[a]
+        assert all(torch.equal(x, y) for x, y in zip(pools, self.pools)) and torch.equal(states, self.states)
+        self.same()
+
+    def free(self, g, seqs):
+        g.free_pages(self.table, self.lens, self.ref, ints(seqs))
+        self.m.free(seqs)
+        self.same()
+
+    def compact(self, g, inplace):
+        pools = [p.clone() for p in self.pools]
+        old = self.table.clone(), self.ref.clone()
+        table, ref, moves = g.compact_pages(self.table, self.ref, self.pools, inplace=inplace)
+        if not inplace:
+            assert torch.equal(self.table, old[0]) and torch.equal(self.ref, old[1])
+            self.table, self.ref = table, ref
+        pairs = self.m.compact()
+        assert int(moves) == len(pairs)
+        for s, d in pairs:
+            for p in pools:
+                p[d] = p[s]
+        assert all(torch.equal(x, y) for x, y in zip(pools, self.pools))
+        self.same()
+
+
+@gpu
+@pytest.mark.parametrize("seqs,width,pages,page,strided", [(4, 3, 8, 4, False), (9, 40, 200, 16, True), (30, 300, 9000, 16, False),
+                                                          (1, 1, 1, 16, False), (1500, 4, 5000, 8, True)])
+def test_a_life_of_requests(seqs, width, pages, page, strided):
+    import gated_deltanet_linear_15_gb300 as g
+    r = random.Random(seqs * 31 + pages)
+    d = Device(seqs, width, pages, page, strided)
+    for step in range(14):
+        some = r.sample(range(seqs), r.randint(1, seqs))
+        d.extend(g, some, [r.choice([0, 1, page - 1, page, r.randint(0, width * page)]) for _ in some])
+        empty = [s for s in range(seqs) if d.m.lens[s] == 0]
+        full = [s for s in range(seqs) if d.m.lens[s]]
+        if empty and full:
+            children = r.sample(empty, r.randint(1, len(empty)))
+            d.fork(g, [r.choice(full) for _ in children], children)
+        d.free(g, r.sample(range(seqs), r.randint(0, seqs // 2)) or [0])
+        if step % 3 == 2:
+            d.compact(g, inplace=step % 2 == 0)
+
+
+@gpu
+def test_fork_shares_full_pages_only():
+    import gated_deltanet_linear_15_gb300 as g
+    d = Device(5, 6, 20, 16)
+    d.extend(g, [0, 1], [40, 32])
+    d.fork(g, [0, 1, 0], [2, 3, 4])
+    assert d.m.ref[:3] == [3, 3, 1] and d.m.table[3] == d.m.table[1]
+    d.extend(g, [0, 2, 4], [3, 9, 1])     # each writes into a last page of its own
+    d.free(g, [0, 1])
+    d.compact(g, True)
+
+
+@gpu
+def test_out_of_pages_and_bad_requests():
+    import gated_deltanet_linear_15_gb300 as g
+    d = Device(6, 4, 5, 16)
+    d.extend(g, [0, 1, 2, 3], [33, 20, 0, 5])          # 3 + 2 pages, then one that is not there
+    d.extend(g, [4, 0], [1, 15])                       # no page, but room in a last page
+    d.extend(g, [7, -1, 0, 5], [1, 1, -4, 65])         # bad numbers, a row that is too short
+    d.fork(g, [0, 0, 9, 1], [4, 1, 5, -2])             # no page; child not empty; bad parent; bad child
+    d.free(g, [1])
+    d.fork(g, [0, 0, 0, 3], [1, 4, 5, 2])              # two pages for three children; an empty parent
+    d.free(g, [0, -1, 77])
+
+
+@gpu
+def test_shared_partial_page_is_not_extended():
+    """A table that shares a partly filled page (no fork makes one) cannot grow into it."""
+    import gated_deltanet_linear_15_gb300 as g
+    table, lens, ref = ints([[0, -1], [0, -1]]), ints([5, 5]), ints([2, 0])
+    assert g.extend_pages(table, lens, ref, ints([0, 1]), ints([1, 0]), 16).tolist() == [0, 1]
+    assert lens.tolist() == [5, 5] and ref.tolist() == [2, 0]
+
+
+@gpu
+def test_sequence_named_twice_is_freed_once():
+    import gated_deltanet_linear_15_gb300 as g
+    table, lens, ref = ints([[0, 1], [0, -1]]), ints([20, 16]), ints([2, 1])
+    g.free_pages(table, lens, ref, ints([0, 0, 0]))
+    assert ref.tolist() == [1, 0] and table.tolist() == [[-1, -1], [0, -1]] and lens.tolist() == [0, 16]
+
+
+@gpu
+@pytest.mark.parametrize("slots,inner,dtype", [(7, 8, torch.float32), (40, 50000, torch.bfloat16), (3, 16384, torch.int8)])
+def test_copy_slots(slots, inner, dtype):
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator(device=DEV).manual_seed(slots)
+    pools = [torch.randint(-100, 100, (slots, inner + 16 * i), generator=gen, device=DEV).to(dtype) for i in range(70)]
+    src, dst = [0, 2, -1, 1, slots], [slots - 1, 1 if slots < 5 else 4, 0, -5, 0]
+    src, dst = (src, dst) if slots > 3 else ([0, -1], [2, 1])
+    want = [p.clone() for p in pools]
+    for p in want:
+        for a, b in zip(src, dst):
+            if 0 <= a < slots and 0 <= b < slots:
+                p[b] = p[a]
+    g.copy_slots(pools, ints(src), ints(dst))
+    assert all(torch.equal(a, b) for a, b in zip(want, pools))
+    g.copy_slots(pools, ints([]), ints([]))
+    g.copy_slots([], ints(src), ints(dst))
+
+
+@gpu
+def test_offsets_past_32_bits():
+    import gated_deltanet_linear_15_gb300 as g
+    pool = torch.empty(1300, 1 << 22, dtype=torch.int8, device=DEV)
+    pool[1299], pool[700], pool[0] = 3, 2, 1
+    g.copy_slots([pool], ints([1299, 0]), ints([600, 1298]))
+    assert (pool[600] == 3).all() and (pool[1298] == 1).all() and (pool[700] == 2).all()
+
+
+@gpu
+def test_binding_refuses():
+    import gated_deltanet_linear_15_gb300 as g
+    table, lens, ref = ints([[-1, -1]]), ints([0]), ints([0, 0])
+    pool = torch.zeros(2, 16, device=DEV)
+    with pytest.raises(ValueError):
+        g.extend_pages(table, lens, ref, ints([0]), ints([1, 2]), 16)
+    with pytest.raises(ValueError):
+        g.free_pages(table.long(), lens, ref, ints([0]))
+    with pytest.raises(ValueError):
+        g.fork_pages(table, ints([0, 0]), ref, ints([0]), ints([0]), [pool], 16)
+    with pytest.raises(ValueError):
+        g.copy_slots([torch.zeros(4, 4, 4, device=DEV).transpose(1, 2)], ints([0]), ints([1]))
+    with pytest.raises(RuntimeError):
+        g.copy_slots([torch.zeros(4, 3, device=DEV)], ints([0]), ints([1]))       # 12 bytes
+    with pytest.raises(RuntimeError):
+        g.extend_pages(table, lens, ref, ints([0]), ints([1]), 0)
+    with pytest.raises(ValueError):
+        g.compact_pages(table, ref.cpu())
+
+
+# ------------------------------------------------------------------ refusals of the C entry points (no GPU needed)
+def _shape(**kw):
+    s = _lib.GdnPagesShape()
+    s.num_seqs, s.max_pages, s.num_pages, s.page_size, s.table_stride = 4, 8, 100, 16, 8
+    for k, v in kw.items():
+        if k == "reserved":
+            s.reserved[1] = v
+        else:
+            setattr(s, k, v)
+    return s
+
+
+@pytest.mark.parametrize("kw", [dict(num_seqs=0), dict(max_pages=0), dict(num_pages=0), dict(num_pages=(1 << 20) + 1),
+                                dict(page_size=0), dict(table_stride=7), dict(reserved=1)])
+def test_c_entries_refuse_shapes(lib, kw):
+    s, p, big = _shape(**kw), 0x10000, 1 << 40
+    ref = ctypes.byref(s)
+    assert lib.gdn_pages_extend(ref, p, p, p, p, p, 1, p, p, big, None) != 0
+    assert lib.gdn_pages_fork(ref, p, p, p, p, p, 1, None, 0, None, 0, p, p, big, None) != 0
+    assert lib.gdn_pages_free(ref, p, p, p, p, 1, None) != 0
+    assert lib.gdn_pages_compact(ref, p, p, p, p, None, 0, None, p, big, None) != 0
+    assert lib.gdn_pages_workspace_size(ref, 4) == 0
+    assert lib.gdn_last_error_string() != b""
+
+
+def test_c_entries_refuse_arguments(lib):
+    s, p, big = _shape(), 0x10000, 1 << 40
+    ref = ctypes.byref(s)
+    need = lib.gdn_pages_workspace_size(ref, 5)
+    assert need > 0 and lib.gdn_pages_workspace_size(ref, -1) == 0
+    for i in range(5):
+        a = [p] * 5
+        a[i] = None
+        assert lib.gdn_pages_extend(ref, *a, 5, p, p, big, None) == 1
+        assert lib.gdn_pages_fork(ref, *a, 5, None, 0, None, 0, p, p, big, None) == 1
+    for i in range(4):
+        a = [p] * 4
+        a[i] = None
+        assert lib.gdn_pages_free(ref, *a, 5, None) == 1
+        assert lib.gdn_pages_compact(ref, *a, None, 0, None, p, big, None) == 1
+    assert lib.gdn_pages_extend(ref, p, p, p, p, p, 5, None, p, big, None) == 1
+    assert lib.gdn_pages_extend(ref, p, p, p, p, p, 5, p, p, need - 1, None) == 3
+    assert lib.gdn_pages_extend(ref, p, p, p, p, p, 5, p, None, big, None) == 3
+    assert lib.gdn_pages_extend(ref, p, p, p, p, p, -1, p, p, big, None) == 1
+    assert lib.gdn_pages_extend(ref, p, p, p, p, p, 0, p, p, big, None) == 0
+    assert lib.gdn_pages_free(ref, p, p, p, p, 0, None) == 0
+    pool = (_lib.GdnSlotPool * 1)()
+    for kw in (dict(base=None), dict(base=0x10008), dict(stride=24), dict(bytes=40), dict(bytes=8), dict(bytes=-16), dict(slots=-1)):
+        pool[0].base, pool[0].stride, pool[0].bytes, pool[0].slots = 0x10000, 32, 32, 4
+        for k, v in kw.items():
+            setattr(pool[0], k, v)
+        assert lib.gdn_slots_copy(pool, 1, p, p, 1, None) == 1, kw
+        assert lib.gdn_pages_fork(ref, p, p, p, p, p, 1, pool, 1, None, 0, p, p, big, None) == 1, kw
+    assert lib.gdn_slots_copy(None, 1, p, p, 1, None) == 1
+    assert lib.gdn_slots_copy(None, -1, p, p, 1, None) == 1
+    assert lib.gdn_slots_copy(None, 0, p, p, -1, None) == 1
