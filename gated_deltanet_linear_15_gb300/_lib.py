@@ -24,7 +24,8 @@ EXPORTS = ("gdn_fwd_workspace_size", "gdn_bwd_workspace_size", "gdn_chunk_fwd", 
 
 
 # every symbol include/gdn_block.h declares
-BLOCK_EXPORTS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_rotary_table", "gdn_rotary",
+BLOCK_EXPORTS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_paged_attn_status",
+                 "gdn_rotary_table", "gdn_rotary",
                  "gdn_rotary_append", "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork",
                  "gdn_pages_free", "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size",
                  "gdn_rmsnorm_bwd")
@@ -133,6 +134,7 @@ def load():
         Z, D = ctypes.c_size_t, ctypes.c_double
         for name, args in {
                 "gdn_paged_attn_fwd": [P] * 10 + [Z, P],
+                "gdn_paged_attn_status": [P, P, P],
                 "gdn_rotary_table": [P, _I, _I, D, P, P],
                 "gdn_rotary": [P] * 8,
                 "gdn_rotary_append": [P] * 12,

@@ -19,7 +19,7 @@ import torch
 from . import _lib
 from ._lib import GdnNormShape, GdnPagedShape, GdnPagesShape, GdnRotaryShape, GdnSlotPool
 
-__all__ = ["paged_attention", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding", "rotary_append",
+__all__ = ["paged_attention", "paged_attention_status", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding", "rotary_append",
            "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_slots", "rms_norm", "rms_norm_bwd",
            "residual_rms_norm", "NormOutput"]
 
@@ -133,6 +133,14 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, max_q: 
                                   None if lse is None else lse.data_ptr(), workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(), _stream()), "gdn_paged_attn_fwd")
     return (o, lse) if return_lse else o
+
+
+def paged_attention_status(q, k_cache, v_cache, page_table, kv_lens, workspace, cu_q=None, max_q: int = 0) -> int:
+    """Status word of the last ``paged_attention`` call with these arguments and this workspace (0: clean; see
+    gdn_paged_attn_status).  Synchronises the stream."""
+    s = _paged_shape(q, k_cache, v_cache, page_table, kv_lens, cu_q)
+    s.max_q, s.scale, s.o_tok, s.o_head = int(max_q), 1.0, q.stride(0), q.stride(1)
+    return int(_lib.load().gdn_paged_attn_status(_byref(s), workspace.data_ptr(), _stream()))
 
 
 # ------------------------------------------------------------------ rotary positions

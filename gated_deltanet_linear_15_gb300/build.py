@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
 SOURCES = ["api.cu", "plan.cu", "fwd.cu", "fwd_prep_tc.cu", "fwd_tc.cu", "bwd.cu", "bwd_chain_tc.cu", "bwd_local_tc.cu",
-           "recurrent.cu", "block_api.cu", "attn_rows.cu", "rope.cu", "pages.cu", "rmsnorm.cu"]
+           "recurrent.cu", "block_api.cu", "attn_rows.cu", "attn_chunk_tc.cu",
+           "rope.cu", "pages.cu", "rmsnorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

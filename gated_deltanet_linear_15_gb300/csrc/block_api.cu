@@ -2,6 +2,7 @@
 // delta rule (paged attention, rotary positions, cache pages, root-mean-square norm).
 #include <algorithm>
 #include <cmath>
+#include <vector>
 
 #include "block.h"
 #include "host.h"
@@ -70,23 +71,40 @@ int check_attn(const gdn_paged_shape *s) {
   return GDN_OK;
 }
 
-// The kernel of a call and its grid.  rows: up to 16 or 32 (query, head) rows per key head and tile.
+// The kernel of a call and its grid: bf16 with more than 32 (query, head) rows per key head in the longest sequence
+// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 or 32 rows).
 struct AttnPlan {
   bool tc;
   int MT, ctas;
-  size_t off_part, total;
+  size_t off_status, off_part, total;
 };
 AttnPlan attn_plan(const gdn_paged_shape *s) {
   AttnPlan p;
   const int G = s->num_heads / s->num_kv_heads;
   const long long rows = (long long)(s->max_q > 0 ? s->max_q : (s->total_q + s->num_seqs - 1) / std::max(1, s->num_seqs)) * G;
   const bool bf = s->dtype == GDN_BF16;
-  p.tc = false;
-  p.MT = bf && rows > 16 ? 32 : 16;
-  p.ctas = num_sms() * (bf ? 2 : 1);
-  p.off_part = up256((size_t)p.ctas * 2 * sizeof(int4));
+  auto strided = [](int64_t x) { return x > 0 && x < (1ll << 38); };  // what a tensor map can hold
+  p.tc = bf && rows > 32 && strided(s->k_page) && strided(s->k_tok) && strided(s->k_head) && strided(s->v_page) &&
+         strided(s->v_tok) && strided(s->v_head);
+  p.MT = p.tc ? 256 : (bf && rows > 16 ? 32 : 16);
+  p.ctas = num_sms() * (bf && !p.tc ? 2 : 1);
+  p.off_status = up256((size_t)p.ctas * 2 * sizeof(int4));
+  p.off_part = p.off_status + up256((size_t)p.ctas * sizeof(int));
   p.total = p.off_part + up256((size_t)p.ctas * 2 * record_floats(p.MT, s->head_dim) * 4);
   return p;
+}
+
+// keys or values as [pages, slots, heads, features], box = 64 features of one head, min(page_size, 128) slots
+int cache_map(CUtensorMap *m, const void *p, const gdn_paged_shape *s, int64_t page, int64_t tok, int64_t head) {
+  const EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[4] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->num_kv_heads, (cuuint64_t)s->page_size, (cuuint64_t)s->num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)head * 2, (cuuint64_t)tok * 2, (cuuint64_t)page * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)std::min(s->page_size, 128), 1}, es[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GDN_OK : fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
 // ------------------------------------------------------------------ pages
@@ -197,8 +215,15 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   a.scale_log2 = s->scale * 1.4426950408889634f;
   a.hdr = static_cast<int4 *>(ws);
   a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.off_part);
+  a.status = reinterpret_cast<int *>(static_cast<char *>(ws) + p.off_status);
   const bool bf = s->dtype == GDN_BF16;
-  {
+  if (p.tc) {
+    CUtensorMap tk, tv;
+    TRY(cache_map(&tk, k, s, s->k_page, s->k_tok, s->k_head));
+    TRY(cache_map(&tv, v, s, s->v_page, s->v_tok, s->v_head));
+    PROF("attn_chunk");
+    CK(launch_attn_chunk_tc(a, tk, tv, s->head_dim, p.ctas, st));
+  } else {
     PROF("attn_rows");
     CK(launch_attn_rows(a, bf, s->head_dim, p.MT, p.ctas, st));
   }
@@ -207,6 +232,23 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
     CK(launch_attn_join(a, bf, s->head_dim, p.MT, p.ctas, st));
   }
   return GDN_OK;
+}
+
+int gdn_paged_attn_status(const gdn_paged_shape *s, const void *ws, gdn_stream_t stream) {
+  if (check_attn(s) || need_ptr(ws, "workspace")) return -1;
+  const AttnPlan p = attn_plan(s);
+  if (cudaStreamSynchronize((Stream)stream) != cudaSuccess) return -1;
+  if (!p.tc || s->total_q == 0 || s->num_seqs == 0) return 0;
+  int word = 0;
+  try {
+    std::vector<int> st(p.ctas);
+    if (cudaMemcpy(st.data(), static_cast<const char *>(ws) + p.off_status, st.size() * sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return -1;
+    for (int x : st) word |= x ? 4 : 0;
+  } catch (...) {
+    return -1;
+  }
+  return word;
 }
 
 int gdn_rotary_table(const double *freq, int pairs, int rows, double amplitude, float *table, gdn_stream_t stream) {

@@ -27,6 +27,7 @@ struct PagedArgs {
   int N, total_q, per_seq;  // per_seq: new tokens of every sequence when cu_q is NULL
   int Hq, Hkv, G, log2P, num_pages, max_pages, window;
   float scale_log2;         // scale * log2(e): the softmax runs in powers of two
+  int *status;              // one word per CTA of the tensor-core kernel
   // cut items: headers [C][2] and records [C][2][MT * (D + 2)] (sums [MT][D], maxima [MT], masses [MT])
   int4 *hdr;
   float *part;
@@ -79,7 +80,10 @@ template <int MT> __device__ __forceinline__ int tiles_of(const PagedArgs &a, co
   return (int)(((long long)s.qlen * a.G + MT - 1) / MT);
 }
 
-// inclusive scan over the CTA's NT threads (all call it); sh holds NT / 32 values
+// barrier of the NT threads that look for the CTA's range (a CTA may have more)
+template <int NT> __device__ __forceinline__ void plan_bar() { asm volatile("bar.sync 1, %0;\n" ::"n"(NT) : "memory"); }
+
+// inclusive scan over threads 0 .. NT - 1 (all of them call it); sh holds NT / 32 values
 template <int NT> __device__ __forceinline__ long long block_scan(long long x, long long *sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -87,9 +91,9 @@ template <int NT> __device__ __forceinline__ long long block_scan(long long x, l
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
+  plan_bar<NT>();
   if (lane == 31) sh[warp] = x;
-  __syncthreads();
+  plan_bar<NT>();
   long long add = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) add += w < warp ? sh[w] : 0;
@@ -113,7 +117,7 @@ struct Cursor {
   int skip;           // units of the item that came before u
 };
 
-// Finds where this CTA's range begins.  False when it has none.  NT: threads of the CTA (a power of two, all call it).
+// Finds where this CTA's range begins.  False when it has none.  Threads 0 .. NT - 1 call it (NT a power of two).
 template <int NT, int MT, int BN>
 __device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long long (*pre)[NT + 1], long long *sh) {
   const int tid = threadIdx.x;
@@ -125,7 +129,7 @@ __device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long
   const long long inc = block_scan<NT>(cnt, sh);
   pre[0][tid + 1] = inc;
   if (tid == 0) pre[0][0] = 0;
-  __syncthreads();
+  plan_bar<NT>();
   const long long NTILE = pre[0][NT];
   // units of the tiles, NT equal shares of them
   const long long ct = (NTILE + NT - 1) / NT;
@@ -164,7 +168,7 @@ __device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long
   const long long uinc = block_scan<NT>(units * a.Hkv, sh);
   pre[1][tid + 1] = uinc;
   if (tid == 0) pre[1][0] = 0;
-  __syncthreads();
+  plan_bar<NT>();
   const long long total = pre[1][NT];
   const long long C = min((long long)gridDim.x, total);
   if (blockIdx.x >= C) return false;

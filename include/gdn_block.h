@@ -82,6 +82,11 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *shape, const void *q, const void *
                        const int32_t *page_table, const int32_t *cu_q /* nullable */, const int32_t *kv_lens, void *o,
                        float *lse /* nullable */, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/* The status word of the last gdn_paged_attn_fwd with this shape and workspace (synchronises the stream): 0, or 4 when a
+ * bounded device wait ran past its limit (that call's outputs are not reliable; gdn_device_status_code maps it), or -1 on
+ * an error. */
+int gdn_paged_attn_status(const gdn_paged_shape *shape, const void *workspace, gdn_stream_t stream);
+
 /* ------------------------------------------------------------------ rotary positions
  * The pair (a, b) of features at a position turns by the position's angle of that pair:
  *     (a, b) -> (a cos - b sin, b cos + a sin).
