@@ -7,14 +7,15 @@
 // CTA holds 256 query rows as two tiles of 128, so that while the tensor core multiplies for one tile the other tile's
 // softmax runs.  Scores and sums live in TMEM (two times 128 columns of S, two times D of O); a softmax warp reads its
 // 32 rows of S, one whole row per thread, so a row's maximum and sum need no shuffles, and writes the weights as bf16
-// over the scores, from where the second product takes them as its A operand.  O is rescaled in TMEM only when a
-// maximum of the warp rises by more than 8 (2^8, which fp32 sums and bf16 weights carry without loss).
+// over the scores, from where the second product takes them as its A operand.  A row keeps the maximum of its first
+// block as long as the weights of later blocks sum to less than 2^40 against it; O is rescaled in TMEM only when they
+// do not, and most blocks look for no maximum at all.
 //
 // Warps: 0-3 and 4-7 the softmax of the two tiles, 8 issues every product, 9 loads.  Keys and values come in 128-token
 // tiles through a ring, one TMA box per page and 64 features; a page outside the pool, or outside what the rows see,
-// is loaded from an out-of-range coordinate, which fills zeros.  (Warps 10 and 11 only complete the third warpgroup,
-// which gives up registers: 168 a thread at launch become 224 for the softmax, which holds a row of S, and 56 here.)  Slots past the last key (or before the first of a
-// window) may hold anything, so warp 8 clears their value rows before the product that would multiply them by zero.
+// is loaded from an out-of-range coordinate, which fills zeros.  (Warps 10 and 11 only complete the third warpgroup, which
+// gives up registers: 168 a thread at launch become 224 for the softmax, which holds a row of S, and 56 here.)  Slots past the last key (or before the first of a
+// window) may hold anything, so their value rows are cleared before the product that would multiply them by zero.
 // The work split over CTAs is paged.cuh's.  Every wait is bounded; one that expires ends the CTA with a status word.
 #include "paged.cuh"
 #include "umma.cuh"
@@ -26,7 +27,7 @@ using namespace umma;
 namespace {
 
 constexpr int NTHR = 384, SOFT = 256, MT = 256, BN = 128;
-constexpr float RAISE = 8.f;
+constexpr float RAISED = 1099511627776.f;  // 2^40: a block's weights that sum to more have their maximum raised
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major, bool neg_a) {
@@ -44,7 +45,7 @@ template <int D> struct Cfg {
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
 struct Bars {
-  uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t full[8], empty[8], q_full[2], s_full[2], o_full[2], drain[2];
   uint32_t tmem;
   int dead;
 };
@@ -94,6 +95,19 @@ __device__ __forceinline__ void tmem_st32_nw(uint32_t taddr, const uint32_t *r) 
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// one lane of the warp, chosen so that the compiler knows it: products issued behind `lane == 0` instead leave the tensor
+// core idle between them (350 us against 256 us for 2048 tokens after 8192, 32 heads)
+__device__ __forceinline__ bool elect1() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred P;\nelect.sync _|P, 0xffffffff;\nselp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// 32 bytes of one thread, 32-byte aligned: whole sectors, though the rows of neighbouring threads lie apart
+__device__ __forceinline__ void st_global_32b(void *p, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+               "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // packed pairs of fp32
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
@@ -112,11 +126,39 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// bounded wait; gives up at once when another role of the CTA has
+// keeps what is computed from v where it is used, instead of in registers across the loop
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+// cursor_next of a cursor in shared memory: lane 0 moves it for the warp
+__device__ __forceinline__ bool cursor_advance(const PagedArgs &a, Cursor &shared, int n) {
+  bool more = false;
+  if ((threadIdx.x & 31) == 0) {
+    Cursor c = shared;
+    more = cursor_next<MT, BN>(a, c, n);
+    shared = c;
+  }
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, more, 0);
+}
+
+// Bounded wait.  The plain test comes first: when the phase is complete already, as it mostly is for the issuing warps, it
+// answers sooner than the test that may suspend.  Gives up soon when another role of the CTA has.
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
   const uint32_t b = smem_u32(bar);
+  uint32_t done;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(done)
+      : "r"(b), "r"(parity)
+      : "memory");
+  if (done) return true;
   for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
-    uint32_t done;
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
@@ -132,6 +174,18 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
   *dead = 1;
   return false;
 }
+// weights of tile x are in TMEM: four softmax warps arrive, the issuing warp waits.  A hardware barrier, which answers in
+// tens of cycles where an mbarrier, in the shared memory that the products read at full rate, takes about 200.  Every
+// warp passes it once per block whatever happened to its bounded waits, so it cannot hang.
+__device__ __forceinline__ void weights_ready(int x) { asm volatile("bar.arrive %0, 160;\n" ::"r"(2 + x) : "memory"); }
+__device__ __forceinline__ void weights_wait(int x) { asm volatile("bar.sync %0, 160;\n" ::"r"(2 + x) : "memory"); }
+
+// The issuing warps of the two tiles take turns, one block's products each, so that one tile's softmax runs under the
+// other's products; without turns the tiles fall into step in many CTAs, and both halves of the work wait for each other.
+// Handed over by hardware barriers too; an issue returns when all but a product or two are done, so the tensor core sees
+// hardly a gap.
+__device__ __forceinline__ void turn_wait(int x) { asm volatile("bar.sync %0, 64;\n" ::"r"(4 + x) : "memory"); }
+__device__ __forceinline__ void turn_give(int x) { asm volatile("bar.arrive %0, 64;\n" ::"r"(4 + x) : "memory"); }
 
 }  // namespace
 
@@ -141,7 +195,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   using C = Cfg<D>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
-  __shared__ Cursor start;
+  __shared__ Cursor cursors[11], ahead[8];  // every warp walks its own, out of registers; the softmax also looks ahead
   __shared__ int has_work;
   __shared__ long long scan_sh[SOFT / 32];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -152,15 +206,15 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(smem_u32(&bars.full[i]), 1);
-      mbar_init(smem_u32(&bars.empty[i]), 1);
+      mbar_init(smem_u32(&bars.empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars.q_full[i]), 128);
+      mbar_init(smem_u32(&bars.q_full[i]), 4);
       mbar_init(smem_u32(&bars.s_full[i]), 1);
-      mbar_init(smem_u32(&bars.p_full[i]), 128);
       mbar_init(smem_u32(&bars.o_full[i]), 1);
     }
-    mbar_init(smem_u32(&bars.drain), 1);
+    mbar_init(smem_u32(&bars.drain[0]), 1);
+    mbar_init(smem_u32(&bars.drain[1]), 1);
     bars.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     tma_prefetch_desc(&tk);
@@ -175,8 +229,9 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   if (tid < SOFT) {
     Cursor c;
     const bool more = cursor_begin<SOFT, MT, BN>(a, c, reinterpret_cast<long long(*)[SOFT + 1]>(ring), scan_sh);
+    if (lane == 0) cursors[warp] = c;
     if (tid == 0) {
-      start = c;
+      cursors[8] = cursors[9] = cursors[10] = c;
       has_work = more;
     }
     fence_async_smem();  // the search used the ring's memory
@@ -184,30 +239,30 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   fence_before();
   __syncthreads();
   fence_after();
-  Cursor cur = start;
   bool more = has_work;
   const uint32_t tmem = bars.tmem;
-  int used = 0;
 
   // registers: 128 * (2 * 224 + 56) = 384 * 168, those of the launch
   if (warp >= 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
   if (warp == 9) {
     // ------------------------------------------------------------ loader
+    Cursor &cur = cursors[9];
     const int P = 1 << a.log2P, box = min(P, BN), pieces = BN / box;
     const int piece = lane / C::HALVES, half = lane % C::HALVES;
     uint32_t st = 0, ph = 0;  // next stage and its parity
     uint32_t issued = 0;      // stages ever filled
     bool ok = true;
-    while (more && ok) {
+    while (more) {
       int b0, b1;
       bool first, last;
       const int n = cursor_piece(cur, b0, b1, first, last);
       const int *trow = a.table + (long long)cur.n * a.table_stride;
-      for (int b = b0; b < b1 && ok; ++b) {
-        const int t = (cur.w.blk0 + b) * BN + piece * box;
+      const int lo = cur.w.lo, hi = cur.w.hi, kvh = cur.h;
+      int t = (cur.w.blk0 + b0) * BN + piece * box;
+      for (int b = b0; b < b1 && ok; ++b, t += BN) {
         int page = a.num_pages;  // zeros
-        if (piece < pieces && t < cur.w.hi && t + box > cur.w.lo) {
+        if (piece < pieces && t < hi && t + box > lo) {
           const int pg = trow[t >> a.log2P];
           if ((unsigned)pg < (unsigned)a.num_pages) page = pg;
         }
@@ -219,7 +274,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           if (lane == 0) mbar_expect_tx(smem_u32(&bars.full[st]), C::STAGE);
           __syncwarp();
           if (piece < pieces)
-            tma_load_4d(smem_u32(ring + st * C::STAGE + half * (BN * 128) + piece * box * 128), kv ? &tv : &tk, half * 64, cur.h, off,
+            tma_load_4d(smem_u32(ring + st * C::STAGE + half * (BN * 128) + piece * box * 128), kv ? &tv : &tk, half * 64, kvh, off,
                         page, smem_u32(&bars.full[st]));
           ++issued;
           if (++st == C::STAGES) {
@@ -228,7 +283,8 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           }
         }
       }
-      more = cursor_next<MT, BN>(a, cur, n);
+      __syncwarp();
+      more = cursor_advance(a, cur, n);
     }
     // a CTA that gives up waits (bounded) for the copies in flight before its shared memory goes
     if (*dead) {
@@ -242,218 +298,259 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         mbar_wait(smem_u32(&bars.full[st]), ph, nullptr, 0, 1u << 20);
       }
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ products
+  } else if (warp != 11) {
+    // ------------------------------------------------------------ products of tile x
+    const int x = (warp - 8) >> 1;
+    Cursor &cur = cursors[warp];
     const uint32_t id_s = idesc_bf16(128, BN, false, neg != 0), id_o = idesc_bf16(128, D, true, false);
-    uint32_t st = 0, ph = 0;
-    uint32_t pq[2] = {0, 0}, pp[2] = {0, 0};  // parities of the tiles' barriers
-    bool ok = true;
+    const uint32_t ts = tmem + TM_S + x * BN, to = tmem + TM_O + x * D;
+    uint32_t st = 0, ph = 0, pq = 0;  // ring stage and its parity, parity of the tile's query barrier
+    bool ok = true;                   // no wait of this warp has expired
     auto next = [&] {
       if (++st == C::STAGES) {
         st = 0;
         ph ^= 1;
       }
     };
-    auto scores = [&](int x, uint32_t ks) {  // S[x] = Q[x] K^T
-      const SDesc q = sdesc_s(smem_u32(qs + x * C::QT), 16, 1024), k = sdesc_s(ks, 16, 1024);
-#pragma unroll 1
+    auto scores = [&](uint32_t stage) {  // S = Q K^T
+      const SDesc q = sdesc_s(opaque(smem_u32(qs + x * C::QT)), 16, 1024);
+      const SDesc k = sdesc_s(opaque(smem_u32(ring + stage * C::STAGE)), 16, 1024);
+#pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         const uint32_t o = (i >> 2) * (BN * 128) + (i & 3) * 32;
-        mma_f16s(tmem + TM_S + x * BN, q + o, k + o, id_s, i > 0);
+        mma_f16s(ts, q + o, k + o, id_s, i > 0);
       }
       mma_commit(smem_u32(&bars.s_full[x]));
+      mma_commit(smem_u32(&bars.empty[stage]));
     };
-    auto sums = [&](int x, uint32_t vs, bool acc) {  // O[x] += P[x] V
-      const SDesc v = sdesc_s(vs, BN * 128, 1024);
-#pragma unroll 1
-      for (int i = 0; i < BN / 16; ++i) mma_ts(tmem + TM_O + x * D, tmem + TM_S + x * BN + 8 * i, v + i * 2048, id_o, acc || i > 0);
+    auto sums = [&](uint32_t stage, bool acc) {  // O += P V
+      const SDesc v = sdesc_s(opaque(smem_u32(ring + stage * C::STAGE)), BN * 128, 1024);
+#pragma unroll
+      for (int i = 0; i < BN / 16; ++i) mma_ts(to, ts + 8 * i, v + i * 2048, id_o, acc || i > 0);
     };
-    while (more && ok) {
+    if (x == 1) turn_give(0);  // tile 0 begins
+    while (more) {
       int b0, b1;
       bool first, last;
       const int n = cursor_piece(cur, b0, b1, first, last);
-      const int nx = cur.w.rows > 128 ? 2 : 1;
-      if (b0 < b1) {
-        for (int x = 0; x < nx; ++x) {
-          ok = ok && wait(&bars.q_full[x], pq[x], dead);
-          pq[x] ^= 1;
-        }
-        // keys of the first block
-        ok = ok && wait(&bars.full[st], ph, dead);
-        if (!ok) break;
-        fence_after();
-        if (lane == 0) {
-          for (int x = 0; x < nx; ++x) scores(x, smem_u32(ring + st * C::STAGE));
-          mma_commit(smem_u32(&bars.empty[st]));
-        }
-        __syncwarp();
-        next();
-        for (int b = b0; b < b1 && ok; ++b) {
-          const uint32_t vstage = st;
+      const bool both = cur.w.rows > 128;
+      if (b0 < b1 && x * 128 >= cur.w.rows) {  // no such tile here: only hand the stages back
+        for (int i = 0; i < 2 * (b1 - b0); ++i) {
           ok = ok && wait(&bars.full[st], ph, dead);
-          if (!ok) break;
-          // value rows that no query sees become zeros: whatever those slots hold, zero weights keep them out
-          const int t0 = (cur.w.blk0 + b) * BN, r_lo = cur.w.lo - t0, r_hi = cur.w.hi - t0;
+          if (lane == 0) mbar_arrive(smem_u32(&bars.empty[st]));
+          next();
+        }
+      } else if (b0 < b1) {
+        ok = ok && wait(&bars.q_full[x], pq, dead);
+        pq ^= 1;
+        ok = ok && wait(&bars.full[st], ph, dead);  // keys of the first block
+        if (both) turn_wait(x);
+        fence_after();
+        if (ok && elect1()) scores(st);
+        __syncwarp();
+        if (both) turn_give(x ^ 1);
+        next();
+        int r_lo = cur.w.lo - (cur.w.blk0 + b0) * BN, r_hi = cur.w.hi - (cur.w.blk0 + b0) * BN;
+        for (int b = b0; b < b1; ++b, r_lo -= BN, r_hi -= BN) {
+          // values of the block and keys of the next, while the softmax works
+          const uint32_t vst = st;
+          ok = ok && wait(&bars.full[vst], ph, dead);
           if (r_lo > 0 || r_hi < BN) {
-            uint8_t *vs = ring + vstage * C::STAGE;
+            // value rows that no query sees become zeros: whatever those slots hold, zero weights keep them out (the
+            // warps of both tiles write the same zeros)
+            uint4 *v = reinterpret_cast<uint4 *>(ring + vst * C::STAGE);
             for (int i = lane; i < BN * 8 * C::HALVES; i += 32) {
               const int r = (i >> 3) & (BN - 1);
-              if (r < r_lo || r >= r_hi) reinterpret_cast<uint4 *>(vs)[i] = make_uint4(0, 0, 0, 0);
+              if (r < r_lo || r >= r_hi) v[i] = make_uint4(0, 0, 0, 0);
             }
             fence_async_smem();
             __syncwarp();
           }
           next();
           const bool has_next = b + 1 < b1;
-          const uint32_t kstage = st;
-          for (int x = 0; x < nx && ok; ++x) {
-            ok = wait(&bars.p_full[x], pp[x], dead);
-            if (!ok) break;
-            pp[x] ^= 1;
-            fence_after();
-            if (lane == 0) {
-              sums(x, smem_u32(ring + vstage * C::STAGE), b > b0);
-              if (x == nx - 1) mma_commit(smem_u32(&bars.empty[vstage]));
-              if (!has_next) mma_commit(smem_u32(&bars.o_full[x]));
-            }
-            __syncwarp();
-            if (has_next) {
-              if (x == 0) ok = wait(&bars.full[kstage], ph, dead);
-              if (!ok) break;
-              fence_after();
-              if (lane == 0) {
-                scores(x, smem_u32(ring + kstage * C::STAGE));
-                if (x == nx - 1) mma_commit(smem_u32(&bars.empty[kstage]));
-              }
-              __syncwarp();
-            }
+          const uint32_t kst = st;
+          if (has_next) {
+            ok = ok && wait(&bars.full[kst], ph, dead);
+            next();
           }
-          if (has_next) next();
+          weights_wait(x);
+          if (both) turn_wait(x);
+          fence_after();
+          if (ok && elect1()) {
+            sums(vst, b > b0);
+            if (has_next) scores(kst);
+            else mma_commit(smem_u32(&bars.o_full[x]));
+          }
+          __syncwarp();
+          if (both) turn_give(x ^ 1);
+          if (ok && elect1()) mma_commit(smem_u32(&bars.empty[vst]));
+          __syncwarp();
         }
       }
-      more = cursor_next<MT, BN>(a, cur, n);
-    }
-    if (*dead) {  // products in flight end before TMEM goes
-      if (lane == 0) mma_commit(smem_u32(&bars.drain));
       __syncwarp();
-      mbar_wait(smem_u32(&bars.drain), 0, nullptr, 0, 1u << 20);
+      more = cursor_advance(a, cur, n);
+    }
+    if (x == 0) turn_wait(0);  // the turn that was given last
+    if (*dead) {  // products in flight end before TMEM goes
+      if (elect1()) mma_commit(smem_u32(&bars.drain[x]));
+      __syncwarp();
+      mbar_wait(smem_u32(&bars.drain[x]), 0, nullptr, 0, 1u << 20);
     }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
     // ------------------------------------------------------------ softmax of tile x
+    Cursor &cur = cursors[warp];
+    int used = 0;
     const int x = warp >> 2, wr = (warp & 3) * 32 + lane;  // row in the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + TM_S + x * BN, to = tmem + lane_base + TM_O + x * D;
     uint32_t ps = 0, po = 0;
     bool ok = true;
-    const bf16 *Q = static_cast<const bf16 *>(a.q);
-    while (more && ok) {
+    // The warp's 32 query rows of the piece at cursor c, asked for but not waited for: 16 bytes a lane, neighbours in a
+    // row; every lane finds its own row and hands the address on.  False when the piece has no products of this tile.
+    auto load_q = [&](const Cursor &c) {
+      int b0, b1;
+      bool first, last;
+      cursor_piece(c, b0, b1, first, last);
+      const int rows = c.w.rows - x * 128;
+      if (b0 >= b1 || rows <= 0) return false;
+      int tok, head;
+      row_place(a, c, MT, x * 128 + (wr < rows ? wr : 0), tok, head);
+      const unsigned long long mine = reinterpret_cast<unsigned long long>(static_cast<const bf16 *>(a.q) + tok * a.q_tok + head * a.q_head);
+      constexpr int CPR = D / 8, RPI = 32 / CPR;  // chunks of a row, rows of one instruction
+      uint8_t *qt = qs + x * C::QT;
+      const int ch = lane % CPR;
+#pragma unroll
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int sub = i * RPI + lane / CPR, r = (warp & 3) * 32 + sub;
+        const unsigned long long p = __shfl_sync(0xffffffffu, mine, sub);
+        cp_async16(qt + (ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   reinterpret_cast<const void *>(p + ch * 16), r < rows);
+      }
+      return true;
+    };
+    auto q_arrived = [&](bool pending) {
+      if (!pending) return;
+      cp_async_wait_all();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.q_full[x]));
+    };
+    q_arrived(more && load_q(cur));
+    while (more) {
       int b0, b1;
       bool first, last;
       const int n = cursor_piece(cur, b0, b1, first, last);
       const int rows = cur.w.rows - x * 128;  // of this tile
+      bool more_next = false;
+      // moves `ahead` to the next piece and asks for its queries
+      auto look_ahead = [&] {
+        if (lane == 0) ahead[warp] = cur;
+        __syncwarp();
+        more_next = cursor_advance(a, ahead[warp], n);
+        return more_next && load_q(ahead[warp]);
+      };
+      if (rows <= 0) q_arrived(look_ahead());
       if (rows > 0) {
         const int row = x * 128 + wr;
         const bool live = wr < rows;
-        int tok, head;
-        row_place(a, cur, MT, live ? row : 0, tok, head);
-        const int pos = live ? cur.s.kv - cur.s.qlen + tok - cur.s.qbeg : -1;
-        float m = -INFINITY, l = 0.f;
+        int pos = -1;
+        if (live) {
+          int tok, head;
+          row_place(a, cur, MT, row, tok, head);
+          pos = cur.s.kv - cur.s.qlen + tok - cur.s.qbeg;
+        }
+        float m = live ? -INFINITY : 0.f, l = 0.f;
+        bool pending = false;
+        if (b0 >= b1) pending = look_ahead();
         if (b0 < b1) {
-          // ---- the warp's 32 query rows, 16 bytes a lane, neighbours in a row
-          uint8_t *qt = qs + x * C::QT;
-          constexpr int CPR = D / 8;
-          for (int i = lane; i < 32 * CPR; i += 32) {
-            const int r = (warp & 3) * 32 + i / CPR, c = i % CPR;
-            int qt_tok, qt_head;
-            const bool there = r < rows;
-            row_place(a, cur, MT, x * 128 + (there ? r : 0), qt_tok, qt_head);
-            cp_async16(qt + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                       Q + qt_tok * a.q_tok + qt_head * a.q_head + c * 8, there);
-          }
-          cp_async_wait_all();
-          fence_async_smem();
-          mbar_arrive(smem_u32(&bars.q_full[x]));
-
-          for (int b = b0; b < b1; ++b) {
-            ok = wait(&bars.s_full[x], ps, dead);
-            if (!ok) break;
+          int t0 = (cur.w.blk0 + b0) * BN;
+          for (int b = b0; b < b1; ++b, t0 += BN) {
+            ok = ok && wait(&bars.s_full[x], ps, dead);
             ps ^= 1;
             fence_after();
-            uint32_t s[BN];
+            // the last scores of the piece are there, so its queries are done with: the next ones come meanwhile
+            if (b == b1 - 1) pending = look_ahead();
+            // Weights against the maximum as it stands, without looking for a new one.  Their sum tells whether that
+            // will do: below 2^40 so is every weight, and sums and products stay far inside fp32 (bf16 has the same
+            // exponents).  Above it, or while a row has no maximum yet, the maximum is taken and the weights are formed
+            // anew from the scores, which stay in TMEM until the weights replace them.
+            uint32_t s[BN], w[BN / 2];
+            float part;
+            for (bool raise = __any_sync(0xffffffffu, m == -INFINITY);; raise = true) {
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) tmem_ld32_nw(ts + 32 * i, s + 32 * i);
-            tmem_wait_ld();
-            const int t0 = (cur.w.blk0 + b) * BN;
-            const bool cut = t0 + BN - 1 > pos || (a.window && t0 <= pos - a.window);
-            if (__any_sync(0xffffffffu, cut)) {
-              const int hi = pos - t0, lo = a.window ? pos - a.window - t0 : -1;
+              for (int i = 0; i < BN / 32; ++i) tmem_ld32_nw(ts + 32 * i, s + 32 * i);
+              tmem_wait_ld();
+              if (__any_sync(0xffffffffu, t0 + BN - 1 > pos || (a.window && t0 <= pos - a.window))) {
+                const int hi = pos - t0, lo = a.window ? pos - a.window - t0 : -1;
 #pragma unroll
-              for (int i = 0; i < BN; ++i)
-                if (i > hi || i <= lo) s[i] = 0xff800000u;
-            }
-            float mx[4];
+                for (int i = 0; i < BN; ++i)
+                  if (i > hi || i <= lo) s[i] = 0xff800000u;
+              }
+              if (raise) {
+                float mx[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+                for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(s[k]);
 #pragma unroll
-            for (int i = 4; i < BN; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
-            const float z = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-            if (__any_sync(0xffffffffu, z > m + RAISE)) {
-              const float mn = fmaxf(m, z);
-              const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-              m = mn;
-              l *= f;
-              if (b > b0) {
-                // the products that wrote O completed before this tile's scores did, the next ones wait for the weights
+                for (int i = 4; i < BN; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2);
+                const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                m = mn;
+                l *= f;
+                if (b > b0) {
+                  // the products that wrote O completed before this tile's scores did, the next wait for the weights
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                  uint32_t o[32];
-                  tmem_ld32_nw(to + 32 * i, o);
-                  tmem_wait_ld();
+                  for (int i = 0; i < D / 32; ++i) {
+                    uint32_t o[32];
+                    tmem_ld32_nw(to + 32 * i, o);
+                    tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st32_nw(to + 32 * i, o);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    tmem_st32_nw(to + 32 * i, o);
+                  }
                 }
               }
-            }
-            const float mm = m == -INFINITY ? 0.f : m;
-            const uint64_t sc = pk(a.scale_log2, a.scale_log2), nm = pk(-mm, -mm);
-            uint64_t sum[2] = {0, 0};
+              const float mm = m == -INFINITY ? 0.f : m;
+              const uint64_t sc = pk(a.scale_log2, a.scale_log2), nm = pk(-mm, -mm);
+              uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t w[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int e = hh * 64 + 2 * i;
+              for (int i = 0; i < BN / 2; ++i) {
                 float p0, p1;
-                upk(fma2(pk(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc, nm), p0, p1);
+                upk(fma2(pk(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc, nm), p0, p1);
                 p0 = ex2(p0);
                 p1 = ex2(p1);
-                sum[i & 1] = add2(sum[i & 1], pk(p0, p1));
+                sum[i & 3] = add2(sum[i & 3], pk(p0, p1));
                 w[i] = pack_bf16(p0, p1);
               }
-              tmem_st32_nw(ts + 32 * hh, w);
+              float u0, u1;
+              upk(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u0, u1);
+              part = u0 + u1;
+              if (raise || !__any_sync(0xffffffffu, part > RAISED)) break;
             }
-            float u0, u1;
-            upk(add2(sum[0], sum[1]), u0, u1);
-            l += u0 + u1;
+            l += part;
+            tmem_st32_nw(ts, w);
+            tmem_st32_nw(ts + 32, w + 32);
             tmem_wait_st();
             fence_before();
-            mbar_arrive(smem_u32(&bars.p_full[x]));
+            weights_ready(x);
           }
-          if (ok) {
-            ok = wait(&bars.o_full[x], po, dead);
-            po ^= 1;
-            fence_after();
-          }
+          q_arrived(pending);
+          pending = false;
+          ok = ok && wait(&bars.o_full[x], po, dead);
+          po ^= 1;
+          fence_after();
         }
-        if (ok) {
+        q_arrived(pending);
+        {
           const bool whole = first && last;
+          int tok, head;
+          row_place(a, cur, MT, live ? row : 0, tok, head);
           const int slot = first ? 1 : 0;
           float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
           const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
           bf16 *op = static_cast<bf16 *>(a.o) + tok * a.o_tok + head * a.o_head;
+          const bool wide = (reinterpret_cast<uintptr_t>(op) & 31) == 0;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
@@ -466,18 +563,19 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
             }
             if (live) {
               if (whole) {
+                uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint32_t w[4];
+                for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                if (wide) {
+                  st_global_32b(op + 32 * i, w);
+                  st_global_32b(op + 32 * i + 16, w + 8);
+                } else {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    w[k] = pack_bf16(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                  *reinterpret_cast<uint4 *>(op + 32 * i + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                  for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(op + 32 * i + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                 }
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                  *reinterpret_cast<uint4 *>(rec + (size_t)row * D + 32 * i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                for (int e = 0; e < 32; e += 8) st_global_32b(rec + (size_t)row * D + 32 * i + e, o + e);
               }
             }
           }
@@ -500,7 +598,10 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
               make_int4(last ? 1 : 2, cur.s.qbeg + (int)(r0 / a.G), cur.h, cur.w.rows << 16 | (int)(r0 % a.G));
         }
       }
-      more = cursor_next<MT, BN>(a, cur, n);
+      __syncwarp();
+      if (lane == 0) cur = ahead[warp];
+      __syncwarp();
+      more = more_next;
     }
     if (tid < 2 && !(used >> tid & 1)) a.hdr[cta * 2 + tid] = make_int4(0, 0, 0, 0);
   }

@@ -65,10 +65,10 @@ struct Tile {
 };
 template <int MT, int BN>
 __device__ __forceinline__ Tile tile_of(const PagedArgs &a, const SeqInfo &s, int t) {
-  Tile w;
-  const long long R = (long long)s.qlen * a.G, r0 = (long long)t * MT;
-  w.rows = (int)max(0ll, min((long long)MT, R - r0));
-  const int i0 = (int)(r0 / a.G), i1 = (int)((r0 + w.rows - 1) / a.G);
+  Tile w;  // the host keeps total_q * G below 2^31
+  const unsigned R = (unsigned)s.qlen * a.G, r0 = (unsigned)t * MT;
+  w.rows = R > r0 ? (int)min((unsigned)MT, R - r0) : 0;
+  const int i0 = (int)(r0 / (unsigned)a.G), i1 = w.rows ? (int)((r0 + w.rows - 1) / (unsigned)a.G) : i0;
   w.pos0 = s.kv - s.qlen + i0;
   w.hi = max(0, min(s.kv, s.kv - s.qlen + i1 + 1));
   w.lo = a.window ? max(0, w.pos0 - a.window + 1) : 0;
@@ -77,7 +77,7 @@ __device__ __forceinline__ Tile tile_of(const PagedArgs &a, const SeqInfo &s, in
   return w;
 }
 template <int MT> __device__ __forceinline__ int tiles_of(const PagedArgs &a, const SeqInfo &s) {
-  return (int)(((long long)s.qlen * a.G + MT - 1) / MT);
+  return (int)(((unsigned)s.qlen * a.G + MT - 1) / MT);
 }
 
 // barrier of the NT threads that look for the CTA's range (a CTA may have more)
@@ -226,10 +226,9 @@ template <int MT, int BN> __device__ __forceinline__ bool cursor_next(const Page
 
 // where row r of the cursor's tile lies in q and o
 __device__ __forceinline__ void row_place(const PagedArgs &a, const Cursor &c, int MT, int r, int &tok, int &head) {
-  const long long g = (long long)c.t * MT + r;
-  const int i = (int)(g / a.G);
-  tok = c.s.qbeg + i;
-  head = c.h * a.G + (int)(g - (long long)i * a.G);
+  const unsigned g = (unsigned)c.t * MT + r, i = g / (unsigned)a.G;
+  tok = c.s.qbeg + (int)i;
+  head = c.h * a.G + (int)(g - i * a.G);
 }
 
 cudaError_t launch_attn_rows(const PagedArgs &a, bool bf16_type, int D, int MT, int ctas, cudaStream_t st);
