@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   __shared__ Bars bars;
   __shared__ Cursor cursors[11], ahead[8];  // every warp walks its own, out of registers; the softmax also looks ahead
   __shared__ int has_work;
-  __shared__ long long scan_sh[SOFT / 32];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *qs = sm, *ring = sm + 2 * C::QT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
@@ -226,19 +225,28 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   }
   pdl_trigger();
   pdl_wait();
-  if (tid < SOFT) {
-    Cursor c;
-    const bool more = cursor_begin<SOFT, MT, BN>(a, c, reinterpret_cast<long long(*)[SOFT + 1]>(ring), scan_sh);
-    if (lane == 0) cursors[warp] = c;
-    if (tid == 0) {
-      cursors[8] = cursors[9] = cursors[10] = c;
-      has_work = more;
-    }
-    fence_async_smem();  // the search used the ring's memory
+  if (warp == 0) {
+    const int found = cursor_begin_small<MT, BN>(a, cursors[0]);
+    if (lane == 0) has_work = found;
   }
   fence_before();
   __syncthreads();
   fence_after();
+  if (const int found = has_work; found == 2) {  // more than 32 tiles
+    __syncthreads();                             // everyone has read it
+    if (tid < SOFT) {
+      Cursor c;
+      const bool some = cursor_begin_any<SOFT, MT, BN>(a, c, *reinterpret_cast<PlanSmem<SOFT> *>(ring));
+      if (tid == 0) {
+        cursors[0] = c;
+        has_work = some;
+      }
+      fence_async_smem();  // the search used the ring's memory
+    }
+    __syncthreads();
+  }
+  if (warp > 0 && warp < 11 && lane == 0) cursors[warp] = cursors[0];
+  __syncthreads();
   bool more = has_work;
   const uint32_t tmem = bars.tmem;
 
@@ -401,7 +409,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
     // ------------------------------------------------------------ softmax of tile x
     Cursor &cur = cursors[warp];
-    int used = 0;
+    bool cut = false;  // this CTA's header is written
     const int x = warp >> 2, wr = (warp & 3) * 32 + lane;  // row in the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + TM_S + x * BN, to = tmem + lane_base + TM_O + x * D;
@@ -590,20 +598,16 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           fence_before();
         }
       }
-      if (!(first && last)) {
-        used |= 1 << (first ? 1 : 0);
-        if (tid == 0) {
-          const long long r0 = (long long)cur.t * MT;
-          a.hdr[cta * 2 + (first ? 1 : 0)] =
-              make_int4(last ? 1 : 2, cur.s.qbeg + (int)(r0 / a.G), cur.h, cur.w.rows << 16 | (int)(r0 % a.G));
-        }
+      if (first && !last) {
+        cut = true;
+        if (tid == 0) a.hdr[cta] = cut_header<MT>(a, cur);
       }
       __syncwarp();
       if (lane == 0) cur = ahead[warp];
       __syncwarp();
       more = more_next;
     }
-    if (tid < 2 && !(used >> tid & 1)) a.hdr[cta * 2 + tid] = make_int4(0, 0, 0, 0);
+    if (tid == 0 && !cut) a.hdr[cta] = make_int4(0, 0, 0, 0);
   }
   fence_before();
   __syncthreads();

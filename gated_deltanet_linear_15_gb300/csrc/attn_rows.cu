@@ -6,10 +6,15 @@
 // Bound by the bytes of the cache: each key and value is used by MT = 16 or 32 rows only (16 flops per byte at four
 // query heads per key head), far below the tensor cores' ratio.  So the kernel is a stream: the units of the whole
 // batch are split evenly over the CTAs (paged.cuh), and inside a CTA each of the four warps owns a 16-token slice of
-// every 64-token block with its own ring of cp.async stages, its own running maximum, mass and sums, and no barrier
+// every 64-token block with its own ring of TMA stages, its own running maximum, mass and sums, and no barrier
 // with the other warps until the piece ends.  The query rows stay in registers as mma.sync A fragments; scores come
 // out in the layout that the second product takes as its A operand.  tcgen05 has no use here: its 128-row tile would
 // be one eighth full, and the softmax would leave registers for TMEM and come back.
+//
+// A slice is loaded by one lane, one box of 16 tokens by 128 bytes each, with the 128-byte swizzle, which is what the
+// fragment reads want.  (Sixteen-byte copies by every lane took 40 % of the instructions of the loop.)  Rows of a slice
+// outside what the tile sees are cleared in shared memory; a missing page is loaded from an out-of-range coordinate,
+// which fills zeros.
 //
 // The sums are rescaled only when a row's maximum rises by more than 8 (a factor of 256 that fp32 sums and bf16
 // weights carry without loss), so most slices skip that pass over the accumulator.
@@ -17,8 +22,11 @@
 // fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the exact rest):
 // hi hi + hi lo + lo hi leaves about 2^-21 of a product.
 #include "paged.cuh"
+#include "umma.cuh"
 
 namespace gdn {
+
+using namespace umma;
 
 namespace {
 
@@ -30,8 +38,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
   return y;
 }
-template <int K> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(K) : "memory"); }
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -66,92 +72,139 @@ __device__ __forceinline__ float quad_max(float x) {
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
 
-// byte offset of 16-byte chunk c of row r in a [16][D] slice: chunks of a row change places by the row's low three
-// bits, so that eight rows at one column lie in eight different bank groups
-template <int RB> __device__ __forceinline__ uint32_t slice_off(int r, int c) { return r * RB + ((c ^ (r & 7)) << 4); }
+// byte offset of 16-byte chunk c of row r in a tile of `ROWS` rows: boxes of 128 bytes by ROWS rows, 128-byte swizzle
+template <int ROWS> __device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  return (c >> 3) * (ROWS * 128) + r * 128 + (((c ^ r) & 7) << 4);
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
+      : "memory");
+}
+constexpr uint32_t WAIT_LIMIT = 1u << 22;
 
 }  // namespace
 
 template <typename I, int D, int MI, int STAGES>
-__global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel(PagedArgs a) {
+__global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1))
+attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   constexpr int MT = 16 * MI, RB = D * sizeof(I), CPR = RB / 16, SLB = SL * RB;  // row bytes, chunks, slice bytes
+  constexpr int BOXES = RB / 128, BW = 128 / sizeof(I);                          // boxes of a slice, features of a box
   constexpr bool F32 = sizeof(I) == 4;
   constexpr int KS = F32 ? D / 8 : D / 16;  // k steps of q . k
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long pre[2][NT + 1];
-  __shared__ long long scan_sh[NT / 32];
-  pdl_trigger();
-  pdl_wait();
+  extern __shared__ uint8_t raw[];
+  __shared__ Cursor cur;  // one for the CTA, out of registers
+  __shared__ int going;
+  __shared__ uint64_t full[WARPS][STAGES];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t *qsm = smem + WARPS * STAGES * 2 * SLB;  // the query rows, [MT][D]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
   const int cta = blockIdx.x;
   const int P = 1 << a.log2P;
-  int used = 0;  // record slots written
-  Cursor cur;
-  bool more = cursor_begin<NT, MT, BN>(a, cur, pre, scan_sh);
+  if (tid < WARPS * STAGES) mbar_init(smem_u32(&full[0][0] + tid), 1);
+  if (tid == 0) {
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  pdl_trigger();
+  pdl_wait();
+  bool cut = false;  // this CTA's header is written
+  int expired = 0;   // a bounded wait ran out
+  if (warp == 0) {
+    const int found = cursor_begin_small<MT, BN>(a, cur);
+    if (lane == 0) going = found;
+  }
+  __syncthreads();
+  if (const int found = going; found == 2) {  // more than 32 tiles
+    __syncthreads();                          // everyone has read it
+    Cursor c;
+    const bool some = cursor_begin_any<NT, MT, BN>(a, c, *reinterpret_cast<PlanSmem<NT> *>(smem));
+    if (tid == 0) {
+      cur = c;
+      going = some;
+    }
+    fence_async_smem();  // the search used the rings' memory
+    __syncthreads();
+  }
+  bool more = going;
   uint8_t *ring = smem + warp * (STAGES * 2 * SLB);
-  const uint32_t ring_u = smem_u32(ring);
+  const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(&full[warp][0]);
   const I *Q = static_cast<const I *>(a.q);
-  const char *Kb = static_cast<const char *>(a.k), *Vb = static_cast<const char *>(a.v);
+  uint32_t st = 0, ph = 0;  // the ring's next stage to be read and its parity
 
   while (more) {
     int b0, b1;
     bool first, last;
     const int n = cursor_piece(cur, b0, b1, first, last);
-    const Tile w = cur.w;
-    // ---- the slices of this piece: lane l copies chunks l, l + 32, ... of the keys and of the values
+    const int lo = cur.w.lo, hi = cur.w.hi, rows = cur.w.rows, pos0 = cur.w.pos0;
+    const int tw = cur.w.blk0 * BN + warp * SL;  // the warp's first token of block 0
+    // blocks of the piece in which the warp's slice holds a key that some row sees
+    if (b0 < b1) {
+      if (tw + b0 * BN + SL <= lo) ++b0;
+      if (tw + (b1 - 1) * BN >= hi) --b1;
+    }
     const int *trow = a.table + (long long)cur.n * a.table_stride;
-    auto page_of = [&](int b) {  // page of the warp's slice of block b, -1 where nothing is to be read
-      const int t0 = (w.blk0 + b) * BN + warp * SL;
-      if (b >= b1 || t0 >= w.hi || t0 + SL <= w.lo) return -1;
-      const int pg = trow[t0 >> a.log2P];
-      return (unsigned)pg < (unsigned)a.num_pages ? pg : -1;
+    auto page_of = [&](int b) {
+      if (b >= b1) return 0;
+      const int pg = trow[(tw + b * BN) >> a.log2P];
+      return (unsigned)pg < (unsigned)a.num_pages ? pg : a.num_pages;
     };
-    auto issue = [&](int b, int pg, int stage) {
-      const int t0 = (w.blk0 + b) * BN + warp * SL;
-      if (b < b1) {
-        const long long kb = ((long long)max(pg, 0) * a.k_page + (long long)(t0 & (P - 1)) * a.k_tok + cur.h * a.k_head) * (int)sizeof(I);
-        const long long vb = ((long long)max(pg, 0) * a.v_page + (long long)(t0 & (P - 1)) * a.v_tok + cur.h * a.v_head) * (int)sizeof(I);
-        uint8_t *ks = ring + stage * 2 * SLB, *vs = ks + SLB;
+    auto issue = [&](int b, int pg, uint32_t stage) {
+      if (b < b1 && lane == 0 && !expired) {
+        const uint32_t bar = full_u + 8 * stage, dst = ring_u + stage * 2 * SLB;
+        const int off = (tw + b * BN) & (P - 1);
+        mbar_expect_tx(bar, 2 * SLB);
 #pragma unroll
-        for (int i = 0; i < SLB / 512; ++i) {
-          const int r = (lane + 32 * i) / CPR, c = (lane + 32 * i) % CPR;
-          const bool ok = pg >= 0 && t0 + r >= w.lo && t0 + r < w.hi;  // other slots read as zeros
-          const int rr = ok ? r : 0;
-          cp_async16(ks + slice_off<RB>(r, c), Kb + kb + (rr * a.k_tok * (int)sizeof(I) + c * 16), ok);
-          cp_async16(vs + slice_off<RB>(r, c), Vb + vb + (rr * a.v_tok * (int)sizeof(I) + c * 16), ok);
-        }
+        for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + i * (SL * 128), &tk, i * BW, cur.h, off, pg, bar);
+#pragma unroll
+        for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + SLB + i * (SL * 128), &tv, i * BW, cur.h, off, pg, bar);
       }
-      cp_async_commit();
     };
+    {
+      int pg[STAGES - 1];
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(b0 + s, page_of(b0 + s), s);
+      for (int s = 0; s < STAGES - 1; ++s) pg[s] = page_of(b0 + s);
+#pragma unroll
+      for (int s = 0; s < STAGES - 1; ++s) issue(b0 + s, pg[s], st + s < STAGES ? st + s : st + s - STAGES);
+    }
     int pg_next = page_of(b0 + STAGES - 1);
 
-    // ---- query fragments: rows g and g + 8 of each 16-row tile
+    // ---- the query rows: coalesced into shared memory, then fragments of rows g and g + 8 of each 16-row tile
+#pragma unroll
+    for (int i = 0; i < (MT * CPR + NT - 1) / NT; ++i) {
+      const int x = tid + i * NT, r = x / CPR, c = x % CPR;
+      if (x < MT * CPR) {
+        int tok, head;
+        row_place(a, cur, MT, r < rows ? r : 0, tok, head);
+        cp_async16(qsm + tile_off<MT>(r, c), Q + tok * a.q_tok + head * a.q_head + c * (16 / (int)sizeof(I)), r < rows);
+      }
+    }
+    cp_async_wait_all();
+    __syncthreads();
     uint32_t qf[MI][KS][4];
     int pos[MI][2];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < MI; ++i) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * i + g + 8 * e;
-        const bool ok = r < w.rows;
-        int tok, head;
-        row_place(a, cur, MT, ok ? r : 0, tok, head);
-        pos[i][e] = cur.s.kv - cur.s.qlen + tok - cur.s.qbeg;
-        const I *p = Q + tok * a.q_tok + head * a.q_head;
+      for (int k = 0; k < KS; ++k) {
+        if constexpr (F32) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          if constexpr (F32) {
-            qf[i][k][e] = ok ? __float_as_uint(p[8 * k + qd]) : 0u;
-            qf[i][k][e + 2] = ok ? __float_as_uint(p[8 * k + qd + 4]) : 0u;
-          } else {
-            qf[i][k][e] = ok ? *reinterpret_cast<const uint32_t *>(p + 16 * k + 2 * qd) : 0u;
-            qf[i][k][e + 2] = ok ? *reinterpret_cast<const uint32_t *>(p + 16 * k + 2 * qd + 8) : 0u;
-          }
+          for (int e = 0; e < 4; ++e)
+            qf[i][k][e] = *reinterpret_cast<const uint32_t *>(qsm + tile_off<MT>(16 * i + g + 8 * (e & 1), 2 * k + (e >> 1)) + 4 * qd);
+        } else {
+          ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(16 * i + (lane & 15), 2 * k + (lane >> 4)), qf[i][k]);
         }
       }
-    const int pos_last = cur.s.kv - cur.s.qlen + (int)(((long long)cur.t * MT + w.rows - 1) / a.G);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const unsigned r = (unsigned)cur.t * MT + min(16 * i + g + 8 * e, rows - 1);
+        pos[i][e] = cur.s.kv - cur.s.qlen + (int)(r / (unsigned)a.G);
+      }
+    }
+    const int pos_last = cur.s.kv - cur.s.qlen + (int)(((unsigned)cur.t * MT + rows - 1) / (unsigned)a.G);
 
     float acc[MI][D / 8][4], m[MI][2], l[MI][2];
 #pragma unroll
@@ -164,20 +217,27 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
         for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
     }
 
-    int stage = 0;
     for (int b = b0; b < b1; ++b) {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();
-      {
-        const int nx = stage == 0 ? STAGES - 1 : stage - 1;
-        issue(b + STAGES - 1, pg_next, nx);
-        pg_next = page_of(b + STAGES);
+      if (!expired && !mbar_wait(full_u + 8 * st, ph, nullptr, 0, WAIT_LIMIT)) expired = 4;
+      __syncwarp();  // every lane is done with the block before, too
+      issue(b + STAGES - 1, pg_next, st == 0 ? STAGES - 1 : st - 1);  // the stage that the last block was read from
+      pg_next = page_of(b + STAGES);
+      const uint32_t ks = ring_u + st * 2 * SLB, vs = ks + SLB;
+      uint8_t *ksp = ring + st * 2 * SLB, *vsp = ksp + SLB;
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1;
       }
-      const uint32_t ks = ring_u + stage * 2 * SLB, vs = ks + SLB;
-      const uint8_t *vsp = ring + stage * 2 * SLB + SLB, *ksp = ring + stage * 2 * SLB;
-      stage = stage == STAGES - 1 ? 0 : stage + 1;
-      const int t0 = (w.blk0 + b) * BN + warp * SL;
-      if (t0 >= w.hi || t0 + SL <= w.lo) continue;
+      const int t0 = tw + b * BN;
+      if (t0 < lo || t0 + SL > hi) {
+        // value rows that no query sees become zeros: whatever those slots hold, zero weights keep them out
+        for (int i = lane; i < SLB / 16; i += 32) {
+          const int r = (i >> 3) & (SL - 1);
+          if (t0 + r < lo || t0 + r >= hi) reinterpret_cast<uint4 *>(vsp)[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();  // the stage is loaded again later
+        __syncwarp();
+      }
       // ---- scores of 16 tokens: tiles 0 (tokens 0-7) and 1 (8-15)
       float s[MI][2][4];
 #pragma unroll
@@ -190,7 +250,7 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           uint32_t bk[4];
-          const uint32_t ad = ks + slice_off<RB>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
+          const uint32_t ad = ks + tile_off<SL>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                        : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
 #pragma unroll
@@ -207,7 +267,7 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              bk[j][e] = *reinterpret_cast<const float *>(ksp + slice_off<RB>(g + 8 * j, 2 * k + e) + qd * 4);
+              bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
 #pragma unroll
           for (int i = 0; i < MI; ++i) {
             uint32_t ah[4], al[4];
@@ -219,7 +279,7 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
         }
       }
       // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
-      const bool mask = t0 + SL - 1 > w.pos0 || (a.window && t0 < pos_last - a.window + 1);
+      const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
       float mx[MI][2];
       bool raise = false;
 #pragma unroll
@@ -284,7 +344,7 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           uint32_t bv[4];
-          const uint32_t ad = vs + slice_off<RB>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
+          const uint32_t ad = vs + tile_off<SL>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                        : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
 #pragma unroll
@@ -309,15 +369,14 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
             const int r = 8 * jt + 2 * qd, c = 2 * j + (g >> 2);
-            const float v0 = *reinterpret_cast<const float *>(vsp + slice_off<RB>(r, c) + (g & 3) * 4);
-            const float v1 = *reinterpret_cast<const float *>(vsp + slice_off<RB>(r + 1, c) + (g & 3) * 4);
+            const float v0 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r, c) + (g & 3) * 4);
+            const float v1 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r + 1, c) + (g & 3) * 4);
 #pragma unroll
             for (int i = 0; i < MI; ++i) mma_3tf32(acc[i][j], ph[i], pl[i], v0, v1);
           }
         }
       }
     }
-    cp_async_wait_all();
     __syncthreads();
 
     // ---- the four warps' sums meet in shared memory (over the rings, which are empty)
@@ -341,7 +400,7 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
     const float *all = reinterpret_cast<const float *>(smem);
     const int slot = first ? 1 : 0;
     float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
-    for (int r = warp * (32 / LPR) + lane / LPR; r < w.rows; r += WARPS * (32 / LPR)) {
+    for (int r = warp * (32 / LPR) + lane / LPR; r < rows; r += WARPS * (32 / LPR)) {
       const int c = lane % LPR;
       float mw[WARPS], M = -INFINITY;
 #pragma unroll
@@ -382,100 +441,176 @@ __global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1)) attn_rows_kernel
         }
       }
     }
-    if (!(first && last)) {
-      used |= 1 << slot;
-      if (tid == 0) {
-        const long long r0 = (long long)cur.t * MT;
-        a.hdr[cta * 2 + slot] = make_int4(last ? 1 : 2, cur.s.qbeg + (int)(r0 / a.G), cur.h, w.rows << 16 | (int)(r0 % a.G));
-      }
+    if (first && !last) {
+      cut = true;
+      if (tid == 0) a.hdr[cta] = cut_header<MT>(a, cur);
     }
-    more = cursor_next<MT, BN>(a, cur, n);
+    fence_async_smem();  // the rings are loaded again
     __syncthreads();
+    if (tid == 0) {
+      Cursor c = cur;
+      going = cursor_next<MT, BN>(a, c, n);
+      cur = c;
+    }
+    __syncthreads();
+    more = going;
   }
-  if (tid < 2 && !(used >> tid & 1)) a.hdr[cta * 2 + tid] = make_int4(0, 0, 0, 0);
+  if (tid == 0 && !cut) a.hdr[cta] = make_int4(0, 0, 0, 0);
+  if (expired) {  // copies in flight end, if they do, before the shared memory goes
+    for (int s = 0; s < STAGES; ++s) mbar_wait(full_u + 8 * s, (uint32_t)s < st ? ph ^ 1 : ph, nullptr, 0, 1u << 18);
+  }
+  expired = __syncthreads_or(expired);
+  if (tid == 0) a.status[cta] = expired ? 4 : 0;
 }
 
-// Joins the pieces of cut items.  Block (c, y): the item that began in CTA c and went on; its warps take rows
-// y * 4 + warp, + 4 gridDim.y, ...  A row's pieces are weighted by their maxima and added in the order of the CTAs.
-template <typename I, int D>
+// Joins the pieces of cut items.  Block (j, y): rows of the j-th of them, which began in some CTA c and went on in the
+// next ones (the block looks for c in the headers, so that the grid need not be larger than the number of items).  JW
+// warps share a row (4 for the few rows of decoding, whose items may be cut into hundreds of pieces; 1 for the 256-row
+// tiles): each takes every JW-th batch of 8 pieces, asks for all of a batch before it uses any, and weights the batch by
+// the running maximum; the warps' results meet in shared memory.  The order of the sums is fixed.
+template <typename I, int D, int JW>
 __global__ void __launch_bounds__(128) attn_join_kernel(PagedArgs a, int MT, int C) {
+  constexpr int RW = 4 / JW, E = D / 32, BATCH = 8;
+  __shared__ float sh[4][32 * E + 2];
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 h = a.hdr[c * 2 + 1];
-  if (h.x != 2) return;
-  const int rows = h.w >> 16, gr = h.w & 0xffff;
-  // the piece after CTA c's own is slot 0 of c + 1, and so on until one that ends the item
-  int np = 0;
-  for (int x = c + 1; x < C; x += 32) {
-    const bool end = x + lane < C && a.hdr[(x + lane) * 2].x != 2;
-    const unsigned b = __ballot_sync(0xffffffffu, end);
-    if (b) {
-      np = x + __ffs(b) - 1 - c + 1;
-      break;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int c = -1, left = blockIdx.x;
+  for (int b = 0; b < C && c < 0; b += 256) {
+    int x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = b + 32 * i + lane < C ? a.hdr[b + 32 * i + lane].x : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned m = __ballot_sync(0xffffffffu, x[i] != 0);
+      const unsigned me = __ballot_sync(0xffffffffu, x[i] != 0 && __popc(m & ((1u << lane) - 1)) == left);
+      if (c < 0 && me) c = b + 32 * i + __ffs(me) - 1;
+      left -= __popc(m);
     }
   }
-  if (np == 0) np = C - c;
-  const size_t rf = record_floats(MT, D);
-  auto rec = [&](int i) { return a.part + ((long long)(c + i) * 2 + (i == 0 ? 1 : 0)) * rf; };
-  for (int r = blockIdx.y * 4 + warp; r < rows; r += 4 * gridDim.y) {
-    float M = -INFINITY;
-    for (int i = lane; i < np; i += 32) M = fmaxf(M, rec(i)[(size_t)MT * D + r]);
+  if (c < 0) return;
+  const int4 h = a.hdr[c];
+  const int np = h.x, rows = h.w >> 16, gr = h.w & 0xffff;
+  const int r = blockIdx.y * RW + warp / JW, sub = warp % JW;
+  if (blockIdx.y * RW >= rows) return;
+  const long long rf = (long long)record_floats(MT, D);
+  // piece 0 is slot 1 of CTA c, piece i slot 0 of CTA c + i
+  const float *p0 = a.part + ((long long)c * 2 + 1) * rf, *p1 = a.part + (long long)c * 2 * rf;
+  float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, o[D / 32];
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  if (r < rows) {
+    for (int b = sub * BATCH; b < np; b += JW * BATCH) {
+      float m[BATCH], l[BATCH], v[BATCH][E];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-      const float *p = rec(i);
-      const float mi = p[(size_t)MT * D + r], li = p[(size_t)MT * D + MT + r];
-      const float f = mi == -INFINITY ? 0.f : ex2(mi - M);
-      L += f * li;
-      if constexpr (D == 128) {
-        const float4 v = *reinterpret_cast<const float4 *>(p + (size_t)r * D + 4 * lane);
-        o[0] += f * v.x; o[1] += f * v.y; o[2] += f * v.z; o[3] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(p + (size_t)r * D + 2 * lane);
-        o[0] += f * v.x; o[1] += f * v.y;
+      for (int i = 0; i < BATCH; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+        if (b + i < np) {
+          const float *p = b + i == 0 ? p0 : p1 + (b + i) * 2 * rf;
+          m[i] = p[MT * D + r];
+          l[i] = p[MT * D + MT + r];
+          if constexpr (D == 128) {
+            const float4 t = *reinterpret_cast<const float4 *>(p + r * D + 4 * lane);
+            v[i][0] = t.x; v[i][1] = t.y; v[i][2] = t.z; v[i][3] = t.w;
+          } else {
+            const float2 t = *reinterpret_cast<const float2 *>(p + r * D + 2 * lane);
+            v[i][0] = t.x; v[i][1] = t.y;
+          }
+        }
       }
-    }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    const int tok = h.y + (gr + r) / a.G, head = h.z * a.G + (gr + r) % a.G;
-    I *op = static_cast<I *>(a.o) + tok * a.o_tok + head * a.o_head + (D / 32) * lane;
+      float mn = M;
 #pragma unroll
-    for (int e = 0; e < D / 32; e += 2) st2(op + e, o[e] * inv, o[e + 1] * inv);
-    if (a.lse && lane == 0)
-      a.lse[(long long)tok * a.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, m[i]);
+      if (mn == -INFINITY) mn = 0.f;  // nothing seen yet: every factor below is 0
+      float f = ex2(M - mn);
+      L *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        f = ex2(m[i] - mn);
+        L += f * l[i];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f * v[i][e];
+      }
+      M = mn;
+    }
   }
+  if constexpr (JW > 1) {
+    if (lane == 0) {
+      sh[warp][32 * E] = L == 0.f ? -INFINITY : M;  // a warp without mass has no say in the maximum
+      sh[warp][32 * E + 1] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh[warp][E * lane + e] = o[e];
+    __syncthreads();
+    if (sub != 0) return;
+    float mw[JW], mn = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < JW; ++w) {
+      mw[w] = sh[warp + w][32 * E];
+      mn = fmaxf(mn, mw[w]);
+    }
+    if (mn == -INFINITY) mn = 0.f;
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < JW; ++w) {
+      const float f = mw[w] == -INFINITY && sh[warp + w][32 * E + 1] == 0.f ? 0.f : ex2(mw[w] - mn);
+      L += f * sh[warp + w][32 * E + 1];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += f * sh[warp + w][E * lane + e];
+    }
+    M = mn;
+  }
+  if (r >= rows) return;
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // nothing seen: zeros; a NaN stays
+  const int tok = h.y + (gr + r) / a.G, head = h.z * a.G + (gr + r) % a.G;
+  I *op = static_cast<I *>(a.o) + tok * a.o_tok + head * a.o_head + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) st2(op + e, o[e] * inv, o[e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[(long long)tok * a.Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 namespace {
-template <typename I, int D, int MI, int STAGES> cudaError_t launch_rows(const PagedArgs &a, int ctas, cudaStream_t st) {
+template <typename I, int D, int MI, int STAGES>
+cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
   constexpr size_t ring = (size_t)WARPS * STAGES * 2 * SL * D * sizeof(I);
-  constexpr size_t meet = (size_t)WARPS * record_floats(16 * MI, D) * 4;
-  constexpr size_t smem = ring > meet ? ring : meet;
+  static_assert(ring >= (size_t)WARPS * record_floats(16 * MI, D) * 4, "the sums meet in the rings' memory");
+  static_assert(ring >= sizeof(PlanSmem<NT>), "the search uses it too");
+  constexpr size_t smem = 1024 + ring + (size_t)16 * MI * D * sizeof(I);
   auto *k = attn_rows_kernel<I, D, MI, STAGES>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(ctas), dim3(NT), smem, st, a);
+  return launch_pdl(k, dim3(ctas), dim3(NT), smem, st, a, tk, tv);
 }
 }  // namespace
 
 // bf16: rings of 96 KB, so that two CTAs share an SM; fp32: 16 rows, and 96 KB (D = 64) or 192 KB rings
-cudaError_t launch_attn_rows(const PagedArgs &a, bool bf, int D, int MT, int ctas, cudaStream_t st) {
-  if (!bf) return D == 64 ? launch_rows<float, 64, 1, 3>(a, ctas, st) : launch_rows<float, 128, 1, 3>(a, ctas, st);
-  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 6>(a, ctas, st) : launch_rows<bf16, 64, 2, 6>(a, ctas, st);
-  return MT == 16 ? launch_rows<bf16, 128, 1, 3>(a, ctas, st) : launch_rows<bf16, 128, 2, 3>(a, ctas, st);
+cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf, int D, int MT, int ctas,
+                             cudaStream_t st) {
+  if (!bf) return D == 64 ? launch_rows<float, 64, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 1, 3>(a, tk, tv, ctas, st);
+  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 6>(a, tk, tv, ctas, st);
+  return MT == 16 ? launch_rows<bf16, 128, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 2, 3>(a, tk, tv, ctas, st);
 }
 
-cudaError_t launch_attn_join(const PagedArgs &a, bool bf, int D, int MT, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas, MT <= 32 ? MT / 4 : 16);
+cudaError_t launch_attn_join(const PagedArgs &a, bool bf, int D, int MT, int ctas, int items, cudaStream_t st) {
+  const int n = items < ctas ? items : ctas;  // cut items at most
+  if (MT == 256) {  // bf16
+    const dim3 grid(n, 64);
+    return D == 64 ? launch_pdl(attn_join_kernel<bf16, 64, 1>, grid, dim3(128), 0, st, a, MT, ctas)
+                   : launch_pdl(attn_join_kernel<bf16, 128, 1>, grid, dim3(128), 0, st, a, MT, ctas);
+  }
+  const dim3 grid(n, MT);
   if (bf)
-    return D == 64 ? launch_pdl(attn_join_kernel<bf16, 64>, grid, dim3(128), 0, st, a, MT, ctas)
-                   : launch_pdl(attn_join_kernel<bf16, 128>, grid, dim3(128), 0, st, a, MT, ctas);
-  return D == 64 ? launch_pdl(attn_join_kernel<float, 64>, grid, dim3(128), 0, st, a, MT, ctas)
-                 : launch_pdl(attn_join_kernel<float, 128>, grid, dim3(128), 0, st, a, MT, ctas);
+    return D == 64 ? launch_pdl(attn_join_kernel<bf16, 64, 4>, grid, dim3(128), 0, st, a, MT, ctas)
+                   : launch_pdl(attn_join_kernel<bf16, 128, 4>, grid, dim3(128), 0, st, a, MT, ctas);
+  return D == 64 ? launch_pdl(attn_join_kernel<float, 64, 4>, grid, dim3(128), 0, st, a, MT, ctas)
+                 : launch_pdl(attn_join_kernel<float, 128, 4>, grid, dim3(128), 0, st, a, MT, ctas);
 }
 
 }  // namespace gdn

@@ -66,6 +66,8 @@ int check_attn(const gdn_paged_shape *s) {
       {s->v_page, "v_page"}, {s->v_tok, "v_tok"}, {s->v_head, "v_head"}, {s->o_tok, "o_tok"}, {s->o_head, "o_head"}};
   for (const auto &x : st) {
     if (x.v < 0) return fail(GDN_ERR_INVALID_ARG, "stride %s is negative", x.name);
+    if ((x.name[0] == 'k' || x.name[0] == 'v') && (x.v == 0 || x.v >= (1ll << 37)))  // what a tensor map can hold
+      return fail(GDN_ERR_UNSUPPORTED, "stride %s must be positive and below 2^37", x.name);
     if (x.v % v) return fail(GDN_ERR_INVALID_ARG, "stride %s is not a multiple of 16 bytes", x.name);
   }
   return GDN_OK;
@@ -83,25 +85,25 @@ AttnPlan attn_plan(const gdn_paged_shape *s) {
   const int G = s->num_heads / s->num_kv_heads;
   const long long rows = (long long)(s->max_q > 0 ? s->max_q : (s->total_q + s->num_seqs - 1) / std::max(1, s->num_seqs)) * G;
   const bool bf = s->dtype == GDN_BF16;
-  auto strided = [](int64_t x) { return x > 0 && x < (1ll << 38); };  // what a tensor map can hold
-  p.tc = bf && rows > 32 && strided(s->k_page) && strided(s->k_tok) && strided(s->k_head) && strided(s->v_page) &&
-         strided(s->v_tok) && strided(s->v_head);
+  p.tc = bf && rows > 32;
   p.MT = p.tc ? 256 : (bf && rows > 16 ? 32 : 16);
   p.ctas = num_sms() * (bf && !p.tc ? 2 : 1);
-  p.off_status = up256((size_t)p.ctas * 2 * sizeof(int4));
+  p.off_status = up256((size_t)p.ctas * sizeof(int4));
   p.off_part = p.off_status + up256((size_t)p.ctas * sizeof(int));
   p.total = p.off_part + up256((size_t)p.ctas * 2 * record_floats(p.MT, s->head_dim) * 4);
   return p;
 }
 
-// keys or values as [pages, slots, heads, features], box = 64 features of one head, min(page_size, 128) slots
-int cache_map(CUtensorMap *m, const void *p, const gdn_paged_shape *s, int64_t page, int64_t tok, int64_t head) {
+// keys or values as [pages, slots, heads, features], box = 128 bytes of one head's features, `slots` slots
+int cache_map(CUtensorMap *m, const void *p, const gdn_paged_shape *s, int64_t page, int64_t tok, int64_t head, int slots) {
+  const int es = (int)esize(s->dtype);
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[4] = {(cuuint64_t)s->head_dim, (cuuint64_t)s->num_kv_heads, (cuuint64_t)s->page_size, (cuuint64_t)s->num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)head * 2, (cuuint64_t)tok * 2, (cuuint64_t)page * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)std::min(s->page_size, 128), 1}, es[4] = {1, 1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+  const cuuint64_t strides[3] = {(cuuint64_t)head * es, (cuuint64_t)tok * es, (cuuint64_t)page * es};
+  const cuuint32_t box[4] = {(cuuint32_t)(128 / es), 1, (cuuint32_t)slots, 1}, step[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void *>(p),
+                        dims, strides, box, step,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GDN_OK : fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
@@ -217,19 +219,22 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.off_part);
   a.status = reinterpret_cast<int *>(static_cast<char *>(ws) + p.off_status);
   const bool bf = s->dtype == GDN_BF16;
+  CUtensorMap tk, tv;
+  const int slots = p.tc ? std::min(s->page_size, 128) : 16;
+  TRY(cache_map(&tk, k, s, s->k_page, s->k_tok, s->k_head, slots));
+  TRY(cache_map(&tv, v, s, s->v_page, s->v_tok, s->v_head, slots));
   if (p.tc) {
-    CUtensorMap tk, tv;
-    TRY(cache_map(&tk, k, s, s->k_page, s->k_tok, s->k_head));
-    TRY(cache_map(&tv, v, s, s->v_page, s->v_tok, s->v_head));
     PROF("attn_chunk");
     CK(launch_attn_chunk_tc(a, tk, tv, s->head_dim, p.ctas, st));
   } else {
     PROF("attn_rows");
-    CK(launch_attn_rows(a, bf, s->head_dim, p.MT, p.ctas, st));
+    CK(launch_attn_rows(a, tk, tv, bf, s->head_dim, p.MT, p.ctas, st));
   }
   {
+    // tiles: every sequence has at most one that is not full
+    const long long tiles = s->num_seqs + (long long)s->total_q * a.G / p.MT;
     PROF("attn_join");
-    CK(launch_attn_join(a, bf, s->head_dim, p.MT, p.ctas, st));
+    CK(launch_attn_join(a, bf, s->head_dim, p.MT, p.ctas, (int)std::min(tiles * s->num_kv_heads, (long long)p.ctas), st));
   }
   return GDN_OK;
 }
@@ -238,7 +243,7 @@ int gdn_paged_attn_status(const gdn_paged_shape *s, const void *ws, gdn_stream_t
   if (check_attn(s) || need_ptr(ws, "workspace")) return -1;
   const AttnPlan p = attn_plan(s);
   if (cudaStreamSynchronize((Stream)stream) != cudaSuccess) return -1;
-  if (!p.tc || s->total_q == 0 || s->num_seqs == 0) return 0;
+  if (s->total_q == 0 || s->num_seqs == 0) return 0;
   int word = 0;
   try {
     std::vector<int> st(p.ctas);

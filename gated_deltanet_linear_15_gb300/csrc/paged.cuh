@@ -27,15 +27,15 @@ struct PagedArgs {
   int N, total_q, per_seq;  // per_seq: new tokens of every sequence when cu_q is NULL
   int Hq, Hkv, G, log2P, num_pages, max_pages, window;
   float scale_log2;         // scale * log2(e): the softmax runs in powers of two
-  int *status;              // one word per CTA of the tensor-core kernel
-  // cut items: headers [C][2] and records [C][2][MT * (D + 2)] (sums [MT][D], maxima [MT], masses [MT])
+  int *status;              // one word per CTA: 0, or 4 when a bounded wait of it ran out
+  // cut items: headers [C] and records [C][2][MT * (D + 2)] (sums [MT][D], maxima [MT], masses [MT])
   int4 *hdr;
   float *part;
 };
 
-// header of a CTA's piece record: slot 1 holds the first piece of an item that goes on in the next CTA, slot 0 a
-// piece of an item that began in an earlier one.  x: 0 none, 1 the item ends here, 2 it goes on.
-// Slot 1: y = first row's token in q, z = key head, w = rows << 16 | first row's place in its group.
+// Records of a CTA: slot 1 holds the first piece of an item that goes on in the next CTA, slot 0 a piece of an item that
+// began in an earlier one.  Header of the CTA: x the number of pieces of the item in slot 1 (0: none), y its first row's
+// token in q, z its key head, w = rows << 16 | first row's place in its group.
 __host__ __device__ constexpr size_t record_floats(int MT, int D) { return (size_t)MT * (D + 2); }
 
 struct SeqInfo {
@@ -84,24 +84,23 @@ template <int MT> __device__ __forceinline__ int tiles_of(const PagedArgs &a, co
 template <int NT> __device__ __forceinline__ void plan_bar() { asm volatile("bar.sync 1, %0;\n" ::"n"(NT) : "memory"); }
 
 // inclusive scan over threads 0 .. NT - 1 (all of them call it); sh holds NT / 32 values
-template <int NT> __device__ __forceinline__ long long block_scan(long long x, long long *sh) {
+template <int NT, typename T> __device__ __forceinline__ T block_scan(T x, T *sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  plan_bar<NT>();
   if (lane == 31) sh[warp] = x;
   plan_bar<NT>();
-  long long add = 0;
+  T add = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) add += w < warp ? sh[w] : 0;
   return x + add;
 }
 
 // largest i in [0, NT) with pre[i] <= u (pre[0] = 0, non-decreasing)
-template <int NT> __device__ __forceinline__ int find_slot(const long long *pre, long long u) {
+template <int NT, typename T> __device__ __forceinline__ int find_slot(const T *pre, T u) {
   int i = 0;
 #pragma unroll
   for (int s = NT / 2; s > 0; s >>= 1)
@@ -109,34 +108,58 @@ template <int NT> __device__ __forceinline__ int find_slot(const long long *pre,
   return i;
 }
 
+// 64-bit quotient; most lines are shorter than 2^32 units, for which the 32-bit division is several times as fast
+__device__ __forceinline__ long long div_units(long long a, long long b) {
+  if ((unsigned long long)a >> 32 == 0 && (unsigned long long)b >> 32 == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
+// The split of the line: CTA c begins at unit c q + min(c, r).
+struct Split {
+  long long q;
+  int r, C;
+  __device__ __forceinline__ long long begin(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int owner(long long u) const {  // the CTA that holds unit u
+    const long long big = r * (q + 1);
+    return (int)(u < big ? div_units(u, q + 1) : r + div_units(u - big, q));
+  }
+};
+
 struct Cursor {
   int n, t, h;        // the item
   SeqInfo s;
   Tile w;
-  long long u, end;   // this CTA's next unit and the end of its range
   int skip;           // units of the item that came before u
+  long long u, end;   // this CTA's next unit and the end of its range
+  Split split;
+};
+
+// shared memory of the search
+template <int NT> struct PlanSmem {
+  long long units[NT + 1], scan[NT / 32];
+  int tiles[NT + 1], scan_tiles[NT / 32];
 };
 
 // Finds where this CTA's range begins.  False when it has none.  Threads 0 .. NT - 1 call it (NT a power of two).
 template <int NT, int MT, int BN>
-__device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long long (*pre)[NT + 1], long long *sh) {
+__device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, PlanSmem<NT> &sm) {
   const int tid = threadIdx.x;
-  // tiles of the sequences, NT equal shares of them
+  // tiles of the sequences, NT equal shares of them (a thread with one sequence keeps what it read)
   const int cs = (a.N + NT - 1) / NT;
   const int n0 = min(a.N, tid * cs), n1 = min(a.N, n0 + cs);
-  long long cnt = 0;
+  int cnt = 0;
   for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seq_info(a, n));
-  const long long inc = block_scan<NT>(cnt, sh);
-  pre[0][tid + 1] = inc;
-  if (tid == 0) pre[0][0] = 0;
+  const int inc = block_scan<NT>(cnt, sm.scan_tiles);
+  sm.tiles[tid + 1] = inc;
+  if (tid == 0) sm.tiles[0] = 0;
   plan_bar<NT>();
-  const long long NTILE = pre[0][NT];
+  const int NTILE = sm.tiles[NT];
   // units of the tiles, NT equal shares of them
-  const long long ct = (NTILE + NT - 1) / NT;
-  auto seek = [&](long long x, int &n, int &t, SeqInfo &s) {  // tile number x of the line
-    const int sl = find_slot<NT>(pre[0], x);
+  const int ct = (NTILE + NT - 1) / NT;
+  auto seek = [&](int x, int &n, int &t, SeqInfo &s) {  // tile number x of the line
+    const int sl = find_slot<NT>(sm.tiles, x);
     n = sl * cs;
-    long long left = x - pre[0][sl];
+    int left = x - sm.tiles[sl];
     for (;;) {
       s = seq_info(a, n);
       const int k = tiles_of<MT>(a, s);
@@ -144,16 +167,16 @@ __device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long
       left -= k;
       ++n;
     }
-    t = (int)left;
+    t = left;
   };
-  const long long x0 = min(NTILE, tid * ct), x1 = min(NTILE, x0 + ct);
+  const int x0 = (int)min((long long)NTILE, (long long)tid * ct), x1 = (int)min((long long)NTILE, (long long)x0 + ct);
   long long units = 0;
   if (x0 < x1) {
     int n, t;
     SeqInfo s;
     seek(x0, n, t, s);
     int k = tiles_of<MT>(a, s);
-    for (long long x = x0;;) {
+    for (int x = x0;;) {
       units += tile_of<MT, BN>(a, s, t).units();
       if (++x >= x1) break;
       if (++t >= k) {
@@ -165,27 +188,29 @@ __device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long
       }
     }
   }
-  const long long uinc = block_scan<NT>(units * a.Hkv, sh);
-  pre[1][tid + 1] = uinc;
-  if (tid == 0) pre[1][0] = 0;
+  const long long uinc = block_scan<NT>(units * a.Hkv, sm.scan);
+  sm.units[tid + 1] = uinc;
+  if (tid == 0) sm.units[0] = 0;
   plan_bar<NT>();
-  const long long total = pre[1][NT];
-  const long long C = min((long long)gridDim.x, total);
-  if (blockIdx.x >= C) return false;
-  c.u = total * blockIdx.x / C;
-  c.end = total * (blockIdx.x + 1) / C;
-  const int sl = find_slot<NT>(pre[1], c.u);
-  seek(min(NTILE - 1, sl * ct), c.n, c.t, c.s);
-  long long left = c.u - pre[1][sl];
+  const long long total = sm.units[NT];
+  c.split.C = (int)min((long long)gridDim.x, total);
+  if (blockIdx.x >= c.split.C) return false;
+  c.split.q = div_units(total, c.split.C);
+  c.split.r = (int)(total - c.split.q * c.split.C);
+  c.u = c.split.begin(blockIdx.x);
+  c.end = c.split.begin(blockIdx.x + 1);
+  const int sl = find_slot<NT>(sm.units, c.u);
+  seek((int)min((long long)NTILE - 1, (long long)sl * ct), c.n, c.t, c.s);
+  long long left = c.u - sm.units[sl];
   for (;;) {
     c.w = tile_of<MT, BN>(a, c.s, c.t);
-    const long long per = c.w.units();
-    if (left < per * a.Hkv) {
-      c.h = (int)(left / per);
-      c.skip = (int)(left - c.h * per);
+    const int per = c.w.units();
+    if (left < (long long)per * a.Hkv) {
+      c.h = (int)div_units(left, per);
+      c.skip = (int)(left - (long long)c.h * per);
       break;
     }
-    left -= per * a.Hkv;
+    left -= (long long)per * a.Hkv;
     if (++c.t >= tiles_of<MT>(a, c.s)) {
       c.t = 0;
       do c.s = seq_info(a, ++c.n);
@@ -193,6 +218,70 @@ __device__ __forceinline__ bool cursor_begin(const PagedArgs &a, Cursor &c, long
     }
   }
   return true;
+}
+
+// The same for up to 32 sequences with up to 32 tiles, by one warp without barriers: a lane per sequence, then a lane per
+// tile.  A CTA runs this code once, so its time is mostly that of fetching instructions: the general search costs a
+// decode step of one sequence 3 us and more.  Writes c (from one lane) and returns 1, 0 when the CTA has no work, or 2 when the
+// batch is too large.
+template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(const PagedArgs &a, Cursor &c) {
+  if (a.N > 32) return 2;
+  const int lane = threadIdx.x & 31;
+  auto scan = [&](int x) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  SeqInfo s = {0, 0, 0};
+  if (lane < a.N) s = seq_info(a, lane);
+  const int k = lane < a.N ? tiles_of<MT>(a, s) : 0;
+  if (__any_sync(0xffffffffu, k > 32)) return 2;
+  const int inc = scan(k), tiles = __shfl_sync(0xffffffffu, inc, 31);
+  if (tiles > 32) return 2;
+  // lane x takes tile x of the line: its sequence is the first whose tiles reach beyond x
+  int n = 0;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1)
+    if (__shfl_sync(0xffffffffu, inc, n + o - 1) <= lane) n += o;
+  n = min(n, 31);
+  const int t = lane - __shfl_sync(0xffffffffu, inc - k, n);
+  s.qbeg = __shfl_sync(0xffffffffu, s.qbeg, n);
+  s.qlen = __shfl_sync(0xffffffffu, s.qlen, n);
+  s.kv = __shfl_sync(0xffffffffu, s.kv, n);
+  const bool mine = lane < tiles;
+  const Tile w = tile_of<MT, BN>(a, s, mine ? t : 0);
+  const long long un = mine ? (long long)w.units() * a.Hkv : 0;
+  if (__any_sync(0xffffffffu, un > (1 << 25))) return 2;
+  const int uinc = scan((int)un), total = __shfl_sync(0xffffffffu, uinc, 31);
+  const int C = min((int)gridDim.x, total);
+  if ((int)blockIdx.x >= C) return 0;
+  const int q = (unsigned)total / (unsigned)C, r = total - q * C;
+  const int u = blockIdx.x * q + min((int)blockIdx.x, r);
+  if (lane == __ffs(__ballot_sync(0xffffffffu, uinc > u)) - 1) {
+    const int left = u - (uinc - (int)un), per = w.units();
+    c.n = n;
+    c.t = t;
+    c.h = (unsigned)left / (unsigned)per;
+    c.s = s;
+    c.w = w;
+    c.skip = left - c.h * per;
+    c.u = u;
+    c.end = u + q + ((int)blockIdx.x < r);
+    c.split.q = q;
+    c.split.r = r;
+    c.split.C = C;
+  }
+  return 1;
+}
+
+// The header of a CTA whose last item goes on behind its range: c is the cursor at the item's first piece.
+template <int MT> __device__ __forceinline__ int4 cut_header(const PagedArgs &a, const Cursor &c) {
+  const int last = c.split.owner(c.u + c.w.units() - 1);
+  const unsigned r0 = (unsigned)c.t * MT, i = r0 / (unsigned)a.G;
+  return make_int4(last - (int)blockIdx.x + 1, c.s.qbeg + (int)i, c.h, c.w.rows << 16 | (int)(r0 - i * a.G));
 }
 
 // The piece at the cursor: key blocks [b0, b1) (relative to the tile's first), whether it is the item's first and
@@ -231,8 +320,10 @@ __device__ __forceinline__ void row_place(const PagedArgs &a, const Cursor &c, i
   head = c.h * a.G + (int)(g - i * a.G);
 }
 
-cudaError_t launch_attn_rows(const PagedArgs &a, bool bf16_type, int D, int MT, int ctas, cudaStream_t st);
-cudaError_t launch_attn_join(const PagedArgs &a, bool bf16_type, int D, int MT, int ctas, cudaStream_t st);
+cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf16_type, int D, int MT,
+                             int ctas, cudaStream_t st);
+// items: an upper bound on the items of the call
+cudaError_t launch_attn_join(const PagedArgs &a, bool bf16_type, int D, int MT, int ctas, int items, cudaStream_t st);
 cudaError_t launch_attn_chunk_tc(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int D, int ctas,
                                  cudaStream_t st);
 
