@@ -3,18 +3,20 @@
 // Background of the softmax layer in a hybrid stack: onedev.kr summary of the FlashQLA talk, linear-attention
 // background paragraph.
 //
-// Bound by the bytes of the cache: each key and value is used by MT = 16 or 32 rows only (16 flops per byte at four
-// query heads per key head), far below the tensor cores' ratio.  So the kernel is a stream: the units of the whole
-// batch are split evenly over the CTAs (paged.cuh), and inside a CTA each of the four warps owns a 16-token slice of
-// every 64-token block with its own ring of TMA stages, its own running maximum, mass and sums, and no barrier
-// with the other warps until the piece ends.  The query rows stay in registers as mma.sync A fragments; scores come
-// out in the layout that the second product takes as its A operand.  tcgen05 has no use here: its 128-row tile would
-// be one eighth full, and the softmax would leave registers for TMEM and come back.
+// Bound by the bytes of the cache: each key and value is used by a few rows only (16 flops per byte at four query heads
+// per key head), far below the tensor cores' ratio.  So the kernel is a stream: the units of the whole batch are split
+// evenly over the CTAs (paged.cuh), and a CTA's 64-token blocks are cut into four slices of 16 tokens.  A slice belongs
+// to RG warps, each with 16 MI of the tile's rows (MT = 16 MI RG), and has its own ring of TMA stages; every warp has its
+// own running maximum, mass and sums, and meets the other slices only when the piece ends.  The query rows stay in
+// registers as mma.sync A fragments; scores come out in the layout that the second product takes as its A operand.
+// tcgen05 has no use here: its 128-row tile would be an eighth full, and the softmax would leave registers for TMEM and
+// come back.
 //
 // A slice is loaded by one lane, one box of 16 tokens by 128 bytes each, with the 128-byte swizzle, which is what the
 // fragment reads want.  (Sixteen-byte copies by every lane took 40 % of the instructions of the loop.)  Rows of a slice
 // outside what the tile sees are cleared in shared memory; a missing page is loaded from an out-of-range coordinate,
-// which fills zeros.
+// which fills zeros.  At a piece's end the sums go into the stages read last, while the first slices and the queries of
+// the next piece are on their way to the others.
 //
 // The sums are rescaled only when a row's maximum rises by more than 8 (a factor of 256 that fp32 sums and bf16
 // weights carry without loss), so most slices skip that pass over the accumulator.
@@ -30,7 +32,7 @@ using namespace umma;
 
 namespace {
 
-constexpr int WARPS = 4, NT = WARPS * 32, SL = 16, BN = WARPS * SL;
+constexpr int SLICES = 4, SL = 16, BN = SLICES * SL;
 constexpr float RAISE = 8.f;  // log2 of the growth of a row's maximum that is left in its weights
 
 __device__ __forceinline__ float ex2(float x) {
@@ -52,7 +54,7 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 }
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to 11 significant bits, halves away from zero
-  lo = __float_as_uint(x - __uint_as_float(hi));
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;  // rounded likewise (the product ignores the low 13 bits)
 }
 // c += a b with both operands in two TF32 parts
 __device__ __forceinline__ void mma_3tf32(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0, float b1) {
@@ -83,27 +85,54 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
       : "memory");
 }
-constexpr uint32_t WAIT_LIMIT = 1u << 22;
+// Bounded wait that polls with the plain test: a slice is mostly there or about to be, and the test that may suspend costs
+// more than it saves (64 sequences of 512 .. 16384 tokens: 336 us against 345 us).
+__device__ __forceinline__ bool slice_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t it = 0; it < (1u << 25); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+// the warps of one slice
+template <int RG> __device__ __forceinline__ void slice_sync(int slice) {
+  if constexpr (RG == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;\n" ::"r"(2 + slice), "n"(32 * RG) : "memory");
+}
 
 }  // namespace
 
-template <typename I, int D, int MI, int STAGES>
-__global__ void __launch_bounds__(NT, (sizeof(I) == 2 ? 2 : 1))
+template <typename I, int D, int MI, int RG, int STAGES>
+__global__ void __launch_bounds__(128 * RG, RG == 1 && D * sizeof(I) <= 256 ? 2 : 1)
 attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-  constexpr int MT = 16 * MI, RB = D * sizeof(I), CPR = RB / 16, SLB = SL * RB;  // row bytes, chunks, slice bytes
-  constexpr int BOXES = RB / 128, BW = 128 / sizeof(I);                          // boxes of a slice, features of a box
+  constexpr int NT = 128 * RG, MT = 16 * MI * RG, RB = D * sizeof(I), CPR = RB / 16, SLB = SL * RB;
+  constexpr int BOXES = RB / 128, BW = 128 / sizeof(I);  // boxes of a slice, features of a box
+  constexpr int DIST = STAGES - RG;                      // slices on their way ahead of the one in use
   constexpr bool F32 = sizeof(I) == 4;
   constexpr int KS = F32 ? D / 8 : D / 16;  // k steps of q . k
+  static_assert(16 * MI * D * 4 <= 2 * SLB, "a warp's sums fit a stage");
   extern __shared__ uint8_t raw[];
-  __shared__ Cursor cur;  // one for the CTA, out of registers
+  __shared__ Cursor cur, nxt;  // one for the CTA, out of registers
   __shared__ int going;
-  __shared__ uint64_t full[WARPS][STAGES];
+  __shared__ uint64_t full[SLICES][STAGES];
+  __shared__ float mass[4 * RG][2][16 * MI];  // maxima and masses of the warps' rows
+  __shared__ uint32_t where[4 * RG];          // the stages that hold their sums
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t *qsm = smem + WARPS * STAGES * 2 * SLB;  // the query rows, [MT][D]
+  uint8_t *qsm = smem + SLICES * STAGES * 2 * SLB;  // the query rows, [MT][D]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
+  const int slice = warp & 3, rg = warp >> 2;
   const int cta = blockIdx.x;
   const int P = 1 << a.log2P;
-  if (tid < WARPS * STAGES) mbar_init(smem_u32(&full[0][0] + tid), 1);
+  if (tid < SLICES * STAGES) mbar_init(smem_u32(&full[0][0] + tid), 1);
   if (tid == 0) {
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     tma_prefetch_desc(&tk);
@@ -130,77 +159,96 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     __syncthreads();
   }
   bool more = going;
-  uint8_t *ring = smem + warp * (STAGES * 2 * SLB);
-  const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(&full[warp][0]);
+  uint8_t *ring = smem + slice * (STAGES * 2 * SLB);
+  const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(&full[slice][0]);
   const I *Q = static_cast<const I *>(a.q);
   uint32_t st = 0, ph = 0;  // the ring's next stage to be read and its parity
+  auto stage_at = [&](uint32_t k) { return st + k < STAGES ? st + k : st + k - STAGES; };  // k stages on, k < STAGES
 
+  // the blocks [b0, b1) of a piece in which the slice holds a key that some row sees
+  auto blocks = [&](const Cursor &c, int &b0, int &b1) {
+    bool first, last;
+    cursor_piece(c, b0, b1, first, last);
+    const int tw = c.w.blk0 * BN + slice * SL;
+    if (b0 < b1) {
+      if (tw + b0 * BN + SL <= c.w.lo) ++b0;
+      if (tw + (b1 - 1) * BN >= c.w.hi) --b1;
+    }
+    return tw;
+  };
+  auto page_of = [&](const int *trow, int token) {
+    const int pg = trow[token >> a.log2P];
+    return (unsigned)pg < (unsigned)a.num_pages ? pg : a.num_pages;
+  };
+  auto issue = [&](int token, int pg, int h, uint32_t stage) {
+    if (lane == 0 && rg == 0 && !expired) {
+      const uint32_t bar = full_u + 8 * stage, dst = ring_u + stage * 2 * SLB;
+      const int off = token & (P - 1);
+      mbar_expect_tx(bar, 2 * SLB);
+#pragma unroll
+      for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + i * (SL * 128), &tk, i * BW, h, off, pg, bar);
+#pragma unroll
+      for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + SLB + i * (SL * 128), &tv, i * BW, h, off, pg, bar);
+    }
+  };
+  // asks for the queries and the first slices of the piece at c
+  auto begin_piece = [&](const Cursor &c) {
+#pragma unroll
+    for (int i = 0; i < (MT * CPR + NT - 1) / NT; ++i) {  // the rows, coalesced
+      const int x = tid + i * NT, r = x / CPR, ch = x % CPR;
+      if (x < MT * CPR) {
+        int tok, head;
+        row_place(a, c, MT, r < c.w.rows ? r : 0, tok, head);
+        cp_async16(qsm + tile_off<MT>(r, ch), Q + tok * a.q_tok + head * a.q_head + ch * (16 / (int)sizeof(I)), r < c.w.rows);
+      }
+    }
+    int b0, b1, pg[DIST];
+    const int tw = blocks(c, b0, b1);
+    const int *trow = a.table + (long long)c.n * a.table_stride;
+#pragma unroll
+    for (int s = 0; s < DIST; ++s) pg[s] = b0 + s < b1 ? page_of(trow, tw + (b0 + s) * BN) : 0;
+#pragma unroll
+    for (int s = 0; s < DIST; ++s)
+      if (b0 + s < b1) issue(tw + (b0 + s) * BN, pg[s], c.h, stage_at(s));
+  };
+
+  if (more) begin_piece(cur);
   while (more) {
     int b0, b1;
     bool first, last;
     const int n = cursor_piece(cur, b0, b1, first, last);
-    const int lo = cur.w.lo, hi = cur.w.hi, rows = cur.w.rows, pos0 = cur.w.pos0;
-    const int tw = cur.w.blk0 * BN + warp * SL;  // the warp's first token of block 0
-    // blocks of the piece in which the warp's slice holds a key that some row sees
-    if (b0 < b1) {
-      if (tw + b0 * BN + SL <= lo) ++b0;
-      if (tw + (b1 - 1) * BN >= hi) --b1;
-    }
+    const int tw = blocks(cur, b0, b1);
+    const int lo = cur.w.lo, hi = cur.w.hi, rows = cur.w.rows, pos0 = cur.w.pos0, kvh = cur.h;
     const int *trow = a.table + (long long)cur.n * a.table_stride;
-    auto page_of = [&](int b) {
-      if (b >= b1) return 0;
-      const int pg = trow[(tw + b * BN) >> a.log2P];
-      return (unsigned)pg < (unsigned)a.num_pages ? pg : a.num_pages;
-    };
-    auto issue = [&](int b, int pg, uint32_t stage) {
-      if (b < b1 && lane == 0 && !expired) {
-        const uint32_t bar = full_u + 8 * stage, dst = ring_u + stage * 2 * SLB;
-        const int off = (tw + b * BN) & (P - 1);
-        mbar_expect_tx(bar, 2 * SLB);
-#pragma unroll
-        for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + i * (SL * 128), &tk, i * BW, cur.h, off, pg, bar);
-#pragma unroll
-        for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + SLB + i * (SL * 128), &tv, i * BW, cur.h, off, pg, bar);
-      }
-    };
-    {
-      int pg[STAGES - 1];
-#pragma unroll
-      for (int s = 0; s < STAGES - 1; ++s) pg[s] = page_of(b0 + s);
-#pragma unroll
-      for (int s = 0; s < STAGES - 1; ++s) issue(b0 + s, pg[s], st + s < STAGES ? st + s : st + s - STAGES);
-    }
-    int pg_next = page_of(b0 + STAGES - 1);
-
-    // ---- the query rows: coalesced into shared memory, then fragments of rows g and g + 8 of each 16-row tile
-#pragma unroll
-    for (int i = 0; i < (MT * CPR + NT - 1) / NT; ++i) {
-      const int x = tid + i * NT, r = x / CPR, c = x % CPR;
-      if (x < MT * CPR) {
-        int tok, head;
-        row_place(a, cur, MT, r < rows ? r : 0, tok, head);
-        cp_async16(qsm + tile_off<MT>(r, c), Q + tok * a.q_tok + head * a.q_head + c * (16 / (int)sizeof(I)), r < rows);
-      }
+    int pg_next = b0 + DIST < b1 ? page_of(trow, tw + (b0 + DIST) * BN) : 0;
+    if (tid == NT - 1) {
+      Cursor c = cur;
+      going = cursor_next<MT, BN>(a, c, n);
+      nxt = c;
     }
     cp_async_wait_all();
     __syncthreads();
+    more = going;
+
+    // ---- query fragments: rows g and g + 8 of each 16-row tile
     uint32_t qf[MI][KS][4];
     int pos[MI][2];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
+      const int r0 = 16 * (MI * rg + i);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         if constexpr (F32) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            qf[i][k][e] = *reinterpret_cast<const uint32_t *>(qsm + tile_off<MT>(16 * i + g + 8 * (e & 1), 2 * k + (e >> 1)) + 4 * qd);
+            qf[i][k][e] = *reinterpret_cast<const uint32_t *>(qsm + tile_off<MT>(r0 + g + 8 * (e & 1), 2 * k + (e >> 1)) + 4 * qd);
         } else {
-          ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(16 * i + (lane & 15), 2 * k + (lane >> 4)), qf[i][k]);
+          ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(r0 + (lane & 15), 2 * k + (lane >> 4)), qf[i][k]);
         }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const unsigned r = (unsigned)cur.t * MT + min(16 * i + g + 8 * e, rows - 1);
+        const unsigned r = (unsigned)cur.t * MT + min(r0 + g + 8 * e, rows - 1);
         pos[i][e] = cur.s.kv - cur.s.qlen + (int)(r / (unsigned)a.G);
       }
     }
@@ -218,10 +266,10 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     }
 
     for (int b = b0; b < b1; ++b) {
-      if (!expired && !mbar_wait(full_u + 8 * st, ph, nullptr, 0, WAIT_LIMIT)) expired = 4;
-      __syncwarp();  // every lane is done with the block before, too
-      issue(b + STAGES - 1, pg_next, st == 0 ? STAGES - 1 : st - 1);  // the stage that the last block was read from
-      pg_next = page_of(b + STAGES);
+      if (!expired && !slice_wait(full_u + 8 * st, ph)) expired = 4;
+      slice_sync<RG>(slice);  // every lane of the slice's warps is done with the block before, too
+      if (b + DIST < b1) issue(tw + (b + DIST) * BN, pg_next, kvh, stage_at(DIST));
+      if (b + DIST + 1 < b1) pg_next = page_of(trow, tw + (b + DIST + 1) * BN);
       const uint32_t ks = ring_u + st * 2 * SLB, vs = ks + SLB;
       uint8_t *ksp = ring + st * 2 * SLB, *vsp = ksp + SLB;
       if (++st == STAGES) {
@@ -230,7 +278,8 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       }
       const int t0 = tw + b * BN;
       if (t0 < lo || t0 + SL > hi) {
-        // value rows that no query sees become zeros: whatever those slots hold, zero weights keep them out
+        // value rows that no query sees become zeros: whatever those slots hold, zero weights keep them out (the
+        // slice's warps write the same zeros)
         for (int i = lane; i < SLB / 16; i += 32) {
           const int r = (i >> 3) & (SL - 1);
           if (t0 + r < lo || t0 + r >= hi) reinterpret_cast<uint4 *>(vsp)[i] = make_uint4(0, 0, 0, 0);
@@ -377,45 +426,49 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         }
       }
     }
-    __syncthreads();
-
-    // ---- the four warps' sums meet in shared memory (over the rings, which are empty)
-    float *om = reinterpret_cast<float *>(smem) + warp * (MT * (D + 2));
+    // ---- the slices' sums meet: each warp leaves its own in a stage it has read (16-byte chunks of a row change places
+    // by the row's low bits, against bank conflicts)
+    {
+      const uint32_t stage = stage_at(STAGES - 1 - rg);
+      float *om = reinterpret_cast<float *>(ring + stage * 2 * SLB);
+      slice_sync<RG>(slice);  // the other warp of the slice has read it too
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * i + g + 8 * e;
-        const float ls = quad_sum(l[i][e]);
-        if (qd == 0) {
-          om[MT * D + r] = m[i][e];
-          om[MT * D + MT + r] = ls;
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * i + g + 8 * e;
+          const float ls = quad_sum(l[i][e]);
+          if (qd == 0) {
+            mass[warp][0][r] = m[i][e];
+            mass[warp][1][r] = ls;
+          }
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2 *>(om + r * D + (((2 * j + (qd >> 1)) ^ (r & 7)) << 2) + 2 * (qd & 1)) =
+                make_float2(acc[i][j][2 * e], acc[i][j][2 * e + 1]);
         }
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2 *>(om + r * D + 8 * j + 2 * qd) = make_float2(acc[i][j][2 * e], acc[i][j][2 * e + 1]);
-      }
+      if (lane == 0) where[warp] = slice * (STAGES * 2 * SLB) + stage * 2 * SLB;
+    }
     __syncthreads();
+    if (more) begin_piece(nxt);
     constexpr int LPR = D / 4;  // lanes of a row
-    const float *all = reinterpret_cast<const float *>(smem);
     const int slot = first ? 1 : 0;
     float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
-    for (int r = warp * (32 / LPR) + lane / LPR; r < rows; r += WARPS * (32 / LPR)) {
-      const int c = lane % LPR;
-      float mw[WARPS], M = -INFINITY;
+    for (int r = warp * (32 / LPR) + lane / LPR; r < rows; r += 4 * RG * (32 / LPR)) {
+      const int c = lane % LPR, w0 = r / (16 * MI) * 4, rr = r % (16 * MI);  // the row's four warps
+      float mw[4], M = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < WARPS; ++x) {
-        mw[x] = all[x * (MT * (D + 2)) + MT * D + r];
+      for (int x = 0; x < 4; ++x) {
+        mw[x] = mass[w0 + x][0][rr];
         M = fmaxf(M, mw[x]);
       }
       float L = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < WARPS; ++x) {
+      for (int x = 0; x < 4; ++x) {
         const float f = mw[x] == -INFINITY ? 0.f : ex2(mw[x] - M);
-        const float *base = all + x * (MT * (D + 2));
-        const float4 v = *reinterpret_cast<const float4 *>(base + r * D + 4 * c);
-        L += f * base[MT * D + MT + r];
+        const float4 v = *reinterpret_cast<const float4 *>(smem + where[w0 + x] + (rr * D + ((c ^ (rr & 7)) << 2)) * 4);
+        L += f * mass[w0 + x][1][rr];
         o.x += f * v.x;
         o.y += f * v.y;
         o.z += f * v.z;
@@ -445,15 +498,10 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       cut = true;
       if (tid == 0) a.hdr[cta] = cut_header<MT>(a, cur);
     }
-    fence_async_smem();  // the rings are loaded again
+    fence_async_smem();  // the stages with the sums are loaded again
     __syncthreads();
-    if (tid == 0) {
-      Cursor c = cur;
-      going = cursor_next<MT, BN>(a, c, n);
-      cur = c;
-    }
+    if (tid == 0) cur = nxt;
     __syncthreads();
-    more = going;
   }
   if (tid == 0 && !cut) a.hdr[cta] = make_int4(0, 0, 0, 0);
   if (expired) {  // copies in flight end, if they do, before the shared memory goes
@@ -465,17 +513,17 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 
 // Joins the pieces of cut items.  Block (j, y): rows of the j-th of them, which began in some CTA c and went on in the
 // next ones (the block looks for c in the headers, so that the grid need not be larger than the number of items).  JW
-// warps share a row (4 for the few rows of decoding, whose items may be cut into hundreds of pieces; 1 for the 256-row
-// tiles): each takes every JW-th batch of 8 pieces, asks for all of a batch before it uses any, and weights the batch by
+// warps share a row (8 where few items are cut into many pieces each, 1 where many are cut into a few): each takes every JW-th batch of 8 pieces, asks for all of a batch before it uses any, and weights the batch by
 // the running maximum; the warps' results meet in shared memory.  The order of the sums is fixed.
 template <typename I, int D, int JW>
-__global__ void __launch_bounds__(128) attn_join_kernel(PagedArgs a, int MT, int C) {
-  constexpr int RW = 4 / JW, E = D / 32, BATCH = 8;
-  __shared__ float sh[4][32 * E + 2];
+__global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(PagedArgs a, int MT, int C) {
+  constexpr int WARPS = JW == 1 ? 4 : JW, RW = WARPS / JW, E = D / 32, BATCH = 8;
+  __shared__ float sh[WARPS][32 * E + 2];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int c = -1, left = blockIdx.x;
+  if ((int)gridDim.x == C) c = left;  // as many blocks as CTAs: no search
   for (int b = 0; b < C && c < 0; b += 256) {
     int x[8];
 #pragma unroll
@@ -492,7 +540,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(PagedArgs a, int MT, int
   const int4 h = a.hdr[c];
   const int np = h.x, rows = h.w >> 16, gr = h.w & 0xffff;
   const int r = blockIdx.y * RW + warp / JW, sub = warp % JW;
-  if (blockIdx.y * RW >= rows) return;
+  if (np == 0 || blockIdx.y * RW >= rows) return;
   const long long rf = (long long)record_floats(MT, D);
   // piece 0 is slot 1 of CTA c, piece i slot 0 of CTA c + i
   const float *p0 = a.part + ((long long)c * 2 + 1) * rf, *p1 = a.part + (long long)c * 2 * rf;
@@ -577,40 +625,45 @@ __global__ void __launch_bounds__(128) attn_join_kernel(PagedArgs a, int MT, int
 }
 
 namespace {
-template <typename I, int D, int MI, int STAGES>
+template <typename I, int D, int MI, int RG, int STAGES>
 cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  constexpr size_t ring = (size_t)WARPS * STAGES * 2 * SL * D * sizeof(I);
-  static_assert(ring >= (size_t)WARPS * record_floats(16 * MI, D) * 4, "the sums meet in the rings' memory");
-  static_assert(ring >= sizeof(PlanSmem<NT>), "the search uses it too");
-  constexpr size_t smem = 1024 + ring + (size_t)16 * MI * D * sizeof(I);
-  auto *k = attn_rows_kernel<I, D, MI, STAGES>;
+  constexpr size_t ring = (size_t)SLICES * STAGES * 2 * SL * D * sizeof(I);
+  static_assert(ring >= sizeof(PlanSmem<128 * RG>), "the search uses the rings' memory");
+  constexpr size_t smem = 1024 + ring + (size_t)16 * MI * RG * D * sizeof(I);
+  auto *k = attn_rows_kernel<I, D, MI, RG, STAGES>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k, dim3(ctas), dim3(NT), smem, st, a, tk, tv);
+  return launch_pdl(k, dim3(ctas), dim3(128 * RG), smem, st, a, tk, tv);
 }
 }  // namespace
 
-// bf16: rings of 96 KB, so that two CTAs share an SM; fp32: 16 rows, and 96 KB (D = 64) or 192 KB rings
+// 16 rows a tile where that is enough, and then 96 KB of rings and two CTAs per SM unless a slice is 16 KB (fp32, D =
+// 128); more rows: two row groups (fp32, D = 64: of 32 rows each, so that a key's split into two parts serves both
+// 16-row tiles), 192 KB of rings.
+int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 ? 16 : (!bf && D == 64 ? 64 : 32); }
+int attn_rows_per_sm(bool bf, int D, int MT) { return MT == 16 && (bf || D == 64) ? 2 : 1; }
 cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf, int D, int MT, int ctas,
                              cudaStream_t st) {
-  if (!bf) return D == 64 ? launch_rows<float, 64, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 1, 3>(a, tk, tv, ctas, st);
-  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 6>(a, tk, tv, ctas, st);
-  return MT == 16 ? launch_rows<bf16, 128, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 2, 3>(a, tk, tv, ctas, st);
+  if (!bf) {
+    if (D == 64) return MT == 16 ? launch_rows<float, 64, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 64, 2, 2, 6>(a, tk, tv, ctas, st);
+    return MT == 16 ? launch_rows<float, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 1, 2, 3>(a, tk, tv, ctas, st);
+  }
+  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 1, 2, 12>(a, tk, tv, ctas, st);
+  return MT == 16 ? launch_rows<bf16, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 1, 2, 6>(a, tk, tv, ctas, st);
 }
 
-cudaError_t launch_attn_join(const PagedArgs &a, bool bf, int D, int MT, int ctas, int items, cudaStream_t st) {
+namespace {
+template <typename I, int D> cudaError_t launch_join(const PagedArgs &a, int MT, int ctas, int items, cudaStream_t st) {
   const int n = items < ctas ? items : ctas;  // cut items at most
-  if (MT == 256) {  // bf16
-    const dim3 grid(n, 64);
-    return D == 64 ? launch_pdl(attn_join_kernel<bf16, 64, 1>, grid, dim3(128), 0, st, a, MT, ctas)
-                   : launch_pdl(attn_join_kernel<bf16, 128, 1>, grid, dim3(128), 0, st, a, MT, ctas);
-  }
-  const dim3 grid(n, MT);
-  if (bf)
-    return D == 64 ? launch_pdl(attn_join_kernel<bf16, 64, 4>, grid, dim3(128), 0, st, a, MT, ctas)
-                   : launch_pdl(attn_join_kernel<bf16, 128, 4>, grid, dim3(128), 0, st, a, MT, ctas);
-  return D == 64 ? launch_pdl(attn_join_kernel<float, 64, 4>, grid, dim3(128), 0, st, a, MT, ctas)
-                 : launch_pdl(attn_join_kernel<float, 128, 4>, grid, dim3(128), 0, st, a, MT, ctas);
+  // few items: many pieces each
+  if (items * 8 <= ctas) return launch_pdl(attn_join_kernel<I, D, 8>, dim3(n, MT), dim3(256), 0, st, a, MT, ctas);
+  return launch_pdl(attn_join_kernel<I, D, 1>, dim3(n, (MT + 3) / 4), dim3(128), 0, st, a, MT, ctas);
+}
+}  // namespace
+
+cudaError_t launch_attn_join(const PagedArgs &a, bool bf, int D, int MT, int ctas, int items, cudaStream_t st) {
+  if (bf) return D == 64 ? launch_join<bf16, 64>(a, MT, ctas, items, st) : launch_join<bf16, 128>(a, MT, ctas, items, st);
+  return D == 64 ? launch_join<float, 64>(a, MT, ctas, items, st) : launch_join<float, 128>(a, MT, ctas, items, st);
 }
 
 }  // namespace gdn

@@ -74,7 +74,7 @@ int check_attn(const gdn_paged_shape *s) {
 }
 
 // The kernel of a call and its grid: bf16 with more than 32 (query, head) rows per key head in the longest sequence
-// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 or 32 rows).
+// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 to 64 rows).
 struct AttnPlan {
   bool tc;
   int MT, ctas;
@@ -86,8 +86,8 @@ AttnPlan attn_plan(const gdn_paged_shape *s) {
   const long long rows = (long long)(s->max_q > 0 ? s->max_q : (s->total_q + s->num_seqs - 1) / std::max(1, s->num_seqs)) * G;
   const bool bf = s->dtype == GDN_BF16;
   p.tc = bf && rows > 32;
-  p.MT = p.tc ? 256 : (bf && rows > 16 ? 32 : 16);
-  p.ctas = num_sms() * (bf && !p.tc ? 2 : 1);
+  p.MT = p.tc ? 256 : attn_rows_tile(bf, s->head_dim, (int)std::min(rows, 1ll << 20));
+  p.ctas = num_sms() * (p.tc ? 1 : attn_rows_per_sm(bf, s->head_dim, p.MT));
   p.off_status = up256((size_t)p.ctas * sizeof(int4));
   p.off_part = p.off_status + up256((size_t)p.ctas * sizeof(int));
   p.total = p.off_part + up256((size_t)p.ctas * 2 * record_floats(p.MT, s->head_dim) * 4);
