@@ -226,13 +226,13 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   pdl_trigger();
   pdl_wait();
   if (warp == 0) {
-    const int found = cursor_begin_small<MT, BN>(a, cursors[0]);
+    const int found = cursor_begin_one_warp<MT, BN>(a, cursors[0]);
     if (lane == 0) has_work = found;
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (const int found = has_work; found == 2) {  // more than 32 tiles
+  if (const int found = has_work; found == 2) {  // a batch too large for one warp
     __syncthreads();                             // everyone has read it
     if (tid < SOFT) {
       Cursor c;

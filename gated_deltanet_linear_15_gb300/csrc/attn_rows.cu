@@ -143,11 +143,11 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
   bool cut = false;  // this CTA's header is written
   int expired = 0;   // a bounded wait ran out
   if (warp == 0) {
-    const int found = cursor_begin_small<MT, BN>(a, cur);
+    const int found = cursor_begin_one_warp<MT, BN>(a, cur);
     if (lane == 0) going = found;
   }
   __syncthreads();
-  if (const int found = going; found == 2) {  // more than 32 tiles
+  if (const int found = going; found == 2) {  // a batch too large for one warp
     __syncthreads();                          // everyone has read it
     Cursor c;
     const bool some = cursor_begin_any<NT, MT, BN>(a, c, *reinterpret_cast<PlanSmem<NT> *>(smem));

@@ -220,10 +220,96 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
   return true;
 }
 
-// The same for up to 32 sequences with up to 32 tiles, by one warp without barriers: a lane per sequence, then a lane per
-// tile.  A CTA runs this code once, so its time is mostly that of fetching instructions: the general search costs a
-// decode step of one sequence 3 us and more.  Writes c (from one lane) and returns 1, 0 when the CTA has no work, or 2 when the
-// batch is too large.
+// The same for up to 512 sequences with up to 2048 tiles, by one warp without barriers, each lane taking an equal share of
+// the sequences and then of the tiles.  A CTA runs this code once, so most of its time is that of fetching instructions;
+// the search above costs 64 sequences 7 us more.  Writes c (from one lane) and returns 1, 0 when the CTA
+// has no work, or 2 when the batch is too large.
+template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const PagedArgs &a, Cursor &c) {
+  if (a.N > 512) return 2;
+  const int lane = threadIdx.x & 31;
+  auto scan = [&](long long x) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  const int cs = (a.N + 31) >> 5, n0 = min(a.N, lane * cs), n1 = min(a.N, n0 + cs);
+  long long cnt = 0;
+#pragma unroll 1
+  for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seq_info(a, n));
+  const long long inc = scan(cnt), all = __shfl_sync(0xffffffffu, inc, 31);
+  if (all > 2048) return 2;
+  // this lane's tiles [x0, x1); the first one's sequence is among those of the first lane whose tiles reach beyond x0
+  const int tiles = (int)all, ct = (tiles + 31) >> 5, x0 = min(tiles, lane * ct), x1 = min(tiles, x0 + ct);
+  int own = 0;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1)
+    if ((int)__shfl_sync(0xffffffffu, (int)inc, own + o - 1) <= x0) own += o;
+  int left = x0 - __shfl_sync(0xffffffffu, (int)(inc - cnt), own);
+  // walks from tile x0 on; a second time, up to unit `stop`, for the lane that holds the CTA's first one
+  int n = own * cs, t = 0, k = 0;
+  SeqInfo s = {0, 0, 0};
+  Tile w;
+  long long units = 0, stop = 1ll << 62;
+  bool twice = false;
+  long long u = 0, uinc = 0, mine = 0;
+  Split sp = {1, 0, 1};
+  for (;;) {
+    if (x0 < x1) {
+      int nn = n;
+      t = left;
+#pragma unroll 1
+      for (;; ++nn) {
+        s = seq_info(a, nn);
+        k = tiles_of<MT>(a, s);
+        if (t < k) break;
+        t -= k;
+      }
+      units = 0;
+#pragma unroll 1
+      for (int x = x0;;) {
+        w = tile_of<MT, BN>(a, s, t);
+        const long long per = (long long)w.units() * a.Hkv;
+        if (units + per > stop) break;
+        units += per;
+        if (++x >= x1) break;
+        for (++t; t >= k; t = 0) {
+          s = seq_info(a, ++nn);
+          k = tiles_of<MT>(a, s);
+        }
+      }
+      if (twice) n = nn;
+    }
+    if (twice) break;
+    mine = units;
+    uinc = scan(units);
+    const long long total = __shfl_sync(0xffffffffu, uinc, 31);
+    sp.C = (int)min((long long)gridDim.x, total);
+    if ((int)blockIdx.x >= sp.C) return 0;
+    sp.q = div_units(total, sp.C);
+    sp.r = (int)(total - sp.q * sp.C);
+    u = sp.begin(blockIdx.x);
+    if (lane != __ffs(__ballot_sync(0xffffffffu, uinc > u)) - 1) return 1;
+    stop = u - (uinc - mine);
+    twice = true;
+  }
+  const int per = w.units();
+  c.n = n;
+  c.t = t;
+  c.h = (int)div_units(stop - units, per);
+  c.s = s;
+  c.w = w;
+  c.skip = (int)(stop - units - (long long)c.h * per);
+  c.u = u;
+  c.end = sp.begin(blockIdx.x + 1);
+  c.split = sp;
+  return 1;
+}
+
+// And for up to 32 sequences with up to 32 tiles: a lane per sequence, then a lane per tile (1 us less than the search
+// above for a decode step of one sequence).  Returns what it returns.
 template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(const PagedArgs &a, Cursor &c) {
   if (a.N > 32) return 2;
   const int lane = threadIdx.x & 31;
@@ -275,6 +361,12 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(cons
     c.split.C = C;
   }
   return 1;
+}
+
+// One warp's search, whichever fits
+template <int MT, int BN> __device__ __forceinline__ int cursor_begin_one_warp(const PagedArgs &a, Cursor &c) {
+  const int found = cursor_begin_small<MT, BN>(a, c);
+  return found == 2 ? cursor_begin_warp<MT, BN>(a, c) : found;
 }
 
 // The header of a CTA whose last item goes on behind its range: c is the cursor at the item's first piece.

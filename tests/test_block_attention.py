@@ -138,6 +138,22 @@ def test_long_context_is_split_and_joined():
 
 
 @gpu
+@pytest.mark.parametrize("N,q,dtype", [(33, 1, BF), (300, 1, BF), (300, 3, F32), (513, 1, BF), (700, 2, BF), (90, 40, BF), (600, 20, BF),
+                                       (3, 1500, F32)])
+def test_many_sequences(N, q, dtype):
+    """Batches of every size class of the search for a CTA's share, with empty sequences and sequences without new tokens
+    among them."""
+    import random
+
+    import gated_deltanet_linear_15_gb300 as g
+    r = random.Random(N)
+    seqs = [(r.choice([q, q, r.randint(0, q)]), r.randint(0, 70)) for _ in range(N)]
+    x, qs = make(seqs, dtype, 64, 2, 1, 16, seed=N)
+    o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=q, return_lse=True)
+    close(o, lse, x, qs, 0.125)
+
+
+@gpu
 def test_peaked_and_growing_logits():
     """Logits that grow along the context (the maximum rises at every step) and by far more than fp32's exponent range
     would bear without it."""
