@@ -33,27 +33,36 @@ cudaError_t launch_rope_table(const double *freq, int pairs, int rows, double am
 constexpr int MAX_POOLS = 64;  // pools of one launch
 struct PoolList {
   gdn_slot_pool p[MAX_POOLS];
+  int list[MAX_POOLS];              // which of the launch's two pair lists a pool follows
   long long chunk0[MAX_POOLS + 1];  // chunks of the pools before, per pair
   int n;
+};
+struct PairList {
+  const int *src, *dst;  // slot src[i] -> dst[i]; negative numbers are left out
 };
 struct PagesArgs {
   int S, W, NP, P;
   long long ts;
   int *table, *lens, *ref;
 };
-// pairs src[i] -> dst[i] for i < (count_dev ? *count_dev : count); negative numbers are left out
-cudaError_t launch_slots_copy(const PoolList &pl, const int *src, const int *dst, int count, const int *count_dev,
+// what a copy launch does to the tables first: nothing, the rows of forked children, or the renaming of moved pages
+struct TableJob {
+  enum { NONE, FORK, REMAP } kind;
+  PagesArgs a;
+  const int *psrc, *pdst, *new_page;  // FORK: parent, child, copied page of every fork
+  int m;
+  const int *table_in, *ref_in, *map, *front;  // REMAP: new number of every moved page, pages in use
+};
+// pairs i < (count_dev ? min(count, *count_dev) : count) of both lists
+cudaError_t launch_slots_copy(const PoolList &pl, const PairList (&pairs)[2], int count, const int *count_dev, const TableJob &job,
                               cudaStream_t st);
 cudaError_t launch_pages_extend(const PagesArgs &a, const int *seqs, const int *add, int m, int *ok, int *ws,
                                 cudaStream_t st);
 cudaError_t launch_pages_fork_plan(const PagesArgs &a, const int *parents, const int *children, int m, int *new_page,
                                    int *src, int *psrc, int *pdst, cudaStream_t st);
-cudaError_t launch_pages_fork_rows(const PagesArgs &a, const int *psrc, const int *pdst, const int *new_page, int m,
-                                   cudaStream_t st);
 cudaError_t launch_pages_free(const PagesArgs &a, const int *seqs, int m, cudaStream_t st);
 cudaError_t launch_pages_compact_plan(const PagesArgs &a, const int *ref_in, int *map, int *src, int *dst, int *moves,
-                                      cudaStream_t st);
-cudaError_t launch_pages_remap(const PagesArgs &a, const int *table_in, const int *map, cudaStream_t st);
+                                      int *front, cudaStream_t st);
 
 // ---- norm
 struct NormArgs {

@@ -143,15 +143,22 @@ int check_pools(const gdn_slot_pool *p, int n, const char *what) {
   }
   return GDN_OK;
 }
-// the copies of a call, MAX_POOLS pools to a launch
-int copy_slots(const gdn_slot_pool *p, int n, const int *src, const int *dst, int count, const int *count_dev, Stream st) {
-  for (int b = 0; b < n; b += MAX_POOLS) {
+// the copies of a call, MAX_POOLS pools to a launch, the first of which does the job on the tables too
+int copy_slots(const gdn_slot_pool *p, int n, const gdn_slot_pool *q, int nq, const PairList (&pairs)[2], int count,
+               const int *count_dev, TableJob job, Stream st) {
+  int b = 0;
+  do {
     PoolList l;
-    l.n = std::min(MAX_POOLS, n - b);
-    for (int i = 0; i < l.n; ++i) l.p[i] = p[b + i];
+    l.n = std::min(MAX_POOLS, n + nq - b);
+    for (int i = 0; i < l.n; ++i) {
+      l.list[i] = b + i >= n;
+      l.p[i] = b + i < n ? p[b + i] : q[b + i - n];
+    }
     PROF("slots_copy");
-    CK(launch_slots_copy(l, src, dst, count, count_dev, st));
-  }
+    CK(launch_slots_copy(l, pairs, count, count_dev, job, st));
+    job.kind = TableJob::NONE;
+    b += l.n;
+  } while (b < n + nq);
   return GDN_OK;
 }
 
@@ -294,7 +301,7 @@ int gdn_rotary(const gdn_rotary_shape *s, const void *q, const void *k, const fl
   TRY(need_ptr(positions, "positions"));
   RopeArgs a = {};
   const int v = 16 / (int)esize(s->dtype);
-  bool vec = s->head_dim % (2 * v) == 0 && s->rot % (2 * v) == 0;
+  bool vec = s->head_dim % (2 * v) == 0 && s->rot % (2 * v) == 0 && s->head_dim <= 256 * 2 * v;  // a CTA holds a head
   auto add = [&](const void *src, void *dst, int heads, int64_t st_, int64_t sh, int64_t dt, int64_t dh) {
     if (!heads) return;
     a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, 0, heads, 1};
@@ -334,7 +341,7 @@ int gdn_rotary_append(const gdn_paged_shape *s, const void *q, const void *k, co
   if (s->k_page < 1 || s->v_page < 1) return fail(GDN_ERR_INVALID_ARG, "page strides must be positive");
   RopeArgs a = {};
   const int w = 16 / (int)esize(s->dtype);
-  bool vec = s->head_dim % (2 * w) == 0 && s->rot % (2 * w) == 0;
+  bool vec = s->head_dim % (2 * w) == 0 && s->rot % (2 * w) == 0 && s->head_dim <= 256 * 2 * w;  // a CTA holds a head
   auto add = [&](const void *src, void *dst, int heads, int turn, int64_t st_, int64_t sh, int64_t dt, int64_t dh, int64_t dp) {
     a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, dp, heads, turn};
     a.heads += heads;
@@ -360,7 +367,8 @@ int gdn_slots_copy(const gdn_slot_pool *pools, int num_pools, const int32_t *src
   if (count == 0 || num_pools == 0) return GDN_OK;
   TRY(need_ptr(src, "src"));
   TRY(need_ptr(dst, "dst"));
-  return copy_slots(pools, num_pools, src, dst, count, nullptr, (Stream)stream);
+  const PairList pairs[2] = {{src, dst}, {src, dst}};
+  return copy_slots(pools, num_pools, nullptr, 0, pairs, count, nullptr, TableJob{}, (Stream)stream);
 }
 
 size_t gdn_pages_workspace_size(const gdn_pages_shape *s, int m) {
@@ -369,8 +377,8 @@ size_t gdn_pages_workspace_size(const gdn_pages_shape *s, int m) {
     fail(GDN_ERR_INVALID_ARG, "m must be >= 0");
     return 0;
   }
-  // extend: prefix [m + 1]; fork: src, parents, children [m] and two lists [m]; compact: map, src, dst [pages], count
-  return up256(std::max((size_t)5 * m + 1, (size_t)3 * s->num_pages + 1) * 4);
+  // extend: prefix [m + 1]; fork: src, parents, children [m] and two lists [m]; compact: map, src, dst [pages], two counts
+  return up256(std::max((size_t)5 * m + 1, (size_t)3 * s->num_pages + 2) * 4);
 }
 #define CHECK_WS(need)                                                                                                   \
   if (!ws || ws_bytes < (need))                                                                                          \
@@ -417,12 +425,15 @@ int gdn_pages_fork(const gdn_pages_shape *s, int32_t *table, int32_t *lens, int3
     PROF("pages_fork_plan");
     CK(launch_pages_fork_plan(a, parents, children, m, new_page, src, psrc, pdst, st));
   }
-  {
-    PROF("pages_fork_rows");
-    CK(launch_pages_fork_rows(a, psrc, pdst, new_page, m, st));
-  }
-  TRY(copy_slots(pools, num_pools, src, new_page, m, nullptr, st));
-  return copy_slots(states, num_states, psrc, pdst, m, nullptr, st);
+  TableJob job = {};
+  job.kind = TableJob::FORK;
+  job.a = a;
+  job.psrc = psrc;
+  job.pdst = pdst;
+  job.new_page = new_page;
+  job.m = m;
+  const PairList pairs[2] = {{src, new_page}, {psrc, pdst}};
+  return copy_slots(pools, num_pools, states, num_states, pairs, m, nullptr, job, st);
 }
 
 int gdn_pages_free(const gdn_pages_shape *s, int32_t *table, int32_t *lens, int32_t *ref, const int32_t *seqs, int m, gdn_stream_t stream) {
@@ -450,18 +461,22 @@ int gdn_pages_compact(const gdn_pages_shape *s, const int32_t *table, const int3
   TRY(need_ptr(ref_out, "refcount_out"));
   CHECK_WS(gdn_pages_workspace_size(s, 0));
   const Stream st = (Stream)stream;
-  int *map = static_cast<int *>(ws), *src = map + s->num_pages, *dst = src + s->num_pages, *count = dst + s->num_pages;
+  int *map = static_cast<int *>(ws), *src = map + s->num_pages, *dst = src + s->num_pages, *count = dst + s->num_pages, *front = count + 1;
   if (!moves) moves = count;
   const PagesArgs a = pages_args(s, table_out, nullptr, ref_out);
   {
     PROF("pages_compact_plan");
-    CK(launch_pages_compact_plan(a, ref, map, src, dst, moves, st));
+    CK(launch_pages_compact_plan(a, ref, map, src, dst, moves, front, st));
   }
-  {
-    PROF("pages_remap");
-    CK(launch_pages_remap(a, table, map, st));
-  }
-  return copy_slots(pools, num_pools, src, dst, s->num_pages / 2, moves, st);
+  TableJob job = {};
+  job.kind = TableJob::REMAP;
+  job.a = a;
+  job.table_in = table;
+  job.ref_in = ref;
+  job.map = map;
+  job.front = front;
+  const PairList pairs[2] = {{src, dst}, {src, dst}};
+  return copy_slots(pools, num_pools, nullptr, 0, pairs, s->num_pages / 2, moves, job, st);
 }
 
 int gdn_rmsnorm_fwd(const gdn_norm_shape *s, const void *x, const void *residual, const float *weight, void *h_out,
@@ -500,7 +515,7 @@ static NormArgs bwd_args(const gdn_norm_shape *s, const void *dy, const void *h,
 
 size_t gdn_rmsnorm_bwd_workspace_size(const gdn_norm_shape *s) {
   if (check_norm(s, true)) return 0;
-  return up256((size_t)num_sms() * 2 * s->dim * 4);  // one partial row of dw for each of at most two CTAs per SM
+  return up256((size_t)num_sms() * 4 * s->dim * 4);  // one partial row of dw for each of at most four CTAs per SM
 }
 
 int gdn_rmsnorm_bwd(const gdn_norm_shape *s, const void *dy, const void *h, const float *weight, const float *rstd,

@@ -4,7 +4,7 @@
 //
 // The bookkeeping is whole numbers: free pages are handed out lowest first, in the order of the request list, by
 // prefix sums, so every run gives the same tables.  One CTA plans (its scans run over the requests and, until enough
-// are found, over the pages' counts, 4096 of them a step); what is long, the rows of the tables and the copies, goes to
+// are found, over the pages' counts, 16384 of them a step); what is long, the rows of the tables and the copies, goes to
 // the whole GPU in a second launch.  Copies are bound by bytes (each slot read and written once): a slot is cut into
 // 16 KB chunks, the chunks of all pairs and pools stand in one line, and a warp-coalesced thread moves four 16-byte
 // pieces at a time, loaded before the first is stored.
@@ -43,45 +43,91 @@ __device__ __forceinline__ int scan_1024(int x, int *sh) {
   return x + (warp ? sh[warp - 1] : 0);
 }
 
-// counts ref[i], i = base + 4 tid + e, of a step of 4096 pages (1 past the end)
-__device__ __forceinline__ void load_refs(const int *ref, int NP, int base, int (&r)[4]) {
-  const int i = base + 4 * threadIdx.x;
-  if (i + 3 < NP && (reinterpret_cast<uintptr_t>(ref) & 15) == 0) {
-    const int4 v = *reinterpret_cast<const int4 *>(ref + i);
-    r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-  } else {
+constexpr int SUB = 4, STEP = SUB * 4 * NP_T;  // a step: SUB rounds of four counts per thread, 16384 in all
+
+// r[4 k + e] = the count of page base + 4096 k + 4 tid + e (`past` past the end): neighbours in neighbouring threads
+__device__ __forceinline__ void load_refs(const int *ref, int NP, int base, int past, int (&r)[4 * SUB]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = i + e < NP ? ref[i + e] : 1;
+  for (int k = 0; k < SUB; ++k) {
+    const int i = base + 4 * (NP_T * k + (int)threadIdx.x);
+    if (i + 4 <= NP && (reinterpret_cast<uintptr_t>(ref) & 15) == 0) {
+      const int4 v = *reinterpret_cast<const int4 *>(ref + i);
+      r[4 * k] = v.x; r[4 * k + 1] = v.y; r[4 * k + 2] = v.z; r[4 * k + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[4 * k + e] = i + e < NP ? ref[i + e] : past;
+    }
   }
+}
+
+// The SUB rounds' counts in one scan: 16 bits each (a round has 4096 pages at most).  n: this thread's; on return rank[k]
+// pages of the step come before this thread's of round k.  Returns the step's total.
+__device__ __forceinline__ int scan_rounds(const int (&n)[SUB], int (&rank)[SUB], unsigned long long *sh) {
+  unsigned long long x = 0;
+#pragma unroll
+  for (int k = 0; k < SUB; ++k) x |= (unsigned long long)n[k] << (16 * k);
+  const unsigned long long own = x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  unsigned long long y = sh[lane];  // every warp sums the warps' totals for itself
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
+  }
+  const unsigned long long all = __shfl_sync(0xffffffffu, y, 31), before = __shfl_sync(0xffffffffu, y, warp ? warp - 1 : 0);
+  x += (warp ? before : 0) - own;
+  int sum = 0;
+#pragma unroll
+  for (int k = 0; k < SUB; ++k) {
+    rank[k] = sum + (int)(x >> (16 * k) & 0xffff);
+    sum += (int)(all >> (16 * k) & 0xffff);
+  }
+  return sum;
 }
 
 // Calls give(rank, page) for the free pages of rank 0 .. want - 1 (ascending numbers), and returns how many free pages
 // were seen (at least `want` when there are so many).
-template <class F> __device__ __forceinline__ int hand_out(const int *ref, int NP, int want, int *sh, F give) {
+template <class F>
+__device__ __forceinline__ int hand_out(const int *ref, int NP, int want, unsigned long long *sh, F give) {
   int seen = 0;
-  for (int base = 0; base < NP && seen < want; base += 4 * NP_T) {
-    int r[4];
-    load_refs(ref, NP, base, r);
-    int n = 0;
+  for (int base = 0; base < NP && seen < want; base += STEP) {
+    int r[4 * SUB], n[SUB], rank[SUB];
+    load_refs(ref, NP, base, 1, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) n += r[e] <= 0;
-    const int inc = scan_1024(n, sh);
-    int rank = seen + inc - n;
+    for (int k = 0; k < SUB; ++k) {
+      n[k] = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (r[e] <= 0) {
-        if (rank < want) give(rank, base + 4 * (int)threadIdx.x + e);
-        ++rank;
+      for (int e = 0; e < 4; ++e) n[k] += r[4 * k + e] <= 0;
+    }
+    const int all = scan_rounds(n, rank, sh);
+#pragma unroll
+    for (int k = 0; k < SUB; ++k) {
+      int x = seen + rank[k];
+      if (n[k] > 0 && x < want) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r[4 * k + e] <= 0) {
+            if (x < want) give(x, base + 4 * (NP_T * k + (int)threadIdx.x) + e);
+            ++x;
+          }
       }
-    const int all = sh[31];
-    __syncthreads();
+    }
     seen += all;
   }
+  __syncthreads();
   return seen;
 }
 
 // free pages in all, up to `want`
-__device__ __forceinline__ int count_free(const int *ref, int NP, int want, int *sh) {
+__device__ __forceinline__ int count_free(const int *ref, int NP, int want, unsigned long long *sh) {
   return hand_out(ref, NP, want, sh, [](int, int) {});
 }
 
@@ -92,6 +138,7 @@ __device__ __forceinline__ int pages_of(int len, int P) { return (int)(((long lo
 // ws: prefix[m + 1] of the pages that the granted requests take
 __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const int *seqs, const int *add, int m, int *ok, int *pre) {
   __shared__ int sh[32];
+  __shared__ unsigned long long sh64[32];
   __shared__ int granted;
   pdl_trigger();
   pdl_wait();
@@ -131,7 +178,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
     granted = 0;
   }
   __syncthreads();
-  const int avail = count_free(a.ref, a.NP, (int)total, sh);
+  const int avail = count_free(a.ref, a.NP, (int)total, sh64);
   // the requests whose pages, and all before theirs, are there
   for (int i = tid; i < m; i += NP_T) {
     const int need = pre[i + 1] - pre[i];
@@ -140,7 +187,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
   }
   __syncthreads();
   const int want = granted;
-  hand_out(a.ref, a.NP, want, sh, [&](int rank, int page) {
+  hand_out(a.ref, a.NP, want, sh64, [&](int rank, int page) {
     int lo = 0, hi = m;  // the request with pre[lo] <= rank < pre[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -161,6 +208,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
 __global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, const int *parents, const int *children, int m,
                                                                int *new_page, int *src, int *psrc, int *pdst) {
   __shared__ int sh[32];
+  __shared__ unsigned long long sh64[32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -199,7 +247,7 @@ __global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, cons
   for (int i = tid; i < m; i += NP_T)
     if (new_page[i] >= 0) list[new_page[i]] = i;
   __syncthreads();
-  const int seen = hand_out(a.ref, a.NP, total, sh, [&](int rank, int page) { list[m + rank] = page; });
+  const int seen = hand_out(a.ref, a.NP, total, sh64, [&](int rank, int page) { list[m + rank] = page; });
   __syncthreads();
   for (int r = tid; r < total; r += NP_T) {
     const int i = list[r];
@@ -216,25 +264,6 @@ __global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, cons
     if (pdst[i] >= 0) a.lens[pdst[i]] = a.lens[psrc[i]];
 }
 
-// the children's table rows, and a reference more for every page that they share
-__global__ void __launch_bounds__(256) pages_fork_rows_kernel(PagesArgs a, const int *psrc, const int *pdst, const int *new_page) {
-  pdl_trigger();
-  pdl_wait();
-  const int i = blockIdx.x, p = psrc[i], c = pdst[i];
-  if (p < 0) return;
-  const int len = a.lens[p], full = len / a.P;
-  for (int j = blockIdx.y * 256 + threadIdx.x; j < a.W; j += 256 * gridDim.y) {
-    int pg = -1;
-    if (j < full) {
-      pg = a.table[p * a.ts + j];
-      if ((unsigned)pg < (unsigned)a.NP) atomicAdd(a.ref + pg, 1);
-    } else if (j == full && len % a.P != 0) {
-      pg = new_page[i];
-    }
-    a.table[c * a.ts + j] = pg;
-  }
-}
-
 __global__ void __launch_bounds__(256) pages_free_kernel(PagesArgs a, const int *seqs) {
   pdl_trigger();
   pdl_wait();
@@ -248,77 +277,115 @@ __global__ void __launch_bounds__(256) pages_free_kernel(PagesArgs a, const int 
   if (blockIdx.y == 0 && threadIdx.x == 0) a.lens[s] = 0;
 }
 
-// map[page]: the page's number after compaction.  src / dst: the moves, ascending; *moves their number.
-__global__ void __launch_bounds__(NP_T) pages_compact_plan_kernel(PagesArgs a, const int *ref_in, int *map, int *src, int *dst, int *moves) {
-  __shared__ int sh[32];
+// src / dst: the moves, ascending; *moves their number; *front how many pages are in use; map[page] the new number of a
+// page that is not in front.  The launch that renames writes the counts of the pages that stay, this one the others.
+__global__ void __launch_bounds__(NP_T) pages_compact_plan_kernel(PagesArgs a, const int *ref_in, int *map, int *src, int *dst, int *moves,
+                                                                  int *front) {
+  __shared__ unsigned long long sh[32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
-  int live = 0;
-  for (int base = 0; base < a.NP; base += 4 * NP_T) {
-    int r[4];
-    load_refs(ref_in, a.NP, base, r);
+  int live = 0, r[4 * SUB], n[SUB], rank[SUB];
+  for (int base = 0; base < a.NP; base += STEP) {
+    load_refs(ref_in, a.NP, base, 0, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) live += base + 4 * tid + e < a.NP && r[e] > 0;
+    for (int k = 0; k < SUB; ++k) {
+      n[k] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) n[k] += r[4 * k + e] > 0;
+    }
+    live += scan_rounds(n, rank, sh);
   }
-  scan_1024(live, sh);
-  live = sh[31];
-  __syncthreads();
   int holes = 0, highs = 0;
-  for (int base = 0; base < a.NP; base += 4 * NP_T) {
-    int r[4];
-    load_refs(ref_in, a.NP, base, r);
-    int nh = 0, ng = 0;
+  for (int base = 0; base < a.NP; base += STEP) {
+    if (a.NP > STEP) load_refs(ref_in, a.NP, base, 0, r);  // one step: they are still here
+    // free pages of the front, then pages to move
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = base + 4 * tid + e;
-      nh += i < live && r[e] <= 0;
-      ng += i < a.NP && i >= live && r[e] > 0;
-    }
-    const int ih = scan_1024(nh, sh);
-    const int ah = sh[31];
-    __syncthreads();
-    const int ig = scan_1024(ng, sh);
-    const int ag = sh[31];
-    __syncthreads();
-    int kh = holes + ih - nh, kg = highs + ig - ng;
+    for (int w = 0; w < 2; ++w) {
+      auto mine = [&](int k, int e) {
+        const int i = base + 4 * (NP_T * k + tid) + e;
+        return w == 0 ? i < live && r[4 * k + e] <= 0 : i >= live && r[4 * k + e] > 0;
+      };
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = base + 4 * tid + e;
-      if (i >= a.NP) continue;
-      if (i < live && r[e] <= 0) dst[kh++] = i;
-      else if (i >= live && r[e] > 0) src[kg++] = i;
-      map[i] = i;
-      a.ref[i] = r[e];
+      for (int k = 0; k < SUB; ++k) {
+        n[k] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) n[k] += mine(k, e);
+      }
+      const int all = scan_rounds(n, rank, sh);
+      int *to = w ? src + highs : dst + holes;
+#pragma unroll
+      for (int k = 0; k < SUB; ++k) {
+        int x = rank[k];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (mine(k, e)) to[x++] = base + 4 * (NP_T * k + tid) + e;
+      }
+      if (w) {
+#pragma unroll
+        for (int k = 0; k < SUB; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = base + 4 * (NP_T * k + tid) + e;
+            if (i >= live && i < a.NP && r[4 * k + e] <= 0) {
+              map[i] = i;
+              a.ref[i] = 0;
+            }
+          }
+      }
+      if (w) highs += all;
+      else holes += all;
     }
-    holes += ah;
-    highs += ag;
   }
   __syncthreads();
-  for (int k = tid; k < highs; k += NP_T) {  // as many holes below `live` as pages in use above
+  for (int k = tid; k < highs; k += NP_T) {  // as many holes in front as pages in use behind
     const int s = src[k], d = dst[k];
     map[s] = d;
-    a.ref[d] = a.ref[s];
+    a.ref[d] = ref_in[s];
     a.ref[s] = 0;
   }
-  if (tid == 0) *moves = highs;
-}
-
-__global__ void __launch_bounds__(256) pages_remap_kernel(PagesArgs a, const int *table_in, const int *map) {
-  pdl_trigger();
-  pdl_wait();
-  const long long n = (long long)a.S * a.W;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += 256ll * gridDim.x) {
-    const long long at = (i / a.W) * a.ts + i % a.W;
-    const int pg = table_in[at];
-    a.table[at] = (unsigned)pg < (unsigned)a.NP ? map[pg] : pg;
+  if (tid == 0) {
+    *moves = highs;
+    *front = live;
   }
 }
 
-__global__ void __launch_bounds__(COPY_T) slots_copy_kernel(const __grid_constant__ PoolList pl, const int *src, const int *dst,
-                                                           int count, const int *count_dev) {
+__global__ void __launch_bounds__(COPY_T) slots_copy_kernel(const __grid_constant__ PoolList pl, const PairList l0, const PairList l1,
+                                                           int count, const int *count_dev, const __grid_constant__ TableJob job) {
   pdl_trigger();
   pdl_wait();
+  const PagesArgs &a = job.a;
+  if (job.kind == TableJob::FORK) {
+    // the children's table rows, and a reference more for every page that they share
+    for (int i = blockIdx.x; i < job.m; i += gridDim.x) {
+      const int p = job.psrc[i], c = job.pdst[i];
+      if (p < 0) continue;
+      const int len = a.lens[p], full = len / a.P;
+      for (int j = threadIdx.x; j < a.W; j += COPY_T) {
+        int pg = -1;
+        if (j < full) {
+          pg = a.table[p * a.ts + j];
+          if ((unsigned)pg < (unsigned)a.NP) atomicAdd(a.ref + pg, 1);
+        } else if (j == full && len % a.P != 0) {
+          pg = job.new_page[i];
+        }
+        a.table[c * a.ts + j] = pg;
+      }
+    }
+  } else if (job.kind == TableJob::REMAP) {
+    const long long n = (long long)a.S * a.W, t0 = blockIdx.x * (long long)COPY_T + threadIdx.x, step = (long long)COPY_T * gridDim.x;
+    const int front = *job.front;
+    for (long long i = t0; i < n; i += step) {
+      const long long at = (i / a.W) * a.ts + i % a.W;
+      const int pg = job.table_in[at];
+      a.table[at] = pg >= front && pg < a.NP ? job.map[pg] : pg;
+    }
+    // the counts of pages that stay; the others are there already
+    for (long long i = t0; i < front; i += step) {
+      const int x = job.ref_in[i];
+      if (x > 0) a.ref[i] = x;
+    }
+  }
   if (count_dev) count = min(count, *count_dev);
   const long long per = pl.chunk0[pl.n], total = per * count;  // chunks of a pair in all pools
   for (long long x = blockIdx.x; x < total; x += gridDim.x) {
@@ -327,7 +394,8 @@ __global__ void __launch_bounds__(COPY_T) slots_copy_kernel(const __grid_constan
     int p = 0;
     while (in >= pl.chunk0[p + 1]) ++p;
     const gdn_slot_pool &g = pl.p[p];
-    const int s = src[i], d = dst[i];
+    const PairList &l = pl.list[p] ? l1 : l0;
+    const int s = l.src[i], d = l.dst[i];
     if (s < 0 || d < 0 || s >= g.slots || d >= g.slots) continue;
     const long long b0 = (in - pl.chunk0[p]) * CHUNK;
     const int n16 = (int)(min((long long)CHUNK, g.bytes - b0) >> 4);
@@ -343,14 +411,21 @@ __global__ void __launch_bounds__(COPY_T) slots_copy_kernel(const __grid_constan
   }
 }
 
-cudaError_t launch_slots_copy(const PoolList &pl, const int *src, const int *dst, int count, const int *count_dev, cudaStream_t st) {
+cudaError_t launch_slots_copy(const PoolList &pl, const PairList (&pairs)[2], int count, const int *count_dev, const TableJob &job,
+                              cudaStream_t st) {
   PoolList l = pl;
   l.chunk0[0] = 0;
   for (int i = 0; i < l.n; ++i) l.chunk0[i + 1] = l.chunk0[i] + (l.p[i].bytes + CHUNK - 1) / CHUNK;
-  const long long total = l.chunk0[l.n] * count;
-  if (total <= 0) return cudaSuccess;
+  long long want = l.chunk0[l.n] * count;
+  if (job.kind == TableJob::FORK) want = want > job.m ? want : job.m;
+  if (job.kind == TableJob::REMAP) {
+    const long long n = ((long long)job.a.S * job.a.W + COPY_T - 1) / COPY_T;
+    want = want > n ? want : n;
+  }
+  if (want <= 0) return cudaSuccess;
   const long long cap = 152 * 8;  // eight CTAs of 256 threads fill an SM
-  return launch_pdl(slots_copy_kernel, dim3((unsigned)(total < cap ? total : cap)), dim3(COPY_T), 0, st, l, src, dst, count, count_dev);
+  return launch_pdl(slots_copy_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(COPY_T), 0, st, l, pairs[0], pairs[1], count,
+                    count_dev, job);
 }
 
 namespace {
@@ -364,18 +439,11 @@ cudaError_t launch_pages_fork_plan(const PagesArgs &a, const int *parents, const
                                    int *psrc, int *pdst, cudaStream_t st) {
   return launch_pdl(pages_fork_plan_kernel, dim3(1), dim3(NP_T), 0, st, a, parents, children, m, new_page, src, psrc, pdst);
 }
-cudaError_t launch_pages_fork_rows(const PagesArgs &a, const int *psrc, const int *pdst, const int *new_page, int m, cudaStream_t st) {
-  return launch_pdl(pages_fork_rows_kernel, rows_grid(m, a.W), dim3(256), 0, st, a, psrc, pdst, new_page);
-}
 cudaError_t launch_pages_free(const PagesArgs &a, const int *seqs, int m, cudaStream_t st) {
   return launch_pdl(pages_free_kernel, rows_grid(m, a.W), dim3(256), 0, st, a, seqs);
 }
-cudaError_t launch_pages_compact_plan(const PagesArgs &a, const int *ref_in, int *map, int *src, int *dst, int *moves, cudaStream_t st) {
-  return launch_pdl(pages_compact_plan_kernel, dim3(1), dim3(NP_T), 0, st, a, ref_in, map, src, dst, moves);
+cudaError_t launch_pages_compact_plan(const PagesArgs &a, const int *ref_in, int *map, int *src, int *dst, int *moves, int *front,
+                                      cudaStream_t st) {
+  return launch_pdl(pages_compact_plan_kernel, dim3(1), dim3(NP_T), 0, st, a, ref_in, map, src, dst, moves, front);
 }
-cudaError_t launch_pages_remap(const PagesArgs &a, const int *table_in, const int *map, cudaStream_t st) {
-  const long long n = ((long long)a.S * a.W + 255) / 256;
-  return launch_pdl(pages_remap_kernel, dim3((unsigned)(n < 152 * 8 ? n : 152 * 8)), dim3(256), 0, st, a, table_in, map);
-}
-
 }  // namespace gdn

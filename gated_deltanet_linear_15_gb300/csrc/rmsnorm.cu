@@ -6,12 +6,15 @@
 // describes, background paragraph.)
 //
 // Bound by bytes: a row is read once into registers (16-byte pieces, neighbours in neighbouring threads), reduced, and
-// written once; the fp8 scales come from the same registers.  TPR threads hold a row: 32 (no barrier at all) for short
-// rows, 128 for rows up to a few thousand features, 512 for longer ones or when there are fewer rows than SMs and
-// latency counts.  CTAs stay and walk over rows, with the weight in registers.  The backward keeps its share of dw in
-// registers too; each CTA leaves one partial row, and a second kernel adds these in order.  Sums are fp32; rows of
-// which dim, stride or alignment does not allow 16-byte pieces go one feature at a time.
+// written once; the fp8 scales come from the same registers.  TPR threads hold a row, two pieces each where that works
+// out, so that a CTA of 256 threads works on several short rows at once; rows of at most 32 pieces need no barrier at all.
+// CTAs stay and walk over rows, with the weight in registers, and ask for the next row before they reduce the one they
+// have.  The backward keeps its share of dw in registers too; each CTA leaves one partial row, and a second kernel adds
+// these in order.  Sums are fp32; rows of which dim, stride or alignment does not allow 16-byte pieces go one feature at a
+// time.
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "block.h"
 #include "common.cuh"
@@ -59,7 +62,7 @@ __device__ __forceinline__ uint8_t fp8x1(float a) { return __nv_cvt_float_to_fp8
 // one barrier per reduction is enough.  Every thread of the CTA takes part.
 template <int TPR, bool MAX> __device__ __forceinline__ float row_reduce(float x, float *sh, int &turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
     const float y = __shfl_xor_sync(0xffffffffu, x, o);
     x = MAX ? fmaxf(x, y) : x + y;
   }
@@ -81,7 +84,8 @@ template <int TPR, bool MAX> __device__ __forceinline__ float row_reduce(float x
 template <typename I, int NTH, int TPR, int NV>
 __global__ void __launch_bounds__(NTH) norm_fwd_kernel(NormArgs a) {
   constexpr int V = Vec<I>::N, RPC = NTH / TPR;
-  __shared__ float sh[RPC][2 * (TPR / 32)];
+  constexpr bool AHEAD = NV <= 2;  // registers for the next row
+  __shared__ float sh[RPC][TPR > 32 ? 2 * (TPR / 32) : 1];
   pdl_trigger();
   pdl_wait();
   const int tr = threadIdx.x % TPR, grp = threadIdx.x / TPR, pieces = a.D / V;
@@ -100,24 +104,28 @@ __global__ void __launch_bounds__(NTH) norm_fwd_kernel(NormArgs a) {
     }
   }
   const float invD = 1.f / a.D;
-  for (long long r0 = (long long)blockIdx.x * RPC; r0 < a.T; r0 += (long long)gridDim.x * RPC) {
-    const long long r = r0 + grp;
-    const bool live = r < a.T;
-    float h[NV][V];
-    float ss = 0.f;
-    uint4 xr[NV], rr[NV];
+  const long long step = (long long)gridDim.x * RPC;
+  uint4 xr[NV], rr[NV];  // the row that comes next
+  auto load = [&](long long r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = tr + k * TPR;
       xr[k] = rr[k] = make_uint4(0, 0, 0, 0);
-      if (live && c < pieces) {
+      if (r < a.T && c < pieces) {
         xr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.x) + r * a.x_row + c * V);
         if (a.res) rr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.res) + r * a.r_row + c * V);
       }
     }
+  };
+  long long r = (long long)blockIdx.x * RPC + grp;
+  if (AHEAD) load(r);
+  for (long long r0 = (long long)blockIdx.x * RPC; r0 < a.T; r0 += step, r += step) {
+    const bool live = r < a.T;
+    if (!AHEAD) load(r);
+    float h[NV][V];
+    float ss = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = tr + k * TPR;
       float t[V];
       widen<I>(xr[k], h[k]);
       widen<I>(rr[k], t);
@@ -126,8 +134,14 @@ __global__ void __launch_bounds__(NTH) norm_fwd_kernel(NormArgs a) {
         if (a.res) h[k][i] += t[i];
         ss += h[k][i] * h[k][i];
       }
-      if (a.h_out && live && c < pieces)
-        *reinterpret_cast<uint4 *>(static_cast<I *>(a.h_out) + r * a.h_row + c * V) = narrow<I>(h[k]);
+    }
+    if (AHEAD) load(r + step);
+    if (a.h_out) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int c = tr + k * TPR;
+        if (live && c < pieces) *reinterpret_cast<uint4 *>(static_cast<I *>(a.h_out) + r * a.h_row + c * V) = narrow<I>(h[k]);
+      }
     }
     const float rstd = rsqrtf(row_reduce<TPR, false>(ss, sh[grp], turn) * invD + a.eps);
     if (a.rstd && live && tr == 0) a.rstd[r] = rstd;
@@ -221,7 +235,8 @@ template <typename I> __global__ void __launch_bounds__(256) norm_fwd_any_kernel
 template <typename I, int NTH, int TPR, int NV>
 __global__ void __launch_bounds__(NTH) norm_bwd_kernel(NormArgs a) {
   constexpr int V = Vec<I>::N, RPC = NTH / TPR;
-  __shared__ float sh[RPC][2 * (TPR / 32)];
+  constexpr bool AHEAD = TPR <= 256;  // registers for the next row; with 512 threads a row two CTAs per SM do better without
+  __shared__ float sh[RPC][TPR > 32 ? 2 * (TPR / 32) : 1];
   extern __shared__ float dsh[];  // [D], when several row groups share a CTA
   pdl_trigger();
   pdl_wait();
@@ -238,21 +253,36 @@ __global__ void __launch_bounds__(NTH) norm_bwd_kernel(NormArgs a) {
     }
   }
   const float invD = 1.f / a.D;
-  for (long long r0 = (long long)blockIdx.x * RPC; r0 < a.T; r0 += (long long)gridDim.x * RPC) {
-    const long long r = r0 + grp;
-    const bool live = r < a.T;
-    uint4 hr[NV], gr[NV], er[NV];
+  const long long step = (long long)gridDim.x * RPC;
+  uint4 hn[NV], gn[NV], en[NV];  // the row that comes next
+  float rn = 0.f;
+  auto load = [&](long long r) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = tr + k * TPR;
-      hr[k] = gr[k] = er[k] = make_uint4(0, 0, 0, 0);
-      if (live && c < pieces) {
-        hr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.h) + r * a.x_row + c * V);
-        gr[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.x) + r * a.y_row + c * V);
-        if (a.res) er[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.res) + r * a.r_row + c * V);
+      hn[k] = gn[k] = en[k] = make_uint4(0, 0, 0, 0);
+      if (r < a.T && c < pieces) {
+        hn[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.h) + r * a.x_row + c * V);
+        gn[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.x) + r * a.y_row + c * V);
+        if (a.res) en[k] = *reinterpret_cast<const uint4 *>(static_cast<const I *>(a.res) + r * a.r_row + c * V);
       }
     }
-    const float rstd = live ? a.rstd_in[r] : 0.f;
+    rn = r < a.T ? a.rstd_in[r] : 0.f;
+  };
+  long long r = (long long)blockIdx.x * RPC + grp;
+  if (AHEAD) load(r);
+  for (long long r0 = (long long)blockIdx.x * RPC; r0 < a.T; r0 += step, r += step) {
+    const bool live = r < a.T;
+    if (!AHEAD) load(r);
+    uint4 hr[NV], gr[NV], er[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      hr[k] = hn[k];
+      gr[k] = gn[k];
+      er[k] = en[k];
+    }
+    const float rstd = rn;
+    if (AHEAD) load(r + step);
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -337,24 +367,23 @@ template <typename I> __global__ void __launch_bounds__(256) norm_bwd_any_kernel
   }
 }
 
-// dw = the partial rows, added in order: eight threads per column take every eighth row, then join
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float *part, int rows, int D, float *dw) {
-  __shared__ float sh[8][33];
+// dw = the partial rows, added in order: 32 warps take every 32nd row of 32 columns, then join
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float *part, int rows, int D, float *dw) {
+  __shared__ float sh[32][33];
   pdl_trigger();
   pdl_wait();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < D) {
-#pragma unroll 8
-    for (int r = y; r < rows; r += 8) s += part[(long long)r * D + c];
+#pragma unroll 10
+    for (int r = y; r < rows; r += 32) s += part[(long long)r * D + c];
   }
-  sh[y][threadIdx.x & 31] = s;
+  sh[y][lane] = s;
   __syncthreads();
-  if (y == 0 && c < D) {
+  s = sh[lane][y];  // column y of the 32, its 32 partial sums over the lanes
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
-    dw[c] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + y < D) dw[blockIdx.x * 32 + y] = s;
 }
 
 namespace {
@@ -367,57 +396,65 @@ template <typename I, int NTH, int TPR, int NV> cudaError_t fwd(const NormArgs &
   const long long want = (a.T + NTH / TPR - 1) / (NTH / TPR), cap = (long long)sms * per_sm;
   return launch_pdl(norm_fwd_kernel<I, NTH, TPR, NV>, dim3((unsigned)(want < cap ? want : cap)), dim3(NTH), 0, st, a);
 }
-// how many threads hold a row, and how many pieces each: the first shape that holds it (0: none)
-int row_shape(const NormArgs &a, int V, int sms) {
-  const int pieces = a.D / V;
-  if (pieces <= 32 * 4) return a.T < sms && pieces > 32 ? (pieces <= 128 ? 2 : 3) : (pieces <= 32 ? 0 : 1);
-  if (pieces <= 128 * 4) return a.T < sms && pieces > 128 ? 4 : 3;
-  return pieces <= 512 ? 4 : (pieces <= 512 * 4 ? 5 : -1);
+// Threads of a row and pieces of each: two pieces, up to 512 threads, then four; one piece each where a row needs no
+// second, or where there are fewer rows than SMs and a call is as long as its slowest row.
+struct RowShape {
+  int tpr, nv;  // tpr 0: the row does not fit
+};
+RowShape row_shape(const NormArgs &a, int V, int sms) {
+  const int p = a.D / V;
+  if (p <= 16) return {16, 1};
+  if (p <= 32) return {32, 1};
+  if (a.T < sms && p > 128 && p <= 512) return {512, 1};
+  for (int t = 32; t <= 512; t *= 2)
+    if (p <= 2 * t) return {t, 2};
+  return p <= 512 * 4 ? RowShape{512, 4} : RowShape{0, 0};
 }
 template <typename I> cudaError_t fwd_shape(const NormArgs &a, int sms, cudaStream_t st) {
-  switch (row_shape(a, Vec<I>::N, sms)) {
-    case 0: return fwd<I, 128, 32, 1>(a, sms, st);
-    case 1: return fwd<I, 128, 32, 4>(a, sms, st);
-    case 2: return fwd<I, 128, 128, 1>(a, sms, st);
-    case 3: return fwd<I, 128, 128, 4>(a, sms, st);
-    case 4: return fwd<I, 512, 512, 1>(a, sms, st);
-    case 5: return fwd<I, 512, 512, 4>(a, sms, st);
+  const RowShape s = row_shape(a, Vec<I>::N, sms);
+  switch (s.tpr * 8 + s.nv) {
+    case 16 * 8 + 1: return fwd<I, 256, 16, 1>(a, sms, st);
+    case 32 * 8 + 1: return fwd<I, 256, 32, 1>(a, sms, st);
+    case 32 * 8 + 2: return fwd<I, 256, 32, 2>(a, sms, st);
+    case 64 * 8 + 2: return fwd<I, 256, 64, 2>(a, sms, st);
+    case 128 * 8 + 2: return fwd<I, 256, 128, 2>(a, sms, st);
+    case 256 * 8 + 2: return fwd<I, 256, 256, 2>(a, sms, st);
+    case 512 * 8 + 1: return fwd<I, 512, 512, 1>(a, sms, st);
+    case 512 * 8 + 2: return fwd<I, 512, 512, 2>(a, sms, st);
+    case 512 * 8 + 4: return fwd<I, 512, 512, 4>(a, sms, st);
   }
   return cudaErrorInvalidValue;
 }
 
-constexpr int BWD_PER_SM = 2;
 template <typename I, int NTH, int TPR, int NV> cudaError_t bwd(const NormArgs &a, int ctas, cudaStream_t st) {
   const size_t smem = NTH > TPR ? (size_t)a.D * 4 : 0;
   return launch_pdl(norm_bwd_kernel<I, NTH, TPR, NV>, dim3(ctas), dim3(NTH), smem, st, a);
 }
-template <typename I> int bwd_rows_per_cta(const NormArgs &a, int sms) {
-  switch (row_shape(a, Vec<I>::N, sms)) {
-    case 0: case 1: return 8;
-    case 2: case 3: return 2;
-  }
-  return 1;
-}
 template <typename I> cudaError_t bwd_shape(const NormArgs &a, int sms, int ctas, cudaStream_t st) {
-  switch (row_shape(a, Vec<I>::N, sms)) {
-    case 0: return bwd<I, 256, 32, 1>(a, ctas, st);
-    case 1: return bwd<I, 256, 32, 4>(a, ctas, st);
-    case 2: return bwd<I, 256, 128, 1>(a, ctas, st);
-    case 3: return bwd<I, 256, 128, 4>(a, ctas, st);
-    case 4: return bwd<I, 512, 512, 1>(a, ctas, st);
-    case 5: return bwd<I, 512, 512, 4>(a, ctas, st);
+  const RowShape s = row_shape(a, Vec<I>::N, sms);
+  switch (s.tpr * 8 + s.nv) {
+    case 16 * 8 + 1: return bwd<I, 256, 16, 1>(a, ctas, st);
+    case 32 * 8 + 1: return bwd<I, 256, 32, 1>(a, ctas, st);
+    case 32 * 8 + 2: return bwd<I, 256, 32, 2>(a, ctas, st);
+    case 64 * 8 + 2: return bwd<I, 256, 64, 2>(a, ctas, st);
+    case 128 * 8 + 2: return bwd<I, 256, 128, 2>(a, ctas, st);
+    case 256 * 8 + 2: return bwd<I, 256, 256, 2>(a, ctas, st);
+    case 512 * 8 + 1: return bwd<I, 512, 512, 1>(a, ctas, st);
+    case 512 * 8 + 2: return bwd<I, 512, 512, 2>(a, ctas, st);
+    case 512 * 8 + 4: return bwd<I, 512, 512, 4>(a, ctas, st);
   }
   return cudaErrorInvalidValue;
 }
 
-bool in_registers(const NormArgs &a, bool bf, bool vec, int sms) { return vec && row_shape(a, bf ? 8 : 4, sms) >= 0; }
+bool in_registers(const NormArgs &a, bool bf, bool vec, int sms) { return vec && row_shape(a, bf ? 8 : 4, sms).tpr > 0; }
 
 }  // namespace
 
+// CTAs of the backward: what the registers of a thread let an SM hold, three with one piece per thread, two otherwise
 int norm_bwd_ctas(const NormArgs &a, bool bf, bool vec, int sms) {
-  const long long cap = (long long)sms * BWD_PER_SM;
+  const long long cap = (long long)sms * (row_shape(a, bf ? 8 : 4, sms).nv == 1 ? 3 : 2);
   long long rows = 1;
-  if (in_registers(a, bf, vec, sms)) rows = bf ? bwd_rows_per_cta<bf16>(a, sms) : bwd_rows_per_cta<float>(a, sms);
+  if (in_registers(a, bf, vec, sms)) rows = std::max(1, 256 / row_shape(a, bf ? 8 : 4, sms).tpr);
   const long long want = (a.T + rows - 1) / rows;
   return (int)(want < cap ? (want > 0 ? want : 1) : cap);
 }
@@ -439,7 +476,7 @@ cudaError_t launch_norm_bwd(const NormArgs &a, bool bf, bool vec, int sms, cudaS
            : launch_pdl(norm_bwd_any_kernel<float>, dim3(ctas), dim3(256), 0, st, a);
   }
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_dw_kernel, dim3((a.D + 31) / 32), dim3(256), 0, st, (const float *)a.part, ctas, a.D, a.dw);
+  return launch_pdl(norm_dw_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, st, (const float *)a.part, ctas, a.D, a.dw);
 }
 
 }  // namespace gdn
