@@ -155,5 +155,34 @@ def load():
         return lib
 
 
+# the C entry points that csrc/block_py.cpp calls, in the order of its table
+_PY_CALLS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_paged_attn_status", "gdn_rotary", "gdn_rotary_append",
+             "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork", "gdn_pages_free",
+             "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd", "gdn_status_string",
+             "gdn_last_error_string")
+_py = None
+
+
+def load_py():
+    """Load the Python extension of the operators in block.py and connect it to libgdn.so.  Raises if either is missing."""
+    global _py
+    if _py is not None:
+        return _py
+    lib = load()
+    with _lock:
+        if _py is None:
+            import importlib.machinery
+            import importlib.util
+            if not os.path.exists(_build.PY_LIB):
+                raise ImportError(f"{_build.PY_LIB} is missing: build the library first "
+                                  "(gated_deltanet_linear_15_gb300.build.build() or __graft_entry__.build())")
+            loader = importlib.machinery.ExtensionFileLoader("gdn_block_py", _build.PY_LIB)
+            mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_block_py", _build.PY_LIB, loader=loader))
+            loader.exec_module(mod)
+            mod.connect(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _PY_CALLS))
+            _py = mod
+    return _py
+
+
 def last_error() -> str:
     return load().gdn_last_error_string().decode()

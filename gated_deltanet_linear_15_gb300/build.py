@@ -1,7 +1,9 @@
 """Build step of the CUDA library: nvcc for sm_103a, in-tree (``_build/libgdn.so``).
 
 Each translation unit is compiled in parallel, then linked into one shared
-library with the C ABI of ``include/gdn.h`` and ``include/gdn_block.h``.
+library with the C ABI of ``include/gdn.h`` and ``include/gdn_block.h``.  Beside
+them g++ compiles ``csrc/block_py.cpp``, the Python extension that checks and
+allocates for the operators of ``include/gdn_block.h`` (``_build/gdn_block_py.so``).
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ LIB = os.path.join(BUILD, "libgdn.so")
 SOURCES = ["api.cu", "plan.cu", "fwd.cu", "fwd_prep_tc.cu", "fwd_tc.cu", "bwd.cu", "bwd_chain_tc.cu", "bwd_local_tc.cu",
            "recurrent.cu", "block_api.cu", "attn_rows.cu", "attn_chunk_tc.cu",
            "rope.cu", "pages.cu", "rmsnorm.cu"]
+PY_SOURCE = os.path.join(CSRC, "block_py.cpp")
+PY_LIB = os.path.join(BUILD, "gdn_block_py.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -38,7 +42,7 @@ def _deps_mtime() -> float:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every kernel for sm_103a and link ``libgdn.so``; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, PY_LIB)):
         return LIB
     nvcc = _nvcc()
 
@@ -52,13 +56,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(len(SOURCES)) as ex:
+    def compile_py():
+        import sysconfig
+
+        import torch
+        root = os.path.join(os.path.dirname(torch.__file__))
+        inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include"), os.path.join(ROOT, "include")]
+        tmp = PY_LIB + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *(f"-I{i}" for i in inc), PY_SOURCE, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch",
+               "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for block_py.cpp:\n{r.stderr}")
+        return tmp
+
+    with cf.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        py = ex.submit(compile_py)
         objs = list(ex.map(compile_one, SOURCES))
+        py_tmp = py.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(py_tmp, PY_LIB)
     return LIB
 
 
