@@ -23,6 +23,8 @@
 //
 // fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the exact rest):
 // hi hi + hi lo + lo hi leaves about 2^-21 of a product.
+#include <type_traits>
+
 #include "paged.cuh"
 #include "umma.cuh"
 
@@ -252,6 +254,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         pos[i][e] = cur.s.kv - cur.s.qlen + (int)(r / (unsigned)a.G);
       }
     }
+    const int active = max(0, min(MI, (rows - 16 * MI * rg + 15) / 16));  // of this warp's 16-row tiles
     const int pos_last = cur.s.kv - cur.s.qlen + (int)(((unsigned)cur.t * MT + rows - 1) / (unsigned)a.G);
 
     float acc[MI][D / 8][4], m[MI][2], l[MI][2];
@@ -287,144 +290,150 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         fence_async_smem();  // the stage is loaded again later
         __syncwarp();
       }
-      // ---- scores of 16 tokens: tiles 0 (tokens 0-7) and 1 (8-15)
-      float s[MI][2][4];
+      // the 16-row tiles that hold rows
+      auto multiply = [&](auto tiles) {
+        constexpr int NI = decltype(tiles)::value;
+        // ---- scores of 16 tokens: tiles 0 (tokens 0-7) and 1 (8-15)
+        float s[NI][2][4];
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
-      if constexpr (!F32) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t bk[4];
-          const uint32_t ad = ks + tile_off<SL>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                       : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
-#pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            mma_bf16(s[i][0], qf[i][k], bk[0], bk[1]);
-            mma_bf16(s[i][1], qf[i][k], bk[2], bk[3]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          float bk[2][2];
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
+            for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+        if constexpr (!F32) {
 #pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            uint32_t ah[4], al[4];
+          for (int k = 0; k < KS; ++k) {
+            uint32_t bk[4];
+            const uint32_t ad = ks + tile_off<SL>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[i][k][e]), ah[e], al[e]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma_3tf32(s[i][j], ah, al, bk[j][0], bk[j][1]);
-          }
-        }
-      }
-      // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
-      const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
-      float mx[MI][2];
-      bool raise = false;
-#pragma unroll
-      for (int i = 0; i < MI; ++i) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float z = s[i][j][e] * a.scale_log2;
-            if (mask) {
-              const int key = t0 + 8 * j + 2 * qd + (e & 1), p = pos[i][e >> 1];
-              if (key > p || (a.window && key <= p - a.window)) z = -INFINITY;
+            for (int i = 0; i < NI; ++i) {
+              mma_bf16(s[i][0], qf[i][k], bk[0], bk[1]);
+              mma_bf16(s[i][1], qf[i][k], bk[2], bk[3]);
             }
-            s[i][j][e] = z;
           }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[i][e] = quad_max(fmaxf(fmaxf(s[i][0][2 * e], s[i][0][2 * e + 1]), fmaxf(s[i][1][2 * e], s[i][1][2 * e + 1])));
-          raise |= mx[i][e] > m[i][e] + RAISE;
+          for (int k = 0; k < KS; ++k) {
+            float bk[2][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              uint32_t ah[4], al[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[i][k][e]), ah[e], al[e]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) mma_3tf32(s[i][j], ah, al, bk[j][0], bk[j][1]);
+            }
+          }
         }
-      }
-      if (__any_sync(0xffffffffu, raise)) {
+        // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
+        const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
+        float mx[NI][2];
+        bool raise = false;
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float z = s[i][j][e] * a.scale_log2;
+              if (mask) {
+                const int key = t0 + 8 * j + 2 * qd + (e & 1), p = pos[i][e >> 1];
+                if (key > p || (a.window && key <= p - a.window)) z = -INFINITY;
+              }
+              s[i][j][e] = z;
+            }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m[i][e], mx[i][e]);
-            const float f = mn == -INFINITY ? 1.f : ex2(m[i][e] - mn);
-            m[i][e] = mn;
-            l[i][e] *= f;
+            mx[i][e] = quad_max(fmaxf(fmaxf(s[i][0][2 * e], s[i][0][2 * e + 1]), fmaxf(s[i][1][2 * e], s[i][1][2 * e + 1])));
+            raise |= mx[i][e] > m[i][e] + RAISE;
+          }
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mn = fmaxf(m[i][e], mx[i][e]);
+              const float f = mn == -INFINITY ? 1.f : ex2(m[i][e] - mn);
+              m[i][e] = mn;
+              l[i][e] *= f;
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j) {
+                acc[i][j][2 * e] *= f;
+                acc[i][j][2 * e + 1] *= f;
+              }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mm = m[i][e] == -INFINITY ? 0.f : m[i][e];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const float p = ex2(s[i][j][2 * e + x] - mm);
+                l[i][e] += p;
+                s[i][j][2 * e + x] = p;
+              }
+          }
+        // ---- sums += weights x values
+        if constexpr (!F32) {
+          uint32_t pa[NI][4];
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            pa[i][0] = pack2(s[i][0][0], s[i][0][1]);
+            pa[i][1] = pack2(s[i][0][2], s[i][0][3]);
+            pa[i][2] = pack2(s[i][1][0], s[i][1][1]);
+            pa[i][3] = pack2(s[i][1][2], s[i][1][3]);
+          }
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t bv[4];
+            const uint32_t ad = vs + tile_off<SL>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              mma_bf16(acc[i][2 * j], pa[i], bv[0], bv[1]);
+              mma_bf16(acc[i][2 * j + 1], pa[i], bv[2], bv[3]);
+            }
+          }
+        } else {
+          // the 8 tokens of score tile jt are the k of one step: index qd is token 2 qd and qd + 4 is token 2 qd + 1,
+          // in the weights (as the scores came out) and in the values alike
+#pragma unroll
+          for (int jt = 0; jt < 2; ++jt) {
+            uint32_t ph[NI][4], pl[NI][4];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              split_tf32(s[i][jt][0], ph[i][0], pl[i][0]);
+              split_tf32(s[i][jt][2], ph[i][1], pl[i][1]);
+              split_tf32(s[i][jt][1], ph[i][2], pl[i][2]);
+              split_tf32(s[i][jt][3], ph[i][3], pl[i][3]);
+            }
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) {
-              acc[i][j][2 * e] *= f;
-              acc[i][j][2 * e + 1] *= f;
+              const int r = 8 * jt + 2 * qd, c = 2 * j + (g >> 2);
+              const float v0 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r, c) + (g & 3) * 4);
+              const float v1 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r + 1, c) + (g & 3) * 4);
+#pragma unroll
+              for (int i = 0; i < NI; ++i) mma_3tf32(acc[i][j], ph[i], pl[i], v0, v1);
             }
           }
-      }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mm = m[i][e] == -INFINITY ? 0.f : m[i][e];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float p = ex2(s[i][j][2 * e + x] - mm);
-              l[i][e] += p;
-              s[i][j][2 * e + x] = p;
-            }
         }
-      // ---- sums += weights x values
-      if constexpr (!F32) {
-        uint32_t pa[MI][4];
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          pa[i][0] = pack2(s[i][0][0], s[i][0][1]);
-          pa[i][1] = pack2(s[i][0][2], s[i][0][3]);
-          pa[i][2] = pack2(s[i][1][0], s[i][1][1]);
-          pa[i][3] = pack2(s[i][1][2], s[i][1][3]);
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t bv[4];
-          const uint32_t ad = vs + tile_off<SL>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                       : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
-#pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            mma_bf16(acc[i][2 * j], pa[i], bv[0], bv[1]);
-            mma_bf16(acc[i][2 * j + 1], pa[i], bv[2], bv[3]);
-          }
-        }
-      } else {
-        // the 8 tokens of score tile jt are the k of one step: index qd is token 2 qd and qd + 4 is token 2 qd + 1,
-        // in the weights (as the scores came out) and in the values alike
-#pragma unroll
-        for (int jt = 0; jt < 2; ++jt) {
-          uint32_t ph[MI][4], pl[MI][4];
-#pragma unroll
-          for (int i = 0; i < MI; ++i) {
-            split_tf32(s[i][jt][0], ph[i][0], pl[i][0]);
-            split_tf32(s[i][jt][2], ph[i][1], pl[i][1]);
-            split_tf32(s[i][jt][1], ph[i][2], pl[i][2]);
-            split_tf32(s[i][jt][3], ph[i][3], pl[i][3]);
-          }
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            const int r = 8 * jt + 2 * qd, c = 2 * j + (g >> 2);
-            const float v0 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r, c) + (g & 3) * 4);
-            const float v1 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r + 1, c) + (g & 3) * 4);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) mma_3tf32(acc[i][j], ph[i], pl[i], v0, v1);
-          }
-        }
-      }
+      };
+      if (active == MI) multiply(std::integral_constant<int, MI>{});
+      else if (MI > 1 && active == 1) multiply(std::integral_constant<int, 1>{});
     }
     // ---- the slices' sums meet: each warp leaves its own in a stage it has read (16-byte chunks of a row change places
     // by the row's low bits, against bank conflicts)
