@@ -117,12 +117,13 @@ class RotaryFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dq, dk):
         table, positions = ctx.saved_tensors
-        dq, dk = rotary(dq.contiguous(), dk.contiguous(), table, positions, ctx.interleaved, inverse=True)
+        dk = None if dk is None else dk.contiguous()  # there is none without k
+        dq, dk = rotary(dq.contiguous(), dk, table, positions, ctx.interleaved, inverse=True)
         return dq, dk, None, None, None
 
 
 def rotary_embedding(q, k, table, positions, interleaved: bool = False):
-    """``rotary`` with gradients for q and k."""
+    """``rotary`` with gradients for q and k (or q alone, with k None)."""
     return RotaryFunction.apply(q, k, table, positions, interleaved)
 
 

@@ -6,7 +6,7 @@
 // Bound by the bytes of the cache: each key and value is used by a few rows only (16 flops per byte at four query heads
 // per key head), far below the tensor cores' ratio.  So the kernel is a stream: the units of the whole batch are split
 // evenly over the CTAs (paged.cuh), and a CTA's 64-token blocks are cut into four slices of 16 tokens.  A slice belongs
-// to RG warps, each with 16 MI of the tile's rows (MT = 16 MI RG), and has its own ring of TMA stages; every warp has its
+// to RG warps, each with 16 of the tile's rows (MT = 16 RG), and has its own ring of TMA stages; every warp has its
 // own running maximum, mass and sums, and meets the other slices only when the piece ends.  The query rows stay in
 // registers as mma.sync A fragments; scores come out in the layout that the second product takes as its A operand.
 // tcgen05 has no use here: its 128-row tile would be an eighth full, and the softmax would leave registers for TMEM and
@@ -23,8 +23,6 @@
 //
 // fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the exact rest):
 // hi hi + hi lo + lo hi leaves about 2^-21 of a product.
-#include <type_traits>
-
 #include "paged.cuh"
 #include "umma.cuh"
 
@@ -113,21 +111,21 @@ template <int RG> __device__ __forceinline__ void slice_sync(int slice) {
 
 }  // namespace
 
-template <typename I, int D, int MI, int RG, int STAGES>
+template <typename I, int D, int RG, int STAGES>
 __global__ void __launch_bounds__(128 * RG, RG == 1 && D * sizeof(I) <= 256 ? 2 : 1)
 attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-  constexpr int NT = 128 * RG, MT = 16 * MI * RG, RB = D * sizeof(I), CPR = RB / 16, SLB = SL * RB;
+  constexpr int NT = 128 * RG, MT = 16 * RG, RB = D * sizeof(I), CPR = RB / 16, SLB = SL * RB;
   constexpr int BOXES = RB / 128, BW = 128 / sizeof(I);  // boxes of a slice, features of a box
   constexpr int DIST = STAGES - RG;                      // slices on their way ahead of the one in use
   constexpr bool F32 = sizeof(I) == 4;
   constexpr int KS = F32 ? D / 8 : D / 16;  // k steps of q . k
-  static_assert(16 * MI * D * 4 <= 2 * SLB, "a warp's sums fit a stage");
+  static_assert(16 * D * 4 <= 2 * SLB, "a warp's sums fit a stage");
   extern __shared__ uint8_t raw[];
   __shared__ Cursor cur, nxt;  // one for the CTA, out of registers
   __shared__ int going;
   __shared__ uint64_t full[SLICES][STAGES];
-  __shared__ float mass[4 * RG][2][16 * MI];  // maxima and masses of the warps' rows
-  __shared__ uint32_t where[4 * RG];          // the stages that hold their sums
+  __shared__ float mass[4 * RG][2][16];  // maxima and masses of the warps' rows
+  __shared__ uint32_t where[4 * RG];     // the stages that hold their sums
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint8_t *qsm = smem + SLICES * STAGES * 2 * SLB;  // the query rows, [MT][D]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
@@ -232,41 +230,35 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     __syncthreads();
     more = going;
 
-    // ---- query fragments: rows g and g + 8 of each 16-row tile
-    uint32_t qf[MI][KS][4];
-    int pos[MI][2];
+    // ---- query fragments: rows g and g + 8 of the warp's 16
+    uint32_t qf[KS][4];
+    int pos[2];
+    const int r0 = 16 * rg;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int r0 = 16 * (MI * rg + i);
+    for (int k = 0; k < KS; ++k) {
+      if constexpr (F32) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        if constexpr (F32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            qf[i][k][e] = *reinterpret_cast<const uint32_t *>(qsm + tile_off<MT>(r0 + g + 8 * (e & 1), 2 * k + (e >> 1)) + 4 * qd);
-        } else {
-          ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(r0 + (lane & 15), 2 * k + (lane >> 4)), qf[i][k]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const unsigned r = (unsigned)cur.t * MT + min(r0 + g + 8 * e, rows - 1);
-        pos[i][e] = cur.s.kv - cur.s.qlen + (int)(r / (unsigned)a.G);
+        for (int e = 0; e < 4; ++e)
+          qf[k][e] = *reinterpret_cast<const uint32_t *>(qsm + tile_off<MT>(r0 + g + 8 * (e & 1), 2 * k + (e >> 1)) + 4 * qd);
+      } else {
+        ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(r0 + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
       }
     }
-    const int active = max(0, min(MI, (rows - 16 * MI * rg + 15) / 16));  // of this warp's 16-row tiles
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const unsigned r = (unsigned)cur.t * MT + min(r0 + g + 8 * e, rows - 1);
+      pos[e] = cur.s.kv - cur.s.qlen + (int)(r / (unsigned)a.G);
+    }
+    const bool active = rows > r0;  // the warp's 16 rows are not all past the tile's
     const int pos_last = cur.s.kv - cur.s.qlen + (int)(((unsigned)cur.t * MT + rows - 1) / (unsigned)a.G);
 
-    float acc[MI][D / 8][4], m[MI][2], l[MI][2];
+    float acc[D / 8][4], m[2], l[2];
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      m[i][0] = m[i][1] = -INFINITY;
-      l[i][0] = l[i][1] = 0.f;
+    for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
     for (int b = b0; b < b1; ++b) {
       if (!expired && !slice_wait(full_u + 8 * st, ph)) expired = 4;
@@ -290,150 +282,120 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         fence_async_smem();  // the stage is loaded again later
         __syncwarp();
       }
-      // the 16-row tiles that hold rows
-      auto multiply = [&](auto tiles) {
-        constexpr int NI = decltype(tiles)::value;
-        // ---- scores of 16 tokens: tiles 0 (tokens 0-7) and 1 (8-15)
-        float s[NI][2][4];
+      if (!active) continue;
+      // ---- scores of 16 tokens: tiles 0 (tokens 0-7) and 1 (8-15)
+      float s[2][4];
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+      if constexpr (!F32) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t bk[4];
+          const uint32_t ad = ks + tile_off<SL>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                       : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
+          mma_bf16(s[0], qf[k], bk[0], bk[1]);
+          mma_bf16(s[1], qf[k], bk[2], bk[3]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          float bk[2][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
-        if constexpr (!F32) {
+            for (int e = 0; e < 2; ++e)
+              bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
+          uint32_t ah[4], al[4];
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t bk[4];
-            const uint32_t ad = ks + tile_off<SL>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                         : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
+          for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[k][e]), ah[e], al[e]);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              mma_bf16(s[i][0], qf[i][k], bk[0], bk[1]);
-              mma_bf16(s[i][1], qf[i][k], bk[2], bk[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            float bk[2][2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              uint32_t ah[4], al[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[i][k][e]), ah[e], al[e]);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) mma_3tf32(s[i][j], ah, al, bk[j][0], bk[j][1]);
-            }
-          }
+          for (int j = 0; j < 2; ++j) mma_3tf32(s[j], ah, al, bk[j][0], bk[j][1]);
         }
-        // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
-        const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
-        float mx[NI][2];
-        bool raise = false;
+      }
+      // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
+      const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
+      float mx[2];
+      bool raise = false;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float z = s[i][j][e] * a.scale_log2;
-              if (mask) {
-                const int key = t0 + 8 * j + 2 * qd + (e & 1), p = pos[i][e >> 1];
-                if (key > p || (a.window && key <= p - a.window)) z = -INFINITY;
-              }
-              s[i][j][e] = z;
-            }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mx[i][e] = quad_max(fmaxf(fmaxf(s[i][0][2 * e], s[i][0][2 * e + 1]), fmaxf(s[i][1][2 * e], s[i][1][2 * e + 1])));
-            raise |= mx[i][e] > m[i][e] + RAISE;
+        for (int e = 0; e < 4; ++e) {
+          float z = s[j][e] * a.scale_log2;
+          if (mask) {
+            const int key = t0 + 8 * j + 2 * qd + (e & 1), p = pos[e >> 1];
+            if (key > p || (a.window && key <= p - a.window)) z = -INFINITY;
           }
-        }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float mn = fmaxf(m[i][e], mx[i][e]);
-              const float f = mn == -INFINITY ? 1.f : ex2(m[i][e] - mn);
-              m[i][e] = mn;
-              l[i][e] *= f;
-#pragma unroll
-              for (int j = 0; j < D / 8; ++j) {
-                acc[i][j][2 * e] *= f;
-                acc[i][j][2 * e + 1] *= f;
-              }
-            }
+          s[j][e] = z;
         }
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = quad_max(fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])));
+        raise |= mx[e] > m[e] + RAISE;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mm = m[i][e] == -INFINITY ? 0.f : m[i][e];
+        for (int e = 0; e < 2; ++e) {
+          const float mn = fmaxf(m[e], mx[e]);
+          const float f = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
+          m[e] = mn;
+          l[e] *= f;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float p = ex2(s[i][j][2 * e + x] - mm);
-                l[i][e] += p;
-                s[i][j][2 * e + x] = p;
-              }
-          }
-        // ---- sums += weights x values
-        if constexpr (!F32) {
-          uint32_t pa[NI][4];
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            pa[i][0] = pack2(s[i][0][0], s[i][0][1]);
-            pa[i][1] = pack2(s[i][0][2], s[i][0][3]);
-            pa[i][2] = pack2(s[i][1][0], s[i][1][1]);
-            pa[i][3] = pack2(s[i][1][2], s[i][1][3]);
-          }
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            uint32_t bv[4];
-            const uint32_t ad = vs + tile_off<SL>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                         : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              mma_bf16(acc[i][2 * j], pa[i], bv[0], bv[1]);
-              mma_bf16(acc[i][2 * j + 1], pa[i], bv[2], bv[3]);
-            }
-          }
-        } else {
-          // the 8 tokens of score tile jt are the k of one step: index qd is token 2 qd and qd + 4 is token 2 qd + 1,
-          // in the weights (as the scores came out) and in the values alike
-#pragma unroll
-          for (int jt = 0; jt < 2; ++jt) {
-            uint32_t ph[NI][4], pl[NI][4];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-              split_tf32(s[i][jt][0], ph[i][0], pl[i][0]);
-              split_tf32(s[i][jt][2], ph[i][1], pl[i][1]);
-              split_tf32(s[i][jt][1], ph[i][2], pl[i][2]);
-              split_tf32(s[i][jt][3], ph[i][3], pl[i][3]);
-            }
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-              const int r = 8 * jt + 2 * qd, c = 2 * j + (g >> 2);
-              const float v0 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r, c) + (g & 3) * 4);
-              const float v1 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r + 1, c) + (g & 3) * 4);
-#pragma unroll
-              for (int i = 0; i < NI; ++i) mma_3tf32(acc[i][j], ph[i], pl[i], v0, v1);
-            }
+          for (int j = 0; j < D / 8; ++j) {
+            acc[j][2 * e] *= f;
+            acc[j][2 * e + 1] *= f;
           }
         }
-      };
-      if (active == MI) multiply(std::integral_constant<int, MI>{});
-      else if (MI > 1 && active == 1) multiply(std::integral_constant<int, 1>{});
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mm = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p = ex2(s[j][2 * e + x] - mm);
+            l[e] += p;
+            s[j][2 * e + x] = p;
+          }
+      }
+      // ---- sums += weights x values
+      if constexpr (!F32) {
+        uint32_t pa[4];
+        pa[0] = pack2(s[0][0], s[0][1]);
+        pa[1] = pack2(s[0][2], s[0][3]);
+        pa[2] = pack2(s[1][0], s[1][1]);
+        pa[3] = pack2(s[1][2], s[1][3]);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t bv[4];
+          const uint32_t ad = vs + tile_off<SL>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                       : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
+          mma_bf16(acc[2 * j], pa, bv[0], bv[1]);
+          mma_bf16(acc[2 * j + 1], pa, bv[2], bv[3]);
+        }
+      } else {
+        // the 8 tokens of score tile jt are the k of one step: index qd is token 2 qd and qd + 4 is token 2 qd + 1,
+        // in the weights (as the scores came out) and in the values alike
+#pragma unroll
+        for (int jt = 0; jt < 2; ++jt) {
+          uint32_t ph[4], pl[4];
+          split_tf32(s[jt][0], ph[0], pl[0]);
+          split_tf32(s[jt][2], ph[1], pl[1]);
+          split_tf32(s[jt][1], ph[2], pl[2]);
+          split_tf32(s[jt][3], ph[3], pl[3]);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            const int r = 8 * jt + 2 * qd, c = 2 * j + (g >> 2);
+            const float v0 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r, c) + (g & 3) * 4);
+            const float v1 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r + 1, c) + (g & 3) * 4);
+            mma_3tf32(acc[j], ph, pl, v0, v1);
+          }
+        }
+      }
     }
     // ---- the slices' sums meet: each warp leaves its own in a stage it has read (16-byte chunks of a row change places
     // by the row's low bits, against bank conflicts)
@@ -442,20 +404,18 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       float *om = reinterpret_cast<float *>(ring + stage * 2 * SLB);
       slice_sync<RG>(slice);  // the other warp of the slice has read it too
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 16 * i + g + 8 * e;
-          const float ls = quad_sum(l[i][e]);
-          if (qd == 0) {
-            mass[warp][0][r] = m[i][e];
-            mass[warp][1][r] = ls;
-          }
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-            *reinterpret_cast<float2 *>(om + r * D + (((2 * j + (qd >> 1)) ^ (r & 7)) << 2) + 2 * (qd & 1)) =
-                make_float2(acc[i][j][2 * e], acc[i][j][2 * e + 1]);
+      for (int e = 0; e < 2; ++e) {
+        const int r = g + 8 * e;
+        const float ls = quad_sum(l[e]);
+        if (qd == 0) {
+          mass[warp][0][r] = m[e];
+          mass[warp][1][r] = ls;
         }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<float2 *>(om + r * D + (((2 * j + (qd >> 1)) ^ (r & 7)) << 2) + 2 * (qd & 1)) =
+              make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+      }
       if (lane == 0) where[warp] = slice * (STAGES * 2 * SLB) + stage * 2 * SLB;
     }
     __syncthreads();
@@ -464,7 +424,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     const int slot = first ? 1 : 0;
     float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
     for (int r = warp * (32 / LPR) + lane / LPR; r < rows; r += 4 * RG * (32 / LPR)) {
-      const int c = lane % LPR, w0 = r / (16 * MI) * 4, rr = r % (16 * MI);  // the row's four warps
+      const int c = lane % LPR, w0 = r / 16 * 4, rr = r % 16;  // the row's four warps
       float mw[4], M = -INFINITY;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -522,11 +482,13 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 
 // Joins the pieces of cut items.  Block (j, y): rows of the j-th of them, which began in some CTA c and went on in the
 // next ones (the block looks for c in the headers, so that the grid need not be larger than the number of items).  JW
-// warps share a row (8 where few items are cut into many pieces each, 1 where many are cut into a few): each takes every JW-th batch of 8 pieces, asks for all of a batch before it uses any, and weights the batch by
-// the running maximum; the warps' results meet in shared memory.  The order of the sums is fixed.
+// warps share a row (8 where few items are cut into many pieces each, 1 where many are cut into a few): each takes every
+// JW-th batch of pieces (8, or 2 where a warp has the row alone and there are seldom more: 2048 new tokens after 8192
+// take 191 us in all, 197 us with 8), asks for all of a batch before it uses any, and weights the batch by the running
+// maximum; the warps' results meet in shared memory.  The order of the sums is fixed.
 template <typename I, int D, int JW>
 __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(PagedArgs a, int MT, int C) {
-  constexpr int WARPS = JW == 1 ? 4 : JW, RW = WARPS / JW, E = D / 32, BATCH = 8;
+  constexpr int WARPS = JW == 1 ? 4 : JW, RW = WARPS / JW, E = D / 32, BATCH = JW == 1 ? 2 : 8;
   __shared__ float sh[WARPS][32 * E + 2];
   pdl_trigger();
   pdl_wait();
@@ -634,31 +596,32 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
 }
 
 namespace {
-template <typename I, int D, int MI, int RG, int STAGES>
+template <typename I, int D, int RG, int STAGES>
 cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
   constexpr size_t ring = (size_t)SLICES * STAGES * 2 * SL * D * sizeof(I);
   static_assert(ring >= sizeof(PlanSmem<128 * RG>), "the search uses the rings' memory");
-  constexpr size_t smem = 1024 + ring + (size_t)16 * MI * RG * D * sizeof(I);
-  auto *k = attn_rows_kernel<I, D, MI, RG, STAGES>;
+  constexpr size_t smem = 1024 + ring + (size_t)16 * RG * D * sizeof(I);
+  auto *k = attn_rows_kernel<I, D, RG, STAGES>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(ctas), dim3(128 * RG), smem, st, a, tk, tv);
 }
 }  // namespace
 
-// 16 rows a tile where that is enough, and then 96 KB of rings and two CTAs per SM unless a slice is 16 KB (fp32, D =
-// 128); more rows: two row groups (fp32, D = 64: of 32 rows each, so that a key's split into two parts serves both
-// 16-row tiles), 192 KB of rings.
-int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 ? 16 : (!bf && D == 64 ? 64 : 32); }
+// 16 rows a tile where that is enough, and in fp32 with D = 64 always: 96 KB of rings (fp32, D = 128: 192 KB) and then two
+// CTAs per SM.  More rows: two row groups and 192 KB of rings, so that a key or value is fetched and, in fp32, split into
+// its two parts half as often (fp32: D = 64, 8 sequences of up to 256 new tokens: 78 us with 16 rows, 85 us with 64 or 32;
+// D = 128, 512 new tokens after 3584: 403 us with 32 rows, 600 us with 16).
+int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 || (!bf && D == 64) ? 16 : 32; }
 int attn_rows_per_sm(bool bf, int D, int MT) { return MT == 16 && (bf || D == 64) ? 2 : 1; }
 cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf, int D, int MT, int ctas,
                              cudaStream_t st) {
   if (!bf) {
-    if (D == 64) return MT == 16 ? launch_rows<float, 64, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 64, 2, 2, 6>(a, tk, tv, ctas, st);
-    return MT == 16 ? launch_rows<float, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 1, 2, 3>(a, tk, tv, ctas, st);
+    if (D == 64) return launch_rows<float, 64, 1, 3>(a, tk, tv, ctas, st);
+    return MT == 16 ? launch_rows<float, 128, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 2, 3>(a, tk, tv, ctas, st);
   }
-  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 1, 2, 12>(a, tk, tv, ctas, st);
-  return MT == 16 ? launch_rows<bf16, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 1, 2, 6>(a, tk, tv, ctas, st);
+  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 12>(a, tk, tv, ctas, st);
+  return MT == 16 ? launch_rows<bf16, 128, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 2, 6>(a, tk, tv, ctas, st);
 }
 
 namespace {

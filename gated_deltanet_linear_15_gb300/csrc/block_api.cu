@@ -60,6 +60,8 @@ int check_attn(const gdn_paged_shape *s) {
   if (!std::isfinite(s->scale)) return fail(GDN_ERR_INVALID_ARG, "scale must be finite");
   if ((long long)s->total_q * (s->num_heads / s->num_kv_heads) > 0x7fffffffll)
     return fail(GDN_ERR_UNSUPPORTED, "too many query rows");
+  if (s->num_heads / s->num_kv_heads > 65535)  // a cut item's header has 16 bits for the place in the group
+    return fail(GDN_ERR_UNSUPPORTED, "more than 65535 query heads per key head");
   const int v = 16 / (int)esize(s->dtype);
   const struct { int64_t v; const char *name; } st[] = {
       {s->q_tok, "q_tok"}, {s->q_head, "q_head"}, {s->k_page, "k_page"}, {s->k_tok, "k_tok"}, {s->k_head, "k_head"},
@@ -74,7 +76,7 @@ int check_attn(const gdn_paged_shape *s) {
 }
 
 // The kernel of a call and its grid: bf16 with more than 32 (query, head) rows per key head in the longest sequence
-// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 to 64 rows).
+// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 or 32 rows).
 struct AttnPlan {
   bool tc;
   int MT, ctas;
@@ -208,6 +210,8 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   const AttnPlan p = attn_plan(s);
   if (!ws || ws_bytes < p.total) return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.total, ws ? ws_bytes : (size_t)0);
   TRY(need_aligned(ws, "workspace"));
+  // a CTA reads queries and cache rows after another wrote its outputs
+  if (o == q || o == k || o == v) return fail(GDN_ERR_INVALID_ARG, "o is one of the inputs");
   const Stream st = (Stream)stream;
   PagedArgs a;
   a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;

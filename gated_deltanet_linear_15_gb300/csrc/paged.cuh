@@ -2,8 +2,7 @@
 //
 // The (token, head-of-group) pairs of one sequence and key head are its query rows: row r is token r / G, query head
 // h G + r % G.  A tile of MT consecutive rows reads the keys [lo, hi) that any of its rows sees, in blocks of BN
-// tokens.  An item is one (sequence, tile, key head); its units are its key blocks (one when there are none), or, in the
-// fp32 kernel of 64-row tiles, whose time goes with the rows, so many times one more than its 16-row groups.  All
+// tokens.  An item is one (sequence, tile, key head); its units are its key blocks (one when there are none).  All
 // items' units stand in one line, sequence by sequence, and CTA c of C = min(grid, total) takes the units
 // [total c / C, total (c + 1) / C): the same work for everyone to one block, whatever the lengths are, with at most two
 // cut items per CTA.  A cut item's pieces, which consecutive CTAs hold, leave unnormalised sums, maxima and masses in
@@ -61,8 +60,7 @@ struct Tile {
   int rows;       // valid rows (0: no such tile)
   int lo, hi;     // keys that some row sees
   int blk0, nblk; // in blocks of BN
-  int weight;     // units of a block
-  __device__ __forceinline__ int units() const { return max(nblk, 1) * weight; }
+  __device__ __forceinline__ int units() const { return max(nblk, 1); }
   int pos0;       // position of token r0 / G of the sequence's new tokens
 };
 template <int MT, int BN>
@@ -76,7 +74,6 @@ __device__ __forceinline__ Tile tile_of(const PagedArgs &a, const SeqInfo &s, in
   w.lo = a.window ? max(0, w.pos0 - a.window + 1) : 0;
   w.blk0 = w.lo / BN;
   w.nblk = w.rows > 0 && w.hi > w.lo ? (w.hi + BN - 1) / BN - w.blk0 : 0;
-  w.weight = MT == 64 ? 1 + (w.rows + 15) / 16 : 1;
   return w;
 }
 template <int MT> __device__ __forceinline__ int tiles_of(const PagedArgs &a, const SeqInfo &s) {
@@ -384,8 +381,8 @@ template <int MT> __device__ __forceinline__ int4 cut_header(const PagedArgs &a,
 __device__ __forceinline__ int cursor_piece(const Cursor &c, int &b0, int &b1, bool &first, bool &last) {
   const int per = c.w.units();
   const int n = (int)min((long long)(per - c.skip), c.end - c.u);
-  b0 = c.w.weight == 1 ? c.skip : min(c.w.nblk, (c.skip + c.w.weight - 1) / c.w.weight);  // blocks that begin in the piece
-  b1 = min(c.w.nblk, c.w.weight == 1 ? c.skip + n : (c.skip + n + c.w.weight - 1) / c.w.weight);
+  b0 = c.skip;
+  b1 = min(c.w.nblk, c.skip + n);
   first = c.skip == 0;
   last = c.skip + n == per;
   return n;

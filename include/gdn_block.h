@@ -71,11 +71,12 @@ typedef struct {
  *
  * A query that sees no key (p < 0, or an empty sequence) gets o = 0, lse = -inf.  lse fp32 [total_q, Hq], contiguous,
  * or NULL.  Slots outside what the queries see may hold anything, NaN included; a key that only some of the queries
- * computed together see (32 or 256 (query, head) rows) must have a finite value vector.  A missing page counts as
+ * computed together see (16, 32 or 256 (query, head) rows) must have a finite value vector.  A missing page counts as
  * keys and values of zero.
  * bf16: products in bf16 with fp32 sums, the weights rounded to bf16 before the second product.  fp32: products in
  * three TF32 parts each, about 2^-21 relative.  q, k_cache, v_cache, o: 16-byte aligned with strides of whole 16
- * bytes.
+ * bytes, those of the caches positive and below 2^37; at most 65535 query heads per key head.  o and lse share no
+ * memory with the inputs.
  */
 size_t gdn_paged_attn_workspace_size(const gdn_paged_shape *shape);
 int gdn_paged_attn_fwd(const gdn_paged_shape *shape, const void *q, const void *k_cache, const void *v_cache,

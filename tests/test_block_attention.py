@@ -328,6 +328,19 @@ def test_c_entry_refuses_pointers(lib):
     assert _call(lib, _shape(total_q=0)) == 0            # nothing to do: no launch
 
 
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_c_entry_refuses_output_over_input(lib, name):
+    """Other CTAs still read what one has written over."""
+    assert _call(lib, _shape(), **{"o": 0x50000, "q": 0x20000, "k": 0x30000, "v": 0x40000, name: 0x50000}) == 1
+    assert b"inputs" in lib.gdn_last_error_string()
+
+
+def test_c_entry_refuses_group_beyond_16_bits(lib):
+    s = _shape(num_heads=65536, num_kv_heads=1, total_q=2)
+    assert _call(lib, s) == 2 and lib.gdn_paged_attn_workspace_size(ctypes.byref(s)) == 0
+    assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(num_heads=65535, num_kv_heads=1, total_q=2))) > 0
+
+
 def test_header_and_binding_agree(lib):
     import os
     import re

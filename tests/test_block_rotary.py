@@ -140,6 +140,18 @@ def test_gradient_by_formula_and_differences(interleaved):
     assert abs(lhs - rhs) <= 10 * math.sqrt(T * 4 * D) * 8 * 2 ** -24 * 8
 
 
+@gpu
+def test_gradient_of_queries_alone():
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(9)
+    q, gq = torch.randn(7, 3, 32, generator=gen).to(DEV).requires_grad_(), torch.randn(7, 3, 32, generator=gen).to(DEV)
+    table, pos = table_ref(64, 32).float().to(DEV), torch.arange(7, dtype=torch.int32, device=DEV)
+    out, none = g.rotary_embedding(q, None, table, pos)
+    assert none is None
+    out.backward(gq)
+    close(q.grad, ref.rotate(gq, table, pos, False, inverse=True), gq)
+
+
 def _append_case(seqs, dtype, D, Hq, Hkv, page, head_major, seed):
     gen = torch.Generator().manual_seed(seed)
     qs, ks = [s[0] for s in seqs], [s[1] for s in seqs]
