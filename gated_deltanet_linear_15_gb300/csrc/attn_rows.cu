@@ -5,14 +5,18 @@
 //
 // Bound by the bytes of the cache: each key and value is used by a few rows only (16 flops per byte at four query heads
 // per key head), far below the tensor cores' ratio.  So the kernel is a stream: the units of the whole batch are split
-// evenly over the CTAs (paged.cuh), and a CTA's 64-token blocks are cut into four slices of 16 tokens.  A slice belongs
-// to RG warps, each with 16 of the tile's rows (MT = 16 RG), and has its own ring of TMA stages; every warp has its
-// own running maximum, mass and sums, and meets the other slices only when the piece ends.  The query rows stay in
-// registers as mma.sync A fragments; scores come out in the layout that the second product takes as its A operand.
-// tcgen05 has no use here: its 128-row tile would be an eighth full, and the softmax would leave registers for TMEM and
-// come back.
+// evenly over the CTAs (paged.cuh), and a CTA's blocks are cut into four slices of 16 NS tokens.  A slice belongs to RG
+// warps, each with 16 of the tile's rows (MT = 16 RG), and has its own ring of TMA stages; every warp has its own running
+// maximum, mass and sums, and meets the other slices only when the piece ends.  The query rows stay in registers as
+// mma.sync A fragments; scores come out in the layout that the second product takes as its A operand.  tcgen05 has no use
+// here: its 128-row tile would be an eighth full, and the softmax would leave registers for TMEM and come back.
 //
-// A slice is loaded by one lane, one box of 16 tokens by 128 bytes each, with the 128-byte swizzle, which is what the
+// 16 tokens a slice keep the units small, which evens out ragged batches (64 sequences of 512 .. 16384 tokens, one new:
+// 336 us, 6.4 TB/s).  With two row groups a step of 16 tokens is bound by its chain of latencies (wait, score, maximum,
+// weight), and 32 tokens halve the steps: 4 new tokens after 65527 (32 rows, 67 MB) take 25.0 us instead of 26.4, after
+// 262140 54 us (5.0 TB/s with the fixed costs, 6.9 without) instead of 60.
+//
+// A slice is loaded by one lane, a box of 16 or 32 tokens by 128 bytes each, with the 128-byte swizzle, which is what the
 // fragment reads want.  (Sixteen-byte copies by every lane took 40 % of the instructions of the loop.)  Rows of a slice
 // outside what the tile sees are cleared in shared memory; a missing page is loaded from an out-of-range coordinate,
 // which fills zeros.  At a piece's end the sums go into the stages read last, while the first slices and the queries of
@@ -32,7 +36,7 @@ using namespace umma;
 
 namespace {
 
-constexpr int SLICES = 4, SL = 16, BN = SLICES * SL;
+constexpr int SLICES = 4;
 constexpr float RAISE = 8.f;  // log2 of the growth of a row's maximum that is left in its weights
 
 __device__ __forceinline__ float ex2(float x) {
@@ -111,15 +115,17 @@ template <int RG> __device__ __forceinline__ void slice_sync(int slice) {
 
 }  // namespace
 
-template <typename I, int D, int RG, int STAGES>
+template <typename I, int D, int RG, int NS, int STAGES>
 __global__ void __launch_bounds__(128 * RG, RG == 1 && D * sizeof(I) <= 256 ? 2 : 1)
 attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  constexpr int SL = 16 * NS, BN = SLICES * SL;
   constexpr int NT = 128 * RG, MT = 16 * RG, RB = D * sizeof(I), CPR = RB / 16, SLB = SL * RB;
   constexpr int BOXES = RB / 128, BW = 128 / sizeof(I);  // boxes of a slice, features of a box
-  constexpr int DIST = STAGES - RG;                      // slices on their way ahead of the one in use
+  constexpr int SUMS = 16 * D * 4, PER = 2 * SLB / SUMS < RG ? 2 * SLB / SUMS : RG;  // a warp's sums; of them in a stage
+  constexpr int DIST = STAGES - RG / PER;                // slices on their way ahead of the one in use
   constexpr bool F32 = sizeof(I) == 4;
   constexpr int KS = F32 ? D / 8 : D / 16;  // k steps of q . k
-  static_assert(16 * D * 4 <= 2 * SLB, "a warp's sums fit a stage");
+  static_assert(PER >= 1 && RG % PER == 0, "a warp's sums fit a stage");
   extern __shared__ uint8_t raw[];
   __shared__ Cursor cur, nxt;  // one for the CTA, out of registers
   __shared__ int going;
@@ -177,18 +183,32 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     return tw;
   };
   auto page_of = [&](const int *trow, int token) {
-    const int pg = trow[token >> a.log2P];
+    const int j = token >> a.log2P, pg = j < a.max_pages ? trow[j] : -1;
     return (unsigned)pg < (unsigned)a.num_pages ? pg : a.num_pages;
   };
-  auto issue = [&](int token, int pg, int h, uint32_t stage) {
+  struct Pages {
+    int p[NS];  // of each 16 tokens of a slice
+  };
+  auto pages_of = [&](const int *trow, int token) {
+    Pages pg;
+#pragma unroll
+    for (int u = 0; u < NS; ++u) pg.p[u] = page_of(trow, token + 16 * u);
+    return pg;
+  };
+  const bool whole = NS > 1 && P >= SL;  // a slice lies in one page, and the boxes have its height
+  auto issue = [&](int token, const Pages &pg, int h, uint32_t stage) {
     if (lane == 0 && rg == 0 && !expired) {
       const uint32_t bar = full_u + 8 * stage, dst = ring_u + stage * 2 * SLB;
-      const int off = token & (P - 1);
       mbar_expect_tx(bar, 2 * SLB);
 #pragma unroll
-      for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + i * (SL * 128), &tk, i * BW, h, off, pg, bar);
+      for (int u = 0; u < NS; ++u) {
+        if (u > 0 && whole) break;
+        const int off = (token + 16 * u) & (P - 1);
 #pragma unroll
-      for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + SLB + i * (SL * 128), &tv, i * BW, h, off, pg, bar);
+        for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + (i * SL + 16 * u) * 128, &tk, i * BW, h, off, pg.p[u], bar);
+#pragma unroll
+        for (int i = 0; i < BOXES; ++i) tma_load_4d(dst + SLB + (i * SL + 16 * u) * 128, &tv, i * BW, h, off, pg.p[u], bar);
+      }
     }
   };
   // asks for the queries and the first slices of the piece at c
@@ -202,11 +222,12 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         cp_async16(qsm + tile_off<MT>(r, ch), Q + tok * a.q_tok + head * a.q_head + ch * (16 / (int)sizeof(I)), r < c.w.rows);
       }
     }
-    int b0, b1, pg[DIST];
+    int b0, b1;
+    Pages pg[DIST];
     const int tw = blocks(c, b0, b1);
     const int *trow = a.table + (long long)c.n * a.table_stride;
 #pragma unroll
-    for (int s = 0; s < DIST; ++s) pg[s] = b0 + s < b1 ? page_of(trow, tw + (b0 + s) * BN) : 0;
+    for (int s = 0; s < DIST; ++s) if (b0 + s < b1) pg[s] = pages_of(trow, tw + (b0 + s) * BN);
 #pragma unroll
     for (int s = 0; s < DIST; ++s)
       if (b0 + s < b1) issue(tw + (b0 + s) * BN, pg[s], c.h, stage_at(s));
@@ -220,7 +241,8 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     const int tw = blocks(cur, b0, b1);
     const int lo = cur.w.lo, hi = cur.w.hi, rows = cur.w.rows, pos0 = cur.w.pos0, kvh = cur.h;
     const int *trow = a.table + (long long)cur.n * a.table_stride;
-    int pg_next = b0 + DIST < b1 ? page_of(trow, tw + (b0 + DIST) * BN) : 0;
+    Pages pg_next = {};
+    if (b0 + DIST < b1) pg_next = pages_of(trow, tw + (b0 + DIST) * BN);
     if (tid == NT - 1) {
       Cursor c = cur;
       going = cursor_next<MT, BN>(a, c, n);
@@ -264,7 +286,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       if (!expired && !slice_wait(full_u + 8 * st, ph)) expired = 4;
       slice_sync<RG>(slice);  // every lane of the slice's warps is done with the block before, too
       if (b + DIST < b1) issue(tw + (b + DIST) * BN, pg_next, kvh, stage_at(DIST));
-      if (b + DIST + 1 < b1) pg_next = page_of(trow, tw + (b + DIST + 1) * BN);
+      if (b + DIST + 1 < b1) pg_next = pages_of(trow, tw + (b + DIST + 1) * BN);
       const uint32_t ks = ring_u + st * 2 * SLB, vs = ks + SLB;
       uint8_t *ksp = ring + st * 2 * SLB, *vsp = ksp + SLB;
       if (++st == STAGES) {
@@ -283,28 +305,30 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         __syncwarp();
       }
       if (!active) continue;
-      // ---- scores of 16 tokens: tiles 0 (tokens 0-7) and 1 (8-15)
-      float s[2][4];
+      // ---- scores: tile j holds tokens 8 j .. 8 j + 7
+      float s[2 * NS][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
       if constexpr (!F32) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t bk[4];
-          const uint32_t ad = ks + tile_off<SL>((lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                       : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
-          mma_bf16(s[0], qf[k], bk[0], bk[1]);
-          mma_bf16(s[1], qf[k], bk[2], bk[3]);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int u = 0; u < NS; ++u) {
+            uint32_t bk[4];
+            const uint32_t ad = ks + tile_off<SL>(16 * u + (lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
+            mma_bf16(s[2 * u], qf[k], bk[0], bk[1]);
+            mma_bf16(s[2 * u + 1], qf[k], bk[2], bk[3]);
+          }
       } else {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          float bk[2][2];
+          float bk[2 * NS][2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
               bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
@@ -312,15 +336,15 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[k][e]), ah[e], al[e]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) mma_3tf32(s[j], ah, al, bk[j][0], bk[j][1]);
+          for (int j = 0; j < 2 * NS; ++j) mma_3tf32(s[j], ah, al, bk[j][0], bk[j][1]);
         }
       }
       // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
       const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
-      float mx[2];
+      float mx[2] = {-INFINITY, -INFINITY};
       bool raise = false;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float z = s[j][e] * a.scale_log2;
@@ -329,10 +353,11 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
             if (key > p || (a.window && key <= p - a.window)) z = -INFINITY;
           }
           s[j][e] = z;
+          mx[e >> 1] = fmaxf(mx[e >> 1], z);
         }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = quad_max(fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])));
+        mx[e] = quad_max(mx[e]);
         raise |= mx[e] > m[e] + RAISE;
       }
       if (__any_sync(0xffffffffu, raise)) {
@@ -353,7 +378,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       for (int e = 0; e < 2; ++e) {
         const float mm = m[e] == -INFINITY ? 0.f : m[e];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float p = ex2(s[j][2 * e + x] - mm);
@@ -363,25 +388,28 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       }
       // ---- sums += weights x values
       if constexpr (!F32) {
-        uint32_t pa[4];
-        pa[0] = pack2(s[0][0], s[0][1]);
-        pa[1] = pack2(s[0][2], s[0][3]);
-        pa[2] = pack2(s[1][0], s[1][1]);
-        pa[3] = pack2(s[1][2], s[1][3]);
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          uint32_t bv[4];
-          const uint32_t ad = vs + tile_off<SL>((lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-                       : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
-          mma_bf16(acc[2 * j], pa, bv[0], bv[1]);
-          mma_bf16(acc[2 * j + 1], pa, bv[2], bv[3]);
+        for (int u = 0; u < NS; ++u) {
+          uint32_t pa[4];
+          pa[0] = pack2(s[2 * u][0], s[2 * u][1]);
+          pa[1] = pack2(s[2 * u][2], s[2 * u][3]);
+          pa[2] = pack2(s[2 * u + 1][0], s[2 * u + 1][1]);
+          pa[3] = pack2(s[2 * u + 1][2], s[2 * u + 1][3]);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t bv[4];
+            const uint32_t ad = vs + tile_off<SL>(16 * u + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                         : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
+            mma_bf16(acc[2 * j], pa, bv[0], bv[1]);
+            mma_bf16(acc[2 * j + 1], pa, bv[2], bv[3]);
+          }
         }
       } else {
         // the 8 tokens of score tile jt are the k of one step: index qd is token 2 qd and qd + 4 is token 2 qd + 1,
         // in the weights (as the scores came out) and in the values alike
 #pragma unroll
-        for (int jt = 0; jt < 2; ++jt) {
+        for (int jt = 0; jt < 2 * NS; ++jt) {
           uint32_t ph[4], pl[4];
           split_tf32(s[jt][0], ph[0], pl[0]);
           split_tf32(s[jt][2], ph[1], pl[1]);
@@ -400,8 +428,8 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     // ---- the slices' sums meet: each warp leaves its own in a stage it has read (16-byte chunks of a row change places
     // by the row's low bits, against bank conflicts)
     {
-      const uint32_t stage = stage_at(STAGES - 1 - rg);
-      float *om = reinterpret_cast<float *>(ring + stage * 2 * SLB);
+      const uint32_t at = stage_at(STAGES - 1 - rg / PER) * 2 * SLB + rg % PER * SUMS;
+      float *om = reinterpret_cast<float *>(ring + at);
       slice_sync<RG>(slice);  // the other warp of the slice has read it too
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -416,7 +444,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
           *reinterpret_cast<float2 *>(om + r * D + (((2 * j + (qd >> 1)) ^ (r & 7)) << 2) + 2 * (qd & 1)) =
               make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
       }
-      if (lane == 0) where[warp] = slice * (STAGES * 2 * SLB) + stage * 2 * SLB;
+      if (lane == 0) where[warp] = slice * (STAGES * 2 * SLB) + at;
     }
     __syncthreads();
     if (more) begin_piece(nxt);
@@ -596,12 +624,12 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
 }
 
 namespace {
-template <typename I, int D, int RG, int STAGES>
+template <typename I, int D, int RG, int NS, int STAGES>
 cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
-  constexpr size_t ring = (size_t)SLICES * STAGES * 2 * SL * D * sizeof(I);
+  constexpr size_t ring = (size_t)SLICES * STAGES * 2 * 16 * NS * D * sizeof(I);
   static_assert(ring >= sizeof(PlanSmem<128 * RG>), "the search uses the rings' memory");
   constexpr size_t smem = 1024 + ring + (size_t)16 * RG * D * sizeof(I);
-  auto *k = attn_rows_kernel<I, D, RG, STAGES>;
+  auto *k = attn_rows_kernel<I, D, RG, NS, STAGES>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(ctas), dim3(128 * RG), smem, st, a, tk, tv);
@@ -613,15 +641,16 @@ cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtenso
 // its two parts half as often (fp32: D = 64, 8 sequences of up to 256 new tokens: 78 us with 16 rows, 85 us with 64 or 32;
 // D = 128, 512 new tokens after 3584: 403 us with 32 rows, 600 us with 16).
 int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 || (!bf && D == 64) ? 16 : 32; }
+int attn_rows_box(bool bf, int MT, int page) { return bf && MT == 32 && page >= 32 ? 32 : 16; }
 int attn_rows_per_sm(bool bf, int D, int MT) { return MT == 16 && (bf || D == 64) ? 2 : 1; }
 cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf, int D, int MT, int ctas,
                              cudaStream_t st) {
   if (!bf) {
-    if (D == 64) return launch_rows<float, 64, 1, 3>(a, tk, tv, ctas, st);
-    return MT == 16 ? launch_rows<float, 128, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 2, 3>(a, tk, tv, ctas, st);
+    if (D == 64) return launch_rows<float, 64, 1, 1, 3>(a, tk, tv, ctas, st);
+    return MT == 16 ? launch_rows<float, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 2, 1, 3>(a, tk, tv, ctas, st);
   }
-  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 12>(a, tk, tv, ctas, st);
-  return MT == 16 ? launch_rows<bf16, 128, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 2, 6>(a, tk, tv, ctas, st);
+  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 2, 6>(a, tk, tv, ctas, st);
+  return MT == 16 ? launch_rows<bf16, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 2, 2, 3>(a, tk, tv, ctas, st);
 }
 
 namespace {

@@ -231,7 +231,7 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   a.status = reinterpret_cast<int *>(static_cast<char *>(ws) + p.off_status);
   const bool bf = s->dtype == GDN_BF16;
   CUtensorMap tk, tv;
-  const int slots = p.tc ? std::min(s->page_size, 128) : 16;
+  const int slots = p.tc ? std::min(s->page_size, 128) : attn_rows_box(bf, p.MT, s->page_size);
   TRY(cache_map(&tk, k, s, s->k_page, s->k_tok, s->k_head, slots));
   TRY(cache_map(&tv, v, s, s->v_page, s->v_tok, s->v_head, slots));
   if (p.tc) {

@@ -415,6 +415,7 @@ __device__ __forceinline__ void row_place(const PagedArgs &a, const Cursor &c, i
 // rows of a tile of the row kernel for up to `rows` rows per key head, and its CTAs per SM
 int attn_rows_tile(bool bf16_type, int D, int rows);
 int attn_rows_per_sm(bool bf16_type, int D, int MT);
+int attn_rows_box(bool bf16_type, int MT, int page_size);  // slots of a box of its tensor maps
 cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf16_type, int D, int MT,
                              int ctas, cudaStream_t st);
 // items: an upper bound on the items of the call

@@ -138,6 +138,27 @@ def test_long_context_is_split_and_joined():
 
 
 @gpu
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (BF, 64), (F32, 128)])
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_slices_that_end_past_their_pages(dtype, D, page):
+    """17 to 32 rows per key head, whose slices may reach over two pages: one that ends with the table, one whose second
+    half is a missing page (zeros), windows that begin inside a slice."""
+    import gated_deltanet_linear_15_gb300 as g
+    for seqs, G, window in (([(3, 97)], 8, 0), ([(3, 97), (4, 33), (2, 17)], 8, 19), ([(30, 353)], 1, 21)):
+        x, qs = make(seqs, dtype, D, 2, G, page, seed=page, spare=0)
+        x["page_table"] = x["page_table"][:, :-1].contiguous()
+        o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), window=window, return_lse=True)
+        close(o, lse, x, qs, D ** -0.5, window)
+        if page == 16 and not window:
+            pg = int(x["page_table"][0, 1])
+            x["page_table"][0, 1] = -1
+            o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), return_lse=True)
+            x["page_table"][0, 1] = pg
+            x["k_cache"][pg], x["v_cache"][pg] = 0, 0
+            close(o, lse, x, qs, D ** -0.5)
+
+
+@gpu
 @pytest.mark.parametrize("N,q,dtype", [(33, 1, BF), (300, 1, BF), (300, 3, F32), (513, 1, BF), (700, 2, BF), (90, 40, BF), (600, 20, BF),
                                        (3, 1500, F32)])
 def test_many_sequences(N, q, dtype):
