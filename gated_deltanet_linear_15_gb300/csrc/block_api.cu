@@ -381,7 +381,7 @@ size_t gdn_pages_workspace_size(const gdn_pages_shape *s, int m) {
     fail(GDN_ERR_INVALID_ARG, "m must be >= 0");
     return 0;
   }
-  // extend: prefix [m + 1]; fork: src, parents, children [m] and two lists [m]; compact: map, src, dst [pages], two counts
+  // extend: prefix [m + 1]; fork: src, parents, children and a list [m]; compact: map, src, dst [pages], two counts
   return up256(std::max((size_t)5 * m + 1, (size_t)3 * s->num_pages + 2) * 4);
 }
 #define CHECK_WS(need)                                                                                                   \

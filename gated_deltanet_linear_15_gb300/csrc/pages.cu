@@ -94,13 +94,19 @@ __device__ __forceinline__ int scan_rounds(const int (&n)[SUB], int (&rank)[SUB]
 }
 
 // Calls give(rank, page) for the free pages of rank 0 .. want - 1 (ascending numbers), and returns how many free pages
-// were seen (at least `want` when there are so many).
+// were seen (at least `want` when there are so many).  r0: the first step's counts, which the caller asks for before it
+// goes through its requests, so that the two waits for memory are one.
 template <class F>
-__device__ __forceinline__ int hand_out(const int *ref, int NP, int want, unsigned long long *sh, F give) {
+__device__ __forceinline__ int hand_out(const int *ref, int NP, int want, const int (&r0)[4 * SUB], unsigned long long *sh, F give) {
   int seen = 0;
   for (int base = 0; base < NP && seen < want; base += STEP) {
     int r[4 * SUB], n[SUB], rank[SUB];
-    load_refs(ref, NP, base, 1, r);
+    if (base == 0) {
+#pragma unroll
+      for (int i = 0; i < 4 * SUB; ++i) r[i] = r0[i];
+    } else {
+      load_refs(ref, NP, base, 1, r);
+    }
 #pragma unroll
     for (int k = 0; k < SUB; ++k) {
       n[k] = 0;
@@ -127,8 +133,8 @@ __device__ __forceinline__ int hand_out(const int *ref, int NP, int want, unsign
 }
 
 // free pages in all, up to `want`
-__device__ __forceinline__ int count_free(const int *ref, int NP, int want, unsigned long long *sh) {
-  return hand_out(ref, NP, want, sh, [](int, int) {});
+__device__ __forceinline__ int count_free(const int *ref, int NP, int want, const int (&r0)[4 * SUB], unsigned long long *sh) {
+  return hand_out(ref, NP, want, r0, sh, [](int, int) {});
 }
 
 __device__ __forceinline__ int pages_of(int len, int P) { return (int)(((long long)len + P - 1) / P); }
@@ -143,6 +149,8 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
+  int r0[4 * SUB];
+  load_refs(a.ref, a.NP, 0, 1, r0);
   // what each request needs, and the prefix of the needs in list order
   long long total = 0;
   for (int b = 0; b < m; b += NP_T) {
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
     granted = 0;
   }
   __syncthreads();
-  const int avail = count_free(a.ref, a.NP, (int)total, sh64);
+  const int avail = count_free(a.ref, a.NP, (int)total, r0, sh64);
   // the requests whose pages, and all before theirs, are there
   for (int i = tid; i < m; i += NP_T) {
     const int need = pre[i + 1] - pre[i];
@@ -187,7 +195,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
   }
   __syncthreads();
   const int want = granted;
-  hand_out(a.ref, a.NP, want, sh64, [&](int rank, int page) {
+  hand_out(a.ref, a.NP, want, r0, sh64, [&](int rank, int page) {
     int lo = 0, hi = m;  // the request with pre[lo] <= rank < pre[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -207,13 +215,15 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
 // child, all -1 for what is not to be done; the new page is the copy's target (negative: none).
 __global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, const int *parents, const int *children, int m,
                                                                int *new_page, int *src, int *psrc, int *pdst) {
-  __shared__ int sh[32];
+  __shared__ int sh[32], few[NP_T];
   __shared__ unsigned long long sh64[32];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
-  int total = 0;
-  for (int b = 0; b < m; b += NP_T) {  // new_page holds the rank of the page until it is known
+  int *list = m <= NP_T ? few : pdst + m;  // the request of every rank
+  int total = 0, r0[4 * SUB];
+  load_refs(a.ref, a.NP, 0, 1, r0);
+  for (int b = 0; b < m; b += NP_T) {
     const int i = b + tid;
     int need = 0, p = -1, c = -1, from = -1;
     bool good = false;
@@ -233,7 +243,8 @@ __global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, cons
     }
     const int inc = scan_1024(need, sh);
     if (i < m) {
-      new_page[i] = !good ? -2 : (need ? total + inc - 1 : -1);
+      if (need) list[total + inc - 1] = i;
+      else new_page[i] = good ? -1 : -2;
       src[i] = need ? from : -1;
       psrc[i] = good ? p : -1;
       pdst[i] = good ? c : -1;
@@ -243,21 +254,14 @@ __global__ void __launch_bounds__(NP_T) pages_fork_plan_kernel(PagesArgs a, cons
     total += all;
   }
   __syncthreads();
-  int *list = pdst + m;  // the request of every rank, then the page of every rank
-  for (int i = tid; i < m; i += NP_T)
-    if (new_page[i] >= 0) list[new_page[i]] = i;
-  __syncthreads();
-  const int seen = hand_out(a.ref, a.NP, total, sh64, [&](int rank, int page) { list[m + rank] = page; });
-  __syncthreads();
-  for (int r = tid; r < total; r += NP_T) {
+  const int seen = hand_out(a.ref, a.NP, total, r0, sh64, [&](int rank, int page) {
+    new_page[list[rank]] = page;
+    a.ref[page] = 1;
+  });
+  for (int r = seen + tid; r < total; r += NP_T) {  // no page left: the fork is left out
     const int i = list[r];
-    if (r < seen) {
-      new_page[i] = list[m + r];
-      a.ref[list[m + r]] = 1;
-    } else {  // no page left: the fork is left out
-      new_page[i] = -2;
-      src[i] = psrc[i] = pdst[i] = -1;
-    }
+    new_page[i] = -2;
+    src[i] = psrc[i] = pdst[i] = -1;
   }
   __syncthreads();
   for (int i = tid; i < m; i += NP_T)
