@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     __syncthreads();
   }
   if (warp > 0 && warp < 11 && lane == 0) cursors[warp] = cursors[0];
+  if (tid == 0 && !cursors[0].works()) has_work = 0;
   __syncthreads();
   bool more = has_work;
   const uint32_t tmem = bars.tmem;

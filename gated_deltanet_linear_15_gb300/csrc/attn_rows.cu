@@ -45,13 +45,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -60,14 +60,15 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) 
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to 11 significant bits, halves away from zero
   lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;  // rounded likewise (the product ignores the low 13 bits)
 }
-// c += a b with both operands in two TF32 parts
-__device__ __forceinline__ void mma_3tf32(float (&c)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0, float b1) {
+// sum of c[] += a b with both operands in two TF32 parts; N accumulators, so that the parts wait for one another less
+template <int N>
+__device__ __forceinline__ void mma_3tf32(float (&c)[N][4], const uint32_t (&ah)[4], const uint32_t (&al)[4], float b0, float b1) {
   uint32_t h0, l0, h1, l1;
   split_tf32(b0, h0, l0);
   split_tf32(b1, h1, l1);
-  mma_tf32(c, al, h0, h1);
-  mma_tf32(c, ah, l0, l1);
-  mma_tf32(c, ah, h0, h1);
+  mma_tf32(c[0], al, h0, h1);
+  mma_tf32(c[1 % N], ah, l0, l1);
+  mma_tf32(c[2 % N], ah, h0, h1);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -125,10 +126,11 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
   constexpr int DIST = STAGES - RG / PER;                // slices on their way ahead of the one in use
   constexpr bool F32 = sizeof(I) == 4;
   constexpr int KS = F32 ? D / 8 : D / 16;  // k steps of q . k
+  constexpr bool ROOM = F32 && D == 64;     // registers for both parts of the queries and three sets of scores
   static_assert(PER >= 1 && RG % PER == 0, "a warp's sums fit a stage");
   extern __shared__ uint8_t raw[];
   __shared__ Cursor cur, nxt;  // one for the CTA, out of registers
-  __shared__ int going;
+  __shared__ int found, going;  // what the search found; whether there is a next piece
   __shared__ uint64_t full[SLICES][STAGES];
   __shared__ float mass[4 * RG][2][16];  // maxima and masses of the warps' rows
   __shared__ uint32_t where[4 * RG];     // the stages that hold their sums
@@ -149,22 +151,22 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
   bool cut = false;  // this CTA's header is written
   int expired = 0;   // a bounded wait ran out
   if (warp == 0) {
-    const int found = cursor_begin_one_warp<MT, BN>(a, cur);
-    if (lane == 0) going = found;
+    const int x = cursor_begin_one_warp<MT, BN>(a, cur);
+    if (lane == 0) found = x;
   }
   __syncthreads();
-  if (const int found = going; found == 2) {  // a batch too large for one warp
-    __syncthreads();                          // everyone has read it
+  if (found == 2) {   // a batch too large for one warp
+    __syncthreads();  // everyone has read it
     Cursor c;
     const bool some = cursor_begin_any<NT, MT, BN>(a, c, *reinterpret_cast<PlanSmem<NT> *>(smem));
     if (tid == 0) {
       cur = c;
-      going = some;
+      found = some;
     }
     fence_async_smem();  // the search used the rings' memory
     __syncthreads();
   }
-  bool more = going;
+  bool more = found && cur.works();
   uint8_t *ring = smem + slice * (STAGES * 2 * SLB);
   const uint32_t ring_u = smem_u32(ring), full_u = smem_u32(&full[slice][0]);
   const I *Q = static_cast<const I *>(a.q);
@@ -252,19 +254,35 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     __syncthreads();
     more = going;
 
-    // ---- query fragments: rows g and g + 8 of the warp's 16
-    uint32_t qf[KS][4];
+    // ---- query fragments: rows g and g + 8 of the warp's 16.  fp32: which feature is which k of a product is free as long
+    // as both sides agree, and so 16 bytes of a row serve two k steps: indexes qd and qd + 4 of steps 2 p and 2 p + 1
+    // are the four features of 16-byte piece 2 qd + (p & 1) of the 128 bytes p / 2, which a quarter warp reads from all
+    // banks (one load for four: 512 new tokens after 3584 with D = 128 take
+    // 314 us instead of 403).
+    uint32_t qf[KS][4], ql[ROOM ? KS : 1][4];
     int pos[2];
     const int r0 = 16 * rg;
+    auto piece = [&](int p) { return 8 * (p >> 1) + 2 * qd + (p & 1); };
+    if constexpr (F32) {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      if constexpr (F32) {
+      for (int p = 0; p < KS / 2; ++p)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          qf[k][e] = *reinterpret_cast<const uint32_t *>(qsm + tile_off<MT>(r0 + g + 8 * (e & 1), 2 * k + (e >> 1)) + 4 * qd);
-      } else {
-        ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(r0 + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
+        for (int x = 0; x < 2; ++x) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(qsm + tile_off<MT>(r0 + g + 8 * x, piece(p)));
+          qf[2 * p][x] = v.x;
+          qf[2 * p][x + 2] = v.y;
+          qf[2 * p + 1][x] = v.z;
+          qf[2 * p + 1][x + 2] = v.w;
+        }
+      if constexpr (ROOM) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[k][e]), qf[k][e], ql[k][e]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) ldmatrix_x4(smem_u32(qsm) + tile_off<MT>(r0 + (lane & 15), 2 * k + (lane >> 4)), qf[k]);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -274,13 +292,13 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     const bool active = rows > r0;  // the warp's 16 rows are not all past the tile's
     const int pos_last = cur.s.kv - cur.s.qlen + (int)(((unsigned)cur.t * MT + rows - 1) / (unsigned)a.G);
 
-    float acc[D / 8][4], m[2], l[2];
+    float acc[D / 8][1][4], m[2], l[2];
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[j][0][e] = 0.f;
 
     for (int b = b0; b < b1; ++b) {
       if (!expired && !slice_wait(full_u + 8 * st, ph)) expired = 4;
@@ -306,11 +324,14 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       }
       if (!active) continue;
       // ---- scores: tile j holds tokens 8 j .. 8 j + 7
-      float s[2 * NS][4];
+      constexpr int NA = ROOM ? 3 : 1;
+      float s3[2 * NS][NA][4];
 #pragma unroll
       for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+        for (int n = 0; n < NA; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s3[j][n][e] = 0.f;
       if constexpr (!F32) {
 #pragma unroll
         for (int k = 0; k < KS; ++k)
@@ -320,25 +341,37 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
             const uint32_t ad = ks + tile_off<SL>(16 * u + (lane & 7) + 8 * (lane >> 4), 2 * k + ((lane >> 3) & 1));
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                          : "=r"(bk[0]), "=r"(bk[1]), "=r"(bk[2]), "=r"(bk[3]) : "r"(ad) : "memory");
-            mma_bf16(s[2 * u], qf[k], bk[0], bk[1]);
-            mma_bf16(s[2 * u + 1], qf[k], bk[2], bk[3]);
+            mma_bf16(s3[2 * u][0], qf[k], bk[0], bk[1]);
+            mma_bf16(s3[2 * u + 1][0], qf[k], bk[2], bk[3]);
           }
       } else {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          float bk[2 * NS][2];
+        for (int p = 0; p < KS / 2; ++p) {
+          float4 bk[2 * NS];
 #pragma unroll
-          for (int j = 0; j < 2 * NS; ++j)
+          for (int j = 0; j < 2 * NS; ++j) bk[j] = *reinterpret_cast<const float4 *>(ksp + tile_off<SL>(g + 8 * j, piece(p)));
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              bk[j][e] = *reinterpret_cast<const float *>(ksp + tile_off<SL>(g + 8 * j, 2 * k + e) + qd * 4);
-          uint32_t ah[4], al[4];
+          for (int x = 0; x < 2; ++x) {
+            uint32_t ah[4], al[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split_tf32(__uint_as_float(qf[k][e]), ah[e], al[e]);
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (ROOM) {
+                ah[e] = qf[2 * p + x][e];
+                al[e] = ql[2 * p + x][e];
+              } else {
+                split_tf32(__uint_as_float(qf[2 * p + x][e]), ah[e], al[e]);
+              }
+            }
 #pragma unroll
-          for (int j = 0; j < 2 * NS; ++j) mma_3tf32(s[j], ah, al, bk[j][0], bk[j][1]);
+            for (int j = 0; j < 2 * NS; ++j) mma_3tf32(s3[j], ah, al, x ? bk[j].z : bk[j].x, x ? bk[j].w : bk[j].y);
+          }
         }
       }
+      float s[2 * NS][4];
+#pragma unroll
+      for (int j = 0; j < 2 * NS; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = ROOM ? s3[j][0][e] + s3[j][1 % NA][e] + s3[j][2 % NA][e] : s3[j][0][e];
       // ---- softmax: thread holds rows g, g + 8 (e >> 1), tokens 8 j + 2 qd + (e & 1)
       const bool mask = t0 + SL - 1 > pos0 || (a.window && t0 < pos_last - a.window + 1);
       float mx[2] = {-INFINITY, -INFINITY};
@@ -369,8 +402,8 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
           l[e] *= f;
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
-            acc[j][2 * e] *= f;
-            acc[j][2 * e + 1] *= f;
+            acc[j][0][2 * e] *= f;
+            acc[j][0][2 * e + 1] *= f;
           }
         }
       }
@@ -401,13 +434,14 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
             const uint32_t ad = vs + tile_off<SL>(16 * u + (lane & 7) + 8 * ((lane >> 3) & 1), 2 * j + (lane >> 4));
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                          : "=r"(bv[0]), "=r"(bv[1]), "=r"(bv[2]), "=r"(bv[3]) : "r"(ad) : "memory");
-            mma_bf16(acc[2 * j], pa, bv[0], bv[1]);
-            mma_bf16(acc[2 * j + 1], pa, bv[2], bv[3]);
+            mma_bf16(acc[2 * j][0], pa, bv[0], bv[1]);
+            mma_bf16(acc[2 * j + 1][0], pa, bv[2], bv[3]);
           }
         }
       } else {
         // the 8 tokens of score tile jt are the k of one step: index qd is token 2 qd and qd + 4 is token 2 qd + 1,
-        // in the weights (as the scores came out) and in the values alike
+        // in the weights (as the scores came out) and in the values alike; column g of the output tiles 4 p + i is
+        // feature 4 g + i of the 128 bytes p, so that 16 bytes of a row serve four tiles
 #pragma unroll
         for (int jt = 0; jt < 2 * NS; ++jt) {
           uint32_t ph[4], pl[4];
@@ -416,11 +450,14 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
           split_tf32(s[jt][1], ph[2], pl[2]);
           split_tf32(s[jt][3], ph[3], pl[3]);
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            const int r = 8 * jt + 2 * qd, c = 2 * j + (g >> 2);
-            const float v0 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r, c) + (g & 3) * 4);
-            const float v1 = *reinterpret_cast<const float *>(vsp + tile_off<SL>(r + 1, c) + (g & 3) * 4);
-            mma_3tf32(acc[j], ph, pl, v0, v1);
+          for (int p = 0; p < D / 32; ++p) {
+            const int r = 8 * jt + 2 * qd;
+            const float4 v0 = *reinterpret_cast<const float4 *>(vsp + tile_off<SL>(r, 8 * p + g));
+            const float4 v1 = *reinterpret_cast<const float4 *>(vsp + tile_off<SL>(r + 1, 8 * p + g));
+            mma_3tf32(acc[4 * p], ph, pl, v0.x, v1.x);
+            mma_3tf32(acc[4 * p + 1], ph, pl, v0.y, v1.y);
+            mma_3tf32(acc[4 * p + 2], ph, pl, v0.z, v1.z);
+            mma_3tf32(acc[4 * p + 3], ph, pl, v0.w, v1.w);
           }
         }
       }
@@ -439,10 +476,19 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
           mass[warp][0][r] = m[e];
           mass[warp][1][r] = ls;
         }
+        if constexpr (F32) {
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<float2 *>(om + r * D + (((2 * j + (qd >> 1)) ^ (r & 7)) << 2) + 2 * (qd & 1)) =
-              make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+          for (int p = 0; p < D / 32; ++p)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              *reinterpret_cast<float4 *>(om + r * D + (((8 * p + 2 * qd + x) ^ (r & 7)) << 2)) =
+                  make_float4(acc[4 * p][0][2 * e + x], acc[4 * p + 1][0][2 * e + x], acc[4 * p + 2][0][2 * e + x], acc[4 * p + 3][0][2 * e + x]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2 *>(om + r * D + (((2 * j + (qd >> 1)) ^ (r & 7)) << 2) + 2 * (qd & 1)) =
+                make_float2(acc[j][0][2 * e], acc[j][0][2 * e + 1]);
+        }
       }
       if (lane == 0) where[warp] = slice * (STAGES * 2 * SLB) + at;
     }
