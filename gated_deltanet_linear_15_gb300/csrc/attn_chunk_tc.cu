@@ -108,6 +108,33 @@ __device__ __forceinline__ void st_global_32b(void *p, const uint32_t *v) {
                "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+// 16 lanes x 64 columns, not waited for: r[4 i + 2 e], r[4 i + 2 e + 1] = row lane / 4 + 8 e, columns 8 i + 2 (lane % 4), + 1
+__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// among the four lanes of a quad: t[i] of lane j becomes t[j] of lane i
+__device__ __forceinline__ void quad_transpose(uint32_t (&t)[4][2], int qd) {
+#pragma unroll
+  for (int b = 1; b <= 2; b <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & b)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool up = qd & b;
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? t[i][k] : t[i | b][k], b);
+          t[i][k] = up ? got : t[i][k];
+          t[i | b][k] = up ? t[i | b][k] : got;
+        }
+      }
+}
 // packed pairs of fp32
 __device__ __forceinline__ uint64_t pk(float a, float b) {
   uint64_t r;
@@ -452,15 +479,12 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
       bool first, last;
       const int n = cursor_piece(cur, b0, b1, first, last);
       const int rows = cur.w.rows - x * 128;  // of this tile
-      bool more_next = false;
-      // moves `ahead` to the next piece and asks for its queries
-      auto look_ahead = [&] {
-        if (lane == 0) ahead[warp] = cur;
-        __syncwarp();
-        more_next = cursor_advance(a, ahead[warp], n);
-        return more_next && load_q(ahead[warp]);
-      };
-      if (rows <= 0) q_arrived(look_ahead());
+      // the next piece, found while this one's first scores are on their way
+      if (lane == 0) ahead[warp] = cur;
+      __syncwarp();
+      const bool more_next = cursor_advance(a, ahead[warp], n);
+      auto next_q = [&] { return more_next && load_q(ahead[warp]); };
+      if (rows <= 0) q_arrived(next_q());
       if (rows > 0) {
         const int row = x * 128 + wr;
         const bool live = wr < rows;
@@ -472,7 +496,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         }
         float m = live ? -INFINITY : 0.f, l = 0.f;
         bool pending = false;
-        if (b0 >= b1) pending = look_ahead();
+        if (b0 >= b1) pending = next_q();
         if (b0 < b1) {
           int t0 = (cur.w.blk0 + b0) * BN;
           for (int b = b0; b < b1; ++b, t0 += BN) {
@@ -480,7 +504,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
             ps ^= 1;
             fence_after();
             // the last scores of the piece are there, so its queries are done with: the next ones come meanwhile
-            if (b == b1 - 1) pending = look_ahead();
+            if (b == b1 - 1) pending = next_q();
             // Weights against the maximum as it stands, without looking for a new one.  Their sum tells whether that
             // will do: below 2^40 so is every weight, and sums and products stay far inside fp32 (bf16 has the same
             // exponents).  Above it, or while a row has no maximum yet, the maximum is taken and the weights are formed
@@ -558,33 +582,60 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           const int slot = first ? 1 : 0;
           float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
           const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-          bf16 *op = static_cast<bf16 *>(a.o) + tok * a.o_tok + head * a.o_head;
-          const bool wide = (reinterpret_cast<uintptr_t>(op) & 31) == 0;
+          const unsigned long long op = reinterpret_cast<unsigned long long>(static_cast<bf16 *>(a.o) + tok * a.o_tok + head * a.o_head);
+          // 16 rows by 64 features at a time.  The lane holds two neighbouring features of rows g and g + 8 in each of
+          // eight 8-feature groups; a transposition among the four lanes of a row gives each 32 bytes, so that a store
+          // of the warp fills whole lines (one row to a thread, 32 lines to a store, took 2 us of a piece).
+          const int g = lane >> 2, qd = lane & 3;
+#pragma unroll 1
+          for (int hb = 0; hb < 2; ++hb) {
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            if (b0 < b1) {
-              tmem_ld32_nw(to + 32 * i, o);
-              tmem_wait_ld();
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0;
-            }
-            if (live) {
-              if (whole) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                if (wide) {
-                  st_global_32b(op + 32 * i, w);
-                  st_global_32b(op + 32 * i + 16, w + 8);
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4 *>(op + 32 * i + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-                }
+            for (int cb = 0; cb < D / 64; ++cb) {
+              uint32_t o[32];
+              if (b0 < b1) {
+                tmem_ld16x64(to + ((uint32_t)(16 * hb) << 16) + 64 * cb, o);
+                tmem_wait_ld();
               } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) st_global_32b(rec + (size_t)row * D + 32 * i + e, o + e);
+                for (int e = 0; e < 32; ++e) o[e] = 0;
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int sub = 16 * hb + 8 * e + g;  // the row in the warp's 32
+                const bool there = (warp & 3) * 32 + sub < rows;
+                if (whole) {
+                  const float f = __shfl_sync(0xffffffffu, inv, sub);
+                  const unsigned long long at = __shfl_sync(0xffffffffu, op, sub) + 2 * (64 * cb + 16 * qd);
+                  uint32_t t[4][2], w[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    t[i >> 1][i & 1] = pack_bf16(__uint_as_float(o[4 * i + 2 * e]) * f, __uint_as_float(o[4 * i + 2 * e + 1]) * f);
+                  quad_transpose(t, qd);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) w[i] = t[i & 3][i >> 2];
+                  if (there) {
+                    if ((at & 31) == 0) {
+                      st_global_32b(reinterpret_cast<void *>(at), w);
+                    } else {
+                      reinterpret_cast<uint4 *>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                      reinterpret_cast<uint4 *>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                  }
+                } else {
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t t[4][2], w[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      t[i][0] = o[16 * hf + 4 * i + 2 * e];
+                      t[i][1] = o[16 * hf + 4 * i + 2 * e + 1];
+                    }
+                    quad_transpose(t, qd);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = t[i >> 1][i & 1];
+                    if (there) st_global_32b(rec + (size_t)(x * 128 + (warp & 3) * 32 + sub) * D + 64 * cb + 32 * hf + 8 * qd, w);
+                  }
+                }
               }
             }
           }
