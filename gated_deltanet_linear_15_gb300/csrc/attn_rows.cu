@@ -11,10 +11,11 @@
 // mma.sync A fragments; scores come out in the layout that the second product takes as its A operand.  tcgen05 has no use
 // here: its 128-row tile would be an eighth full, and the softmax would leave registers for TMEM and come back.
 //
-// 16 tokens a slice keep the units small, which evens out ragged batches (64 sequences of 512 .. 16384 tokens, one new:
-// 336 us, 6.4 TB/s).  With two row groups a step of 16 tokens is bound by its chain of latencies (wait, score, maximum,
-// weight), and 32 tokens halve the steps: 4 new tokens after 65527 (32 rows, 67 MB) take 25.0 us instead of 26.4, after
-// 262140 54 us (5.0 TB/s with the fixed costs, 6.9 without) instead of 60.
+// 16 tokens a slice keep the units small, which evens out ragged batches (64 sequences of 512 .. 16384 tokens, one new,
+// 2.16 GB: 325 to 338 us, 6.4 to 6.6 TB/s; one new token of a sequence of 1024: 9.5 us, nearly all of it launches and
+// latencies in a row).  With two row groups a step of 16 tokens is bound by its chain of latencies (wait, score, maximum,
+// weight), and 32 tokens halve the steps: 4 new tokens after 65527 (32 rows, 67 MB) took 25.0 us instead of 26.4 (23.7 now
+// with the split's setup units), after 262140 54 us (5.0 TB/s with the fixed costs, 6.9 without) instead of 60.
 //
 // A slice is loaded by one lane, a box of 16 or 32 tokens by 128 bytes each, with the 128-byte swizzle, which is what the
 // fragment reads want.  (Sixteen-byte copies by every lane took 40 % of the instructions of the loop.)  Rows of a slice
@@ -26,7 +27,8 @@
 // weights carry without loss), so most slices skip that pass over the accumulator.
 //
 // fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the exact rest):
-// hi hi + hi lo + lo hi leaves about 2^-21 of a product.
+// hi hi + hi lo + lo hi leaves about 2^-21 of a product.  Bound by instructions and the latency of the products' chains
+// (8 sequences of 1 .. 256 new tokens, D = 64, window 1024: 44 us, issue slots 34 % busy, tensor pipe 29 %, 17 MB).
 #include "paged.cuh"
 #include "umma.cuh"
 
@@ -482,7 +484,8 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               *reinterpret_cast<float4 *>(om + r * D + (((8 * p + 2 * qd + x) ^ (r & 7)) << 2)) =
-                  make_float4(acc[4 * p][0][2 * e + x], acc[4 * p + 1][0][2 * e + x], acc[4 * p + 2][0][2 * e + x], acc[4 * p + 3][0][2 * e + x]);
+                  make_float4(acc[4 * p][0][2 * e + x], acc[4 * p + 1][0][2 * e + x], acc[4 * p + 2][0][2 * e + x],
+                              acc[4 * p + 3][0][2 * e + x]);
         } else {
 #pragma unroll
           for (int j = 0; j < D / 8; ++j)
@@ -558,7 +561,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 // next ones (the block looks for c in the headers, so that the grid need not be larger than the number of items).  JW
 // warps share a row (8 where few items are cut into many pieces each, 1 where many are cut into a few): each takes every
 // JW-th batch of pieces (8, or 2 where a warp has the row alone and there are seldom more: 2048 new tokens after 8192
-// take 191 us in all, 197 us with 8), asks for all of a batch before it uses any, and weights the batch by the running
+// take 6 us less than with 8), asks for all of a batch before it uses any, and weights the batch by the running
 // maximum; the warps' results meet in shared memory.  The order of the sums is fixed.
 template <typename I, int D, int JW>
 __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(PagedArgs a, int MT, int C) {
@@ -684,8 +687,8 @@ cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtenso
 
 // 16 rows a tile where that is enough, and in fp32 with D = 64 always: 96 KB of rings (fp32, D = 128: 192 KB) and then two
 // CTAs per SM.  More rows: two row groups and 192 KB of rings, so that a key or value is fetched and, in fp32, split into
-// its two parts half as often (fp32: D = 64, 8 sequences of up to 256 new tokens: 78 us with 16 rows, 85 us with 64 or 32;
-// D = 128, 512 new tokens after 3584: 403 us with 32 rows, 600 us with 16).
+// its two parts half as often (fp32: D = 64, 8 sequences of up to 256 new tokens: 44 us with 16 rows, 47 us with 32, 1024
+// new tokens after 3072: 313 and 324 us; D = 128, 512 new tokens after 3584: 530 us with 16 rows, 317 us with 32).
 int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 || (!bf && D == 64) ? 16 : 32; }
 int attn_rows_box(bool bf, int MT, int page) { return bf && MT == 32 && page >= 32 ? 32 : 16; }
 int attn_rows_per_sm(bool bf, int D, int MT) { return MT == 16 && (bf || D == 64) ? 2 : 1; }
@@ -693,9 +696,11 @@ cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CU
                              cudaStream_t st) {
   if (!bf) {
     if (D == 64) return launch_rows<float, 64, 1, 1, 3>(a, tk, tv, ctas, st);
-    return MT == 16 ? launch_rows<float, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<float, 128, 2, 1, 3>(a, tk, tv, ctas, st);
+    return MT == 16 ? launch_rows<float, 128, 1, 1, 3>(a, tk, tv, ctas, st)
+                    : launch_rows<float, 128, 2, 1, 3>(a, tk, tv, ctas, st);
   }
-  if (D == 64) return MT == 16 ? launch_rows<bf16, 64, 1, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 2, 6>(a, tk, tv, ctas, st);
+  if (D == 64)
+    return MT == 16 ? launch_rows<bf16, 64, 1, 1, 6>(a, tk, tv, ctas, st) : launch_rows<bf16, 64, 2, 2, 6>(a, tk, tv, ctas, st);
   return MT == 16 ? launch_rows<bf16, 128, 1, 1, 3>(a, tk, tv, ctas, st) : launch_rows<bf16, 128, 2, 2, 3>(a, tk, tv, ctas, st);
 }
 

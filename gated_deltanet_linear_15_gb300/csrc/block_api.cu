@@ -76,7 +76,9 @@ int check_attn(const gdn_paged_shape *s) {
 }
 
 // The kernel of a call and its grid: bf16 with more than 32 (query, head) rows per key head in the longest sequence
-// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 or 32 rows).
+// takes the tensor-core kernel (256 rows, one CTA per SM), everything else the row kernel (16 or 32 rows).  Sequences of
+// 16384 tokens, 8 key heads of 128, 4 heads each, row kernel / tensor-core kernel: 8 new tokens (32 rows) of one sequence
+// 22 / 29 us, of 16 ragged ones 105 / 136 us; 9 new tokens 30 / 28 and 185 / 136 us; 16 new tokens 33 / 30 and 192 / 132 us.
 struct AttnPlan {
   bool tc;
   int MT, ctas;

@@ -5,9 +5,9 @@
 // tokens.  An item is one (sequence, tile, key head); its units are a few for its setup, then its key blocks (one when
 // there are none).  All items' units stand in one line, sequence by sequence, and CTA c of C = min(grid, total) takes the
 // units [total c / C, total (c + 1) / C): the same work for everyone to one block, whatever the lengths are, with at most
-// two cut items per CTA.  A range that ends among an item's setup units leaves the item to the next CTA.  A cut item's pieces, which consecutive CTAs hold, leave unnormalised sums, maxima and masses in
-// the workspace, and a second kernel joins them in the order of the line, so the result does not depend on who finished
-// first.
+// two cut items per CTA.  A range that ends among an item's setup units leaves the item to the next CTA.  A cut item's
+// pieces, which consecutive CTAs hold, leave unnormalised sums, maxima and masses in the workspace, and a second kernel
+// joins them in the order of the line, so the result does not depend on who finished first.
 //
 // Every CTA finds its range itself: it counts the tiles of all sequences, then the units of all tiles (two block
 // scans), which costs about a microsecond and saves a planning launch.

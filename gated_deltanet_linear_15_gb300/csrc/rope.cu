@@ -10,7 +10,8 @@
 // keeps one unit's place in the head and one token, and walks over heads, `slots` apart: it reads the unit's cos and sin
 // once for all of them, asks for the data of UN heads before it turns any, and finds the token's position and cache slot
 // while the first of them are on their way.  (A line of units with one head per thread reads the table, 64 bytes for 32 of
-// data, for every head: 41 us instead of 37 us for the append of 8192 tokens of 32 + 8 + 8 heads, bf16.)
+// data, for every head: 41 us instead of 37 us for the append of 8192 tokens of 32 + 8 + 8 heads, bf16, which is 5.6 TB/s;
+// 16384 tokens of 16 + 16 heads in fp32: 80.5 us, 6.7 TB/s.)
 #include <math.h>
 
 #include "block.h"
