@@ -8,6 +8,8 @@
 
 namespace gdn {
 
+constexpr int ROPE_THREADS = 128;  // of a CTA, which holds at least a head's 32-byte units
+
 // ---- rotary positions
 // One head group of a launch: heads of one tensor, turned (or only copied, when `turn` is 0) from src to dst; dst NULL
 // for the keys and values of an append, which go to the cache.

@@ -307,7 +307,7 @@ int gdn_rotary(const gdn_rotary_shape *s, const void *q, const void *k, const fl
   TRY(need_ptr(positions, "positions"));
   RopeArgs a = {};
   const int v = 16 / (int)esize(s->dtype);
-  bool vec = s->head_dim % (2 * v) == 0 && s->rot % (2 * v) == 0 && s->head_dim <= 256 * 2 * v;  // a CTA holds a head
+  bool vec = s->head_dim % (2 * v) == 0 && s->rot % (2 * v) == 0 && s->head_dim <= ROPE_THREADS * 2 * v;  // a CTA holds a head
   auto add = [&](const void *src, void *dst, int heads, int64_t st_, int64_t sh, int64_t dt, int64_t dh) {
     if (!heads) return;
     a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, 0, heads, 1};
@@ -347,7 +347,7 @@ int gdn_rotary_append(const gdn_paged_shape *s, const void *q, const void *k, co
   if (s->k_page < 1 || s->v_page < 1) return fail(GDN_ERR_INVALID_ARG, "page strides must be positive");
   RopeArgs a = {};
   const int w = 16 / (int)esize(s->dtype);
-  bool vec = s->head_dim % (2 * w) == 0 && s->rot % (2 * w) == 0 && s->head_dim <= 256 * 2 * w;  // a CTA holds a head
+  bool vec = s->head_dim % (2 * w) == 0 && s->rot % (2 * w) == 0 && s->head_dim <= ROPE_THREADS * 2 * w;  // a CTA holds a head
   auto add = [&](const void *src, void *dst, int heads, int turn, int64_t st_, int64_t sh, int64_t dt, int64_t dh, int64_t dp) {
     a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, dp, heads, turn};
     a.heads += heads;

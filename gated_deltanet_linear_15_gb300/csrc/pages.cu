@@ -7,8 +7,8 @@
 // are found, over the pages' counts, 16384 of them a step); what is long, the rows of the tables and the copies, goes to
 // the whole GPU in a second launch.  Copies are bound by bytes (each slot read and written once): a slot is cut into
 // 16 KB chunks, the chunks of all pairs and pools stand in one line, and a warp-coalesced thread moves four 16-byte
-// pieces at a time, loaded before the first is stored.  8192 pages of 16 tokens compacted, 522 MB read and written: 93 us,
-// 5.6 TB/s; 64 sequences branched, 132 MB: 29 us, of which ending the old branches takes 3, the plan 7 and the copies 18.
+// pieces at a time, loaded before the first is stored.  8192 pages of 16 tokens compacted, 522 MB read and written: 88 us,
+// 5.9 TB/s; 64 sequences branched, 132 MB: 29 us, of which ending the old branches takes 3, the plan 7 and the copies 18.
 #include "block.h"
 #include "common.cuh"
 
@@ -428,7 +428,10 @@ cudaError_t launch_slots_copy(const PoolList &pl, const PairList (&pairs)[2], in
     want = want > n ? want : n;
   }
   if (want <= 0) return cudaSuccess;
-  const long long cap = 152 * 8;  // eight CTAs of 256 threads fill an SM
+  // Eight CTAs of 256 threads fill an SM.  Eight times as many, of which one starts as another ends, drift apart and keep
+  // reads and writes mixed (8192 pages compacted: 88 us; 95 us with eight per SM that all walk in step, 100 us without a
+  // limit, when most find that their pair is not among those that move).
+  const long long cap = 152 * 64;
   return launch_pdl(slots_copy_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(COPY_T), 0, st, l, pairs[0], pairs[1], count,
                     count_dev, job);
 }

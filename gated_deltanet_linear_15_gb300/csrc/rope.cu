@@ -10,8 +10,9 @@
 // keeps one unit's place in the head and one token, and walks over heads, `slots` apart: it reads the unit's cos and sin
 // once for all of them, asks for the data of UN heads before it turns any, and finds the token's position and cache slot
 // while the first of them are on their way.  (A line of units with one head per thread reads the table, 64 bytes for 32 of
-// data, for every head: 41 us instead of 37 us for the append of 8192 tokens of 32 + 8 + 8 heads, bf16, which is 5.6 TB/s;
-// 16384 tokens of 16 + 16 heads in fp32: 80.5 us, 6.7 TB/s.)
+// data, for every head: 41 us for the append of 8192 tokens of 32 + 8 + 8 heads, bf16, instead of 37.  CTAs of 128 threads,
+// seven to an SM, leave a shorter last wave than three of 256: 34.6 us, 5.9 TB/s.  16384 tokens of 16 + 16 heads in fp32:
+// 80.7 us, 6.7 TB/s.)
 #include <math.h>
 
 #include "block.h"
@@ -21,7 +22,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int NTR = 256;
+constexpr int NTR = ROPE_THREADS;
 
 // position and cache slot of a token: slot -1 when it has none, position -1 when it is outside the table
 struct TokPlace {
@@ -100,7 +101,7 @@ template <> __device__ __forceinline__ uint4 repack<float>(const float (&x)[4]) 
 // 16-byte path: D and rot multiples of two pieces' features, every pointer and stride a multiple of 16 bytes.  uph: units
 // of a head; slots: heads that a token's threads begin with.
 template <typename I, int UN>
-__global__ void __launch_bounds__(NTR) rope_kernel(RopeArgs a, int uph, int slots) {
+__global__ void __launch_bounds__(NTR, 7) rope_kernel(RopeArgs a, int uph, int slots) {
   constexpr int V = 16 / sizeof(I);  // features of a piece
   pdl_trigger();
   pdl_wait();
@@ -255,7 +256,7 @@ cudaError_t launch_rope(const RopeArgs &a, bool bf, bool vec, cudaStream_t st) {
   // 64 threads a token (each walks over a few heads), more while that leaves SMs without work
   const int uph = a.D * (bf ? 2 : 4) / 32;
   int slots = 64 / uph > 0 ? 64 / uph : 1;
-  while (slots < a.heads && 2 * slots * uph <= NTR && (long long)a.tokens * slots * uph < 152ll * 2 * NTR) slots *= 2;
+  while (slots < a.heads && 2 * slots * uph <= NTR && (long long)a.tokens * slots * uph < 152ll * 4 * NTR) slots *= 2;
   const int tpb = NTR / (slots * uph);
   const dim3 grid((unsigned)((a.tokens + tpb - 1) / tpb));
   return bf ? launch_pdl(rope_kernel<bf16, 3>, grid, dim3(NTR), 0, st, a, uph, slots)

@@ -90,6 +90,25 @@ def test_rotary(dtype, interleaved, inverse, T, Hq, Hk, D, rot):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,D", [(BF, 2048), (BF, 2064), (BF, 4096), (F32, 1024), (F32, 1032), (F32, 2048)])
+def test_heads_as_wide_as_a_block_and_wider(dtype, D):
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(D)
+    qkv = torch.randn(3, 4, D, generator=gen).to(DEV, dtype)
+    q, k, v = qkv.split([2, 1, 1], 1)
+    cs, pos = table_ref(16, D).float().to(DEV), torch.tensor([4, 5, 6], dtype=torch.int32)
+    want_q, want_k = ref.rotate(q, cs, pos), ref.rotate(k, cs, pos)
+    a, b = g.rotary(q, k, cs, pos.to(DEV))
+    close(a, want_q, q)
+    close(b, want_k, k)
+    kc, vc = torch.zeros(1, 16, 1, D, dtype=dtype, device=DEV), torch.zeros(1, 16, 1, D, dtype=dtype, device=DEV)
+    o = g.rotary_append(q, k, v, cs, kc, vc, torch.zeros(1, 1, dtype=torch.int32, device=DEV),
+                        torch.tensor([7], dtype=torch.int32, device=DEV))
+    assert torch.equal(o, a) and torch.equal(kc[0, 4:7], b) and torch.equal(vc[0, 4:7], v)
+    assert not kc[0, :4].any() and not kc[0, 7:].any()
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_rotary_strided_and_unaligned(dtype, shift):
