@@ -256,10 +256,13 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   }
   pdl_trigger();
   pdl_wait();
+  SeqInfo *seqs = reinterpret_cast<SeqInfo *>(ring);  // the search uses the ring's memory
+  cursor_prepare<NTHR>(a, seqs);
   if (warp == 0) {
-    const int found = cursor_begin_one_warp<MT, BN>(a, cursors[0]);
+    const int found = cursor_begin_one_warp<MT, BN>(a, cursors[0], seqs);
     if (lane == 0) has_work = found;
   }
+  fence_async_smem();
   fence_before();
   __syncthreads();
   fence_after();
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         cursors[0] = c;
         has_work = some;
       }
-      fence_async_smem();  // the search used the ring's memory
+      fence_async_smem();
     }
     __syncthreads();
   }

@@ -152,10 +152,13 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
   pdl_wait();
   bool cut = false;  // this CTA's header is written
   int expired = 0;   // a bounded wait ran out
+  SeqInfo *seqs = reinterpret_cast<SeqInfo *>(smem);  // the search uses the rings' memory
+  cursor_prepare<NT>(a, seqs);
   if (warp == 0) {
-    const int x = cursor_begin_one_warp<MT, BN>(a, cur);
+    const int x = cursor_begin_one_warp<MT, BN>(a, cur, seqs);
     if (lane == 0) found = x;
   }
+  fence_async_smem();
   __syncthreads();
   if (found == 2) {   // a batch too large for one warp
     __syncthreads();  // everyone has read it
@@ -165,7 +168,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       cur = c;
       found = some;
     }
-    fence_async_smem();  // the search used the rings' memory
+    fence_async_smem();
     __syncthreads();
   }
   bool more = found && cur.works();
@@ -215,29 +218,41 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       }
     }
   };
+  // the pages of the first slices of the piece at c
+  struct Ahead {
+    int token, h;  // first slice
+    int n;         // slices of the piece
+    Pages pg[DIST];
+  };
+  auto look = [&](const Cursor &c) {
+    Ahead x;
+    int b0, b1;
+    x.token = blocks(c, b0, b1) + b0 * BN;
+    x.n = b1 - b0;
+    x.h = c.h;
+    const int *trow = a.table + (long long)c.n * a.table_stride;
+#pragma unroll
+    for (int s = 0; s < DIST; ++s)
+      if (s < x.n) x.pg[s] = pages_of(trow, x.token + s * BN);
+    return x;
+  };
   // asks for the queries and the first slices of the piece at c
-  auto begin_piece = [&](const Cursor &c) {
+  auto begin_piece = [&](const Cursor &c, const Ahead &x) {
 #pragma unroll
     for (int i = 0; i < (MT * CPR + NT - 1) / NT; ++i) {  // the rows, coalesced
-      const int x = tid + i * NT, r = x / CPR, ch = x % CPR;
-      if (x < MT * CPR) {
+      const int y = tid + i * NT, r = y / CPR, ch = y % CPR;
+      if (y < MT * CPR) {
         int tok, head;
         row_place(a, c, MT, r < c.w.rows ? r : 0, tok, head);
         cp_async16(qsm + tile_off<MT>(r, ch), Q + tok * a.q_tok + head * a.q_head + ch * (16 / (int)sizeof(I)), r < c.w.rows);
       }
     }
-    int b0, b1;
-    Pages pg[DIST];
-    const int tw = blocks(c, b0, b1);
-    const int *trow = a.table + (long long)c.n * a.table_stride;
-#pragma unroll
-    for (int s = 0; s < DIST; ++s) if (b0 + s < b1) pg[s] = pages_of(trow, tw + (b0 + s) * BN);
 #pragma unroll
     for (int s = 0; s < DIST; ++s)
-      if (b0 + s < b1) issue(tw + (b0 + s) * BN, pg[s], c.h, stage_at(s));
+      if (s < x.n) issue(x.token + s * BN, x.pg[s], x.h, stage_at(s));
   };
 
-  if (more) begin_piece(cur);
+  if (more) begin_piece(cur, look(cur));
   while (more) {
     int b0, b1;
     bool first, last;
@@ -255,6 +270,8 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     cp_async_wait_all();
     __syncthreads();
     more = going;
+    Ahead ahead = {};
+    if (!F32 && more) ahead = look(nxt);  // its pages are there when this piece ends (fp32 has no registers to keep them in)
 
     // ---- query fragments: rows g and g + 8 of the warp's 16.  fp32: which feature is which k of a product is free as long
     // as both sides agree, and so 16 bytes of a row serve two k steps: indexes qd and qd + 4 of steps 2 p and 2 p + 1
@@ -496,7 +513,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
       if (lane == 0) where[warp] = slice * (STAGES * 2 * SLB) + at;
     }
     __syncthreads();
-    if (more) begin_piece(nxt);
+    if (more) begin_piece(nxt, F32 ? look(nxt) : ahead);
     constexpr int LPR = D / 4;  // lanes of a row
     const int slot = first ? 1 : 0;
     float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
@@ -676,7 +693,7 @@ namespace {
 template <typename I, int D, int RG, int NS, int STAGES>
 cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int ctas, cudaStream_t st) {
   constexpr size_t ring = (size_t)SLICES * STAGES * 2 * 16 * NS * D * sizeof(I);
-  static_assert(ring >= sizeof(PlanSmem<128 * RG>), "the search uses the rings' memory");
+  static_assert(ring >= sizeof(PlanSmem<128 * RG>) && ring >= WARP_SEQS * sizeof(SeqInfo), "the search uses the rings' memory");
   constexpr size_t smem = 1024 + ring + (size_t)16 * RG * D * sizeof(I);
   auto *k = attn_rows_kernel<I, D, RG, NS, STAGES>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

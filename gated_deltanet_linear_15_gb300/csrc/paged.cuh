@@ -232,10 +232,9 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
 
 // The same for up to 512 sequences with up to 2048 tiles, by one warp without barriers, each lane taking an equal share of
 // the sequences and then of the tiles.  A CTA runs this code once, so most of its time is that of fetching instructions;
-// the search above costs 64 sequences 7 us more.  Writes c (from one lane) and returns 1, 0 when the CTA
-// has no work, or 2 when the batch is too large.
-template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const PagedArgs &a, Cursor &c) {
-  if (a.N > 512) return 2;
+// the search above costs 64 sequences 7 us more.  seqs: what is known of the sequences, in shared memory.  Writes c (from
+// one lane) and returns 1, 0 when the CTA has no work, or 2 when the batch is too large.
+template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const PagedArgs &a, Cursor &c, const SeqInfo *seqs) {
   const int lane = threadIdx.x & 31;
   auto scan = [&](long long x) {
 #pragma unroll 1
@@ -248,7 +247,7 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const
   const int cs = (a.N + 31) >> 5, n0 = min(a.N, lane * cs), n1 = min(a.N, n0 + cs);
   long long cnt = 0;
 #pragma unroll 1
-  for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seq_info(a, n));
+  for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seqs[n]);
   const long long inc = scan(cnt), all = __shfl_sync(0xffffffffu, inc, 31);
   if (all > 2048) return 2;
   // this lane's tiles [x0, x1); the first one's sequence is among those of the first lane whose tiles reach beyond x0
@@ -272,7 +271,7 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const
       t = left;
 #pragma unroll 1
       for (;; ++nn) {
-        s = seq_info(a, nn);
+        s = seqs[nn];
         k = tiles_of<MT>(a, s);
         if (t < k) break;
         t -= k;
@@ -286,7 +285,7 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const
         units += per;
         if (++x >= x1) break;
         for (++t; t >= k; t = 0) {
-          s = seq_info(a, ++nn);
+          s = seqs[++nn];
           k = tiles_of<MT>(a, s);
         }
       }
@@ -373,10 +372,25 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(cons
   return 1;
 }
 
-// One warp's search, whichever fits
-template <int MT, int BN> __device__ __forceinline__ int cursor_begin_one_warp(const PagedArgs &a, Cursor &c) {
+// What every thread of the CTA does before one warp searches: the lengths of more than 32 sequences come to shared memory,
+// all loads at once (256 decoded sequences of up to 128 tokens: 36.4 us, with the pages of the next
+// piece asked for a piece ahead, instead of 38.0).
+constexpr int WARP_SEQS = 512;
+template <int NT> __device__ __forceinline__ void cursor_prepare(const PagedArgs &a, SeqInfo *seqs) {
+  if (a.N <= 32 || a.N > WARP_SEQS) return;
+  for (int n = threadIdx.x; n < a.N; n += NT) seqs[n] = seq_info(a, n);
+  __syncthreads();
+}
+// One warp's search, whichever fits.  The caller's kernel has to keep its asynchronous copies off `seqs` until then.
+template <int MT, int BN> __device__ __forceinline__ int cursor_begin_one_warp(const PagedArgs &a, Cursor &c, SeqInfo *seqs) {
   const int found = cursor_begin_small<MT, BN>(a, c);
-  return found == 2 ? cursor_begin_warp<MT, BN>(a, c) : found;
+  if (found != 2 || a.N > WARP_SEQS) return found;
+  if (a.N <= 32) {
+    const int lane = threadIdx.x & 31;
+    if (lane < a.N) seqs[lane] = seq_info(a, lane);
+    __syncwarp();
+  }
+  return cursor_begin_warp<MT, BN>(a, c, seqs);
 }
 
 // The header of a CTA whose last item goes on behind its range: c is the cursor at the item's first piece.
