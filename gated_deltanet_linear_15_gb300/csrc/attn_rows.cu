@@ -29,6 +29,8 @@
 // fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the exact rest):
 // hi hi + hi lo + lo hi leaves about 2^-21 of a product.  Bound by instructions and the latency of the products' chains
 // (8 sequences of 1 .. 256 new tokens, D = 64, window 1024: 44 us, issue slots 34 % busy, tensor pipe 29 %, 17 MB).
+#include <algorithm>
+
 #include "paged.cuh"
 #include "umma.cuh"
 
@@ -575,11 +577,12 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 }
 
 // Joins the pieces of cut items.  Block (j, y): rows of the j-th of them, which began in some CTA c and went on in the
-// next ones (the block looks for c in the headers, so that the grid need not be larger than the number of items).  JW
-// warps share a row (8 or 4 where few items are cut into many pieces each, 1 where many are cut into a few): each takes
-// every JW-th batch of pieces (JW, or 2 where a warp has the row alone and there are seldom more: 2048 new tokens after
-// 8192 take 6 us less than with 8), asks for all of a batch before it uses any, and weights the batch by the running
-// maximum; the warps' results meet in shared memory.  The order of the sums is fixed.
+// next ones (the block looks for c in the headers, so that the grid need not be larger than the number of items), a row
+// of every gridDim.y, or four neighbours where a warp has one for itself.  JW warps share a row (8 or 4 where few items are
+// cut into many pieces each, 1 where many are cut into a few): each takes every JW-th batch of pieces (JW, or 2 where a
+// warp has the row alone and there are seldom more: 2048 new tokens after 8192 take 6 us less than with 8), asks for all of
+// a batch before it uses any, and weights the batch by the running maximum; the warps' results meet in shared memory.  The
+// order of the sums is fixed.
 template <typename I, int D, int JW>
 __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(PagedArgs a, int MT, int C) {
   constexpr int WARPS = JW == 1 ? 4 : JW, RW = WARPS / JW, E = D / 32, BATCH = JW == 1 ? 2 : JW;
@@ -604,89 +607,92 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
   if (c < 0) return;
   const int4 h = a.hdr[c];
   const int np = h.x, rows = h.w >> 16, gr = h.w & 0xffff;
-  const int r = blockIdx.y * RW + warp / JW, sub = warp % JW;
-  if (np == 0 || blockIdx.y * RW >= rows) return;
+  const int sub = warp % JW;
+  if (np == 0) return;
   const long long rf = (long long)record_floats(MT, D);
   // piece 0 is slot 1 of CTA c, piece i slot 0 of CTA c + i
   const float *p0 = a.part + ((long long)c * 2 + 1) * rf, *p1 = a.part + (long long)c * 2 * rf;
-  float M = -INFINITY, L = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  if (r < rows) {
-    for (int b = sub * BATCH; b < np; b += JW * BATCH) {
-      float m[BATCH], l[BATCH], v[BATCH][E];
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-        if (b + i < np) {
-          const float *p = b + i == 0 ? p0 : p1 + (b + i) * 2 * rf;
-          m[i] = p[MT * D + r];
-          l[i] = p[MT * D + MT + r];
-          if constexpr (D == 128) {
-            const float4 t = *reinterpret_cast<const float4 *>(p + r * D + 4 * lane);
-            v[i][0] = t.x; v[i][1] = t.y; v[i][2] = t.z; v[i][3] = t.w;
-          } else {
-            const float2 t = *reinterpret_cast<const float2 *>(p + r * D + 2 * lane);
-            v[i][0] = t.x; v[i][1] = t.y;
-          }
-        }
-      }
-      float mn = M;
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, m[i]);
-      if (mn == -INFINITY) mn = 0.f;  // nothing seen yet: every factor below is 0
-      float f = ex2(M - mn);
-      L *= f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        f = ex2(m[i] - mn);
-        L += f * l[i];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f * v[i][e];
-      }
-      M = mn;
-    }
-  }
-  if constexpr (JW > 1) {
-    if (lane == 0) {
-      sh[warp][32 * E] = L == 0.f ? -INFINITY : M;  // a warp without mass has no say in the maximum
-      sh[warp][32 * E + 1] = L;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sh[warp][E * lane + e] = o[e];
-    __syncthreads();
-    if (sub != 0) return;
-    float mw[JW], mn = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < JW; ++w) {
-      mw[w] = sh[warp + w][32 * E];
-      mn = fmaxf(mn, mw[w]);
-    }
-    if (mn == -INFINITY) mn = 0.f;
-    L = 0.f;
+  for (int r0 = blockIdx.y * RW; r0 < rows; r0 += gridDim.y * RW) {
+    const int r = r0 + warp / JW;
+    float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
+    if (r < rows) {
+      for (int b = sub * BATCH; b < np; b += JW * BATCH) {
+        float m[BATCH], l[BATCH], v[BATCH][E];
 #pragma unroll
-    for (int w = 0; w < JW; ++w) {
-      const float f = mw[w] == -INFINITY && sh[warp + w][32 * E + 1] == 0.f ? 0.f : ex2(mw[w] - mn);
-      L += f * sh[warp + w][32 * E + 1];
+        for (int i = 0; i < BATCH; ++i) {
+          m[i] = -INFINITY;
+          l[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += f * sh[warp + w][E * lane + e];
+          for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+          if (b + i < np) {
+            const float *p = b + i == 0 ? p0 : p1 + (b + i) * 2 * rf;
+            m[i] = p[MT * D + r];
+            l[i] = p[MT * D + MT + r];
+            if constexpr (D == 128) {
+              const float4 t = *reinterpret_cast<const float4 *>(p + r * D + 4 * lane);
+              v[i][0] = t.x; v[i][1] = t.y; v[i][2] = t.z; v[i][3] = t.w;
+            } else {
+              const float2 t = *reinterpret_cast<const float2 *>(p + r * D + 2 * lane);
+              v[i][0] = t.x; v[i][1] = t.y;
+            }
+          }
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, m[i]);
+        if (mn == -INFINITY) mn = 0.f;  // nothing seen yet: every factor below is 0
+        float f = ex2(M - mn);
+        L *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          f = ex2(m[i] - mn);
+          L += f * l[i];
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += f * v[i][e];
+        }
+        M = mn;
+      }
     }
-    M = mn;
-  }
-  if (r >= rows) return;
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // nothing seen: zeros; a NaN stays
-  const int tok = h.y + (gr + r) / a.G, head = h.z * a.G + (gr + r) % a.G;
-  I *op = static_cast<I *>(a.o) + tok * a.o_tok + head * a.o_head + E * lane;
+    if constexpr (JW > 1) {
+      if (lane == 0) {
+        sh[warp][32 * E] = L == 0.f ? -INFINITY : M;  // a warp without mass has no say in the maximum
+        sh[warp][32 * E + 1] = L;
+      }
 #pragma unroll
-  for (int e = 0; e < E; e += 2) st2(op + e, o[e] * inv, o[e + 1] * inv);
-  if (a.lse && lane == 0) a.lse[(long long)tok * a.Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      for (int e = 0; e < E; ++e) sh[warp][E * lane + e] = o[e];
+      __syncthreads();
+      float mw[JW], mn = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < JW; ++w) {
+        mw[w] = sh[w][32 * E];
+        mn = fmaxf(mn, mw[w]);
+      }
+      if (mn == -INFINITY) mn = 0.f;
+      L = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < JW; ++w) {
+        const float f = mw[w] == -INFINITY && sh[w][32 * E + 1] == 0.f ? 0.f : ex2(mw[w] - mn);
+        L += f * sh[w][32 * E + 1];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += f * sh[w][E * lane + e];
+      }
+      M = mn;
+      __syncthreads();  // all have read
+    }
+    if (r >= rows || sub != 0) continue;
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // nothing seen: zeros; a NaN stays
+    const int tok = h.y + (gr + r) / a.G, head = h.z * a.G + (gr + r) % a.G;
+    I *op = static_cast<I *>(a.o) + tok * a.o_tok + head * a.o_head + E * lane;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) st2(op + e, o[e] * inv, o[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[(long long)tok * a.Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
 }
 
 namespace {
@@ -724,11 +730,15 @@ cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CU
 namespace {
 template <typename I, int D> cudaError_t launch_join(const PagedArgs &a, int MT, int ctas, int items, cudaStream_t st) {
   const int n = items < ctas ? items : ctas;  // cut items at most
+  // Row blocks of an item, each of which walks over rows: in all as many as there is room for at once, since starting a
+  // block costs more than a row (one sequence, 64 new tokens, 16 items of 256 rows: 43 us with 32 blocks to an item, 35
+  // with 64, 38 with 256; 32 new tokens, 8 items: 29 us with 64, 20 with 256).
+  const int rows = std::min(MT, std::max(16, 152 * 8 / n));
   // few items: many pieces each (8 new tokens of 8 sequences, fp32, 32 items on 304 CTAs: 14.8 us with four warps to a
-  // row, 18.3 with one; 512 new tokens, 64 items of 256 rows on 152 CTAs: 34 us with four, 21 with one)
-  if (items * 8 <= ctas) return launch_pdl(attn_join_kernel<I, D, 8>, dim3(n, MT), dim3(256), 0, st, a, MT, ctas);
-  if (items * 4 <= ctas) return launch_pdl(attn_join_kernel<I, D, 4>, dim3(n, MT), dim3(128), 0, st, a, MT, ctas);
-  return launch_pdl(attn_join_kernel<I, D, 1>, dim3(n, (MT + 3) / 4), dim3(128), 0, st, a, MT, ctas);
+  // row, 18.3 with one)
+  if (items * 8 <= ctas) return launch_pdl(attn_join_kernel<I, D, 8>, dim3(n, rows), dim3(256), 0, st, a, MT, ctas);
+  if (items * 4 <= ctas) return launch_pdl(attn_join_kernel<I, D, 4>, dim3(n, rows), dim3(128), 0, st, a, MT, ctas);
+  return launch_pdl(attn_join_kernel<I, D, 1>, dim3(n, std::min((MT + 3) / 4, 32)), dim3(128), 0, st, a, MT, ctas);
 }
 }  // namespace
 

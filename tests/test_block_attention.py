@@ -175,6 +175,18 @@ def test_many_sequences(N, q, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("seqs,Hkv,G", [
+    ([(20, 3000), (20, 2500), (19, 1777), (3, 900)], 4, 4),     # a few 256-row items in many pieces, more rows than blocks
+    ([(130, 1300), (200, 700), (64, 64), (90, 2222)], 8, 4),    # many items in few pieces
+])
+def test_joins_of_tall_items(seqs, Hkv, G):
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make(seqs, BF, 128, Hkv, G, 64, seed=Hkv)
+    o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), return_lse=True)
+    close(o, lse, x, qs, 128 ** -0.5)
+
+
+@gpu
 def test_peaked_and_growing_logits():
     """Logits that grow along the context (the maximum rises at every step) and by far more than fp32's exponent range
     would bear without it."""
