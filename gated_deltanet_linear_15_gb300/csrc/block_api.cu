@@ -211,7 +211,8 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   TRY(need_ptr(kv_lens, "kv_lens"));
   const AttnPlan p = attn_plan(s);
   if (!ws || ws_bytes < p.total) return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.total, ws ? ws_bytes : (size_t)0);
-  TRY(need_aligned(ws, "workspace"));
+  // a cut item's record leaves in 32-byte stores (attn_chunk_tc.cu); every part of the workspace is a multiple of that
+  if (reinterpret_cast<uintptr_t>(ws) & 31) return fail(GDN_ERR_INVALID_ARG, "workspace is not 32-byte aligned");
   // a CTA reads queries and cache rows after another wrote its outputs
   if (o == q || o == k || o == v) return fail(GDN_ERR_INVALID_ARG, "o is one of the inputs");
   const Stream st = (Stream)stream;

@@ -361,6 +361,13 @@ def test_c_entry_refuses_pointers(lib):
     assert _call(lib, _shape(total_q=0)) == 0            # nothing to do: no launch
 
 
+@pytest.mark.parametrize("at", [0x10004, 0x10010, 0x10030])
+def test_c_entry_refuses_workspace_off_32_bytes(lib, at):
+    """The records of cut items are written 32 bytes at a time."""
+    for s in (_shape(), _shape(total_q=200, max_q=100)):   # the row kernel and the chunk kernel
+        assert _call(lib, s, w=at) == 1 and b"32-byte" in lib.gdn_last_error_string()
+
+
 @pytest.mark.parametrize("name", ["q", "k", "v"])
 def test_c_entry_refuses_output_over_input(lib, name):
     """Other CTAs still read what one has written over."""
