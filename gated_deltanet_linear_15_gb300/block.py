@@ -40,7 +40,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, max_q: 
     """Causal attention of new tokens over a paged cache that already holds their keys and values.
 
     q [new tokens, heads, D]; k_cache, v_cache [pages, page_size, kv heads, D] (any strides with contiguous features);
-    page_table int32 [sequences, pages]; kv_lens int32 [sequences], the tokens of each sequence with the new ones;
+    page_table int32 [sequences, pages] (one row may be expanded over all sequences); kv_lens int32 [sequences], the tokens of each sequence with the new ones;
     cu_q int32 [sequences + 1], where each sequence's new tokens begin in q (None: as many for each).  max_q: the most
     new tokens of a sequence, if known on the host (it only picks the kernel).  window > 0: a query sees that many
     keys.  Returns o like q, or (o, lse) with lse fp32 [new tokens, heads]; a query without keys has o = 0 and

@@ -47,7 +47,7 @@ int check_paged(const gdn_paged_shape *s) {
   if (!pow2(s->page_size) || s->page_size < 16 || s->page_size > 4096)
     return fail(GDN_ERR_UNSUPPORTED, "page_size must be a power of two from 16 to 4096 (got %d)", s->page_size);
   if (s->num_pages < 1 || s->max_pages < 0) return fail(GDN_ERR_INVALID_ARG, "need num_pages >= 1, max_pages >= 0");
-  if (s->max_pages > 0 && s->num_seqs > 1 && s->table_stride < s->max_pages)
+  if (s->max_pages > 0 && s->num_seqs > 1 && s->table_stride != 0 && s->table_stride < s->max_pages)
     return fail(GDN_ERR_INVALID_ARG, "table_stride is smaller than max_pages");
   return GDN_OK;
 }

@@ -117,6 +117,8 @@ void page_table(const Tensor &t) {
     bad("page_table must be an int32 CUDA tensor [sequences, pages] with contiguous rows");
   here(t, "page_table");
 }
+// of a table's rows, as it is (0 where one row is expanded over all sequences); one row alone may have any
+int64_t table_stride(const Tensor &t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 void angle_table(const Tensor &t) {
   here(t, "table");
   if (t.dim() != 3 || t.size(2) != 2 || t.scalar_type() != at::kFloat || !t.is_contiguous())
@@ -158,7 +160,7 @@ gdn_paged_shape paged_shape(const Tensor &q, const Tensor &k, const Tensor &v, c
   s.num_pages = fits(k.size(0), "the number of pages");
   s.page_size = fits(k.size(1), "the page size");
   s.max_pages = fits(table.size(1), "the width of page_table");
-  s.table_stride = std::max<int64_t>(table.stride(0), s.max_pages);
+  s.table_stride = table_stride(table);
   s.q_tok = q.stride(0);
   s.q_head = q.stride(1);
   s.k_page = k.stride(0);
@@ -332,7 +334,7 @@ gdn_pages_shape pages_shape(const Tensor &table, const Tensor &ref, int page_siz
   s.max_pages = fits(table.size(1), "the width of page_table");
   s.num_pages = fits(ref.numel(), "the number of pages");
   s.page_size = page_size;
-  s.table_stride = std::max<int64_t>(table.stride(0), s.max_pages);
+  s.table_stride = table_stride(table);
   return s;
 }
 Tensor pages_workspace(const gdn_pages_shape &s, int m, const Tensor &t) {

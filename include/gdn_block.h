@@ -48,7 +48,7 @@ typedef struct {
                                /* picks the kernel)                                            */
   int window;                  /* attention: keys a query sees, itself included; 0: no limit   */
   float scale;                 /* attention: logits are scale * q . k                          */
-  int64_t table_stride;        /* of page_table rows                                           */
+  int64_t table_stride;        /* of page_table rows; 0: one row for all sequences (read only)  */
   int64_t q_tok, q_head;       /* strides of q: token, head                                    */
   int64_t k_page, k_tok, k_head; /* strides of k_cache: page, slot, head                       */
   int64_t v_page, v_tok, v_head; /* strides of v_cache                                         */

@@ -245,6 +245,24 @@ def test_bad_device_data_stays_in_bounds():
 
 
 @gpu
+@pytest.mark.parametrize("N,q", [(5, 1), (40, 3), (3, 90)])
+def test_one_table_row_for_all_sequences(N, q):
+    """An expanded row is read with its stride of 0.  The rows behind it hold other pages of the pool, so that reading them
+    instead would stay in bounds and show."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(q, 200 + n) for n in range(N)], BF, 128, 1, 2, 16, seed=N)
+    x["kv_lens"] = torch.clamp(x["kv_lens"], max=x["kv_lens"][0])
+    full = x["page_table"]
+    for row in (full[:1], full[1:2]):
+        want = g.paged_attention(**dict(x, page_table=row.repeat(N, 1)), max_q=q)
+        assert torch.equal(g.paged_attention(**dict(x, page_table=row.expand(N, -1)), max_q=q), want)
+    close(*g.paged_attention(**dict(x, page_table=full[:1].expand(N, -1)), max_q=q, return_lse=True),
+          dict(x, page_table=full[:1].expand(N, -1)), qs, 128 ** -0.5)
+    with pytest.raises(RuntimeError):   # rows that overlap one another
+        g.paged_attention(**dict(x, page_table=full.as_strided((2, full.shape[1]), (1, 1)), kv_lens=x["kv_lens"][:2], q=x["q"][:2 * q]), max_q=q)
+
+
+@gpu
 def test_non_finite_values_reach_only_their_readers():
     """A NaN in one cached value of an early token reaches every query; infinities and NaN behind a window, in later
     tokens' tiles or in free slots reach none."""
@@ -344,6 +362,11 @@ def test_c_entry_refuses_shapes(lib, kw, code):
     assert _call(lib, s) == code
     assert lib.gdn_last_error_string() != b""
     assert lib.gdn_paged_attn_workspace_size(ctypes.byref(s)) == 0
+
+
+def test_c_entry_takes_one_row_for_all(lib):
+    assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(table_stride=0))) > 0
+    assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(table_stride=-10))) == 0
 
 
 def test_c_entry_refuses_pointers(lib):

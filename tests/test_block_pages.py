@@ -191,6 +191,25 @@ def test_binding_refuses():
         g.compact_pages(table, ref.cpu())
 
 
+@gpu
+def test_tables_whose_rows_share_memory_are_refused():
+    """The page functions write rows, so an expanded row or rows that overlap are refused; nothing is written."""
+    import gated_deltanet_linear_15_gb300 as g
+    whole, lens, ref = ints([[-1] * 4] * 6), ints([0] * 3), ints([0] * 8)
+    pool = torch.zeros(8, 16, device=DEV)
+    for table in (whole[:1].expand(3, -1), whole.as_strided((3, 4), (2, 1))):
+        for call in (lambda: g.extend_pages(table, lens, ref, ints([0, 1, 2]), ints([5, 5, 5]), 16),
+                     lambda: g.fork_pages(table, lens, ref, ints([0]), ints([1]), [pool], 16),
+                     lambda: g.free_pages(table, lens, ref, ints([2])), lambda: g.compact_pages(table, ref, [pool]),
+                     lambda: g.compact_pages(table, ref, [pool], inplace=False)):
+            with pytest.raises(RuntimeError, match="table_stride"):
+                call()
+    assert (whole == -1).all() and not lens.any() and not ref.any()
+    one = whole.as_strided((1, 4), (1, 1))    # a single row has no stride to speak of
+    assert g.extend_pages(one, lens[:1], ref, ints([0]), ints([20]), 16).tolist() == [1]
+    assert one.tolist() == [[0, 1, -1, -1]]
+
+
 # ------------------------------------------------------------------ refusals of the C entry points (no GPU needed)
 def _shape(**kw):
     s = _lib.GdnPagesShape()

@@ -249,6 +249,20 @@ def test_append_leaves_out_what_has_no_place():
 
 
 @gpu
+def test_append_through_one_table_row():
+    """Sequences that share one (expanded) table row, at positions of their own; the rows behind it are other pages."""
+    import gated_deltanet_linear_15_gb300 as g
+    qs, ks, table, kc, vc, qkv = _append_case([(2, 2 + 5 * n) for n in range(9)], BF, 64, 2, 1, 16, False, seed=3)
+    q, k, v = qkv.split([2, 1, 1], 1)
+    cs, table = table_ref(64, 64).float().to(DEV), table.to(DEV)
+    lens = torch.tensor(ks, dtype=torch.int32, device=DEV)
+    kc2, vc2 = kc.clone(), vc.clone()
+    a = g.rotary_append(q, k, v, cs, kc, vc, table[-1:].repeat(9, 1), lens)
+    b = g.rotary_append(q, k, v, cs, kc2, vc2, table[-1:].expand(9, -1), lens)
+    assert torch.equal(a, b) and torch.equal(kc, kc2) and torch.equal(vc, vc2)
+
+
+@gpu
 def test_many_equal_sequences_without_cu():
     import gated_deltanet_linear_15_gb300 as g
     seqs = [(2, 2 + 3 * n) for n in range(50)]
