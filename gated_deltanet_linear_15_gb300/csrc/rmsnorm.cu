@@ -223,7 +223,9 @@ template <typename I> __global__ void __launch_bounds__(256) norm_fwd_any_kernel
       if (a.group)
         for (int i = g0 + threadIdx.x; i < g0 + gsz; i += 256) static_cast<uint8_t *>(a.y)[r * a.y_row + i] = fp8x1(y_at(i) * inv);
     }
-    // outputs that may take an input's place are written once nothing of the feature is read any more
+    // h_out may take an input's place: without groups a feature is read and written by one thread, but the last group's
+    // reads are those of other threads
+    if (a.group && a.h_out) __syncthreads();
     for (int i = threadIdx.x; i < a.D; i += 256) {
       const float h = tof(x[i]) + (q ? tof(q[i]) : 0.f), y = h * rstd * (a.weight[i] + a.off);
       if (a.h_out) static_cast<I *>(a.h_out)[r * a.h_row + i] = fromf<I>(h);

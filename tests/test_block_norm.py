@@ -104,6 +104,23 @@ def test_fp8_edges():
 
 
 @gpu
+@pytest.mark.parametrize("T,D,group", [(700, 256, 128), (300, 512, 128), (50, 20096, 128), (300, 640, 128), (300, 257, 0)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_fp8_in_place_off_the_16_byte_path(T, D, group, dtype):
+    """Rows that begin one element off a 16-byte boundary, h in residual's place: the same bits as with an h of its own."""
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(D)
+    x, w = rand(gen, T, D + 1, dtype=dtype)[:, 1:], 1 + 0.2 * rand(gen, D)
+    r = rand(gen, T, D + 1, dtype=dtype)
+    want = g.rms_norm(x, w, r[:, 1:], fp8=True, group=group)
+    for _ in range(5):
+        again = r.clone()[:, 1:]
+        got = g.rms_norm(x, w, again, fp8=True, group=group, inplace=True)
+        assert torch.equal(again, want.h) and torch.equal(got.scale, want.scale)
+        assert torch.equal(got.y.view(torch.uint8), want.y.view(torch.uint8))
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_with_strides_and_odd_alignment(dtype):
     import gated_deltanet_linear_15_gb300 as g
