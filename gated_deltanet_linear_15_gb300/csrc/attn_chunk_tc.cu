@@ -205,16 +205,19 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
   *dead = 1;
   return false;
 }
-// weights of tile x are in TMEM: four softmax warps arrive, the issuing warp waits.  A hardware barrier, which answers in
-// tens of cycles where an mbarrier, in the shared memory that the products read at full rate, takes about 200.  Every
-// warp passes it once per block whatever happened to its bounded waits, so it cannot hang.
-__device__ __forceinline__ void weights_ready(int x) { asm volatile("bar.arrive %0, 160;\n" ::"r"(2 + x) : "memory"); }
+// weights of tile x are in TMEM: four softmax warps and the tile's issuing warp meet.  A hardware barrier, which answers in
+// tens of cycles where an mbarrier, in the shared memory that the products read at full rate, takes about 200.  Every warp
+// passes it once per block whatever happened to its bounded waits, and both sides wait: a softmax warp that only arrived
+// could, once its waits have run out, arrive again in the same generation and leave the others one short for ever.  (It has
+// nothing to do before the products that the issuing warp starts here, so waiting costs it nothing.)
+__device__ __forceinline__ void weights_ready(int x) { asm volatile("bar.sync %0, 160;\n" ::"r"(2 + x) : "memory"); }
 __device__ __forceinline__ void weights_wait(int x) { asm volatile("bar.sync %0, 160;\n" ::"r"(2 + x) : "memory"); }
 
 // The issuing warps of the two tiles take turns, one block's products each, so that one tile's softmax runs under the
 // other's products; without turns the tiles fall into step in many CTAs, and both halves of the work wait for each other.
-// Handed over by hardware barriers too; an issue returns when all but a product or two are done, so the tensor core sees
-// hardly a gap.
+// Handed over by hardware barriers too (a warp that gave its turn waits for the other's before it gives again, so one
+// arrival per generation is sure); an issue returns when all but a product or two are done, so the tensor core sees hardly a
+// gap.
 __device__ __forceinline__ void turn_wait(int x) { asm volatile("bar.sync %0, 64;\n" ::"r"(4 + x) : "memory"); }
 __device__ __forceinline__ void turn_give(int x) { asm volatile("bar.arrive %0, 64;\n" ::"r"(4 + x) : "memory"); }
 

@@ -404,6 +404,49 @@ def test_c_entry_refuses_group_beyond_16_bits(lib):
     assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(num_heads=65535, num_kv_heads=1, total_q=2))) > 0
 
 
+def _can_stall(threads, programs):
+    """Whether warps that run `programs`, lists of ("sync" | "arrive", barrier), can come to stand: every order is tried.  A
+    barrier's generation ends when `threads[barrier]` have arrived, whoever they are; a sync leaves with its generation."""
+    start = (tuple((0, False) for _ in programs), tuple(0 for _ in threads))
+    seen, todo = {start}, [start]
+    while todo:
+        warps, count = todo.pop()
+        moved = False
+        for w, (pc, blocked) in enumerate(warps):
+            if blocked or pc == len(programs[w]):
+                continue
+            moved = True
+            kind, b = programs[w][pc]
+            now, full = list(warps), count[b] + 32 == threads[b]
+            now[w] = (pc + 1, False) if kind == "arrive" or full else (pc, True)
+            if full:
+                now = [(p + 1, False) if held and programs[v][p][1] == b else (p, held) for v, (p, held) in enumerate(now)]
+            state = (tuple(now), tuple(0 if i == b and full else c + 32 * (i == b) for i, c in enumerate(count)))
+            if state not in seen:
+                seen.add(state)
+                todo.append(state)
+        if not moved and any(pc < len(p) for (pc, _), p in zip(warps, programs)):
+            return True
+    return False
+
+
+def test_barriers_hold_after_an_expired_wait():
+    """The chunk kernel's hand-overs by hardware barrier, with the bounded waits between them run out (so that nothing else
+    orders the warps): no order of the warps may leave one waiting for ever."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(_lib.__file__), "csrc", "attn_chunk_tc.cu")).read()
+    op = {n: (k, int(c)) for n, k, c in
+          re.findall(r"void (weights_ready|weights_wait|turn_wait|turn_give)\(int x\) \{ asm volatile\(\"bar\.(\w+) %0, (\d+);", src)}
+    assert len(op) == 4 and op["weights_ready"][1] == op["weights_wait"][1] and op["turn_wait"][1] == op["turn_give"][1]
+    assert _can_stall([160], [[("arrive", 0)] * 3] * 4 + [[("sync", 0)] * 3])   # the model sees a second arrival
+    ready, wait = op["weights_ready"][0], op["weights_wait"][0]
+    assert not _can_stall([op["weights_wait"][1]], [[(ready, 0)] * 3] * 4 + [[(wait, 0)] * 3])
+    give, turn = op["turn_give"][0], op["turn_wait"][0]
+    first = [(turn, 0), (give, 1)] * 4 + [(turn, 0)]
+    assert not _can_stall([op["turn_wait"][1]] * 2, [first, [(give, 0)] + [(turn, 1), (give, 0)] * 4])
+
+
 def test_header_and_binding_agree(lib):
     import os
     import re
