@@ -52,6 +52,7 @@ struct Bars {
   uint64_t full[8], empty[8], q_full[2], s_full[2], o_full[2], drain[2];
   uint32_t tmem;
   int dead;
+  uint3 stages;  // the loader's next stage and its parity at the end, and how many before it have been filled
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -332,18 +333,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
       __syncwarp();
       more = cursor_advance(a, cur, n);
     }
-    // a CTA that gives up waits (bounded) for the copies in flight before its shared memory goes
-    if (*dead) {
-      const uint32_t k = min(issued, (uint32_t)C::STAGES);
-      for (uint32_t i = 0; i < k; ++i) {
-        if (st == 0) {
-          st = C::STAGES;
-          ph ^= 1;
-        }
-        --st;
-        mbar_wait(smem_u32(&bars.full[st]), ph, nullptr, 0, 1u << 20);
-      }
-    }
+    if (lane == 0) bars.stages = make_uint3(st, ph, min(issued, (uint32_t)C::STAGES));
   } else if (warp != 11) {
     // ------------------------------------------------------------ products of tile x
     const int x = (warp - 8) >> 1;
@@ -437,11 +427,6 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
       more = cursor_advance(a, cur, n);
     }
     if (x == 0) turn_wait(0);  // the turn that was given last
-    if (*dead) {  // products in flight end before TMEM goes
-      if (elect1()) mma_commit(smem_u32(&bars.drain[x]));
-      __syncwarp();
-      mbar_wait(smem_u32(&bars.drain[x]), 0, nullptr, 0, 1u << 20);
-    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;\n");
@@ -674,6 +659,27 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   fence_before();
   __syncthreads();
   fence_after();
+  // A CTA in which a wait ran out waits (bounded) for what is in flight before its memory goes, once every role has ended:
+  // none starts a copy or a product any more, and all see the same `dead`.
+  if (bars.dead) {
+    if (warp == 9) {  // the copies of the stages filled last
+      uint32_t st = bars.stages.x, ph = bars.stages.y;
+      for (uint32_t i = 0; i < bars.stages.z; ++i) {
+        if (st == 0) {
+          st = C::STAGES;
+          ph ^= 1;
+        }
+        --st;
+        mbar_wait(smem_u32(&bars.full[st]), ph, nullptr, 0, 1u << 20);
+      }
+    } else if (warp == 8 || warp == 10) {  // the products of the tile
+      const int x = (warp - 8) >> 1;
+      if (elect1()) mma_commit(smem_u32(&bars.drain[x]));
+      __syncwarp();
+      mbar_wait(smem_u32(&bars.drain[x]), 0, nullptr, 0, 1u << 20);
+    }
+    __syncthreads();
+  }
   if (tid == 0) a.status[cta] = bars.dead;
   if (warp == 8) tmem_dealloc(tmem, TM_COLS);
 }
