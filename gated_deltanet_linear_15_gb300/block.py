@@ -44,13 +44,14 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, max_q: 
     cu_q int32 [sequences + 1], where each sequence's new tokens begin in q (None: as many for each).  max_q: the most
     new tokens of a sequence, if known on the host (it only picks the kernel).  window > 0: a query sees that many
     keys.  Returns o like q, or (o, lse) with lse fp32 [new tokens, heads]; a query without keys has o = 0 and
-    lse = -inf.  workspace: a tensor to use as scratch memory, 32-byte aligned.  Decoding is the case of one new token per sequence."""
+    lse = -inf.  workspace: a tensor to use as scratch memory (contiguous, 32-byte
+    aligned, refused when it is too small).  Decoding is the case of one new token per sequence."""
     return _py.paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q, scale, window, return_lse, out, workspace)
 
 
 def paged_attention_status(q, k_cache, v_cache, page_table, kv_lens, workspace, cu_q=None, max_q: int = 0) -> int:
-    """Status word of the last ``paged_attention`` call with these arguments and this workspace (0: clean; see
-    gdn_paged_attn_status).  Synchronises the stream."""
+    """Status word of the last ``paged_attention`` call with these arguments and this workspace, which that call must have
+    been given (0: clean; see gdn_paged_attn_status).  Synchronises the stream."""
     return _py.paged_attention_status(q, k_cache, v_cache, page_table, kv_lens, workspace, cu_q, max_q)
 
 

@@ -177,7 +177,7 @@ __device__ __forceinline__ bool cursor_advance(const PagedArgs &a, Cursor &share
 
 // Bounded wait.  The plain test comes first: when the phase is complete already, as it mostly is for the issuing warps, it
 // answers sooner than the test that may suspend.  Gives up soon when another role of the CTA has.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *dead, uint32_t limit = WAIT_LIMIT) {
   const uint32_t b = smem_u32(bar);
   uint32_t done;
   asm volatile(
@@ -190,7 +190,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
       : "r"(b), "r"(parity)
       : "memory");
   if (done) return true;
-  for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
+  for (uint32_t it = 0; it < limit; ++it) {
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
@@ -253,6 +253,16 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
+  }
+  if (a.expire) {  // before TMEM is taken or any copy asked for
+    pdl_trigger();
+    pdl_wait();
+    if (tid == 0) {
+      a.hdr[cta] = make_int4(0, 0, 0, 0);
+      wait(&bars.full[0], 0, dead, 1024);
+      a.status[cta] = *dead;
+    }
+    return;
   }
   if (warp == 8) {
     tmem_alloc(smem_u32(&bars.tmem), TM_COLS);

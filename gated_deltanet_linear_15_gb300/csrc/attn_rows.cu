@@ -96,8 +96,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap
 }
 // Bounded wait that polls with the plain test: a slice is mostly there or about to be, and the test that may suspend costs
 // more than it saves (64 sequences of 512 .. 16384 tokens: 336 us against 345 us).
-__device__ __forceinline__ bool slice_wait(uint32_t bar, uint32_t parity) {
-  for (uint32_t it = 0; it < (1u << 25); ++it) {
+__device__ __forceinline__ bool slice_wait(uint32_t bar, uint32_t parity, uint32_t limit = 1u << 25) {
+  for (uint32_t it = 0; it < limit; ++it) {
     uint32_t done;
     asm volatile(
         "{\n"
@@ -152,6 +152,13 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
   }
   pdl_trigger();
   pdl_wait();
+  if (a.expire) {  // no copy has been asked for
+    if (tid == 0) {
+      a.hdr[cta] = make_int4(0, 0, 0, 0);
+      a.status[cta] = slice_wait(smem_u32(&full[0][0]), 0, 1024) ? 0 : 4;
+    }
+    return;
+  }
   bool cut = false;  // this CTA's header is written
   int expired = 0;   // a bounded wait ran out
   SeqInfo *seqs = reinterpret_cast<SeqInfo *>(smem);  // the search uses the rings' memory

@@ -37,9 +37,10 @@ int need_aligned(const void *p, const char *name) {
   } while (0)
 
 // ------------------------------------------------------------------ paged shapes
-int check_paged(const gdn_paged_shape *s) {
+int check_paged(const gdn_paged_shape *s, bool attn) {
   if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
-  if (s->reserved) return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
+  if (s->reserved && !(attn && (uint32_t)s->reserved == (uint32_t)GDN_DEBUG_WAIT_TIMEOUT))
+    return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
   if (s->dtype != GDN_BF16 && s->dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "unknown dtype");
   if (s->num_seqs < 0 || s->total_q < 0) return fail(GDN_ERR_INVALID_ARG, "need num_seqs >= 0, total_q >= 0");
   if (s->num_heads < 1 || s->num_kv_heads < 1 || s->num_heads % s->num_kv_heads)
@@ -53,7 +54,7 @@ int check_paged(const gdn_paged_shape *s) {
 }
 
 int check_attn(const gdn_paged_shape *s) {
-  TRY(check_paged(s));
+  TRY(check_paged(s, true));
   if (s->head_dim != 64 && s->head_dim != 128) return fail(GDN_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", s->head_dim);
   if (s->window < 0) return fail(GDN_ERR_INVALID_ARG, "window must be >= 0");
   if (s->max_q < 0) return fail(GDN_ERR_INVALID_ARG, "max_q must be >= 0");
@@ -229,6 +230,7 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   a.log2P = ilog2(s->page_size);
   a.num_pages = s->num_pages; a.max_pages = s->max_pages; a.window = s->window;
   a.scale_log2 = s->scale * 1.4426950408889634f;
+  a.expire = s->reserved != 0;
   a.hdr = static_cast<int4 *>(ws);
   a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.off_part);
   a.status = reinterpret_cast<int *>(static_cast<char *>(ws) + p.off_status);
@@ -328,7 +330,7 @@ int gdn_rotary(const gdn_rotary_shape *s, const void *q, const void *k, const fl
 int gdn_rotary_append(const gdn_paged_shape *s, const void *q, const void *k, const void *v, const float *table,
                       void *k_cache, void *v_cache, const int32_t *page_table, const int32_t *cu_q,
                       const int32_t *kv_lens, void *q_out, gdn_stream_t stream) {
-  TRY(check_paged(s));
+  TRY(check_paged(s, false));
   if (s->head_dim < 2 || s->rot < 2 || s->rot % 2 || s->rot > s->head_dim)
     return fail(GDN_ERR_INVALID_ARG, "need an even rot with 2 <= rot <= head_dim (got rot %d, head_dim %d)", s->rot, s->head_dim);
   if (s->head_dim > 65536 || (long long)s->num_heads * s->head_dim > (1 << 26)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");

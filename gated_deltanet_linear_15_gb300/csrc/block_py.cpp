@@ -134,6 +134,11 @@ Tensor like(const Tensor *out, const Tensor &q) {
 }
 void *stream(const Tensor &t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
 Tensor bytes(size_t n, const Tensor &t) { return at::empty({(int64_t)n}, t.options().dtype(at::kByte)); }
+// a workspace that the caller gives: its status word is read later, so it is used as it is or refused
+void scratch(const Tensor &t, size_t need) {
+  here(t, "workspace");
+  if (!t.is_contiguous() || t.nbytes() < need) bad("workspace must be contiguous and have at least " + std::to_string(need) + " bytes");
+}
 int32_t *i32(const Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); }
 const int32_t *i32(const Tensor *t) { return t ? static_cast<const int32_t *>(t->data_ptr()) : nullptr; }
 const void *ptr(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
@@ -204,8 +209,8 @@ PyObject *paged_attention(PyObject *const *a) {
   if (!need) check(GDN_ERR_INVALID_ARG, "gdn_paged_attn_workspace_size");
   Tensor lse;
   if (truth(a[9])) lse = at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat));
-  if (given) here(*given, "workspace");
-  const Tensor ws = given && given->is_contiguous() && given->nbytes() >= need ? *given : bytes(need, q);
+  if (given) scratch(*given, need);
+  const Tensor ws = given ? *given : bytes(need, q);
   check(api.paged_attn_fwd(&s, q.data_ptr(), k.data_ptr(), v.data_ptr(), i32(table), i32(cu), i32(lens), o.data_ptr(),
                            lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(),
                            (gdn_stream_t)stream(q)),
@@ -222,6 +227,9 @@ PyObject *paged_attention_status(PyObject *const *a) {
   s.scale = 1.f;
   s.o_tok = q.size(1) * q.size(2);
   s.o_head = q.size(2);
+  const size_t need = api.paged_attn_workspace_size(&s);
+  if (!need) check(GDN_ERR_INVALID_ARG, "gdn_paged_attn_workspace_size");
+  scratch(ws, need);
   return PyLong_FromLong(api.paged_attn_status(&s, ws.data_ptr(), (gdn_stream_t)stream(q)));
 }
 

@@ -28,6 +28,7 @@ struct PagedArgs {
   int Hq, Hkv, G, log2P, num_pages, max_pages, window;
   float scale_log2;         // scale * log2(e): the softmax runs in powers of two
   int *status;              // one word per CTA: 0, or 4 when a bounded wait of it ran out
+  int expire;               // test hook: one wait that runs out, and nothing else
   // cut items: headers [C] and records [C][2][MT * (D + 2)] (sums [MT][D], maxima [MT], masses [MT])
   int4 *hdr;
   float *part;

@@ -58,7 +58,7 @@ typedef struct {
   int rot;                     /* append: leading features of q and k that turn, even, <= D    */
   int interleaved;             /* append: pairs (2i, 2i + 1) instead of (i, i + rot / 2)       */
   int table_rows;              /* append: positions of the rotary table                        */
-  int reserved;                /* must be 0                                                    */
+  int reserved;                /* must be 0; attention: or GDN_DEBUG_WAIT_TIMEOUT              */
 } gdn_paged_shape;
 
 /*
@@ -85,7 +85,9 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *shape, const void *q, const void *
 
 /* The status word of the last gdn_paged_attn_fwd with this shape and workspace (synchronises the stream): 0, or 4 when a
  * bounded device wait ran past its limit (that call's outputs are not reliable; gdn_device_status_code maps it), or -1 on
- * an error. */
+ * an error.  workspace: the whole one that the call was given, at least gdn_paged_attn_workspace_size bytes.  With
+ * GDN_DEBUG_WAIT_TIMEOUT in `reserved` (a test hook) a call only waits, with a short limit, for a barrier that nothing
+ * arrives at, sets the status and returns without writing its outputs. */
 int gdn_paged_attn_status(const gdn_paged_shape *shape, const void *workspace, gdn_stream_t stream);
 
 /* ------------------------------------------------------------------ rotary positions

@@ -315,6 +315,65 @@ def test_captured_in_a_graph():
     assert torch.equal(out, g.paged_attention(**x, max_q=1))
 
 
+def _raw(x, o, ws, q, **kw):
+    """The C entry's arguments for a batch of equal new lengths."""
+    s = _lib.GdnPagedShape()
+    n, (t, hq, d), kc, vc = x["kv_lens"].numel(), x["q"].shape, x["k_cache"], x["v_cache"]
+    s.num_seqs, s.total_q, s.num_heads, s.num_kv_heads, s.head_dim, s.page_size = n, t, hq, kc.shape[2], d, kc.shape[1]
+    s.num_pages, s.max_pages, s.table_stride = kc.shape[0], x["page_table"].shape[1], x["page_table"].stride(0)
+    s.dtype, s.max_q, s.scale = _lib.GDN_BF16 if x["q"].dtype == BF else _lib.GDN_FP32, q, d ** -0.5
+    (s.q_tok, s.q_head), (s.o_tok, s.o_head) = x["q"].stride()[:2], o.stride()[:2]
+    (s.k_page, s.k_tok, s.k_head), (s.v_page, s.v_tok, s.v_head) = kc.stride()[:3], vc.stride()[:3]
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return ctypes.byref(s), [t.data_ptr() for t in (x["q"], kc, vc, x["page_table"])] + [None, x["kv_lens"].data_ptr(), o.data_ptr(),
+                                                                                        None, ws.data_ptr(), ws.numel()]
+
+
+@gpu
+@pytest.mark.parametrize("q,dtype", [(1, BF), (40, BF), (3, F32)])
+def test_status_of_a_clean_call_and_of_an_expired_wait(lib, q, dtype):
+    """A call that is made to wait, with a short limit, for what never comes returns and leaves 4; the next call is clean."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(q, 300), (q, 77 + q)], dtype, 128, 2, 2, 16, seed=q)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    args = (x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["kv_lens"])
+    o, lse = g.paged_attention(**x, max_q=q, return_lse=True, workspace=ws)
+    assert g.paged_attention_status(*args, ws, max_q=q) == 0
+    close(o, lse, x, qs, 128 ** -0.5)
+    stream = torch.cuda.current_stream().cuda_stream
+    out = torch.full_like(o, 7.0)
+    ws.fill_(255)
+    shape, raw = _raw(x, out, ws, q, reserved=_lib.GDN_DEBUG_WAIT_TIMEOUT - (1 << 32))
+    assert lib.gdn_paged_attn_fwd(shape, *raw, stream) == 0
+    torch.cuda.synchronize()
+    word = lib.gdn_paged_attn_status(shape, ws.data_ptr(), stream)
+    assert word == 4 and g.gdn_device_status_code(word) == _lib.GDN_ERR_TIMEOUT and (out == 7).all()
+    assert g.paged_attention_status(*args, ws, max_q=q) == 4
+    assert torch.equal(g.paged_attention(**x, max_q=q, workspace=ws), o)
+    assert g.paged_attention_status(*args, ws, max_q=q) == 0
+
+
+@gpu
+def test_workspaces_too_small_are_refused(lib):
+    """Both calls name the bytes that are needed, instead of working with other memory or reading behind the tensor."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(1, 300)], BF, 128, 2, 2, 16)
+    args = (x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["kv_lens"])
+    need = lib.gdn_paged_attn_workspace_size(_raw(x, x["q"], x["q"], 1)[0])
+    ws = torch.zeros(2 * need, dtype=torch.uint8, device=DEV)
+    for bad in (ws[:need - 1], ws[:0], ws[::2], ws.cpu()):
+        with pytest.raises(ValueError, match="workspace"):
+            g.paged_attention(**x, max_q=1, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            g.paged_attention_status(*args, bad, max_q=1)
+    with pytest.raises(RuntimeError, match="32-byte"):
+        g.paged_attention(**x, max_q=1, workspace=ws[16:])
+    want = g.paged_attention(**x, max_q=1)
+    assert torch.equal(g.paged_attention(**x, max_q=1, workspace=ws[:need]), want)
+    assert g.paged_attention_status(*args, ws[:need], max_q=1) == 0
+
+
 @gpu
 @pytest.mark.parametrize("change", [
     dict(q=lambda t: t.half()), dict(q=lambda t: t[:, :3]), dict(q=lambda t: t.cpu()), dict(kv_lens=lambda t: t.long()),
@@ -362,6 +421,14 @@ def test_c_entry_refuses_shapes(lib, kw, code):
     assert _call(lib, s) == code
     assert lib.gdn_last_error_string() != b""
     assert lib.gdn_paged_attn_workspace_size(ctypes.byref(s)) == 0
+
+
+def test_c_entry_knows_the_debug_hook(lib):
+    hook = _lib.GDN_DEBUG_WAIT_TIMEOUT - (1 << 32)
+    assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(reserved=hook))) > 0
+    assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(reserved=hook + 1))) == 0
+    s = _shape(reserved=hook, rot=128, table_rows=10)
+    assert lib.gdn_rotary_append(ctypes.byref(s), *[0x10000] * 10, None) == 1
 
 
 def test_c_entry_takes_one_row_for_all(lib):
