@@ -32,7 +32,8 @@ namespace {
 
 constexpr int NTHR = 384, SOFT = 256, MT = 256, BN = 128;
 constexpr float RAISED = 1099511627776.f;  // 2^40: a block's weights that sum to more have their maximum raised
-constexpr uint32_t WAIT_LIMIT = 1u << 22;
+constexpr uint32_t WAIT_LIMIT = 1u << 18;   // polls of 3.8 us when nothing comes: a second
+constexpr uint32_t DRAIN_LIMIT = 1u << 16;  // of each stage or tile after that
 
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major, bool neg_a) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((neg_a ? 1u : 0u) << 13) | ((b_mn_major ? 1u : 0u) << 16) |
@@ -680,13 +681,13 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           ph ^= 1;
         }
         --st;
-        mbar_wait(smem_u32(&bars.full[st]), ph, nullptr, 0, 1u << 20);
+        mbar_wait(smem_u32(&bars.full[st]), ph, nullptr, 0, DRAIN_LIMIT);
       }
     } else if (warp == 8 || warp == 10) {  // the products of the tile
       const int x = (warp - 8) >> 1;
       if (elect1()) mma_commit(smem_u32(&bars.drain[x]));
       __syncwarp();
-      mbar_wait(smem_u32(&bars.drain[x]), 0, nullptr, 0, 1u << 20);
+      mbar_wait(smem_u32(&bars.drain[x]), 0, nullptr, 0, DRAIN_LIMIT);
     }
     __syncthreads();
   }

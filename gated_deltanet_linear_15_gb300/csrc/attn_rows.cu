@@ -95,7 +95,7 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap
       : "memory");
 }
 // Bounded wait that polls with the plain test: a slice is mostly there or about to be, and the test that may suspend costs
-// more than it saves (64 sequences of 512 .. 16384 tokens: 336 us against 345 us).
+// more than it saves (64 sequences of 512 .. 16384 tokens: 336 us against 345 us).  The limit is about a second.
 __device__ __forceinline__ bool slice_wait(uint32_t bar, uint32_t parity, uint32_t limit = 1u << 25) {
   for (uint32_t it = 0; it < limit; ++it) {
     uint32_t done;
@@ -577,7 +577,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
   }
   if (tid == 0 && !cut) a.hdr[cta] = make_int4(0, 0, 0, 0);
   if (expired) {  // copies in flight end, if they do, before the shared memory goes
-    for (int s = 0; s < STAGES; ++s) mbar_wait(full_u + 8 * s, (uint32_t)s < st ? ph ^ 1 : ph, nullptr, 0, 1u << 18);
+    for (int s = 0; s < STAGES; ++s) mbar_wait(full_u + 8 * s, (uint32_t)s < st ? ph ^ 1 : ph, nullptr, 0, 1u << 16);
   }
   expired = __syncthreads_or(expired);
   if (tid == 0) a.status[cta] = expired ? 4 : 0;
