@@ -148,7 +148,7 @@ struct Cursor {
 // shared memory of the search
 template <int NT> struct PlanSmem {
   long long units[NT + 1], scan[NT / 32];
-  int tiles[NT + 1], scan_tiles[NT / 32];
+  int tiles[NT + 1];
 };
 
 // Finds where this CTA's range begins.  False when it has none.  Threads 0 .. NT - 1 call it (NT a power of two).
@@ -156,15 +156,21 @@ template <int NT, int MT, int BN>
 __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, PlanSmem<NT> &sm) {
   const int tid = threadIdx.x;
   // tiles of the sequences, NT equal shares of them (a thread with one sequence keeps what it read)
-  const int cs = (a.N + NT - 1) / NT;
-  const int n0 = min(a.N, tid * cs), n1 = min(a.N, n0 + cs);
-  int cnt = 0;
+  const int cs = a.N / NT + (a.N % NT > 0);
+  const int n0 = (int)min((long long)a.N, (long long)tid * cs), n1 = (int)min((long long)a.N, (long long)n0 + cs);
+  long long cnt = 0;
   for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seq_info(a, n));
-  const int inc = block_scan<NT>(cnt, sm.scan_tiles);
-  sm.tiles[tid + 1] = inc;
+  const long long inc = block_scan<NT>(cnt, sm.scan);
+  sm.tiles[tid + 1] = (int)inc;
   if (tid == 0) sm.tiles[0] = 0;
+  if (tid == NT - 1) sm.units[0] = inc;
   plan_bar<NT>();
-  const int NTILE = sm.tiles[NT];
+  // Sequences that share no tokens have no more tiles than this (each at most one that is not full).  A cu_q that goes back
+  // names tokens many times over, more tiles than 31 bits hold in the worst case: such a batch is left undone.
+  const long long most = a.N + (long long)a.total_q * a.G / MT, named = sm.units[0];
+  plan_bar<NT>();  // sm.units and sm.scan are written again
+  if (named > most || named > 0x7fffffffll - NT) return false;
+  const int NTILE = (int)named;
   // units of the tiles, NT equal shares of them
   const int ct = (NTILE + NT - 1) / NT;
   auto seek = [&](int x, int &n, int &t, SeqInfo &s) {  // tile number x of the line

@@ -63,7 +63,8 @@ typedef struct {
 
 /*
  * Attention of new tokens over the cache (causal).  The new tokens of sequence n are rows cu_q[n] .. cu_q[n+1]-1 of
- * q [total_q, Hq, D] (cu_q device int32 [N+1]; NULL: every sequence has total_q / N of them).  Query i of a
+ * q [total_q, Hq, D] (cu_q device int32 [N+1], not decreasing; NULL: every sequence has total_q / N of them; rows that no
+ * sequence names, and a batch whose cu_q goes back and names tokens many times, may be left without an output).  Query i of a
  * sequence with `ql` new tokens sits at position p = kv_lens[n] - ql + i and sees the keys at positions
  * max(0, p - window + 1) .. p, whose own keys and values the cache must hold already:
  *

@@ -245,6 +245,23 @@ def test_bad_device_data_stays_in_bounds():
 
 
 @gpu
+@pytest.mark.parametrize("N,T,max_q", [((1 << 18) + 2, 1 << 18, 1), (700, 3000, 1), (700, 3000, 3000)])
+def test_cu_q_that_names_tokens_many_times(N, T, max_q):
+    """cu_q goes to and fro, which in the first case makes more tiles than 31 bits hold: the call ends at once without touching
+    anything, and the next one is right."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make([(1, 20)], BF, 64, 1, 1, 16)
+    cu = torch.zeros(N + 1, dtype=torch.int32, device=DEV)
+    cu[1::2] = T
+    out = torch.full((T, 1, 64), 7.0, dtype=BF, device=DEV)
+    lens, table = torch.full((N,), 20, dtype=torch.int32, device=DEV), x["page_table"].repeat(N, 1)
+    g.paged_attention(torch.zeros(T, 1, 64, dtype=BF, device=DEV), x["k_cache"], x["v_cache"], table, lens, cu_q=cu, max_q=max_q,
+                      out=out)
+    assert (out == 7).all()
+    close(*g.paged_attention(**x, max_q=1, return_lse=True), x, qs, 0.125)
+
+
+@gpu
 @pytest.mark.parametrize("N,q", [(5, 1), (40, 3), (3, 90)])
 def test_one_table_row_for_all_sequences(N, q):
     """An expanded row is read with its stride of 0.  The rows behind it hold other pages of the pool, so that reading them
