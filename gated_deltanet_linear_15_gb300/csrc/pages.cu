@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
       if ((unsigned)s < (unsigned)a.S && d >= 0) {
         const int len = a.lens[s], have = pages_of(max(len, 0), a.P);
         const long long end = (long long)len + d;
-        good = len >= 0 && end <= (long long)a.W * a.P;
+        good = len >= 0 && end <= min((long long)a.W * a.P, 0x7fffffffll);  // a length has 31 bits
         if (good && len % a.P != 0 && d > 0) {  // it will write into its last page: that page has to be its own
           const int pg = a.table[s * a.ts + have - 1];
           good = (unsigned)pg < (unsigned)a.NP && a.ref[pg] == 1;

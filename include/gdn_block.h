@@ -156,7 +156,7 @@ int gdn_slots_copy(const gdn_slot_pool *pools, int num_pools, const int32_t *src
                    gdn_stream_t stream);
 
 /* Grows sequences: seqs int32 [m] (distinct), add int32 [m] tokens.  ok int32 [m] gets 1, or 0 where the sequence is
- * left as it was: a bad number, no room in its table row, a last page that is shared, or not enough free pages (once
+ * left as it was: a bad number, no room in its table row (or in 31 bits), a last page that is shared, or not enough free pages (once
  * the list has asked for more pages than there are, that request and the later ones that need pages get none). */
 size_t gdn_pages_workspace_size(const gdn_pages_shape *shape, int m);
 int gdn_pages_extend(const gdn_pages_shape *shape, int32_t *page_table, int32_t *seq_lens, int32_t *refcount,

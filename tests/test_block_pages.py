@@ -135,6 +135,19 @@ def test_shared_partial_page_is_not_extended():
 
 
 @gpu
+def test_lengths_end_at_31_bits():
+    """A table row may have room for more tokens than a length can count."""
+    import gated_deltanet_linear_15_gb300 as g
+    P, start = 1 << 20, (1 << 31) - (1 << 20)
+    table, lens, ref = torch.full((2, 4096), -1, dtype=torch.int32, device=DEV), ints([start, 0]), ints([0] * 4)
+    assert g.extend_pages(table, lens, ref, ints([0, 1]), ints([P, P + 1]), P).tolist() == [0, 1]
+    assert lens.tolist() == [start, P + 1] and ref.tolist() == [1, 1, 0, 0] and (table[0] == -1).all()
+    assert g.extend_pages(table, lens, ref, ints([0]), ints([P - 1]), P).tolist() == [1]
+    assert lens.tolist() == [2 ** 31 - 1, P + 1] and ref.tolist() == [1, 1, 1, 0] and int(table[0, 2047]) == 2
+    assert g.extend_pages(table, lens, ref, ints([0]), ints([1]), P).tolist() == [0]
+
+
+@gpu
 def test_sequence_named_twice_is_freed_once():
     import gated_deltanet_linear_15_gb300 as g
     table, lens, ref = ints([[0, 1], [0, -1]]), ints([20, 16]), ints([2, 1])
