@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
     const long long upto = min(total + inc, 1ll << 30);
     if (i < m) {
       pre[i + 1] = (int)upto;
-      ok[i] = good;
+      ok[i] = good ? 1 + (need > 0) : 0;  // 2: takes pages (the prefix cannot tell where it has stopped growing)
     }
     const int all = sh[31];
     __syncthreads();
@@ -190,9 +190,8 @@ __global__ void __launch_bounds__(NP_T) pages_extend_kernel(PagesArgs a, const i
   const int avail = count_free(a.ref, a.NP, (int)total, r0, sh64);
   // the requests whose pages, and all before theirs, are there
   for (int i = tid; i < m; i += NP_T) {
-    const int need = pre[i + 1] - pre[i];
-    if (need > 0 && pre[i + 1] > avail) ok[i] = 0;
-    else atomicMax(&granted, pre[i + 1] <= avail ? pre[i + 1] : 0);
+    if (ok[i] == 2) ok[i] = pre[i + 1] <= avail;
+    if (pre[i + 1] <= avail) atomicMax(&granted, pre[i + 1]);
   }
   __syncthreads();
   const int want = granted;

@@ -148,6 +148,19 @@ def test_lengths_end_at_31_bits():
 
 
 @gpu
+def test_requests_for_more_pages_than_30_bits_count():
+    """Together the requests ask for more than 2^30 pages: none of those that need pages is granted, the later ones included."""
+    import gated_deltanet_linear_15_gb300 as g
+    NP, m = 1 << 20, 1027
+    table = torch.full((m, NP + 1), -1, dtype=torch.int32, device=DEV)
+    lens, ref = ints([0] * m), torch.zeros(NP, dtype=torch.int32, device=DEV)
+    add = [NP + 1] * m
+    add[-1] = 0
+    assert g.extend_pages(table, lens, ref, ints(list(range(m))), ints(add), 1).tolist() == [0] * (m - 1) + [1]
+    assert not lens.any() and not ref.any()
+
+
+@gpu
 def test_sequence_named_twice_is_freed_once():
     import gated_deltanet_linear_15_gb300 as g
     table, lens, ref = ints([[0, 1], [0, -1]]), ints([20, 16]), ints([2, 1])
