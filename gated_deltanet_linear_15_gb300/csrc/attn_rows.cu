@@ -649,14 +649,16 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
         float mn = M;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) mn = fmaxf(mn, m[i]);
-        if (mn == -INFINITY) mn = 0.f;  // nothing seen yet: every factor below is 0
-        float f = ex2(M - mn);
+        // Nothing seen yet: every factor below is 0.  M stays -inf then: a row whose first pieces lie outside its window
+        // may have its maximum far below 0.
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        float f = ex2(M - ref);
         L *= f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] *= f;
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-          f = ex2(m[i] - mn);
+          f = ex2(m[i] - ref);
           L += f * l[i];
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] += f * v[i][e];
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
     }
     if constexpr (JW > 1) {
       if (lane == 0) {
-        sh[warp][32 * E] = L == 0.f ? -INFINITY : M;  // a warp without mass has no say in the maximum
+        sh[warp][32 * E] = M;
         sh[warp][32 * E + 1] = L;
       }
 #pragma unroll
@@ -678,13 +680,13 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
         mw[w] = sh[w][32 * E];
         mn = fmaxf(mn, mw[w]);
       }
-      if (mn == -INFINITY) mn = 0.f;
+      const float ref = mn == -INFINITY ? 0.f : mn;
       L = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll
       for (int w = 0; w < JW; ++w) {
-        const float f = mw[w] == -INFINITY && sh[w][32 * E + 1] == 0.f ? 0.f : ex2(mw[w] - mn);
+        const float f = ex2(mw[w] - ref);
         L += f * sh[w][32 * E + 1];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += f * sh[w][E * lane + e];

@@ -187,6 +187,32 @@ def test_joins_of_tall_items(seqs, Hkv, G):
 
 
 @gpu
+@pytest.mark.parametrize("seqs,Hkv,window", [
+    ([(200, 300)] * 25, 1, 16),              # items in three pieces of a block, the last rows see keys in the third only
+    ([(256, 1000)] * 39, 1, 64),
+    ([(256, 900), (250, 700)], 2, 20),       # a few items in many pieces
+    ([(30, 800), (17, 400), (9, 1000)], 1, 12),
+])
+@pytest.mark.parametrize("level", [-100.0, -1000.0])
+def test_joins_of_rows_that_see_nothing_in_the_first_pieces(seqs, Hkv, window, level):
+    """Under a window the last rows of a tile see nothing of its first key blocks; with all logits far below zero, what they
+    do see must not be measured against a maximum of zero.  Bound: the logits' fp32 sums pass |level| / scale, and each of
+    their 8 steps may lose 2^-23 of 2 of that: 16 * 2^-23 |level| in a logit, twice that in a weight."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make(seqs, BF, 128, Hkv, 1, 16, seed=17, fill=0.0)
+    scale = 128 ** -0.5
+    a = (-level / (128 * scale)) ** 0.5
+    x["q"] = (a + 0.02 * x["q"]).to(BF)
+    x["k_cache"] = (-a + 0.02 * x["k_cache"]).to(BF)
+    o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), window=window, return_lse=True)
+    ro, rl, mag = ref.attention(x["q"], x["k_cache"], x["v_cache"], x["page_table"], x["kv_lens"], qs, scale, window)
+    assert (rl < level / 2).all()
+    slack = 16 * 2 ** -23 * 2 * abs(level)
+    assert ((lse.cpu().double() - rl).abs() <= slack + 1e-5 + 1e-6 * rl.abs()).all()
+    assert ((o.cpu().double() - ro).abs() <= 1.05 * 2 ** -8 * (ro.abs() + mag) + 2 * slack * mag).all()
+
+
+@gpu
 def test_peaked_and_growing_logits():
     """Logits that grow along the context (the maximum rises at every step) and by far more than fp32's exponent range
     would bear without it."""
