@@ -228,7 +228,9 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
   a.N = s->num_seqs; a.total_q = s->total_q; a.per_seq = cu_q ? 0 : s->total_q / s->num_seqs;
   a.Hq = s->num_heads; a.Hkv = s->num_kv_heads; a.G = s->num_heads / s->num_kv_heads;
   a.log2P = ilog2(s->page_size);
-  a.num_pages = s->num_pages; a.max_pages = s->max_pages; a.window = s->window;
+  a.num_pages = s->num_pages; a.max_pages = s->max_pages;
+  // a window as long as a table row limits nothing; what stays is far from where differences of positions would wrap
+  a.window = s->window < (long long)s->max_pages * s->page_size ? s->window : 0;
   a.scale_log2 = s->scale * 1.4426950408889634f;
   a.expire = s->reserved != 0;
   a.hdr = static_cast<int4 *>(ws);

@@ -81,7 +81,7 @@ __device__ __forceinline__ Tile tile_of(const PagedArgs &a, const SeqInfo &s, in
   const int i0 = (int)(r0 / (unsigned)a.G), i1 = w.rows ? (int)((r0 + w.rows - 1) / (unsigned)a.G) : i0;
   w.pos0 = s.kv - s.qlen + i0;
   w.hi = max(0, min(s.kv, s.kv - s.qlen + i1 + 1));
-  w.lo = a.window ? max(0, w.pos0 - a.window + 1) : 0;
+  w.lo = a.window ? (int)max(0ll, (long long)w.pos0 - a.window + 1) : 0;  // pos0 < 0: fewer cached tokens than new ones
   w.blk0 = w.lo / BN;
   w.nblk = w.rows > 0 && w.hi > w.lo ? (w.hi + BN - 1) / BN - w.blk0 : 0;
   return w;

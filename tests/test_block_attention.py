@@ -187,6 +187,26 @@ def test_joins_of_tall_items(seqs, Hkv, G):
 
 
 @gpu
+@pytest.mark.parametrize("seqs,dtype", [([(8, 3)], BF), ([(9, 4), (1, 30)], BF), ([(140, 12), (200, 300)], BF), ([(9, 4)], F32)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 1 << 30, 40])
+def test_windows_longer_than_the_context(seqs, dtype, window):
+    """Also where the first queries lie before the first key."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make(seqs, dtype, 128, 1, 2, 16, seed=18)
+    if window == 40:   # 40 is longer than the contexts here, and shorter than the table's row
+        seqs, window = [(min(a, 40), min(b, 40)) for a, b in seqs], 40
+        x, qs = make(seqs + [(1, 200)], dtype, 128, 1, 2, 16, seed=18)
+        close(*g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), window=window, return_lse=True), x, qs,
+              128 ** -0.5, window)
+        return
+    cu = ref.lens_to_cu(qs, DEV)
+    o, lse = g.paged_attention(**x, cu_q=cu, max_q=max(qs), window=window, return_lse=True)
+    want = g.paged_attention(**x, cu_q=cu, max_q=max(qs), return_lse=True)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    close(o, lse, x, qs, 128 ** -0.5)
+
+
+@gpu
 @pytest.mark.parametrize("seqs,Hkv,window", [
     ([(200, 300)] * 25, 1, 16),              # items in three pieces of a block, the last rows see keys in the third only
     ([(256, 1000)] * 39, 1, 64),
