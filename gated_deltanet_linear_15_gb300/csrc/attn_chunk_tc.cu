@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           }
           if (live) {
             if (whole) {
-              if (a.lse) a.lse[(long long)tok * a.Hq + head] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+              if (a.lse) a.lse[(long long)tok * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else {
               rec[(size_t)MT * D + row] = m;
               rec[(size_t)MT * D + MT + row] = l;

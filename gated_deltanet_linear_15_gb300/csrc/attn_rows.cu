@@ -557,7 +557,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
           *reinterpret_cast<uint2 *>(op) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
         }
         if (a.lse && c == 0)
-          a.lse[(long long)tok * a.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          a.lse[(long long)tok * a.Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
       } else {
         *reinterpret_cast<float4 *>(rec + r * D + 4 * c) = o;
         if (c == 0) {

@@ -346,6 +346,19 @@ def test_non_finite_values_reach_only_their_readers():
 
 
 @gpu
+@pytest.mark.parametrize("seqs", [[(1, 5)], [(1, 20001)], [(40, 40)], [(150, 4000)], [(9, 4), (2, 30)], [(140, 12), (1, 0)]])
+def test_scores_that_are_all_nan(seqs):
+    """o and lse are NaN, whether the item is whole or cut into pieces; only a query without keys has lse = -inf."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs = make(seqs, BF, 128, 1, 2, 16, seed=19)
+    x["k_cache"].fill_(float("nan"))
+    o, lse = g.paged_attention(**x, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), return_lse=True)
+    blind = torch.cat([torch.arange(k - q, k) < 0 for q, k in seqs])
+    assert torch.isnan(o[~blind]).all() and torch.isnan(lse[~blind]).all()
+    assert (o[blind] == 0).all() and (lse[blind] == -math.inf).all()
+
+
+@gpu
 def test_runs_on_the_current_stream():
     import gated_deltanet_linear_15_gb300 as g
     x, qs = make([(1, 3000)], BF, 128, 2, 4, 64, seed=15)
