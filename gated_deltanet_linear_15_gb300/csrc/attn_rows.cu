@@ -26,9 +26,9 @@
 // The sums are rescaled only when a row's maximum rises by more than 8 (a factor of 256 that fp32 sums and bf16
 // weights carry without loss), so most slices skip that pass over the accumulator.
 //
-// fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the exact rest):
+// fp32: every product as three TF32 mma.sync parts, x = hi + lo (hi rounded to 11 bits, lo the rest):
 // hi hi + hi lo + lo hi leaves about 2^-21 of a product.  Bound by instructions and the latency of the products' chains
-// (8 sequences of 1 .. 256 new tokens, D = 64, window 1024: 44 us, issue slots 34 % busy, tensor pipe 29 %, 17 MB).
+// (8 sequences of 1 .. 256 new tokens, D = 64, window 1024: 45 us, issue slots 34 % busy, tensor pipe 29 %, 17 MB).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -60,9 +60,24 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// x = hi + lo: hi has 11 significant bits, rounded with halves away from zero, and what is left has 12, of which the product
+// reads 11 (it ignores the low 13 bits of a word).  Rounding may carry into infinity or past a NaN, so hi stops at the
+// largest value of its sign (one minimum of signed and one of unsigned numbers for the two signs): an infinity or a NaN is
+// one in lo.  Without them, and with lo rounded by an integer sum, the NaN that fp32 arithmetic makes (0x7fffffff) came out
+// as zero and the largest values as inf - inf; they cost 1 to 3 % (512 new tokens after 3584, 32 heads of 128: 637 to 652 us;
+// 8 sequences of 1 .. 256, D = 64: 43.8 to 45.0 us).  Weights are below 2^9 or NaN, and need none.
+__device__ __forceinline__ uint32_t round_tf32(float x) { return __float_as_uint(x) + 0x1000u; }
+__device__ __forceinline__ void rest_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  hi &= 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to 11 significant bits, halves away from zero
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;  // rounded likewise (the product ignores the low 13 bits)
+  hi = min((uint32_t)min((int)round_tf32(x), 0x7f7fffff), 0xff7fffffu);
+  rest_tf32(x, hi, lo);
+}
+__device__ __forceinline__ void split_weight(float x, uint32_t &hi, uint32_t &lo) {
+  hi = round_tf32(x);
+  rest_tf32(x, hi, lo);
 }
 // sum of c[] += a b with both operands in two TF32 parts; N accumulators, so that the parts wait for one another less
 template <int N>
@@ -473,10 +488,10 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 #pragma unroll
         for (int jt = 0; jt < 2 * NS; ++jt) {
           uint32_t ph[4], pl[4];
-          split_tf32(s[jt][0], ph[0], pl[0]);
-          split_tf32(s[jt][2], ph[1], pl[1]);
-          split_tf32(s[jt][1], ph[2], pl[2]);
-          split_tf32(s[jt][3], ph[3], pl[3]);
+          split_weight(s[jt][0], ph[0], pl[0]);
+          split_weight(s[jt][2], ph[1], pl[1]);
+          split_weight(s[jt][1], ph[2], pl[2]);
+          split_weight(s[jt][3], ph[3], pl[3]);
 #pragma unroll
           for (int p = 0; p < D / 32; ++p) {
             const int r = 8 * jt + 2 * qd;

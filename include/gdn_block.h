@@ -75,9 +75,10 @@ typedef struct {
  * computed together see (16, 32 or 256 (query, head) rows) must have a finite value vector.  A missing page counts as
  * keys and values of zero.
  * bf16: products in bf16 with fp32 sums, the weights rounded to bf16 before the second product.  fp32: products in
- * three TF32 parts each, about 2^-21 relative.  q, k_cache, v_cache, o: 16-byte aligned with strides of whole 16
- * bytes, those of the caches positive and below 2^37; at most 65535 query heads per key head.  o and lse share no
- * memory with the inputs.  workspace: 32-byte aligned (GDN_ERR_INVALID_ARG otherwise).
+ * three TF32 parts each, about 2^-21 relative (less where a part of a factor is below 2^-126); a NaN or an infinity
+ * reaches what it should (an infinity times a factor beyond 2^11 may come out as NaN).  q, k_cache, v_cache, o:
+ * 16-byte aligned with strides of whole 16 bytes, those of the caches positive and below 2^37; at most 65535 query heads
+ * per key head.  o and lse share no memory with the inputs.  workspace: 32-byte aligned (GDN_ERR_INVALID_ARG otherwise).
  */
 size_t gdn_paged_attn_workspace_size(const gdn_paged_shape *shape);
 int gdn_paged_attn_fwd(const gdn_paged_shape *shape, const void *q, const void *k_cache, const void *v_cache,

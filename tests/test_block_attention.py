@@ -358,6 +358,77 @@ def test_scores_that_are_all_nan(seqs):
     assert (o[blind] == 0).all() and (lse[blind] == -math.inf).all()
 
 
+NANS = [0x7fffffff, 0x7fc00000, 0x7f800001, 0xffffffff, 0xff800001]   # the first is what fp32 arithmetic makes on the GPU
+
+
+def _bits(u):
+    return torch.tensor([u - (1 << 32) if u >> 31 else u], dtype=torch.int32, device=DEV).view(torch.float32)
+
+
+@gpu
+@pytest.mark.parametrize("nan", NANS + [None])
+@pytest.mark.parametrize("D,G,q", [(64, 1, 1), (64, 2, 20), (128, 1, 1), (128, 2, 20)])
+def test_fp32_nan_reaches_its_readers(nan, D, G, q):
+    """Every bit pattern of a NaN, and one that the GPU computes, in a value, a key and a query."""
+    import gated_deltanet_linear_15_gb300 as g
+    nan = _bits(nan) if nan else torch.full((1,), math.inf, device=DEV) - math.inf
+    x, qs = make([(q, 300)], F32, D, 1, G, 64, seed=20)
+    clean = g.paged_attention(**x, max_q=q)
+    pg = int(x["page_table"][0, 1])
+    y = dict(x, v_cache=x["v_cache"].clone())
+    y["v_cache"][pg, 5, 0, 7] = nan
+    o = g.paged_attention(**y, max_q=q)
+    assert torch.isnan(o[:, :, 7]).all()
+    o[:, :, 7] = clean[:, :, 7]
+    assert torch.equal(o, clean)
+    y = dict(x, k_cache=x["k_cache"].clone())
+    y["k_cache"][pg, 5, 0, D - 3] = nan
+    o, lse = g.paged_attention(**y, max_q=q, return_lse=True)
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
+    y = dict(x, q=x["q"].clone())
+    y["q"][q - 1, G - 1, 9] = nan
+    o, lse = g.paged_attention(**y, max_q=q, return_lse=True)
+    assert torch.isnan(o[q - 1, G - 1]).all() and torch.isnan(lse[q - 1, G - 1])
+    o[q - 1, G - 1] = clean[q - 1, G - 1]
+    assert torch.equal(o, clean)
+
+
+@gpu
+@pytest.mark.parametrize("D,q", [(64, 1), (128, 1), (128, 30)])
+def test_fp32_largest_values(D, q):
+    """The largest finite values of either sign do not become infinite on the way, and infinities are as good as any value.  All queries see one key, so o is its
+    value row (weight 1, the three parts of a product leave 2^-21); then keys near the top with queries of 2^-96 and a scale that undo
+    them (parts below 2^-126 would lose their low bits)."""
+    import gated_deltanet_linear_15_gb300 as g
+    top = float(torch.finfo(F32).max)
+    x, qs = make([(q, q)], F32, D, 1, 1, 64, seed=21, fill=0.0)
+    v = torch.tensor([top, -top, top * (1 - 2.0 ** -13), 3.3e38, 1.0, -2.5, 1e-30, 0.0], device=DEV).repeat(D // 8)
+    x["v_cache"][:] = v
+    o = g.paged_attention(**x, max_q=q, window=1)
+    assert torch.isfinite(o).all() and ((o - v).abs() <= 2.0 ** -20 * v.abs()).all()
+    for inf in (math.inf, -math.inf):   # an infinite value, and a key that is infinitely far away
+        y, qs = make([(q, 50)], F32, D, 1, 1, 64, seed=23)
+        want = g.paged_attention(**y, max_q=q)
+        pg = int(y["page_table"][0, 0])
+        y["v_cache"][pg, 3, 0, 6] = inf
+        o = g.paged_attention(**y, max_q=q)
+        assert (o[:, :, 6] == inf).all()
+        o[:, :, 6] = want[:, :, 6]
+        assert torch.equal(o, want)
+        y["q"][..., 5] = -1.7
+        y["k_cache"][pg, 3, 0, 5], y["v_cache"][pg, 3, 0, 6] = math.inf, 0.25
+        o, lse = g.paged_attention(**y, max_q=q, return_lse=True)
+        y["k_cache"][pg, 3, 0, 5] = 1e4      # 1e4 * 1.7 / sqrt(D) below the others: a weight of zero too
+        assert torch.isfinite(o).all() and torch.equal(o, g.paged_attention(**y, max_q=q))
+    x, qs = make([(q, 50)], F32, D, 1, 1, 64, seed=22, fill=0.0)
+    k, qq = x["k_cache"].clone(), x["q"].clone()
+    k[..., 3], qq[..., 3] = top, 2.0 ** -96
+    k[..., 4], qq[..., 4] = -top, 1.3 * 2.0 ** -96
+    k[..., :3], k[..., 5:] = k[..., :3] * 2.0 ** 31, k[..., 5:] * 2.0 ** 31
+    x["k_cache"], x["q"] = k, qq
+    close(*g.paged_attention(**x, max_q=q, scale=D ** -0.5 * 2.0 ** -31, return_lse=True), x, qs, D ** -0.5 * 2.0 ** -31)
+
+
 @gpu
 def test_runs_on_the_current_stream():
     import gated_deltanet_linear_15_gb300 as g
