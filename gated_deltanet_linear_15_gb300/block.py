@@ -146,7 +146,7 @@ def extend_pages(page_table, seq_lens, refcount, seqs, add, page_size: int):
 def fork_pages(page_table, seq_lens, refcount, parents, children, pools=(), page_size: int = 16, states=()):
     """Makes each (empty) child sequence a copy of its parent: full pages shared, a partly filled last page copied to a
     new page in every pool [pages, ...], slot `child` of every states tensor [sequences, ...] a copy of slot `parent`
-    (the recurrent states of delta-rule layers).  Returns int32 [m]: the new page, -1 where none was needed, -2 where
+    (the recurrent states of delta-rule layers).  Pools and states with fewer slots than that are refused.  Returns int32 [m]: the new page, -1 where none was needed, -2 where
     the fork was left out."""
     return _py.fork_pages(page_table, seq_lens, refcount, parents, children, pools, page_size, states)
 

@@ -136,7 +136,8 @@ PagesArgs pages_args(const gdn_pages_shape *s, int *table, int *lens, int *ref) 
   a.ref = ref;
   return a;
 }
-int check_pools(const gdn_slot_pool *p, int n, const char *what) {
+// least: slots that each has to have
+int check_pools(const gdn_slot_pool *p, int n, const char *what, int least) {
   if (n < 0) return fail(GDN_ERR_INVALID_ARG, "negative number of %s", what);
   if (n && !p) return fail(GDN_ERR_INVALID_ARG, "%s is NULL", what);
   for (int i = 0; i < n; ++i) {
@@ -145,6 +146,8 @@ int check_pools(const gdn_slot_pool *p, int n, const char *what) {
       return fail(GDN_ERR_INVALID_ARG, "%s[%d]: need 0 <= bytes <= stride and slots >= 0", what, i);
     if (!aligned16(p[i].base) || p[i].stride % 16 || p[i].bytes % 16)
       return fail(GDN_ERR_INVALID_ARG, "%s[%d]: base, stride and bytes must be multiples of 16", what, i);
+    if (p[i].slots < least)
+      return fail(GDN_ERR_INVALID_ARG, "%s[%d] has %lld slots where %d are named", what, i, (long long)p[i].slots, least);
   }
   return GDN_OK;
 }
@@ -373,7 +376,7 @@ int gdn_rotary_append(const gdn_paged_shape *s, const void *q, const void *k, co
 }
 
 int gdn_slots_copy(const gdn_slot_pool *pools, int num_pools, const int32_t *src, const int32_t *dst, int count, gdn_stream_t stream) {
-  TRY(check_pools(pools, num_pools, "pools"));
+  TRY(check_pools(pools, num_pools, "pools", 0));
   if (count < 0) return fail(GDN_ERR_INVALID_ARG, "count must be >= 0");
   if (count == 0 || num_pools == 0) return GDN_OK;
   TRY(need_ptr(src, "src"));
@@ -418,8 +421,8 @@ int gdn_pages_fork(const gdn_pages_shape *s, int32_t *table, int32_t *lens, int3
                    const int32_t *children, int m, const gdn_slot_pool *pools, int num_pools, const gdn_slot_pool *states,
                    int num_states, int32_t *new_page, void *ws, size_t ws_bytes, gdn_stream_t stream) {
   TRY(check_pages(s));
-  TRY(check_pools(pools, num_pools, "pools"));
-  TRY(check_pools(states, num_states, "states"));
+  TRY(check_pools(pools, num_pools, "pools", s->num_pages));
+  TRY(check_pools(states, num_states, "states", s->num_seqs));
   if (m < 0) return fail(GDN_ERR_INVALID_ARG, "m must be >= 0");
   if (m == 0) return GDN_OK;
   TRY(need_ptr(table, "page_table"));
@@ -465,7 +468,7 @@ int gdn_pages_compact(const gdn_pages_shape *s, const int32_t *table, const int3
                       int32_t *ref_out, const gdn_slot_pool *pools, int num_pools, int32_t *moves, void *ws,
                       size_t ws_bytes, gdn_stream_t stream) {
   TRY(check_pages(s));
-  TRY(check_pools(pools, num_pools, "pools"));
+  TRY(check_pools(pools, num_pools, "pools", s->num_pages));
   TRY(need_ptr(table, "page_table"));
   TRY(need_ptr(ref, "refcount"));
   TRY(need_ptr(table_out, "page_table_out"));

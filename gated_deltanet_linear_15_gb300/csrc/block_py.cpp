@@ -302,7 +302,8 @@ PyObject *rotary_append(PyObject *const *a) {
   return THPVariable_Wrap(o);
 }
 
-std::vector<gdn_slot_pool> pools(PyObject *seq, const char *name) {
+// least: slots that each has to have
+std::vector<gdn_slot_pool> pools(PyObject *seq, const char *name, int64_t least) {
   PyObject *fast = PySequence_Fast(seq, "pools must be a sequence of tensors");
   if (!fast) throw std::invalid_argument("");
   const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
@@ -313,6 +314,7 @@ std::vector<gdn_slot_pool> pools(PyObject *seq, const char *name) {
       if (t.dim() < 1) bad(std::string(name) + " must be tensors of slots");
       here(t, name);
       const int64_t slots = t.size(0);
+      if (slots < least) bad(std::string(name) + " must have " + std::to_string(least) + " slots or more (the first dimension counts them)");
       int64_t inner = t.element_size(), want = 1;
       for (int64_t d = t.dim() - 1; d > 0; --d) {  // a slot's values lie in one piece
         if (slots && t.size(d) > 1 && t.stride(d) != want) bad(std::string("each slot of ") + name + " must be contiguous");
@@ -375,7 +377,7 @@ PyObject *fork_pages(PyObject *const *a) {
   ints(lens, "seq_lens", s.num_seqs);
   ints(par, "parents");
   ints(chi, "children", par.numel());
-  const std::vector<gdn_slot_pool> p = pools(a[5], "pools"), st = pools(a[7], "states");
+  const std::vector<gdn_slot_pool> p = pools(a[5], "pools", s.num_pages), st = pools(a[7], "states", s.num_seqs);
   const int m = fits(par.numel(), "the number of forks");
   const Tensor fresh = at::empty_like(par), ws = pages_workspace(s, m, par);
   check(api.pages_fork(&s, i32(table), i32(lens), i32(ref), i32(par), i32(chi), m, p.data(), (int)p.size(), st.data(), (int)st.size(),
@@ -400,7 +402,7 @@ PyObject *free_pages(PyObject *const *a) {
 PyObject *compact_pages(PyObject *const *a) {
   const Tensor &table = tensor(a[0], "page_table"), &ref = tensor(a[1], "refcount");
   const gdn_pages_shape s = pages_shape(table, ref, 1);
-  const std::vector<gdn_slot_pool> p = pools(a[2], "pools");
+  const std::vector<gdn_slot_pool> p = pools(a[2], "pools", s.num_pages);
   const bool inplace = truth(a[3]);
   const Tensor t = inplace ? table : at::empty_strided(table.sizes(), {s.table_stride, 1}, table.options());
   const Tensor r = inplace ? ref : at::empty_like(ref);
@@ -416,7 +418,7 @@ PyObject *copy_slots(PyObject *const *a) {
   const Tensor &src = tensor(a[1], "src"), &dst = tensor(a[2], "dst");
   ints(src, "src");
   ints(dst, "dst", src.numel());
-  const std::vector<gdn_slot_pool> p = pools(a[0], "pools");
+  const std::vector<gdn_slot_pool> p = pools(a[0], "pools", 0);
   check(api.slots_copy(p.data(), (int)p.size(), i32(src), i32(dst), fits(src.numel(), "the number of pairs"), (gdn_stream_t)stream(src)),
         "gdn_slots_copy");
   Py_RETURN_NONE;

@@ -149,7 +149,8 @@ typedef struct {
 typedef struct {
   void *base;
   int64_t stride, bytes;
-  int64_t slots; /* pairs that name a slot outside [0, slots) are left out */
+  int64_t slots; /* gdn_slots_copy leaves out pairs that name a slot outside [0, slots); fork and compact refuse a  */
+                 /* pool of fewer slots than pages, and a state pool of fewer than sequences                        */
 } gdn_slot_pool;
 
 /* Copies slot src[i] to slot dst[i] in every pool, i < count.  No dst may appear twice or among the src. */

@@ -236,6 +236,24 @@ def test_tables_whose_rows_share_memory_are_refused():
     assert one.tolist() == [[0, 1, -1, -1]]
 
 
+@gpu
+def test_binding_refuses_pools_of_too_few_slots():
+    """[layers, pages, ...] in place of one tensor for each layer, or states of another batch; more slots are no fault."""
+    import gated_deltanet_linear_15_gb300 as g
+    table, lens, ref = ints([[0, -1], [-1, -1]]), ints([3, 0]), ints([1, 0, 0])
+    good, layers = torch.zeros(4, 16, device=DEV), torch.zeros(2, 3, 16, device=DEV)
+    for pools, states in (([layers], []), ([good, good[:2]], []), ([good], [good[:1]]), ([good[:0]], [])):
+        with pytest.raises(ValueError, match="slots"):
+            g.fork_pages(table, lens, ref, ints([0]), ints([1]), pools, 16, states)
+        if not states:
+            with pytest.raises(ValueError, match="slots"):
+                g.compact_pages(table, ref, pools)
+    assert table.tolist() == [[0, -1], [-1, -1]] and ref.tolist() == [1, 0, 0] and lens.tolist() == [3, 0]
+    good[0] = 5
+    assert g.fork_pages(table, lens, ref, ints([0]), ints([1]), [good], 16, [good]).tolist() == [1]
+    assert (good[1] == 5).all() and table.tolist() == [[0, -1], [1, -1]]
+
+
 # ------------------------------------------------------------------ refusals of the C entry points (no GPU needed)
 def _shape(**kw):
     s = _lib.GdnPagesShape()
@@ -259,6 +277,22 @@ def test_c_entries_refuse_shapes(lib, kw):
     assert lib.gdn_pages_compact(ref, p, p, p, p, None, 0, None, p, big, None) != 0
     assert lib.gdn_pages_workspace_size(ref, 4) == 0
     assert lib.gdn_last_error_string() != b""
+
+
+def test_c_entries_refuse_pools_of_too_few_slots(lib):
+    """A pool that lacks the slots would lose what the tables go on to name."""
+    s, p, big = _shape(), 0x10000, 1 << 40
+    ref, pool = ctypes.byref(s), (_lib.GdnSlotPool * 1)()
+    pool[0].base, pool[0].stride, pool[0].bytes = 0x10000, 32, 32
+    for slots, least in ((99, b"100"), (2, b"100"), (0, b"100")):
+        pool[0].slots = slots
+        assert lib.gdn_pages_fork(ref, p, p, p, p, p, 1, pool, 1, None, 0, p, p, big, None) == 1
+        assert least in lib.gdn_last_error_string()
+        assert lib.gdn_pages_compact(ref, p, p, p, p, pool, 1, None, p, big, None) == 1
+        assert least in lib.gdn_last_error_string()
+    pool[0].slots = 3
+    assert lib.gdn_pages_fork(ref, p, p, p, p, p, 1, None, 0, pool, 1, p, p, big, None) == 1
+    assert b"states" in lib.gdn_last_error_string()
 
 
 def test_c_entries_refuse_arguments(lib):
