@@ -14,6 +14,7 @@ import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -110,21 +111,22 @@ def rotary(q, k, table, positions, interleaved: bool = False, inverse: bool = Fa
 
 class RotaryFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, table, positions, interleaved):
+    def forward(ctx, q, k, table, positions, interleaved, inverse=False):
         ctx.save_for_backward(table, positions)
-        ctx.interleaved = interleaved
-        return rotary(q, k, table, positions, interleaved)
+        ctx.interleaved, ctx.inverse = interleaved, inverse
+        return rotary(q, k, table, positions, interleaved, inverse)
 
     @staticmethod
     def backward(ctx, dq, dk):
         table, positions = ctx.saved_tensors
         dk = None if dk is None else dk.contiguous()  # there is none without k
-        dq, dk = rotary(dq.contiguous(), dk, table, positions, ctx.interleaved, inverse=True)
-        return dq, dk, None, None, None
+        # linear in q and k, so its own gradient is the function again, the other way round
+        dq, dk = RotaryFunction.apply(dq.contiguous(), dk, table, positions, ctx.interleaved, not ctx.inverse)
+        return dq, dk, None, None, None, None
 
 
 def rotary_embedding(q, k, table, positions, interleaved: bool = False):
-    """``rotary`` with gradients for q and k (or q alone, with k None)."""
+    """``rotary`` with gradients of any order for q and k (or q alone, with k None)."""
     return RotaryFunction.apply(q, k, table, positions, interleaved)
 
 
@@ -201,6 +203,7 @@ class ResidualRMSNormFunction(torch.autograd.Function):
         return r.y, r.h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
         dx, dw = rms_norm_bwd(dy.contiguous(), h, weight, rstd, None if dh is None else dh.contiguous(), ctx.weight_offset)
@@ -208,5 +211,5 @@ class ResidualRMSNormFunction(torch.autograd.Function):
 
 
 def residual_rms_norm(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
-    """``rms_norm`` with gradients: (y, h), or y alone without a residual."""
+    """``rms_norm`` with (first) gradients: (y, h), or y alone without a residual."""
     return ResidualRMSNormFunction.apply(x, residual, weight, eps, weight_offset)

@@ -201,6 +201,20 @@ def test_gradient_without_a_residual():
 
 
 @gpu
+@pytest.mark.parametrize("residual", [False, True])
+def test_second_derivatives_are_refused(residual):
+    """The backward is a kernel that autograd does not see into: a second derivative raises instead of missing terms."""
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(7)
+    x, w, r = rand(gen, 5, 64).requires_grad_(), (1 + 0.2 * rand(gen, 64)).requires_grad_(), rand(gen, 5, 64)
+    out = g.residual_rms_norm(x, w, r if residual else None)
+    y = out[0] if residual else out
+    dx = torch.autograd.grad(y.square().sum(), x, create_graph=True)[0]
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
+
+
+@gpu
 def test_binding_refuses():
     import gated_deltanet_linear_15_gb300 as g
     x, w = torch.zeros(4, 64, device=DEV), torch.ones(64, device=DEV)

@@ -160,6 +160,24 @@ def test_gradient_by_formula_and_differences(interleaved):
 
 
 @gpu
+@pytest.mark.parametrize("with_k", [False, True])
+def test_second_derivatives(with_k):
+    """<gradient of q for v, u> is linear in v, and its derivative is u turned; so is that of a gradient of a gradient."""
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(12)
+    q, v, u = (torch.randn(7, 3, 32, generator=gen).to(DEV) for _ in range(3))
+    k = torch.randn(7, 1, 32, generator=gen).to(DEV).requires_grad_() if with_k else None
+    table, pos = table_ref(64, 24).float().to(DEV), torch.arange(7, dtype=torch.int32, device=DEV)
+    q.requires_grad_(), v.requires_grad_()
+    a, b = g.rotary_embedding(q, k, table, pos)
+    outs, gouts = ([a, b], [v, torch.ones_like(b)]) if with_k else ([a], [v])
+    dq = torch.autograd.grad(outs, q, gouts, create_graph=True)[0]
+    close(dq.detach(), ref.rotate(v.detach(), table, pos, inverse=True), v.detach())
+    dv = torch.autograd.grad((dq * u).sum(), v)[0]
+    close(dv, ref.rotate(u, table, pos), u)
+
+
+@gpu
 def test_gradient_of_queries_alone():
     import gated_deltanet_linear_15_gb300 as g
     gen = torch.Generator().manual_seed(9)
