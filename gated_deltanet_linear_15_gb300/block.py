@@ -7,6 +7,10 @@ upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual s
 output).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
 arguments are checked, and outputs and workspaces allocated, by the extension csrc/block_py.cpp.  Bad arguments raise
 ``ValueError`` (found there) or ``RuntimeError`` (found by the library, with its reason).
+
+Gradients come from ``rotary_embedding`` and ``residual_rms_norm``.  Every other function computes outside autograd, as
+the ``_fwd`` / ``_bwd`` functions of the delta rule do: its outputs carry no graph, whatever its inputs require.  What a
+function writes in place counts as an in-place operation (its version moves on).
 """
 from __future__ import annotations
 

@@ -139,6 +139,14 @@ void scratch(const Tensor &t, size_t need) {
   here(t, "workspace");
   if (!t.is_contiguous() || t.nbytes() < need) bad("workspace must be contiguous and have at least " + std::to_string(need) + " bytes");
 }
+// tells autograd that t has been written, so that a backward that saved what was there before fails instead of using this
+void wrote(const Tensor &t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void wrote(std::initializer_list<const Tensor *> ts) {
+  for (const Tensor *t : ts)
+    if (t) wrote(*t);
+}
 int32_t *i32(const Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); }
 const int32_t *i32(const Tensor *t) { return t ? static_cast<const int32_t *>(t->data_ptr()) : nullptr; }
 const void *ptr(const Tensor *t) { return t ? t->data_ptr() : nullptr; }
@@ -215,6 +223,7 @@ PyObject *paged_attention(PyObject *const *a) {
                            lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(),
                            (gdn_stream_t)stream(q)),
         "gdn_paged_attn_fwd");
+  wrote({out});
   return lse.defined() ? pack({o, lse}) : THPVariable_Wrap(o);
 }
 
@@ -270,6 +279,7 @@ PyObject *rotary(PyObject *const *a) {
   check(api.rotary(&s, q.data_ptr(), ptr(k), static_cast<const float *>(table.data_ptr()), i32(pos), qo.data_ptr(),
                    ko.defined() ? ko.data_ptr() : nullptr, (gdn_stream_t)stream(q)),
         "gdn_rotary");
+  if (inplace) wrote({&q, k});
   return pack({qo, ko});
 }
 
@@ -299,15 +309,26 @@ PyObject *rotary_append(PyObject *const *a) {
   check(api.rotary_append(&s, q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const float *>(table.data_ptr()), kc.data_ptr(),
                           vc.data_ptr(), i32(pages), i32(cu), i32(lens), o.data_ptr(), (gdn_stream_t)stream(q)),
         "gdn_rotary_append");
+  wrote({&kc, &vc, out});
   return THPVariable_Wrap(o);
 }
 
+// the pools of a call, and the tensors that hold them
+struct Pools {
+  std::vector<gdn_slot_pool> p;
+  std::vector<Tensor> held;
+  const gdn_slot_pool *data() const { return p.data(); }
+  int size() const { return (int)p.size(); }
+  void wrote_all() const {
+    for (const Tensor &t : held) wrote(t);
+  }
+};
 // least: slots that each has to have
-std::vector<gdn_slot_pool> pools(PyObject *seq, const char *name, int64_t least) {
+Pools pools(PyObject *seq, const char *name, int64_t least) {
   PyObject *fast = PySequence_Fast(seq, "pools must be a sequence of tensors");
   if (!fast) throw std::invalid_argument("");
   const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
-  std::vector<gdn_slot_pool> p((size_t)n);
+  Pools r;
   try {
     for (Py_ssize_t i = 0; i < n; ++i) {
       const Tensor &t = tensor(PySequence_Fast_GET_ITEM(fast, i), name);
@@ -321,19 +342,16 @@ std::vector<gdn_slot_pool> pools(PyObject *seq, const char *name, int64_t least)
         want *= t.size(d);
       }
       inner *= slots ? want : 0;
-      p[i] = {t.data_ptr(), slots > 1 ? t.stride(0) * (int64_t)t.element_size() : inner, inner, slots};
+      // an empty pool has no address: it has nothing to copy either
+      if (inner > 0) r.p.push_back({t.data_ptr(), slots > 1 ? t.stride(0) * (int64_t)t.element_size() : inner, inner, slots});
+      r.held.push_back(t);
     }
   } catch (...) {
     Py_DECREF(fast);
     throw;
   }
   Py_DECREF(fast);
-  // an empty pool has no address: it has nothing to copy either
-  size_t kept = 0;
-  for (const gdn_slot_pool &x : p)
-    if (x.bytes > 0) p[kept++] = x;
-  p.resize(kept);
-  return p;
+  return r;
 }
 
 gdn_pages_shape pages_shape(const Tensor &table, const Tensor &ref, int page_size) {
@@ -366,6 +384,7 @@ PyObject *extend_pages(PyObject *const *a) {
   check(api.pages_extend(&s, i32(table), i32(lens), i32(ref), i32(seqs), i32(add), m, i32(ok), ws.data_ptr(), ws.nbytes(),
                          (gdn_stream_t)stream(seqs)),
         "gdn_pages_extend");
+  wrote({&table, &lens, &ref});
   return THPVariable_Wrap(ok);
 }
 
@@ -377,12 +396,15 @@ PyObject *fork_pages(PyObject *const *a) {
   ints(lens, "seq_lens", s.num_seqs);
   ints(par, "parents");
   ints(chi, "children", par.numel());
-  const std::vector<gdn_slot_pool> p = pools(a[5], "pools", s.num_pages), st = pools(a[7], "states", s.num_seqs);
+  const Pools p = pools(a[5], "pools", s.num_pages), st = pools(a[7], "states", s.num_seqs);
   const int m = fits(par.numel(), "the number of forks");
   const Tensor fresh = at::empty_like(par), ws = pages_workspace(s, m, par);
-  check(api.pages_fork(&s, i32(table), i32(lens), i32(ref), i32(par), i32(chi), m, p.data(), (int)p.size(), st.data(), (int)st.size(),
+  check(api.pages_fork(&s, i32(table), i32(lens), i32(ref), i32(par), i32(chi), m, p.data(), p.size(), st.data(), st.size(),
                        i32(fresh), ws.data_ptr(), ws.nbytes(), (gdn_stream_t)stream(par)),
         "gdn_pages_fork");
+  wrote({&table, &lens, &ref});
+  p.wrote_all();
+  st.wrote_all();
   return THPVariable_Wrap(fresh);
 }
 
@@ -395,6 +417,7 @@ PyObject *free_pages(PyObject *const *a) {
   check(api.pages_free(&s, i32(table), i32(lens), i32(ref), i32(seqs), fits(seqs.numel(), "the number of sequences"),
                        (gdn_stream_t)stream(seqs)),
         "gdn_pages_free");
+  wrote({&table, &lens, &ref});
   Py_RETURN_NONE;
 }
 
@@ -402,14 +425,16 @@ PyObject *free_pages(PyObject *const *a) {
 PyObject *compact_pages(PyObject *const *a) {
   const Tensor &table = tensor(a[0], "page_table"), &ref = tensor(a[1], "refcount");
   const gdn_pages_shape s = pages_shape(table, ref, 1);
-  const std::vector<gdn_slot_pool> p = pools(a[2], "pools", s.num_pages);
+  const Pools p = pools(a[2], "pools", s.num_pages);
   const bool inplace = truth(a[3]);
   const Tensor t = inplace ? table : at::empty_strided(table.sizes(), {s.table_stride, 1}, table.options());
   const Tensor r = inplace ? ref : at::empty_like(ref);
   const Tensor moves = at::empty({}, ref.options()), ws = pages_workspace(s, 0, ref);
-  check(api.pages_compact(&s, i32(table), i32(ref), i32(t), i32(r), p.data(), (int)p.size(), i32(moves), ws.data_ptr(), ws.nbytes(),
+  check(api.pages_compact(&s, i32(table), i32(ref), i32(t), i32(r), p.data(), p.size(), i32(moves), ws.data_ptr(), ws.nbytes(),
                           (gdn_stream_t)stream(ref)),
         "gdn_pages_compact");
+  if (inplace) wrote({&table, &ref});
+  p.wrote_all();
   return pack({t, r, moves});
 }
 
@@ -418,9 +443,10 @@ PyObject *copy_slots(PyObject *const *a) {
   const Tensor &src = tensor(a[1], "src"), &dst = tensor(a[2], "dst");
   ints(src, "src");
   ints(dst, "dst", src.numel());
-  const std::vector<gdn_slot_pool> p = pools(a[0], "pools", 0);
-  check(api.slots_copy(p.data(), (int)p.size(), i32(src), i32(dst), fits(src.numel(), "the number of pairs"), (gdn_stream_t)stream(src)),
+  const Pools p = pools(a[0], "pools", 0);
+  check(api.slots_copy(p.data(), p.size(), i32(src), i32(dst), fits(src.numel(), "the number of pairs"), (gdn_stream_t)stream(src)),
         "gdn_slots_copy");
+  p.wrote_all();
   Py_RETURN_NONE;
 }
 
@@ -492,6 +518,7 @@ PyObject *rms_norm(PyObject *const *a) {
                         fp8 ? static_cast<float *>(scale.data_ptr()) : nullptr, static_cast<float *>(rstd.data_ptr()),
                         (gdn_stream_t)stream(x)),
         "gdn_rmsnorm_fwd");
+  if (inplace) wrote({res});
   return pack({y, h, scale, rstd});
 }
 

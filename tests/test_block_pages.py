@@ -237,6 +237,47 @@ def test_tables_whose_rows_share_memory_are_refused():
 
 
 @gpu
+def test_what_is_written_has_a_new_version():
+    """Autograd compares versions before it uses a saved tensor; every function counts its writes, also for inference
+    tensors (which have none) and pools that come from a generator."""
+    import gated_deltanet_linear_15_gb300 as g
+    d = Device(4, 6, 20, 16)
+
+    def moved(call, written, kept=()):
+        old = [t._version for t in written], [t._version for t in kept]
+        call()
+        assert all(t._version > v for t, v in zip(written, old[0])) and [t._version for t in kept] == old[1]
+
+    book, caches = [d.table, d.lens, d.ref], d.pools
+    moved(lambda: g.extend_pages(d.table, d.lens, d.ref, ints([0]), ints([20]), 16), book, caches)
+    moved(lambda: g.fork_pages(*book, ints([0]), ints([1]), (p for p in caches), 16, (s for s in [d.states])),
+          book + caches + [d.states])
+    moved(lambda: g.free_pages(*book, ints([0])), book, caches)
+    moved(lambda: g.compact_pages(d.table, d.ref, caches, inplace=False), caches, [d.table, d.ref])
+    moved(lambda: g.compact_pages(d.table, d.ref, caches), [d.table, d.ref] + caches, [d.lens])
+    moved(lambda: g.copy_slots(caches, ints([0]), ints([3])), caches)
+    q, k, v = (torch.randn(2, 2, 64, device=DEV) for _ in range(3))
+    kc, vc, out = torch.zeros(4, 16, 2, 64, device=DEV), torch.zeros(4, 16, 2, 64, device=DEV), torch.zeros_like(q)
+    cs, table, lens, pos = torch.ones(8, 32, 2, device=DEV), ints([[0], [1]]), ints([1, 1]), ints([0, 1])
+    moved(lambda: g.rotary(q, k, cs, pos, inplace=True), [q, k], [cs, pos])
+    moved(lambda: g.rotary(q, k, cs, pos), [], [q, k])
+    moved(lambda: g.rotary_append(q, k, v, cs, kc, vc, table, lens), [kc, vc], [q, k, v, table, lens])
+    moved(lambda: g.paged_attention(q, kc, vc, table, lens, out=out), [out], [q, kc, vc])
+    x, r, w = torch.randn(3, 64, device=DEV), torch.randn(3, 64, device=DEV), torch.ones(64, device=DEV)
+    moved(lambda: g.rms_norm(x, w, r), [], [x, r, w])
+    moved(lambda: g.rms_norm(x, w, r, inplace=True), [r], [x, w])
+    a = torch.randn(3, 64, device=DEV, requires_grad=True)
+    y = (a * r).sum()                            # saves r
+    g.rms_norm(x, w, r, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        x, r = torch.randn(3, 64, device=DEV), torch.randn(3, 64, device=DEV)
+        g.rms_norm(x, w, r, inplace=True)
+    g.rms_norm(x, w, r, inplace=True)
+
+
+@gpu
 def test_binding_refuses_pools_of_too_few_slots():
     """[layers, pages, ...] in place of one tensor for each layer, or states of another batch; more slots are no fault."""
     import gated_deltanet_linear_15_gb300 as g
