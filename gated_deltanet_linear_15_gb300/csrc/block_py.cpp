@@ -95,6 +95,11 @@ void heads(const Tensor &t, const char *name) {
   if (t.dim() != 3) bad(std::string(name) + " must have 3 dimensions [tokens, heads, features]");
   features(t, name);
 }
+// of a tensor that is written: no two of its elements may be one (an expanded dimension), or threads would race on it
+void written(const Tensor &t, const char *name) {
+  for (int64_t d = 0; d < t.dim(); ++d)
+    if (t.size(d) > 1 && t.stride(d) == 0) bad(std::string(name) + " is written, so it must not be expanded");
+}
 void same_type(const Tensor &t, const Tensor &q, const char *name) {
   if (t.scalar_type() != q.scalar_type()) bad(std::string(name) + " must have the dtype of the other inputs");
 }
@@ -128,6 +133,7 @@ void angle_table(const Tensor &t) {
 Tensor like(const Tensor *out, const Tensor &q) {
   if (!out) return at::empty(q.sizes(), q.options());
   heads(*out, "out");
+  written(*out, "out");
   same_type(*out, q, "out");
   if (out->sizes() != q.sizes()) bad("out must have the shape of q");
   return *out;
@@ -259,6 +265,8 @@ PyObject *rotary(PyObject *const *a) {
   s.table_rows = fits(table.size(0), "the table");
   s.interleaved = truth(a[4]);
   s.inverse = truth(a[5]);
+  if (inplace) written(q, "q");
+  if (inplace && k) written(*k, "k");
   const Tensor qo = inplace ? q : at::empty(q.sizes(), q.options());
   s.q_tok = q.stride(0);
   s.q_head = q.stride(1);
@@ -289,6 +297,8 @@ PyObject *rotary_append(PyObject *const *a) {
                &kc = tensor(a[4], "k_cache"), &vc = tensor(a[5], "v_cache"), &pages = tensor(a[6], "page_table"), &lens = tensor(a[7], "kv_lens");
   const Tensor *cu = maybe(a[8], "cu_q"), *out = maybe(a[10], "out");
   gdn_paged_shape s = paged_shape(q, kc, vc, pages, lens, cu);
+  written(kc, "k_cache");
+  written(vc, "v_cache");
   heads(k, "k");
   heads(v, "v");
   same_type(k, q, "k");

@@ -281,6 +281,27 @@ def test_append_through_one_table_row():
 
 
 @gpu
+def test_expanded_tensors_are_read_but_not_written():
+    """Heads that share memory may be turned into new tensors; in place, or as an output or a cache, they are refused."""
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(13)
+    one, q = torch.randn(5, 1, 64, generator=gen).to(DEV), torch.randn(5, 4, 64, generator=gen).to(DEV)
+    wide, table, pos = one.expand(-1, 4, -1), table_ref(8, 64).float().to(DEV), torch.arange(5, dtype=torch.int32, device=DEV)
+    a, b = g.rotary(wide, wide, table, pos)
+    close(a, ref.rotate(wide, table, pos), wide)
+    assert torch.equal(a, b)
+    kc, cache = torch.zeros(2, 16, 1, 64, device=DEV), torch.zeros(2, 16, 4, 64, device=DEV)
+    pages, lens = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([5], dtype=torch.int32, device=DEV)
+    for call in (lambda: g.rotary(wide, None, table, pos, inplace=True), lambda: g.rotary(q, wide, table, pos, inplace=True),
+                 lambda: g.rotary_append(q, q, q, table, kc.expand(-1, -1, 4, -1), cache, pages, lens),
+                 lambda: g.rotary_append(q, q, q, table, cache, kc.expand(-1, -1, 4, -1), pages, lens),
+                 lambda: g.rotary_append(q, q, q, table, cache, cache.clone(), pages, lens, out=torch.empty_like(one).expand(-1, 4, -1)),
+                 lambda: g.paged_attention(q, cache, cache, pages, lens, out=torch.empty_like(one).expand(-1, 4, -1))):
+        with pytest.raises(ValueError, match="expanded"):
+            call()
+
+
+@gpu
 def test_many_equal_sequences_without_cu():
     import gated_deltanet_linear_15_gb300 as g
     seqs = [(2, 2 + 3 * n) for n in range(50)]
