@@ -174,8 +174,8 @@ def load_py():
             import importlib.machinery
             import importlib.util
             if not os.path.exists(_build.PY_LIB):
-                raise ImportError(f"{_build.PY_LIB} is missing: build the library first "
-                                  "(gated_deltanet_linear_15_gb300.build.build() or __graft_entry__.build())")
+                raise ImportError(f"{_build.PY_LIB} is missing: build the library first, with this torch and Python "
+                                  "(gated_deltanet_linear_15_gb300.build.build(), which says why where it cannot)")
             loader = importlib.machinery.ExtensionFileLoader("gdn_block_py", _build.PY_LIB)
             mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_block_py", _build.PY_LIB, loader=loader))
             loader.exec_module(mod)
