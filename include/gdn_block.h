@@ -203,7 +203,8 @@ typedef struct {
 /* h = x + residual (just x without one), rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd (weight + weight_offset).
  * residual and h_out may be NULL (h_out may be x or residual); rstd fp32 [T] or NULL; weight fp32 [D].  The norm is
  * that of the fp32 sum, before its rounding to h_out.  fp8: scale fp32 [T, D / group] (or [T]) = amax / 448 of the
- * unrounded y, amax not below 1e-30, and y = round(y / scale) in e4m3. */
+ * unrounded y, amax not below 1e-30, and y in e4m3 = round(y * (448 / amax)), products and quotients in fp32 (as far from
+ * the exact quotient as y / scale in fp32; where that lies next to a tie the two may be an e4m3 step apart). */
 int gdn_rmsnorm_fwd(const gdn_norm_shape *shape, const void *x, const void *residual, const float *weight, void *h_out,
                     void *y, float *scale, float *rstd, gdn_stream_t stream);
 

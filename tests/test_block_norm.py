@@ -83,6 +83,22 @@ def test_fp8(T, D, group, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("D,group", [(256, 128), (256, 0), (257, 0)])
+def test_fp8_is_the_product_with_the_reciprocal_scale(D, group):
+    """With rstd = 1 and a weight of 1, y is x: the 8-bit output is fp32 x * (448 / amax), rounded to e4m3, bit for bit."""
+    import gated_deltanet_linear_15_gb300 as g
+    gen = torch.Generator().manual_seed(D + group)
+    x = rand(gen, 400, D)
+    x = x / x.double().square().mean(-1, keepdim=True).sqrt().float()
+    w = torch.ones(D, device=DEV)
+    got = g.rms_norm(x, w, fp8=True, group=group)
+    y = x * got.rstd[:, None]
+    b = y.view(400, -1, group or D)
+    inv = torch.full((), 448.0, device=DEV) / b.abs().amax(-1, keepdim=True).clamp(min=1e-30)
+    assert torch.equal(got.y.float().view_as(b), (b * inv).clamp(-448, 448).to(torch.float8_e4m3fn).float())
+
+
+@gpu
 def test_fp8_edges():
     """A row of zeros gives zeros and the floor's scale, a group of tiny values keeps its precision, NaN stays NaN in its
     row only, one huge value leaves the others at zero or nearly."""
