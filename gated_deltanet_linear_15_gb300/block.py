@@ -6,7 +6,8 @@ the cache), ``extend_pages`` / ``fork_pages`` / ``free_pages`` / ``compact_pages
 upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual stream's norm, optionally with an 8-bit
 output).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
 arguments are checked, and outputs and workspaces allocated, by the extension csrc/block_py.cpp.  Bad arguments raise
-``ValueError`` (found there) or ``RuntimeError`` (found by the library, with its reason).
+``ValueError`` (found there) or ``RuntimeError`` (found by the library, with its reason), a lack of memory
+``torch.OutOfMemoryError``.
 
 Gradients come from ``rotary_embedding`` and ``residual_rms_norm``.  Every other function computes outside autograd, as
 the ``_fwd`` / ``_bwd`` functions of the delta rule do: its outputs carry no graph, whatever its inputs require.  What a

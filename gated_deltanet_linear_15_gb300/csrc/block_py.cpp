@@ -588,6 +588,11 @@ template <PyObject *(*F)(PyObject *const *), int N> PyObject *entry(PyObject *, 
     return F(args);
   } catch (const ValueError &e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::OutOfMemoryError &e) {  // of an output or a workspace: callers may free memory and try again
+    PyObject *torch = PyImport_ImportModule("torch"), *type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception &e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

@@ -302,6 +302,15 @@ def test_expanded_tensors_are_read_but_not_written():
 
 
 @gpu
+def test_lack_of_memory_is_named():
+    """An output of 2 TB for an expanded input."""
+    import gated_deltanet_linear_15_gb300 as g
+    q = torch.zeros(4, 1, 128, dtype=BF, device=DEV).expand(-1, 2 ** 31 - 1, -1)
+    with pytest.raises(torch.OutOfMemoryError):
+        g.rotary(q, None, table_ref(8, 128).float().to(DEV), torch.arange(4, dtype=torch.int32, device=DEV))
+
+
+@gpu
 def test_many_equal_sequences_without_cu():
     import gated_deltanet_linear_15_gb300 as g
     seqs = [(2, 2 + 3 * n) for n in range(50)]
