@@ -35,11 +35,6 @@ constexpr float RAISED = 1099511627776.f;  // 2^40: a block's weights that sum t
 constexpr uint32_t WAIT_LIMIT = 1u << 18;   // polls of 3.8 us when nothing comes: a second
 constexpr uint32_t DRAIN_LIMIT = 1u << 16;  // of each stage or tile after that
 
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn_major, bool neg_a) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((neg_a ? 1u : 0u) << 13) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
 template <int D> struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr int QT = 128 * D * 2;      // bytes of a query tile
@@ -56,11 +51,6 @@ struct Bars {
   uint3 stages;  // the loader's next stage and its parity at the end, and how many before it have been filled
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 // D[tmem] (+)= A[tmem] * B
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, SDesc b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -72,13 +62,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, SDesc b
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n"
       "}\n" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate));
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];\n" ::"r"(smem_dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
-      : "memory");
 }
 // 32 lanes x 32 columns, not waited for
 __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t *r) {
@@ -349,7 +332,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     // ------------------------------------------------------------ products of tile x
     const int x = (warp - 8) >> 1;
     Cursor &cur = cursors[warp];
-    const uint32_t id_s = idesc_bf16(128, BN, false, neg != 0), id_o = idesc_bf16(128, D, true, false);
+    const uint32_t id_s = idesc_bf16(128, BN, false, false, neg != 0), id_o = idesc_bf16(128, D, false, true);
     const uint32_t ts = tmem + TM_S + x * BN, to = tmem + TM_O + x * D;
     uint32_t st = 0, ph = 0, pq = 0;  // ring stage and its parity, parity of the tile's query barrier
     bool ok = true;                   // no wait of this warp has expired

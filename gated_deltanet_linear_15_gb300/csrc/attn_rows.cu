@@ -43,11 +43,6 @@ namespace {
 constexpr int SLICES = 4;
 constexpr float RAISE = 8.f;  // log2 of the growth of a row's maximum that is left in its weights
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -89,10 +84,6 @@ __device__ __forceinline__ void mma_3tf32(float (&c)[N][4], const uint32_t (&ah)
   mma_tf32(c[1 % N], ah, l0, l1);
   mma_tf32(c[2 % N], ah, h0, h1);
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&b);
-}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -101,13 +92,6 @@ __device__ __forceinline__ float quad_max(float x) {
 // byte offset of 16-byte chunk c of row r in a tile of `ROWS` rows: boxes of 128 bytes by ROWS rows, 128-byte swizzle
 template <int ROWS> __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return (c >> 3) * (ROWS * 128) + r * 128 + (((c ^ r) & 7) << 4);
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];\n" ::"r"(smem_dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(mbar)
-      : "memory");
 }
 // Bounded wait that polls with the plain test: a slice is mostly there or about to be, and the test that may suspend costs
 // more than it saves (64 sequences of 512 .. 16384 tokens: 336 us against 345 us).  The limit is about a second.
@@ -467,10 +451,10 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
           uint32_t pa[4];
-          pa[0] = pack2(s[2 * u][0], s[2 * u][1]);
-          pa[1] = pack2(s[2 * u][2], s[2 * u][3]);
-          pa[2] = pack2(s[2 * u + 1][0], s[2 * u + 1][1]);
-          pa[3] = pack2(s[2 * u + 1][2], s[2 * u + 1][3]);
+          pa[0] = pack_bf16(s[2 * u][0], s[2 * u][1]);
+          pa[1] = pack_bf16(s[2 * u][2], s[2 * u][3]);
+          pa[2] = pack_bf16(s[2 * u + 1][0], s[2 * u + 1][1]);
+          pa[3] = pack_bf16(s[2 * u + 1][2], s[2 * u + 1][3]);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             uint32_t bv[4];
@@ -569,7 +553,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
         if constexpr (F32) {
           *reinterpret_cast<float4 *>(op) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         } else {
-          *reinterpret_cast<uint2 *>(op) = make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+          *reinterpret_cast<uint2 *>(op) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         }
         if (a.lse && c == 0)
           a.lse[(long long)tok * a.Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
