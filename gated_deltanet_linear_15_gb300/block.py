@@ -68,8 +68,10 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] =
 
     scaling None: base^(-2 i / rot).  "linear": positions stretched by `factor`.  "base": the base raised so that the
     slowest pair is stretched by `factor` and the fastest is kept.  "parts": pairs that turn fewer than `slow` times over
-    the original `context` are stretched, those that turn more than `fast` times are kept, the ones between are blended;
-    the amplitude grows by 0.1 ln(factor) + 1."""
+    the original `context` are stretched, those that turn more than `fast` times are kept, and the share that is kept of
+    those between grows linearly with their turns (not with their index); for factor > 1 the amplitude is
+    0.1 ln(factor) + 1.  With another blend or amplitude a program forms the table itself: any fp32 tensor [positions,
+    rot / 2, 2] of (amplitude cos, amplitude sin)."""
     if rot < 2 or rot % 2:
         raise ValueError("rot must be even and at least 2")
     if factor <= 0 or base <= 1:

@@ -110,7 +110,8 @@ typedef struct {
   int head_dim;            /* D >= 2                                                     */
   int rot;                 /* even, 2 <= rot <= D                                        */
   int interleaved;         /* 0 or 1                                                     */
-  int inverse;             /* 1: turn back (the gradient of the turn)                    */
+  int inverse;             /* 1: turn by the opposite angle, which is the gradient of    */
+                           /* the turn, and undoes it where the amplitude is 1           */
   int table_rows;
   gdn_dtype dtype;
   int reserved;            /* must be 0                                                  */
