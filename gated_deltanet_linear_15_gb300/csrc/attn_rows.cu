@@ -719,7 +719,8 @@ cudaError_t launch_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtenso
 // 16 rows a tile where that is enough, and in fp32 with D = 64 always: 96 KB of rings (fp32, D = 128: 192 KB) and then two
 // CTAs per SM.  More rows: two row groups and 192 KB of rings, so that a key or value is fetched and, in fp32, split into
 // its two parts half as often (fp32: D = 64, 8 sequences of up to 256 new tokens: 44 us with 16 rows, 47 us with 32, the last
-// 1024 of 4096 tokens: 313 and 324 us; D = 128, 512 new tokens after 3584: 530 us with 16 rows, 317 us with 32).
+// 1024 of 4096 tokens: 313 and 324 us; D = 128, 512 new tokens after 3584: 530 us with 16 rows, 317 us with 32; both sides
+// before the guard in split_tf32, which adds 1 to 3 %).
 int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 || (!bf && D == 64) ? 16 : 32; }
 int attn_rows_box(bool bf, int MT, int page) { return bf && MT == 32 && page >= 32 ? 32 : 16; }
 int attn_rows_per_sm(bool bf, int D, int MT) { return MT == 16 && (bf || D == 64) ? 2 : 1; }
