@@ -118,7 +118,7 @@ def rotary(q, k, table, positions, interleaved: bool = False, inverse: bool = Fa
 
 class RotaryFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, table, positions, interleaved, inverse=False):
+    def forward(ctx, q, k, table, positions, interleaved, inverse):
         ctx.save_for_backward(table, positions)
         ctx.interleaved, ctx.inverse = interleaved, inverse
         return rotary(q, k, table, positions, interleaved, inverse)
@@ -134,7 +134,7 @@ class RotaryFunction(torch.autograd.Function):
 
 def rotary_embedding(q, k, table, positions, interleaved: bool = False):
     """``rotary`` with gradients of any order for q and k (or q alone, with k None)."""
-    return RotaryFunction.apply(q, k, table, positions, interleaved)
+    return RotaryFunction.apply(q, k, table, positions, interleaved, False)
 
 
 def rotary_append(q, k, v, table, k_cache, v_cache, page_table, kv_lens, cu_q=None, interleaved: bool = False, out=None):

@@ -88,7 +88,8 @@ struct AttnPlan {
 AttnPlan attn_plan(const gdn_paged_shape *s) {
   AttnPlan p;
   const int G = s->num_heads / s->num_kv_heads;
-  const long long rows = (long long)(s->max_q > 0 ? s->max_q : (s->total_q + s->num_seqs - 1) / std::max(1, s->num_seqs)) * G;
+  const long long mean = ((long long)s->total_q + s->num_seqs - 1) / std::max(1, s->num_seqs);
+  const long long rows = (s->max_q > 0 ? s->max_q : mean) * G;
   const bool bf = s->dtype == GDN_BF16;
   p.tc = bf && rows > 32;
   p.MT = p.tc ? 256 : attn_rows_tile(bf, s->head_dim, (int)std::min(rows, 1ll << 20));

@@ -258,7 +258,7 @@ cudaError_t launch_rope(const RopeArgs &a, bool bf, bool vec, cudaStream_t st) {
   int slots = 64 / uph > 0 ? 64 / uph : 1;
   while (slots < a.heads && 2 * slots * uph <= NTR && (long long)a.tokens * slots * uph < 152ll * 4 * NTR) slots *= 2;
   const int tpb = NTR / (slots * uph);
-  const dim3 grid((unsigned)((a.tokens + tpb - 1) / tpb));
+  const dim3 grid(((unsigned)a.tokens + tpb - 1) / tpb);
   return bf ? launch_pdl(rope_kernel<bf16, 3>, grid, dim3(NTR), 0, st, a, uph, slots)
             : launch_pdl(rope_kernel<float, 2>, grid, dim3(NTR), 0, st, a, uph, slots);
 }

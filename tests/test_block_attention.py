@@ -570,6 +570,17 @@ def test_c_entry_refuses_shapes(lib, kw, code):
     assert lib.gdn_paged_attn_workspace_size(ctypes.byref(s)) == 0
 
 
+def test_plan_of_the_largest_counts(lib):
+    """2^31 - 1 tokens in a few sequences take the kernel, and the scratch memory, of other long chunks; in as many sequences
+    as tokens those of a decode step."""
+    def need(t, n):
+        return lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(num_heads=2, total_q=t, num_seqs=n, max_q=0)))
+
+    most = 2 ** 31 - 1
+    assert need(most, 2) == need(1 << 20, 2) > 0
+    assert need(most, most) == need(8, 8) > 0
+
+
 def test_c_entry_knows_the_debug_hook(lib):
     hook = _lib.GDN_DEBUG_WAIT_TIMEOUT - (1 << 32)
     assert lib.gdn_paged_attn_workspace_size(ctypes.byref(_shape(reserved=hook))) > 0
