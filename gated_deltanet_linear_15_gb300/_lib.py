@@ -71,6 +71,11 @@ class GdnNormShape(ctypes.Structure):
                 ("x_row", _L), ("r_row", _L), ("h_row", _L), ("y_row", _L), ("reserved", _I * 2)]
 
 
+class GdnScanShape(ctypes.Structure):
+    _fields_ = [("num_seqs", _I), ("tokens", _I), ("dim", _I), ("dtype", _I), ("gate_dtype", _I), ("reserved", _I),
+                ("x_row", _L), ("g_row", _L), ("y_row", _L), ("dy_row", _L), ("dg_row", _L), ("state_row", _L)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -144,13 +149,17 @@ def load():
                 "gdn_pages_free": [P] * 5 + [_I, P],
                 "gdn_pages_compact": [P] * 6 + [_I, P, P, Z, P],
                 "gdn_rmsnorm_fwd": [P] * 9,
-                "gdn_rmsnorm_bwd": [P] * 9 + [Z, P]}.items():
+                "gdn_rmsnorm_bwd": [P] * 9 + [Z, P],
+                "gdn_scan_fwd": [P] * 9,
+                "gdn_scan_bwd": [P] * 12,
+                "gdn_scan_step": [P] * 6}.items():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         for name, args in {"gdn_paged_attn_workspace_size": [P], "gdn_pages_workspace_size": [P, _I],
                            "gdn_rmsnorm_bwd_workspace_size": [P]}.items():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = Z
+        lib.gdn_scan_states_rows.argtypes, lib.gdn_scan_states_rows.restype = [P], _L
         _lib = lib
         return lib
 
@@ -158,8 +167,8 @@ def load():
 # the C entry points that csrc/block_py.cpp calls, in the order of its table
 _PY_CALLS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_paged_attn_status", "gdn_rotary", "gdn_rotary_append",
              "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork", "gdn_pages_free",
-             "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd", "gdn_status_string",
-             "gdn_last_error_string")
+             "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd", "gdn_scan_states_rows",
+             "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_status_string", "gdn_last_error_string")
 _py = None
 
 

@@ -4,12 +4,13 @@
 ``rotary_embedding`` / ``rotary_append`` (rotary positions, their gradient, and the write of new keys and values into
 the cache), ``extend_pages`` / ``fork_pages`` / ``free_pages`` / ``compact_pages`` / ``copy_slots`` (the cache's
 upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual stream's norm, optionally with an 8-bit
-output).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
+output), ``gated_scan`` / ``gated_scan_bwd`` / ``gated_linear_recurrence`` / ``gated_scan_step`` (a gated linear recurrence with
+one state per channel: forward, backward, with gradients, and for single tokens).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
 arguments are checked, and outputs and workspaces allocated, by the extension csrc/block_py.cpp.  Bad arguments raise
 ``ValueError`` (found there) or ``RuntimeError`` (found by the library, with its reason), a lack of memory
 ``torch.OutOfMemoryError``.
 
-Gradients come from ``rotary_embedding`` and ``residual_rms_norm``.  Every other function computes outside autograd, as
+Gradients come from ``rotary_embedding``, ``residual_rms_norm`` and ``gated_linear_recurrence``.  Every other function computes outside autograd, as
 the ``_fwd`` / ``_bwd`` functions of the delta rule do: its outputs carry no graph, whatever its inputs require.  What a
 function writes in place counts as an in-place operation (its version moves on).
 """
@@ -25,7 +26,8 @@ from . import _lib
 
 __all__ = ["paged_attention", "paged_attention_status", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding",
            "rotary_append", "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_slots", "rms_norm",
-           "rms_norm_bwd", "residual_rms_norm", "NormOutput"]
+           "rms_norm_bwd", "residual_rms_norm", "NormOutput", "gated_scan", "gated_scan_bwd", "gated_scan_step",
+           "gated_linear_recurrence"]
 
 
 class _Extension:
@@ -220,3 +222,50 @@ class ResidualRMSNormFunction(torch.autograd.Function):
 def residual_rms_norm(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0):
     """``rms_norm`` with (first) gradients: (y, h), or y alone without a residual."""
     return ResidualRMSNormFunction.apply(x, residual, weight, eps, weight_offset)
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+def gated_scan(x, g, initial_state=None, cu_seqlens=None, output_final_state: bool = True, save_states: bool = False):
+    """h_t = exp(g_t) h_{t-1} + x_t in every channel; y_t = h_t.
+
+    x [sequences, tokens, D] (rows of one stride), g like x in its dtype or fp32: the log-gates, meant to be <= 0 (-inf
+    forgets).  Packed sequences: x [1, tokens, D] and cu_seqlens int32 [sequences + 1] on the device; rows that no sequence
+    names stay uninitialised in y.  initial_state fp32 [sequences, D] (None: zeros).  Returns (y, final state fp32 [sequences, D], or None
+    without output_final_state), and with save_states the states that ``gated_scan_bwd`` reads."""
+    y, final, states = _py.gated_scan(x, g, initial_state, cu_seqlens, output_final_state, save_states)
+    return (y, final, states) if save_states else (y, final)
+
+
+def gated_scan_bwd(dy, x, g, states, initial_state=None, d_final=None, cu_seqlens=None):
+    """(dx, dg, gradient of initial_state or None) from dy, d_final (fp32 [sequences, D], the gradient of the final states;
+    None: zero) and the forward's inputs and ``save_states`` output."""
+    return _py.gated_scan_bwd(dy, x, g, states, initial_state, d_final, cu_seqlens)
+
+
+def gated_scan_step(x, g, state):
+    """One token of each sequence: state fp32 [sequences, D] becomes exp(g) state + x in place.  x, g [sequences, D].
+    Returns (y, state), y the new state in x's dtype."""
+    return _py.gated_scan_step(x, g, state), state
+
+
+class GatedLinearRecurrenceFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, initial_state, cu_seqlens):
+        y, final, states = gated_scan(x, g, initial_state, cu_seqlens, save_states=True)
+        ctx.save_for_backward(x, g, states, initial_state, cu_seqlens)
+        ctx.set_materialize_grads(False)
+        return y, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, d_final):
+        x, g, states, initial_state, cu_seqlens = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else dy.contiguous()
+        d_final = None if d_final is None else d_final.contiguous()
+        dx, dg, dh0 = gated_scan_bwd(dy, x, g, states, initial_state, d_final, cu_seqlens)
+        return dx, dg, dh0, None
+
+
+def gated_linear_recurrence(x, g, initial_state=None, cu_seqlens=None):
+    """``gated_scan`` with (first) gradients for x, g and initial_state: (y, final state)."""
+    return GatedLinearRecurrenceFunction.apply(x, g, initial_state, cu_seqlens)

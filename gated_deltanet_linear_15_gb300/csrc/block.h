@@ -83,4 +83,19 @@ int norm_bwd_ctas(const NormArgs &a, bool bf16_type, bool vec, int sms);
 cudaError_t launch_norm_fwd(const NormArgs &a, bool bf16_type, bool vec, int sms, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs &a, bool bf16_type, bool vec, int sms, cudaStream_t st);
 
+// ---- gated linear recurrence
+constexpr int SCAN_SEG = 16;  // tokens between two stored states
+struct ScanArgs {
+  const void *x, *g, *dy;
+  void *y, *dg;             // y: backward dx
+  const float *h0, *dhT;
+  float *hT, *dh0, *states; // hT: step the state; states: read by the backward
+  const int *cu;
+  int N, tokens, T, D;      // T: tokens of each sequence without cu
+  long long x_row, g_row, y_row, dy_row, dg_row, h_row;
+};
+// move: bytes of an access that every row allows: 16, 4, or 2 (single bf16 elements)
+cudaError_t launch_scan(const ScanArgs &a, bool bf16_type, bool bf16_gate, int move, bool bwd, int sms, cudaStream_t st);
+cudaError_t launch_scan_step(const ScanArgs &a, bool bf16_type, bool bf16_gate, bool vec, cudaStream_t st);
+
 }  // namespace gdn

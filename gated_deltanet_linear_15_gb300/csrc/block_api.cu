@@ -1,7 +1,8 @@
 // C entry points of include/gdn_block.h: argument checks, workspace layout and launches of the operators next to the
-// delta rule (paged attention, rotary positions, cache pages, root-mean-square norm).
+// delta rule (paged attention, rotary positions, cache pages, root-mean-square norm, gated linear recurrence).
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <vector>
 
 #include "block.h"
@@ -192,6 +193,65 @@ int check_row(int64_t row, const gdn_norm_shape *s, const char *name) {
   return s->rows > 1 && row < s->dim ? fail(GDN_ERR_INVALID_ARG, "%s is smaller than dim", name) : GDN_OK;
 }
 bool vec_ok(const void *p, int64_t row, int v) { return !p || (aligned16(p) && row % v == 0); }
+
+// ------------------------------------------------------------------ gated linear recurrence
+int check_scan(const gdn_scan_shape *s) {
+  if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
+  if (s->reserved) return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
+  if (s->dtype != GDN_BF16 && s->dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "unknown dtype");
+  if (s->gate_dtype != s->dtype && s->gate_dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "gate_dtype must be dtype or fp32");
+  if (s->num_seqs < 1 || s->tokens < 0) return fail(GDN_ERR_INVALID_ARG, "need num_seqs >= 1, tokens >= 0");
+  if (s->tokens > 0x7fff0000) return fail(GDN_ERR_UNSUPPORTED, "too many tokens");
+  if (s->dim < 1 || s->dim > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "dim must be 1 .. 2^20 (got %d)", s->dim);
+  if (s->x_row < 0 || s->g_row < 0 || s->y_row < 0 || s->dy_row < 0 || s->dg_row < 0 || s->state_row < 0)
+    return fail(GDN_ERR_INVALID_ARG, "row strides must be >= 0");
+  return GDN_OK;
+}
+// rows written must not overlap one another
+int check_scan_row(int64_t row, const gdn_scan_shape *s, const char *name) {
+  return s->tokens > 1 && row < s->dim ? fail(GDN_ERR_INVALID_ARG, "%s is smaller than dim", name) : GDN_OK;
+}
+ScanArgs scan_args(const gdn_scan_shape *s, const void *x, const void *g, const int32_t *cu) {
+  ScanArgs a = {};
+  a.x = x;
+  a.g = g;
+  a.cu = cu;
+  a.N = s->num_seqs;
+  a.tokens = s->tokens;
+  a.T = cu ? 0 : s->tokens / s->num_seqs;
+  a.D = s->dim;
+  a.x_row = s->x_row;
+  a.g_row = s->g_row;
+  a.y_row = s->y_row;
+  a.dy_row = s->dy_row;
+  a.dg_row = s->dg_row;
+  a.h_row = s->state_row;
+  return a;
+}
+// whether rows and pointer allow accesses of `bytes` that do not leave the row's features
+struct Access {
+  int move = 16;
+  void add(const void *p, int64_t row, int es, int dim) {
+    for (; move > 2; move = move == 16 ? 4 : 2)
+      if (reinterpret_cast<uintptr_t>(p) % move == 0 && row * es % move == 0 && (int64_t)dim * es % move == 0) return;
+  }
+};
+// the bytes of an access for a call: rows as in m; the fp32 states go by pairs of channels then, or singly with single ones
+int scan_move(const Access &m, const gdn_scan_shape *s, std::initializer_list<const float *> states) {
+  int move = m.move;
+  for (const float *p : states)
+    if (p && reinterpret_cast<uintptr_t>(p) % 8) move = std::min(move, s->dtype == GDN_FP32 ? 4 : 2);
+  // without 16-byte pieces, channels of bf16 go in pairs and of fp32 singly; rows of both types at once go singly
+  if (move == 4 && s->dtype != s->gate_dtype) move = 2;
+  return move;
+}
+// no tokens at all: every state passes through
+int scan_no_tokens(const gdn_scan_shape *s, const float *in, float *out, Stream st) {
+  const size_t n = (size_t)s->num_seqs * s->dim * sizeof(float);
+  if (out && in) CK(cudaMemcpyAsync(out, in, n, cudaMemcpyDeviceToDevice, st));
+  else if (out) CK(cudaMemsetAsync(out, 0, n, st));
+  return GDN_OK;
+}
 
 }  // namespace
 
@@ -552,6 +612,97 @@ int gdn_rmsnorm_bwd(const gdn_norm_shape *s, const void *dy, const void *h, cons
   const Stream st = (Stream)stream;
   PROF("rmsnorm_bwd");
   CK(launch_norm_bwd(a, s->dtype == GDN_BF16, vec, num_sms(), st));
+  return GDN_OK;
+}
+
+int64_t gdn_scan_states_rows(const gdn_scan_shape *s) {
+  if (check_scan(s)) return -1;
+  return ((int64_t)s->tokens + SCAN_SEG - 1) / SCAN_SEG;
+}
+
+int gdn_scan_fwd(const gdn_scan_shape *s, const void *x, const void *g, const float *h0, const int32_t *cu, void *y, float *final,
+                 float *states, gdn_stream_t stream) {
+  TRY(check_scan(s));
+  if (!cu && s->tokens % s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "without cu_seqlens, tokens must be a multiple of num_seqs");
+  TRY(check_scan_row(s->y_row, s, "y_row"));
+  const Stream st = (Stream)stream;
+  if (s->tokens == 0) return scan_no_tokens(s, h0, final, st);
+  TRY(need_ptr(x, "x"));
+  TRY(need_ptr(g, "g"));
+  TRY(need_ptr(y, "y"));
+  if (y == x || y == g) return fail(GDN_ERR_INVALID_ARG, "y is one of the inputs");
+  if (final && final == h0) return fail(GDN_ERR_INVALID_ARG, "final is h0");
+  ScanArgs a = scan_args(s, x, g, cu);
+  a.y = y;
+  a.h0 = h0;
+  a.hT = final;
+  a.states = states;
+  const int e = (int)esize(s->dtype), eg = (int)esize(s->gate_dtype);
+  Access m;
+  m.add(x, s->x_row, e, s->dim);
+  m.add(g, s->g_row, eg, s->dim);
+  m.add(y, s->y_row, e, s->dim);
+  PROF("scan_fwd");
+  CK(launch_scan(a, s->dtype == GDN_BF16, s->gate_dtype == GDN_BF16, scan_move(m, s, {h0, final, states}), false, num_sms(), st));
+  return GDN_OK;
+}
+
+int gdn_scan_bwd(const gdn_scan_shape *s, const void *dy, const void *x, const void *g, const float *states, const float *h0,
+                 const float *d_final, const int32_t *cu, void *dx, void *dg, float *dh0, gdn_stream_t stream) {
+  TRY(check_scan(s));
+  if (!cu && s->tokens % s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "without cu_seqlens, tokens must be a multiple of num_seqs");
+  TRY(check_scan_row(s->y_row, s, "y_row"));
+  TRY(check_scan_row(s->dg_row, s, "dg_row"));
+  const Stream st = (Stream)stream;
+  if (s->tokens == 0) return scan_no_tokens(s, d_final, dh0, st);
+  TRY(need_ptr(dy, "dy"));
+  TRY(need_ptr(x, "x"));
+  TRY(need_ptr(g, "g"));
+  TRY(need_ptr(states, "states"));
+  TRY(need_ptr(dx, "dx"));
+  TRY(need_ptr(dg, "dg"));
+  if (dx == dg || dx == dy || dx == x || dx == g || dg == dy || dg == x || dg == g)
+    return fail(GDN_ERR_INVALID_ARG, "dx and dg need memory of their own");
+  if (dh0 && (dh0 == d_final || dh0 == h0)) return fail(GDN_ERR_INVALID_ARG, "dh0 is one of the inputs");
+  ScanArgs a = scan_args(s, x, g, cu);
+  a.dy = dy;
+  a.y = dx;
+  a.dg = dg;
+  a.h0 = h0;
+  a.dhT = d_final;
+  a.dh0 = dh0;
+  a.states = const_cast<float *>(states);
+  const int e = (int)esize(s->dtype), eg = (int)esize(s->gate_dtype);
+  Access m;
+  m.add(x, s->x_row, e, s->dim);
+  m.add(dy, s->dy_row, e, s->dim);
+  m.add(g, s->g_row, eg, s->dim);
+  m.add(dx, s->y_row, e, s->dim);
+  m.add(dg, s->dg_row, eg, s->dim);
+  PROF("scan_bwd");
+  CK(launch_scan(a, s->dtype == GDN_BF16, s->gate_dtype == GDN_BF16, scan_move(m, s, {h0, d_final, dh0, states}), true, num_sms(), st));
+  return GDN_OK;
+}
+
+int gdn_scan_step(const gdn_scan_shape *s, const void *x, const void *g, float *state, void *y, gdn_stream_t stream) {
+  TRY(check_scan(s));
+  if (s->tokens != s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "a step takes one token of each sequence");
+  TRY(check_scan_row(s->y_row, s, "y_row"));
+  TRY(check_scan_row(s->state_row, s, "state_row"));
+  TRY(need_ptr(x, "x"));
+  TRY(need_ptr(g, "g"));
+  TRY(need_ptr(state, "state"));
+  TRY(need_ptr(y, "y"));
+  if (y == x || y == g || y == state || state == x || state == g) return fail(GDN_ERR_INVALID_ARG, "y and state need memory of their own");
+  ScanArgs a = scan_args(s, x, g, nullptr);
+  a.y = y;
+  a.hT = state;
+  auto four = [&](const void *p, int64_t row, size_t es) { return reinterpret_cast<uintptr_t>(p) % (4 * es) == 0 && row % 4 == 0; };
+  const bool vec = s->dim % 4 == 0 && four(x, s->x_row, esize(s->dtype)) && four(g, s->g_row, esize(s->gate_dtype)) &&
+                   four(y, s->y_row, esize(s->dtype)) && four(state, s->state_row, 4);
+  const Stream st = (Stream)stream;
+  PROF("scan_step");
+  CK(launch_scan_step(a, s->dtype == GDN_BF16, s->gate_dtype == GDN_BF16, vec, st));
   return GDN_OK;
 }
 

@@ -38,6 +38,10 @@ struct Api {
   decltype(&gdn_rmsnorm_fwd) rmsnorm_fwd;
   decltype(&gdn_rmsnorm_bwd_workspace_size) rmsnorm_bwd_workspace_size;
   decltype(&gdn_rmsnorm_bwd) rmsnorm_bwd;
+  decltype(&gdn_scan_states_rows) scan_states_rows;
+  decltype(&gdn_scan_fwd) scan_fwd;
+  decltype(&gdn_scan_bwd) scan_bwd;
+  decltype(&gdn_scan_step) scan_step;
   decltype(&gdn_status_string) status_string;
   decltype(&gdn_last_error_string) last_error_string;
 } api;
@@ -566,6 +570,98 @@ PyObject *rms_norm_bwd(PyObject *const *a) {
   return pack({dx, dw});
 }
 
+// ------------------------------------------------------------------ gated linear recurrence
+int64_t line_stride(const Tensor &t, const char *name) { return t.numel() ? row_stride(t, name) : t.size(-1); }
+// x and g [..., D] of one shape; packed or not, cu counts the sequences
+gdn_scan_shape scan_shape(const Tensor &x, const Tensor &g, const Tensor *cu, bool step) {
+  features(x, "x");
+  features(g, "g");
+  gdn_scan_shape s = {};
+  s.dtype = dtype(x, "x");
+  s.gate_dtype = dtype(g, "g");
+  if (x.dim() != (step ? 2 : 3)) bad(step ? "x must be [sequences, features]" : "x must be [sequences, tokens, features]");
+  if (g.sizes() != x.sizes()) bad("x and g must have one shape");
+  if (cu) {
+    ints(*cu, "cu_seqlens");
+    if (cu->dim() != 1 || cu->size(0) < 2) bad("cu_seqlens must have an entry more than there are sequences, one at least");
+    if (x.size(0) != 1) bad("packed sequences have a first dimension of 1");
+  }
+  const int64_t n = cu ? cu->size(0) - 1 : x.size(0);
+  s.num_seqs = fits(n, "the number of sequences");
+  s.tokens = fits(step ? n : x.size(0) * x.size(1), "the number of tokens");
+  s.dim = fits(x.size(-1), "the number of features");
+  s.x_row = line_stride(x, "x");
+  s.g_row = line_stride(g, "g");
+  return s;
+}
+void scan_state(const Tensor &t, const gdn_scan_shape &s, const char *name) {
+  here(t, name);
+  if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != s.num_seqs || t.size(1) != s.dim || !t.is_contiguous())
+    bad(std::string(name) + " must be a contiguous fp32 CUDA tensor [sequences, features]");
+}
+float *f32(const Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; }
+const float *f32(const Tensor *t) { return t ? static_cast<const float *>(t->data_ptr()) : nullptr; }
+
+// x, g, initial_state, cu_seqlens, output_final_state, save_states -> (y, final, states)
+PyObject *gated_scan(PyObject *const *a) {
+  const Tensor &x = tensor(a[0], "x"), &g = tensor(a[1], "g");
+  const Tensor *h0 = maybe(a[2], "initial_state"), *cu = maybe(a[3], "cu_seqlens");
+  gdn_scan_shape s = scan_shape(x, g, cu, false);
+  if (h0) scan_state(*h0, s, "initial_state");
+  const Tensor y = at::empty(x.sizes(), x.options());
+  s.y_row = s.dim;
+  Tensor final, states;
+  if (truth(a[4])) final = at::empty({s.num_seqs, s.dim}, x.options().dtype(at::kFloat));
+  if (truth(a[5])) {
+    const int64_t rows = api.scan_states_rows(&s);
+    if (rows < 0) check(GDN_ERR_INVALID_ARG, "gdn_scan_states_rows");
+    states = at::empty({rows, s.dim}, x.options().dtype(at::kFloat));
+  }
+  check(api.scan_fwd(&s, x.data_ptr(), g.data_ptr(), f32(h0), i32(cu), y.data_ptr(), f32(final), f32(states), (gdn_stream_t)stream(x)),
+        "gdn_scan_fwd");
+  return pack({y, final, states});
+}
+
+// dy, x, g, states, initial_state, d_final, cu_seqlens -> (dx, dg, d_initial)
+PyObject *gated_scan_bwd(PyObject *const *a) {
+  const Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &g = tensor(a[2], "g"), &states = tensor(a[3], "states");
+  const Tensor *h0 = maybe(a[4], "initial_state"), *dT = maybe(a[5], "d_final"), *cu = maybe(a[6], "cu_seqlens");
+  gdn_scan_shape s = scan_shape(x, g, cu, false);
+  same_as(dy, x, "dy");
+  if (h0) scan_state(*h0, s, "initial_state");
+  if (dT) scan_state(*dT, s, "d_final");
+  const int64_t rows = api.scan_states_rows(&s);
+  if (rows < 0) check(GDN_ERR_INVALID_ARG, "gdn_scan_states_rows");
+  here(states, "states");
+  if (states.scalar_type() != at::kFloat || states.dim() != 2 || states.size(0) != rows || states.size(1) != s.dim || !states.is_contiguous())
+    bad("states must be what gated_scan with save_states returned for these inputs");
+  const Tensor dx = at::empty(x.sizes(), x.options()), dg = at::empty(g.sizes(), g.options());
+  s.dy_row = line_stride(dy, "dy");
+  s.y_row = s.dg_row = s.dim;
+  Tensor dh0;
+  if (h0) dh0 = at::empty({s.num_seqs, s.dim}, states.options());
+  check(api.scan_bwd(&s, dy.data_ptr(), x.data_ptr(), g.data_ptr(), f32(states), f32(h0), f32(dT), i32(cu), dx.data_ptr(), dg.data_ptr(),
+                     f32(dh0), (gdn_stream_t)stream(x)),
+        "gdn_scan_bwd");
+  return pack({dx, dg, dh0});
+}
+
+// x, g, state -> y
+PyObject *gated_scan_step(PyObject *const *a) {
+  const Tensor &x = tensor(a[0], "x"), &g = tensor(a[1], "g"), &state = tensor(a[2], "state");
+  gdn_scan_shape s = scan_shape(x, g, nullptr, true);
+  features(state, "state");
+  if (state.scalar_type() != at::kFloat || state.sizes() != x.sizes()) bad("state must be an fp32 CUDA tensor of x's shape");
+  written(state, "state");
+  s.state_row = row_stride(state, "state");
+  const Tensor y = at::empty(x.sizes(), x.options());
+  s.y_row = s.dim;
+  if (s.num_seqs == 0) return THPVariable_Wrap(y);
+  check(api.scan_step(&s, x.data_ptr(), g.data_ptr(), f32(state), y.data_ptr(), (gdn_stream_t)stream(x)), "gdn_scan_step");
+  wrote(state);
+  return THPVariable_Wrap(y);
+}
+
 // addresses of the C entry points, in the order of Api
 PyObject *connect(PyObject *const *a) {
   void **slot = reinterpret_cast<void **>(&api);
@@ -614,6 +710,9 @@ PyMethodDef methods[] = {ENTRY(connect, (int)(sizeof(Api) / sizeof(void *))),
                          ENTRY(copy_slots, 3),
                          ENTRY(rms_norm, 8),
                          ENTRY(rms_norm_bwd, 6),
+                         ENTRY(gated_scan, 6),
+                         ENTRY(gated_scan_bwd, 7),
+                         ENTRY(gated_scan_step, 3),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "gdn_block_py", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

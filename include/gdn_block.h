@@ -1,7 +1,7 @@
 /*
  * gdn_block.h -- C ABI of the operators that a hybrid stack puts next to its gated delta-rule layers (GB300,
  * sm_103a): attention of new tokens over a paged key/value cache, rotary positions, the upkeep of the cache's
- * pages, and the root-mean-square norm of the residual stream.
+ * pages, the root-mean-square norm of the residual stream, and a gated linear recurrence with one state per channel.
  *
  * A stack of gated delta-rule layers carries a softmax-attention layer after every few of them (onedev.kr summary
  * of the FlashQLA AICon 2026 talk, background paragraph: hybrids of three linear layers to one softmax layer).
@@ -215,6 +215,46 @@ int gdn_rmsnorm_fwd(const gdn_norm_shape *shape, const void *x, const void *resi
 size_t gdn_rmsnorm_bwd_workspace_size(const gdn_norm_shape *shape);
 int gdn_rmsnorm_bwd(const gdn_norm_shape *shape, const void *dy, const void *h, const float *weight, const float *rstd,
                     const void *dh, void *dx, float *dw, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------ gated linear recurrence
+ * The elementwise sister of the delta rule: one state per channel, the gate in its logarithm,
+ *     h_t = exp(g_t) h_{t-1} + x_t,   y_t = h_t.
+ * x, g, y [tokens, D] (row strides), the sequences one behind the other: token b * T + t of N equal ones of
+ * T = tokens / N, or cu_seqlens device int32 [N + 1] (not decreasing; rows that no sequence names are left as they were).
+ * h0 and final fp32 [N, D], contiguous: the states before and after each sequence (an empty one's passes through).
+ * Gates are meant to be <= 0 (-inf forgets); with larger ones every product of gates over consecutive tokens of a
+ * sequence has to stay finite.  Sums and states are fp32; a NaN or an infinity reaches what follows in its sequence and
+ * channel.  No output may share memory with an input.
+ */
+typedef struct {
+  int num_seqs;         /* N >= 1                                                        */
+  int tokens;           /* of all sequences; without cu_seqlens a multiple of N          */
+  int dim;              /* D, 1 .. 2^20                                                  */
+  gdn_dtype dtype;      /* of x, y, dy, dx                                               */
+  gdn_dtype gate_dtype; /* of g, dg: dtype or GDN_FP32                                   */
+  int reserved;         /* must be 0                                                     */
+  int64_t x_row, g_row; /* row strides                                                   */
+  int64_t y_row;        /* of y; backward: of dx                                         */
+  int64_t dy_row, dg_row; /* backward                                                    */
+  int64_t state_row;    /* step: of the state                                            */
+} gdn_scan_shape;
+
+/* states fp32 [gdn_scan_states_rows, D] or NULL: gets the state before every 16th token of the line, for the backward.
+ * h0 NULL: zeros.  final NULL: not wanted. */
+int64_t gdn_scan_states_rows(const gdn_scan_shape *shape);
+int gdn_scan_fwd(const gdn_scan_shape *shape, const void *x, const void *g, const float *h0 /* nullable */,
+                 const int32_t *cu_seqlens /* nullable */, void *y, float *final /* nullable */, float *states /* nullable */,
+                 gdn_stream_t stream);
+
+/* Gradients, given dy, d_final (of the final states; NULL: zero) and the forward's x, g, h0 and states:
+ *     d_t = dy_t + exp(g_{t+1}) d_{t+1} (the last token's: dy + d_final),  dx = d,  dg_t = exp(g_t) d_t h_{t-1},
+ *     dh0 = exp(g_0) d_0 (NULL: not wanted). */
+int gdn_scan_bwd(const gdn_scan_shape *shape, const void *dy, const void *x, const void *g, const float *states,
+                 const float *h0 /* nullable */, const float *d_final /* nullable */, const int32_t *cu_seqlens /* nullable */,
+                 void *dx, void *dg, float *dh0 /* nullable */, gdn_stream_t stream);
+
+/* One token of each sequence (tokens = N): state [N, D] fp32 (state_row) is updated in place, y is the new state. */
+int gdn_scan_step(const gdn_scan_shape *shape, const void *x, const void *g, float *state, void *y, gdn_stream_t stream);
 
 #ifdef __cplusplus
 }
