@@ -30,7 +30,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int SEG = SCAN_SEG, CB = 64, W = 8, NTH = 32 * W, MAXC = 8;  // MAXC: CTAs of a cluster
+constexpr int SEG = SCAN_SEG, CB = 64, STAGES = 3, MAXC = 8;  // MAXC: CTAs of a cluster
 
 // what moves rows: 16-byte pieces, 4-byte pieces, or single bf16 elements
 enum Move { M16, M4, M2 };
@@ -58,52 +58,64 @@ __device__ __forceinline__ void load_rows(E *dst, const E *src, long long row, i
     }
   } else {
     constexpr int B = M == M16 ? 16 : 4, V = B / (int)sizeof(E), PER = CB / V;  // pieces of a row
+    constexpr int RPI = PER < 32 ? 32 / PER : 1, CPI = PER < 32 ? PER : 32;       // rows and pieces of one instruction
+    const int r0 = lane / CPI;
 #pragma unroll
-    for (int i = 0; i < SEG * PER / 32; ++i) {
-      const int p = i * 32 + lane, r = p / PER, c = p % PER * V;
-      const bool ok = t0 + r >= lo && t0 + r < hi && c0 + c < D;
-      const E *s = ok ? src + (long long)(t0 + r) * row + c0 + c : src;
-      if constexpr (M == M16) cp_async16(dst + r * CB + c, s, ok);
-      else cp_async4(dst + r * CB + c, s, ok);
+    for (int k = 0; k < PER / CPI; ++k) {
+      const int c = (lane % CPI + 32 * k) * V;
+      const unsigned span = c0 + c < D ? hi - lo : 0, rel = t0 + r0 - lo;
+      const E *s = src + (long long)(t0 + r0) * row + c0 + c;
+#pragma unroll
+      for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) {
+        const bool ok = rel + i * RPI < span;
+        E *d = dst + (r0 + i * RPI) * CB + c;
+        if constexpr (M == M16) cp_async16(d, ok ? s : src, ok);
+        else cp_async4(d, ok ? s : src, ok);
+      }
     }
   }
 }
-template <typename E, int M> __device__ __forceinline__ void get2(const E *row, int lane, float (&v)[2]) {
+// the lane's two values of a row in shared memory
+template <typename E, int M> __device__ __forceinline__ uint64_t get2(const E *row, int lane) {
   using L = Lanes<E, M>;
   if constexpr (L::PAIR && sizeof(E) == 2) {
     const uint32_t u = *reinterpret_cast<const uint32_t *>(row + 2 * lane);
-    v[0] = __uint_as_float(u << 16);
-    v[1] = __uint_as_float(u & 0xffff0000u);
+    return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   } else if constexpr (L::PAIR) {
-    const float2 u = *reinterpret_cast<const float2 *>(row + 2 * lane);
-    v[0] = u.x;
-    v[1] = u.y;
+    return *reinterpret_cast<const uint64_t *>(row + 2 * lane);
   } else {
-    v[0] = tof(row[lane]);
-    v[1] = tof(row[lane + 32]);
+    return pk(tof(row[lane]), tof(row[lane + 32]));
+  }
+}
+// Gates of a row.  With bf16 rows the product with log2(e) and ex2.approx, off by 2^-22 of themselves, which a bf16 result does
+// not show and which the state carries for 16 tokens at most (its map takes expf of the sum); expf in fp32, where 16 such
+// errors would be half of all.
+template <bool EXACT> __device__ __forceinline__ uint64_t gates(uint64_t g) {
+  float a, b;
+  if constexpr (EXACT) {
+    upk(g, a, b);
+    return pk(expf(a), expf(b));
+  } else {
+    upk(mul2(g, pk(1.4426950408889634f, 1.4426950408889634f)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;\n" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;\n" : "+f"(b));
+    return pk(a, b);
   }
 }
 // a row of a block, the lane's channels, of which c is the first; only those below D exist
-template <typename E, bool PAIR> __device__ __forceinline__ void put2(E *row, int c, int D, const float (&v)[2]) {
+template <typename E, bool PAIR> __device__ __forceinline__ void put2(E *row, int c, int D, uint64_t p) {
+  float u, v;
+  upk(p, u, v);
   if constexpr (PAIR) {
-    if (c < D) st2(row + c, v[0], v[1]);
+    if (c < D) st2(row + c, u, v);
   } else {
-    if (c < D) row[c] = fromf<E>(v[0]);
-    if (c + 32 < D) row[c + 32] = fromf<E>(v[1]);
+    if (c < D) row[c] = fromf<E>(u);
+    if (c + 32 < D) row[c + 32] = fromf<E>(v);
   }
 }
-template <bool PAIR> __device__ __forceinline__ void take2(const float *row, int c, int D, float (&v)[2]) {
-  v[0] = v[1] = 0.f;
-  if constexpr (PAIR) {
-    if (c < D) {
-      const float2 u = *reinterpret_cast<const float2 *>(row + c);
-      v[0] = u.x;
-      v[1] = u.y;
-    }
-  } else {
-    if (c < D) v[0] = row[c];
-    if (c + 32 < D) v[1] = row[c + 32];
-  }
+template <bool PAIR> __device__ __forceinline__ uint64_t take2(const float *row, int c, int D) {
+  if constexpr (PAIR) return c < D ? *reinterpret_cast<const uint64_t *>(row + c) : 0;
+  else return pk(c < D ? row[c] : 0.f, c + 32 < D ? row[c + 32] : 0.f);
 }
 
 // ------------------------------------------------------------------ where sequences begin
@@ -187,9 +199,12 @@ struct Bounds {
 // c -> A c + H; A < 0 marks one that forgets c (whatever c holds, an infinity among it)
 struct Map2 {
   float A[2], H[2];
-  __device__ __forceinline__ void apply(float (&c)[2]) const {
+  __device__ __forceinline__ uint64_t apply(uint64_t p) const {
+    float c[2];
+    upk(p, c[0], c[1]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) c[k] = A[k] < 0.f ? H[k] : fmaf(A[k], c[k], H[k]);
+    return pk(c[0], c[1]);
   }
   __device__ __forceinline__ void then(const Map2 &n) {  // this one first, then n
 #pragma unroll
@@ -199,13 +214,22 @@ struct Map2 {
     }
   }
 };
-struct Meet {
+// of a segment: the sum of its log-gates and its result from zero
+__device__ __forceinline__ float4 segment_map(bool fresh, uint64_t sum, uint64_t h) {
+  float s0, s1, h0, h1;
+  upk(sum, s0, s1);
+  upk(h, h0, h1);
+  return make_float4(fresh ? -1.f : expf(s0), fresh ? -1.f : expf(s1), h0, h1);
+}
+template <int W> struct Meet {
   float4 warp[2][W][32];     // by round parity: maps of the CTA's segments
   float4 peer[2][MAXC][32];  // of the cluster's CTAs
 };
 __device__ __forceinline__ Map2 map_of(const float4 &v) { return {{v.x, v.y}, {v.z, v.w}}; }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+// of a warp that has written nothing that peers read: it need not wait for its own stores
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void store_peer(const float4 *p, int rank, const float4 &v) {
   uint32_t at;
@@ -213,277 +237,316 @@ __device__ __forceinline__ void store_peer(const float4 *p, int rank, const floa
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
-// A round's exchange: every warp hands in its segment's map and gets the state before it; `carry` becomes the state after
-// the round.  `between` runs while the cluster's CTAs meet.
-template <typename F>
-__device__ __forceinline__ void exchange(Meet &mt, int buf, int cs, int rank, const Map2 &mine, float (&carry)[2], float (&in)[2], F between) {
+// A round's exchange: every warp hands in its segment's map, and later gets the state before it; `carry` becomes the state
+// after the round.
+template <int W> __device__ __forceinline__ void hand_in(Meet<W> &mt, int buf, int cs, int rank, const float4 &mine) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  mt.warp[buf][warp][lane] = make_float4(mine.A[0], mine.A[1], mine.H[0], mine.H[1]);
+  mt.warp[buf][warp][lane] = mine;
   __syncthreads();
-  if (cs == 1) {
-    between();
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      if (j == warp) {
-        in[0] = carry[0];
-        in[1] = carry[1];
-      }
-      map_of(mt.warp[buf][j][lane]).apply(carry);
-    }
-    return;
-  }
+  if (cs == 1) return;
   if (warp == 0) {
     Map2 all = map_of(mt.warp[buf][0][lane]);
 #pragma unroll
     for (int j = 1; j < W; ++j) all.then(map_of(mt.warp[buf][j][lane]));
     for (int r = 0; r < cs; ++r) store_peer(&mt.peer[buf][rank][lane], r, make_float4(all.A[0], all.A[1], all.H[0], all.H[1]));
+    cluster_arrive();
+  } else {
+    cluster_arrive_relaxed();
   }
-  cluster_arrive();
-  between();
+}
+template <int W> __device__ __forceinline__ uint64_t get_state(const Meet<W> &mt, int buf, int cs, int rank, uint64_t &carry) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t in = carry;
+  if (cs == 1) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      if (j == warp) in = carry;
+      carry = map_of(mt.warp[buf][j][lane]).apply(carry);
+    }
+    return in;
+  }
   cluster_wait();
   for (int r = 0; r < cs; ++r) {
-    if (r == rank) {
-      in[0] = carry[0];
-      in[1] = carry[1];
-    }
-    map_of(mt.peer[buf][r][lane]).apply(carry);
+    if (r == rank) in = carry;
+    carry = map_of(mt.peer[buf][r][lane]).apply(carry);
   }
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    if (j < warp) map_of(mt.warp[buf][j][lane]).apply(in);
+  for (int j = 0; j < warp; ++j) in = map_of(mt.warp[buf][j][lane]).apply(in);
+  return in;
 }
 
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 // the state of sequences without tokens passes through: out[n] = in[n], shared out among a channel block's CTAs
-template <bool PAIR> __device__ __forceinline__ void pass_empty(const ScanArgs &a, const float *in, float *out, int c, int ctas, int cta) {
+template <bool PAIR, int W>
+__device__ __forceinline__ void pass_empty(const ScanArgs &a, const float *in, float *out, int c, int ctas, int cta) {
   if (!a.cu || !out) return;
   for (int n = cta * W + (threadIdx.x >> 5); n < a.N; n += ctas * W) {
     if (a.cu[n + 1] > a.cu[n]) continue;
-    float v[2] = {0.f, 0.f};
-    if (in) take2<PAIR>(in + (long long)n * a.D, c, a.D, v);
-    put2<float, PAIR>(out + (long long)n * a.D, c, a.D, v);
+    put2<float, PAIR>(out + (long long)n * a.D, c, a.D, in ? take2<PAIR>(in + (long long)n * a.D, c, a.D) : 0);
   }
 }
 
-}  // namespace
-
-// grid: CTAs of a cluster, channel blocks, parts
-template <typename X, typename G, int M, int STAGES>
-__global__ void __launch_bounds__(NTH, 2) scan_fwd_kernel(ScanArgs a) {
-  constexpr bool PAIR = Lanes<X, M>::PAIR;
-  static_assert(Lanes<X, M>::PAIR == Lanes<G, M>::PAIR || M == M4, "one layout of channels");
-  extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ Meet mt;
-  constexpr int BX = SEG * CB * sizeof(X), BG = SEG * CB * sizeof(G);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + Lanes<X, M>::first(lane);
-  uint8_t *ring = raw + warp * (STAGES * (BX + BG));
-  const X *xs = static_cast<const X *>(a.x);
-  const G *gs = static_cast<const G *>(a.g);
-  X *ys = static_cast<X *>(a.y);
-  if (cs > 1) cluster_arrive();  // peers have begun before anything is written to them
-  pdl_trigger();
-  pdl_wait();
-  const int lo = part_begin(a, blockIdx.z, gridDim.z), hi = part_begin(a, blockIdx.z + 1, gridDim.z);
-  const int s0 = lo / SEG, ns = hi > lo ? (hi + SEG - 1) / SEG - s0 : 0, per = cs * W, rounds = (ns + per - 1) / per;
-  const int s_mine = s0 + rank * W + warp;  // segment of the first round
-  auto load = [&](int k) {
-    if (k < rounds) {
-      uint8_t *st = ring + k % STAGES * (BX + BG);
-      const int t = (s_mine + k * per) * SEG;
-      if (t < hi) {
-        load_rows<X, M>(reinterpret_cast<X *>(st), xs, a.x_row, t, lo, hi, c0, a.D);
-        load_rows<G, M>(reinterpret_cast<G *>(st + BX), gs, a.g_row, t, lo, hi, c0, a.D);
-      }
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) load(k);
+// Where a CTA's walk through its part stands.  Segments count in the direction of the walk: number 0 is the part's first
+// one, or its last one going backward.
+struct Walk {
+  int lo, hi;        // tokens of the part
+  int rounds, per;   // segments of a round: one for every warp of the cluster
+  int first, last;   // the warp's segment of round 0; the line's segment with number 0 going backward
+  template <int W> __device__ __forceinline__ void init(const ScanArgs &a, int cs, int rank) {
+    lo = part_begin(a, blockIdx.z, gridDim.z);
+    hi = part_begin(a, blockIdx.z + 1, gridDim.z);
+    const int s0 = lo / SEG, ns = hi > lo ? (hi + SEG - 1) / SEG - s0 : 0;
+    per = cs * W;
+    rounds = (ns + per - 1) / per;
+    first = s0 + rank * W + (threadIdx.x >> 5);
+    last = 2 * s0 + ns - 1;
+  }
+  __device__ __forceinline__ int up(int k) const { return first + k * per; }
+  __device__ __forceinline__ int down(int k) const { return last - (first + k * per); }
+  __device__ __forceinline__ bool has(int seg) const { return seg * SEG < hi && (seg + 1) * SEG > lo; }
+};
+// A segment of a round.  One inside a sequence (plain) goes through unrolled code.  One with a boundary, or at a part's end,
+// takes loops that look at every row, kept short: code for both in every row was five times as long, and its fetching took
+// most of the time (4 x 4096 tokens of 2048 channels: 109 us forward).
+struct Piece {
+  int seg, t0;
+  bool live, plain;
+  uint32_t cut;  // boundaries
   Bounds bd;
-  bd.init(a, s_mine * SEG);
-  pass_empty<PAIR>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
-  if (cs > 1) cluster_wait();
-  float carry[2] = {0.f, 0.f};
-  for (int k = 0; k < rounds; ++k) {
-    const int seg = s_mine + k * per, t0 = seg * SEG;
-    const bool live = t0 < hi;
-    uint32_t cut = 0;  // boundaries
+  __device__ __forceinline__ void look(const ScanArgs &a, const Walk &w, int s) {
+    seg = s;
+    t0 = s * SEG;
+    live = w.has(s);
+    cut = 0;
     if (live) {
       bd.seek(a, t0);
       cut = bd.mask(a, t0);
     }
-    cp_wait<STAGES - 2>();
-    __syncwarp();
-    const X *xr = reinterpret_cast<const X *>(ring + k % STAGES * (BX + BG));
-    const G *gr = reinterpret_cast<const G *>(ring + k % STAGES * (BX + BG) + BX);
-    float al[SEG][2];
-    Map2 m = {{1.f, 1.f}, {0.f, 0.f}};
-    auto begins = [&](int i) { return (cut >> i & 1) && t0 + i >= lo && t0 + i < hi; };
-    auto ends = [&](int i) { return (cut >> (i + 1) & 1) && t0 + i >= lo && t0 + i < hi; };
-    auto start = [&](int i, float (&h)[2]) {
-      h[0] = h[1] = 0.f;
-      if (a.h0) take2<PAIR>(a.h0 + (long long)bd.seq(a, t0 + i) * a.D, c, a.D, h);
-    };
-    if (live) {
-      float sum[2] = {0.f, 0.f};
+    plain = cut == 0 && t0 >= w.lo && t0 + SEG <= w.hi;
+  }
+  __device__ __forceinline__ bool inside(const Walk &w, int i) const { return t0 + i >= w.lo && t0 + i < w.hi; }
+  __device__ __forceinline__ bool begins(int i) const { return cut >> i & 1; }
+  __device__ __forceinline__ bool ends(int i) const { return cut >> (i + 1) & 1; }
+};
+
+}  // namespace
+
+// grid: CTAs of a cluster, channel blocks, parts.  Each step hands in the maps of round k + 1 and, while the CTAs of the cluster
+// meet, finishes round k, whose states are known.
+template <typename X, typename G, int M, int W>
+__global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
+  constexpr bool PAIR = Lanes<X, M>::PAIR, EXACT = sizeof(X) == 4;
+  static_assert(Lanes<X, M>::PAIR == Lanes<G, M>::PAIR, "one layout of channels");
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ Meet<W> mt;
+  constexpr int BX = SEG * CB * sizeof(X), ST = BX + SEG * CB * sizeof(G);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + Lanes<X, M>::first(lane);
+  uint8_t *ring = raw + warp * (STAGES * ST);
+  if (cs > 1) cluster_arrive();  // peers have begun before anything is written to them
+  pdl_trigger();
+  pdl_wait();
+  Walk w = {};
+  w.init<W>(a, cs, rank);
+  auto load = [&](int k, int slot) {
+    if (k < w.rounds && w.has(w.up(k))) {
+      uint8_t *st = ring + slot * ST;
+      load_rows<X, M>(reinterpret_cast<X *>(st), static_cast<const X *>(a.x), a.x_row, w.up(k) * SEG, w.lo, w.hi, c0, a.D);
+      load_rows<G, M>(reinterpret_cast<G *>(st + BX), static_cast<const G *>(a.g), a.g_row, w.up(k) * SEG, w.lo, w.hi, c0, a.D);
+    }
+    cp_async_commit();
+  };
+  load(0, 0);
+  load(1, 1);
+  Piece now = {}, next = {};
+  next.bd.init(a, w.up(0) * SEG);
+  pass_empty<PAIR, W>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  if (cs > 1) cluster_wait();
+  auto x_of = [&](const uint8_t *st, int i) { return get2<X, M>(reinterpret_cast<const X *>(st) + i * CB, lane); };
+  auto g_of = [&](const uint8_t *st, int i) { return get2<G, M>(reinterpret_cast<const G *>(st + BX) + i * CB, lane); };
+  auto start = [&](const Piece &p, int i) { return a.h0 ? take2<PAIR>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : 0; };
+  uint64_t carry = 0, h = 0;
+  int slot = STAGES - 1;  // of round k
+  for (int k = -1; k < w.rounds; ++k) {
+    const int slot1 = slot + 1 == STAGES ? 0 : slot + 1;
+    const bool more = k + 1 < w.rounds;
+    if (more) {
+      next.look(a, w, w.up(k + 1));
+      cp_wait<1>();
+      __syncwarp();
+      const uint8_t *st = ring + slot1 * ST;
+      uint64_t sum = 0, z = 0;
       bool fresh = false;
+      if (next.plain) {
 #pragma unroll
-      for (int i = 0; i < SEG; ++i) {
-        float x[2], g[2];
-        get2<X, M>(xr + i * CB, lane, x);
-        get2<G, M>(gr + i * CB, lane, g);
-        if (cut && begins(i)) {
-          start(i, m.H);
-          fresh = true;
+        for (int i = 0; i < SEG; ++i) {
+          const uint64_t g = g_of(st, i);
+          sum = add2(sum, g);
+          z = fma2(gates<EXACT>(g), z, x_of(st, i));
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          al[i][e] = expf(g[e]);
-          sum[e] += g[e];
-          m.H[e] = fmaf(al[i][e], m.H[e], x[e]);
+      } else if (next.live) {
+#pragma unroll 1
+        for (int i = 0; i < SEG; ++i) {
+          const uint64_t g = g_of(st, i);
+          if (next.begins(i) && next.inside(w, i)) {
+            z = start(next, i);
+            fresh = true;
+          }
+          sum = add2(sum, g);
+          z = fma2(gates<EXACT>(g), z, x_of(st, i));
         }
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m.A[e] = fresh ? -1.f : expf(sum[e]);
+      hand_in(mt, k + 1 & 1, cs, rank, segment_map(fresh, sum, z));
     }
-    float h[2];
-    exchange(mt, k & 1, cs, rank, m, carry, h, [&] { load(k + STAGES - 1); });
-    if (!live) continue;
-    if (a.states && t0 >= lo) put2<float, PAIR>(a.states + (long long)seg * a.D, c, a.D, h);
-    X *yr = ys + (long long)t0 * a.y_row;
+    if (k >= 0 && now.live) {
+      const uint8_t *st = ring + slot * ST;
+      if (a.states && now.t0 >= w.lo) put2<float, PAIR>(a.states + (long long)now.seg * a.D, c, a.D, h);
+      X *yr = static_cast<X *>(a.y) + (long long)now.t0 * a.y_row;
+      if (now.plain) {
 #pragma unroll
-    for (int i = 0; i < SEG; ++i) {
-      float x[2];
-      get2<X, M>(xr + i * CB, lane, x);
-      if (cut && begins(i)) start(i, h);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) h[e] = fmaf(al[i][e], h[e], x[e]);
-      if (t0 + i >= lo && t0 + i < hi) put2<X, PAIR>(yr + i * a.y_row, c, a.D, h);
-      if (cut && ends(i) && a.hT) put2<float, PAIR>(a.hT + (long long)bd.seq(a, t0 + i) * a.D, c, a.D, h);
+        for (int i = 0; i < SEG; ++i, yr += a.y_row) {
+          h = fma2(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
+          put2<X, PAIR>(yr, c, a.D, h);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < SEG; ++i, yr += a.y_row) {
+          if (!now.inside(w, i)) continue;
+          if (now.begins(i)) h = start(now, i);
+          h = fma2(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
+          put2<X, PAIR>(yr, c, a.D, h);
+          if (now.ends(i) && a.hT) put2<float, PAIR>(a.hT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, h);
+        }
+      }
     }
-    __syncwarp();  // the stage is loaded again in the next round
+    __syncwarp();  // the stage is loaded again
+    load(k + STAGES, slot);
+    if (more) {
+      h = get_state(mt, k + 1 & 1, cs, rank, carry);
+      now = next;
+    }
+    slot = slot1;
   }
   cp_async_wait_all();
 }
 
-// The same walk from the line's end; in a part, segment 0 of the walk is the last one.
-template <typename X, typename G, int M, int STAGES>
-__global__ void __launch_bounds__(NTH, 2) scan_bwd_kernel(ScanArgs a) {
-  constexpr bool PAIR = Lanes<X, M>::PAIR;
+template <typename X, typename G, int M, int W>
+__global__ void __launch_bounds__(32 * W, 2) scan_bwd_kernel(ScanArgs a) {
+  constexpr bool PAIR = Lanes<X, M>::PAIR, EXACT = sizeof(X) == 4;
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ Meet mt;
-  constexpr int BX = SEG * CB * sizeof(X), BG = SEG * CB * sizeof(G), ST = 2 * BX + BG;
+  __shared__ Meet<W> mt;
+  constexpr int BX = SEG * CB * sizeof(X), ST = 2 * BX + SEG * CB * sizeof(G);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + Lanes<X, M>::first(lane);
   uint8_t *ring = raw + warp * (STAGES * ST);
-  const X *xs = static_cast<const X *>(a.x), *dys = static_cast<const X *>(a.dy);
-  const G *gs = static_cast<const G *>(a.g);
-  X *dxs = static_cast<X *>(a.y);
-  G *dgs = static_cast<G *>(a.dg);
   if (cs > 1) cluster_arrive();
   pdl_trigger();
   pdl_wait();
-  const int lo = part_begin(a, blockIdx.z, gridDim.z), hi = part_begin(a, blockIdx.z + 1, gridDim.z);
-  const int s0 = lo / SEG, ns = hi > lo ? (hi + SEG - 1) / SEG - s0 : 0, per = cs * W, rounds = (ns + per - 1) / per;
-  const int s_mine = s0 + ns - 1 - (rank * W + warp);
-  auto load = [&](int k) {
-    if (k < rounds) {
-      uint8_t *st = ring + k % STAGES * ST;
-      const int seg = s_mine - k * per;
-      if (seg >= s0) {
-        load_rows<X, M>(reinterpret_cast<X *>(st), xs, a.x_row, seg * SEG, lo, hi, c0, a.D);
-        load_rows<X, M>(reinterpret_cast<X *>(st + BX), dys, a.dy_row, seg * SEG, lo, hi, c0, a.D);
-        load_rows<G, M>(reinterpret_cast<G *>(st + 2 * BX), gs, a.g_row, seg * SEG, lo, hi, c0, a.D);
-      }
+  Walk w = {};
+  w.init<W>(a, cs, rank);
+  auto load = [&](int k, int slot) {
+    if (k < w.rounds && w.has(w.down(k))) {
+      uint8_t *st = ring + slot * ST;
+      const int t = w.down(k) * SEG;
+      load_rows<X, M>(reinterpret_cast<X *>(st), static_cast<const X *>(a.x), a.x_row, t, w.lo, w.hi, c0, a.D);
+      load_rows<X, M>(reinterpret_cast<X *>(st + BX), static_cast<const X *>(a.dy), a.dy_row, t, w.lo, w.hi, c0, a.D);
+      load_rows<G, M>(reinterpret_cast<G *>(st + 2 * BX), static_cast<const G *>(a.g), a.g_row, t, w.lo, w.hi, c0, a.D);
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) load(k);
-  Bounds bd;
-  bd.init(a, max(s_mine, s0) * SEG);
-  pass_empty<PAIR>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  load(0, 0);
+  load(1, 1);
+  Piece now = {}, next = {};
+  next.bd.init(a, max(w.down(0) * SEG, 0));
+  pass_empty<PAIR, W>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
   if (cs > 1) cluster_wait();
-  float carry[2] = {0.f, 0.f};
-  for (int k = 0; k < rounds; ++k) {
-    const int seg = s_mine - k * per, t0 = seg * SEG;
-    const bool live = seg >= s0;
-    uint32_t cut = 0;
-    float h[2] = {0.f, 0.f};
-    if (live) {
-      take2<PAIR>(a.states + (long long)seg * a.D, c, a.D, h);
-      bd.seek(a, t0);
-      cut = bd.mask(a, t0);
-    }
-    cp_wait<STAGES - 2>();
-    __syncwarp();
-    const X *xr = reinterpret_cast<const X *>(ring + k % STAGES * ST), *dyr = xr + SEG * CB;
-    const G *gr = reinterpret_cast<const G *>(ring + k % STAGES * ST + 2 * BX);
-    float al[SEG][2], hp[SEG][2];  // gates, and states before the tokens
-    Map2 m = {{1.f, 1.f}, {0.f, 0.f}};
-    auto begins = [&](int i) { return (cut >> i & 1) && t0 + i >= lo && t0 + i < hi; };
-    auto ends = [&](int i) { return (cut >> (i + 1) & 1) && t0 + i >= lo && t0 + i < hi; };
-    auto at_end = [&](int i, float (&d)[2]) {
-      d[0] = d[1] = 0.f;
-      if (a.dhT) take2<PAIR>(a.dhT + (long long)bd.seq(a, t0 + i) * a.D, c, a.D, d);
-    };
-    if (live) {
-      float sum[2] = {0.f, 0.f};
+  auto x_of = [&](const uint8_t *st, int i) { return get2<X, M>(reinterpret_cast<const X *>(st) + i * CB, lane); };
+  auto dy_of = [&](const uint8_t *st, int i) { return get2<X, M>(reinterpret_cast<const X *>(st + BX) + i * CB, lane); };
+  auto g_of = [&](const uint8_t *st, int i) { return get2<G, M>(reinterpret_cast<const G *>(st + 2 * BX) + i * CB, lane); };
+  auto start = [&](const Piece &p, int i) { return a.h0 ? take2<PAIR>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : 0; };
+  auto at_end = [&](const Piece &p, int i) { return a.dhT ? take2<PAIR>(a.dhT + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : 0; };
+  uint64_t carry = 0, d = 0;  // d: what reaches the state from later tokens
+  uint64_t h = 0, h1 = 0;     // stored states before the segments of rounds k and k + 1
+  int slot = STAGES - 1;
+  for (int k = -1; k < w.rounds; ++k) {
+    const int slot1 = slot + 1 == STAGES ? 0 : slot + 1;
+    const bool more = k + 1 < w.rounds;
+    if (more) {
+      next.look(a, w, w.down(k + 1));
+      h1 = next.live ? take2<PAIR>(a.states + (long long)next.seg * a.D, c, a.D) : 0;
+      cp_wait<1>();
+      __syncwarp();
+      const uint8_t *st = ring + slot1 * ST;
+      uint64_t sum = 0, z = 0;
       bool fresh = false;
+      if (next.plain) {
 #pragma unroll
-      for (int i = 0; i < SEG; ++i) {
-        float x[2], g[2];
-        get2<X, M>(xr + i * CB, lane, x);
-        get2<G, M>(gr + i * CB, lane, g);
-        if (cut && begins(i)) {
-          h[0] = h[1] = 0.f;
-          if (a.h0) take2<PAIR>(a.h0 + (long long)bd.seq(a, t0 + i) * a.D, c, a.D, h);
+        for (int i = SEG - 1; i >= 0; --i) {
+          const uint64_t g = g_of(st, i);
+          sum = add2(sum, g);
+          z = mul2(gates<EXACT>(g), add2(dy_of(st, i), z));
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          hp[i][e] = h[e];
-          al[i][e] = expf(g[e]);
-          sum[e] += g[e];
-          h[e] = fmaf(al[i][e], h[e], x[e]);
+      } else if (next.live) {
+#pragma unroll 1
+        for (int i = SEG - 1; i >= 0; --i) {
+          const uint64_t g = g_of(st, i);
+          if (next.ends(i) && next.inside(w, i)) {
+            z = at_end(next, i);
+            fresh = true;
+          }
+          sum = add2(sum, g);
+          z = mul2(gates<EXACT>(g), add2(dy_of(st, i), z));
         }
       }
-#pragma unroll
-      for (int i = SEG - 1; i >= 0; --i) {
-        float dy[2];
-        get2<X, M>(dyr + i * CB, lane, dy);
-        if (cut && ends(i)) {
-          at_end(i, m.H);
-          fresh = true;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) m.H[e] = al[i][e] * (dy[e] + m.H[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) m.A[e] = fresh ? -1.f : expf(sum[e]);
+      hand_in(mt, k + 1 & 1, cs, rank, segment_map(fresh, sum, z));
     }
-    float d[2];  // what reaches the state from later tokens
-    exchange(mt, k & 1, cs, rank, m, carry, d, [&] { load(k + STAGES - 1); });
-    if (!live) continue;
+    if (k >= 0 && now.live) {
+      const uint8_t *st = ring + slot * ST;
+      X *dxr = static_cast<X *>(a.y) + (long long)(now.t0 + SEG - 1) * a.y_row;
+      G *dgr = static_cast<G *>(a.dg) + (long long)(now.t0 + SEG - 1) * a.dg_row;
+      if (now.plain) {
+        uint64_t al[SEG], hp[SEG];  // gates, and states before the tokens
 #pragma unroll
-    for (int i = SEG - 1; i >= 0; --i) {
-      float dy[2], dg[2];
-      get2<X, M>(dyr + i * CB, lane, dy);
-      if (cut && ends(i)) at_end(i, d);
+        for (int i = 0; i < SEG; ++i) {
+          hp[i] = h;
+          al[i] = gates<EXACT>(g_of(st, i));
+          h = fma2(al[i], h, x_of(st, i));
+        }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        dy[e] += d[e];
-        d[e] = al[i][e] * dy[e];
-        dg[e] = d[e] * hp[i][e];
+        for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
+          const uint64_t dx = add2(dy_of(st, i), d);
+          d = mul2(al[i], dx);
+          put2<X, PAIR>(dxr, c, a.D, dx);
+          put2<G, PAIR>(dgr, c, a.D, mul2(d, hp[i]));
+        }
+      } else {
+        uint64_t hp[SEG];  // in local memory
+#pragma unroll 1
+        for (int i = 0; i < SEG; ++i) {
+          if (now.begins(i) && now.inside(w, i)) h = start(now, i);
+          hp[i] = h;
+          h = fma2(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
+        }
+#pragma unroll 1
+        for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
+          if (!now.inside(w, i)) continue;
+          if (now.ends(i)) d = at_end(now, i);
+          const uint64_t dx = add2(dy_of(st, i), d);
+          d = mul2(gates<EXACT>(g_of(st, i)), dx);
+          put2<X, PAIR>(dxr, c, a.D, dx);
+          put2<G, PAIR>(dgr, c, a.D, mul2(d, hp[i]));
+          if (now.begins(i) && a.dh0) put2<float, PAIR>(a.dh0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, d);
+        }
       }
-      if (t0 + i >= lo && t0 + i < hi) {
-        put2<X, PAIR>(dxs + (long long)(t0 + i) * a.y_row, c, a.D, dy);
-        put2<G, PAIR>(dgs + (long long)(t0 + i) * a.dg_row, c, a.D, dg);
-      }
-      if (cut && begins(i) && a.dh0) put2<float, PAIR>(a.dh0 + (long long)bd.seq(a, t0 + i) * a.D, c, a.D, d);
     }
     __syncwarp();
+    load(k + STAGES, slot);
+    if (more) {
+      d = get_state(mt, k + 1 & 1, cs, rank, carry);
+      now = next;
+      h = h1;
+    }
+    slot = slot1;
   }
   cp_async_wait_all();
 }
@@ -535,15 +598,13 @@ template <typename X, typename G, int V> __global__ void __launch_bounds__(256) 
 
 namespace {
 
-// The split of a call: parts of whole sequences and CTAs of a cluster, for about two CTAs per SM.  Equal sequences go to
+// The split of a call: parts of whole sequences and CTAs of a cluster, for two CTAs per SM.  Equal sequences go to
 // parts first, which exchange nothing; packed ones may be one long sequence and many short ones, so there the line is cut
 // within a cluster first.
-void split(const ScanArgs &a, int sms, int &parts, int &cs) {
+void split(const ScanArgs &a, int W, int sms, int &parts, int &cs) {
   const int nb = (a.D + CB - 1) / CB, want = std::max(1, 2 * sms / nb);  // CTAs of a channel block
   const auto clustered = [&](int most, long long tokens) {
-    int c = 1;
-    while (c < MAXC && 2 * c <= most && tokens > (long long)c * W * SEG) c *= 2;
-    return c;
+    return (int)std::max(1ll, std::min({(long long)most, (long long)MAXC, tokens / (W * SEG)}));
   };
   if (!a.cu) {
     parts = std::min(a.N, want);
@@ -555,15 +616,16 @@ void split(const ScanArgs &a, int sms, int &parts, int &cs) {
   parts = std::min(parts, 65535);
 }
 
-template <typename... KArgs>
-cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int sms, size_t smem, cudaStream_t st) {
+template <int W, typename... KArgs>
+cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int sms, int row_bytes, cudaStream_t st) {
+  const size_t smem = (size_t)W * STAGES * SEG * CB * row_bytes;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   int parts, cs;
-  split(a, sms, parts, cs);
+  split(a, W, sms, parts, cs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs, (a.D + CB - 1) / CB, parts);
-  cfg.blockDim = dim3(NTH);
+  cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -577,10 +639,9 @@ cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int sms, si
   return cudaLaunchKernelEx(&cfg, k, a);
 }
 template <typename X, typename G, int M> cudaError_t launch_move(const ScanArgs &a, bool bwd, int sms, cudaStream_t st) {
-  constexpr int F = sizeof(X) + sizeof(G) == 4 ? 3 : 2, B = 2;  // stages
-  constexpr size_t row = (size_t)W * SEG * CB;
-  if (bwd) return launch_clustered(scan_bwd_kernel<X, G, M, B>, a, sms, row * B * (2 * sizeof(X) + sizeof(G)), st);
-  return launch_clustered(scan_fwd_kernel<X, G, M, F>, a, sms, row * F * (sizeof(X) + sizeof(G)), st);
+  constexpr int F = sizeof(X) + sizeof(G) == 4 ? 8 : 4, B = sizeof(X) == 2 ? 4 : 2;  // warps, so that two CTAs' stages fit an SM
+  if (bwd) return launch_clustered<B>(scan_bwd_kernel<X, G, M, B>, a, sms, 2 * sizeof(X) + sizeof(G), st);
+  return launch_clustered<F>(scan_fwd_kernel<X, G, M, F>, a, sms, sizeof(X) + sizeof(G), st);
 }
 template <typename X, typename G> cudaError_t launch_types(const ScanArgs &a, int move, bool bwd, int sms, cudaStream_t st) {
   if (move == 16) return launch_move<X, G, M16>(a, bwd, sms, st);

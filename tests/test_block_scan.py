@@ -1,10 +1,11 @@
 """The gated linear recurrence, forward, backward and by single tokens, against a token loop in 64 bits.
 
 Bounds.  M is the recurrence of the magnitudes, M_t = a_t M_{t-1} + |x_t|.  In a segment of 16 tokens each step multiplies by
-a gate that is off by 2^-23 of itself (expf, one ulp) and rounds once (2^-24): at most 16 * 1.5 * 2^-23 of M.  A state that
+a gate that is off by at most 2^-22 of itself (ex2.approx; expf has 2^-23), with the argument's rounding |g| exp(g) 2^-24 <=
+2^-25, and rounds once (2^-24): at most 16 * 2.75 * 2^-23 = 44 * 2^-23 of M.  A state that
 passes a whole segment is multiplied by the exponential of a sum of 16 gates, off by 16 * 2^-24 |sum| exp(sum) <= 3 * 2^-23 and
 by 2^-23 of itself, and added to (two roundings where maps meet): 5 * 2^-23, and as much again where the maps of eight segments
-are joined before they are applied.  So (24 + 10 n) 2^-23 M for n segments.  Gradients are the same recurrence of the other
+are joined before they are applied.  So (44 + 10 n) 2^-23 M for n segments.  Gradients are the same recurrence of the other
 direction; that of the gate is a product of both, so both bounds add up.  A bf16 output adds half a step, 2^-8 of the value."""
 import ctypes
 
@@ -61,7 +62,7 @@ def loop_bwd(dy, g, d_final, cu):
 
 
 def bound(longest):
-    return (24 + 10 * (longest // 16 + 2)) * 2.0 ** -23
+    return (44 + 10 * (longest // 16 + 2)) * 2.0 ** -23
 
 
 def near(got, want, tol, what):
