@@ -143,6 +143,9 @@ def load():
                 "gdn_rotary_table": [P, _I, _I, D, P, P],
                 "gdn_rotary": [P] * 8,
                 "gdn_rotary_append": [P] * 12,
+                "gdn_norm_rotary": [P, _F, _F] + [P] * 9,
+                "gdn_norm_rotary_bwd": [P, _F, _F] + [P] * 13 + [Z, P],
+                "gdn_norm_rotary_append": [P, _F, _F] + [P] * 13,
                 "gdn_slots_copy": [P, _I, P, P, _I, P],
                 "gdn_pages_extend": [P] * 6 + [_I, P, P, Z, P],
                 "gdn_pages_fork": [P] * 6 + [_I, P, _I, P, _I, P, P, Z, P],
@@ -156,7 +159,7 @@ def load():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         for name, args in {"gdn_paged_attn_workspace_size": [P], "gdn_pages_workspace_size": [P, _I],
-                           "gdn_rmsnorm_bwd_workspace_size": [P]}.items():
+                           "gdn_rmsnorm_bwd_workspace_size": [P], "gdn_norm_rotary_bwd_workspace_size": [P]}.items():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = Z
         lib.gdn_scan_states_rows.argtypes, lib.gdn_scan_states_rows.restype = [P], _L
@@ -168,7 +171,8 @@ def load():
 _PY_CALLS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_paged_attn_status", "gdn_rotary", "gdn_rotary_append",
              "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork", "gdn_pages_free",
              "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd", "gdn_scan_states_rows",
-             "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_status_string", "gdn_last_error_string")
+             "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_rotary", "gdn_norm_rotary_bwd_workspace_size", "gdn_norm_rotary_bwd",
+             "gdn_norm_rotary_append", "gdn_status_string", "gdn_last_error_string")
 _py = None
 
 

@@ -4,13 +4,14 @@
 ``rotary_embedding`` / ``rotary_append`` (rotary positions, their gradient, and the write of new keys and values into
 the cache), ``extend_pages`` / ``fork_pages`` / ``free_pages`` / ``compact_pages`` / ``copy_slots`` (the cache's
 upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual stream's norm, optionally with an 8-bit
-output), ``gated_scan`` / ``gated_scan_bwd`` / ``gated_linear_recurrence`` / ``gated_scan_step`` (a gated linear recurrence with
+output), ``norm_rotary`` / ``norm_rotary_bwd`` / ``norm_rotary_embedding`` / ``norm_rotary_append`` (the norm of each head of q and k with
+their rotary positions: forward, backward, with gradients, and into the cache), ``gated_scan`` / ``gated_scan_bwd`` / ``gated_linear_recurrence`` / ``gated_scan_step`` (a gated linear recurrence with
 one state per channel: forward, backward, with gradients, and for single tokens).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
 arguments are checked, and outputs and workspaces allocated, by the extension csrc/block_py.cpp.  Bad arguments raise
 ``ValueError`` (found there) or ``RuntimeError`` (found by the library, with its reason), a lack of memory
 ``torch.OutOfMemoryError``.
 
-Gradients come from ``rotary_embedding``, ``residual_rms_norm`` and ``gated_linear_recurrence``.  Every other function computes outside autograd, as
+Gradients come from ``rotary_embedding``, ``residual_rms_norm``, ``norm_rotary_embedding`` and ``gated_linear_recurrence``.  Every other function computes outside autograd, as
 the ``_fwd`` / ``_bwd`` functions of the delta rule do: its outputs carry no graph, whatever its inputs require.  What a
 function writes in place counts as an in-place operation (its version moves on).
 """
@@ -26,7 +27,8 @@ from . import _lib
 
 __all__ = ["paged_attention", "paged_attention_status", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding",
            "rotary_append", "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_slots", "rms_norm",
-           "rms_norm_bwd", "residual_rms_norm", "NormOutput", "gated_scan", "gated_scan_bwd", "gated_scan_step",
+           "rms_norm_bwd", "residual_rms_norm", "NormOutput", "norm_rotary", "norm_rotary_bwd",
+           "norm_rotary_embedding", "norm_rotary_append", "gated_scan", "gated_scan_bwd", "gated_scan_step",
            "gated_linear_recurrence"]
 
 
@@ -145,6 +147,52 @@ def rotary_append(q, k, v, table, k_cache, v_cache, page_table, kv_lens, cu_q=No
     q [new tokens, heads, D], k, v [new tokens, kv heads, D], as slices of one projection if need be.  The caches,
     page_table, kv_lens and cu_q are those of ``paged_attention``: kv_lens counts the new tokens already."""
     return _py.rotary_append(q, k, v, table, k_cache, v_cache, page_table, kv_lens, cu_q, interleaved, out)
+
+
+# ------------------------------------------------------------------ norm of heads with rotary positions
+def norm_rotary(q, k, q_weight, k_weight, table, positions, eps: float = 1e-6, weight_offset: float = 0.0,
+                interleaved: bool = False):
+    """The root-mean-square norm of every head of q and k, then ``rotary``, in one pass.
+
+    q [T, heads, D] and k [T, heads, D] (or None, with its weight), D at most 1024; q_weight, k_weight fp32 [D] (one for all
+    heads of q, one for those of k): head / sqrt(mean(head^2) + eps) * (weight + weight_offset).  table, positions and
+    interleaved as in ``rotary``.  Returns (q, k)."""
+    return _py.norm_rotary(q, k, q_weight, k_weight, table, positions, eps, weight_offset, interleaved)
+
+
+def norm_rotary_bwd(dq, dk, q, k, q_weight, k_weight, table, positions, eps: float = 1e-6, weight_offset: float = 0.0,
+                    interleaved: bool = False):
+    """(dq, dk, dq_weight, dk_weight): the gradients of ``norm_rotary``'s inputs from those of its outputs and the inputs."""
+    return _py.norm_rotary_bwd(dq, dk, q, k, q_weight, k_weight, table, positions, eps, weight_offset, interleaved)
+
+
+class NormRotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, table, positions, eps, weight_offset, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, table, positions)
+        ctx.how = (eps, weight_offset, interleaved)
+        return norm_rotary(q, k, q_weight, k_weight, table, positions, *ctx.how)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, table, positions = ctx.saved_tensors
+        dk = None if dk is None else dk.contiguous()  # there is none without k
+        grads = norm_rotary_bwd(dq.contiguous(), dk, q, k, q_weight, k_weight, table, positions, *ctx.how)
+        return (*grads, None, None, None, None, None)
+
+
+def norm_rotary_embedding(q, k, q_weight, k_weight, table, positions, eps: float = 1e-6, weight_offset: float = 0.0,
+                          interleaved: bool = False):
+    """``norm_rotary`` with (first) gradients for q, k and both weights (or q and its weight alone, with k None)."""
+    return NormRotaryFunction.apply(q, k, q_weight, k_weight, table, positions, eps, weight_offset, interleaved)
+
+
+def norm_rotary_append(q, k, v, q_weight, k_weight, table, k_cache, v_cache, page_table, kv_lens, cu_q=None, eps: float = 1e-6,
+                       weight_offset: float = 0.0, interleaved: bool = False, out=None):
+    """``rotary_append`` with the heads of q and k normed first, as in ``norm_rotary``, in the same pass."""
+    return _py.norm_rotary_append(q, k, v, q_weight, k_weight, table, k_cache, v_cache, page_table, kv_lens, cu_q, eps,
+                                  weight_offset, interleaved, out)
 
 
 # ------------------------------------------------------------------ pages

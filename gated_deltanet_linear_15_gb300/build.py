@@ -24,7 +24,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
 SOURCES = ["api.cu", "plan.cu", "fwd.cu", "fwd_prep_tc.cu", "fwd_tc.cu", "bwd.cu", "bwd_chain_tc.cu", "bwd_local_tc.cu",
            "recurrent.cu", "block_api.cu", "attn_rows.cu", "attn_chunk_tc.cu",
-           "rope.cu", "pages.cu", "rmsnorm.cu", "scan.cu"]
+           "rope.cu", "norm_rope.cu", "pages.cu", "rmsnorm.cu", "scan.cu"]
 PY_SOURCE = os.path.join(CSRC, "block_py.cpp")
 # tied to the C++ ABI of one torch and one Python, so it carries both in its name
 PY_LIB = os.path.join(BUILD, f"gdn_block_py.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")

@@ -31,6 +31,20 @@ struct RopeArgs {
 cudaError_t launch_rope(const RopeArgs &a, bool bf16_type, bool vec, cudaStream_t st);
 cudaError_t launch_rope_table(const double *freq, int pairs, int rows, double amplitude, float *table, cudaStream_t st);
 
+// ---- norm of heads with rotary positions
+constexpr int NORM_ROPE_MAX_DIM = 1024;  // features of a head
+struct NormRopeArgs {
+  RopeArgs r;                // groups q, k[, v]; backward: src x, dst dx, inverse set
+  const float *w[2];         // of q and k
+  float eps, off;
+  const void *dy[2];         // backward
+  long long dy_tok[2], dy_head[2];
+  float *part;               // backward: [CTAs][D]
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, bool bf16_type, bool vec, cudaStream_t st);
+int norm_rope_bwd_ctas(int tokens, int heads, int sms);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs &a, bool bf16_type, bool vec, int ctas, float *dw0, float *dw1, cudaStream_t st);
+
 // ---- pages
 constexpr int MAX_POOLS = 64;  // pools of one launch
 struct PoolList {

@@ -194,6 +194,108 @@ int check_row(int64_t row, const gdn_norm_shape *s, const char *name) {
 }
 bool vec_ok(const void *p, int64_t row, int v) { return !p || (aligned16(p) && row % v == 0); }
 
+// ------------------------------------------------------------------ rotary positions
+int check_rotary(const gdn_rotary_shape *s) {
+  if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
+  if (s->reserved) return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
+  if (s->dtype != GDN_BF16 && s->dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "unknown dtype");
+  if (s->tokens < 0 || s->q_heads < 0 || s->k_heads < 0) return fail(GDN_ERR_INVALID_ARG, "negative size");
+  if (s->head_dim < 2 || s->rot < 2 || s->rot % 2 || s->rot > s->head_dim)
+    return fail(GDN_ERR_INVALID_ARG, "need an even rot with 2 <= rot <= head_dim (got rot %d, head_dim %d)", s->rot, s->head_dim);
+  if (s->head_dim > 65536) return fail(GDN_ERR_UNSUPPORTED, "head_dim must be at most 65536");
+  if (s->table_rows < 0) return fail(GDN_ERR_INVALID_ARG, "table_rows must be >= 0");
+  if ((s->interleaved | s->inverse) & ~1) return fail(GDN_ERR_INVALID_ARG, "interleaved and inverse must be 0 or 1");
+  if ((long long)(s->q_heads + (long long)s->k_heads) * s->head_dim > (1 << 28)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  return GDN_OK;
+}
+int check_rotary_args(const gdn_rotary_shape *s, const void *q, const void *k, const float *table, const int32_t *positions,
+                      const void *q_out, const void *k_out) {
+  if (s->q_heads) {
+    TRY(need_ptr(q, "q"));
+    TRY(need_ptr(q_out, "q_out"));
+  }
+  if (s->k_heads) {
+    TRY(need_ptr(k, "k"));
+    TRY(need_ptr(k_out, "k_out"));
+  }
+  if (s->table_rows) TRY(need_aligned(table, "table"));
+  return need_ptr(positions, "positions");
+}
+// vec: every access may take 16 bytes
+RopeArgs rotary_args(const gdn_rotary_shape *s, const void *q, const void *k, const float *table, const int32_t *positions, void *q_out,
+                     void *k_out, bool &vec) {
+  RopeArgs a = {};
+  const int v = 16 / (int)esize(s->dtype);
+  vec = s->head_dim % (2 * v) == 0 && s->rot % (2 * v) == 0 && s->head_dim <= ROPE_THREADS * 2 * v;  // a CTA holds a head
+  auto add = [&](const void *src, void *dst, int heads, int64_t st_, int64_t sh, int64_t dt, int64_t dh) {
+    if (!heads) return;
+    a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, 0, heads, 1};
+    a.heads += heads;
+    vec = vec && aligned16(src) && aligned16(dst) && st_ % v == 0 && sh % v == 0 && dt % v == 0 && dh % v == 0;
+  };
+  add(q, q_out, s->q_heads, s->q_tok, s->q_head, s->qo_tok, s->qo_head);
+  add(k, k_out, s->k_heads, s->k_tok, s->k_head, s->ko_tok, s->ko_head);
+  a.tokens = s->tokens; a.D = s->head_dim; a.rot = s->rot; a.interleaved = s->interleaved; a.inverse = s->inverse;
+  a.rows = s->table_rows; a.table = table; a.positions = positions;
+  return a;
+}
+int check_append(const gdn_paged_shape *s) {
+  TRY(check_paged(s, false));
+  if (s->head_dim < 2 || s->rot < 2 || s->rot % 2 || s->rot > s->head_dim)
+    return fail(GDN_ERR_INVALID_ARG, "need an even rot with 2 <= rot <= head_dim (got rot %d, head_dim %d)", s->rot, s->head_dim);
+  if (s->head_dim > 65536 || (long long)s->num_heads * s->head_dim > (1 << 26)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  if (s->interleaved & ~1) return fail(GDN_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (s->table_rows < 0) return fail(GDN_ERR_INVALID_ARG, "table_rows must be >= 0");
+  return GDN_OK;
+}
+int check_append_args(const gdn_paged_shape *s, const void *q, const void *k, const void *v, const float *table, const void *k_cache,
+                      const void *v_cache, const int32_t *page_table, const int32_t *cu_q, const int32_t *kv_lens, const void *q_out) {
+  if (!cu_q && s->total_q % s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "without cu_q, total_q must be a multiple of num_seqs");
+  TRY(need_ptr(q, "q"));
+  TRY(need_ptr(k, "k"));
+  TRY(need_ptr(v, "v"));
+  TRY(need_ptr(k_cache, "k_cache"));
+  TRY(need_ptr(v_cache, "v_cache"));
+  TRY(need_ptr(q_out, "q_out"));
+  if (s->max_pages > 0) TRY(need_ptr(page_table, "page_table"));
+  TRY(need_ptr(kv_lens, "kv_lens"));
+  if (s->table_rows) TRY(need_aligned(table, "table"));
+  if (s->k_page < 1 || s->v_page < 1) return fail(GDN_ERR_INVALID_ARG, "page strides must be positive");
+  return GDN_OK;
+}
+RopeArgs append_args(const gdn_paged_shape *s, const void *q, const void *k, const void *v, const float *table, void *k_cache, void *v_cache,
+                     const int32_t *page_table, const int32_t *cu_q, const int32_t *kv_lens, void *q_out, bool &vec) {
+  RopeArgs a = {};
+  const int w = 16 / (int)esize(s->dtype);
+  vec = s->head_dim % (2 * w) == 0 && s->rot % (2 * w) == 0 && s->head_dim <= ROPE_THREADS * 2 * w;  // a CTA holds a head
+  auto add = [&](const void *src, void *dst, int heads, int turn, int64_t st_, int64_t sh, int64_t dt, int64_t dh, int64_t dp) {
+    a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, dp, heads, turn};
+    a.heads += heads;
+    vec = vec && aligned16(src) && aligned16(dst) && st_ % w == 0 && sh % w == 0 && dt % w == 0 && dh % w == 0 && dp % w == 0;
+  };
+  add(q, q_out, s->num_heads, 1, s->q_tok, s->q_head, s->o_tok, s->o_head, 0);
+  add(k, k_cache, s->num_kv_heads, 1, s->kn_tok, s->kn_head, s->k_tok, s->k_head, s->k_page);
+  add(v, v_cache, s->num_kv_heads, 0, s->vn_tok, s->vn_head, s->v_tok, s->v_head, s->v_page);
+  a.tokens = s->total_q; a.D = s->head_dim; a.rot = s->rot; a.interleaved = s->interleaved;
+  a.rows = s->table_rows; a.table = table;
+  a.cu_q = cu_q; a.kv_lens = kv_lens; a.pages = page_table; a.table_stride = s->table_stride;
+  a.N = s->num_seqs; a.per_seq = cu_q ? 0 : s->total_q / s->num_seqs;
+  a.log2P = ilog2(s->page_size); a.num_pages = s->num_pages; a.max_pages = s->max_pages;
+  return a;
+}
+int check_head_norm(int head_dim, int inverse, float eps, float off) {
+  if (head_dim > NORM_ROPE_MAX_DIM) return fail(GDN_ERR_UNSUPPORTED, "head_dim must be at most %d with a norm (got %d)", NORM_ROPE_MAX_DIM, head_dim);
+  if (inverse) return fail(GDN_ERR_INVALID_ARG, "inverse must be 0 with a norm");
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(GDN_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (!std::isfinite(off)) return fail(GDN_ERR_INVALID_ARG, "weight_offset must be finite");
+  return GDN_OK;
+}
+// the 32-byte units of a head are a power of two, in one warp
+bool head_in_warp(int head_dim, gdn_dtype d) {
+  const int units = head_dim * (int)esize(d) / 32;
+  return pow2(units) && units <= 32;
+}
+
 // ------------------------------------------------------------------ gated linear recurrence
 int check_scan(const gdn_scan_shape *s) {
   if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
@@ -353,40 +455,11 @@ int gdn_rotary_table(const double *freq, int pairs, int rows, double amplitude, 
 
 int gdn_rotary(const gdn_rotary_shape *s, const void *q, const void *k, const float *table, const int32_t *positions,
                void *q_out, void *k_out, gdn_stream_t stream) {
-  if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
-  if (s->reserved) return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
-  if (s->dtype != GDN_BF16 && s->dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "unknown dtype");
-  if (s->tokens < 0 || s->q_heads < 0 || s->k_heads < 0) return fail(GDN_ERR_INVALID_ARG, "negative size");
-  if (s->head_dim < 2 || s->rot < 2 || s->rot % 2 || s->rot > s->head_dim)
-    return fail(GDN_ERR_INVALID_ARG, "need an even rot with 2 <= rot <= head_dim (got rot %d, head_dim %d)", s->rot, s->head_dim);
-  if (s->head_dim > 65536) return fail(GDN_ERR_UNSUPPORTED, "head_dim must be at most 65536");
-  if (s->table_rows < 0) return fail(GDN_ERR_INVALID_ARG, "table_rows must be >= 0");
-  if ((s->interleaved | s->inverse) & ~1) return fail(GDN_ERR_INVALID_ARG, "interleaved and inverse must be 0 or 1");
-  if ((long long)(s->q_heads + (long long)s->k_heads) * s->head_dim > (1 << 28)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  TRY(check_rotary(s));
   if (s->tokens == 0 || s->q_heads + s->k_heads == 0) return GDN_OK;
-  if (s->q_heads) {
-    TRY(need_ptr(q, "q"));
-    TRY(need_ptr(q_out, "q_out"));
-  }
-  if (s->k_heads) {
-    TRY(need_ptr(k, "k"));
-    TRY(need_ptr(k_out, "k_out"));
-  }
-  if (s->table_rows) TRY(need_aligned(table, "table"));
-  TRY(need_ptr(positions, "positions"));
-  RopeArgs a = {};
-  const int v = 16 / (int)esize(s->dtype);
-  bool vec = s->head_dim % (2 * v) == 0 && s->rot % (2 * v) == 0 && s->head_dim <= ROPE_THREADS * 2 * v;  // a CTA holds a head
-  auto add = [&](const void *src, void *dst, int heads, int64_t st_, int64_t sh, int64_t dt, int64_t dh) {
-    if (!heads) return;
-    a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, 0, heads, 1};
-    a.heads += heads;
-    vec = vec && aligned16(src) && aligned16(dst) && st_ % v == 0 && sh % v == 0 && dt % v == 0 && dh % v == 0;
-  };
-  add(q, q_out, s->q_heads, s->q_tok, s->q_head, s->qo_tok, s->qo_head);
-  add(k, k_out, s->k_heads, s->k_tok, s->k_head, s->ko_tok, s->ko_head);
-  a.tokens = s->tokens; a.D = s->head_dim; a.rot = s->rot; a.interleaved = s->interleaved; a.inverse = s->inverse;
-  a.rows = s->table_rows; a.table = table; a.positions = positions;
+  TRY(check_rotary_args(s, q, k, table, positions, q_out, k_out));
+  bool vec;
+  const RopeArgs a = rotary_args(s, q, k, table, positions, q_out, k_out, vec);
   const Stream st = (Stream)stream;
   PROF("rope");
   CK(launch_rope(a, s->dtype == GDN_BF16, vec, st));
@@ -396,43 +469,117 @@ int gdn_rotary(const gdn_rotary_shape *s, const void *q, const void *k, const fl
 int gdn_rotary_append(const gdn_paged_shape *s, const void *q, const void *k, const void *v, const float *table,
                       void *k_cache, void *v_cache, const int32_t *page_table, const int32_t *cu_q,
                       const int32_t *kv_lens, void *q_out, gdn_stream_t stream) {
-  TRY(check_paged(s, false));
-  if (s->head_dim < 2 || s->rot < 2 || s->rot % 2 || s->rot > s->head_dim)
-    return fail(GDN_ERR_INVALID_ARG, "need an even rot with 2 <= rot <= head_dim (got rot %d, head_dim %d)", s->rot, s->head_dim);
-  if (s->head_dim > 65536 || (long long)s->num_heads * s->head_dim > (1 << 26)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
-  if (s->interleaved & ~1) return fail(GDN_ERR_INVALID_ARG, "interleaved must be 0 or 1");
-  if (s->table_rows < 0) return fail(GDN_ERR_INVALID_ARG, "table_rows must be >= 0");
+  TRY(check_append(s));
   if (s->total_q == 0 || s->num_seqs == 0) return GDN_OK;
-  if (!cu_q && s->total_q % s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "without cu_q, total_q must be a multiple of num_seqs");
-  TRY(need_ptr(q, "q"));
-  TRY(need_ptr(k, "k"));
-  TRY(need_ptr(v, "v"));
-  TRY(need_ptr(k_cache, "k_cache"));
-  TRY(need_ptr(v_cache, "v_cache"));
-  TRY(need_ptr(q_out, "q_out"));
-  if (s->max_pages > 0) TRY(need_ptr(page_table, "page_table"));
-  TRY(need_ptr(kv_lens, "kv_lens"));
-  if (s->table_rows) TRY(need_aligned(table, "table"));
-  if (s->k_page < 1 || s->v_page < 1) return fail(GDN_ERR_INVALID_ARG, "page strides must be positive");
-  RopeArgs a = {};
-  const int w = 16 / (int)esize(s->dtype);
-  bool vec = s->head_dim % (2 * w) == 0 && s->rot % (2 * w) == 0 && s->head_dim <= ROPE_THREADS * 2 * w;  // a CTA holds a head
-  auto add = [&](const void *src, void *dst, int heads, int turn, int64_t st_, int64_t sh, int64_t dt, int64_t dh, int64_t dp) {
-    a.grp[a.ngrp++] = {src, dst, st_, sh, dt, dh, dp, heads, turn};
-    a.heads += heads;
-    vec = vec && aligned16(src) && aligned16(dst) && st_ % w == 0 && sh % w == 0 && dt % w == 0 && dh % w == 0 && dp % w == 0;
-  };
-  add(q, q_out, s->num_heads, 1, s->q_tok, s->q_head, s->o_tok, s->o_head, 0);
-  add(k, k_cache, s->num_kv_heads, 1, s->kn_tok, s->kn_head, s->k_tok, s->k_head, s->k_page);
-  add(v, v_cache, s->num_kv_heads, 0, s->vn_tok, s->vn_head, s->v_tok, s->v_head, s->v_page);
-  a.tokens = s->total_q; a.D = s->head_dim; a.rot = s->rot; a.interleaved = s->interleaved;
-  a.rows = s->table_rows; a.table = table;
-  a.cu_q = cu_q; a.kv_lens = kv_lens; a.pages = page_table; a.table_stride = s->table_stride;
-  a.N = s->num_seqs; a.per_seq = cu_q ? 0 : s->total_q / s->num_seqs;
-  a.log2P = ilog2(s->page_size); a.num_pages = s->num_pages; a.max_pages = s->max_pages;
+  TRY(check_append_args(s, q, k, v, table, k_cache, v_cache, page_table, cu_q, kv_lens, q_out));
+  bool vec;
+  const RopeArgs a = append_args(s, q, k, v, table, k_cache, v_cache, page_table, cu_q, kv_lens, q_out, vec);
   const Stream st = (Stream)stream;
   PROF("rope_append");
   CK(launch_rope(a, s->dtype == GDN_BF16, vec, st));
+  return GDN_OK;
+}
+
+int gdn_norm_rotary(const gdn_rotary_shape *s, float eps, float off, const void *q, const void *k, const float *wq, const float *wk,
+                    const float *table, const int32_t *positions, void *q_out, void *k_out, gdn_stream_t stream) {
+  TRY(check_rotary(s));
+  TRY(check_head_norm(s->head_dim, s->inverse, eps, off));
+  if (s->tokens == 0 || s->q_heads + s->k_heads == 0) return GDN_OK;
+  TRY(check_rotary_args(s, q, k, table, positions, q_out, k_out));
+  if (s->q_heads) TRY(need_ptr(wq, "q_weight"));
+  if (s->k_heads) TRY(need_ptr(wk, "k_weight"));
+  bool vec;
+  NormRopeArgs n = {};
+  n.r = rotary_args(s, q, k, table, positions, q_out, k_out, vec);
+  n.w[0] = s->q_heads ? wq : wk;
+  n.w[1] = s->q_heads && s->k_heads ? wk : nullptr;
+  n.eps = eps;
+  n.off = off;
+  const Stream st = (Stream)stream;
+  PROF("norm_rope");
+  CK(launch_norm_rope(n, s->dtype == GDN_BF16, vec && head_in_warp(s->head_dim, s->dtype), st));
+  return GDN_OK;
+}
+
+size_t gdn_norm_rotary_bwd_workspace_size(const gdn_rotary_shape *s) {
+  if (check_rotary(s) || check_head_norm(s->head_dim, s->inverse, 1.f, 0.f)) return 0;
+  return up256((size_t)norm_rope_bwd_ctas(s->tokens, s->q_heads + s->k_heads, num_sms()) * s->head_dim * sizeof(float));
+}
+
+int gdn_norm_rotary_bwd(const gdn_rotary_shape *s, float eps, float off, const void *dq_out, const void *dk_out, const void *q,
+                        const void *k, const float *wq, const float *wk, const float *table, const int32_t *positions, void *dq, void *dk,
+                        float *dwq, float *dwk, void *ws, size_t ws_bytes, gdn_stream_t stream) {
+  TRY(check_rotary(s));
+  TRY(check_head_norm(s->head_dim, s->inverse, eps, off));
+  const Stream st = (Stream)stream;
+  if (s->q_heads) TRY(need_ptr(dwq, "dq_weight"));
+  if (s->k_heads) TRY(need_ptr(dwk, "dk_weight"));
+  // a weight that no head takes has a gradient of zero
+  const bool none = s->tokens == 0;
+  if (dwq && (none || !s->q_heads)) CK(cudaMemsetAsync(dwq, 0, s->head_dim * sizeof(float), st));
+  if (dwk && (none || !s->k_heads)) CK(cudaMemsetAsync(dwk, 0, s->head_dim * sizeof(float), st));
+  if (none || s->q_heads + s->k_heads == 0) return GDN_OK;
+  TRY(check_rotary_args(s, q, k, table, positions, dq, dk));
+  if (s->q_heads) {
+    TRY(need_ptr(dq_out, "dq_out"));
+    TRY(need_ptr(wq, "q_weight"));
+  }
+  if (s->k_heads) {
+    TRY(need_ptr(dk_out, "dk_out"));
+    TRY(need_ptr(wk, "k_weight"));
+  }
+  if (s->q_heads && s->k_heads && dwq == dwk) return fail(GDN_ERR_INVALID_ARG, "dq_weight and dk_weight need memory of their own");
+  const size_t need = gdn_norm_rotary_bwd_workspace_size(s);
+  if (!ws || ws_bytes < need) return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+  TRY(need_aligned(ws, "workspace"));
+  gdn_rotary_shape o = *s;  // of the outputs
+  o.qo_tok = (int64_t)s->q_heads * s->head_dim;
+  o.ko_tok = (int64_t)s->k_heads * s->head_dim;
+  o.qo_head = o.ko_head = s->head_dim;
+  bool vec;
+  NormRopeArgs n = {};
+  n.r = rotary_args(&o, q, k, table, positions, dq, dk, vec);
+  n.r.inverse = 1;
+  const int v = 16 / (int)esize(s->dtype);
+  int g = 0;
+  auto add = [&](const void *dy, int64_t tok, int64_t head, const float *w) {
+    n.w[g] = w;
+    n.dy[g] = dy;
+    n.dy_tok[g] = tok;
+    n.dy_head[g++] = head;
+    vec = vec && aligned16(dy) && tok % v == 0 && head % v == 0;
+  };
+  if (s->q_heads) add(dq_out, s->qo_tok, s->qo_head, wq);
+  if (s->k_heads) add(dk_out, s->ko_tok, s->ko_head, wk);
+  n.eps = eps;
+  n.off = off;
+  n.part = static_cast<float *>(ws);
+  PROF("norm_rope_bwd");
+  CK(launch_norm_rope_bwd(n, s->dtype == GDN_BF16, vec && head_in_warp(s->head_dim, s->dtype),
+                          norm_rope_bwd_ctas(s->tokens, s->q_heads + s->k_heads, num_sms()), s->q_heads ? dwq : dwk,
+                          s->q_heads && s->k_heads ? dwk : nullptr, st));
+  return GDN_OK;
+}
+
+int gdn_norm_rotary_append(const gdn_paged_shape *s, float eps, float off, const void *q, const void *k, const void *v, const float *wq,
+                           const float *wk, const float *table, void *k_cache, void *v_cache, const int32_t *page_table,
+                           const int32_t *cu_q, const int32_t *kv_lens, void *q_out, gdn_stream_t stream) {
+  TRY(check_append(s));
+  TRY(check_head_norm(s->head_dim, 0, eps, off));
+  if (s->total_q == 0 || s->num_seqs == 0) return GDN_OK;
+  TRY(check_append_args(s, q, k, v, table, k_cache, v_cache, page_table, cu_q, kv_lens, q_out));
+  TRY(need_ptr(wq, "q_weight"));
+  TRY(need_ptr(wk, "k_weight"));
+  bool vec;
+  NormRopeArgs n = {};
+  n.r = append_args(s, q, k, v, table, k_cache, v_cache, page_table, cu_q, kv_lens, q_out, vec);
+  n.w[0] = wq;
+  n.w[1] = wk;
+  n.eps = eps;
+  n.off = off;
+  const Stream st = (Stream)stream;
+  PROF("norm_rope_append");
+  CK(launch_norm_rope(n, s->dtype == GDN_BF16, vec && head_in_warp(s->head_dim, s->dtype), st));
   return GDN_OK;
 }
 

@@ -42,6 +42,10 @@ struct Api {
   decltype(&gdn_scan_fwd) scan_fwd;
   decltype(&gdn_scan_bwd) scan_bwd;
   decltype(&gdn_scan_step) scan_step;
+  decltype(&gdn_norm_rotary) norm_rotary;
+  decltype(&gdn_norm_rotary_bwd_workspace_size) norm_rotary_bwd_workspace_size;
+  decltype(&gdn_norm_rotary_bwd) norm_rotary_bwd;
+  decltype(&gdn_norm_rotary_append) norm_rotary_append;
   decltype(&gdn_status_string) status_string;
   decltype(&gdn_last_error_string) last_error_string;
 } api;
@@ -252,11 +256,8 @@ PyObject *paged_attention_status(PyObject *const *a) {
   return PyLong_FromLong(api.paged_attn_status(&s, ws.data_ptr(), (gdn_stream_t)stream(q)));
 }
 
-// q, k, table, positions, interleaved, inverse, inplace
-PyObject *rotary(PyObject *const *a) {
-  const Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "table"), &pos = tensor(a[3], "positions");
-  const Tensor *k = maybe(a[1], "k");
-  const bool inplace = truth(a[6]);
+// the shape of q [T, heads, D] and k (or none) with their angles; the outputs' strides stay open
+gdn_rotary_shape rotary_shape(const Tensor &q, const Tensor *k, const Tensor &table, const Tensor &pos) {
   heads(q, "q");
   angle_table(table);
   gdn_rotary_shape s = {};
@@ -267,39 +268,51 @@ PyObject *rotary(PyObject *const *a) {
   s.head_dim = fits(q.size(2), "the number of features");
   s.rot = fits(2 * table.size(1), "rot");
   s.table_rows = fits(table.size(0), "the table");
+  s.q_tok = q.stride(0);
+  s.q_head = q.stride(1);
+  if (k) {
+    heads(*k, "k");
+    same_type(*k, q, "k");
+    if (k->size(0) != q.size(0) || k->size(2) != q.size(2)) bad("q and k must have the same tokens and features");
+    s.k_heads = fits(k->size(1), "the number of heads");
+    s.k_tok = k->stride(0);
+    s.k_head = k->stride(1);
+  }
+  return s;
+}
+void out_strides(gdn_rotary_shape &s, const Tensor &q, const Tensor &k) {
+  s.qo_tok = q.stride(0);
+  s.qo_head = q.stride(1);
+  if (!k.defined()) return;
+  s.ko_tok = k.stride(0);
+  s.ko_head = k.stride(1);
+}
+void *data(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+// q, k, table, positions, interleaved, inverse, inplace
+PyObject *rotary(PyObject *const *a) {
+  const Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "table"), &pos = tensor(a[3], "positions");
+  const Tensor *k = maybe(a[1], "k");
+  const bool inplace = truth(a[6]);
+  gdn_rotary_shape s = rotary_shape(q, k, table, pos);
   s.interleaved = truth(a[4]);
   s.inverse = truth(a[5]);
   if (inplace) written(q, "q");
   if (inplace && k) written(*k, "k");
   const Tensor qo = inplace ? q : at::empty(q.sizes(), q.options());
-  s.q_tok = q.stride(0);
-  s.q_head = q.stride(1);
-  s.qo_tok = qo.stride(0);
-  s.qo_head = qo.stride(1);
   Tensor ko;
-  if (k) {
-    heads(*k, "k");
-    same_type(*k, q, "k");
-    if (k->size(0) != q.size(0) || k->size(2) != q.size(2)) bad("q and k must have the same tokens and features");
-    ko = inplace ? *k : at::empty(k->sizes(), k->options());
-    s.k_heads = fits(k->size(1), "the number of heads");
-    s.k_tok = k->stride(0);
-    s.k_head = k->stride(1);
-    s.ko_tok = ko.stride(0);
-    s.ko_head = ko.stride(1);
-  }
-  check(api.rotary(&s, q.data_ptr(), ptr(k), static_cast<const float *>(table.data_ptr()), i32(pos), qo.data_ptr(),
-                   ko.defined() ? ko.data_ptr() : nullptr, (gdn_stream_t)stream(q)),
+  if (k) ko = inplace ? *k : at::empty(k->sizes(), k->options());
+  out_strides(s, qo, ko);
+  check(api.rotary(&s, q.data_ptr(), ptr(k), static_cast<const float *>(table.data_ptr()), i32(pos), qo.data_ptr(), data(ko),
+                   (gdn_stream_t)stream(q)),
         "gdn_rotary");
   if (inplace) wrote({&q, k});
   return pack({qo, ko});
 }
 
-// q, k, v, table, k_cache, v_cache, page_table, kv_lens, cu_q, interleaved, out
-PyObject *rotary_append(PyObject *const *a) {
-  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &table = tensor(a[3], "table"),
-               &kc = tensor(a[4], "k_cache"), &vc = tensor(a[5], "v_cache"), &pages = tensor(a[6], "page_table"), &lens = tensor(a[7], "kv_lens");
-  const Tensor *cu = maybe(a[8], "cu_q"), *out = maybe(a[10], "out");
+// the new tokens of an append: a shape with everything but interleaved
+gdn_paged_shape append_shape(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &table, const Tensor &kc, const Tensor &vc,
+                             const Tensor &pages, const Tensor &lens, const Tensor *cu, const Tensor &o) {
   gdn_paged_shape s = paged_shape(q, kc, vc, pages, lens, cu);
   written(kc, "k_cache");
   written(vc, "v_cache");
@@ -310,7 +323,6 @@ PyObject *rotary_append(PyObject *const *a) {
   if (k.size(0) != q.size(0) || k.size(1) != kc.size(2) || k.size(2) != q.size(2) || v.sizes() != k.sizes())
     bad("k and v must be [new tokens, kv heads, features]");
   angle_table(table);
-  const Tensor o = like(out, q);
   s.o_tok = o.stride(0);
   s.o_head = o.stride(1);
   s.kn_tok = k.stride(0);
@@ -319,10 +331,109 @@ PyObject *rotary_append(PyObject *const *a) {
   s.vn_head = v.stride(1);
   s.rot = fits(2 * table.size(1), "rot");
   s.table_rows = fits(table.size(0), "the table");
+  return s;
+}
+
+// q, k, v, table, k_cache, v_cache, page_table, kv_lens, cu_q, interleaved, out
+PyObject *rotary_append(PyObject *const *a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &table = tensor(a[3], "table"),
+               &kc = tensor(a[4], "k_cache"), &vc = tensor(a[5], "v_cache"), &pages = tensor(a[6], "page_table"), &lens = tensor(a[7], "kv_lens");
+  const Tensor *cu = maybe(a[8], "cu_q"), *out = maybe(a[10], "out");
+  heads(q, "q");
+  const Tensor o = like(out, q);
+  gdn_paged_shape s = append_shape(q, k, v, table, kc, vc, pages, lens, cu, o);
   s.interleaved = truth(a[9]);
   check(api.rotary_append(&s, q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const float *>(table.data_ptr()), kc.data_ptr(),
                           vc.data_ptr(), i32(pages), i32(cu), i32(lens), o.data_ptr(), (gdn_stream_t)stream(q)),
         "gdn_rotary_append");
+  wrote({&kc, &vc, out});
+  return THPVariable_Wrap(o);
+}
+
+// ------------------------------------------------------------------ norm of heads with rotary positions
+const float *head_weight(const Tensor &w, const Tensor &q, const char *name) {
+  here(w, name);
+  if (w.scalar_type() != at::kFloat || w.dim() != 1 || w.size(0) != q.size(2) || !w.is_contiguous())
+    bad(std::string(name) + " must be a contiguous fp32 CUDA tensor [features]");
+  return static_cast<const float *>(w.data_ptr());
+}
+// of k: there is none without k
+const float *head_weight(PyObject *o, const Tensor *k, const char *name) {
+  const Tensor *w = maybe(o, name);
+  if (!k) return nullptr;
+  if (!w) bad(std::string(name) + " is missing");
+  return head_weight(*w, *k, name);
+}
+
+// q, k, q_weight, k_weight, table, positions, eps, weight_offset, interleaved
+PyObject *norm_rotary(PyObject *const *a) {
+  const Tensor &q = tensor(a[0], "q"), &wq = tensor(a[2], "q_weight"), &table = tensor(a[4], "table"), &pos = tensor(a[5], "positions");
+  const Tensor *k = maybe(a[1], "k");
+  gdn_rotary_shape s = rotary_shape(q, k, table, pos);
+  s.interleaved = truth(a[8]);
+  const float *pq = head_weight(wq, q, "q_weight"), *pk = head_weight(a[3], k, "k_weight");
+  const Tensor qo = at::empty(q.sizes(), q.options());
+  Tensor ko;
+  if (k) ko = at::empty(k->sizes(), k->options());
+  out_strides(s, qo, ko);
+  check(api.norm_rotary(&s, (float)number(a[6]), (float)number(a[7]), q.data_ptr(), ptr(k), pq, pk,
+                        static_cast<const float *>(table.data_ptr()), i32(pos), qo.data_ptr(), data(ko), (gdn_stream_t)stream(q)),
+        "gdn_norm_rotary");
+  return pack({qo, ko});
+}
+
+// dq, dk, q, k, q_weight, k_weight, table, positions, eps, weight_offset, interleaved -> (dq, dk, dq_weight, dk_weight)
+PyObject *norm_rotary_bwd(PyObject *const *a) {
+  const Tensor &dy = tensor(a[0], "dq"), &q = tensor(a[2], "q"), &wq = tensor(a[4], "q_weight"), &table = tensor(a[6], "table"),
+               &pos = tensor(a[7], "positions");
+  const Tensor *dk = maybe(a[1], "dk"), *k = maybe(a[3], "k");
+  gdn_rotary_shape s = rotary_shape(q, k, table, pos);
+  s.interleaved = truth(a[10]);
+  heads(dy, "dq");
+  same_type(dy, q, "dq");
+  if (dy.sizes() != q.sizes()) bad("dq must have the shape of q");
+  if ((dk != nullptr) != (k != nullptr)) bad("dk and k go together");
+  Tensor gk, wk;
+  if (k) {
+    heads(*dk, "dk");
+    same_type(*dk, q, "dk");
+    if (dk->sizes() != k->sizes()) bad("dk must have the shape of k");
+    gk = *dk;
+  }
+  const float *pq = head_weight(wq, q, "q_weight"), *pk = head_weight(a[5], k, "k_weight");
+  out_strides(s, dy, gk);
+  const Tensor dq = at::empty(q.sizes(), q.options()), dwq = at::empty(wq.sizes(), wq.options());
+  Tensor dkk, dwk;
+  if (k) {
+    dkk = at::empty(k->sizes(), k->options());
+    dwk = at::empty(wq.sizes(), wq.options());
+  }
+  const size_t need = api.norm_rotary_bwd_workspace_size(&s);
+  if (!need) check(GDN_ERR_INVALID_ARG, "gdn_norm_rotary_bwd_workspace_size");
+  const Tensor ws = bytes(need, q);
+  check(api.norm_rotary_bwd(&s, (float)number(a[8]), (float)number(a[9]), dy.data_ptr(), data(gk), q.data_ptr(), ptr(k), pq, pk,
+                            static_cast<const float *>(table.data_ptr()), i32(pos), dq.data_ptr(), data(dkk),
+                            static_cast<float *>(dwq.data_ptr()), static_cast<float *>(data(dwk)), ws.data_ptr(), ws.nbytes(),
+                            (gdn_stream_t)stream(q)),
+        "gdn_norm_rotary_bwd");
+  return pack({dq, dkk, dwq, dwk});
+}
+
+// q, k, v, q_weight, k_weight, table, k_cache, v_cache, page_table, kv_lens, cu_q, eps, weight_offset, interleaved, out
+PyObject *norm_rotary_append(PyObject *const *a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &wq = tensor(a[3], "q_weight"),
+               &wk = tensor(a[4], "k_weight"), &table = tensor(a[5], "table"), &kc = tensor(a[6], "k_cache"), &vc = tensor(a[7], "v_cache"),
+               &pages = tensor(a[8], "page_table"), &lens = tensor(a[9], "kv_lens");
+  const Tensor *cu = maybe(a[10], "cu_q"), *out = maybe(a[14], "out");
+  heads(q, "q");
+  const Tensor o = like(out, q);
+  gdn_paged_shape s = append_shape(q, k, v, table, kc, vc, pages, lens, cu, o);
+  s.interleaved = truth(a[13]);
+  const float *pq = head_weight(wq, q, "q_weight"), *pk = head_weight(wk, q, "k_weight");
+  check(api.norm_rotary_append(&s, (float)number(a[11]), (float)number(a[12]), q.data_ptr(), k.data_ptr(), v.data_ptr(), pq, pk,
+                               static_cast<const float *>(table.data_ptr()), kc.data_ptr(), vc.data_ptr(), i32(pages), i32(cu), i32(lens),
+                               o.data_ptr(), (gdn_stream_t)stream(q)),
+        "gdn_norm_rotary_append");
   wrote({&kc, &vc, out});
   return THPVariable_Wrap(o);
 }
@@ -710,6 +821,9 @@ PyMethodDef methods[] = {ENTRY(connect, (int)(sizeof(Api) / sizeof(void *))),
                          ENTRY(copy_slots, 3),
                          ENTRY(rms_norm, 8),
                          ENTRY(rms_norm_bwd, 6),
+                         ENTRY(norm_rotary, 9),
+                         ENTRY(norm_rotary_bwd, 11),
+                         ENTRY(norm_rotary_append, 15),
                          ENTRY(gated_scan, 6),
                          ENTRY(gated_scan_bwd, 7),
                          ENTRY(gated_scan_step, 3),

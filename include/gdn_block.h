@@ -1,6 +1,6 @@
 /*
  * gdn_block.h -- C ABI of the operators that a hybrid stack puts next to its gated delta-rule layers (GB300,
- * sm_103a): attention of new tokens over a paged key/value cache, rotary positions, the upkeep of the cache's
+ * sm_103a): attention of new tokens over a paged key/value cache, rotary positions (alone or behind a norm of each head), the upkeep of the cache's
  * pages, the root-mean-square norm of the residual stream, and a gated linear recurrence with one state per channel.
  *
  * A stack of gated delta-rule layers carries a softmax-attention layer after every few of them (onedev.kr summary
@@ -132,6 +132,31 @@ int gdn_rotary(const gdn_rotary_shape *shape, const void *q, const void *k, cons
 int gdn_rotary_append(const gdn_paged_shape *shape, const void *q, const void *k, const void *v, const float *table,
                       void *k_cache, void *v_cache, const int32_t *page_table, const int32_t *cu_q /* nullable */,
                       const int32_t *kv_lens, void *q_out, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------ norm of heads with rotary positions
+ * The root-mean-square norm of every head of q and k, and its turn, in one pass (y and all between in fp32, rounded once):
+ *     r = 1 / sqrt(mean(x^2) + eps),   y = turn(x r (weight + weight_offset))
+ * over the features of a head; turn, table and positions as in gdn_rotary (inverse must be 0); weights fp32 [D], one for
+ * the heads of q and one for those of k.  head_dim at most 1024.  q_out and k_out may be q and k themselves, with
+ * their strides. */
+int gdn_norm_rotary(const gdn_rotary_shape *shape, float eps, float weight_offset, const void *q, const void *k,
+                    const float *q_weight, const float *k_weight, const float *table, const int32_t *positions, void *q_out,
+                    void *k_out, gdn_stream_t stream);
+
+/* Gradients, given dq_out and dk_out (strides qo_*, ko_* of the shape) and the inputs q and k (q_*, k_*): dq [T, q_heads, D] and
+ * dk [T, k_heads, D], contiguous, and dq_weight, dk_weight fp32 [D] (summed in a fixed order).  With u the turned-back gradient
+ * and xhat = x r: dx = r (u w - xhat mean(u w xhat)), w = weight + weight_offset, dw = sum of u xhat. */
+size_t gdn_norm_rotary_bwd_workspace_size(const gdn_rotary_shape *shape);
+int gdn_norm_rotary_bwd(const gdn_rotary_shape *shape, float eps, float weight_offset, const void *dq_out, const void *dk_out,
+                        const void *q, const void *k, const float *q_weight, const float *k_weight, const float *table,
+                        const int32_t *positions, void *dq, void *dk, float *dq_weight, float *dk_weight, void *workspace,
+                        size_t workspace_bytes, gdn_stream_t stream);
+
+/* gdn_rotary_append with the heads of q and k normed before they turn. */
+int gdn_norm_rotary_append(const gdn_paged_shape *shape, float eps, float weight_offset, const void *q, const void *k,
+                           const void *v, const float *q_weight, const float *k_weight, const float *table, void *k_cache,
+                           void *v_cache, const int32_t *page_table, const int32_t *cu_q /* nullable */,
+                           const int32_t *kv_lens, void *q_out, gdn_stream_t stream);
 
 /* ------------------------------------------------------------------ pages
  * Bookkeeping on the device: page_table int32 [num_seqs, max_pages] (-1: none), seq_lens int32 [num_seqs] (tokens),
