@@ -6,8 +6,11 @@
 //
 // Bound by bytes: every element is read once and written once (backward: x and dy read, dx written).  A thread's unit is
 // that of rope.cu, 32 bytes of a head that hold whole pairs; the D sizeof(I) / 32 threads of a head are neighbours in a
-// warp, so a head's sums take a few shuffles, and the data stay in registers between the sum and the turn.  Weights come
-// from shared memory: in registers, those of q and k take 32 and cost a third of the loads in flight.
+// warp, so a head's sums take a few shuffles, and the data stay in registers between the sum and the turn.  Units come by
+// cp.async to places of the thread's own, a few ahead of the one in work.  (Loaded to registers instead, as in rope.cu,
+// the sums' latencies left too few bytes in flight: 8192 tokens of 32 + 8 + 8 heads 50 us.)  Arithmetic is in packed
+// pairs of fp32.  8192 tokens of 32 + 8 + 8 heads of 128, bf16, appended: 36.8 us on the GPU, 5.6 TB/s (rope.cu without the
+// norm: 34.3); the backward of 16384 tokens of 16 + 4 heads: 44 us, 5.8 TB/s, and 4 us for the weights' sums.
 //
 // The backward's CTAs stay and walk over tokens, some of them over the heads of q and the others over those of k, since a
 // thread's place in the head does not change: it keeps its sums of dw in registers.  Each CTA leaves one partial row, and a
@@ -22,32 +25,170 @@ namespace gdn {
 
 namespace {
 
+constexpr int UNF = 3, UNB = 2;  // units of a thread on their way, forward and backward
 constexpr int NTB = 256, MAXD = NORM_ROPE_MAX_DIM;  // threads of the backward, features of a head
 
-// sum over the `n` neighbouring lanes (a power of two) that hold a head
-__device__ __forceinline__ float head_sum(float x, int n) {
-  const unsigned mask = n == 32 ? 0xffffffffu : ((1u << n) - 1) << (threadIdx.x & 31 & ~(n - 1));
-  for (int o = n >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+// sum over the neighbouring lanes (UPH, or n where that is 0: a power of two) that hold a head
+template <int UPH> __device__ __forceinline__ float head_sum(float x, int n) {
+  const int m = UPH ? UPH : n;
+  const unsigned mask = m == 32 ? 0xffffffffu : ((1u << m) - 1) << (threadIdx.x & 31 & ~(m - 1));
+  if constexpr (UPH > 0) {
+#pragma unroll
+    for (int o = UPH / 2; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+  } else {
+    for (int o = m >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+  }
   return x;
 }
-template <int V> __device__ __forceinline__ void read_weights(const float *w, int f0, int f1, float (&p)[V], float (&q)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; i += 4) {
-    const float4 a = *reinterpret_cast<const float4 *>(w + f0 + i), b = *reinterpret_cast<const float4 *>(w + f1 + i);
-    p[i] = a.x; p[i + 1] = a.y; p[i + 2] = a.z; p[i + 3] = a.w;
-    q[i] = b.x; q[i + 1] = b.y; q[i + 2] = b.z; q[i + 3] = b.w;
+// 16 bytes to shared memory.  Where a unit's pieces are neighbours, each of its two copies takes half a sector, and they go by
+// way of L1, so that L2 is asked once (with this and the stores below 16384 tokens of 16 + 4 interleaved heads go backward in
+// 44 us instead of 66; pieces that are not neighbours are 2 us faster past L1, 8192 tokens of 48 heads appended).
+__device__ __forceinline__ void copy16(void *smem, const void *gmem, bool neighbours) {
+  if (neighbours) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem));
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem));
+}
+// both pieces of a unit to global memory, in one store where they are neighbours on a 32-byte boundary (two of half a
+// sector each otherwise)
+template <typename I> __device__ __forceinline__ void store_unit(I *p, int gap, const uint4 &a, const uint4 &b) {
+  if (gap * sizeof(I) == 16 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                 "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4 *>(p) = a;
+    *reinterpret_cast<uint4 *>(p + gap) = b;
   }
 }
-// the angles of the unit's pairs u V .. at position pos
-template <int V> __device__ __forceinline__ void read_angles(const RopeArgs &a, int pos, int u, float (&c)[V], float (&s)[V]) {
-  const float2 *cs = reinterpret_cast<const float2 *>(a.table) + (long long)pos * (a.rot / 2) + u * V;
+// A unit's features as packed pairs: piece 0 in v[0 .. PV), piece 1 in v[PV .. 2 PV).
+template <typename I> struct Unit {
+  static constexpr int V = 16 / sizeof(I), PV = V / 2;
+  uint64_t v[2 * PV];
+  __device__ __forceinline__ void widen(const uint4 &a, const uint4 &b) {
+    if constexpr (sizeof(I) == 2) {
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int i = 0; i < V; i += 2) {
-    const float4 w = *reinterpret_cast<const float4 *>(cs + i);
-    c[i] = w.x;
-    c[i + 1] = w.z;
-    s[i] = a.inverse ? -w.y : w.y;
-    s[i + 1] = a.inverse ? -w.w : w.w;
+      for (int i = 0; i < 8; ++i) v[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+      v[0] = pk(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[1] = pk(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[2] = pk(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[3] = pk(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+  }
+  __device__ __forceinline__ void pack(uint4 &a, uint4 &b) const {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 2 * PV; ++i) {
+      float x, y;
+      upk(v[i], x, y);
+      if constexpr (sizeof(I) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        w[2 * i] = __float_as_uint(x);
+        w[2 * i + 1] = __float_as_uint(y);
+      }
+    }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  // four values every `step` places
+  __device__ __forceinline__ void read(const float4 *p, int step) {
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p + i * step);
+      v[2 * i] = a.x;
+      v[2 * i + 1] = a.y;
+    }
+  }
+  __device__ __forceinline__ float dot(const Unit &o) const {
+    uint64_t s0 = mul2(v[0], o.v[0]), s1 = mul2(v[PV], o.v[PV]);
+#pragma unroll
+    for (int i = 1; i < PV; ++i) {
+      s0 = fma2(v[i], o.v[i], s0);
+      s1 = fma2(v[PV + i], o.v[PV + i], s1);
+    }
+    float x, y;
+    upk(add2(s0, s1), x, y);
+    return x + y;
+  }
+  __device__ __forceinline__ Unit operator*(const Unit &o) const {
+    Unit r;
+#pragma unroll
+    for (int i = 0; i < 2 * PV; ++i) r.v[i] = mul2(v[i], o.v[i]);
+    return r;
+  }
+  __device__ __forceinline__ Unit operator*(float f) const {
+    const uint64_t ff = pk(f, f);
+    Unit r;
+#pragma unroll
+    for (int i = 0; i < 2 * PV; ++i) r.v[i] = mul2(v[i], ff);
+    return r;
+  }
+  __device__ __forceinline__ Unit plus(const Unit &o, float f) const {  // this + o f
+    const uint64_t ff = pk(f, f);
+    Unit r;
+#pragma unroll
+    for (int i = 0; i < 2 * PV; ++i) r.v[i] = fma2(o.v[i], ff, v[i]);
+    return r;
+  }
+};
+// A unit's angles: halves (IL false): pairs of feature i of both pieces, c, s and -s of two neighbours in a word; interleaved:
+// pairs of neighbours, (c, c) and (-s, s).
+template <typename I, bool IL> struct Angles {
+  static constexpr int V = Unit<I>::V, PV = V / 2, N = IL ? V : PV;
+  uint64_t c[N], s[N], m[IL ? 1 : N];
+  // from the table's floats of the pairs u V .., four every `step` places
+  __device__ __forceinline__ void read(const float4 *cs, int step, bool inverse) {
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+      float4 w = cs[i * step];
+      if (inverse) {
+        w.y = -w.y;
+        w.w = -w.w;
+      }
+      if constexpr (IL) {
+        c[2 * i] = pk(w.x, w.x);
+        c[2 * i + 1] = pk(w.z, w.z);
+        s[2 * i] = pk(-w.y, w.y);
+        s[2 * i + 1] = pk(-w.w, w.w);
+      } else {
+        c[i] = pk(w.x, w.z);
+        s[i] = pk(w.y, w.w);
+        m[i] = pk(-w.y, -w.w);
+      }
+    }
+  }
+  __device__ __forceinline__ void turn(Unit<I> &x) const {
+    if constexpr (IL) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float p, q;
+        upk(x.v[i], p, q);
+        x.v[i] = fma2(pk(q, p), s[i], mul2(x.v[i], c[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PV; ++i) {
+        const uint64_t p = x.v[i], q = x.v[PV + i];
+        x.v[i] = fma2(q, m[i], mul2(p, c[i]));
+        x.v[PV + i] = fma2(p, s[i], mul2(q, c[i]));
+      }
+    }
+  }
+};
+// where a position's angles of the unit's pairs u V .. lie
+template <int V> __device__ __forceinline__ const float4 *angles_at(const RopeArgs &a, int pos, int u) {
+  return reinterpret_cast<const float4 *>(a.table + ((long long)pos * (a.rot / 2) + u * V) * 2);
+}
+// Weights in shared memory in the units' order: the k-th four of unit u at [k * uph + u], so that neighbouring lanes
+// read neighbouring places (in the features' order four lanes at a time met in the same banks: a quarter of the backward's time).
+template <int V, bool IL, int NT> __device__ __forceinline__ void stage_weights(float4 *dst, const float *w, float off, const RopeArgs &a, int uph) {
+  for (int i = threadIdx.x; i < uph * (V / 2); i += NT) {
+    const int u = i % uph, k = i / uph;
+    const bool halves = u * 2 * V < a.rot && !IL;
+    const int f0 = halves ? u * V : u * 2 * V, gap = halves ? a.rot / 2 : V, f = k < V / 4 ? f0 + 4 * k : f0 + gap + 4 * (k - V / 4);
+    dst[i] = make_float4(w[f] + off, w[f + 1] + off, w[f + 2] + off, w[f + 3] + off);
   }
 }
 struct HeadOf {
@@ -60,80 +201,94 @@ __device__ __forceinline__ HeadOf head_of(const RopeArgs &a, int h) {
 
 }  // namespace
 
-template <typename I, int UN>
-__global__ void __launch_bounds__(NTR, 6) norm_rope_kernel(NormRopeArgs n, int uph, int slots) {
+// The next UN units of a thread are on their way to its own places in shared memory at any time: what is in flight takes no
+// registers, and only the thread itself reads it.
+template <typename I, int UN, bool IL, int UPH, bool PAGED>
+__global__ void __launch_bounds__(NTR, 7) norm_rope_kernel(const __grid_constant__ NormRopeArgs n, int units, int slots) {
   constexpr int V = 16 / sizeof(I);
   const RopeArgs &a = n.r;
-  __shared__ __align__(16) float w[2][MAXD];
+  const int uph = UPH ? UPH : units;
+  __shared__ uint4 ring[UN][2][NTR];
+  __shared__ float4 w[2][(UPH ? UPH * 2 * V : MAXD) / 4];
   pdl_trigger();
   pdl_wait();
-  for (int i = threadIdx.x; i < 2 * a.D; i += NTR) {
-    const int g = i >= a.D, f = i - g * a.D;
-    w[g][f] = n.w[g] ? n.w[g][f] + n.off : 0.f;
-  }
-  __syncthreads();
   const int tpt = uph * slots, tpb = NTR / tpt;
   const int tl = threadIdx.x / tpt, in = threadIdx.x - tl * tpt, hs = in / uph, u = in - hs * uph;
   const long long t = (long long)blockIdx.x * tpb + tl;
-  if (tl >= tpb || t >= a.tokens) return;
-  const bool turned = u * 2 * V < a.rot, halves = turned && !a.interleaved;
-  const int f0 = halves ? u * V : u * 2 * V, f1 = halves ? u * V + a.rot / 2 : u * 2 * V + V;
-  TokPlace pl;
-  float c[V], s[V];
-  bool placed = false;
-  for (int h0 = hs; h0 < a.heads; h0 += slots * UN) {
-    uint4 x0[UN], x1[UN];
-#pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      const int h = h0 + j * slots;
-      if (h < a.heads) {
-        const HeadOf ho = head_of(a, h);
-        const RopeGroup &g = a.grp[ho.group];
-        const I *src = static_cast<const I *>(g.src) + t * g.s_tok + ho.head * g.s_head;
-        x0[j] = *reinterpret_cast<const uint4 *>(src + f0);
-        x1[j] = *reinterpret_cast<const uint4 *>(src + f1);
-      }
+  const bool there = tl < tpb && t < a.tokens;
+  const bool turned = u * 2 * V < a.rot, halves = turned && !IL;
+  const int f0 = halves ? u * V : u * 2 * V, gap = halves ? a.rot / 2 : V;  // the unit's pieces
+  // asking: the thread's heads of one group after another
+  int gi = -1, left = 0, slot = 0;  // heads of group gi still to be asked for; the place of the next one
+  const I *src = nullptr;
+  long long s_step = 0;
+  auto ask = [&] {
+    while (left <= 0 && gi + 1 < a.ngrp) {
+      const RopeGroup &g = a.grp[++gi];
+      left = g.heads - hs;
+      s_step = slots * g.s_head;
+      src = static_cast<const I *>(g.src) + t * g.s_tok + hs * g.s_head + f0;
     }
-    if (!placed) {
-      placed = true;
-      pl = place_of(a, (int)t);
-      if (turned && pl.pos >= 0) read_angles<V>(a, pl.pos, u, c, s);
+    if (left > 0) {
+      copy16(&ring[slot][0][threadIdx.x], src, gap == V);
+      copy16(&ring[slot][1][threadIdx.x], src + gap, gap == V);
+      src += s_step;
+      left -= slots;
     }
-#pragma unroll
-    for (int j = 0; j < UN; ++j) {
-      const int h = h0 + j * slots;
-      if (h >= a.heads) break;
-      const HeadOf ho = head_of(a, h);
-      const RopeGroup &g = a.grp[ho.group];
-      if (g.turn) {  // not a value head
-        float p[V], q[V], wp[V], wq[V];
-        unpack<I>(x0[j], p);
-        unpack<I>(x1[j], q);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += p[i] * p[i] + q[i] * q[i];
-        const float r = rsqrtf(head_sum(sum, uph) / (float)a.D + n.eps);
-        read_weights<V>(w[ho.group], f0, f1, wp, wq);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          p[i] *= r * wp[i];
-          q[i] *= r * wq[i];
-        }
-        if (turned && pl.pos >= 0) turn_unit<V>(p, q, c, s, a.interleaved);
-        x0[j] = repack<I>(p);
-        x1[j] = repack<I>(q);
-      }
-      I *dst = static_cast<I *>(g.dst) + ho.head * g.d_head;
-      if (g.d_page) {
-        if (pl.page < 0) continue;
-        dst += pl.page * g.d_page + pl.off * g.d_tok;
-      } else {
-        dst += t * g.d_tok;
-      }
-      *reinterpret_cast<uint4 *>(dst + f0) = x0[j];
-      *reinterpret_cast<uint4 *>(dst + f1) = x1[j];
-    }
+    cp_async_commit();
+    slot = slot + 1 == UN ? 0 : slot + 1;
+  };
+  if (there) {
+#pragma unroll 1
+    for (int j = 0; j < UN; ++j) ask();
   }
+  stage_weights<V, IL, NTR>(w[0], n.w[0], n.off, a, uph);
+  if (n.w[1]) stage_weights<V, IL, NTR>(w[1], n.w[1], n.off, a, uph);
+  __syncthreads();
+  if (!there) return;
+  const float inv_d = 1.f / (float)a.D;
+  const TokPlace pl = place_of(a, (int)t);
+  const bool turns = turned && pl.pos >= 0;
+  Angles<I, IL> an;
+  if (turns) an.read(angles_at<V>(a, pl.pos, u), 1, false);
+  int at = 0;  // the place of the next unit to be worked on
+  // the thread's heads of one group: `norm` and `page` at compile time, so that nothing is asked in the loop
+  auto walk = [&](const RopeGroup &g, const float4 *weight, auto norm, auto page) {
+    const long long d_step = slots * g.d_head;
+    I *dst = static_cast<I *>(g.dst) + hs * g.d_head + f0;
+    if constexpr (decltype(page)::value) dst += pl.page * g.d_page + pl.off * g.d_tok;
+    else dst += t * g.d_tok;
+#pragma unroll 1
+    for (int h = hs; h < g.heads; h += slots) {
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(UN - 1) : "memory");
+      uint4 x0 = ring[at][0][threadIdx.x], x1 = ring[at][1][threadIdx.x];
+      at = at + 1 == UN ? 0 : at + 1;
+      if constexpr (decltype(norm)::value) {
+        Unit<I> x, wt;
+        x.widen(x0, x1);
+        const float r = rsqrtf(fmaf(head_sum<UPH>(x.dot(x), uph), inv_d, n.eps));
+        wt.read(weight + u, uph);
+        x = x * wt;
+        if (turns) an.turn(x);
+        (x * r).pack(x0, x1);
+      }
+      store_unit(dst, gap, x0, x1);
+      dst += d_step;
+      ask();
+    }
+  };
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  walk(a.grp[0], w[0], yes, no);
+  if constexpr (PAGED) {
+    if (pl.page >= 0) {
+      walk(a.grp[1], w[1], yes, yes);
+      walk(a.grp[2], w[1], no, yes);
+    }
+  } else {
+    if (a.ngrp > 1) walk(a.grp[1], w[1], yes, no);
+  }
+  cp_async_wait_all();
 }
 
 // any head of up to MAXD features: a warp to a head, its lanes over pairs (past rot: over features)
@@ -183,118 +338,129 @@ template <typename I> __global__ void __launch_bounds__(NTR) norm_rope_any_kerne
 }
 
 // Backward: group g's src is x, its dst dx; dy beside them.  The first `split` CTAs take the heads of group 0, the others those
-// of group 1.  part: [gridDim.x][D].  A thread's items are its heads of one token after another; the next item's data, and
-// the next token's angles where it begins one, are asked for before the current item is worked on.
-template <typename I>
-__global__ void __launch_bounds__(NTB, 2) norm_rope_bwd_kernel(NormRopeArgs n, int uph, int slots, int split) {
-  constexpr int V = 16 / sizeof(I);
+// of group 1.  part: [gridDim.x][D].  A thread's items are its heads of one token after another, the next UN of them on their
+// way to shared memory as in the forward, a token's angles with its first head.
+template <typename I, int UN, bool IL, int UPH, int gi>
+__device__ __forceinline__ void norm_rope_bwd_group(const NormRopeArgs &n, int units, int slots, int cta, int ctas) {
+  constexpr int V = 16 / sizeof(I), PV = V / 2;
   const RopeArgs &a = n.r;
-  __shared__ __align__(16) float w[MAXD];
-  __shared__ float sums[NTB][2 * V + 1];
-  const int gi = (int)blockIdx.x >= split, cta = blockIdx.x - (gi ? split : 0), ctas = gi ? gridDim.x - split : split;
-  const RopeGroup g = a.grp[gi];
+  const int uph = UPH ? UPH : units;
+  __shared__ float4 w[(UPH ? UPH * 2 * V : MAXD) / 4];
+  extern __shared__ uint4 ring_mem[];
+  uint4(*ring)[4 + PV][NTB] = reinterpret_cast<uint4(*)[4 + PV][NTB]>(ring_mem);  // [UN]: x, dy, angles
+  static_assert(UN * 4 * 16 >= (2 * V + 1) * 4, "the sums fit the rings");
+  const RopeGroup &g = a.grp[gi];
   pdl_trigger();
   pdl_wait();
-  for (int f = threadIdx.x; f < a.D; f += NTB) w[f] = n.w[gi][f] + n.off;
+  stage_weights<V, IL, NTB>(w, n.w[gi], n.off, a, uph);
   __syncthreads();
   const int tpt = uph * slots, tpb = NTB / tpt;
   const int tl = threadIdx.x / tpt, in = threadIdx.x - tl * tpt, hs = in / uph, u = in - hs * uph;
-  const bool turned = u * 2 * V < a.rot, halves = turned && !a.interleaved;
+  const bool turned = u * 2 * V < a.rot, halves = turned && !IL;
   const int f0 = halves ? u * V : u * 2 * V, f1 = halves ? u * V + a.rot / 2 : u * 2 * V + V;
   const int step = ctas * tpb;
-  float dw[2 * V] = {};
-  struct Item {
-    uint4 x0, x1, d0, d1;
-  };
-  auto read = [&](long long t, int h) {
-    Item i;
-    const I *src = static_cast<const I *>(g.src) + t * g.s_tok + h * g.s_head + f0;
-    const I *dy = static_cast<const I *>(n.dy[gi]) + t * n.dy_tok[gi] + h * n.dy_head[gi] + f0;
-    i.x0 = *reinterpret_cast<const uint4 *>(src);
-    i.x1 = *reinterpret_cast<const uint4 *>(src + f1 - f0);
-    i.d0 = *reinterpret_cast<const uint4 *>(dy);
-    i.d1 = *reinterpret_cast<const uint4 *>(dy + f1 - f0);
-    return i;
-  };
+  const float inv_d = 1.f / (float)a.D;
+  Unit<I> dw = {};
   // of a token: its position, -1 where it does not turn
   auto position = [&](long long t) {
-    const int pos = t < a.tokens ? a.positions[t] : -1;
-    return turned && pos >= 0 && pos < a.rows ? pos : -1;
+    const int pos = turned && t < a.tokens ? a.positions[t] : -1;
+    return pos < a.rows ? pos : -1;
   };
   long long t = (long long)cta * tpb + tl;
-  int h = hs;
-  if (tl < tpb && t < a.tokens && h < g.heads) {
-    Item now = read(t, h);
-    int pos = position(t), pos1 = position(t + step);
-    float c[V], s[V];
-    if (pos >= 0) read_angles<V>(a, pos, u, c, s);  // a.inverse is set
-    for (;;) {
-      long long t1 = t;
-      int h1 = h + slots;
-      if (h1 >= g.heads) {
-        h1 = hs;
-        t1 += step;
-      }
-      const bool more = t1 < a.tokens;
-      Item next = {};
-      float c1[V], s1[V];
-      if (more) {
-        next = read(t1, h1);
-        if (t1 != t && pos1 >= 0) read_angles<V>(a, pos1, u, c1, s1);
-      }
-      float p[V], q[V], y[V], z[V], wp[V], wq[V];
-      unpack<I>(now.x0, p);
-      unpack<I>(now.x1, q);
-      unpack<I>(now.d0, y);
-      unpack<I>(now.d1, z);
-      if (pos >= 0) turn_unit<V>(y, z, c, s, a.interleaved);
-      read_weights<V>(w, f0, f1, wp, wq);
-      float sum = 0.f, dot = 0.f;
+  if (tl < tpb && t < a.tokens && hs < g.heads) {
+    const int gap = f1 - f0;
+    // asking: the thread's heads of one token after another, with the first of a token its angles
+    long long ta = t;
+    int ha = hs, slot = 0, at = 0, pos = position(t), pos1 = position(t + step);
+    unsigned turning = 0;  // which places hold the first head of a token that turns
+    const I *src = static_cast<const I *>(g.src) + t * g.s_tok + hs * g.s_head + f0;
+    const I *dy = static_cast<const I *>(n.dy[gi]) + t * n.dy_tok[gi] + hs * n.dy_head[gi] + f0;
+    auto ask = [&] {
+      if (ta < a.tokens) {
+        copy16(&ring[slot][0][threadIdx.x], src, gap == V);
+        copy16(&ring[slot][1][threadIdx.x], src + gap, gap == V);
+        copy16(&ring[slot][2][threadIdx.x], dy, gap == V);
+        copy16(&ring[slot][3][threadIdx.x], dy + gap, gap == V);
+        if (ha == hs) {
+          turning &= ~(1u << slot);
+          if (pos >= 0) {
+            turning |= 1u << slot;
+            const float4 *cs = angles_at<V>(a, pos, u);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        sum += p[i] * p[i] + q[i] * q[i];
-        dot += p[i] * (y[i] * wp[i]) + q[i] * (z[i] * wq[i]);
-      }
-      sum = head_sum(sum, uph);
-      dot = head_sum(dot, uph);
-      const float r = rsqrtf(sum / (float)a.D + n.eps), m = r * r * (dot / (float)a.D);  // xhat mean(..) = x m
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        dw[i] += y[i] * (p[i] * r);
-        dw[V + i] += z[i] * (q[i] * r);
-        p[i] = r * (y[i] * wp[i] - p[i] * m);
-        q[i] = r * (z[i] * wq[i] - q[i] * m);
-      }
-      I *dst = static_cast<I *>(g.dst) + t * g.d_tok + h * g.d_head + f0;
-      *reinterpret_cast<uint4 *>(dst) = repack<I>(p);
-      *reinterpret_cast<uint4 *>(dst + f1 - f0) = repack<I>(q);
-      if (!more) break;
-      if (t1 != t) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          c[i] = c1[i];
-          s[i] = s1[i];
+            for (int i = 0; i < PV; ++i) copy16(&ring[slot][4 + i][threadIdx.x], cs + i, true);
+          }
+          pos = pos1;
+          pos1 = position(ta + 2ll * step);
         }
-        pos = pos1;
-        pos1 = position(t1 + step);
+        ha += slots;
+        if (ha < g.heads) {
+          src += slots * g.s_head;
+          dy += slots * n.dy_head[gi];
+        } else {
+          src += step * g.s_tok - (ha - slots - hs) * g.s_head;
+          dy += step * n.dy_tok[gi] - (ha - slots - hs) * n.dy_head[gi];
+          ha = hs;
+          ta += step;
+        }
       }
-      t = t1;
-      h = h1;
-      now = next;
+      cp_async_commit();
+      slot = slot + 1 == UN ? 0 : slot + 1;
+    };
+#pragma unroll 1
+    for (int j = 0; j < UN; ++j) ask();
+    I *dst = static_cast<I *>(g.dst) + t * g.d_tok + hs * g.d_head + f0;
+    for (; t < a.tokens; t += step, dst += step * g.d_tok) {
+      Angles<I, IL> an;
+      bool turns = false;
+      I *out = dst;
+#pragma unroll 1
+      for (int h = hs; h < g.heads; h += slots, out += slots * g.d_head) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(UN - 1) : "memory");
+        if (h == hs) {
+          turns = turning >> at & 1;
+          if (turns) an.read(reinterpret_cast<const float4 *>(&ring[at][4][threadIdx.x]), NTB, true);
+        }
+        Unit<I> x, y, wt;
+        x.widen(ring[at][0][threadIdx.x], ring[at][1][threadIdx.x]);
+        y.widen(ring[at][2][threadIdx.x], ring[at][3][threadIdx.x]);
+        at = at + 1 == UN ? 0 : at + 1;
+        if (turns) an.turn(y);
+        wt.read(w + u, uph);
+        wt = wt * y;  // u (w + off)
+        const float sum = head_sum<UPH>(x.dot(x), uph), dot = head_sum<UPH>(x.dot(wt), uph);
+        const float r = rsqrtf(fmaf(sum, inv_d, n.eps));
+        y = y * r;
+#pragma unroll
+        for (int i = 0; i < 2 * PV; ++i) dw.v[i] = fma2(y.v[i], x.v[i], dw.v[i]);
+        uint4 o0, o1;
+        (wt * r).plus(x, -r * r * r * (dot * inv_d)).pack(o0, o1);
+        store_unit(out, gap, o0, o1);
+        ask();
+      }
     }
+    cp_async_wait_all();
   }
+  __syncthreads();  // the rings' memory holds the sums now
+  float(&sums)[NTB][2 * V + 1] = *reinterpret_cast<float(*)[NTB][2 * V + 1]>(ring);
   // the threads of one place in the head, in order
 #pragma unroll
-  for (int i = 0; i < 2 * V; ++i) sums[threadIdx.x][i] = dw[i];
+  for (int i = 0; i < 2 * PV; ++i) upk(dw.v[i], sums[threadIdx.x][2 * i], sums[threadIdx.x][2 * i + 1]);
   __syncthreads();
   for (int f = threadIdx.x; f < a.D; f += NTB) {
     const int fu = f / (2 * V), i = f - fu * 2 * V;
     float z = 0.f;
     for (int k = fu; k < tpb * tpt; k += uph) z += sums[k][i];
-    const bool fh = fu * 2 * V < a.rot && !a.interleaved;
+    const bool fh = fu * 2 * V < a.rot && !IL;
     const int at = fh ? (i < V ? fu * V + i : fu * V + a.rot / 2 + i - V) : f;
     n.part[(long long)blockIdx.x * a.D + at] = z;
   }
+}
+
+template <typename I, int UN, bool IL, int UPH>
+__global__ void __launch_bounds__(NTB, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs n, int units, int slots0, int slots1, int split) {
+  // the group at compile time, so that its strides are constants and no loads in the loop
+  if ((int)blockIdx.x < split) norm_rope_bwd_group<I, UN, IL, UPH, 0>(n, units, slots0, blockIdx.x, split);
+  else norm_rope_bwd_group<I, UN, IL, UPH, 1>(n, units, slots1, blockIdx.x - split, gridDim.x - split);
 }
 
 // a warp to a head, which keeps its sums of dw in shared memory; the CTA's warps add up in order at the end
@@ -391,6 +557,30 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float *part, i
   (g ? dw1 : dw0)[f] = z;
 }
 
+// the kernels' variants by type, pairing and the units of a head (0: any)
+namespace {
+template <typename I, int UN, bool IL, bool PAGED> auto forward_kernel(int uph) {
+  switch (uph) {
+    case 4: return norm_rope_kernel<I, UN, IL, 4, PAGED>;
+    case 8: return norm_rope_kernel<I, UN, IL, 8, PAGED>;
+    case 16: return norm_rope_kernel<I, UN, IL, 16, PAGED>;
+    default: return norm_rope_kernel<I, UN, IL, 0, PAGED>;
+  }
+}
+template <typename I, int UN> auto forward_kernel(const RopeArgs &a, int uph) {
+  if (a.positions) return a.interleaved ? forward_kernel<I, UN, true, false>(uph) : forward_kernel<I, UN, false, false>(uph);
+  return a.interleaved ? forward_kernel<I, UN, true, true>(uph) : forward_kernel<I, UN, false, true>(uph);
+}
+template <typename I, bool IL> auto backward_kernel(int uph) {
+  switch (uph) {
+    case 4: return norm_rope_bwd_kernel<I, UNB, IL, 4>;
+    case 8: return norm_rope_bwd_kernel<I, UNB, IL, 8>;
+    case 16: return norm_rope_bwd_kernel<I, UNB, IL, 16>;
+    default: return norm_rope_bwd_kernel<I, UNB, IL, 0>;
+  }
+}
+}  // namespace
+
 cudaError_t launch_norm_rope(const NormRopeArgs &n, bool bf, bool vec, cudaStream_t st) {
   const RopeArgs &a = n.r;
   if (!vec) {
@@ -404,8 +594,8 @@ cudaError_t launch_norm_rope(const NormRopeArgs &n, bool bf, bool vec, cudaStrea
   while (slots < a.heads && 2 * slots * uph <= NTR && (long long)a.tokens * slots * uph < 152ll * 4 * NTR) slots *= 2;
   const int tpb = NTR / (slots * uph);
   const dim3 grid(((unsigned)a.tokens + tpb - 1) / tpb);
-  return bf ? launch_pdl(norm_rope_kernel<bf16, 3>, grid, dim3(NTR), 0, st, n, uph, slots)
-            : launch_pdl(norm_rope_kernel<float, 2>, grid, dim3(NTR), 0, st, n, uph, slots);
+  auto *k = bf ? forward_kernel<bf16, UNF>(a, uph) : forward_kernel<float, UNF>(a, uph);
+  return launch_pdl(k, grid, dim3(NTR), 0, st, n, uph, slots);
 }
 
 int norm_rope_bwd_ctas(int tokens, int heads, int sms) {
@@ -422,25 +612,27 @@ cudaError_t launch_norm_rope_bwd(const NormRopeArgs &n, bool bf, bool vec, int c
     e = bf ? launch_pdl(norm_rope_bwd_any_kernel<bf16>, dim3(ctas), dim3(NTR), smem, st, n, split)
            : launch_pdl(norm_rope_bwd_any_kernel<float>, dim3(ctas), dim3(NTR), smem, st, n, split);
   } else {
-    // heads that a token's threads begin with: what gives the longest thread the fewest items, the fewest heads among equals
-    // (angles are read once for all heads of a thread)
+    // heads that a token's threads begin with: what gives the longest thread the least to do, a token's angles counted as half
+    // an item
     const int uph = a.D * (bf ? 2 : 4) / 32;
-    int slots = 1;
-    long long best = 0;
-    for (int s = 1; s * uph <= NTB; s *= 2) {
-      const int tpb = NTB / (s * uph);
-      long long items = 0;
-      for (int g = 0; g < a.ngrp; ++g) {
-        const long long step = (long long)(a.ngrp == 1 ? ctas : (g ? ctas - split : split)) * tpb;
-        items = std::max(items, (a.tokens + step - 1) / step * ((a.grp[g].heads + s - 1) / s));
-      }
-      if (!best || items < best) {
-        best = items;
-        slots = s;
+    int slots[2] = {1, 1};
+    for (int g = 0; g < a.ngrp; ++g) {
+      long long best = 0;
+      for (int s = 1; s * uph <= NTB; s *= 2) {
+        const long long step = (long long)(g ? ctas - split : split) * (NTB / (s * uph)), tokens = (a.tokens + step - 1) / step;
+        const long long cost = tokens * (2 * ((a.grp[g].heads + s - 1) / s) + 1);
+        if (!best || cost < best) {
+          best = cost;
+          slots[g] = s;
+        }
       }
     }
-    e = bf ? launch_pdl(norm_rope_bwd_kernel<bf16>, dim3(ctas), dim3(NTB), 0, st, n, uph, slots, split)
-           : launch_pdl(norm_rope_bwd_kernel<float>, dim3(ctas), dim3(NTB), 0, st, n, uph, slots, split);
+    auto *k = bf ? (a.interleaved ? backward_kernel<bf16, true>(uph) : backward_kernel<bf16, false>(uph))
+                 : (a.interleaved ? backward_kernel<float, true>(uph) : backward_kernel<float, false>(uph));
+    const int smem = UNB * (4 + (bf ? 4 : 2)) * 16 * NTB;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(k, dim3(ctas), dim3(NTB), smem, st, n, uph, slots[0], slots[1], split);
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_rope_dw_kernel, dim3((a.D + 31) / 32, a.ngrp), dim3(1024), 0, st, (const float *)n.part, ctas, split, a.D, dw0, dw1);
