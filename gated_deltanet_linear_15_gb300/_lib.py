@@ -28,7 +28,9 @@ BLOCK_EXPORTS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_pag
                  "gdn_rotary_table", "gdn_rotary",
                  "gdn_rotary_append", "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork",
                  "gdn_pages_free", "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size",
-                 "gdn_rmsnorm_bwd")
+                 "gdn_rmsnorm_bwd", "gdn_paged_attn_sinks_fwd", "gdn_prefix_attn_workspace_size", "gdn_prefix_attn_fwd",
+                 "gdn_prefix_attn_status", "gdn_norm_rotary", "gdn_norm_rotary_bwd_workspace_size", "gdn_norm_rotary_bwd",
+                 "gdn_norm_rotary_append", "gdn_scan_states_rows", "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step")
 
 
 class GdnShape(ctypes.Structure):
@@ -140,6 +142,9 @@ def load():
         for name, args in {
                 "gdn_paged_attn_fwd": [P] * 10 + [Z, P],
                 "gdn_paged_attn_status": [P, P, P],
+                "gdn_paged_attn_sinks_fwd": [P, _I] + [P] * 9 + [Z, P],
+                "gdn_prefix_attn_fwd": [P, _I, _I] + [P] * 11 + [Z, P],
+                "gdn_prefix_attn_status": [P, _I, _I, P, P],
                 "gdn_rotary_table": [P, _I, _I, D, P, P],
                 "gdn_rotary": [P] * 8,
                 "gdn_rotary_append": [P] * 12,
@@ -159,7 +164,8 @@ def load():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = ctypes.c_int
         for name, args in {"gdn_paged_attn_workspace_size": [P], "gdn_pages_workspace_size": [P, _I],
-                           "gdn_rmsnorm_bwd_workspace_size": [P], "gdn_norm_rotary_bwd_workspace_size": [P]}.items():
+                           "gdn_rmsnorm_bwd_workspace_size": [P], "gdn_norm_rotary_bwd_workspace_size": [P],
+                           "gdn_prefix_attn_workspace_size": [P, _I, _I]}.items():
             getattr(lib, name).argtypes = args
             getattr(lib, name).restype = Z
         lib.gdn_scan_states_rows.argtypes, lib.gdn_scan_states_rows.restype = [P], _L
@@ -172,7 +178,8 @@ _PY_CALLS = ("gdn_paged_attn_workspace_size", "gdn_paged_attn_fwd", "gdn_paged_a
              "gdn_slots_copy", "gdn_pages_workspace_size", "gdn_pages_extend", "gdn_pages_fork", "gdn_pages_free",
              "gdn_pages_compact", "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd_workspace_size", "gdn_rmsnorm_bwd", "gdn_scan_states_rows",
              "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_rotary", "gdn_norm_rotary_bwd_workspace_size", "gdn_norm_rotary_bwd",
-             "gdn_norm_rotary_append", "gdn_status_string", "gdn_last_error_string")
+             "gdn_norm_rotary_append", "gdn_paged_attn_sinks_fwd", "gdn_prefix_attn_workspace_size", "gdn_prefix_attn_fwd",
+             "gdn_prefix_attn_status", "gdn_status_string", "gdn_last_error_string")
 _py = None
 
 

@@ -1,6 +1,7 @@
 """Operators that a hybrid stack puts next to its gated delta-rule layers: the functions of include/gdn_block.h on tensors.
 
-``paged_attention`` (attention of new tokens over a paged key/value cache), ``rotary_table`` / ``rotary`` /
+``paged_attention`` (attention of new tokens over a paged key/value cache), ``prefix_attention`` (the same of sequences that
+share a prefix), ``rotary_table`` / ``rotary`` /
 ``rotary_embedding`` / ``rotary_append`` (rotary positions, their gradient, and the write of new keys and values into
 the cache), ``extend_pages`` / ``fork_pages`` / ``free_pages`` / ``compact_pages`` / ``copy_slots`` (the cache's
 upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual stream's norm, optionally with an 8-bit
@@ -25,7 +26,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 
-__all__ = ["paged_attention", "paged_attention_status", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding",
+__all__ = ["paged_attention", "paged_attention_status", "prefix_attention", "prefix_attention_status", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding",
            "rotary_append", "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_slots", "rms_norm",
            "rms_norm_bwd", "residual_rms_norm", "NormOutput", "norm_rotary", "norm_rotary_bwd",
            "norm_rotary_embedding", "norm_rotary_append", "gated_scan", "gated_scan_bwd", "gated_scan_step",
@@ -46,23 +47,44 @@ _py = _Extension()
 
 # ------------------------------------------------------------------ paged cache
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, max_q: int = 0, scale: Optional[float] = None,
-                    window: int = 0, return_lse: bool = False, out=None, workspace=None):
+                    window: int = 0, return_lse: bool = False, out=None, workspace=None, sinks: int = 0):
     """Causal attention of new tokens over a paged cache that already holds their keys and values.
 
     q [new tokens, heads, D]; k_cache, v_cache [pages, page_size, kv heads, D] (any strides with contiguous features);
     page_table int32 [sequences, pages] (one row may be expanded over all sequences); kv_lens int32 [sequences], the tokens of each sequence with the new ones;
     cu_q int32 [sequences + 1], where each sequence's new tokens begin in q (None: as many for each).  max_q: the most
     new tokens of a sequence, if known on the host (it only picks the kernel).  window > 0: a query sees that many
-    keys.  Returns o like q, or (o, lse) with lse fp32 [new tokens, heads]; a query without keys has o = 0 and
+    keys, and with sinks > 0 the sequence's first `sinks` keys too.  Returns o like q, or (o, lse) with lse fp32 [new tokens, heads]; a query without keys has o = 0 and
     lse = -inf.  workspace: a tensor to use as scratch memory (contiguous, 32-byte
     aligned, refused when it is too small).  Decoding is the case of one new token per sequence."""
-    return _py.paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q, scale, window, return_lse, out, workspace)
+    return _py.paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q, scale, window, return_lse, out, workspace,
+                               sinks)
 
 
 def paged_attention_status(q, k_cache, v_cache, page_table, kv_lens, workspace, cu_q=None, max_q: int = 0) -> int:
     """Status word of the last ``paged_attention`` call with these arguments and this workspace, which that call must have
     been given (0: clean; see gdn_paged_attn_status).  Synchronises the stream."""
     return _py.paged_attention_status(q, k_cache, v_cache, page_table, kv_lens, workspace, cu_q, max_q)
+
+
+def prefix_attention(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_seqs=None, cu_q=None, max_q: int = 0,
+                     max_group: int = 0, scale: Optional[float] = None, return_lse: bool = False, out=None, workspace=None):
+    """``paged_attention`` of groups of sequences that share a prefix, whose keys are read once for each group.
+
+    prefix_lens int32 [groups]: tokens that all sequences of a group have in common; their rows of page_table name the same
+    pages there, as after ``fork_pages``.  A prefix longer than what some sequence had cached before its new tokens is cut to
+    that.  cu_seqs int32 [groups + 1]: where each group's sequences begin (None: as many for each; sequences outside
+    share nothing).  max_group: the most new tokens of a group, if known on the host (it only picks the kernel).  The rest as in
+    ``paged_attention``, without a window."""
+    return _py.prefix_attention(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_seqs, cu_q, max_q, max_group, scale,
+                                return_lse, out, workspace)
+
+
+def prefix_attention_status(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, workspace, cu_seqs=None, cu_q=None,
+                            max_q: int = 0, max_group: int = 0) -> int:
+    """``paged_attention_status`` of the last ``prefix_attention`` call with these arguments and this workspace."""
+    return _py.prefix_attention_status(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, workspace, cu_seqs, cu_q, max_q,
+                                       max_group)
 
 
 # ------------------------------------------------------------------ rotary positions

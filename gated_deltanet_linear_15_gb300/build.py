@@ -23,7 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
 SOURCES = ["api.cu", "plan.cu", "fwd.cu", "fwd_prep_tc.cu", "fwd_tc.cu", "bwd.cu", "bwd_chain_tc.cu", "bwd_local_tc.cu",
-           "recurrent.cu", "block_api.cu", "attn_rows.cu", "attn_chunk_tc.cu",
+           "recurrent.cu", "block_api.cu", "attn_rows.cu", "attn_rows_sinks.cu", "attn_rows_head.cu",
+           "attn_rows_tail.cu", "attn_chunk_tc.cu", "attn_prefix.cu",
            "rope.cu", "norm_rope.cu", "pages.cu", "rmsnorm.cu", "scan.cu"]
 PY_SOURCE = os.path.join(CSRC, "block_py.cpp")
 # tied to the C++ ABI of one torch and one Python, so it carries both in its name

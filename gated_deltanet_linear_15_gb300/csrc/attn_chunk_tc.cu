@@ -130,11 +130,11 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
   return v;
 }
 // cursor_next of a cursor in shared memory: lane 0 moves it for the warp
-__device__ __forceinline__ bool cursor_advance(const PagedArgs &a, Cursor &shared, int n) {
+template <int PART> __device__ __forceinline__ bool cursor_advance(const PagedArgs &a, Cursor &shared, int n) {
   bool more = false;
   if ((threadIdx.x & 31) == 0) {
     Cursor c = shared;
-    more = cursor_next<MT, BN>(a, c, n);
+    more = cursor_next<MT, BN, PART>(a, c, n);
     shared = c;
   }
   __syncwarp();
@@ -190,7 +190,7 @@ __device__ __forceinline__ void turn_give(int x) { asm volatile("bar.arrive %0, 
 
 }  // namespace
 
-template <int D>
+template <int D, int PART>
 __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk,
                                                              const __grid_constant__ CUtensorMap tv, uint32_t neg) {
   using C = Cfg<D>;
@@ -237,9 +237,9 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   pdl_trigger();
   pdl_wait();
   SeqInfo *seqs = reinterpret_cast<SeqInfo *>(ring);  // the search uses the ring's memory
-  cursor_prepare<NTHR>(a, seqs);
+  cursor_prepare<NTHR, PART>(a, seqs);
   if (warp == 0) {
-    const int found = cursor_begin_one_warp<MT, BN>(a, cursors[0], seqs);
+    const int found = cursor_begin_one_warp<MT, BN, PART>(a, cursors[0], seqs);
     if (lane == 0) has_work = found;
   }
   fence_async_smem();
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     __syncthreads();                             // everyone has read it
     if (tid < SOFT) {
       Cursor c;
-      const bool some = cursor_begin_any<SOFT, MT, BN>(a, c, *reinterpret_cast<PlanSmem<SOFT> *>(ring));
+      const bool some = cursor_begin_any<SOFT, MT, BN, PART>(a, c, *reinterpret_cast<PlanSmem<SOFT> *>(ring));
       if (tid == 0) {
         cursors[0] = c;
         has_work = some;
@@ -280,12 +280,14 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
       int b0, b1;
       bool first, last;
       const int n = cursor_piece(cur, b0, b1, first, last);
-      const int *trow = a.table + (long long)cur.n * a.table_stride;
+      const int *trow = table_row<PART>(a, cur);
       const int lo = cur.w.lo, hi = cur.w.hi, kvh = cur.h;
-      int t = (cur.w.blk0 + b0) * BN + piece * box;
+      const int nsink = cur.w.nsink, gap = (cur.w.blk0 - nsink) * BN;  // SINKS: where the blocks behind those of the sinks lie
+      int t = block_begin<BN, PART>(cur.w, b0) + piece * box;
       for (int b = b0; b < b1 && ok; ++b, t += BN) {
+        if (PART == SINKS && b == nsink && b > b0) t += gap;
         int page = a.num_pages;  // zeros
-        if (piece < pieces && t < hi && t + box > lo) {
+        if (piece < pieces && t < hi && (t + box > lo || (PART == SINKS && t < a.sinks))) {
           const int pg = trow[t >> a.log2P];
           if ((unsigned)pg < (unsigned)a.num_pages) page = pg;
         }
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         }
       }
       __syncwarp();
-      more = cursor_advance(a, cur, n);
+      more = cursor_advance<PART>(a, cur, n);
     }
     if (lane == 0) bars.stages = make_uint3(st, ph, min(issued, (uint32_t)C::STAGES));
   } else if (warp != 11) {
@@ -362,8 +364,15 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         __syncwarp();
         if (both) turn_give(x ^ 1);
         next();
-        int r_lo = cur.w.lo - (cur.w.blk0 + b0) * BN, r_hi = cur.w.hi - (cur.w.blk0 + b0) * BN;
-        for (int b = b0; b < b1; ++b, r_lo -= BN, r_hi -= BN) {
+        const int t_first = block_begin<BN, PART>(cur.w, b0);
+        int r_lo = cur.w.lo - t_first, r_hi = cur.w.hi - t_first, r_sink = PART == SINKS ? a.sinks - t_first : 0;
+        for (int b = b0; b < b1; ++b, r_lo -= BN, r_hi -= BN, r_sink -= BN) {
+          if (PART == SINKS && b == cur.w.nsink && b > b0) {
+            const int gap = (cur.w.blk0 - cur.w.nsink) * BN;
+            r_lo -= gap;
+            r_hi -= gap;
+            r_sink -= gap;
+          }
           // values of the block and keys of the next, while the softmax works
           const uint32_t vst = st;
           ok = ok && wait(&bars.full[vst], ph, dead);
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
             uint4 *v = reinterpret_cast<uint4 *>(ring + vst * C::STAGE);
             for (int i = lane; i < BN * 8 * C::HALVES; i += 32) {
               const int r = (i >> 3) & (BN - 1);
-              if (r < r_lo || r >= r_hi) v[i] = make_uint4(0, 0, 0, 0);
+              if (r >= r_hi || (r < r_lo && !(PART == SINKS && r < r_sink))) v[i] = make_uint4(0, 0, 0, 0);
             }
             fence_async_smem();
             __syncwarp();
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         }
       }
       __syncwarp();
-      more = cursor_advance(a, cur, n);
+      more = cursor_advance<PART>(a, cur, n);
     }
     if (x == 0) turn_wait(0);  // the turn that was given last
   }
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
       // the next piece, found while this one's first scores are on their way
       if (lane == 0) ahead[warp] = cur;
       __syncwarp();
-      const bool more_next = cursor_advance(a, ahead[warp], n);
+      const bool more_next = cursor_advance<PART>(a, ahead[warp], n);
       auto next_q = [&] { return more_next && load_q(ahead[warp]); };
       if (rows <= 0) q_arrived(next_q());
       if (rows > 0) {
@@ -463,14 +472,15 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
         if (live) {
           int tok, head;
           row_place(a, cur, MT, row, tok, head);
-          pos = cur.s.kv - cur.s.qlen + tok - cur.s.qbeg;
+          pos = seen_from<PART>(cur.s, cur.s.kv - cur.s.qlen + tok - cur.s.qbeg);
         }
         float m = live ? -INFINITY : 0.f, l = 0.f;
         bool pending = false;
         if (b0 >= b1) pending = next_q();
         if (b0 < b1) {
-          int t0 = (cur.w.blk0 + b0) * BN;
+          int t0 = block_begin<BN, PART>(cur.w, b0);
           for (int b = b0; b < b1; ++b, t0 += BN) {
+            if (PART == SINKS && b == cur.w.nsink && b > b0) t0 += (cur.w.blk0 - cur.w.nsink) * BN;
             ok = ok && wait(&bars.s_full[x], ps, dead);
             ps ^= 1;
             fence_after();
@@ -486,11 +496,21 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
 #pragma unroll
               for (int i = 0; i < BN / 32; ++i) tmem_ld32_nw(ts + 32 * i, s + 32 * i);
               tmem_wait_ld();
-              if (__any_sync(0xffffffffu, t0 + BN - 1 > pos || (a.window && t0 <= pos - a.window))) {
-                const int hi = pos - t0, lo = a.window ? pos - a.window - t0 : -1;
+              if constexpr (PART == SINKS) {
+                if (__any_sync(0xffffffffu, t0 + BN - 1 > pos || t0 <= pos - a.window)) {
+                  const int hi = pos - t0, lo = pos - a.window - t0, sink = a.sinks - t0;
 #pragma unroll
-                for (int i = 0; i < BN; ++i)
-                  if (i > hi || i <= lo) s[i] = 0xff800000u;
+                  for (int i = 0; i < BN; ++i)
+                    if (i > hi || (i <= lo && i >= sink)) s[i] = 0xff800000u;
+                }
+              } else {
+                const int out = PART == TAIL ? cur.w.lo - 1 : (PART == ALL && a.window ? pos - a.window : -1);  // the last key before those seen
+                if (__any_sync(0xffffffffu, t0 + BN - 1 > pos || t0 <= out)) {
+                  const int hi = pos - t0, lo = out - t0;
+#pragma unroll
+                  for (int i = 0; i < BN; ++i)
+                    if (i > hi || i <= lo) s[i] = 0xff800000u;
+                }
               }
               if (raise) {
                 float mx[4];
@@ -552,6 +572,8 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
           row_place(a, cur, MT, live ? row : 0, tok, head);
           const int slot = first ? 1 : 0;
           float *rec = a.part + ((long long)cta * 2 + slot) * record_floats(MT, D);
+          constexpr bool RAW = PART == HEAD || PART == TAIL;  // sums go out as they are
+          const long long raw_at = (long long)tok * a.Hq + head;
           const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
           const unsigned long long op = reinterpret_cast<unsigned long long>(static_cast<bf16 *>(a.o) + tok * a.o_tok + head * a.o_head);
           // 16 rows by 64 features at a time.  The lane holds two neighbouring features of rows g and g + 8 in each of
@@ -574,7 +596,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
               for (int e = 0; e < 2; ++e) {
                 const int sub = 16 * hb + 8 * e + g;  // the row in the warp's 32
                 const bool there = (warp & 3) * 32 + sub < rows;
-                if (whole) {
+                if (!RAW && whole) {
                   const float f = __shfl_sync(0xffffffffu, inv, sub);
                   const unsigned long long at = __shfl_sync(0xffffffffu, op, sub) + 2 * (64 * cb + 16 * qd);
                   uint32_t t[4][2], w[8];
@@ -593,6 +615,11 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
                     }
                   }
                 } else {
+                  float *row = rec + (size_t)(x * 128 + (warp & 3) * 32 + sub) * D;
+                  if constexpr (RAW) {
+                    const long long at = __shfl_sync(0xffffffffu, raw_at, sub);
+                    if (whole) row = a.sums + at * D;
+                  }
 #pragma unroll
                   for (int hf = 0; hf < 2; ++hf) {
                     uint32_t t[4][2], w[8];
@@ -604,14 +631,17 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
                     quad_transpose(t, qd);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) w[i] = t[i >> 1][i & 1];
-                    if (there) st_global_32b(rec + (size_t)(x * 128 + (warp & 3) * 32 + sub) * D + 64 * cb + 32 * hf + 8 * qd, w);
+                    if (there) st_global_32b(row + 64 * cb + 32 * hf + 8 * qd, w);
                   }
                 }
               }
             }
           }
           if (live) {
-            if (whole) {
+            if (RAW && first) note_row(a, whole, tok, head, row);
+            if (RAW && whole) {
+              a.mass[raw_at] = make_float2(m, l);
+            } else if (whole) {
               if (a.lse) a.lse[(long long)tok * a.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else {
               rec[(size_t)MT * D + row] = m;
@@ -660,17 +690,30 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
   if (warp == 8) tmem_dealloc(tmem, TM_COLS);
 }
 
-cudaError_t launch_attn_chunk_tc(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int D, int ctas, cudaStream_t st) {
+namespace {
+template <int PART>
+cudaError_t launch_attn_chunk_part(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int D, int ctas, cudaStream_t st) {
   PagedArgs b = a;
   // the sign of the scale goes into the product, so that the largest score is the largest logit; a scale of zero
   // becomes one that leaves every weight at 1 and still sends masked scores to -inf
   const uint32_t neg = a.scale_log2 < 0.f ? 1 : 0;
   b.scale_log2 = fmaxf(fabsf(a.scale_log2), 1e-37f);
-  auto *k = D == 128 ? attn_chunk_kernel<128> : attn_chunk_kernel<64>;
+  auto *k = D == 128 ? attn_chunk_kernel<128, PART> : attn_chunk_kernel<64, PART>;
   const int smem = D == 128 ? Cfg<128>::SMEM : Cfg<64>::SMEM;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(ctas), dim3(NTHR), (size_t)smem, st, b, tk, tv, neg);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_chunk_tc(const PagedArgs &a, Part part, const CUtensorMap &tk, const CUtensorMap &tv, int D, int ctas, cudaStream_t st) {
+  switch (part) {
+    case ALL: return launch_attn_chunk_part<ALL>(a, tk, tv, D, ctas, st);
+    case SINKS: return launch_attn_chunk_part<SINKS>(a, tk, tv, D, ctas, st);
+    case HEAD: return launch_attn_chunk_part<HEAD>(a, tk, tv, D, ctas, st);
+    default: return launch_attn_chunk_part<TAIL>(a, tk, tv, D, ctas, st);
+  }
 }
 
 }  // namespace gdn

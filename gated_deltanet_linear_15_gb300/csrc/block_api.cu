@@ -194,6 +194,152 @@ int check_row(int64_t row, const gdn_norm_shape *s, const char *name) {
 }
 bool vec_ok(const void *p, int64_t row, int v) { return !p || (aligned16(p) && row % v == 0); }
 
+// ------------------------------------------------------------------ attention
+// the arguments of every attention
+int check_attn_args(const gdn_paged_shape *s, const void *q, const void *k, const void *v, const int32_t *table, const int32_t *cu_q,
+                    const int32_t *kv_lens, const void *o) {
+  if (!cu_q && s->total_q % s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "without cu_q, total_q must be a multiple of num_seqs");
+  TRY(need_aligned(q, "q"));
+  TRY(need_aligned(k, "k_cache"));
+  TRY(need_aligned(v, "v_cache"));
+  TRY(need_aligned(o, "o"));
+  if (s->max_pages > 0) TRY(need_ptr(table, "page_table"));
+  return need_ptr(kv_lens, "kv_lens");
+}
+int check_attn_memory(const void *q, const void *k, const void *v, const void *o, const void *ws, size_t ws_bytes, size_t need) {
+  if (!ws || ws_bytes < need) return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : (size_t)0);
+  // a cut item's record leaves in 32-byte stores (attn_chunk_tc.cu); every part of the workspace is a multiple of that
+  if (reinterpret_cast<uintptr_t>(ws) & 31) return fail(GDN_ERR_INVALID_ARG, "workspace is not 32-byte aligned");
+  // a CTA reads queries and cache rows after another wrote its outputs
+  if (o == q || o == k || o == v) return fail(GDN_ERR_INVALID_ARG, "o is one of the inputs");
+  return GDN_OK;
+}
+PagedArgs attn_args(const gdn_paged_shape *s, const void *q, const void *k, const void *v, const int32_t *table, const int32_t *cu_q,
+                    const int32_t *kv_lens, void *o, float *lse) {
+  PagedArgs a = {};
+  a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
+  a.table = table; a.cu_q = cu_q; a.kv_lens = kv_lens;
+  a.table_stride = s->table_stride;
+  a.q_tok = s->q_tok; a.q_head = s->q_head;
+  a.k_page = s->k_page; a.k_tok = s->k_tok; a.k_head = s->k_head;
+  a.v_page = s->v_page; a.v_tok = s->v_tok; a.v_head = s->v_head;
+  a.o_tok = s->o_tok; a.o_head = s->o_head;
+  a.N = s->num_seqs; a.total_q = s->total_q; a.per_seq = cu_q ? 0 : s->total_q / s->num_seqs;
+  a.Hq = s->num_heads; a.Hkv = s->num_kv_heads; a.G = s->num_heads / s->num_kv_heads;
+  a.log2P = ilog2(s->page_size);
+  a.num_pages = s->num_pages; a.max_pages = s->max_pages;
+  // a window as long as a table row limits nothing; what stays is far from where differences of positions would wrap
+  a.window = s->window < (long long)s->max_pages * s->page_size ? s->window : 0;
+  a.scale_log2 = s->scale * 1.4426950408889634f;
+  a.expire = s->reserved != 0;
+  return a;
+}
+// a kernel's part of the workspace, from `ws` on
+void attn_scratch(PagedArgs &a, const AttnPlan &p, void *ws) {
+  a.hdr = static_cast<int4 *>(ws);
+  a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.off_part);
+  a.status = reinterpret_cast<int *>(static_cast<char *>(ws) + p.off_status);
+}
+int run_attn(const gdn_paged_shape *s, const AttnPlan &p, const PagedArgs &a, Part part, Stream st) {
+  const bool bf = s->dtype == GDN_BF16;
+  CUtensorMap tk, tv;
+  const int slots = p.tc ? std::min(s->page_size, 128) : attn_rows_box(bf, p.MT, s->page_size);
+  TRY(cache_map(&tk, a.k, s, s->k_page, s->k_tok, s->k_head, slots));
+  TRY(cache_map(&tv, a.v, s, s->v_page, s->v_tok, s->v_head, slots));
+  if (p.tc) {
+    PROF("attn_chunk");
+    CK(launch_attn_chunk_tc(a, part, tk, tv, s->head_dim, p.ctas, st));
+  } else {
+    PROF("attn_rows");
+    CK(launch_attn_rows(a, part, tk, tv, bf, s->head_dim, p.MT, p.ctas, st));
+  }
+  return GDN_OK;
+}
+int run_attn_join(const gdn_paged_shape *s, const AttnPlan &p, const PagedArgs &a, Stream st) {
+  // tiles: every sequence has at most one that is not full
+  const long long tiles = s->num_seqs + (long long)s->total_q * a.G / p.MT;
+  PROF("attn_join");
+  CK(launch_attn_join(a, s->dtype == GDN_BF16, s->head_dim, p.MT, p.ctas, (int)std::min(tiles * s->num_kv_heads, (long long)p.ctas), st));
+  return GDN_OK;
+}
+int paged_attn(const gdn_paged_shape *s, int sinks, const void *q, const void *k, const void *v, const int32_t *table, const int32_t *cu_q,
+               const int32_t *kv_lens, void *o, float *lse, void *ws, size_t ws_bytes, Stream st) {
+  TRY(check_attn_args(s, q, k, v, table, cu_q, kv_lens, o));
+  const AttnPlan p = attn_plan(s);
+  TRY(check_attn_memory(q, k, v, o, ws, ws_bytes, p.total));
+  PagedArgs a = attn_args(s, q, k, v, table, cu_q, kv_lens, o, lse);
+  // sinks beyond the table's room stand for all of it; without a window they add nothing
+  a.sinks = (int)std::min((long long)sinks, (long long)s->max_pages * s->page_size);
+  attn_scratch(a, p, ws);
+  TRY(run_attn(s, p, a, a.window && a.sinks ? SINKS : ALL, st));
+  return run_attn_join(s, p, a, st);
+}
+// the words of the CTAs of one kernel
+int attn_status_words(const AttnPlan &p, const void *ws) {
+  try {
+    std::vector<int> st(p.ctas);
+    if (cudaMemcpy(st.data(), static_cast<const char *>(ws) + p.off_status, st.size() * sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return -1;
+    int word = 0;
+    for (int x : st) word |= x ? 4 : 0;
+    return word;
+  } catch (...) {
+    return -1;
+  }
+}
+
+// ------------------------------------------------------------------ attention behind a shared prefix
+#ifndef PREFIX_MIN
+#define PREFIX_MIN 0
+#endif
+constexpr double PREFIX_MIN_BYTES = PREFIX_MIN;
+struct PrefixLayout {
+  bool split;  // in two parts; otherwise as sequences that share nothing
+  gdn_paged_shape groups;  // the batch of heads
+  AttnPlan head, tail;
+  size_t off_head, off_tail, off_info, off_sums[2], off_mass[2], off_loc[2], total;
+};
+int check_prefix(const gdn_paged_shape *s, int groups, int max_group) {
+  TRY(check_attn(s));
+  if (s->window) return fail(GDN_ERR_UNSUPPORTED, "a window and a shared prefix do not go together");
+  if (groups < 0 || (groups == 0 && s->num_seqs > 0) || groups > s->num_seqs)
+    return fail(GDN_ERR_INVALID_ARG, "need 1 <= groups <= num_seqs (got %d, %d)", groups, s->num_seqs);
+  if (max_group < 0) return fail(GDN_ERR_INVALID_ARG, "max_group must be >= 0");
+  return GDN_OK;
+}
+PrefixLayout prefix_layout(const gdn_paged_shape *s, int groups, int max_group) {
+  PrefixLayout l = {};
+  l.tail = attn_plan(s);
+  // bytes that sharing can save at most, as far as the host knows: the sequences of a group read what its first one reads
+  const double saved = (double)(s->num_seqs - groups) * s->max_pages * s->page_size * s->num_kv_heads * s->head_dim * 2 * (double)esize(s->dtype);
+  l.split = saved > PREFIX_MIN_BYTES;
+  if (!l.split) {
+    l.total = l.tail.total;
+    return l;
+  }
+  l.groups = *s;
+  l.groups.num_seqs = groups;
+  l.groups.max_q = max_group;
+  l.head = attn_plan(&l.groups);
+  const size_t rows = (size_t)s->total_q * s->num_heads;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t x = at;
+    at += up256(bytes);
+    return x;
+  };
+  l.off_tail = take(l.tail.total);
+  l.off_head = take(l.head.total);
+  l.off_info = take(((size_t)groups + s->num_seqs) * sizeof(int4));
+  for (int i = 0; i < 2; ++i) {
+    l.off_sums[i] = take(rows * s->head_dim * sizeof(float));
+    l.off_mass[i] = take(rows * sizeof(float2));
+    l.off_loc[i] = take(rows * sizeof(int2));
+  }
+  l.total = at;
+  return l;
+}
+
 // ------------------------------------------------------------------ rotary positions
 int check_rotary(const gdn_rotary_shape *s) {
   if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
@@ -369,75 +515,80 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *s, const void *q, const void *k, c
                        gdn_stream_t stream) {
   TRY(check_attn(s));
   if (s->total_q == 0 || s->num_seqs == 0) return GDN_OK;
-  if (!cu_q && s->total_q % s->num_seqs) return fail(GDN_ERR_INVALID_ARG, "without cu_q, total_q must be a multiple of num_seqs");
-  TRY(need_aligned(q, "q"));
-  TRY(need_aligned(k, "k_cache"));
-  TRY(need_aligned(v, "v_cache"));
-  TRY(need_aligned(o, "o"));
-  if (s->max_pages > 0) TRY(need_ptr(table, "page_table"));
-  TRY(need_ptr(kv_lens, "kv_lens"));
-  const AttnPlan p = attn_plan(s);
-  if (!ws || ws_bytes < p.total) return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.total, ws ? ws_bytes : (size_t)0);
-  // a cut item's record leaves in 32-byte stores (attn_chunk_tc.cu); every part of the workspace is a multiple of that
-  if (reinterpret_cast<uintptr_t>(ws) & 31) return fail(GDN_ERR_INVALID_ARG, "workspace is not 32-byte aligned");
-  // a CTA reads queries and cache rows after another wrote its outputs
-  if (o == q || o == k || o == v) return fail(GDN_ERR_INVALID_ARG, "o is one of the inputs");
+  return paged_attn(s, 0, q, k, v, table, cu_q, kv_lens, o, lse, ws, ws_bytes, (Stream)stream);
+}
+
+int gdn_paged_attn_sinks_fwd(const gdn_paged_shape *s, int sinks, const void *q, const void *k, const void *v, const int32_t *table,
+                             const int32_t *cu_q, const int32_t *kv_lens, void *o, float *lse, void *ws, size_t ws_bytes,
+                             gdn_stream_t stream) {
+  TRY(check_attn(s));
+  if (sinks < 0) return fail(GDN_ERR_INVALID_ARG, "sinks must be >= 0");
+  if (s->total_q == 0 || s->num_seqs == 0) return GDN_OK;
+  return paged_attn(s, sinks, q, k, v, table, cu_q, kv_lens, o, lse, ws, ws_bytes, (Stream)stream);
+}
+
+size_t gdn_prefix_attn_workspace_size(const gdn_paged_shape *s, int groups, int max_group) {
+  if (check_prefix(s, groups, max_group)) return 0;
+  return prefix_layout(s, groups, max_group).total;
+}
+
+int gdn_prefix_attn_fwd(const gdn_paged_shape *s, int groups, int max_group, const void *q, const void *k, const void *v,
+                        const int32_t *table, const int32_t *cu_q, const int32_t *kv_lens, const int32_t *cu_seqs,
+                        const int32_t *prefix_lens, void *o, float *lse, void *ws, size_t ws_bytes, gdn_stream_t stream) {
+  TRY(check_prefix(s, groups, max_group));
+  if (s->total_q == 0 || s->num_seqs == 0) return GDN_OK;
+  if (!cu_seqs && s->num_seqs % groups) return fail(GDN_ERR_INVALID_ARG, "without cu_seqs, num_seqs must be a multiple of groups");
+  TRY(check_attn_args(s, q, k, v, table, cu_q, kv_lens, o));
+  TRY(need_ptr(prefix_lens, "prefix_lens"));
+  const PrefixLayout l = prefix_layout(s, groups, max_group);
+  TRY(check_attn_memory(q, k, v, o, ws, ws_bytes, l.total));
   const Stream st = (Stream)stream;
-  PagedArgs a;
-  a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
-  a.table = table; a.cu_q = cu_q; a.kv_lens = kv_lens;
-  a.table_stride = s->table_stride;
-  a.q_tok = s->q_tok; a.q_head = s->q_head;
-  a.k_page = s->k_page; a.k_tok = s->k_tok; a.k_head = s->k_head;
-  a.v_page = s->v_page; a.v_tok = s->v_tok; a.v_head = s->v_head;
-  a.o_tok = s->o_tok; a.o_head = s->o_head;
-  a.N = s->num_seqs; a.total_q = s->total_q; a.per_seq = cu_q ? 0 : s->total_q / s->num_seqs;
-  a.Hq = s->num_heads; a.Hkv = s->num_kv_heads; a.G = s->num_heads / s->num_kv_heads;
-  a.log2P = ilog2(s->page_size);
-  a.num_pages = s->num_pages; a.max_pages = s->max_pages;
-  // a window as long as a table row limits nothing; what stays is far from where differences of positions would wrap
-  a.window = s->window < (long long)s->max_pages * s->page_size ? s->window : 0;
-  a.scale_log2 = s->scale * 1.4426950408889634f;
-  a.expire = s->reserved != 0;
-  a.hdr = static_cast<int4 *>(ws);
-  a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + p.off_part);
-  a.status = reinterpret_cast<int *>(static_cast<char *>(ws) + p.off_status);
-  const bool bf = s->dtype == GDN_BF16;
-  CUtensorMap tk, tv;
-  const int slots = p.tc ? std::min(s->page_size, 128) : attn_rows_box(bf, p.MT, s->page_size);
-  TRY(cache_map(&tk, k, s, s->k_page, s->k_tok, s->k_head, slots));
-  TRY(cache_map(&tv, v, s, s->v_page, s->v_tok, s->v_head, slots));
-  if (p.tc) {
-    PROF("attn_chunk");
-    CK(launch_attn_chunk_tc(a, tk, tv, s->head_dim, p.ctas, st));
-  } else {
-    PROF("attn_rows");
-    CK(launch_attn_rows(a, tk, tv, bf, s->head_dim, p.MT, p.ctas, st));
+  if (!l.split) return paged_attn(s, 0, q, k, v, table, cu_q, kv_lens, o, lse, ws, ws_bytes, st);
+  char *w = static_cast<char *>(ws);
+  PagedArgs tail = attn_args(s, q, k, v, table, cu_q, kv_lens, o, lse), head = tail;
+  head.N = groups;
+  attn_scratch(head, l.head, w + l.off_head);
+  attn_scratch(tail, l.tail, w + l.off_tail);
+  PrefixPlan plan;
+  plan.cu_seqs = cu_seqs;
+  plan.prefix_lens = prefix_lens;
+  plan.groups = groups;
+  plan.head = reinterpret_cast<int4 *>(w + l.off_info);
+  plan.tail = plan.head + groups;
+  head.info = plan.head;
+  tail.info = plan.tail;
+  PagedArgs *parts[2] = {&head, &tail};
+  for (int i = 0; i < 2; ++i) {
+    parts[i]->sums = reinterpret_cast<float *>(w + l.off_sums[i]);
+    parts[i]->mass = reinterpret_cast<float2 *>(w + l.off_mass[i]);
+    parts[i]->loc = reinterpret_cast<int2 *>(w + l.off_loc[i]);
   }
   {
-    // tiles: every sequence has at most one that is not full
-    const long long tiles = s->num_seqs + (long long)s->total_q * a.G / p.MT;
-    PROF("attn_join");
-    CK(launch_attn_join(a, bf, s->head_dim, p.MT, p.ctas, (int)std::min(tiles * s->num_kv_heads, (long long)p.ctas), st));
+    PROF("prefix_plan");
+    CK(launch_prefix_plan(tail, plan, head.loc, tail.loc, st));
   }
+  TRY(run_attn(&l.groups, l.head, head, HEAD, st));
+  TRY(run_attn(s, l.tail, tail, TAIL, st));
+  PROF("prefix_join");
+  CK(launch_prefix_join(head, tail, s->dtype == GDN_BF16, s->head_dim, l.head.MT, l.tail.MT, l.head.ctas, l.tail.ctas, st));
   return GDN_OK;
+}
+
+int gdn_prefix_attn_status(const gdn_paged_shape *s, int groups, int max_group, const void *ws, gdn_stream_t stream) {
+  if (check_prefix(s, groups, max_group) || need_ptr(ws, "workspace")) return -1;
+  const PrefixLayout l = prefix_layout(s, groups, max_group);
+  if (cudaStreamSynchronize((Stream)stream) != cudaSuccess) return -1;
+  if (s->total_q == 0 || s->num_seqs == 0) return 0;
+  const int tail = attn_status_words(l.tail, static_cast<const char *>(ws) + l.off_tail);
+  const int head = l.split ? attn_status_words(l.head, static_cast<const char *>(ws) + l.off_head) : 0;
+  return tail < 0 || head < 0 ? -1 : tail | head;
 }
 
 int gdn_paged_attn_status(const gdn_paged_shape *s, const void *ws, gdn_stream_t stream) {
   if (check_attn(s) || need_ptr(ws, "workspace")) return -1;
-  const AttnPlan p = attn_plan(s);
   if (cudaStreamSynchronize((Stream)stream) != cudaSuccess) return -1;
   if (s->total_q == 0 || s->num_seqs == 0) return 0;
-  int word = 0;
-  try {
-    std::vector<int> st(p.ctas);
-    if (cudaMemcpy(st.data(), static_cast<const char *>(ws) + p.off_status, st.size() * sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
-      return -1;
-    for (int x : st) word |= x ? 4 : 0;
-  } catch (...) {
-    return -1;
-  }
-  return word;
+  return attn_status_words(attn_plan(s), ws);
 }
 
 int gdn_rotary_table(const double *freq, int pairs, int rows, double amplitude, float *table, gdn_stream_t stream) {

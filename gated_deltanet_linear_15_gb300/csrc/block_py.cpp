@@ -46,6 +46,10 @@ struct Api {
   decltype(&gdn_norm_rotary_bwd_workspace_size) norm_rotary_bwd_workspace_size;
   decltype(&gdn_norm_rotary_bwd) norm_rotary_bwd;
   decltype(&gdn_norm_rotary_append) norm_rotary_append;
+  decltype(&gdn_paged_attn_sinks_fwd) paged_attn_sinks_fwd;
+  decltype(&gdn_prefix_attn_workspace_size) prefix_attn_workspace_size;
+  decltype(&gdn_prefix_attn_fwd) prefix_attn_fwd;
+  decltype(&gdn_prefix_attn_status) prefix_attn_status;
   decltype(&gdn_status_string) status_string;
   decltype(&gdn_last_error_string) last_error_string;
 } api;
@@ -215,7 +219,7 @@ PyObject *pack(std::initializer_list<Tensor> ts) {
 }
 
 // ------------------------------------------------------------------ the functions
-// q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q, scale, window, return_lse, out, workspace
+// q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q, scale, window, return_lse, out, workspace, sinks
 PyObject *paged_attention(PyObject *const *a) {
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_cache"), &v = tensor(a[2], "v_cache"), &table = tensor(a[3], "page_table"),
                &lens = tensor(a[4], "kv_lens");
@@ -233,10 +237,16 @@ PyObject *paged_attention(PyObject *const *a) {
   if (truth(a[9])) lse = at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat));
   if (given) scratch(*given, need);
   const Tensor ws = given ? *given : bytes(need, q);
-  check(api.paged_attn_fwd(&s, q.data_ptr(), k.data_ptr(), v.data_ptr(), i32(table), i32(cu), i32(lens), o.data_ptr(),
-                           lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr, ws.data_ptr(), ws.nbytes(),
-                           (gdn_stream_t)stream(q)),
-        "gdn_paged_attn_fwd");
+  const int sinks = small_int(a[12], "sinks");
+  float *lse_ptr = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
+  if (sinks)
+    check(api.paged_attn_sinks_fwd(&s, sinks, q.data_ptr(), k.data_ptr(), v.data_ptr(), i32(table), i32(cu), i32(lens), o.data_ptr(),
+                                   lse_ptr, ws.data_ptr(), ws.nbytes(), (gdn_stream_t)stream(q)),
+          "gdn_paged_attn_sinks_fwd");
+  else
+    check(api.paged_attn_fwd(&s, q.data_ptr(), k.data_ptr(), v.data_ptr(), i32(table), i32(cu), i32(lens), o.data_ptr(), lse_ptr,
+                             ws.data_ptr(), ws.nbytes(), (gdn_stream_t)stream(q)),
+          "gdn_paged_attn_fwd");
   wrote({out});
   return lse.defined() ? pack({o, lse}) : THPVariable_Wrap(o);
 }
@@ -254,6 +264,58 @@ PyObject *paged_attention_status(PyObject *const *a) {
   if (!need) check(GDN_ERR_INVALID_ARG, "gdn_paged_attn_workspace_size");
   scratch(ws, need);
   return PyLong_FromLong(api.paged_attn_status(&s, ws.data_ptr(), (gdn_stream_t)stream(q)));
+}
+
+// the groups of a batch with shared prefixes
+int prefix_groups(const gdn_paged_shape &s, const Tensor &lens, const Tensor *cu) {
+  ints(lens, "prefix_lens");
+  if (lens.dim() != 1) bad("prefix_lens must have one entry per group");
+  const int groups = fits(lens.size(0), "the number of groups");
+  if (cu) ints(*cu, "cu_seqs", (int64_t)groups + 1);
+  else if (groups == 0 ? s.num_seqs > 0 : s.num_seqs % groups != 0) bad("without cu_seqs the sequences must fall into groups of one size");
+  return groups;
+}
+
+// q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_seqs, cu_q, max_q, max_group, scale, return_lse, out, workspace
+PyObject *prefix_attention(PyObject *const *a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_cache"), &v = tensor(a[2], "v_cache"), &table = tensor(a[3], "page_table"),
+               &lens = tensor(a[4], "kv_lens"), &prefix = tensor(a[5], "prefix_lens");
+  const Tensor *cu_seqs = maybe(a[6], "cu_seqs"), *cu = maybe(a[7], "cu_q"), *out = maybe(a[12], "out"), *given = maybe(a[13], "workspace");
+  gdn_paged_shape s = paged_shape(q, k, v, table, lens, cu);
+  const int groups = prefix_groups(s, prefix, cu_seqs), max_group = small_int(a[9], "max_group");
+  s.max_q = small_int(a[8], "max_q");
+  s.scale = a[10] == Py_None ? (float)(1.0 / std::sqrt((double)q.size(2))) : (float)number(a[10]);
+  const Tensor o = like(out, q);
+  s.o_tok = o.stride(0);
+  s.o_head = o.stride(1);
+  const size_t need = api.prefix_attn_workspace_size(&s, groups, max_group);
+  if (!need) check(GDN_ERR_INVALID_ARG, "gdn_prefix_attn_workspace_size");
+  Tensor lse;
+  if (truth(a[11])) lse = at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat));
+  if (given) scratch(*given, need);
+  const Tensor ws = given ? *given : bytes(need, q);
+  check(api.prefix_attn_fwd(&s, groups, max_group, q.data_ptr(), k.data_ptr(), v.data_ptr(), i32(table), i32(cu), i32(lens), i32(cu_seqs),
+                            i32(prefix), o.data_ptr(), lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr, ws.data_ptr(),
+                            ws.nbytes(), (gdn_stream_t)stream(q)),
+        "gdn_prefix_attn_fwd");
+  wrote({out});
+  return lse.defined() ? pack({o, lse}) : THPVariable_Wrap(o);
+}
+
+// q, k_cache, v_cache, page_table, kv_lens, prefix_lens, workspace, cu_seqs, cu_q, max_q, max_group
+PyObject *prefix_attention_status(PyObject *const *a) {
+  const Tensor &q = tensor(a[0], "q"), &prefix = tensor(a[5], "prefix_lens"), &ws = tensor(a[6], "workspace");
+  gdn_paged_shape s = paged_shape(q, tensor(a[1], "k_cache"), tensor(a[2], "v_cache"), tensor(a[3], "page_table"), tensor(a[4], "kv_lens"),
+                                  maybe(a[8], "cu_q"));
+  const int groups = prefix_groups(s, prefix, maybe(a[7], "cu_seqs")), max_group = small_int(a[10], "max_group");
+  s.max_q = small_int(a[9], "max_q");
+  s.scale = 1.f;
+  s.o_tok = q.size(1) * q.size(2);
+  s.o_head = q.size(2);
+  const size_t need = api.prefix_attn_workspace_size(&s, groups, max_group);
+  if (!need) check(GDN_ERR_INVALID_ARG, "gdn_prefix_attn_workspace_size");
+  scratch(ws, need);
+  return PyLong_FromLong(api.prefix_attn_status(&s, groups, max_group, ws.data_ptr(), (gdn_stream_t)stream(q)));
 }
 
 // the shape of q [T, heads, D] and k (or none) with their angles; the outputs' strides stay open
@@ -810,7 +872,7 @@ template <PyObject *(*F)(PyObject *const *), int N> PyObject *entry(PyObject *, 
 #define ENTRY(name, n) {#name, (PyCFunction)(void (*)(void))entry<name, n>, METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {ENTRY(connect, (int)(sizeof(Api) / sizeof(void *))),
-                         ENTRY(paged_attention, 12),
+                         ENTRY(paged_attention, 13),
                          ENTRY(paged_attention_status, 8),
                          ENTRY(rotary, 7),
                          ENTRY(rotary_append, 11),
@@ -821,6 +883,8 @@ PyMethodDef methods[] = {ENTRY(connect, (int)(sizeof(Api) / sizeof(void *))),
                          ENTRY(copy_slots, 3),
                          ENTRY(rms_norm, 8),
                          ENTRY(rms_norm_bwd, 6),
+                         ENTRY(prefix_attention, 14),
+                         ENTRY(prefix_attention_status, 11),
                          ENTRY(norm_rotary, 9),
                          ENTRY(norm_rotary_bwd, 11),
                          ENTRY(norm_rotary_append, 15),

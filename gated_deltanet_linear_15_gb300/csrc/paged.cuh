@@ -18,6 +18,15 @@
 
 namespace gdn {
 
+// What a kernel computes of the attention:
+//   ALL   every key that a query sees: causal, or a window;
+//   SINKS a window, and the first `sinks` keys of the sequence, which stay visible;
+//   HEAD  the keys of a prefix that a group of sequences shares: all of them, for all the group's new tokens.  The groups
+//         take the sequences' place;
+//   TAIL  the keys behind that prefix.
+// HEAD and TAIL leave unnormalised sums, which attn_prefix.cu joins.
+enum Part { ALL, SINKS, HEAD, TAIL };
+
 struct PagedArgs {
   const void *q, *k, *v;
   void *o;
@@ -25,13 +34,19 @@ struct PagedArgs {
   const int *table, *cu_q, *kv_lens;
   long long table_stride, q_tok, q_head, k_page, k_tok, k_head, v_page, v_tok, v_head, o_tok, o_head;  // elements
   int N, total_q, per_seq;  // per_seq: new tokens of every sequence when cu_q is NULL
-  int Hq, Hkv, G, log2P, num_pages, max_pages, window;
+  int Hq, Hkv, G, log2P, num_pages, max_pages, window, sinks;
   float scale_log2;         // scale * log2(e): the softmax runs in powers of two
   int *status;              // one word per CTA: 0, or 4 when a bounded wait of it ran out
   int expire;               // test hook: one wait that runs out, and nothing else
   // cut items: headers [C] and records [C][2][MT * (D + 2)] (sums [MT][D], maxima [MT], masses [MT])
   int4 *hdr;
   float *part;
+  // HEAD, TAIL: the sequences (HEAD: groups); records of items that are not cut, [total_q][Hq] of D sums, and of maximum and
+  // mass; where each row's pieces are: the CTA of the first one and the row in its records, or {-1, 0}: an uncut record
+  const int4 *info;
+  float *sums;
+  float2 *mass;
+  int2 *loc;
 };
 
 // Records of a CTA: slot 1 holds the first piece of an item that goes on in the next CTA, slot 0 a piece of an item that
@@ -41,9 +56,15 @@ __host__ __device__ constexpr size_t record_floats(int MT, int D) { return (size
 
 struct SeqInfo {
   int qbeg, qlen, kv;
+  int ext;  // HEAD: the sequence whose table row names the prefix; TAIL: tokens of the prefix
 };
-__device__ __forceinline__ SeqInfo seq_info(const PagedArgs &a, int n) {
+template <int PART = ALL> __device__ __forceinline__ SeqInfo seq_info(const PagedArgs &a, int n) {
   SeqInfo s;
+  if constexpr (PART == HEAD || PART == TAIL) {
+    const int4 v = a.info[n];
+    return {v.x, v.y, v.z, v.w};
+  }
+  s.ext = 0;
   if (a.cu_q) {
     const int b = min(max(a.cu_q[n], 0), a.total_q), e = min(max(a.cu_q[n + 1], b), a.total_q);
     s.qbeg = b;
@@ -68,11 +89,12 @@ struct Tile {
   int rows;       // valid rows (0: no such tile)
   int lo, hi;     // keys that some row sees
   int blk0, nblk; // in blocks of BN
+  int nsink;      // SINKS: of them, blocks at the sequence's beginning; the others follow from blk0 on
   int setup;      // SETUP
   __device__ __forceinline__ int units() const { return setup + max(nblk, 1); }
   int pos0;       // position of token r0 / G of the sequence's new tokens
 };
-template <int MT, int BN>
+template <int MT, int BN, int PART = ALL>
 __device__ __forceinline__ Tile tile_of(const PagedArgs &a, const SeqInfo &s, int t) {
   Tile w;
   w.setup = SETUP<MT>;
@@ -82,9 +104,40 @@ __device__ __forceinline__ Tile tile_of(const PagedArgs &a, const SeqInfo &s, in
   w.pos0 = s.kv - s.qlen + i0;
   w.hi = max(0, min(s.kv, s.kv - s.qlen + i1 + 1));
   w.lo = a.window ? (int)max(0ll, (long long)w.pos0 - a.window + 1) : 0;  // pos0 < 0: fewer cached tokens than new ones
+  if constexpr (PART == HEAD) {
+    w.pos0 = s.kv - 1;
+    w.hi = s.kv;
+    w.lo = 0;
+  }
+  if constexpr (PART == TAIL) w.lo = s.ext;
+  if constexpr (PART == SINKS) {
+    if (w.lo <= a.sinks) w.lo = 0;
+  }
   w.blk0 = w.lo / BN;
   w.nblk = w.rows > 0 && w.hi > w.lo ? (w.hi + BN - 1) / BN - w.blk0 : 0;
+  w.nsink = 0;
+  if constexpr (PART == SINKS) {
+    if (w.lo > 0 && w.nblk > 0) {
+      w.nsink = min(a.sinks / BN + (a.sinks % BN > 0), w.blk0);
+      w.nblk += w.nsink;
+    }
+  }
   return w;
+}
+// the position that decides which keys the tile's token of position p (HEAD: any) sees
+template <int PART> __device__ __forceinline__ int seen_from(const SeqInfo &s, int p) { return PART == HEAD ? s.kv - 1 : p; }
+// tokens from the first block of the tile on, of block b; the blocks of sinks lie elsewhere
+template <int BN, int PART> __device__ __forceinline__ int block_begin(const Tile &w, int b) {
+  if (PART == SINKS && b < w.nsink) return b * BN;
+  return (w.blk0 + b - (PART == SINKS ? w.nsink : 0)) * BN;
+}
+// whether key t is one that no row of the tile sees
+template <int PART> __device__ __forceinline__ bool unseen(const PagedArgs &a, int lo, int hi, int t) {
+  return t >= hi || (t < lo && !(PART == SINKS && t < a.sinks));
+}
+// the table row of the cursor's sequence
+template <int PART, typename C> __device__ __forceinline__ const int *table_row(const PagedArgs &a, const C &c) {
+  return a.table + (long long)(PART == HEAD ? c.s.ext : c.n) * a.table_stride;
 }
 template <int MT> __device__ __forceinline__ int tiles_of(const PagedArgs &a, const SeqInfo &s) {
   return (int)(((unsigned)s.qlen * a.G + MT - 1) / MT);
@@ -152,14 +205,14 @@ template <int NT> struct PlanSmem {
 };
 
 // Finds where this CTA's range begins.  False when it has none.  Threads 0 .. NT - 1 call it (NT a power of two).
-template <int NT, int MT, int BN>
+template <int NT, int MT, int BN, int PART>
 __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, PlanSmem<NT> &sm) {
   const int tid = threadIdx.x;
   // tiles of the sequences, NT equal shares of them (a thread with one sequence keeps what it read)
   const int cs = a.N / NT + (a.N % NT > 0);
   const int n0 = (int)min((long long)a.N, (long long)tid * cs), n1 = (int)min((long long)a.N, (long long)n0 + cs);
   long long cnt = 0;
-  for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seq_info(a, n));
+  for (int n = n0; n < n1; ++n) cnt += tiles_of<MT>(a, seq_info<PART>(a, n));
   const long long inc = block_scan<NT>(cnt, sm.scan);
   sm.tiles[tid + 1] = (int)inc;
   if (tid == 0) sm.tiles[0] = 0;
@@ -178,7 +231,7 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
     n = sl * cs;
     int left = x - sm.tiles[sl];
     for (;;) {
-      s = seq_info(a, n);
+      s = seq_info<PART>(a, n);
       const int k = tiles_of<MT>(a, s);
       if (left < k) break;
       left -= k;
@@ -194,12 +247,12 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
     seek(x0, n, t, s);
     int k = tiles_of<MT>(a, s);
     for (int x = x0;;) {
-      units += tile_of<MT, BN>(a, s, t).units();
+      units += tile_of<MT, BN, PART>(a, s, t).units();
       if (++x >= x1) break;
       if (++t >= k) {
         t = 0;
         do {
-          s = seq_info(a, ++n);
+          s = seq_info<PART>(a, ++n);
           k = tiles_of<MT>(a, s);
         } while (k == 0);
       }
@@ -220,7 +273,7 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
   seek((int)min((long long)NTILE - 1, (long long)sl * ct), c.n, c.t, c.s);
   long long left = c.u - sm.units[sl];
   for (;;) {
-    c.w = tile_of<MT, BN>(a, c.s, c.t);
+    c.w = tile_of<MT, BN, PART>(a, c.s, c.t);
     const int per = c.w.units();
     if (left < (long long)per * a.Hkv) {
       c.h = (int)div_units(left, per);
@@ -230,7 +283,7 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
     left -= (long long)per * a.Hkv;
     if (++c.t >= tiles_of<MT>(a, c.s)) {
       c.t = 0;
-      do c.s = seq_info(a, ++c.n);
+      do c.s = seq_info<PART>(a, ++c.n);
       while (tiles_of<MT>(a, c.s) == 0);
     }
   }
@@ -241,7 +294,7 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
 // the sequences and then of the tiles.  A CTA runs this code once, so most of its time is that of fetching instructions;
 // the search above costs 64 sequences 7 us more.  seqs: what is known of the sequences, in shared memory.  Writes c (from
 // one lane) and returns 1, 0 when the CTA has no work, or 2 when the batch is too large.
-template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const PagedArgs &a, Cursor &c, const SeqInfo *seqs) {
+template <int MT, int BN, int PART> __device__ __forceinline__ int cursor_begin_warp(const PagedArgs &a, Cursor &c, const SeqInfo *seqs) {
   const int lane = threadIdx.x & 31;
   auto scan = [&](long long x) {
 #pragma unroll 1
@@ -266,7 +319,7 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const
   int left = x0 - __shfl_sync(0xffffffffu, (int)(inc - cnt), own);
   // walks from tile x0 on; a second time, up to unit `stop`, for the lane that holds the CTA's first one
   int n = own * cs, t = 0, k = 0;
-  SeqInfo s = {0, 0, 0};
+  SeqInfo s = {0, 0, 0, 0};
   Tile w;
   long long units = 0, stop = 1ll << 62;
   bool twice = false;
@@ -286,7 +339,7 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const
       units = 0;
 #pragma unroll 1
       for (int x = x0;;) {
-        w = tile_of<MT, BN>(a, s, t);
+        w = tile_of<MT, BN, PART>(a, s, t);
         const long long per = (long long)w.units() * a.Hkv;
         if (units + per > stop) break;
         units += per;
@@ -326,7 +379,7 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_warp(const
 
 // And for up to 32 sequences with up to 32 tiles: a lane per sequence, then a lane per tile (1 us less than the search
 // above for a decode step of one sequence).  Returns what it returns.
-template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(const PagedArgs &a, Cursor &c) {
+template <int MT, int BN, int PART> __device__ __forceinline__ int cursor_begin_small(const PagedArgs &a, Cursor &c) {
   if (a.N > 32) return 2;
   const int lane = threadIdx.x & 31;
   auto scan = [&](int x) {
@@ -337,8 +390,8 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(cons
     }
     return x;
   };
-  SeqInfo s = {0, 0, 0};
-  if (lane < a.N) s = seq_info(a, lane);
+  SeqInfo s = {0, 0, 0, 0};
+  if (lane < a.N) s = seq_info<PART>(a, lane);
   const int k = lane < a.N ? tiles_of<MT>(a, s) : 0;
   if (__any_sync(0xffffffffu, k > 32)) return 2;
   const int inc = scan(k), tiles = __shfl_sync(0xffffffffu, inc, 31);
@@ -353,8 +406,9 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(cons
   s.qbeg = __shfl_sync(0xffffffffu, s.qbeg, n);
   s.qlen = __shfl_sync(0xffffffffu, s.qlen, n);
   s.kv = __shfl_sync(0xffffffffu, s.kv, n);
+  if constexpr (PART == HEAD || PART == TAIL) s.ext = __shfl_sync(0xffffffffu, s.ext, n);
   const bool mine = lane < tiles;
-  const Tile w = tile_of<MT, BN>(a, s, mine ? t : 0);
+  const Tile w = tile_of<MT, BN, PART>(a, s, mine ? t : 0);
   const long long un = mine ? (long long)w.units() * a.Hkv : 0;
   if (__any_sync(0xffffffffu, un > (1 << 25))) return 2;
   const int uinc = scan((int)un), total = __shfl_sync(0xffffffffu, uinc, 31);
@@ -383,21 +437,21 @@ template <int MT, int BN> __device__ __forceinline__ int cursor_begin_small(cons
 // all loads at once (256 decoded sequences of up to 128 tokens: 36.4 us, with the pages of the next
 // piece asked for a piece ahead, instead of 38.0).
 constexpr int WARP_SEQS = 512;
-template <int NT> __device__ __forceinline__ void cursor_prepare(const PagedArgs &a, SeqInfo *seqs) {
+template <int NT, int PART> __device__ __forceinline__ void cursor_prepare(const PagedArgs &a, SeqInfo *seqs) {
   if (a.N <= 32 || a.N > WARP_SEQS) return;
-  for (int n = threadIdx.x; n < a.N; n += NT) seqs[n] = seq_info(a, n);
+  for (int n = threadIdx.x; n < a.N; n += NT) seqs[n] = seq_info<PART>(a, n);
   __syncthreads();
 }
 // One warp's search, whichever fits.  The caller's kernel has to keep its asynchronous copies off `seqs` until then.
-template <int MT, int BN> __device__ __forceinline__ int cursor_begin_one_warp(const PagedArgs &a, Cursor &c, SeqInfo *seqs) {
-  const int found = cursor_begin_small<MT, BN>(a, c);
+template <int MT, int BN, int PART> __device__ __forceinline__ int cursor_begin_one_warp(const PagedArgs &a, Cursor &c, SeqInfo *seqs) {
+  const int found = cursor_begin_small<MT, BN, PART>(a, c);
   if (found != 2 || a.N > WARP_SEQS) return found;
   if (a.N <= 32) {
     const int lane = threadIdx.x & 31;
-    if (lane < a.N) seqs[lane] = seq_info(a, lane);
+    if (lane < a.N) seqs[lane] = seq_info<PART>(a, lane);
     __syncwarp();
   }
-  return cursor_begin_warp<MT, BN>(a, c, seqs);
+  return cursor_begin_warp<MT, BN, PART>(a, c, seqs);
 }
 
 // The header of a CTA whose last item goes on behind its range: c is the cursor at the item's first piece.
@@ -420,7 +474,7 @@ __device__ __forceinline__ int cursor_piece(const Cursor &c, int &b0, int &b1, b
 }
 
 // Moves past the piece of n units; false at the end of the range.
-template <int MT, int BN> __device__ __forceinline__ bool cursor_next(const PagedArgs &a, Cursor &c, int n) {
+template <int MT, int BN, int PART> __device__ __forceinline__ bool cursor_next(const PagedArgs &a, Cursor &c, int n) {
   c.u += n;
   if (c.u >= c.end) return false;
   c.skip = 0;
@@ -428,10 +482,10 @@ template <int MT, int BN> __device__ __forceinline__ bool cursor_next(const Page
     c.h = 0;
     if (++c.t >= tiles_of<MT>(a, c.s)) {
       c.t = 0;
-      do c.s = seq_info(a, ++c.n);
+      do c.s = seq_info<PART>(a, ++c.n);
       while (tiles_of<MT>(a, c.s) == 0);
     }
-    c.w = tile_of<MT, BN>(a, c.s, c.t);
+    c.w = tile_of<MT, BN, PART>(a, c.s, c.t);
   }
   return c.works();
 }
@@ -443,15 +497,33 @@ __device__ __forceinline__ void row_place(const PagedArgs &a, const Cursor &c, i
   head = c.h * a.G + (int)(g - i * a.G);
 }
 
+// HEAD, TAIL: notes where row r of the cursor's item, which begins here, is found
+__device__ __forceinline__ void note_row(const PagedArgs &a, bool whole, int tok, int head, int r) {
+  a.loc[(long long)tok * a.Hq + head] = whole ? make_int2(-1, 0) : make_int2((int)blockIdx.x, r);
+}
+
 // rows of a tile of the row kernel for up to `rows` rows per key head, and its CTAs per SM
 int attn_rows_tile(bool bf16_type, int D, int rows);
 int attn_rows_per_sm(bool bf16_type, int D, int MT);
 int attn_rows_box(bool bf16_type, int MT, int page_size);  // slots of a box of its tensor maps
-cudaError_t launch_attn_rows(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf16_type, int D, int MT,
+cudaError_t launch_attn_rows(const PagedArgs &a, Part part, const CUtensorMap &tk, const CUtensorMap &tv, bool bf16_type, int D, int MT,
                              int ctas, cudaStream_t st);
 // items: an upper bound on the items of the call
 cudaError_t launch_attn_join(const PagedArgs &a, bool bf16_type, int D, int MT, int ctas, int items, cudaStream_t st);
-cudaError_t launch_attn_chunk_tc(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, int D, int ctas,
+cudaError_t launch_attn_chunk_tc(const PagedArgs &a, Part part, const CUtensorMap &tk, const CUtensorMap &tv, int D, int ctas,
                                  cudaStream_t st);
+// launch_attn_rows of one part, each in a translation unit of its own
+template <int PART>
+cudaError_t launch_attn_rows_part(const PagedArgs &a, const CUtensorMap &tk, const CUtensorMap &tv, bool bf16_type, int D, int MT, int ctas,
+                                  cudaStream_t st);
+// The split of a batch into heads and tails (attn_prefix.cu): what a launch of either reads, from the caller's arrays.
+struct PrefixPlan {
+  const int *cu_seqs, *prefix_lens;  // groups; cu_seqs NULL: equal ones
+  int groups;
+  int4 *head, *tail;                 // info of the groups and of the sequences
+};
+cudaError_t launch_prefix_plan(const PagedArgs &a, const PrefixPlan &p, int2 *head_loc, int2 *tail_loc, cudaStream_t st);
+cudaError_t launch_prefix_join(const PagedArgs &head, const PagedArgs &tail, bool bf16_type, int D, int head_MT, int tail_MT, int head_ctas,
+                               int tail_ctas, cudaStream_t st);
 
 }  // namespace gdn

@@ -92,6 +92,33 @@ int gdn_paged_attn_fwd(const gdn_paged_shape *shape, const void *q, const void *
  * arrives at, sets the status and returns without writing its outputs. */
 int gdn_paged_attn_status(const gdn_paged_shape *shape, const void *workspace, gdn_stream_t stream);
 
+/* gdn_paged_attn_fwd of a window whose sequences' first `sinks` keys stay visible: the query at position p sees the keys j <= p
+ * with j > p - window or j < sinks.  Without a window (0, or one as long as a table row) they add nothing.  The same
+ * workspace and status. */
+int gdn_paged_attn_sinks_fwd(const gdn_paged_shape *shape, int sinks, const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *page_table, const int32_t *cu_q /* nullable */, const int32_t *kv_lens, void *o,
+                             float *lse /* nullable */, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
+ * gdn_paged_attn_fwd of groups of sequences that share a prefix (branches that gdn_pages_fork made, or requests behind one
+ * system prompt), whose keys are read once for a group.  Group g is the sequences cu_seqs[g] .. cu_seqs[g+1]-1 (device int32
+ * [groups + 1], not decreasing; NULL: num_seqs / groups each; sequences that no group names have no prefix).  The first
+ * prefix_lens[g] tokens (device int32 [groups]) of all of them are those of the group's first sequence: the rows of page_table
+ * name the same pages there, and those of the first one are read.  A prefix longer than what some sequence of the
+ * group had cached before its new tokens is cut to that, so any value gives right results where the pages are the same.
+ * The new tokens of a group's sequences follow one another in q (cu_q as in gdn_paged_attn_fwd; one that goes back leaves rows
+ * without an output).  window must be 0.  max_group: most new tokens of a group if the host knows, 0 otherwise (picks the
+ * kernel).  Small batches, where sharing saves too little, are computed as gdn_paged_attn_fwd does, from each sequence's
+ * own row.
+ */
+size_t gdn_prefix_attn_workspace_size(const gdn_paged_shape *shape, int groups, int max_group);
+int gdn_prefix_attn_fwd(const gdn_paged_shape *shape, int groups, int max_group, const void *q, const void *k_cache,
+                        const void *v_cache, const int32_t *page_table, const int32_t *cu_q /* nullable */,
+                        const int32_t *kv_lens, const int32_t *cu_seqs /* nullable */, const int32_t *prefix_lens, void *o,
+                        float *lse /* nullable */, void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+/* gdn_paged_attn_status of the last gdn_prefix_attn_fwd with these arguments. */
+int gdn_prefix_attn_status(const gdn_paged_shape *shape, int groups, int max_group, const void *workspace, gdn_stream_t stream);
+
 /* ------------------------------------------------------------------ rotary positions
  * The pair (a, b) of features at a position turns by the position's angle of that pair:
  *     (a, b) -> (a cos - b sin, b cos + a sin).
