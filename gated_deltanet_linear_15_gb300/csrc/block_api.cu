@@ -289,10 +289,12 @@ int attn_status_words(const AttnPlan &p, const void *ws) {
 }
 
 // ------------------------------------------------------------------ attention behind a shared prefix
-#ifndef PREFIX_MIN
-#define PREFIX_MIN 0
-#endif
-constexpr double PREFIX_MIN_BYTES = PREFIX_MIN;
+// Where sharing saves no more than this many bytes, a batch is computed as if its sequences shared nothing.  Two parts take
+// three launches more, some 10 us; reading shared keys again, mostly from L2, costs 1 us for 13 MB in bf16 and for 7 in fp32.
+// One new token, us as one / in two parts: bf16, 8 key heads of 128: 16 sequences behind 1024 tokens (67 MB) 18 / 25, 4
+// behind 16384 (202 MB) 36 / 32, 64 behind 4096 (1.1 GB) 111 / 33; 2 key heads of 64: 64 behind 4096 (134 MB) 31 / 26; fp32,
+// 2 key heads of 128: 64 behind 256 (41 MB) 23 / 30, 4 behind 16384 (101 MB) 46 / 40.
+double prefix_min_bytes(gdn_dtype d) { return d == GDN_BF16 ? 128e6 : 80e6; }
 struct PrefixLayout {
   bool split;  // in two parts; otherwise as sequences that share nothing
   gdn_paged_shape groups;  // the batch of heads
@@ -312,7 +314,7 @@ PrefixLayout prefix_layout(const gdn_paged_shape *s, int groups, int max_group) 
   l.tail = attn_plan(s);
   // bytes that sharing can save at most, as far as the host knows: the sequences of a group read what its first one reads
   const double saved = (double)(s->num_seqs - groups) * s->max_pages * s->page_size * s->num_kv_heads * s->head_dim * 2 * (double)esize(s->dtype);
-  l.split = saved > PREFIX_MIN_BYTES;
+  l.split = saved > prefix_min_bytes(s->dtype);
   if (!l.split) {
     l.total = l.tail.total;
     return l;

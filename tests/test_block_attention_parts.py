@@ -154,16 +154,20 @@ def test_sinks_drawn(seed):
 
 
 # ------------------------------------------------------------------ shared prefixes
-def shared(groups, dtype, D, Hkv, G, page, seed=0):
+def shared(groups, dtype, D, Hkv, G, page, seed=0, wide=True):
     """groups: (prefix, [(new, own) tokens of each sequence, own ones with the new]); a group's sequences name the same pages for
-    its prefix, up to the end of its last page.  Slots that hold no token are NaN."""
+    its prefix, up to the end of its last page.  Slots that hold no token are NaN.  wide: the table has room for so many tokens
+    that sharing could save a lot, as far as the host knows, and the batch is computed in two parts."""
     gen = torch.Generator().manual_seed(seed)
     lens = [(q, pre + own) for pre, seqs in groups for q, own in seqs]
     full = [-(-pre // page) for pre, seqs in groups for _ in seqs]
     need = [max(-(-kv // page), f) for (_, kv), f in zip(lens, full)]
     pool = sum(-(-pre // page) for pre, _ in groups) + sum(n - f for n, f in zip(need, full)) + 3
     perm, at = torch.randperm(pool, generator=gen).tolist(), 0
-    table = torch.full((len(lens), max(need) + 1), -1, dtype=torch.int32)
+    width = max(need) + 1
+    if wide and len(lens) > len(groups):
+        width = max(width, -(-130 * 10 ** 6 // ((len(lens) - len(groups)) * page * Hkv * D * 4)))
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
     kc, vc = torch.full((pool, page, Hkv, D), math.nan), torch.full((pool, page, Hkv, D), math.nan)
     n = 0
     for pre, seqs in groups:
@@ -208,9 +212,10 @@ PREFIX = [
 
 @gpu
 @pytest.mark.parametrize("groups,dtype,D,Hkv,G,page", PREFIX)
-def test_prefix(groups, dtype, D, Hkv, G, page):
+@pytest.mark.parametrize("wide", [True, False])
+def test_prefix(groups, dtype, D, Hkv, G, page, wide):
     import gated_deltanet_linear_15_gb300 as g
-    x, qs, pre, cu_seqs = shared(groups, dtype, D, Hkv, G, page, seed=D + len(groups))
+    x, qs, pre, cu_seqs = shared(groups, dtype, D, Hkv, G, page, seed=D + len(groups), wide=wide)
     per = [sum(q for q, _ in seqs) for _, seqs in groups]
     args = dict(prefix_lens=pre, cu_seqs=cu_seqs, cu_q=ref.lens_to_cu(qs, DEV), max_q=max(qs), max_group=max(per), return_lse=True)
     o, lse = g.prefix_attention(**x, **args)
