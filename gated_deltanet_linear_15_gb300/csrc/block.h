@@ -106,6 +106,7 @@ struct ScanArgs {
   float *hT, *dh0, *states; // hT: step the state; states: read by the backward
   const int *cu;
   int N, tokens, T, D;      // T: tokens of each sequence without cu
+  int run;                  // segments that a warp takes in a row, at most
   long long x_row, g_row, y_row, dy_row, dg_row, h_row;
 };
 // move: bytes of an access that every row allows: 16, 4, or 2 (single bf16 elements)

@@ -30,67 +30,121 @@ namespace gdn {
 
 namespace {
 
-constexpr int SEG = SCAN_SEG, CB = 64, STAGES = 3, MAXC = 8;  // MAXC: CTAs of a cluster
+constexpr int SEG = SCAN_SEG, MAXC = 8;  // MAXC: CTAs of a cluster
 
 // what moves rows: 16-byte pieces, 4-byte pieces, or single bf16 elements
 enum Move { M16, M4, M2 };
-// a lane's two channels of a block: neighbours, or 32 apart where two neighbours have no common access
-template <typename X, int M> struct Lanes {
-  static constexpr bool PAIR = M == M16 || (M == M4 && sizeof(X) == 2);
-  static __device__ __forceinline__ int first(int lane) { return PAIR ? 2 * lane : lane; }
-};
+// A lane holds NP pairs of a block's 64 NP channels: neighbours, or pairs 64 apart, or single channels 32 apart, as accesses allow.
+enum Lay { NEXT, PAIRS, SINGLE };
+template <typename X, int M> constexpr int LAY = M == M16 ? NEXT : (M == M4 && sizeof(X) == 2 ? PAIRS : SINGLE);
+template <int L, int NP> __device__ __forceinline__ int first_channel(int lane) {
+  return L == NEXT ? 2 * NP * lane : (L == PAIRS ? 2 * lane : lane);
+}
 
-// rows t0 .. t0 + 15, channels c0 .. c0 + 63 of src come to dst [SEG][CB]; zeros outside [lo, hi) x [0, D)
-template <typename E, int M>
-__device__ __forceinline__ void load_rows(E *dst, const E *src, long long row, int t0, int lo, int hi, int c0, int D) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (M == M2) {
+// a lane's values
+template <int NP> struct Vals {
+  uint64_t v[NP];
+  __device__ __forceinline__ float2 pair(int i) const {
+    float2 f;
+    upk(v[i], f.x, f.y);
+    return f;
+  }
+};
+template <int NP> __device__ __forceinline__ Vals<NP> operator+(Vals<NP> a, const Vals<NP> &b) {
 #pragma unroll
-    for (int r = 0; r < SEG; ++r) {
-      const bool ok = t0 + r >= lo && t0 + r < hi;
+  for (int i = 0; i < NP; ++i) a.v[i] = add2(a.v[i], b.v[i]);
+  return a;
+}
+template <int NP> __device__ __forceinline__ Vals<NP> operator*(Vals<NP> a, const Vals<NP> &b) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = lane + 32 * k;
-        E v = fromf<E>(0.f);
-        if (ok && c0 + c < D) v = src[(long long)(t0 + r) * row + c0 + c];
-        dst[r * CB + c] = v;
-      }
-    }
-  } else {
-    constexpr int B = M == M16 ? 16 : 4, V = B / (int)sizeof(E), PER = CB / V;  // pieces of a row
-    constexpr int RPI = PER < 32 ? 32 / PER : 1, CPI = PER < 32 ? PER : 32;       // rows and pieces of one instruction
-    const int r0 = lane / CPI;
+  for (int i = 0; i < NP; ++i) a.v[i] = mul2(a.v[i], b.v[i]);
+  return a;
+}
+template <int NP> __device__ __forceinline__ Vals<NP> fma(Vals<NP> a, const Vals<NP> &b, const Vals<NP> &c) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) a.v[i] = fma2(a.v[i], b.v[i], c.v[i]);
+  return a;
+}
+__device__ __forceinline__ uint64_t wide(uint32_t u) { return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+
+// Rows of segments on their way to shared memory, [SEG][CB]: zeros outside [lo, hi) x [0, D).  The lane's place in the row and the
+// first of its rows stay the same; `at` moves with the segments.
+template <typename E, int M, int CB> struct Loader {
+  static constexpr int B = M == M16 ? 16 : (M == M4 ? 4 : 2), V = B / (int)sizeof(E) > 0 ? B / (int)sizeof(E) : 1;
+  static constexpr int PER = CB / V, RPI = PER < 32 ? 32 / PER : 1, CPI = PER < 32 ? PER : 32;  // pieces of a row; rows, pieces of an instruction
+  const E *src, *at;  // at: of the segment asked for next, the lane's first row
+  long long row, step;
+  // s: the first segment; per: how far the next one lies
+  __device__ __forceinline__ void init(const void *p, long long stride, int c0, long long s, long long per) {
+    const int lane = threadIdx.x & 31;
+    src = static_cast<const E *>(p);
+    row = stride;
+    at = src + (s * SEG + lane / CPI) * row + c0 + lane % CPI * V;
+    step = per * SEG * row;
+  }
+  __device__ __forceinline__ void load(E *dst, int t0, int lo, int hi, int c0, int D) {
+    const int lane = threadIdx.x & 31, r0 = lane / CPI, c = lane % CPI * V;
+    const bool inside = t0 >= lo && t0 + SEG <= hi;
+    E *d = dst + r0 * CB + c;
 #pragma unroll
     for (int k = 0; k < PER / CPI; ++k) {
-      const int c = (lane % CPI + 32 * k) * V;
-      const unsigned span = c0 + c < D ? hi - lo : 0, rel = t0 + r0 - lo;
-      const E *s = src + (long long)(t0 + r0) * row + c0 + c;
+      const E *s = at + 32 * k * V;
+      const bool there = c0 + c + 32 * k * V < D;
+      if constexpr (M == M2) {
+#pragma unroll 4
+        for (int i = 0; i < SEG; ++i, s += row) {
+          E v = fromf<E>(0.f);
+          if (there && t0 + i >= lo && t0 + i < hi) v = *s;
+          d[i * CB + 32 * k] = v;
+        }
+      } else {
+        auto copy = [](E *d, const E *s, bool ok) {
+          if constexpr (M == M16) cp_async16(d, s, ok);
+          else cp_async4(d, s, ok);
+        };
+        if (inside) {
+          if (there) {  // what is past D is never looked at
 #pragma unroll
-      for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) {
-        const bool ok = rel + i * RPI < span;
-        E *d = dst + (r0 + i * RPI) * CB + c;
-        if constexpr (M == M16) cp_async16(d, ok ? s : src, ok);
-        else cp_async4(d, ok ? s : src, ok);
+            for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) copy(d + i * RPI * CB + 32 * k * V, s, true);
+          }
+        } else {
+          const unsigned span = there ? hi - lo : 0, rel = t0 + r0 - lo;
+#pragma unroll 1
+          for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) {
+            const bool ok = rel + i * RPI < span;
+            copy(d + i * RPI * CB + 32 * k * V, ok ? s : src, ok);
+          }
+        }
       }
     }
+    at += step;
   }
-}
-// the lane's two values of a row in shared memory
-template <typename E, int M> __device__ __forceinline__ uint64_t get2(const E *row, int lane) {
-  using L = Lanes<E, M>;
-  if constexpr (L::PAIR && sizeof(E) == 2) {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(row + 2 * lane);
-    return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  } else if constexpr (L::PAIR) {
-    return *reinterpret_cast<const uint64_t *>(row + 2 * lane);
+};
+// the lane's values of a row in shared memory
+template <typename E, int L, int NP> __device__ __forceinline__ Vals<NP> get(const E *row, int lane) {
+  Vals<NP> x;
+  if constexpr (L == NEXT && 2 * NP * sizeof(E) == 8) {
+    const uint64_t u = *reinterpret_cast<const uint64_t *>(row + 2 * NP * lane);
+    if constexpr (NP == 1) {
+      x.v[0] = u;
+    } else {
+      x.v[0] = wide((uint32_t)u);
+      x.v[NP - 1] = wide((uint32_t)(u >> 32));
+    }
+  } else if constexpr (L == SINGLE) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) x.v[i] = pk(tof(row[lane + 64 * i]), tof(row[lane + 64 * i + 32]));
   } else {
-    return pk(tof(row[lane]), tof(row[lane + 32]));
+    static_assert(sizeof(E) == 2 && (L == PAIRS || NP == 1), "pairs of bf16");
+#pragma unroll
+    for (int i = 0; i < NP; ++i) x.v[i] = wide(*reinterpret_cast<const uint32_t *>(row + 2 * lane + 64 * i));
   }
+  return x;
 }
 // Gates of a row.  With bf16 rows the product with log2(e) and ex2.approx, off by 2^-22 of themselves, which a bf16 result does
 // not show and which the state carries for 16 tokens at most (its map takes expf of the sum); expf in fp32, where 16 such
 // errors would be half of all.
-template <bool EXACT> __device__ __forceinline__ uint64_t gates(uint64_t g) {
+template <bool EXACT> __device__ __forceinline__ uint64_t gates2(uint64_t g) {
   float a, b;
   if constexpr (EXACT) {
     upk(g, a, b);
@@ -102,20 +156,54 @@ template <bool EXACT> __device__ __forceinline__ uint64_t gates(uint64_t g) {
     return pk(a, b);
   }
 }
-// a row of a block, the lane's channels, of which c is the first; only those below D exist
-template <typename E, bool PAIR> __device__ __forceinline__ void put2(E *row, int c, int D, uint64_t p) {
-  float u, v;
-  upk(p, u, v);
-  if constexpr (PAIR) {
-    if (c < D) st2(row + c, u, v);
+template <bool EXACT, int NP> __device__ __forceinline__ Vals<NP> gates(Vals<NP> g) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) g.v[i] = gates2<EXACT>(g.v[i]);
+  return g;
+}
+
+// a row in global memory: the lane's channels, of which c is the first; only those below D exist
+template <typename E, int L, int NP> __device__ __forceinline__ void put(E *row, int c, int D, const Vals<NP> &x) {
+  row += c;
+  if constexpr (L == NEXT && NP == 2) {
+    if (c >= D) return;
+    const float2 f = x.pair(0), g = x.pair(1);
+    if constexpr (sizeof(E) == 2) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y), q = __floats2bfloat162_rn(g.x, g.y);
+      *reinterpret_cast<uint2 *>(row) = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
+    } else {
+      *reinterpret_cast<float4 *>(row) = make_float4(f.x, f.y, g.x, g.y);
+    }
   } else {
-    if (c < D) row[c] = fromf<E>(u);
-    if (c + 32 < D) row[c + 32] = fromf<E>(v);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float2 f = x.pair(i);
+      if constexpr (L == SINGLE) {
+        if (c + 64 * i < D) row[64 * i] = fromf<E>(f.x);
+        if (c + 64 * i + 32 < D) row[64 * i + 32] = fromf<E>(f.y);
+      } else if (c + 64 * i < D) {
+        st2(row + 64 * i, f.x, f.y);
+      }
+    }
   }
 }
-template <bool PAIR> __device__ __forceinline__ uint64_t take2(const float *row, int c, int D) {
-  if constexpr (PAIR) return c < D ? *reinterpret_cast<const uint64_t *>(row + c) : 0;
-  else return pk(c < D ? row[c] : 0.f, c + 32 < D ? row[c + 32] : 0.f);
+template <int L, int NP> __device__ __forceinline__ Vals<NP> take(const float *row, int c, int D) {
+  Vals<NP> x = {};
+  row += c;
+  if constexpr (L == NEXT && NP == 2) {
+    if (c < D) {
+      const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
+      x.v[0] = u.x;
+      x.v[1] = u.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if constexpr (L == SINGLE) x.v[i] = pk(c + 64 * i < D ? row[64 * i] : 0.f, c + 64 * i + 32 < D ? row[64 * i + 32] : 0.f);
+      else if (c + 64 * i < D) x.v[i] = *reinterpret_cast<const uint64_t *>(row + 64 * i);
+    }
+  }
+  return x;
 }
 
 // ------------------------------------------------------------------ where sequences begin
@@ -137,9 +225,11 @@ __device__ __forceinline__ int part_begin(const ScanArgs &a, int p, int parts) {
   return min(max(a.cu[at], 0), a.tokens);
 }
 
-// The boundaries between sequences around a warp's segment.  With cu, each lane holds one entry of a window that begins at
-// entry `base`; it moves with the segments.
+// The boundaries between sequences around a warp's segment.  The warp knows the sequence [b0, b1) that its last segment
+// began in; most segments lie inside it, and nothing is looked up for them.  With cu, each lane holds one entry of a window
+// that begins at entry `base`; it moves with the segments.
 struct Bounds {
+  int b0, b1;
   int base, e;
   int left;  // windows that may still be looked at: a cu that is not sorted ends the walk, not the kernel
   __device__ __forceinline__ void load(const ScanArgs &a) {
@@ -147,16 +237,22 @@ struct Bounds {
     e = i <= a.N ? a.cu[i] : 0x7fffffff;
   }
   __device__ __forceinline__ void init(const ScanArgs &a, int t) {
+    b0 = b1 = base = e = 0;
     left = a.N / 8 + 64;
-    base = 0;
-    e = 0;
     if (!a.cu) return;
     base = max(lower_bound(a.cu, a.N + 1, t + 1) - 1, 0);
     load(a);
   }
-  // moves the window to token t: its first entry is the last one at or before t, or near it
-  __device__ __forceinline__ void seek(const ScanArgs &a, int t) {
-    if (!a.cu) return;
+  // bit i (of 17): some sequence begins, or the last one ends, at token t + i.  Moves the window to t: its first entry is
+  // the last one at or before t, or near it.
+  __device__ __forceinline__ uint32_t mask(const ScanArgs &a, int t) {
+    if (t > b0 && t + SEG < b1) return 0;
+    const int lane = threadIdx.x & 31;
+    if (!a.cu) {
+      b0 = (int)((unsigned)t / (unsigned)a.T) * a.T;
+      b1 = b0 + a.T;
+      return __ballot_sync(0xffffffffu, lane <= SEG && (unsigned)(t + lane - b0) % (unsigned)a.T == 0);
+    }
     for (; left > 0; --left) {
       const unsigned at = __ballot_sync(0xffffffffu, e <= t);
       if (at == 0xffffffffu && base + 31 <= a.N) base += 31;
@@ -164,11 +260,8 @@ struct Bounds {
       else break;
       load(a);
     }
-  }
-  // bit i (of 17): some sequence begins, or the last one ends, at token t + i.  The window stands at t.
-  __device__ __forceinline__ uint32_t mask(const ScanArgs &a, int t) {
-    const int lane = threadIdx.x & 31;
-    if (!a.cu) return __ballot_sync(0xffffffffu, lane <= SEG && (unsigned)(t + lane) % (unsigned)a.T == 0);
+    b0 = __reduce_max_sync(0xffffffffu, e <= t ? e : -1);
+    b1 = __reduce_min_sync(0xffffffffu, e > t ? e : 0x7fffffff);
     uint32_t m = 0;
     int b = base, x = e;
     for (int k = 0; k <= a.N / 31 + 1; ++k) {
@@ -197,92 +290,185 @@ struct Bounds {
 
 // ------------------------------------------------------------------ maps of segments
 // c -> A c + H; A < 0 marks one that forgets c (whatever c holds, an infinity among it)
-struct Map2 {
-  float A[2], H[2];
-  __device__ __forceinline__ uint64_t apply(uint64_t p) const {
-    float c[2];
-    upk(p, c[0], c[1]);
+template <int NP> struct Map {
+  float A[2 * NP], H[2 * NP];
+  __device__ __forceinline__ void of(float (&c)[2 * NP]) const {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) c[k] = A[k] < 0.f ? H[k] : fmaf(A[k], c[k], H[k]);
-    return pk(c[0], c[1]);
+    for (int i = 0; i < 2 * NP; ++i) c[i] = A[i] < 0.f ? H[i] : fmaf(A[i], c[i], H[i]);
   }
-  __device__ __forceinline__ void then(const Map2 &n) {  // this one first, then n
+  __device__ __forceinline__ void then(const Map &n) {  // this one first, then n
+    n.of(H);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      H[k] = n.A[k] < 0.f ? n.H[k] : fmaf(n.A[k], H[k], n.H[k]);
-      A[k] = n.A[k] < 0.f || A[k] < 0.f ? -1.f : A[k] * n.A[k];
-    }
+    for (int i = 0; i < 2 * NP; ++i) A[i] = n.A[i] < 0.f || A[i] < 0.f ? -1.f : A[i] * n.A[i];
   }
 };
 // of a segment: the sum of its log-gates and its result from zero
-__device__ __forceinline__ float4 segment_map(bool fresh, uint64_t sum, uint64_t h) {
-  float s0, s1, h0, h1;
-  upk(sum, s0, s1);
-  upk(h, h0, h1);
-  return make_float4(fresh ? -1.f : expf(s0), fresh ? -1.f : expf(s1), h0, h1);
+template <int NP> __device__ __forceinline__ Map<NP> segment_map(bool fresh, const Vals<NP> &sum, const Vals<NP> &h) {
+  Map<NP> m;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const float2 s = sum.pair(i), z = h.pair(i);
+    m.A[2 * i] = fresh ? -1.f : expf(s.x);
+    m.A[2 * i + 1] = fresh ? -1.f : expf(s.y);
+    m.H[2 * i] = z.x;
+    m.H[2 * i + 1] = z.y;
+  }
+  return m;
 }
-template <int W> struct Meet {
-  float4 warp[2][W][32];     // by round parity: maps of the CTA's segments
-  float4 peer[2][MAXC][32];  // of the cluster's CTAs
+// a map in shared memory: 16-byte pieces of every lane
+template <int NP> struct MapSlot {
+  float4 p[NP][32];
 };
-__device__ __forceinline__ Map2 map_of(const float4 &v) { return {{v.x, v.y}, {v.z, v.w}}; }
+template <int NP> __device__ __forceinline__ float4 piece_of(const Map<NP> &m, int i) {
+  return make_float4(m.A[2 * i], m.A[2 * i + 1], m.H[2 * i], m.H[2 * i + 1]);
+}
+template <int NP> __device__ __forceinline__ Map<NP> map_at(const MapSlot<NP> &s) {
+  Map<NP> m;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const float4 v = s.p[i][threadIdx.x & 31];
+    m.A[2 * i] = v.x;
+    m.A[2 * i + 1] = v.y;
+    m.H[2 * i] = v.z;
+    m.H[2 * i + 1] = v.w;
+  }
+  return m;
+}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
-// of a warp that has written nothing that peers read: it need not wait for its own stores
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void store_peer(const float4 *p, int rank, const float4 &v) {
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
   uint32_t at;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
+  return at;
+}
+// 16 bytes into a peer's shared memory, counted by its mbarrier
+__device__ __forceinline__ void store_peer(uint32_t at, uint32_t bar, const float4 &v) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];\n" ::"r"(at), "f"(v.x),
+               "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+// The peers of a cluster run at the same time, so the wait ends; one that did not within about a second gives up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t it = 0; it < (1u << 18); ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
 }
 
 // A round's exchange: every warp hands in its segment's map, and later gets the state before it; `carry` becomes the state
-// after the round.
-template <int W> __device__ __forceinline__ void hand_in(Meet<W> &mt, int buf, int cs, int rank, const float4 &mine) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  mt.warp[buf][warp][lane] = mine;
-  __syncthreads();
-  if (cs == 1) return;
-  if (warp == 0) {
-    Map2 all = map_of(mt.warp[buf][0][lane]);
-#pragma unroll
-    for (int j = 1; j < W; ++j) all.then(map_of(mt.warp[buf][j][lane]));
-    for (int r = 0; r < cs; ++r) store_peer(&mt.peer[buf][rank][lane], r, make_float4(all.A[0], all.A[1], all.H[0], all.H[1]));
-    cluster_arrive();
-  } else {
-    cluster_arrive_relaxed();
-  }
-}
-template <int W> __device__ __forceinline__ uint64_t get_state(const Meet<W> &mt, int buf, int cs, int rank, uint64_t &carry) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t in = carry;
-  if (cs == 1) {
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      if (j == warp) in = carry;
-      carry = map_of(mt.warp[buf][j][lane]).apply(carry);
+// after the round.  The CTA's maps meet behind a barrier; every warp joins them and sends the result to some of the cluster's
+// CTAs, where an mbarrier counts its bytes.  (A cluster barrier instead makes the warp that releases its maps by it wait
+// for its own global stores too.)  Two sets of maps by the round's parity: a CTA sends round r + 2
+// only when it has everyone's maps of round r + 1, which come after their reading of round r.
+template <int W, int NP> struct Meet {
+  typedef MapSlot<NP> Slot;
+  Slot *warp, *peer;  // [2][W], [2][cs]
+  uint64_t *bar;      // [2]
+  int cs, rank;
+  __device__ __forceinline__ void init(uint8_t *smem, uint64_t *bars) {
+    warp = reinterpret_cast<Slot *>(smem);
+    peer = warp + 2 * W;
+    bar = bars;
+    cs = gridDim.x;
+    rank = blockIdx.x;
+    if (cs == 1) return;
+    if (threadIdx.x < 2) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(bar + threadIdx.x)) : "memory");
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    return in;
+    __syncwarp();
+    cluster_arrive();  // peers have begun, and their barriers are there, before anything is sent to them
   }
-  cluster_wait();
-  for (int r = 0; r < cs; ++r) {
-    if (r == rank) in = carry;
-    carry = map_of(mt.peer[buf][r][lane]).apply(carry);
+  __device__ __forceinline__ void ready() const {
+    if (cs > 1) cluster_wait();
   }
-  for (int j = 0; j < warp; ++j) in = map_of(mt.warp[buf][j][lane]).apply(in);
-  return in;
-}
+  __device__ __forceinline__ void hand_in(int round, const Map<NP> &mine) const {
+    const int me = threadIdx.x >> 5, lane = threadIdx.x & 31, par = round & 1;
+    Slot *mw = warp + par * W;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) mw[me].p[i][lane] = piece_of(mine, i);
+    __syncthreads();
+    if (cs == 1) return;
+    if (threadIdx.x == 0) bar_expect(smem_u32(bar + par), cs * sizeof(Slot));
+    if (me >= cs) return;
+    Map<NP> all = map_at(mw[0]);
+#pragma unroll
+    for (int j = 1; j < W; ++j) all.then(map_at(mw[j]));
+    const uint32_t at = smem_u32(&peer[par * cs + rank].p[0][lane]), b = smem_u32(bar + par);
+#pragma unroll 1
+    for (int r = me; r < cs; r += W) {
+      const uint32_t ra = peer_addr(at, r), rb = peer_addr(b, r);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) store_peer(ra + 512 * i, rb, piece_of(all, i));
+    }
+  }
+  __device__ __forceinline__ Vals<NP> state(int round, float (&carry)[2 * NP]) const {
+    const int me = threadIdx.x >> 5, par = round & 1;
+    const Slot *mw = warp + par * W, *mp = peer + par * cs;
+    float in[2 * NP];
+    auto keep = [&] {
+#pragma unroll
+      for (int i = 0; i < 2 * NP; ++i) in[i] = carry[i];
+    };
+    keep();
+    if (cs == 1) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if (j == me) keep();
+        map_at(mw[j]).of(carry);
+      }
+    } else {
+      if (!bar_wait(smem_u32(bar + par), round >> 1 & 1)) {
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) carry[i] = __uint_as_float(0x7fffffffu);  // what follows is not reliable, and shows it
+      }
+#pragma unroll
+      for (int b = 0; b < MAXC; b += 4) {
+        if (b >= cs) break;
+        Map<NP> m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = map_at(mp[min(b + j, cs - 1)]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (b + j < cs) {
+            if (b + j == rank) keep();
+            m[j].of(carry);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        if (j < me) map_at(mw[j]).of(in);
+    }
+    Vals<NP> h;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) h.v[i] = pk(in[2 * i], in[2 * i + 1]);
+    return h;
+  }
+};
 
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 // the state of sequences without tokens passes through: out[n] = in[n], shared out among a channel block's CTAs
-template <bool PAIR, int W>
+template <int L, int NP, int W>
 __device__ __forceinline__ void pass_empty(const ScanArgs &a, const float *in, float *out, int c, int ctas, int cta) {
   if (!a.cu || !out) return;
   for (int n = cta * W + (threadIdx.x >> 5); n < a.N; n += ctas * W) {
     if (a.cu[n + 1] > a.cu[n]) continue;
-    put2<float, PAIR>(out + (long long)n * a.D, c, a.D, in ? take2<PAIR>(in + (long long)n * a.D, c, a.D) : 0);
+    put<float, L>(out + (long long)n * a.D, c, a.D, in ? take<L, NP>(in + (long long)n * a.D, c, a.D) : Vals<NP>{});
   }
 }
 
@@ -317,11 +503,7 @@ struct Piece {
     seg = s;
     t0 = s * SEG;
     live = w.has(s);
-    cut = 0;
-    if (live) {
-      bd.seek(a, t0);
-      cut = bd.mask(a, t0);
-    }
+    cut = live ? bd.mask(a, t0) : 0;
     plain = cut == 0 && t0 >= w.lo && t0 + SEG <= w.hi;
   }
   __device__ __forceinline__ bool inside(const Walk &w, int i) const { return t0 + i >= w.lo && t0 + i < w.hi; }
@@ -332,97 +514,107 @@ struct Piece {
 }  // namespace
 
 // grid: CTAs of a cluster, channel blocks, parts.  Each step hands in the maps of round k + 1 and, while the CTAs of the cluster
-// meet, finishes round k, whose states are known.
-template <typename X, typename G, int M, int W>
+// meet, finishes round k, whose states are known; the stages of round k + 2 are on their way.
+template <typename X, typename G, int M, int W, int NP>
 __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
-  constexpr bool PAIR = Lanes<X, M>::PAIR, EXACT = sizeof(X) == 4;
-  static_assert(Lanes<X, M>::PAIR == Lanes<G, M>::PAIR, "one layout of channels");
+  constexpr int L = LAY<X, M>, CB = 64 * NP;
+  typedef Vals<NP> V;
+  constexpr bool EXACT = sizeof(X) == 4;
+  static_assert(L == LAY<G, M>, "one layout of channels");
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ Meet<W> mt;
   constexpr int BX = SEG * CB * sizeof(X), ST = BX + SEG * CB * sizeof(G);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + Lanes<X, M>::first(lane);
-  uint8_t *ring = raw + warp * (STAGES * ST);
-  if (cs > 1) cluster_arrive();  // peers have begun before anything is written to them
+  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + first_channel<L, NP>(lane);
+  uint8_t *ring = raw + warp * (3 * ST);
+  __shared__ uint64_t bars[2];
+  Meet<W, NP> mt;
+  mt.init(raw + W * 3 * ST, bars);
   pdl_trigger();
   pdl_wait();
   Walk w = {};
   w.init<W>(a, cs, rank);
+  Loader<X, M, CB> lx;
+  Loader<G, M, CB> lg;
+  lx.init(a.x, a.x_row, c0, w.up(0), w.per);
+  lg.init(a.g, a.g_row, c0, w.up(0), w.per);
   auto load = [&](int k, int slot) {
     if (k < w.rounds && w.has(w.up(k))) {
       uint8_t *st = ring + slot * ST;
-      load_rows<X, M>(reinterpret_cast<X *>(st), static_cast<const X *>(a.x), a.x_row, w.up(k) * SEG, w.lo, w.hi, c0, a.D);
-      load_rows<G, M>(reinterpret_cast<G *>(st + BX), static_cast<const G *>(a.g), a.g_row, w.up(k) * SEG, w.lo, w.hi, c0, a.D);
+      const int t0 = w.up(k) * SEG;
+      lx.load(reinterpret_cast<X *>(st), t0, w.lo, w.hi, c0, a.D);
+      lg.load(reinterpret_cast<G *>(st + BX), t0, w.lo, w.hi, c0, a.D);
     }
     cp_async_commit();
   };
-  load(0, 0);
-  load(1, 1);
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) load(k, k);
   Piece now = {}, next = {};
   next.bd.init(a, w.up(0) * SEG);
-  pass_empty<PAIR, W>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
-  if (cs > 1) cluster_wait();
-  auto x_of = [&](const uint8_t *st, int i) { return get2<X, M>(reinterpret_cast<const X *>(st) + i * CB, lane); };
-  auto g_of = [&](const uint8_t *st, int i) { return get2<G, M>(reinterpret_cast<const G *>(st + BX) + i * CB, lane); };
-  auto start = [&](const Piece &p, int i) { return a.h0 ? take2<PAIR>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : 0; };
-  uint64_t carry = 0, h = 0;
-  int slot = STAGES - 1;  // of round k
+  pass_empty<L, NP, W>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  mt.ready();
+  auto x_of = [&](const uint8_t *st, int i) { return get<X, L, NP>(reinterpret_cast<const X *>(st) + i * CB, lane); };
+  auto g_of = [&](const uint8_t *st, int i) { return get<G, L, NP>(reinterpret_cast<const G *>(st + BX) + i * CB, lane); };
+  auto start = [&](const Piece &p, int i) { return a.h0 ? take<L, NP>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : V{}; };
+  float carry[2 * NP] = {};
+  V h = {};
+  int slot = 2;  // of round k
+#pragma unroll 1
   for (int k = -1; k < w.rounds; ++k) {
-    const int slot1 = slot + 1 == STAGES ? 0 : slot + 1;
+    const int slot1 = slot == 2 ? 0 : slot + 1;
     const bool more = k + 1 < w.rounds;
     if (more) {
       next.look(a, w, w.up(k + 1));
       cp_wait<1>();
       __syncwarp();
       const uint8_t *st = ring + slot1 * ST;
-      uint64_t sum = 0, z = 0;
+      V sum = {}, z = {};
       bool fresh = false;
       if (next.plain) {
 #pragma unroll
         for (int i = 0; i < SEG; ++i) {
-          const uint64_t g = g_of(st, i);
-          sum = add2(sum, g);
-          z = fma2(gates<EXACT>(g), z, x_of(st, i));
+          const V g = g_of(st, i);
+          sum = sum + g;
+          z = fma(gates<EXACT>(g), z, x_of(st, i));
         }
       } else if (next.live) {
 #pragma unroll 1
         for (int i = 0; i < SEG; ++i) {
-          const uint64_t g = g_of(st, i);
+          const V g = g_of(st, i);
           if (next.begins(i) && next.inside(w, i)) {
             z = start(next, i);
             fresh = true;
           }
-          sum = add2(sum, g);
-          z = fma2(gates<EXACT>(g), z, x_of(st, i));
+          sum = sum + g;
+          z = fma(gates<EXACT>(g), z, x_of(st, i));
         }
       }
-      hand_in(mt, k + 1 & 1, cs, rank, segment_map(fresh, sum, z));
+      mt.hand_in(k + 1, segment_map(fresh, sum, z));
     }
     if (k >= 0 && now.live) {
       const uint8_t *st = ring + slot * ST;
-      if (a.states && now.t0 >= w.lo) put2<float, PAIR>(a.states + (long long)now.seg * a.D, c, a.D, h);
+      if (a.states && now.t0 >= w.lo) put<float, L>(a.states + (long long)now.seg * a.D, c, a.D, h);
       X *yr = static_cast<X *>(a.y) + (long long)now.t0 * a.y_row;
       if (now.plain) {
 #pragma unroll
         for (int i = 0; i < SEG; ++i, yr += a.y_row) {
-          h = fma2(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
-          put2<X, PAIR>(yr, c, a.D, h);
+          h = fma(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
+          put<X, L>(yr, c, a.D, h);
         }
       } else {
 #pragma unroll 1
         for (int i = 0; i < SEG; ++i, yr += a.y_row) {
           if (!now.inside(w, i)) continue;
           if (now.begins(i)) h = start(now, i);
-          h = fma2(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
-          put2<X, PAIR>(yr, c, a.D, h);
-          if (now.ends(i) && a.hT) put2<float, PAIR>(a.hT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, h);
+          h = fma(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
+          put<X, L>(yr, c, a.D, h);
+          if (now.ends(i) && a.hT) put<float, L>(a.hT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, h);
         }
       }
     }
     __syncwarp();  // the stage is loaded again
-    load(k + STAGES, slot);
+    load(k + 3, slot);
     if (more) {
-      h = get_state(mt, k + 1 & 1, cs, rank, carry);
+      h = mt.state(k + 1, carry);
       now = next;
     }
     slot = slot1;
@@ -430,123 +622,127 @@ __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
   cp_async_wait_all();
 }
 
-template <typename X, typename G, int M, int W>
-__global__ void __launch_bounds__(32 * W, 2) scan_bwd_kernel(ScanArgs a) {
-  constexpr bool PAIR = Lanes<X, M>::PAIR, EXACT = sizeof(X) == 4;
+// The same walk from the part's end, a round at a time: with more CTAs to an SM instead of a round ahead it is faster (4 x 4096
+// tokens of 2048 channels 80 us instead of 89), since the states before all tokens of a segment take the registers that the
+// round ahead needs.  Two stages of dy and g; x is needed after the exchange only, and has one.  LIMIT: CTAs per SM.
+template <typename X, typename G, int M, int W, int NP, int LIMIT>
+__global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
+  constexpr int L = LAY<X, M>, CB = 64 * NP;
+  typedef Vals<NP> V;
+  constexpr bool EXACT = sizeof(X) == 4;
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ Meet<W> mt;
-  constexpr int BX = SEG * CB * sizeof(X), ST = 2 * BX + SEG * CB * sizeof(G);
+  __shared__ uint64_t bars[2];
+  constexpr int BX = SEG * CB * sizeof(X), ST = BX + SEG * CB * sizeof(G);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + Lanes<X, M>::first(lane);
-  uint8_t *ring = raw + warp * (STAGES * ST);
-  if (cs > 1) cluster_arrive();
+  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + first_channel<L, NP>(lane);
+  uint8_t *ring = raw + warp * (2 * ST + BX);
+  X *sx = reinterpret_cast<X *>(ring + 2 * ST);
+  Meet<W, NP> mt;
+  mt.init(raw + W * (2 * ST + BX), bars);
   pdl_trigger();
   pdl_wait();
   Walk w = {};
   w.init<W>(a, cs, rank);
-  auto load = [&](int k, int slot) {
+  Loader<X, M, CB> lx, ld;
+  Loader<G, M, CB> lg;
+  lx.init(a.x, a.x_row, c0, w.down(0), -w.per);
+  ld.init(a.dy, a.dy_row, c0, w.down(0), -w.per);
+  lg.init(a.g, a.g_row, c0, w.down(0), -w.per);
+  auto load = [&](int k) {  // dy and g of round k
     if (k < w.rounds && w.has(w.down(k))) {
-      uint8_t *st = ring + slot * ST;
-      const int t = w.down(k) * SEG;
-      load_rows<X, M>(reinterpret_cast<X *>(st), static_cast<const X *>(a.x), a.x_row, t, w.lo, w.hi, c0, a.D);
-      load_rows<X, M>(reinterpret_cast<X *>(st + BX), static_cast<const X *>(a.dy), a.dy_row, t, w.lo, w.hi, c0, a.D);
-      load_rows<G, M>(reinterpret_cast<G *>(st + 2 * BX), static_cast<const G *>(a.g), a.g_row, t, w.lo, w.hi, c0, a.D);
+      uint8_t *st = ring + (k & 1) * ST;
+      const int t0 = w.down(k) * SEG;
+      ld.load(reinterpret_cast<X *>(st), t0, w.lo, w.hi, c0, a.D);
+      lg.load(reinterpret_cast<G *>(st + BX), t0, w.lo, w.hi, c0, a.D);
     }
     cp_async_commit();
   };
-  load(0, 0);
-  load(1, 1);
-  Piece now = {}, next = {};
-  next.bd.init(a, max(w.down(0) * SEG, 0));
-  pass_empty<PAIR, W>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
-  if (cs > 1) cluster_wait();
-  auto x_of = [&](const uint8_t *st, int i) { return get2<X, M>(reinterpret_cast<const X *>(st) + i * CB, lane); };
-  auto dy_of = [&](const uint8_t *st, int i) { return get2<X, M>(reinterpret_cast<const X *>(st + BX) + i * CB, lane); };
-  auto g_of = [&](const uint8_t *st, int i) { return get2<G, M>(reinterpret_cast<const G *>(st + 2 * BX) + i * CB, lane); };
-  auto start = [&](const Piece &p, int i) { return a.h0 ? take2<PAIR>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : 0; };
-  auto at_end = [&](const Piece &p, int i) { return a.dhT ? take2<PAIR>(a.dhT + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : 0; };
-  uint64_t carry = 0, d = 0;  // d: what reaches the state from later tokens
-  uint64_t h = 0, h1 = 0;     // stored states before the segments of rounds k and k + 1
-  int slot = STAGES - 1;
-  for (int k = -1; k < w.rounds; ++k) {
-    const int slot1 = slot + 1 == STAGES ? 0 : slot + 1;
-    const bool more = k + 1 < w.rounds;
-    if (more) {
-      next.look(a, w, w.down(k + 1));
-      h1 = next.live ? take2<PAIR>(a.states + (long long)next.seg * a.D, c, a.D) : 0;
-      cp_wait<1>();
-      __syncwarp();
-      const uint8_t *st = ring + slot1 * ST;
-      uint64_t sum = 0, z = 0;
-      bool fresh = false;
-      if (next.plain) {
-#pragma unroll
-        for (int i = SEG - 1; i >= 0; --i) {
-          const uint64_t g = g_of(st, i);
-          sum = add2(sum, g);
-          z = mul2(gates<EXACT>(g), add2(dy_of(st, i), z));
-        }
-      } else if (next.live) {
+  load(0);
+  Piece now = {};
+  now.bd.init(a, max(w.down(0) * SEG, 0));
+  pass_empty<L, NP, W>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  mt.ready();
+  const uint8_t *st = ring;
+  auto x_of = [&](int i) { return get<X, L, NP>(sx + i * CB, lane); };
+  auto dy_of = [&](int i) { return get<X, L, NP>(reinterpret_cast<const X *>(st) + i * CB, lane); };
+  auto g_of = [&](int i) { return get<G, L, NP>(reinterpret_cast<const G *>(st + BX) + i * CB, lane); };
+  auto start = [&](int i) { return a.h0 ? take<L, NP>(a.h0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : V{}; };
+  auto at_end = [&](int i) { return a.dhT ? take<L, NP>(a.dhT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : V{}; };
+  float carry[2 * NP] = {};
 #pragma unroll 1
-        for (int i = SEG - 1; i >= 0; --i) {
-          const uint64_t g = g_of(st, i);
-          if (next.ends(i) && next.inside(w, i)) {
-            z = at_end(next, i);
-            fresh = true;
-          }
-          sum = add2(sum, g);
-          z = mul2(gates<EXACT>(g), add2(dy_of(st, i), z));
-        }
+  for (int k = 0; k < w.rounds; ++k) {
+    st = ring + (k & 1) * ST;
+    now.look(a, w, w.down(k));
+    if (now.live) lx.load(sx, now.t0, w.lo, w.hi, c0, a.D);
+    cp_async_commit();
+    load(k + 1);
+    V h = now.live ? take<L, NP>(a.states + (long long)now.seg * a.D, c, a.D) : V{};
+    cp_wait<2>();
+    __syncwarp();
+    V sum = {}, d = {};  // d: what reaches the state from later tokens
+    bool fresh = false;
+    if (now.plain) {
+#pragma unroll
+      for (int i = SEG - 1; i >= 0; --i) {
+        const V g = g_of(i);
+        sum = sum + g;
+        d = gates<EXACT>(g) * (dy_of(i) + d);
       }
-      hand_in(mt, k + 1 & 1, cs, rank, segment_map(fresh, sum, z));
+    } else if (now.live) {
+#pragma unroll 1
+      for (int i = SEG - 1; i >= 0; --i) {
+        const V g = g_of(i);
+        if (now.ends(i) && now.inside(w, i)) {
+          d = at_end(i);
+          fresh = true;
+        }
+        sum = sum + g;
+        d = gates<EXACT>(g) * (dy_of(i) + d);
+      }
     }
-    if (k >= 0 && now.live) {
-      const uint8_t *st = ring + slot * ST;
-      X *dxr = static_cast<X *>(a.y) + (long long)(now.t0 + SEG - 1) * a.y_row;
-      G *dgr = static_cast<G *>(a.dg) + (long long)(now.t0 + SEG - 1) * a.dg_row;
-      if (now.plain) {
-        uint64_t al[SEG], hp[SEG];  // gates, and states before the tokens
+    mt.hand_in(k, segment_map(fresh, sum, d));
+    cp_wait<1>();
+    __syncwarp();
+    X *dxr = static_cast<X *>(a.y) + (long long)(now.t0 + SEG - 1) * a.y_row;
+    G *dgr = static_cast<G *>(a.dg) + (long long)(now.t0 + SEG - 1) * a.dg_row;
+    if (now.plain) {
+      V hp[SEG];  // states before the tokens
 #pragma unroll
-        for (int i = 0; i < SEG; ++i) {
-          hp[i] = h;
-          al[i] = gates<EXACT>(g_of(st, i));
-          h = fma2(al[i], h, x_of(st, i));
-        }
+      for (int i = 0; i < SEG; ++i) {
+        hp[i] = h;
+        h = fma(gates<EXACT>(g_of(i)), h, x_of(i));
+      }
+      d = mt.state(k, carry);
 #pragma unroll
-        for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
-          const uint64_t dx = add2(dy_of(st, i), d);
-          d = mul2(al[i], dx);
-          put2<X, PAIR>(dxr, c, a.D, dx);
-          put2<G, PAIR>(dgr, c, a.D, mul2(d, hp[i]));
-        }
-      } else {
-        uint64_t hp[SEG];  // in local memory
+      for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
+        const V dx = dy_of(i) + d;
+        d = gates<EXACT>(g_of(i)) * dx;
+        put<X, L>(dxr, c, a.D, dx);
+        put<G, L>(dgr, c, a.D, d * hp[i]);
+      }
+    } else {
+      d = mt.state(k, carry);
+      if (now.live) {
+        V hp[SEG];  // in local memory
 #pragma unroll 1
         for (int i = 0; i < SEG; ++i) {
-          if (now.begins(i) && now.inside(w, i)) h = start(now, i);
+          if (now.begins(i) && now.inside(w, i)) h = start(i);
           hp[i] = h;
-          h = fma2(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
+          h = fma(gates<EXACT>(g_of(i)), h, x_of(i));
         }
 #pragma unroll 1
         for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
           if (!now.inside(w, i)) continue;
-          if (now.ends(i)) d = at_end(now, i);
-          const uint64_t dx = add2(dy_of(st, i), d);
-          d = mul2(gates<EXACT>(g_of(st, i)), dx);
-          put2<X, PAIR>(dxr, c, a.D, dx);
-          put2<G, PAIR>(dgr, c, a.D, mul2(d, hp[i]));
-          if (now.begins(i) && a.dh0) put2<float, PAIR>(a.dh0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, d);
+          if (now.ends(i)) d = at_end(i);
+          const V dx = dy_of(i) + d;
+          d = gates<EXACT>(g_of(i)) * dx;
+          put<X, L>(dxr, c, a.D, dx);
+          put<G, L>(dgr, c, a.D, d * hp[i]);
+          if (now.begins(i) && a.dh0) put<float, L>(a.dh0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, d);
         }
       }
     }
     __syncwarp();
-    load(k + STAGES, slot);
-    if (more) {
-      d = get_state(mt, k + 1 & 1, cs, rank, carry);
-      now = next;
-      h = h1;
-    }
-    slot = slot1;
   }
   cp_async_wait_all();
 }
@@ -598,11 +794,11 @@ template <typename X, typename G, int V> __global__ void __launch_bounds__(256) 
 
 namespace {
 
-// The split of a call: parts of whole sequences and CTAs of a cluster, for two CTAs per SM.  Equal sequences go to
+// The split of a call: parts of whole sequences and CTAs of a cluster, for `ctas` of them.  Equal sequences go to
 // parts first, which exchange nothing; packed ones may be one long sequence and many short ones, so there the line is cut
 // within a cluster first.
-void split(const ScanArgs &a, int W, int sms, int &parts, int &cs) {
-  const int nb = (a.D + CB - 1) / CB, want = std::max(1, 2 * sms / nb);  // CTAs of a channel block
+void split(const ScanArgs &a, int W, int CB, int ctas, int &parts, int &cs) {
+  const int nb = (a.D + CB - 1) / CB, want = std::max(1, ctas / nb);  // CTAs of a channel block
   const auto clustered = [&](int most, long long tokens) {
     return (int)std::max(1ll, std::min({(long long)most, (long long)MAXC, tokens / (W * SEG)}));
   };
@@ -616,15 +812,17 @@ void split(const ScanArgs &a, int W, int sms, int &parts, int &cs) {
   parts = std::min(parts, 65535);
 }
 
-template <int W, typename... KArgs>
-cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int sms, int row_bytes, cudaStream_t st) {
-  const size_t smem = (size_t)W * STAGES * SEG * CB * row_bytes;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+// ring: bytes of a warp's stages
+template <int W, int NP, typename... KArgs>
+cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int ctas, int ring, cudaStream_t st) {
+  constexpr int SLOT = sizeof(MapSlot<NP>);
   int parts, cs;
-  split(a, W, sms, parts, cs);
+  split(a, W, 64 * NP, ctas, parts, cs);
+  const int smem = W * ring + 2 * (W + (cs > 1 ? cs : 0)) * SLOT;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W * ring + 2 * (W + MAXC) * SLOT);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, (a.D + CB - 1) / CB, parts);
+  cfg.gridDim = dim3(cs, (a.D + 64 * NP - 1) / (64 * NP), parts);
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -638,10 +836,29 @@ cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int sms, in
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
+// What a CTA of W warps takes, and how many of them share an SM.  The forward has as many warps as leave room for two CTAs.
+template <typename X, typename G, bool BWD> struct Room {
+  static constexpr int row = SEG * 64, SLOT = sizeof(MapSlot<1>), X_ = sizeof(X), G_ = sizeof(G);
+  static constexpr int ring = BWD ? 2 * row * (X_ + G_) + row * X_ : 3 * row * (X_ + G_);
+  static constexpr int fwd_warps = (227 * 1024 / 2 - 1024 - 8 * SLOT) / (ring + 2 * SLOT);
+  static constexpr int fit(int W) { return 227 * 1024 / (W * ring + 2 * (W + MAXC) * SLOT + 1100); }
+  static constexpr int regs(int W) { return 512 / (32 * W); }  // at 128 of a thread
+  static constexpr int limit(int W) { return std::max(1, std::min(fit(W), regs(W))); }
+};
+template <typename X, typename G, int M, int W> cudaError_t launch_bwd(const ScanArgs &a, int sms, cudaStream_t st) {
+  typedef Room<X, G, true> R;
+  return launch_clustered<W, 1>(scan_bwd_kernel<X, G, M, W, 1, R::limit(W)>, a, R::limit(W) * sms, R::ring, st);
+}
 template <typename X, typename G, int M> cudaError_t launch_move(const ScanArgs &a, bool bwd, int sms, cudaStream_t st) {
-  constexpr int F = sizeof(X) + sizeof(G) == 4 ? 8 : 4, B = sizeof(X) == 2 ? 4 : 2;  // warps, so that two CTAs' stages fit an SM
-  if (bwd) return launch_clustered<B>(scan_bwd_kernel<X, G, M, B>, a, sms, 2 * sizeof(X) + sizeof(G), st);
-  return launch_clustered<F>(scan_fwd_kernel<X, G, M, F>, a, sms, sizeof(X) + sizeof(G), st);
+  if (!bwd) {
+    typedef Room<X, G, false> R;
+    return launch_clustered<R::fwd_warps, 1>(scan_fwd_kernel<X, G, M, R::fwd_warps, 1>, a, 2 * sms, R::ring, st);
+  }
+  // Four warps to a CTA, and several CTAs to an SM; as many as fit one where not even clusters of eight reach two SMs in three
+  // (a sequence of 65536 tokens and 64 channels: 8 CTAs).
+  const long long most = (long long)((a.D + 63) / 64) * MAXC * (a.cu ? 1 : a.N);
+  if (3 * most < 2 * sms) return launch_bwd<X, G, M, sizeof(X) == 2 ? 12 : 8>(a, sms, st);
+  return launch_bwd<X, G, M, 4>(a, sms, st);
 }
 template <typename X, typename G> cudaError_t launch_types(const ScanArgs &a, int move, bool bwd, int sms, cudaStream_t st) {
   if (move == 16) return launch_move<X, G, M16>(a, bwd, sms, st);
