@@ -3,7 +3,10 @@
 // backward, with d_t the gradient that reaches h_t:
 //   d_t = dy_t + exp(g_{t+1}) d_{t+1},  dx_t = d_t,  dg_t = exp(g_t) d_t h_{t-1},  dh0 = exp(g_0) d_0.
 //
-// Bound by bytes: x and g are read once and y is written once; the backward reads dy, x and g and writes dx and dg.
+// Bound by bytes: x and g are read once and y is written once; the backward reads dy, x and g and writes dx and dg.  What keeps
+// it from the rate of a copy is the chain of rounds below: 4 x 4096 tokens of 2048 channels take 52 us forward (3.9 TB/s; a
+// kernel that only copies with these accesses 37 us) and 78 us backward (4.3 TB/s) in bf16, 50 and 72 us with half the tokens in
+// fp32; one sequence of 65536 tokens and 64 channels, which eight CTAs share, 126 and 150 us.
 //
 // All sequences stand in one line of tokens, cut into segments of SEG = 16 tokens at multiples of 16.  A warp holds a
 // segment of CB = 64 channels, two per lane: it runs the recurrence from zero, which gives the segment's map
@@ -30,89 +33,107 @@ namespace gdn {
 
 namespace {
 
-constexpr int SEG = SCAN_SEG, MAXC = 8;  // MAXC: CTAs of a cluster
+constexpr int SEG = SCAN_SEG, CB = 64, MAXC = 8;  // tokens of a segment, channels of a block, CTAs of a cluster
 
-// what moves rows: 16-byte pieces, 4-byte pieces, or single bf16 elements
-enum Move { M16, M4, M2 };
-// A lane holds NP pairs of a block's 64 NP channels: neighbours, or pairs 64 apart, or single channels 32 apart, as accesses allow.
-enum Lay { NEXT, PAIRS, SINGLE };
-template <typename X, int M> constexpr int LAY = M == M16 ? NEXT : (M == M4 && sizeof(X) == 2 ? PAIRS : SINGLE);
-template <int L, int NP> __device__ __forceinline__ int first_channel(int lane) {
-  return L == NEXT ? 2 * NP * lane : (L == PAIRS ? 2 * lane : lane);
+// What brings rows: 16-byte copies of rows that begin on 16-byte boundaries; 4-byte copies of bf16 pairs; 16-byte copies
+// of the aligned pieces that hold a row that begins anywhere (4 x 4096 tokens, 1001 channels: bf16 forward 48 us and backward
+// 95, with plain loads of single values 89 and 132; 32749 packed fp32 tokens 134 us, with 4-byte copies 163).  Pairs keep the
+// 4-byte copies where they can, for the stores of pairs that go with them (1002 channels: backward 71 us, 1001: 95).
+enum Move { M16, M4, ANY };
+// Of a block's channels a lane has two neighbours, or two that lie 32 apart where rows begin anywhere.
+template <int M> constexpr bool PAIR = M != ANY;
+template <bool P> __device__ __forceinline__ int first_channel(int lane) { return P ? 2 * lane : lane; }
+
+// a lane's two values
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float a, float b) { return {pk(a, b)}; }
+__device__ __forceinline__ float2 floats(const Two &x) {
+  float2 f;
+  upk(x.v, f.x, f.y);
+  return f;
 }
+__device__ __forceinline__ Two operator+(const Two &a, const Two &b) { return {add2(a.v, b.v)}; }
+__device__ __forceinline__ Two operator*(const Two &a, const Two &b) { return {mul2(a.v, b.v)}; }
+__device__ __forceinline__ Two fma(const Two &a, const Two &b, const Two &c) { return {fma2(a.v, b.v, c.v)}; }
 
-// a lane's values
-template <int NP> struct Vals {
-  uint64_t v[NP];
-  __device__ __forceinline__ float2 pair(int i) const {
-    float2 f;
-    upk(v[i], f.x, f.y);
-    return f;
+// 16 bytes to shared memory, of which the first n are read and the others are zeros
+__device__ __forceinline__ void copy16(void *smem, const void *gmem, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(smem)), "l"(gmem), "r"(n));
+}
+// A segment's rows in shared memory, [SEG][PITCH].  With ANY, row i begins up to 15 bytes into its place, as far behind a
+// 16-byte boundary as in global memory.
+template <typename E, int M> struct Tile {
+  static constexpr int A = 16 / (int)sizeof(E), PITCH = CB + (M == ANY ? A : 0), BYTES = SEG * PITCH * (int)sizeof(E);
+  const E *p;
+  unsigned first, row;  // where row 0 begins, how much further the next one does
+  __device__ __forceinline__ Two at(int i) const {
+    const int lane = threadIdx.x & 31;
+    const E *r = p + i * PITCH;
+    if constexpr (M == ANY) {
+      r += (first + i * row) & (A - 1);
+      return two(tof(r[lane]), tof(r[lane + 32]));
+    } else if constexpr (sizeof(E) == 2) {
+      const uint32_t u = *reinterpret_cast<const uint32_t *>(r + 2 * lane);
+      return two(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+      return {*reinterpret_cast<const uint64_t *>(r + 2 * lane)};
+    }
   }
 };
-template <int NP> __device__ __forceinline__ Vals<NP> operator+(Vals<NP> a, const Vals<NP> &b) {
-#pragma unroll
-  for (int i = 0; i < NP; ++i) a.v[i] = add2(a.v[i], b.v[i]);
-  return a;
-}
-template <int NP> __device__ __forceinline__ Vals<NP> operator*(Vals<NP> a, const Vals<NP> &b) {
-#pragma unroll
-  for (int i = 0; i < NP; ++i) a.v[i] = mul2(a.v[i], b.v[i]);
-  return a;
-}
-template <int NP> __device__ __forceinline__ Vals<NP> fma(Vals<NP> a, const Vals<NP> &b, const Vals<NP> &c) {
-#pragma unroll
-  for (int i = 0; i < NP; ++i) a.v[i] = fma2(a.v[i], b.v[i], c.v[i]);
-  return a;
-}
-__device__ __forceinline__ uint64_t wide(uint32_t u) { return pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
-
-// Rows of segments on their way to shared memory, [SEG][CB]: zeros outside [lo, hi) x [0, D).  The lane's place in the row and the
+// Brings rows of segments, zeros outside [lo, hi).  (What is past D is never looked at.)  The lane's place in a row and the
 // first of its rows stay the same; `at` moves with the segments.
-template <typename E, int M, int CB> struct Loader {
-  static constexpr int B = M == M16 ? 16 : (M == M4 ? 4 : 2), V = B / (int)sizeof(E) > 0 ? B / (int)sizeof(E) : 1;
-  static constexpr int PER = CB / V, RPI = PER < 32 ? 32 / PER : 1, CPI = PER < 32 ? PER : 32;  // pieces of a row; rows, pieces of an instruction
-  const E *src, *at;  // at: of the segment asked for next, the lane's first row
+template <typename E, int M> struct Loader {
+  typedef Tile<E, M> T;
+  static constexpr int V = M == M4 ? 2 : T::A, PER = CB / V;  // values of a piece, pieces of a row
+  const E *src, *at;  // at: of the segment asked for next, the lane's first piece (ANY: the block's first channel of row 0)
   long long row, step;
   // s: the first segment; per: how far the next one lies
   __device__ __forceinline__ void init(const void *p, long long stride, int c0, long long s, long long per) {
     const int lane = threadIdx.x & 31;
     src = static_cast<const E *>(p);
     row = stride;
-    at = src + (s * SEG + lane / CPI) * row + c0 + lane % CPI * V;
+    at = src + s * SEG * row + c0 + (M == ANY ? 0 : lane / PER * row + lane % PER * V);
     step = per * SEG * row;
   }
-  __device__ __forceinline__ void load(E *dst, int t0, int lo, int hi, int c0, int D) {
-    const int lane = threadIdx.x & 31, r0 = lane / CPI, c = lane % CPI * V;
-    const bool inside = t0 >= lo && t0 + SEG <= hi;
-    E *d = dst + r0 * CB + c;
+  __device__ __forceinline__ T tile(const void *place, int t0, int c0) const {
+    const unsigned base = (unsigned)(reinterpret_cast<uintptr_t>(src) / sizeof(E)) + c0;
+    return {static_cast<const E *>(place), base + (unsigned)t0 * (unsigned)row, (unsigned)row};
+  }
+  __device__ __forceinline__ void load(void *place, int t0, int lo, int hi, int c0, int D) {
+    const int lane = threadIdx.x & 31;
+    E *dst = static_cast<E *>(place);
+    if constexpr (M == ANY) {
+      constexpr int C = PER + 1;  // pieces that a row may reach into; none lacks a byte of the row, so none leaves its allocation
+      const int bytes = min(CB, D - c0) * (int)sizeof(E);
 #pragma unroll
-    for (int k = 0; k < PER / CPI; ++k) {
-      const E *s = at + 32 * k * V;
-      const bool there = c0 + c + 32 * k * V < D;
-      if constexpr (M == M2) {
-#pragma unroll 4
-        for (int i = 0; i < SEG; ++i, s += row) {
-          E v = fromf<E>(0.f);
-          if (there && t0 + i >= lo && t0 + i < hi) v = *s;
-          d[i * CB + 32 * k] = v;
-        }
-      } else {
-        auto copy = [](E *d, const E *s, bool ok) {
-          if constexpr (M == M16) cp_async16(d, s, ok);
-          else cp_async4(d, s, ok);
-        };
-        if (inside) {
-          if (there) {  // what is past D is never looked at
+      for (int k = 0; k < (SEG * C + 31) / 32; ++k) {
+        const int i = k * 32 + lane, r = i / C, q = i - r * C;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(at + r * row);
+        const int off = 16 * q - (int)(b & 15);  // the piece's place in the row
+        const int n = t0 + r >= lo && t0 + r < hi ? max(min(16, bytes - off), 0) : 0;  // no byte behind the row's last
+        if (r < SEG) copy16(dst + r * T::PITCH + q * T::A, reinterpret_cast<const void *>(n ? b + off : reinterpret_cast<uintptr_t>(src) & ~(uintptr_t)15), n);
+      }
+    } else {
+      constexpr int RPI = 32 / PER;  // rows of an instruction
+      const int r0 = lane / PER, c = lane % PER * V;
+      E *d = dst + r0 * T::PITCH + c;
+      const E *s = at;
+      auto copy = [](E *d, const E *s, bool ok) {
+        if constexpr (M == M16) copy16(d, s, ok ? 16 : 0);
+        else cp_async4(d, s, ok);
+      };
+      if (c0 + c < D) {
+        if (t0 >= lo && t0 + SEG <= hi) {
 #pragma unroll
-            for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) copy(d + i * RPI * CB + 32 * k * V, s, true);
-          }
+          for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) copy(d + i * RPI * T::PITCH, s, true);
         } else {
-          const unsigned span = there ? hi - lo : 0, rel = t0 + r0 - lo;
+          const unsigned span = hi - lo, rel = t0 + r0 - lo;
 #pragma unroll 1
           for (int i = 0; i < SEG / RPI; ++i, s += RPI * row) {
             const bool ok = rel + i * RPI < span;
-            copy(d + i * RPI * CB + 32 * k * V, ok ? s : src, ok);
+            copy(d + i * RPI * T::PITCH, ok ? s : src, ok);
           }
         }
       }
@@ -120,90 +141,35 @@ template <typename E, int M, int CB> struct Loader {
     at += step;
   }
 };
-// the lane's values of a row in shared memory
-template <typename E, int L, int NP> __device__ __forceinline__ Vals<NP> get(const E *row, int lane) {
-  Vals<NP> x;
-  if constexpr (L == NEXT && 2 * NP * sizeof(E) == 8) {
-    const uint64_t u = *reinterpret_cast<const uint64_t *>(row + 2 * NP * lane);
-    if constexpr (NP == 1) {
-      x.v[0] = u;
-    } else {
-      x.v[0] = wide((uint32_t)u);
-      x.v[NP - 1] = wide((uint32_t)(u >> 32));
-    }
-  } else if constexpr (L == SINGLE) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) x.v[i] = pk(tof(row[lane + 64 * i]), tof(row[lane + 64 * i + 32]));
-  } else {
-    static_assert(sizeof(E) == 2 && (L == PAIRS || NP == 1), "pairs of bf16");
-#pragma unroll
-    for (int i = 0; i < NP; ++i) x.v[i] = wide(*reinterpret_cast<const uint32_t *>(row + 2 * lane + 64 * i));
-  }
-  return x;
-}
 // Gates of a row.  With bf16 rows the product with log2(e) and ex2.approx, off by 2^-22 of themselves, which a bf16 result does
 // not show and which the state carries for 16 tokens at most (its map takes expf of the sum); expf in fp32, where 16 such
 // errors would be half of all.
-template <bool EXACT> __device__ __forceinline__ uint64_t gates2(uint64_t g) {
-  float a, b;
+template <bool EXACT> __device__ __forceinline__ Two gates(const Two &g) {
+  float2 f;
   if constexpr (EXACT) {
-    upk(g, a, b);
-    return pk(expf(a), expf(b));
+    f = floats(g);
+    return two(expf(f.x), expf(f.y));
   } else {
-    upk(mul2(g, pk(1.4426950408889634f, 1.4426950408889634f)), a, b);
-    asm("ex2.approx.ftz.f32 %0, %0;\n" : "+f"(a));
-    asm("ex2.approx.ftz.f32 %0, %0;\n" : "+f"(b));
-    return pk(a, b);
+    f = floats(g * two(1.4426950408889634f, 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %0;\n" : "+f"(f.x));
+    asm("ex2.approx.ftz.f32 %0, %0;\n" : "+f"(f.y));
+    return two(f.x, f.y);
   }
-}
-template <bool EXACT, int NP> __device__ __forceinline__ Vals<NP> gates(Vals<NP> g) {
-#pragma unroll
-  for (int i = 0; i < NP; ++i) g.v[i] = gates2<EXACT>(g.v[i]);
-  return g;
 }
 
 // a row in global memory: the lane's channels, of which c is the first; only those below D exist
-template <typename E, int L, int NP> __device__ __forceinline__ void put(E *row, int c, int D, const Vals<NP> &x) {
-  row += c;
-  if constexpr (L == NEXT && NP == 2) {
-    if (c >= D) return;
-    const float2 f = x.pair(0), g = x.pair(1);
-    if constexpr (sizeof(E) == 2) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y), q = __floats2bfloat162_rn(g.x, g.y);
-      *reinterpret_cast<uint2 *>(row) = make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
-    } else {
-      *reinterpret_cast<float4 *>(row) = make_float4(f.x, f.y, g.x, g.y);
-    }
+template <bool P, typename E> __device__ __forceinline__ void put(E *row, int c, int D, const Two &x) {
+  const float2 f = floats(x);
+  if constexpr (P) {
+    if (c < D) st2(row + c, f.x, f.y);
   } else {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const float2 f = x.pair(i);
-      if constexpr (L == SINGLE) {
-        if (c + 64 * i < D) row[64 * i] = fromf<E>(f.x);
-        if (c + 64 * i + 32 < D) row[64 * i + 32] = fromf<E>(f.y);
-      } else if (c + 64 * i < D) {
-        st2(row + 64 * i, f.x, f.y);
-      }
-    }
+    if (c < D) row[c] = fromf<E>(f.x);
+    if (c + 32 < D) row[c + 32] = fromf<E>(f.y);
   }
 }
-template <int L, int NP> __device__ __forceinline__ Vals<NP> take(const float *row, int c, int D) {
-  Vals<NP> x = {};
-  row += c;
-  if constexpr (L == NEXT && NP == 2) {
-    if (c < D) {
-      const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
-      x.v[0] = u.x;
-      x.v[1] = u.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      if constexpr (L == SINGLE) x.v[i] = pk(c + 64 * i < D ? row[64 * i] : 0.f, c + 64 * i + 32 < D ? row[64 * i + 32] : 0.f);
-      else if (c + 64 * i < D) x.v[i] = *reinterpret_cast<const uint64_t *>(row + 64 * i);
-    }
-  }
-  return x;
+template <bool P> __device__ __forceinline__ Two take(const float *row, int c, int D) {
+  if constexpr (P) return c < D ? Two{*reinterpret_cast<const uint64_t *>(row + c)} : Two{};
+  else return two(c < D ? row[c] : 0.f, c + 32 < D ? row[c + 32] : 0.f);
 }
 
 // ------------------------------------------------------------------ where sequences begin
@@ -290,49 +256,27 @@ struct Bounds {
 
 // ------------------------------------------------------------------ maps of segments
 // c -> A c + H; A < 0 marks one that forgets c (whatever c holds, an infinity among it)
-template <int NP> struct Map {
-  float A[2 * NP], H[2 * NP];
-  __device__ __forceinline__ void of(float (&c)[2 * NP]) const {
-#pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) c[i] = A[i] < 0.f ? H[i] : fmaf(A[i], c[i], H[i]);
-  }
+struct Map {
+  float2 A, H;
+  static __device__ __forceinline__ float one(float A, float H, float c) { return A < 0.f ? H : fmaf(A, c, H); }
+  static __device__ __forceinline__ float both(float A, float B) { return A < 0.f || B < 0.f ? -1.f : A * B; }
+  __device__ __forceinline__ float2 of(const float2 &c) const { return make_float2(one(A.x, H.x, c.x), one(A.y, H.y, c.y)); }
   __device__ __forceinline__ void then(const Map &n) {  // this one first, then n
-    n.of(H);
-#pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) A[i] = n.A[i] < 0.f || A[i] < 0.f ? -1.f : A[i] * n.A[i];
+    H = n.of(H);
+    A = make_float2(both(A.x, n.A.x), both(A.y, n.A.y));
   }
 };
 // of a segment: the sum of its log-gates and its result from zero
-template <int NP> __device__ __forceinline__ Map<NP> segment_map(bool fresh, const Vals<NP> &sum, const Vals<NP> &h) {
-  Map<NP> m;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const float2 s = sum.pair(i), z = h.pair(i);
-    m.A[2 * i] = fresh ? -1.f : expf(s.x);
-    m.A[2 * i + 1] = fresh ? -1.f : expf(s.y);
-    m.H[2 * i] = z.x;
-    m.H[2 * i + 1] = z.y;
-  }
-  return m;
+__device__ __forceinline__ Map segment_map(bool fresh, const Two &sum, const Two &h) {
+  const float2 s = floats(sum);
+  return {fresh ? make_float2(-1.f, -1.f) : make_float2(expf(s.x), expf(s.y)), floats(h)};
 }
-// a map in shared memory: 16-byte pieces of every lane
-template <int NP> struct MapSlot {
-  float4 p[NP][32];
-};
-template <int NP> __device__ __forceinline__ float4 piece_of(const Map<NP> &m, int i) {
-  return make_float4(m.A[2 * i], m.A[2 * i + 1], m.H[2 * i], m.H[2 * i + 1]);
-}
-template <int NP> __device__ __forceinline__ Map<NP> map_at(const MapSlot<NP> &s) {
-  Map<NP> m;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const float4 v = s.p[i][threadIdx.x & 31];
-    m.A[2 * i] = v.x;
-    m.A[2 * i + 1] = v.y;
-    m.H[2 * i] = v.z;
-    m.H[2 * i + 1] = v.w;
-  }
-  return m;
+// a map in shared memory, 16 bytes of every lane
+typedef float4 MapSlot[32];
+__device__ __forceinline__ float4 packed(const Map &m) { return make_float4(m.A.x, m.A.y, m.H.x, m.H.y); }
+__device__ __forceinline__ Map map_at(const MapSlot &s) {
+  const float4 v = s[threadIdx.x & 31];
+  return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
@@ -374,13 +318,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
 // CTAs, where an mbarrier counts its bytes.  (A cluster barrier instead makes the warp that releases its maps by it wait
 // for its own global stores too.)  Two sets of maps by the round's parity: a CTA sends round r + 2
 // only when it has everyone's maps of round r + 1, which come after their reading of round r.
-template <int W, int NP> struct Meet {
-  typedef MapSlot<NP> Slot;
-  Slot *warp, *peer;  // [2][W], [2][cs]
-  uint64_t *bar;      // [2]
+template <int W> struct Meet {
+  MapSlot *warp, *peer;  // [2][W], [2][cs]
+  uint64_t *bar;         // [2]
   int cs, rank;
   __device__ __forceinline__ void init(uint8_t *smem, uint64_t *bars) {
-    warp = reinterpret_cast<Slot *>(smem);
+    warp = reinterpret_cast<MapSlot *>(smem);
     peer = warp + 2 * W;
     bar = bars;
     cs = gridDim.x;
@@ -396,79 +339,64 @@ template <int W, int NP> struct Meet {
   __device__ __forceinline__ void ready() const {
     if (cs > 1) cluster_wait();
   }
-  __device__ __forceinline__ void hand_in(int round, const Map<NP> &mine) const {
+  __device__ __forceinline__ void hand_in(int round, const Map &mine) const {
     const int me = threadIdx.x >> 5, lane = threadIdx.x & 31, par = round & 1;
-    Slot *mw = warp + par * W;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) mw[me].p[i][lane] = piece_of(mine, i);
+    MapSlot *mw = warp + par * W;
+    mw[me][lane] = packed(mine);
     __syncthreads();
     if (cs == 1) return;
-    if (threadIdx.x == 0) bar_expect(smem_u32(bar + par), cs * sizeof(Slot));
+    if (threadIdx.x == 0) bar_expect(smem_u32(bar + par), cs * sizeof(MapSlot));
     if (me >= cs) return;
-    Map<NP> all = map_at(mw[0]);
+    Map all = map_at(mw[0]);
 #pragma unroll
     for (int j = 1; j < W; ++j) all.then(map_at(mw[j]));
-    const uint32_t at = smem_u32(&peer[par * cs + rank].p[0][lane]), b = smem_u32(bar + par);
+    const uint32_t at = smem_u32(&peer[par * cs + rank][lane]), b = smem_u32(bar + par);
 #pragma unroll 1
-    for (int r = me; r < cs; r += W) {
-      const uint32_t ra = peer_addr(at, r), rb = peer_addr(b, r);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) store_peer(ra + 512 * i, rb, piece_of(all, i));
-    }
+    for (int r = me; r < cs; r += W) store_peer(peer_addr(at, r), peer_addr(b, r), packed(all));
   }
-  __device__ __forceinline__ Vals<NP> state(int round, float (&carry)[2 * NP]) const {
+  __device__ __forceinline__ Two state(int round, float2 &carry) const {
     const int me = threadIdx.x >> 5, par = round & 1;
-    const Slot *mw = warp + par * W, *mp = peer + par * cs;
-    float in[2 * NP];
-    auto keep = [&] {
-#pragma unroll
-      for (int i = 0; i < 2 * NP; ++i) in[i] = carry[i];
-    };
-    keep();
+    const MapSlot *mw = warp + par * W, *mp = peer + par * cs;
+    float2 in = carry;
     if (cs == 1) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        if (j == me) keep();
-        map_at(mw[j]).of(carry);
+        if (j == me) in = carry;
+        carry = map_at(mw[j]).of(carry);
       }
     } else {
-      if (!bar_wait(smem_u32(bar + par), round >> 1 & 1)) {
-#pragma unroll
-        for (int i = 0; i < 2 * NP; ++i) carry[i] = __uint_as_float(0x7fffffffu);  // what follows is not reliable, and shows it
-      }
+      if (!bar_wait(smem_u32(bar + par), round >> 1 & 1))  // what follows is not reliable, and shows it
+        carry.x = carry.y = __uint_as_float(0x7fffffffu);
 #pragma unroll
       for (int b = 0; b < MAXC; b += 4) {
         if (b >= cs) break;
-        Map<NP> m[4];
+        Map m[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) m[j] = map_at(mp[min(b + j, cs - 1)]);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (b + j < cs) {
-            if (b + j == rank) keep();
-            m[j].of(carry);
+            if (b + j == rank) in = carry;
+            carry = m[j].of(carry);
           }
       }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
-        if (j < me) map_at(mw[j]).of(in);
+        if (j < me) in = map_at(mw[j]).of(in);
     }
-    Vals<NP> h;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) h.v[i] = pk(in[2 * i], in[2 * i + 1]);
-    return h;
+    return two(in.x, in.y);
   }
 };
 
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
 // the state of sequences without tokens passes through: out[n] = in[n], shared out among a channel block's CTAs
-template <int L, int NP, int W>
+template <bool P, int W>
 __device__ __forceinline__ void pass_empty(const ScanArgs &a, const float *in, float *out, int c, int ctas, int cta) {
   if (!a.cu || !out) return;
   for (int n = cta * W + (threadIdx.x >> 5); n < a.N; n += ctas * W) {
     if (a.cu[n + 1] > a.cu[n]) continue;
-    put<float, L>(out + (long long)n * a.D, c, a.D, in ? take<L, NP>(in + (long long)n * a.D, c, a.D) : Vals<NP>{});
+    put<P>(out + (long long)n * a.D, c, a.D, in ? take<P>(in + (long long)n * a.D, c, a.D) : Two{});
   }
 }
 
@@ -515,34 +443,31 @@ struct Piece {
 
 // grid: CTAs of a cluster, channel blocks, parts.  Each step hands in the maps of round k + 1 and, while the CTAs of the cluster
 // meet, finishes round k, whose states are known; the stages of round k + 2 are on their way.
-template <typename X, typename G, int M, int W, int NP>
+template <typename X, typename G, int M, int W>
 __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
-  constexpr int L = LAY<X, M>, CB = 64 * NP;
-  typedef Vals<NP> V;
-  constexpr bool EXACT = sizeof(X) == 4;
-  static_assert(L == LAY<G, M>, "one layout of channels");
+  constexpr bool P = PAIR<M>, EXACT = sizeof(X) == 4;
   extern __shared__ __align__(16) uint8_t raw[];
-  constexpr int BX = SEG * CB * sizeof(X), ST = BX + SEG * CB * sizeof(G);
+  constexpr int BX = Tile<X, M>::BYTES, ST = BX + Tile<G, M>::BYTES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + first_channel<L, NP>(lane);
+  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + first_channel<P>(lane);
   uint8_t *ring = raw + warp * (3 * ST);
   __shared__ uint64_t bars[2];
-  Meet<W, NP> mt;
+  Meet<W> mt;
   mt.init(raw + W * 3 * ST, bars);
   pdl_trigger();
   pdl_wait();
   Walk w = {};
   w.init<W>(a, cs, rank);
-  Loader<X, M, CB> lx;
-  Loader<G, M, CB> lg;
+  Loader<X, M> lx;
+  Loader<G, M> lg;
   lx.init(a.x, a.x_row, c0, w.up(0), w.per);
   lg.init(a.g, a.g_row, c0, w.up(0), w.per);
   auto load = [&](int k, int slot) {
     if (k < w.rounds && w.has(w.up(k))) {
       uint8_t *st = ring + slot * ST;
       const int t0 = w.up(k) * SEG;
-      lx.load(reinterpret_cast<X *>(st), t0, w.lo, w.hi, c0, a.D);
-      lg.load(reinterpret_cast<G *>(st + BX), t0, w.lo, w.hi, c0, a.D);
+      lx.load(st, t0, w.lo, w.hi, c0, a.D);
+      lg.load(st + BX, t0, w.lo, w.hi, c0, a.D);
     }
     cp_async_commit();
   };
@@ -550,13 +475,11 @@ __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
   for (int k = 0; k < 2; ++k) load(k, k);
   Piece now = {}, next = {};
   next.bd.init(a, w.up(0) * SEG);
-  pass_empty<L, NP, W>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  pass_empty<P, W>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
   mt.ready();
-  auto x_of = [&](const uint8_t *st, int i) { return get<X, L, NP>(reinterpret_cast<const X *>(st) + i * CB, lane); };
-  auto g_of = [&](const uint8_t *st, int i) { return get<G, L, NP>(reinterpret_cast<const G *>(st + BX) + i * CB, lane); };
-  auto start = [&](const Piece &p, int i) { return a.h0 ? take<L, NP>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : V{}; };
-  float carry[2 * NP] = {};
-  V h = {};
+  auto start = [&](const Piece &p, int i) { return a.h0 ? take<P>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : Two{}; };
+  float2 carry = make_float2(0.f, 0.f);
+  Two h = {};
   int slot = 2;  // of round k
 #pragma unroll 1
   for (int k = -1; k < w.rounds; ++k) {
@@ -566,48 +489,50 @@ __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
       next.look(a, w, w.up(k + 1));
       cp_wait<1>();
       __syncwarp();
-      const uint8_t *st = ring + slot1 * ST;
-      V sum = {}, z = {};
+      const Tile<X, M> x = lx.tile(ring + slot1 * ST, next.t0, c0);
+      const Tile<G, M> g = lg.tile(ring + slot1 * ST + BX, next.t0, c0);
+      Two sum = {}, z = {};
       bool fresh = false;
       if (next.plain) {
 #pragma unroll
         for (int i = 0; i < SEG; ++i) {
-          const V g = g_of(st, i);
-          sum = sum + g;
-          z = fma(gates<EXACT>(g), z, x_of(st, i));
+          const Two gi = g.at(i);
+          sum = sum + gi;
+          z = fma(gates<EXACT>(gi), z, x.at(i));
         }
       } else if (next.live) {
 #pragma unroll 1
         for (int i = 0; i < SEG; ++i) {
-          const V g = g_of(st, i);
+          const Two gi = g.at(i);
           if (next.begins(i) && next.inside(w, i)) {
             z = start(next, i);
             fresh = true;
           }
-          sum = sum + g;
-          z = fma(gates<EXACT>(g), z, x_of(st, i));
+          sum = sum + gi;
+          z = fma(gates<EXACT>(gi), z, x.at(i));
         }
       }
       mt.hand_in(k + 1, segment_map(fresh, sum, z));
     }
     if (k >= 0 && now.live) {
-      const uint8_t *st = ring + slot * ST;
-      if (a.states && now.t0 >= w.lo) put<float, L>(a.states + (long long)now.seg * a.D, c, a.D, h);
+      const Tile<X, M> x = lx.tile(ring + slot * ST, now.t0, c0);
+      const Tile<G, M> g = lg.tile(ring + slot * ST + BX, now.t0, c0);
+      if (a.states && now.t0 >= w.lo) put<P>(a.states + (long long)now.seg * a.D, c, a.D, h);
       X *yr = static_cast<X *>(a.y) + (long long)now.t0 * a.y_row;
       if (now.plain) {
 #pragma unroll
         for (int i = 0; i < SEG; ++i, yr += a.y_row) {
-          h = fma(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
-          put<X, L>(yr, c, a.D, h);
+          h = fma(gates<EXACT>(g.at(i)), h, x.at(i));
+          put<P>(yr, c, a.D, h);
         }
       } else {
 #pragma unroll 1
         for (int i = 0; i < SEG; ++i, yr += a.y_row) {
           if (!now.inside(w, i)) continue;
           if (now.begins(i)) h = start(now, i);
-          h = fma(gates<EXACT>(g_of(st, i)), h, x_of(st, i));
-          put<X, L>(yr, c, a.D, h);
-          if (now.ends(i) && a.hT) put<float, L>(a.hT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, h);
+          h = fma(gates<EXACT>(g.at(i)), h, x.at(i));
+          put<P>(yr, c, a.D, h);
+          if (now.ends(i) && a.hT) put<P>(a.hT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, h);
         }
       }
     }
@@ -625,26 +550,24 @@ __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
 // The same walk from the part's end, a round at a time: with more CTAs to an SM instead of a round ahead it is faster (4 x 4096
 // tokens of 2048 channels 80 us instead of 89), since the states before all tokens of a segment take the registers that the
 // round ahead needs.  Two stages of dy and g; x is needed after the exchange only, and has one.  LIMIT: CTAs per SM.
-template <typename X, typename G, int M, int W, int NP, int LIMIT>
+template <typename X, typename G, int M, int W, int LIMIT>
 __global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
-  constexpr int L = LAY<X, M>, CB = 64 * NP;
-  typedef Vals<NP> V;
-  constexpr bool EXACT = sizeof(X) == 4;
+  constexpr bool P = PAIR<M>, EXACT = sizeof(X) == 4;
   extern __shared__ __align__(16) uint8_t raw[];
   __shared__ uint64_t bars[2];
-  constexpr int BX = SEG * CB * sizeof(X), ST = BX + SEG * CB * sizeof(G);
+  constexpr int BX = Tile<X, M>::BYTES, ST = BX + Tile<G, M>::BYTES;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + first_channel<L, NP>(lane);
+  const int cs = gridDim.x, rank = blockIdx.x, c0 = blockIdx.y * CB, c = c0 + first_channel<P>(lane);
   uint8_t *ring = raw + warp * (2 * ST + BX);
-  X *sx = reinterpret_cast<X *>(ring + 2 * ST);
-  Meet<W, NP> mt;
+  uint8_t *sx = ring + 2 * ST;
+  Meet<W> mt;
   mt.init(raw + W * (2 * ST + BX), bars);
   pdl_trigger();
   pdl_wait();
   Walk w = {};
   w.init<W>(a, cs, rank);
-  Loader<X, M, CB> lx, ld;
-  Loader<G, M, CB> lg;
+  Loader<X, M> lx, ld;
+  Loader<G, M> lg;
   lx.init(a.x, a.x_row, c0, w.down(0), -w.per);
   ld.init(a.dy, a.dy_row, c0, w.down(0), -w.per);
   lg.init(a.g, a.g_row, c0, w.down(0), -w.per);
@@ -652,52 +575,50 @@ __global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
     if (k < w.rounds && w.has(w.down(k))) {
       uint8_t *st = ring + (k & 1) * ST;
       const int t0 = w.down(k) * SEG;
-      ld.load(reinterpret_cast<X *>(st), t0, w.lo, w.hi, c0, a.D);
-      lg.load(reinterpret_cast<G *>(st + BX), t0, w.lo, w.hi, c0, a.D);
+      ld.load(st, t0, w.lo, w.hi, c0, a.D);
+      lg.load(st + BX, t0, w.lo, w.hi, c0, a.D);
     }
     cp_async_commit();
   };
   load(0);
   Piece now = {};
   now.bd.init(a, max(w.down(0) * SEG, 0));
-  pass_empty<L, NP, W>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  pass_empty<P, W>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
   mt.ready();
-  const uint8_t *st = ring;
-  auto x_of = [&](int i) { return get<X, L, NP>(sx + i * CB, lane); };
-  auto dy_of = [&](int i) { return get<X, L, NP>(reinterpret_cast<const X *>(st) + i * CB, lane); };
-  auto g_of = [&](int i) { return get<G, L, NP>(reinterpret_cast<const G *>(st + BX) + i * CB, lane); };
-  auto start = [&](int i) { return a.h0 ? take<L, NP>(a.h0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : V{}; };
-  auto at_end = [&](int i) { return a.dhT ? take<L, NP>(a.dhT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : V{}; };
-  float carry[2 * NP] = {};
+  auto start = [&](int i) { return a.h0 ? take<P>(a.h0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : Two{}; };
+  auto at_end = [&](int i) { return a.dhT ? take<P>(a.dhT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : Two{}; };
+  float2 carry = make_float2(0.f, 0.f);
 #pragma unroll 1
   for (int k = 0; k < w.rounds; ++k) {
-    st = ring + (k & 1) * ST;
     now.look(a, w, w.down(k));
+    const uint8_t *st = ring + (k & 1) * ST;
+    const Tile<X, M> x = lx.tile(sx, now.t0, c0), dy = ld.tile(st, now.t0, c0);
+    const Tile<G, M> g = lg.tile(st + BX, now.t0, c0);
     if (now.live) lx.load(sx, now.t0, w.lo, w.hi, c0, a.D);
     cp_async_commit();
     load(k + 1);
-    V h = now.live ? take<L, NP>(a.states + (long long)now.seg * a.D, c, a.D) : V{};
+    Two h = now.live ? take<P>(a.states + (long long)now.seg * a.D, c, a.D) : Two{};
     cp_wait<2>();
     __syncwarp();
-    V sum = {}, d = {};  // d: what reaches the state from later tokens
+    Two sum = {}, d = {};  // d: what reaches the state from later tokens
     bool fresh = false;
     if (now.plain) {
 #pragma unroll
       for (int i = SEG - 1; i >= 0; --i) {
-        const V g = g_of(i);
-        sum = sum + g;
-        d = gates<EXACT>(g) * (dy_of(i) + d);
+        const Two gi = g.at(i);
+        sum = sum + gi;
+        d = gates<EXACT>(gi) * (dy.at(i) + d);
       }
     } else if (now.live) {
 #pragma unroll 1
       for (int i = SEG - 1; i >= 0; --i) {
-        const V g = g_of(i);
+        const Two gi = g.at(i);
         if (now.ends(i) && now.inside(w, i)) {
           d = at_end(i);
           fresh = true;
         }
-        sum = sum + g;
-        d = gates<EXACT>(g) * (dy_of(i) + d);
+        sum = sum + gi;
+        d = gates<EXACT>(gi) * (dy.at(i) + d);
       }
     }
     mt.hand_in(k, segment_map(fresh, sum, d));
@@ -706,39 +627,39 @@ __global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
     X *dxr = static_cast<X *>(a.y) + (long long)(now.t0 + SEG - 1) * a.y_row;
     G *dgr = static_cast<G *>(a.dg) + (long long)(now.t0 + SEG - 1) * a.dg_row;
     if (now.plain) {
-      V hp[SEG];  // states before the tokens
+      Two hp[SEG];  // states before the tokens
 #pragma unroll
       for (int i = 0; i < SEG; ++i) {
         hp[i] = h;
-        h = fma(gates<EXACT>(g_of(i)), h, x_of(i));
+        h = fma(gates<EXACT>(g.at(i)), h, x.at(i));
       }
       d = mt.state(k, carry);
 #pragma unroll
       for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
-        const V dx = dy_of(i) + d;
-        d = gates<EXACT>(g_of(i)) * dx;
-        put<X, L>(dxr, c, a.D, dx);
-        put<G, L>(dgr, c, a.D, d * hp[i]);
+        const Two dx = dy.at(i) + d;
+        d = gates<EXACT>(g.at(i)) * dx;
+        put<P>(dxr, c, a.D, dx);
+        put<P>(dgr, c, a.D, d * hp[i]);
       }
     } else {
       d = mt.state(k, carry);
       if (now.live) {
-        V hp[SEG];  // in local memory
+        Two hp[SEG];  // in local memory
 #pragma unroll 1
         for (int i = 0; i < SEG; ++i) {
           if (now.begins(i) && now.inside(w, i)) h = start(i);
           hp[i] = h;
-          h = fma(gates<EXACT>(g_of(i)), h, x_of(i));
+          h = fma(gates<EXACT>(g.at(i)), h, x.at(i));
         }
 #pragma unroll 1
         for (int i = SEG - 1; i >= 0; --i, dxr -= a.y_row, dgr -= a.dg_row) {
           if (!now.inside(w, i)) continue;
           if (now.ends(i)) d = at_end(i);
-          const V dx = dy_of(i) + d;
-          d = gates<EXACT>(g_of(i)) * dx;
-          put<X, L>(dxr, c, a.D, dx);
-          put<G, L>(dgr, c, a.D, d * hp[i]);
-          if (now.begins(i) && a.dh0) put<float, L>(a.dh0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, d);
+          const Two dx = dy.at(i) + d;
+          d = gates<EXACT>(g.at(i)) * dx;
+          put<P>(dxr, c, a.D, dx);
+          put<P>(dgr, c, a.D, d * hp[i]);
+          if (now.begins(i) && a.dh0) put<P>(a.dh0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D, d);
         }
       }
     }
@@ -747,7 +668,7 @@ __global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
   cp_async_wait_all();
 }
 
-// One token of every sequence: state = exp(g) state + x, y = state.  V channels a thread.
+// One token of every sequence: state = exp(g) state + x, y = state.  Two channels a thread.
 template <typename X, typename G, int V> __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -796,11 +717,11 @@ namespace {
 
 // The split of a call: parts of whole sequences and CTAs of a cluster, for `ctas` of them.  Equal sequences go to
 // parts first, which exchange nothing; packed ones may be one long sequence and many short ones, so there the line is cut
-// within a cluster first.
-void split(const ScanArgs &a, int W, int CB, int ctas, int &parts, int &cs) {
+// within a cluster first.  peers: CTAs of a cluster at most.
+void split(const ScanArgs &a, int W, int ctas, int peers, int &parts, int &cs) {
   const int nb = (a.D + CB - 1) / CB, want = std::max(1, ctas / nb);  // CTAs of a channel block
   const auto clustered = [&](int most, long long tokens) {
-    return (int)std::max(1ll, std::min({(long long)most, (long long)MAXC, tokens / (W * SEG)}));
+    return (int)std::max(1ll, std::min({(long long)most, (long long)peers, tokens / (W * SEG)}));
   };
   if (!a.cu) {
     parts = std::min(a.N, want);
@@ -813,16 +734,16 @@ void split(const ScanArgs &a, int W, int CB, int ctas, int &parts, int &cs) {
 }
 
 // ring: bytes of a warp's stages
-template <int W, int NP, typename... KArgs>
-cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int ctas, int ring, cudaStream_t st) {
-  constexpr int SLOT = sizeof(MapSlot<NP>);
+template <int W, typename... KArgs>
+cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int ctas, int ring, int peers, cudaStream_t st) {
+  constexpr int SLOT = sizeof(MapSlot);
   int parts, cs;
-  split(a, W, 64 * NP, ctas, parts, cs);
+  split(a, W, ctas, peers, parts, cs);
   const int smem = W * ring + 2 * (W + (cs > 1 ? cs : 0)) * SLOT;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W * ring + 2 * (W + MAXC) * SLOT);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cs, (a.D + 64 * NP - 1) / (64 * NP), parts);
+  cfg.gridDim = dim3(cs, (a.D + CB - 1) / CB, parts);
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -836,38 +757,39 @@ cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int ctas, i
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
-// What a CTA of W warps takes, and how many of them share an SM.  The forward has as many warps as leave room for two CTAs.
-template <typename X, typename G, bool BWD> struct Room {
-  static constexpr int row = SEG * 64, SLOT = sizeof(MapSlot<1>), X_ = sizeof(X), G_ = sizeof(G);
-  static constexpr int ring = BWD ? 2 * row * (X_ + G_) + row * X_ : 3 * row * (X_ + G_);
-  static constexpr int fwd_warps = (227 * 1024 / 2 - 1024 - 8 * SLOT) / (ring + 2 * SLOT);
+constexpr int HALF_SM = 227 * 1024 / 2 - 1024;  // shared memory of one of two CTAs
+// What a CTA of W warps takes, and how many of them share an SM.  The forward has as many warps as leave
+// room for two CTAs, and as large clusters (fp32 rows that begin anywhere: 4 warps, clusters of 6).
+template <typename X, typename G, int M, bool BWD> struct Room {
+  static constexpr int SLOT = sizeof(MapSlot), BX = Tile<X, M>::BYTES, BG = Tile<G, M>::BYTES;
+  static constexpr int ring = BWD ? 2 * (BX + BG) + BX : 3 * (BX + BG);
+  static constexpr int fwd_warps() { return (HALF_SM - 4 * 2 * SLOT) / (ring + 2 * SLOT); }
+  static constexpr int fwd_peers() { return std::min(MAXC, (HALF_SM - fwd_warps() * (ring + 2 * SLOT)) / (2 * SLOT)); }
   static constexpr int fit(int W) { return 227 * 1024 / (W * ring + 2 * (W + MAXC) * SLOT + 1100); }
   static constexpr int regs(int W) { return 512 / (32 * W); }  // at 128 of a thread
   static constexpr int limit(int W) { return std::max(1, std::min(fit(W), regs(W))); }
 };
 template <typename X, typename G, int M, int W> cudaError_t launch_bwd(const ScanArgs &a, int sms, cudaStream_t st) {
-  typedef Room<X, G, true> R;
-  return launch_clustered<W, 1>(scan_bwd_kernel<X, G, M, W, 1, R::limit(W)>, a, R::limit(W) * sms, R::ring, st);
+  typedef Room<X, G, M, true> R;
+  return launch_clustered<W>(scan_bwd_kernel<X, G, M, W, R::limit(W)>, a, R::limit(W) * sms, R::ring, MAXC, st);
 }
 template <typename X, typename G, int M> cudaError_t launch_move(const ScanArgs &a, bool bwd, int sms, cudaStream_t st) {
   if (!bwd) {
-    typedef Room<X, G, false> R;
-    return launch_clustered<R::fwd_warps, 1>(scan_fwd_kernel<X, G, M, R::fwd_warps, 1>, a, 2 * sms, R::ring, st);
+    typedef Room<X, G, M, false> R;
+    return launch_clustered<R::fwd_warps()>(scan_fwd_kernel<X, G, M, R::fwd_warps()>, a, 2 * sms, R::ring, R::fwd_peers(), st);
   }
   // Four warps to a CTA, and several CTAs to an SM; as many as fit one where not even clusters of eight reach two SMs in three
   // (a sequence of 65536 tokens and 64 channels: 8 CTAs).
-  const long long most = (long long)((a.D + 63) / 64) * MAXC * (a.cu ? 1 : a.N);
+  const long long most = (long long)((a.D + CB - 1) / CB) * MAXC * (a.cu ? 1 : a.N);
   if (3 * most < 2 * sms) return launch_bwd<X, G, M, sizeof(X) == 2 ? 12 : 8>(a, sms, st);
   return launch_bwd<X, G, M, 4>(a, sms, st);
 }
 template <typename X, typename G> cudaError_t launch_types(const ScanArgs &a, int move, bool bwd, int sms, cudaStream_t st) {
   if (move == 16) return launch_move<X, G, M16>(a, bwd, sms, st);
-  // two bf16 neighbours in 4 bytes and two fp32 ones in 8: one layout of channels for both
-  if constexpr (sizeof(X) == sizeof(G)) {
+  if constexpr (sizeof(X) + sizeof(G) == 4) {
     if (move == 4) return launch_move<X, G, M4>(a, bwd, sms, st);
   }
-  if constexpr (sizeof(X) == 2) return launch_move<X, G, M2>(a, bwd, sms, st);
-  return cudaErrorInvalidValue;
+  return launch_move<X, G, ANY>(a, bwd, sms, st);
 }
 
 }  // namespace
