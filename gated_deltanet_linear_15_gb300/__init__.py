@@ -16,7 +16,9 @@ the forward keeps the per-chunk states and WY tiles for the backward),
 ``cp`` splits sequences across ranks.  Operators next to the delta rule (``block``, include/gdn_block.h):
 ``paged_attention``, ``rotary_table``, ``rotary``, ``rotary_embedding`` (autograd), ``rotary_append``,
 ``extend_pages``, ``fork_pages``, ``free_pages``, ``compact_pages``, ``copy_slots``, ``rms_norm``,
-``rms_norm_bwd``, ``residual_rms_norm`` (autograd).
+``rms_norm_bwd``, ``residual_rms_norm`` (autograd), ``norm_rotary``, ``norm_rotary_bwd``, ``norm_rotary_embedding``
+(autograd), ``norm_rotary_append``, ``prefix_attention``, ``gated_scan``, ``gated_scan_bwd``, ``gated_scan_step``,
+``gated_linear_recurrence`` (autograd).
 """
 from __future__ import annotations
 

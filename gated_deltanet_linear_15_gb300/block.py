@@ -1,20 +1,25 @@
 """Operators that a hybrid stack puts next to its gated delta-rule layers: the functions of include/gdn_block.h on tensors.
 
 ``paged_attention`` (attention of new tokens over a paged key/value cache), ``prefix_attention`` (the same of sequences that
-share a prefix), ``rotary_table`` / ``rotary`` /
-``rotary_embedding`` / ``rotary_append`` (rotary positions, their gradient, and the write of new keys and values into
-the cache), ``extend_pages`` / ``fork_pages`` / ``free_pages`` / ``compact_pages`` / ``copy_slots`` (the cache's
-upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual stream's norm, optionally with an 8-bit
-output), ``norm_rotary`` / ``norm_rotary_bwd`` / ``norm_rotary_embedding`` / ``norm_rotary_append`` (the norm of each head of q and k with
-their rotary positions: forward, backward, with gradients, and into the cache), ``gated_scan`` / ``gated_scan_bwd`` / ``gated_linear_recurrence`` / ``gated_scan_step`` (a gated linear recurrence with
-one state per channel: forward, backward, with gradients, and for single tokens).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
+share a prefix), ``rotary_table`` / ``rotary`` / ``rotary_embedding`` / ``rotary_append`` (rotary positions, their gradient,
+and the write of new keys and values into the cache), ``norm_rotary`` / ``norm_rotary_bwd`` / ``norm_rotary_embedding`` /
+``norm_rotary_append`` (the same behind a norm of every head), ``extend_pages`` / ``fork_pages`` / ``free_pages`` /
+``compact_pages`` / ``copy_slots`` (the cache's upkeep), ``rms_norm`` / ``rms_norm_bwd`` / ``residual_rms_norm`` (the residual
+stream's norm, optionally with an 8-bit output), ``gated_scan`` / ``gated_scan_bwd`` / ``gated_linear_recurrence`` /
+``gated_scan_step`` (a gated linear recurrence with one state per channel: forward, backward, with gradients, and for single
+tokens).  As in the rest of the package, everything runs in the library's CUDA kernels on the current stream; the
 arguments are checked, and outputs and workspaces allocated, by the extension csrc/block_py.cpp.  Bad arguments raise
 ``ValueError`` (found there) or ``RuntimeError`` (found by the library, with its reason), a lack of memory
 ``torch.OutOfMemoryError``.
 
-Gradients come from ``rotary_embedding``, ``residual_rms_norm``, ``norm_rotary_embedding`` and ``gated_linear_recurrence``.  Every other function computes outside autograd, as
+Gradients come from ``rotary_embedding``, ``residual_rms_norm``, ``norm_rotary_embedding`` and ``gated_linear_recurrence``.
+Every other function computes outside autograd, as
 the ``_fwd`` / ``_bwd`` functions of the delta rule do: its outputs carry no graph, whatever its inputs require.  What a
 function writes in place counts as an in-place operation (its version moves on).
+
+All of them can be captured into a CUDA graph; two graphs that may run at once need a workspace each.  A captured
+``backward()`` adds to leaves whose accumulation PyTorch ties to the stream that first used them: let no eager graph of the
+same leaves live then, or take ``torch.autograd.grad``.
 """
 from __future__ import annotations
 
@@ -26,8 +31,8 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 
-__all__ = ["paged_attention", "paged_attention_status", "prefix_attention", "prefix_attention_status", "rotary_frequencies", "rotary_table", "rotary", "rotary_embedding",
-           "rotary_append", "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_slots", "rms_norm",
+__all__ = ["paged_attention", "paged_attention_status", "prefix_attention", "prefix_attention_status", "rotary_frequencies",
+           "rotary_table", "rotary", "rotary_embedding", "rotary_append", "extend_pages", "fork_pages", "free_pages", "compact_pages", "copy_slots", "rms_norm",
            "rms_norm_bwd", "residual_rms_norm", "NormOutput", "norm_rotary", "norm_rotary_bwd",
            "norm_rotary_embedding", "norm_rotary_append", "gated_scan", "gated_scan_bwd", "gated_scan_step",
            "gated_linear_recurrence"]
@@ -51,11 +56,12 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q=None, max_q: 
     """Causal attention of new tokens over a paged cache that already holds their keys and values.
 
     q [new tokens, heads, D]; k_cache, v_cache [pages, page_size, kv heads, D] (any strides with contiguous features);
-    page_table int32 [sequences, pages] (one row may be expanded over all sequences); kv_lens int32 [sequences], the tokens of each sequence with the new ones;
+    page_table int32 [sequences, pages] (one row may be expanded over all sequences); kv_lens int32 [sequences], the tokens
+    of each sequence with the new ones;
     cu_q int32 [sequences + 1], where each sequence's new tokens begin in q (None: as many for each).  max_q: the most
     new tokens of a sequence, if known on the host (it only picks the kernel).  window > 0: a query sees that many
-    keys, and with sinks > 0 the sequence's first `sinks` keys too.  Returns o like q, or (o, lse) with lse fp32 [new tokens, heads]; a query without keys has o = 0 and
-    lse = -inf.  workspace: a tensor to use as scratch memory (contiguous, 32-byte
+    keys, and with sinks > 0 the sequence's first `sinks` keys too.  Returns o like q, or (o, lse) with lse fp32 [new tokens,
+    heads]; a query without keys has o = 0 and lse = -inf.  workspace: a tensor to use as scratch memory (contiguous, 32-byte
     aligned, refused when it is too small).  Decoding is the case of one new token per sequence."""
     return _py.paged_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q, scale, window, return_lse, out, workspace,
                                sinks)
@@ -300,8 +306,8 @@ def gated_scan(x, g, initial_state=None, cu_seqlens=None, output_final_state: bo
 
     x [sequences, tokens, D] (rows of one stride), g like x in its dtype or fp32: the log-gates, meant to be <= 0 (-inf
     forgets).  Packed sequences: x [1, tokens, D] and cu_seqlens int32 [sequences + 1] on the device; rows that no sequence
-    names stay uninitialised in y.  initial_state fp32 [sequences, D] (None: zeros).  Returns (y, final state fp32 [sequences, D], or None
-    without output_final_state), and with save_states the states that ``gated_scan_bwd`` reads."""
+    names stay uninitialised in y.  initial_state fp32 [sequences, D] (None: zeros).  Returns (y, final state fp32 [sequences,
+    D], or None without output_final_state), and with save_states the states that ``gated_scan_bwd`` reads."""
     y, final, states = _py.gated_scan(x, g, initial_state, cu_seqlens, output_final_state, save_states)
     return (y, final, states) if save_states else (y, final)
 
