@@ -37,7 +37,7 @@ constexpr int SEG = SCAN_SEG, CB = 64, MAXC = 8;  // tokens of a segment, channe
 
 // What brings rows: 16-byte copies of rows that begin on 16-byte boundaries; 4-byte copies of bf16 pairs; 16-byte copies
 // of the aligned pieces that hold a row that begins anywhere (4 x 4096 tokens, 1001 channels: bf16 forward 48 us and backward
-// 95, with plain loads of single values 89 and 132; 32749 packed fp32 tokens 134 us, with 4-byte copies 163).  Pairs keep the
+// 95, with plain loads of single values 89 and 132; 32749 packed fp32 tokens 134 us, with 4-byte copies 163, parts as they were).  Pairs keep the
 // 4-byte copies where they can, for the stores of pairs that go with them (1002 channels: backward 71 us, 1001: 95).
 enum Move { M16, M4, ANY };
 // Of a block's channels a lane has two neighbours, or two that lie 32 apart where rows begin anywhere.
@@ -175,7 +175,7 @@ template <bool P> __device__ __forceinline__ Two take(const float *row, int c, i
 // ------------------------------------------------------------------ where sequences begin
 // Tokens of the line that a part takes: whole sequences.  Packed sequences go by where they begin, so that parts are of
 // about the same size; equal ones by number.
-__device__ __forceinline__ int lower_bound(const int *cu, int n, int v) {  // entries of cu[0 .. n) below v
+__device__ __forceinline__ int lower_bound(const int *cu, int n, long long v) {  // entries of cu[0 .. n) below v
   int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -184,11 +184,40 @@ __device__ __forceinline__ int lower_bound(const int *cu, int n, int v) {  // en
   }
   return lo;
 }
+__device__ __forceinline__ int token_at(const ScanArgs &a, int n) { return min(max(a.cu[n], 0), a.tokens); }
+// where part p begins: at the sequence's end that is nearest to an even cut
 __device__ __forceinline__ int part_begin(const ScanArgs &a, int p, int parts) {
   if (!a.cu) return (int)((long long)a.N * p / parts) * a.T;
-  int at = p == 0 ? 0 : (p == parts ? a.N : lower_bound(a.cu, a.N + 1, (int)((long long)a.tokens * p / parts)));
-  at = min(at, a.N);
-  return min(max(a.cu[at], 0), a.tokens);
+  if (p == 0 || p == parts) return token_at(a, p ? a.N : 0);
+  const int want = (int)((long long)a.tokens * p / parts), at = min(lower_bound(a.cu, a.N + 1, want), a.N);
+  const int behind = token_at(a, at), before = at > 0 ? token_at(a, at - 1) : behind;
+  return want - before < behind - want ? before : behind;
+}
+// A part of few packed sequences and many rounds (of `round` tokens): the tokens of the largest part set the time, so the warp
+// looks for the least number that lets every part take whole sequences up to it, among 32 from the mean to three times that.
+// False where there is none, or where the search would take more than it gives.  (16 sequences, 32749 tokens, 1001 channels
+// in fp32, four parts: 123 us, 147 with parts by part_begin; with 8 rounds the search, 1 us, only costs.)
+constexpr int FEW_PARTS = 8, FEW_SEQS = 16, MANY_ROUNDS = 16;
+__device__ __forceinline__ bool even_parts(const ScanArgs &a, int round, int &lo, int &hi) {
+  const int parts = gridDim.z;
+  if (!a.cu || parts == 1 || parts > FEW_PARTS || a.N > FEW_SEQS * parts) return false;
+  if (a.tokens / parts / round < MANY_ROUNDS) return false;
+  const long long mean = ((long long)a.tokens + parts - 1) / parts, most = mean + mean * (threadIdx.x & 31) / 16;
+  int n = 0, at = token_at(a, 0), end = at, p = 0;  // at: where part p begins, from sequence n
+  for (; p < parts && n < a.N; ++p) {
+    const int next = min(lower_bound(a.cu, a.N + 1, at + most + 1) - 1, a.N);
+    if (next <= n) break;  // a sequence of more than that
+    n = next;
+    end = token_at(a, n);
+    if (p == (int)blockIdx.z) lo = at, hi = end;
+    at = end;
+  }
+  if (p <= (int)blockIdx.z) lo = hi = end;  // nothing is left for this part
+  const unsigned ok = __ballot_sync(0xffffffffu, n == a.N);
+  if (!ok) return false;
+  lo = __shfl_sync(0xffffffffu, lo, __ffs(ok) - 1);
+  hi = __shfl_sync(0xffffffffu, hi, __ffs(ok) - 1);
+  return true;
 }
 
 // The boundaries between sequences around a warp's segment.  The warp knows the sequence [b0, b1) that its last segment
@@ -407,10 +436,15 @@ struct Walk {
   int rounds, per;   // segments of a round: one for every warp of the cluster
   int first, last;   // the warp's segment of round 0; the line's segment with number 0 going backward
   template <int W> __device__ __forceinline__ void init(const ScanArgs &a, int cs, int rank) {
-    lo = part_begin(a, blockIdx.z, gridDim.z);
-    hi = part_begin(a, blockIdx.z + 1, gridDim.z);
-    const int s0 = lo / SEG, ns = hi > lo ? (hi + SEG - 1) / SEG - s0 : 0;
     per = cs * W;
+    if (a.cu && a.N <= (int)gridDim.z) {  // a part for every sequence
+      lo = token_at(a, min((int)blockIdx.z, a.N));
+      hi = token_at(a, min((int)blockIdx.z + 1, a.N));
+    } else if (!even_parts(a, per * SEG, lo, hi)) {
+      lo = part_begin(a, blockIdx.z, gridDim.z);
+      hi = part_begin(a, blockIdx.z + 1, gridDim.z);
+    }
+    const int s0 = lo / SEG, ns = hi > lo ? (hi + SEG - 1) / SEG - s0 : 0;
     rounds = (ns + per - 1) / per;
     first = s0 + rank * W + (threadIdx.x >> 5);
     last = 2 * s0 + ns - 1;
@@ -729,6 +763,7 @@ void split(const ScanArgs &a, int W, int ctas, int peers, int &parts, int &cs) {
   } else {
     cs = clustered(want, a.tokens);
     parts = std::min(a.N, std::max(1, want / cs));
+    if (a.N < 2 * parts) parts = a.N;  // (12 sequences of up to 4000 tokens, 512 channels, backward: 2.5 TB/s, 2.3 in 9 parts)
   }
   parts = std::min(parts, 65535);
 }
@@ -759,12 +794,13 @@ cudaError_t launch_clustered(void (*k)(KArgs...), const ScanArgs &a, int ctas, i
 }
 constexpr int HALF_SM = 227 * 1024 / 2 - 1024;  // shared memory of one of two CTAs
 // What a CTA of W warps takes, and how many of them share an SM.  The forward has as many warps as leave
-// room for two CTAs, and as large clusters (fp32 rows that begin anywhere: 4 warps, clusters of 6).
+// room for two CTAs, with eight peers or at least four (fp32 rows that begin anywhere: 16 packed sequences of up to 4000
+// tokens, 1001 channels: 3.2 TB/s with four warps and four peers, 2.7 with three and eight, 2.6 with four and six).
 template <typename X, typename G, int M, bool BWD> struct Room {
   static constexpr int SLOT = sizeof(MapSlot), BX = Tile<X, M>::BYTES, BG = Tile<G, M>::BYTES;
   static constexpr int ring = BWD ? 2 * (BX + BG) + BX : 3 * (BX + BG);
   static constexpr int fwd_warps() { return (HALF_SM - 4 * 2 * SLOT) / (ring + 2 * SLOT); }
-  static constexpr int fwd_peers() { return std::min(MAXC, (HALF_SM - fwd_warps() * (ring + 2 * SLOT)) / (2 * SLOT)); }
+  static constexpr int fwd_peers() { return HALF_SM - fwd_warps() * (ring + 2 * SLOT) >= MAXC * 2 * SLOT ? MAXC : 4; }
   static constexpr int fit(int W) { return 227 * 1024 / (W * ring + 2 * (W + MAXC) * SLOT + 1100); }
   static constexpr int regs(int W) { return 512 / (32 * W); }  // at 128 of a thread
   static constexpr int limit(int W) { return std::max(1, std::min(fit(W), regs(W))); }
@@ -779,8 +815,9 @@ template <typename X, typename G, int M> cudaError_t launch_move(const ScanArgs 
     return launch_clustered<R::fwd_warps()>(scan_fwd_kernel<X, G, M, R::fwd_warps()>, a, 2 * sms, R::ring, R::fwd_peers(), st);
   }
   // Four warps to a CTA, and several CTAs to an SM; as many as fit one where not even clusters of eight reach two SMs in three
-  // (a sequence of 65536 tokens and 64 channels: 8 CTAs).
-  const long long most = (long long)((a.D + CB - 1) / CB) * MAXC * (a.cu ? 1 : a.N);
+  // (a sequence of 65536 tokens and 64 channels: 8 CTAs; but 24 packed ones of up to 2900 tokens and 512 channels take 2.7 TB/s with
+  // four warps and 1.2 with twelve).
+  const long long most = (long long)((a.D + CB - 1) / CB) * MAXC * a.N;
   if (3 * most < 2 * sms) return launch_bwd<X, G, M, sizeof(X) == 2 ? 12 : 8>(a, sms, st);
   return launch_bwd<X, G, M, 4>(a, sms, st);
 }

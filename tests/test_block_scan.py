@@ -155,6 +155,14 @@ def test_wide(packed):
 
 
 @gpu
+@pytest.mark.parametrize("lens,D", [([3000, 100, 2700, 0, 2500, 900], 2001), ([431, 0, 1716, 4325, 3411, 55, 6939, 233], 1001),
+                                    ([200, 300, 15000, 1, 0, 700], 1001), ([1, 9000], 2001), ([0, 0, 8500, 0, 0], 2001)])
+def test_long_packed_sequences(lens, D):
+    """Few packed sequences and many rounds: parts that are evened out, or cannot be."""
+    check(inputs(lens, D, F32, F32, True), D, both=False)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("off", [0, 1, 2, 4, 8])
 def test_rows_with_strides_and_odd_alignment(dtype, off):
