@@ -9,6 +9,9 @@
 //
 // The join takes a warp to a row.  The rows' notes say where its pieces are: a head that 152 CTAs share has as many, and a row
 // reads no more of them than D sums and two numbers each, all from L2.  Bound by latency: a batch of pieces is asked for at once.
+//
+// 64 sequences of up to 1024 tokens of their own behind 8192 shared ones, 8 key heads of 128, one new token each: 71 us (plan 4,
+// HEAD 20, TAIL 34, join 9), 228 as sequences that share nothing.
 #include "paged.cuh"
 
 namespace gdn {

@@ -260,7 +260,7 @@ struct Bounds {
     uint32_t m = 0;
     int b = base, x = e;
     for (int k = 0; k <= a.N / 31 + 1; ++k) {
-      const unsigned d = (unsigned)(x - t);
+      const unsigned d = (unsigned)x - (unsigned)t;
       m |= __reduce_or_sync(0xffffffffu, d <= SEG ? 1u << d : 0u);
       if (__any_sync(0xffffffffu, x > t + SEG) || b + 31 > a.N) break;
       b += 31;

@@ -276,6 +276,18 @@ def test_any_cu_seqlens_ends_within_the_rows(cu):
     torch.cuda.synchronize()
 
 
+@gpu
+@pytest.mark.parametrize("cu", [[0, 5000, 2000, 8300], [8300, 0, 8300, 0], [-5, 1000000, 3, 2 ** 31 - 1], [4000, 3000, 2000, 1000], [8300, 8300, 9]])
+def test_any_cu_seqlens_of_many_rounds_ends(cu):
+    """The same where parts are evened out."""
+    import gated_deltanet_linear_15_gb300 as g
+    x = torch.ones(1, 8300, 2001, device=DEV)
+    dev = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    y, final, states = g.gated_scan(x, -x, cu_seqlens=dev, save_states=True)
+    g.gated_scan_bwd(x, x, -x, states, None, final, cu_seqlens=dev)
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ gradients
 @gpu
 def test_gradient_by_differences():
