@@ -221,8 +221,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     tma_prefetch_desc(&tv);
   }
   if (a.expire) {  // before TMEM is taken or any copy asked for
-    pdl_trigger();
-    pdl_wait();
+    part_wait<PART>(a);
     if (tid == 0) {
       a.hdr[cta] = make_int4(0, 0, 0, 0);
       wait(&bars.full[0], 0, dead, 1024);
@@ -234,8 +233,7 @@ __global__ void __launch_bounds__(NTHR, 1) attn_chunk_kernel(const PagedArgs a, 
     tmem_alloc(smem_u32(&bars.tmem), TM_COLS);
     tmem_relinquish();
   }
-  pdl_trigger();
-  pdl_wait();
+  part_wait<PART>(a);
   SeqInfo *seqs = reinterpret_cast<SeqInfo *>(ring);  // the search uses the ring's memory
   cursor_prepare<NTHR, PART>(a, seqs);
   if (warp == 0) {

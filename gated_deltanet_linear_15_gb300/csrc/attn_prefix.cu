@@ -7,11 +7,15 @@
 // before their new tokens, so that every new token sees all of it, whatever the caller says; and a group of one sequence has
 // none.  It is one block, a warp to a group, and a few more that clear the rows' notes.
 //
+// The parts run at the same time, each on some of the SMs, where one of them at least is the row kernel, which waits for memory
+// most of the time while the other one computes: launches, searches and ends of the two overlap too.  The plan shares
+// the SMs out by the parts' blocks, and the CTAs behind a part's share leave at once.  64 sequences of up to 1024 tokens of their
+// own behind 8192 shared ones, 8 key heads of 128, one new token each: 55 us; one part after the other 72; as sequences
+// that share nothing 228.  Two chunk kernels only take from one another (8 groups of 8 with 5 new tokens each, in a row of
+// calls: 79 us at the same time, 63 one after the other).
+//
 // The join takes a warp to a row.  The rows' notes say where its pieces are: a head that 152 CTAs share has as many, and a row
 // reads no more of them than D sums and two numbers each, all from L2.  Bound by latency: a batch of pieces is asked for at once.
-//
-// 64 sequences of up to 1024 tokens of their own behind 8192 shared ones, 8 key heads of 128, one new token each: 71 us (plan 4,
-// HEAD 20, TAIL 34, join 9), 228 as sequences that share nothing.
 #include "paged.cuh"
 
 namespace gdn {
@@ -23,7 +27,49 @@ constexpr int NONE = -2;  // a row's note: no pieces
 
 }  // namespace
 
-__global__ void __launch_bounds__(NTP) prefix_plan_kernel(PagedArgs a, PrefixPlan p, int2 *head_loc, int2 *tail_loc) {
+// The SMs are shared out so that both parts end at about the same time.  (The sums are of whole numbers, so their order does
+// not matter.  Calls whose parts do not share the SMs have a plan without this code, which costs 3 us even where it is jumped
+// over.)
+__device__ __forceinline__ void share_out(const PagedArgs &a, const PrefixPlan &p) {
+  __syncthreads();  // all is planned
+  long long work[2] = {0, 0};  // blocks of a key head's items, with their setup
+  auto add = [&](int part, int rows, int keys) {
+    const PrefixPlan::Share &s = p.share[part];
+    if (rows > 0) work[part] += (long long)((rows + s.MT - 1) / s.MT) * ((keys + s.BN - 1) / s.BN + s.setup);
+  };
+  for (int g = threadIdx.x; g < p.groups; g += NTP) {
+    const int4 v = p.head[g];
+    if (v.z > 0) add(0, v.y * a.G, v.z);
+  }
+  for (int n = threadIdx.x; n < a.N; n += NTP) {
+    const int4 v = p.tail[n];
+    add(1, v.y * a.G, v.z - v.w);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (work[i]) atomicAdd(p.blocks + i, (unsigned long long)work[i]);
+  }
+  __syncthreads();
+  if (threadIdx.x > 0) return;
+  float w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = (float)__ldcg(p.blocks + i) * (float)a.Hkv;
+  int sms = 0;  // of HEAD
+  if (w[0] > 0.f) {
+    const float late = p.share[0].start - p.share[1].start, h = w[0] * p.share[0].cost, t = w[1] * p.share[1].cost;
+    // no CTA without a block, and no less than a quarter for the tails, whose work is known least
+    int hi = max(1, (int)fminf(0.75f * (float)p.sms, ceilf(w[0] / (float)p.share[0].per_sm)));
+    for (sms = 1; sms < hi;) {
+      const int mid = (sms + hi) >> 1;
+      if (late + h / (float)mid <= t / (float)(p.sms - mid)) hi = mid;
+      else sms = mid + 1;
+    }
+  }
+  p.ctas[0] = sms * p.share[0].per_sm;
+  asm volatile("st.release.gpu.global.b32 [%0], %1;\n" ::"l"(p.ctas + 1), "r"((p.sms - sms) * p.share[1].per_sm) : "memory");
+}
+
+template <bool TOGETHER> __global__ void __launch_bounds__(NTP) prefix_plan_kernel(PagedArgs a, PrefixPlan p, int2 *head_loc, int2 *tail_loc) {
   pdl_trigger();
   pdl_wait();
   if (blockIdx.x > 0) {
@@ -34,6 +80,7 @@ __global__ void __launch_bounds__(NTP) prefix_plan_kernel(PagedArgs a, PrefixPla
     }
     return;
   }
+  if (TOGETHER && threadIdx.x < 2) p.blocks[threadIdx.x] = 0;
   for (int n = threadIdx.x; n < a.N; n += NTP) {  // sequences that no group names have no prefix
     const SeqInfo s = seq_info(a, n);
     p.tail[n] = make_int4(s.qbeg, s.qlen, s.kv, 0);
@@ -66,6 +113,7 @@ __global__ void __launch_bounds__(NTP) prefix_plan_kernel(PagedArgs a, PrefixPla
     if (lane == 0) p.head[g] = prefix > 0 ? make_int4(beg, end - beg, prefix, n0) : make_int4(0, 0, 0, n0);
     for (int n = n0 + lane; n < n1; n += 32) p.tail[n].w = min(prefix, p.tail[n].z);
   }
+  if constexpr (TOGETHER) share_out(a, p);
 }
 
 template <typename I, int D>
@@ -156,7 +204,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) prefix_join_kernel(PagedArgs 
 cudaError_t launch_prefix_plan(const PagedArgs &a, const PrefixPlan &p, int2 *head_loc, int2 *tail_loc, cudaStream_t st) {
   const long long rows = (long long)a.total_q * a.Hq;
   const unsigned clear = (unsigned)((rows + 4 * NTP - 1) / (4 * NTP) < 152 ? (rows + 4 * NTP - 1) / (4 * NTP) : 152);
-  return launch_pdl(prefix_plan_kernel, dim3(1 + clear), dim3(NTP), 0, st, a, p, head_loc, tail_loc);
+  return launch_pdl(p.together ? prefix_plan_kernel<true> : prefix_plan_kernel<false>, dim3(1 + clear), dim3(NTP), 0, st, a, p, head_loc, tail_loc);
 }
 
 cudaError_t launch_prefix_join(const PagedArgs &head, const PagedArgs &tail, bool bf, int D, int head_MT, int tail_MT, int head_ctas,

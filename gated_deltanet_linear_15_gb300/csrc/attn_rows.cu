@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(JW == 1 ? 128 : 32 * JW) attn_join_kernel(Page
 // before the guard in split_tf32, which adds 1 to 3 %).
 int attn_rows_tile(bool bf, int D, int rows) { return rows <= 16 || (!bf && D == 64) ? 16 : 32; }
 int attn_rows_box(bool bf, int MT, int page) { return bf && MT == 32 && page >= 32 ? 32 : 16; }
+int attn_rows_block(bool bf, int MT) { return bf && MT == 32 ? 128 : 64; }
 int attn_rows_per_sm(bool bf, int D, int MT) { return MT == 16 && (bf || D == 64) ? 2 : 1; }
 cudaError_t launch_attn_rows(const PagedArgs &a, Part part, const CUtensorMap &tk, const CUtensorMap &tv, bool bf, int D, int MT, int ctas,
                              cudaStream_t st) {

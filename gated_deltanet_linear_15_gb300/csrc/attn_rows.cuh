@@ -150,8 +150,7 @@ attn_rows_kernel(const PagedArgs a, const __grid_constant__ CUtensorMap tk, cons
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
-  pdl_trigger();
-  pdl_wait();
+  part_wait<PART>(a);
   if (a.expire) {  // no copy has been asked for
     if (tid == 0) {
       a.hdr[cta] = make_int4(0, 0, 0, 0);

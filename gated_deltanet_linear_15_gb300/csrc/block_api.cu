@@ -291,9 +291,10 @@ int attn_status_words(const AttnPlan &p, const void *ws) {
 // ------------------------------------------------------------------ attention behind a shared prefix
 // Where sharing saves no more than this many bytes, a batch is computed as if its sequences shared nothing.  Two parts take
 // three launches more, some 10 us; reading shared keys again, mostly from L2, costs 1 us for 13 MB in bf16 and for 7 in fp32.
-// One new token, us as one / in two parts: bf16, 8 key heads of 128: 16 sequences behind 1024 tokens (67 MB) 18 / 25, 4
-// behind 16384 (202 MB) 36 / 32, 64 behind 4096 (1.1 GB) 111 / 33; 2 key heads of 64: 64 behind 4096 (134 MB) 31 / 26; fp32,
-// 2 key heads of 128: 64 behind 256 (41 MB) 23 / 30, 4 behind 16384 (101 MB) 46 / 40.
+// One new token, caches cold, us as one / in two parts: bf16, 8 key heads of 128: 16 sequences behind 1024 tokens (67 MB)
+// 25 / 34, 32 (138 MB) 29 / 32, 8 behind 4096 (119 MB) 31 / 28, 4 behind 16384 (202 MB) 48 / 39, 64 behind 4096 (1.1 GB)
+// 120 / 43; fp32, 2 key heads of 128: 64 behind 256 (41 MB) 28 / 35, 8 behind 4096 (59 MB) 37 / 41, 64 behind 512 (74 MB)
+// 40 / 37, 4 behind 16384 (101 MB) 54 / 49.
 double prefix_min_bytes(gdn_dtype d) { return d == GDN_BF16 ? 128e6 : 80e6; }
 struct PrefixLayout {
   bool split;  // in two parts; otherwise as sequences that share nothing
@@ -332,7 +333,7 @@ PrefixLayout prefix_layout(const gdn_paged_shape *s, int groups, int max_group) 
   };
   l.off_tail = take(l.tail.total);
   l.off_head = take(l.head.total);
-  l.off_info = take(((size_t)groups + s->num_seqs) * sizeof(int4));
+  l.off_info = take(((size_t)groups + s->num_seqs + 2) * sizeof(int4));
   for (int i = 0; i < 2; ++i) {
     l.off_sums[i] = take(rows * s->head_dim * sizeof(float));
     l.off_mass[i] = take(rows * sizeof(float2));
@@ -340,6 +341,22 @@ PrefixLayout prefix_layout(const gdn_paged_shape *s, int groups, int max_group) 
   }
   l.total = at;
   return l;
+}
+
+// What a part costs, for the sharing of the SMs: a line through times taken with different shares.  Chunk kernel: 19 us and
+// 1.5 for 256 rows and 128 keys (D = 64: 1.1).  Row kernel: 8 us and an SM's bytes at 71 GB/s, 33 with two groups of rows, 40 in
+// fp32, but 0.4 at least for a block.
+PrefixPlan::Share part_share(const gdn_paged_shape *s, const AttnPlan &p) {
+  const bool bf = s->dtype == GDN_BF16;
+  PrefixPlan::Share x;
+  x.MT = p.MT;
+  x.BN = p.tc ? 128 : attn_rows_block(bf, p.MT);
+  x.per_sm = p.ctas / num_sms();
+  x.start = p.tc ? 19.f : 8.f;
+  x.setup = p.tc ? 5 : 2;
+  x.cost = p.tc ? (s->head_dim == 64 ? 1.1f : 1.5f)
+                : std::max(0.4f, x.BN * s->head_dim * 2 * esize(s->dtype) / (p.MT == 32 ? 33e3f : bf ? 71e3f : 40e3f));
+  return x;
 }
 
 // ------------------------------------------------------------------ rotary positions
@@ -557,8 +574,16 @@ int gdn_prefix_attn_fwd(const gdn_paged_shape *s, int groups, int max_group, con
   plan.groups = groups;
   plan.head = reinterpret_cast<int4 *>(w + l.off_info);
   plan.tail = plan.head + groups;
+  plan.ctas = reinterpret_cast<int *>(plan.tail + s->num_seqs);
+  plan.blocks = reinterpret_cast<unsigned long long *>(plan.ctas + 4);
+  plan.sms = num_sms();
+  plan.together = head.together = tail.together = !(l.head.tc && l.tail.tc);
+  plan.share[0] = part_share(s, l.head);
+  plan.share[1] = part_share(s, l.tail);
   head.info = plan.head;
   tail.info = plan.tail;
+  head.ctas = plan.ctas;
+  tail.ctas = plan.ctas + 1;
   PagedArgs *parts[2] = {&head, &tail};
   for (int i = 0; i < 2; ++i) {
     parts[i]->sums = reinterpret_cast<float *>(w + l.off_sums[i]);

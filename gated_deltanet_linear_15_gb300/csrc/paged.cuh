@@ -44,6 +44,8 @@ struct PagedArgs {
   // HEAD, TAIL: the sequences (HEAD: groups); records of items that are not cut, [total_q][Hq] of D sums, and of maximum and
   // mass; where each row's pieces are: the CTA of the first one and the row in its records, or {-1, 0}: an uncut record
   const int4 *info;
+  const int *ctas;   // HEAD, TAIL: of the launched CTAs, how many take part
+  int together;      // HEAD and TAIL run at the same time
   float *sums;
   float2 *mass;
   int2 *loc;
@@ -58,6 +60,34 @@ struct SeqInfo {
   int qbeg, qlen, kv;
   int ext;  // HEAD: the sequence whose table row names the prefix; TAIL: tokens of the prefix
 };
+// With a.together HEAD and TAIL run at the same time: HEAD lets TAIL begin once it has seen the plan's results itself, and of
+// TAIL only the last CTA waits for HEAD, so that what waits for TAIL waits for both.  TAIL's threads acquire what the plan
+// has released; HEAD's wait for the plan came before.
+template <int PART> __device__ __forceinline__ void part_wait(const PagedArgs &a) {
+  if constexpr (PART == HEAD || PART == TAIL) {
+    if (a.together) {
+      if (PART == HEAD) {
+        pdl_wait();
+        pdl_trigger();
+      } else {
+        pdl_trigger();
+        if (blockIdx.x == gridDim.x - 1) pdl_wait();
+        int seen;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];\n" : "=r"(seen) : "l"(a.ctas) : "memory");
+      }
+      return;
+    }
+  }
+  pdl_trigger();
+  pdl_wait();
+}
+// CTAs that share the work
+template <int PART> __device__ __forceinline__ int part_ctas(const PagedArgs &a) {
+  if constexpr (PART == HEAD || PART == TAIL) {
+    if (a.together) return min(max(*a.ctas, 1), (int)gridDim.x);
+  }
+  return gridDim.x;
+}
 template <int PART = ALL> __device__ __forceinline__ SeqInfo seq_info(const PagedArgs &a, int n) {
   SeqInfo s;
   if constexpr (PART == HEAD || PART == TAIL) {
@@ -263,7 +293,7 @@ __device__ __noinline__ bool cursor_begin_any(const PagedArgs &a, Cursor &c, Pla
   if (tid == 0) sm.units[0] = 0;
   plan_bar<NT>();
   const long long total = sm.units[NT];
-  c.split.C = (int)min((long long)gridDim.x, total);
+  c.split.C = (int)min((long long)part_ctas<PART>(a), total);
   if (blockIdx.x >= c.split.C) return false;
   c.split.q = div_units(total, c.split.C);
   c.split.r = (int)(total - c.split.q * c.split.C);
@@ -355,7 +385,7 @@ template <int MT, int BN, int PART> __device__ __forceinline__ int cursor_begin_
     mine = units;
     uinc = scan(units);
     const long long total = __shfl_sync(0xffffffffu, uinc, 31);
-    sp.C = (int)min((long long)gridDim.x, total);
+    sp.C = (int)min((long long)part_ctas<PART>(a), total);
     if ((int)blockIdx.x >= sp.C) return 0;
     sp.q = div_units(total, sp.C);
     sp.r = (int)(total - sp.q * sp.C);
@@ -412,7 +442,7 @@ template <int MT, int BN, int PART> __device__ __forceinline__ int cursor_begin_
   const long long un = mine ? (long long)w.units() * a.Hkv : 0;
   if (__any_sync(0xffffffffu, un > (1 << 25))) return 2;
   const int uinc = scan((int)un), total = __shfl_sync(0xffffffffu, uinc, 31);
-  const int C = min((int)gridDim.x, total);
+  const int C = min(part_ctas<PART>(a), total);
   if ((int)blockIdx.x >= C) return 0;
   const int q = (unsigned)total / (unsigned)C, r = total - q * C;
   const int u = blockIdx.x * q + min((int)blockIdx.x, r);
@@ -505,6 +535,7 @@ __device__ __forceinline__ void note_row(const PagedArgs &a, bool whole, int tok
 // rows of a tile of the row kernel for up to `rows` rows per key head, and its CTAs per SM
 int attn_rows_tile(bool bf16_type, int D, int rows);
 int attn_rows_per_sm(bool bf16_type, int D, int MT);
+int attn_rows_block(bool bf16_type, int MT);  // keys of its blocks
 int attn_rows_box(bool bf16_type, int MT, int page_size);  // slots of a box of its tensor maps
 cudaError_t launch_attn_rows(const PagedArgs &a, Part part, const CUtensorMap &tk, const CUtensorMap &tv, bool bf16_type, int D, int MT,
                              int ctas, cudaStream_t st);
@@ -521,6 +552,14 @@ struct PrefixPlan {
   const int *cu_seqs, *prefix_lens;  // groups; cu_seqs NULL: equal ones
   int groups;
   int4 *head, *tail;                 // info of the groups and of the sequences
+  struct Share {                     // of HEAD, of TAIL
+    int MT, BN, per_sm, setup;       // rows of a tile, keys of a block, CTAs of an SM, blocks that an item takes beside its own
+    float start, cost;               // us: a launch before and behind its blocks; a block on an SM of its own
+  } share[2];
+  int sms;
+  int together;                      // the parts share the SMs
+  int *ctas;                         // [2], with together
+  unsigned long long *blocks;        // [2], with together: counts
 };
 cudaError_t launch_prefix_plan(const PagedArgs &a, const PrefixPlan &p, int2 *head_loc, int2 *tail_loc, cudaStream_t st);
 cudaError_t launch_prefix_join(const PagedArgs &head, const PagedArgs &tail, bool bf16_type, int D, int head_MT, int tail_MT, int head_ctas,
