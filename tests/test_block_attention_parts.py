@@ -283,6 +283,37 @@ def test_any_groups_end_within_the_rows(cu_seqs, cu_q):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,G,groups", [(BF, 4, 1), (BF, 1, 3), (F32, 2, 2), (BF, 40, 2)])
+def test_prefix_right_behind_its_inputs(dtype, G, groups):
+    """Queries, caches, lengths and prefixes written by the kernels just before, call after call with one workspace: the bits of
+    calls that had the GPU to themselves."""
+    import gated_deltanet_linear_15_gb300 as g
+    x, qs, pre, cu = shared([(400 + 16 * k, [(1, 30 + 7 * i) for i in range(12)]) for k in range(groups)], dtype, 128, 2, G, 16)
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    gen = torch.Generator().manual_seed(9)
+    drawn = [dict(q=torch.randn(x["q"].shape, generator=gen).to(DEV, dtype), less=k % 3, shift=16 * (k % 5)) for k in range(12)]
+    lens, fixed = x["kv_lens"].clone(), pre.clone()
+    caches = [(x["k_cache"] * (1 + 0.1 * k), x["v_cache"] * (1 - 0.1 * k)) for k in range(3)]
+
+    def call(d, k):
+        x["q"].copy_(d["q"])
+        torch.sub(lens, d["less"], out=x["kv_lens"])
+        torch.sub(fixed, d["shift"], out=pre)
+        for name, new in zip(("k_cache", "v_cache"), caches[k % 3]):
+            x[name].copy_(new)
+        return g.prefix_attention(**x, prefix_lens=pre, cu_seqs=cu, return_lse=True, workspace=ws)
+
+    want = []
+    for k, d in enumerate(drawn):
+        want.append(call(d, k))
+        torch.cuda.synchronize()
+    for _ in range(8):
+        got = [call(d, k) for k, d in enumerate(drawn)]
+        for p, q in zip(got, want):
+            assert torch.equal(p[0], q[0]) and torch.equal(p[1], q[1])
+
+
+@gpu
 def test_prefix_capture_and_workspaces():
     """Replayed from a graph over new queries and lengths, and on another stream with a workspace of its own: the same bits."""
     import gated_deltanet_linear_15_gb300 as g
