@@ -767,6 +767,13 @@ gdn_scan_shape scan_shape(const Tensor &x, const Tensor &g, const Tensor *cu, bo
   s.g_row = line_stride(g, "g");
   return s;
 }
+// rows of the saved states
+int64_t scan_rows(const gdn_scan_shape &s) {
+  if (s.num_seqs == 0) return 0;
+  const int64_t rows = api.scan_states_rows(&s);
+  if (rows < 0) check(GDN_ERR_INVALID_ARG, "gdn_scan_states_rows");
+  return rows;
+}
 void scan_state(const Tensor &t, const gdn_scan_shape &s, const char *name) {
   here(t, name);
   if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != s.num_seqs || t.size(1) != s.dim || !t.is_contiguous())
@@ -786,10 +793,10 @@ PyObject *gated_scan(PyObject *const *a) {
   Tensor final, states;
   if (truth(a[4])) final = at::empty({s.num_seqs, s.dim}, x.options().dtype(at::kFloat));
   if (truth(a[5])) {
-    const int64_t rows = api.scan_states_rows(&s);
-    if (rows < 0) check(GDN_ERR_INVALID_ARG, "gdn_scan_states_rows");
+    const int64_t rows = scan_rows(s);
     states = at::empty({rows, s.dim}, x.options().dtype(at::kFloat));
   }
+  if (s.num_seqs == 0) return pack({y, final, states});
   check(api.scan_fwd(&s, x.data_ptr(), g.data_ptr(), f32(h0), i32(cu), y.data_ptr(), f32(final), f32(states), (gdn_stream_t)stream(x)),
         "gdn_scan_fwd");
   return pack({y, final, states});
@@ -803,8 +810,7 @@ PyObject *gated_scan_bwd(PyObject *const *a) {
   same_as(dy, x, "dy");
   if (h0) scan_state(*h0, s, "initial_state");
   if (dT) scan_state(*dT, s, "d_final");
-  const int64_t rows = api.scan_states_rows(&s);
-  if (rows < 0) check(GDN_ERR_INVALID_ARG, "gdn_scan_states_rows");
+  const int64_t rows = scan_rows(s);
   here(states, "states");
   if (states.scalar_type() != at::kFloat || states.dim() != 2 || states.size(0) != rows || states.size(1) != s.dim || !states.is_contiguous())
     bad("states must be what gated_scan with save_states returned for these inputs");
@@ -813,6 +819,7 @@ PyObject *gated_scan_bwd(PyObject *const *a) {
   s.y_row = s.dg_row = s.dim;
   Tensor dh0;
   if (h0) dh0 = at::empty({s.num_seqs, s.dim}, states.options());
+  if (s.num_seqs == 0) return pack({dx, dg, dh0});
   check(api.scan_bwd(&s, dy.data_ptr(), x.data_ptr(), g.data_ptr(), f32(states), f32(h0), f32(dT), i32(cu), dx.data_ptr(), dg.data_ptr(),
                      f32(dh0), (gdn_stream_t)stream(x)),
         "gdn_scan_bwd");

@@ -197,6 +197,16 @@ def test_no_and_single_tokens(T):
         assert torch.equal(y[:, 0], final)
 
 
+@gpu
+def test_no_sequences():
+    import gated_deltanet_linear_15_gb300 as g
+    x, h0 = torch.zeros(0, 7, 40, device=DEV), torch.zeros(0, 40, device=DEV)
+    y, final, states = g.gated_scan(x, x, h0, save_states=True)
+    dx, dg, dh0 = g.gated_scan_bwd(x, x, x, states, h0, final)
+    assert y.shape == dx.shape == dg.shape == x.shape and final.shape == dh0.shape == h0.shape
+    assert g.gated_scan_step(h0, h0, final)[0].shape == h0.shape
+
+
 # ------------------------------------------------------------------ what gates and states may hold
 @gpu
 def test_a_gate_of_minus_infinity_forgets():
