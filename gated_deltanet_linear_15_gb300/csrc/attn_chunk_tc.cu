@@ -23,6 +23,7 @@
 // The work split over CTAs is paged.cuh's.  Every wait is bounded; one that expires ends the CTA with a status word.
 #include "paged.cuh"
 #include "umma.cuh"
+#include "pairs.cuh"
 
 namespace gdn {
 

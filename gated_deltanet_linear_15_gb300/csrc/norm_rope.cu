@@ -20,6 +20,7 @@
 #include <algorithm>
 
 #include "rope.cuh"
+#include "pairs.cuh"
 
 namespace gdn {
 

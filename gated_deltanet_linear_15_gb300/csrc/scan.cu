@@ -28,6 +28,7 @@
 
 #include "block.h"
 #include "common.cuh"
+#include "pairs.cuh"
 
 namespace gdn {
 
