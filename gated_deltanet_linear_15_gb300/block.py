@@ -17,8 +17,8 @@ Every other function computes outside autograd, as
 the ``_fwd`` / ``_bwd`` functions of the delta rule do: its outputs carry no graph, whatever its inputs require.  What a
 function writes in place counts as an in-place operation (its version moves on).
 
-All but ``rotary_table`` and the ``_status`` functions can be captured into a CUDA graph; two graphs that may run at once
-need a workspace each.  A captured
+Attention, rotary positions, norms and the recurrence (but not ``rotary_table`` and the ``_status`` functions) can be captured
+into a CUDA graph; two graphs that may run at once need a workspace each.  A captured
 ``backward()`` adds to leaves whose accumulation PyTorch ties to the stream that first used them: let no eager graph of the
 same leaves live then, or take ``torch.autograd.grad``.
 """
