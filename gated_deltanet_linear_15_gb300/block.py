@@ -78,11 +78,11 @@ def prefix_attention(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_s
                      max_group: int = 0, scale: Optional[float] = None, return_lse: bool = False, out=None, workspace=None):
     """``paged_attention`` of groups of sequences that share a prefix, whose keys are read once for each group.
 
-    prefix_lens int32 [groups]: tokens that all sequences of a group have in common; their rows of page_table name the same
-    pages there, as after ``fork_pages``.  A prefix longer than what some sequence had cached before its new tokens is cut to
-    that.  cu_seqs int32 [groups + 1]: where each group's sequences begin (None: as many for each; sequences outside
-    share nothing).  max_group: the most new tokens of a group, if known on the host (it only picks the kernel).  The rest as in
-    ``paged_attention``, without a window."""
+    prefix_lens int32 [groups]: tokens that all sequences of a group with new tokens have in common; their rows of page_table
+    name the same pages there, as after ``fork_pages``.  Those without new tokens may have ended (``free_pages``).  A prefix
+    longer than what some sequence with new tokens had cached before them is cut to that.  cu_seqs int32 [groups + 1]: where
+    each group's sequences begin (None: as many for each; sequences outside share nothing).  max_group: the most new tokens of
+    a group, if known on the host (it only picks the kernel).  The rest as in ``paged_attention``, without a window."""
     return _py.prefix_attention(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_seqs, cu_q, max_q, max_group, scale,
                                 return_lse, out, workspace)
 

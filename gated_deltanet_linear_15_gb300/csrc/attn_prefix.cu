@@ -3,9 +3,11 @@
 // of the pieces i of both parts,
 //   m = max m_i,  o = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i,  lse = ln 2 (m + log2 sum 2^(m_i - m) l_i).
 //
-// The plan looks at the lengths, which only the device knows: a group's prefix is cut to what all its sequences had cached
-// before their new tokens, so that every new token sees all of it, whatever the caller says; and a group of one sequence has
-// none.  It is one block, a warp to a group, and a few more that clear the rows' notes.
+// The plan looks at the lengths, which only the device knows: a group's prefix is cut to what all its sequences with new tokens
+// had cached before them, so that every new token sees all of it, whatever the caller says; and a group with one such sequence
+// has none.  The prefix is read from the table row of the first of them, which therefore holds all of it: a sequence without new
+// tokens may have ended, with a row that names no pages.  It is one block, a warp to a group, and a few more that clear the
+// rows' notes.
 //
 // The parts run at the same time, each on some of the SMs, where one of them at least is the row kernel, which waits for memory
 // most of the time while the other one computes: launches, searches and ends of the two overlap too.  The plan shares
@@ -97,10 +99,12 @@ template <bool TOGETHER> __global__ void __launch_bounds__(NTP) prefix_plan_kern
       n0 = g * per;
       n1 = n0 + per;
     }
-    int cached = 0x7fffffff, beg = 0x7fffffff, end = 0;
+    int cached = 0x7fffffff, beg = 0x7fffffff, end = 0, first = 0x7fffffff, last = -1;
     for (int n = n0 + lane; n < n1; n += 32) {
       const SeqInfo s = seq_info(a, n);
       if (s.qlen == 0) continue;  // sees nothing, and limits nothing
+      first = min(first, n);
+      last = n;
       cached = min(cached, s.kv - s.qlen);
       beg = min(beg, s.qbeg);
       end = max(end, s.qbeg + s.qlen);
@@ -108,9 +112,11 @@ template <bool TOGETHER> __global__ void __launch_bounds__(NTP) prefix_plan_kern
     cached = __reduce_min_sync(0xffffffffu, cached);
     beg = __reduce_min_sync(0xffffffffu, beg);
     end = __reduce_max_sync(0xffffffffu, end);
-    const int prefix = n1 - n0 > 1 && end > beg ? max(0, min(p.prefix_lens[g], cached)) : 0;
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    const int prefix = last > first ? max(0, min(p.prefix_lens[g], cached)) : 0;
     // The group's rows are those from the first token to the last: its sequences follow one another.
-    if (lane == 0) p.head[g] = prefix > 0 ? make_int4(beg, end - beg, prefix, n0) : make_int4(0, 0, 0, n0);
+    if (lane == 0) p.head[g] = prefix > 0 ? make_int4(beg, end - beg, prefix, first) : make_int4(0, 0, 0, 0);
     for (int n = n0 + lane; n < n1; n += 32) p.tail[n].w = min(prefix, p.tail[n].z);
   }
   if constexpr (TOGETHER) share_out(a, p);

@@ -103,9 +103,10 @@ int gdn_paged_attn_sinks_fwd(const gdn_paged_shape *shape, int sinks, const void
  * gdn_paged_attn_fwd of groups of sequences that share a prefix (branches that gdn_pages_fork made, or requests behind one
  * system prompt), whose keys are read once for a group.  Group g is the sequences cu_seqs[g] .. cu_seqs[g+1]-1 (device int32
  * [groups + 1], not decreasing; NULL: num_seqs / groups each; sequences that no group names have no prefix).  The first
- * prefix_lens[g] tokens (device int32 [groups]) of all of them are those of the group's first sequence: the rows of page_table
- * name the same pages there, and those of the first one are read.  A prefix longer than what some sequence of the
+ * prefix_lens[g] tokens (device int32 [groups]) of all its sequences that have new tokens are the same: the rows of page_table
+ * name the same pages there, and those of the first such sequence are read.  A prefix longer than what some sequence of the
  * group had cached before its new tokens is cut to that, so any value gives right results where the pages are the same.
+ * Sequences without new tokens (branches that have ended among them) limit nothing, and their rows are not read.
  * The new tokens of a group's sequences follow one another in q (cu_q as in gdn_paged_attn_fwd; one that goes back leaves rows
  * without an output).  window must be 0.  max_group: most new tokens of a group if the host knows, 0 otherwise (picks the
  * kernel).  Small batches, where sharing saves too little, are computed as gdn_paged_attn_fwd does, from each sequence's
