@@ -75,7 +75,8 @@ class GdnNormShape(ctypes.Structure):
 
 class GdnScanShape(ctypes.Structure):
     _fields_ = [("num_seqs", _I), ("tokens", _I), ("dim", _I), ("dtype", _I), ("gate_dtype", _I), ("reserved", _I),
-                ("x_row", _L), ("g_row", _L), ("y_row", _L), ("dy_row", _L), ("dg_row", _L), ("state_row", _L)]
+                ("x_row", _L), ("g_row", _L), ("y_row", _L), ("dy_row", _L), ("dg_row", _L), ("state_row", _L),
+                ("zero_rest", _I), ("reserved1", _I)]
 
 
 _lock = threading.Lock()

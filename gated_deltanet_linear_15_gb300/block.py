@@ -306,8 +306,8 @@ def gated_scan(x, g, initial_state=None, cu_seqlens=None, output_final_state: bo
     """h_t = exp(g_t) h_{t-1} + x_t in every channel; y_t = h_t.
 
     x [sequences, tokens, D] (rows of one stride), g like x in its dtype or fp32: the log-gates, meant to be <= 0 (-inf
-    forgets).  Packed sequences: x [1, tokens, D] and cu_seqlens int32 [sequences + 1] on the device; rows that no sequence
-    names stay uninitialised in y.  initial_state fp32 [sequences, D] (None: zeros).  Returns (y, final state fp32 [sequences,
+    forgets).  Packed sequences: x [1, tokens, D] and cu_seqlens int32 [sequences + 1] on the device; rows in front of the
+    first and behind the last one are padding, zeros in y and in the gradients.  initial_state fp32 [sequences, D] (None: zeros).  Returns (y, final state fp32 [sequences,
     D], or None without output_final_state), and with save_states the states that ``gated_scan_bwd`` reads."""
     y, final, states = _py.gated_scan(x, g, initial_state, cu_seqlens, output_final_state, save_states)
     return (y, final, states) if save_states else (y, final)

@@ -108,6 +108,7 @@ struct ScanArgs {
   int N, tokens, T, D;      // T: tokens of each sequence without cu
   int run;                  // segments that a warp takes in a row, at most
   long long x_row, g_row, y_row, dy_row, dg_row, h_row;
+  int zero_rest;            // outputs' rows in front of the first and behind the last sequence become zeros
 };
 // move: bytes of an access that every row allows: 16, 4, or 2 (single bf16 elements)
 cudaError_t launch_scan(const ScanArgs &a, bool bf16_type, bool bf16_gate, int move, bool bwd, int sms, cudaStream_t st);

@@ -464,7 +464,8 @@ bool head_in_warp(int head_dim, gdn_dtype d) {
 // ------------------------------------------------------------------ gated linear recurrence
 int check_scan(const gdn_scan_shape *s) {
   if (!s) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
-  if (s->reserved) return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
+  if (s->reserved || s->reserved1) return fail(GDN_ERR_INVALID_ARG, "reserved fields must be 0");
+  if (s->zero_rest & ~1) return fail(GDN_ERR_INVALID_ARG, "zero_rest must be 0 or 1");
   if (s->dtype != GDN_BF16 && s->dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "unknown dtype");
   if (s->gate_dtype != s->dtype && s->gate_dtype != GDN_FP32) return fail(GDN_ERR_INVALID_ARG, "gate_dtype must be dtype or fp32");
   if (s->num_seqs < 1 || s->tokens < 0) return fail(GDN_ERR_INVALID_ARG, "need num_seqs >= 1, tokens >= 0");
@@ -493,6 +494,7 @@ ScanArgs scan_args(const gdn_scan_shape *s, const void *x, const void *g, const 
   a.dy_row = s->dy_row;
   a.dg_row = s->dg_row;
   a.h_row = s->state_row;
+  a.zero_rest = s->zero_rest;
   return a;
 }
 // whether rows and pointer allow accesses of `bytes` that do not leave the row's features

@@ -765,6 +765,7 @@ gdn_scan_shape scan_shape(const Tensor &x, const Tensor &g, const Tensor *cu, bo
   s.dim = fits(x.size(-1), "the number of features");
   s.x_row = line_stride(x, "x");
   s.g_row = line_stride(g, "g");
+  s.zero_rest = cu != nullptr;  // outputs are new tensors: no row stays without a value
   return s;
 }
 // rows of the saved states

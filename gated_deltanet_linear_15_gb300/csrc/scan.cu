@@ -430,6 +430,16 @@ __device__ __forceinline__ void pass_empty(const ScanArgs &a, const float *in, f
   }
 }
 
+// With zero_rest, rows that no sequence names (of y, or of dx and dg) become zeros, shared out in the same way: gradients of a
+// padded batch are summed over all its rows.
+template <bool P, int W, typename E>
+__device__ __forceinline__ void clear_rest(const ScanArgs &a, E *rows, long long stride, int c, int ctas, int cta) {
+  if (!a.cu || !a.zero_rest) return;
+  const int begin = token_at(a, 0), named = max(token_at(a, a.N) - begin, 0);
+  for (long long i = cta * W + (threadIdx.x >> 5); i < a.tokens - named; i += ctas * W)
+    put<P>(rows + (i < begin ? i : i + named) * stride, c, a.D, Two{});
+}
+
 // Where a CTA's walk through its part stands.  Segments count in the direction of the walk: number 0 is the part's first
 // one, or its last one going backward.
 struct Walk {
@@ -511,6 +521,7 @@ __global__ void __launch_bounds__(32 * W, 2) scan_fwd_kernel(ScanArgs a) {
   Piece now = {}, next = {};
   next.bd.init(a, w.up(0) * SEG);
   pass_empty<P, W>(a, a.h0, a.hT, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  clear_rest<P, W>(a, static_cast<X *>(a.y), a.y_row, c, cs * gridDim.z, blockIdx.z * cs + rank);
   mt.ready();
   auto start = [&](const Piece &p, int i) { return a.h0 ? take<P>(a.h0 + (long long)p.bd.seq(a, p.t0 + i) * a.D, c, a.D) : Two{}; };
   float2 carry = make_float2(0.f, 0.f);
@@ -619,6 +630,8 @@ __global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
   Piece now = {};
   now.bd.init(a, max(w.down(0) * SEG, 0));
   pass_empty<P, W>(a, a.dhT, a.dh0, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  clear_rest<P, W>(a, static_cast<X *>(a.y), a.y_row, c, cs * gridDim.z, blockIdx.z * cs + rank);
+  clear_rest<P, W>(a, static_cast<G *>(a.dg), a.dg_row, c, cs * gridDim.z, blockIdx.z * cs + rank);
   mt.ready();
   auto start = [&](int i) { return a.h0 ? take<P>(a.h0 + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : Two{}; };
   auto at_end = [&](int i) { return a.dhT ? take<P>(a.dhT + (long long)now.bd.seq(a, now.t0 + i) * a.D, c, a.D) : Two{}; };

@@ -273,7 +273,8 @@ int gdn_rmsnorm_bwd(const gdn_norm_shape *shape, const void *dy, const void *h, 
  * The elementwise sister of the delta rule: one state per channel, the gate in its logarithm,
  *     h_t = exp(g_t) h_{t-1} + x_t,   y_t = h_t.
  * x, g, y [tokens, D] (row strides), the sequences one behind the other: token b * T + t of N equal ones of
- * T = tokens / N, or cu_seqlens device int32 [N + 1] (not decreasing; rows that no sequence names are left as they were).
+ * T = tokens / N, or cu_seqlens device int32 [N + 1] (not decreasing; outputs' rows in front of the first sequence and behind
+ * the last one are left as they were, or become zeros with zero_rest, as what sums over all rows needs it).
  * h0 and final fp32 [N, D], contiguous: the states before and after each sequence (an empty one's passes through).
  * Gates are meant to be <= 0 (-inf forgets); with larger ones every product of gates over consecutive tokens of a
  * sequence has to stay finite.  Sums and states are fp32; a NaN or an infinity reaches what follows in its sequence and
@@ -290,6 +291,8 @@ typedef struct {
   int64_t y_row;        /* of y; backward: of dx                                         */
   int64_t dy_row, dg_row; /* backward                                                    */
   int64_t state_row;    /* step: of the state                                            */
+  int zero_rest;        /* 1: rows of y, dx and dg that no sequence names become zeros; 0 */
+  int reserved1;        /* must be 0                                                     */
 } gdn_scan_shape;
 
 /* states fp32 [gdn_scan_states_rows, D] or NULL: gets the state before every 16th token of the line, for the backward.
