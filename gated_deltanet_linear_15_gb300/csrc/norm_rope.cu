@@ -2,6 +2,7 @@
 //   r = (mean(x^2) + eps)^(-1/2),  y = R(p) (r x (w + off)),
 // R(p) the turn of the feature pairs by position p (rope.cu).  Backward, with u = R(p)^T dy and xhat = r x:
 //   dx = r (u (w + off) - xhat mean(u (w + off) xhat)),  dw = sum over tokens and heads of u xhat.
+// No power of r stands alone: with a small eps those of a head of zeros leave fp32, and what they multiply is 0.
 // With a paged cache the keys and values of new tokens go to their slots in the same pass.
 //
 // Bound by bytes: every element is read once and written once (backward: x and dy read, dx written).  A thread's unit is
@@ -434,7 +435,7 @@ __device__ __forceinline__ void norm_rope_bwd_group(const NormRopeArgs &n, int u
 #pragma unroll
         for (int i = 0; i < 2 * PV; ++i) dw.v[i] = fma2(y.v[i], x.v[i], dw.v[i]);
         uint4 o0, o1;
-        (wt * r).plus(x, -r * r * r * (dot * inv_d)).pack(o0, o1);
+        (wt.plus(x, -(r * (r * (dot * inv_d)))) * r).pack(o0, o1);
         store_unit(out, gap, o0, o1);
         ask();
       }
@@ -514,7 +515,7 @@ template <typename I> __global__ void __launch_bounds__(NTR) norm_rope_bwd_any_k
     }
     sum = warp_sum(sum);
     dot = warp_sum(dot);
-    const float r = rsqrtf(sum / (float)a.D + n.eps), m = r * r * (dot / (float)a.D);
+    const float r = rsqrtf(sum / (float)a.D + n.eps), m = r * (r * (dot / (float)a.D));
     for (int k = lane; k < per; k += 32) {
       int f0, f1;
       float u0, u1;
