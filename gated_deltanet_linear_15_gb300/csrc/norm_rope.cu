@@ -44,10 +44,11 @@ template <int UPH> __device__ __forceinline__ float head_sum(float x, int n) {
 }
 // 16 bytes to shared memory.  Where a unit's pieces are neighbours, each of its two copies takes half a sector, and they go by
 // way of L1, so that L2 is asked once (with this and the stores below 16384 tokens of 16 + 4 interleaved heads go backward in
-// 44 us instead of 66; pieces that are not neighbours are 2 us faster past L1, 8192 tokens of 48 heads appended).
+// 44 us instead of 66; pieces that are not neighbours are 2 us faster past L1, 8192 tokens of 48 heads appended).  A place is
+// asked for again right after it was read: the copies are "memory" to the compiler, which may not move that read behind them.
 __device__ __forceinline__ void copy16(void *smem, const void *gmem, bool neighbours) {
-  if (neighbours) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem));
-  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem));
+  if (neighbours) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
 }
 // both pieces of a unit to global memory, in one store where they are neighbours on a 32-byte boundary (two of half a
 // sector each otherwise)
