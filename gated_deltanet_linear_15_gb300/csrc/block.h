@@ -106,11 +106,11 @@ struct ScanArgs {
   float *hT, *dh0, *states; // hT: step the state; states: read by the backward
   const int *cu;
   int N, tokens, T, D;      // T: tokens of each sequence without cu
-  int run;                  // segments that a warp takes in a row, at most
   long long x_row, g_row, y_row, dy_row, dg_row, h_row;
   int zero_rest;            // outputs' rows in front of the first and behind the last sequence become zeros
 };
-// move: bytes of an access that every row allows: 16, 4, or 2 (single bf16 elements)
+// move: bytes of an access that all rows and states allow.  16: rows by 16-byte pieces; 4 in bf16: by pairs; else they begin
+// anywhere and come by the aligned 16-byte pieces that hold them, and values are stored singly
 cudaError_t launch_scan(const ScanArgs &a, bool bf16_type, bool bf16_gate, int move, bool bwd, int sms, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanArgs &a, bool bf16_type, bool bf16_gate, bool vec, cudaStream_t st);
 

@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(32 * W, LIMIT) scan_bwd_kernel(ScanArgs a) {
   cp_async_wait_all();
 }
 
-// One token of every sequence: state = exp(g) state + x, y = state.  Two channels a thread.
+// One token of every sequence: state = exp(g) state + x, y = state.  V channels a thread: four where rows allow it, or one.
 template <typename X, typename G, int V> __global__ void __launch_bounds__(256) scan_step_kernel(ScanArgs a) {
   pdl_trigger();
   pdl_wait();
