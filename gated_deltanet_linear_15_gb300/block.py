@@ -82,7 +82,10 @@ def prefix_attention(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_s
     name the same pages there, as after ``fork_pages``.  Those without new tokens may have ended (``free_pages``).  A prefix
     longer than what some sequence with new tokens had cached before them is cut to that.  cu_seqs int32 [groups + 1]: where
     each group's sequences begin (None: as many for each; sequences outside share nothing).  max_group: the most new tokens of
-    a group, if known on the host (it only picks the kernel).  The rest as in ``paged_attention``, without a window."""
+    a group, if known on the host (it only picks the kernel).  The rest as in ``paged_attention``, without a window.
+
+    Where sharing saves too little, the call is ``paged_attention`` of the same arguments: many new tokens to a sequence, or
+    little room in the rows of page_table (the host knows no lengths, so a table as wide as need be is best for few sequences)."""
     return _py.prefix_attention(q, k_cache, v_cache, page_table, kv_lens, prefix_lens, cu_seqs, cu_q, max_q, max_group, scale,
                                 return_lse, out, workspace)
 

@@ -295,7 +295,16 @@ int attn_status_words(const AttnPlan &p, const void *ws) {
 // 25 / 34, 32 (138 MB) 29 / 32, 8 behind 4096 (119 MB) 31 / 28, 4 behind 16384 (202 MB) 48 / 39, 64 behind 4096 (1.1 GB)
 // 120 / 43; fp32, 2 key heads of 128: 64 behind 256 (41 MB) 28 / 35, 8 behind 4096 (59 MB) 37 / 41, 64 behind 512 (74 MB)
 // 40 / 37, 4 behind 16384 (101 MB) 54 / 49.
+// (The host knows the room of a table row, not the lengths: behind a table of 32768 tokens the first of these, and 4 samples
+// after 992 tokens, go in two parts too: 34 instead of 25 us, 26 instead of 17.)
 double prefix_min_bytes(gdn_dtype d) { return d == GDN_BF16 ? 128e6 : 80e6; }
+// Query rows of a sequence and key head, on the mean, from which on a batch is computed in one part: they fill half a tile of the
+// chunk kernel (fp32: one of the row kernel) by themselves, so the products are as many with the prefix shared, and two parts
+// add their fp32 sums.  Us in one / two parts, caches cold: bf16, 8 sequences behind 8192 tokens, 8 key heads of 128, 4 heads each:
+// 8 new tokens (32 rows) 55 / 47, 24: 73 / 65, 32: 59 / 71, 40: 85 / 78, 64: 67 / 98, 80: 129 / 110, 128: 104 / 149, 1024: 656 / 962;
+// 64 behind 2048, 2 heads each, 48 (96 rows): 143 / 141, 64: 110 / 164; fp32, 16 behind 4096, 4 key heads of 128, 4 heads each: 1: 93 / 47, 4: 93 / 92,
+// 8 (32 rows): 109 / 145, 64: 720 / 936; 32 behind 2048, 2 key heads of 64, 8 heads each, 4 (32 rows): 44 / 57.
+int prefix_max_rows(gdn_dtype d) { return d == GDN_BF16 ? 128 : 32; }
 struct PrefixLayout {
   bool split;  // in two parts; otherwise as sequences that share nothing
   gdn_paged_shape groups;  // the batch of heads
@@ -315,7 +324,8 @@ PrefixLayout prefix_layout(const gdn_paged_shape *s, int groups, int max_group) 
   l.tail = attn_plan(s);
   // bytes that sharing can save at most, as far as the host knows: the sequences of a group read what its first one reads
   const double saved = (double)(s->num_seqs - groups) * s->max_pages * s->page_size * s->num_kv_heads * s->head_dim * 2 * (double)esize(s->dtype);
-  l.split = saved > prefix_min_bytes(s->dtype);
+  const double mean = (double)s->total_q * (s->num_heads / s->num_kv_heads) / std::max(1, s->num_seqs);
+  l.split = saved > prefix_min_bytes(s->dtype) && mean < prefix_max_rows(s->dtype);
   if (!l.split) {
     l.total = l.tail.total;
     return l;

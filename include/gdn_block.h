@@ -109,8 +109,9 @@ int gdn_paged_attn_sinks_fwd(const gdn_paged_shape *shape, int sinks, const void
  * Sequences without new tokens (branches that have ended among them) limit nothing, and their rows are not read.
  * The new tokens of a group's sequences follow one another in q (cu_q as in gdn_paged_attn_fwd; one that goes back leaves rows
  * without an output).  window must be 0.  max_group: most new tokens of a group if the host knows, 0 otherwise (picks the
- * kernel).  Small batches, where sharing saves too little, are computed as gdn_paged_attn_fwd does, from each sequence's
- * own row.
+ * kernel).  Batches in which sharing saves too little are computed as gdn_paged_attn_fwd does, from each sequence's own row:
+ * those whose table rows (max_pages, not the lengths, which the host does not know) have room for little, so a table no wider
+ * than need be makes small batches faster; and those with many new tokens to a sequence, which are bound by products.
  */
 size_t gdn_prefix_attn_workspace_size(const gdn_paged_shape *shape, int groups, int max_group);
 int gdn_prefix_attn_fwd(const gdn_paged_shape *shape, int groups, int max_group, const void *q, const void *k_cache,
