@@ -4,9 +4,10 @@
 //   d_t = dy_t + exp(g_{t+1}) d_{t+1},  dx_t = d_t,  dg_t = exp(g_t) d_t h_{t-1},  dh0 = exp(g_0) d_0.
 //
 // Bound by bytes: x and g are read once and y is written once; the backward reads dy, x and g and writes dx and dg.  What keeps
-// it from the rate of a copy is the chain of rounds below: 4 x 4096 tokens of 2048 channels take 52 us forward (3.9 TB/s; a
-// kernel that only copies with these accesses 37 us) and 78 us backward (4.3 TB/s) in bf16, 50 and 72 us with half the tokens in
-// fp32; one sequence of 65536 tokens and 64 channels, which eight CTAs share, 126 and 150 us.
+// it from the rate of a copy is the chain of rounds below: 4 x 4096 tokens of 2048 channels take 47 us forward (4.3 TB/s; a
+// kernel that only copies with these accesses 37 us) and 68 us backward (5.0 TB/s) in bf16, 43 and 66 us with half the tokens in
+// fp32; one sequence of 65536 tokens and 64 channels, which eight CTAs share, 123 and 145 us (a call among others, inputs from
+// memory; alone, under a profiler, 50 and 73 us for the first).
 //
 // All sequences stand in one line of tokens, cut into segments of SEG = 16 tokens at multiples of 16.  A warp holds a
 // segment of CB = 64 channels, two per lane: it runs the recurrence from zero, which gives the segment's map
