@@ -302,8 +302,8 @@ double prefix_min_bytes(gdn_dtype d) { return d == GDN_BF16 ? 128e6 : 80e6; }
 // chunk kernel (fp32: one of the row kernel) by themselves, so the products are as many with the prefix shared, and two parts
 // add their fp32 sums.  Us in one / two parts, caches cold: bf16, 8 sequences behind 8192 tokens, 8 key heads of 128, 4 heads each:
 // 8 new tokens (32 rows) 55 / 47, 24: 73 / 65, 32: 59 / 71, 40: 85 / 78, 64: 67 / 98, 80: 129 / 110, 128: 104 / 149, 1024: 656 / 962;
-// 64 behind 2048, 2 heads each, 48 (96 rows): 143 / 141, 64: 110 / 164; fp32, 16 behind 4096, 4 key heads of 128, 4 heads each: 1: 93 / 47, 4: 93 / 92,
-// 8 (32 rows): 109 / 145, 64: 720 / 936; 32 behind 2048, 2 key heads of 64, 8 heads each, 4 (32 rows): 44 / 57.
+// 64 behind 2048, 2 heads each, 48 (96 rows): 143 / 141, 64: 110 / 164; fp32, 16 behind 4096, 4 key heads of 128, 4 heads each:
+// 1: 93 / 47, 4: 93 / 92, 8 (32 rows): 109 / 145, 64: 720 / 936; 32 behind 2048, 2 key heads of 64, 8 heads each, 4 (32 rows): 44 / 57.
 int prefix_max_rows(gdn_dtype d) { return d == GDN_BF16 ? 128 : 32; }
 struct PrefixLayout {
   bool split;  // in two parts; otherwise as sequences that share nothing

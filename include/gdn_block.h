@@ -292,7 +292,7 @@ typedef struct {
   int64_t y_row;        /* of y; backward: of dx                                         */
   int64_t dy_row, dg_row; /* backward                                                    */
   int64_t state_row;    /* step: of the state                                            */
-  int zero_rest;        /* 1: rows of y, dx and dg that no sequence names become zeros; 0 */
+  int zero_rest;        /* 1: zeros in the rows that no sequence names; 0: these stay    */
   int reserved1;        /* must be 0                                                     */
 } gdn_scan_shape;
 
